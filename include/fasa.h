@@ -367,6 +367,114 @@ int fasa_decode_step_noalloc(const void* q, const int32_t* pos,
                              const fasa_dims_t* dims, fasa_stream_t stream);
 
 /*
+ * ---------------------------------------------------------------- paged cache
+ * A key/value cache in pages, bounded by an eviction.  The entry points below
+ * follow the conventions at the top of this file (ownership, streams, return
+ * values, FASA_DEV_BAD_INPUT), with these of their own:
+ *
+ *  - Shapes (row-major, contiguous, device memory):
+ *      k_pages, v_pages  [n_pages, Hkv, page_size, d]  storage dtype; keys AFTER RoPE
+ *      page_table        [B, max_pages]      int32, the page that holds slots
+ *                                            i * page_size .. of sequence b
+ *      seq_lens          [B]                 int32, cached tokens: slots 0..len-1
+ *      pos               [B]                 int32, a token's position in its text (a
+ *                                            cache that was cut holds fewer tokens)
+ *      weight            [B, Hkv, T_cap]     fp32, accumulated attention weight of
+ *                                            every slot, T_cap = max_pages * page_size
+ *      token_pos         [B, Hkv, T_cap]     int32, position of the token in the slot
+ *      q                 [B, Hq, d]          storage dtype, pre-RoPE query
+ *      out               [B, Hq, d]          fp32
+ *  - Pages may lie anywhere in the pool and belong to several sequences (a
+ *    shared prompt) as long as no call writes them: fasa_paged_append writes
+ *    the pages of the new slots, fasa_paged_evict those of slots below `keep`.
+ *  - A length outside [0, T_cap] is clamped, and nothing is read or written in
+ *    a page outside [0, n_pages): its tokens count as not cached in the
+ *    attention, and their K and V rows do not move in an eviction (their
+ *    statistics do); both set FASA_DEV_BAD_INPUT.  Rows of a page behind a sequence's
+ *    end may hold anything, NaN included; rows of cached tokens are finite.
+ *  - Alignment: k_pages, v_pages, k_new, v_new, q, out, weight, token_pos and
+ *    workspace 16 bytes.
+ *  - Supported: dtype FASA_F32 or FASA_BF16, head_dim 64 or 128, 1 <= G <= 8,
+ *    page_size 16, 32, 64, 128 or 256, batch <= 4096, batch * Hkv <= 65535,
+ *    T_cap <= 524288, n_pages * Hkv * page_size < 2^31.
+ */
+typedef struct fasa_paged_dims {
+  int32_t batch;       /* B                                            */
+  int32_t n_q_heads;   /* Hq                                           */
+  int32_t n_kv_heads;  /* Hkv (Hq % Hkv == 0)                          */
+  int32_t head_dim;    /* d: 64 or 128                                 */
+  int32_t page_size;   /* tokens per page: 16, 32, 64, 128 or 256      */
+  int32_t n_pages;     /* pages in the pool                            */
+  int32_t max_pages;   /* entries of a sequence's row of the page table */
+  int32_t dtype;       /* FASA_F32 or FASA_BF16                        */
+  double rope_theta;   /* RoPE base B: theta_i = B^(-2i/d)             */
+} fasa_paged_dims_t;
+
+/*
+ * Writes new tokens to the cache.  k_new, v_new [n_tokens, Hkv, d] hold the new
+ * tokens of all sequences one after the other: those of sequence b are rows
+ * cu_new[b] .. cu_new[b+1] (cu_new [B+1] int32, ascending from 0), or row b
+ * alone when cu_new is NULL (n_tokens = B then).  For the j-th new token of b:
+ *   slot t = seq_lens[b] + j, position m = pos[b] + j,
+ *   K[t] = R(m) k_new (each FC turned by the angle m * theta_i, as
+ *   fasa_apply_rope_q; computed in fp32 and rounded once), V[t] = v_new,
+ *   weight[b,h,t] = 0, token_pos[b,h,t] = m   (each of the two may be NULL).
+ * Rows at or behind cu_new[B] are padding and are left out.  A token whose
+ * sequence's length is negative, whose slot is not below T_cap, or whose page is
+ * out of range is left out as a whole and sets FASA_DEV_BAD_INPUT, as does a cu_new that does not ascend from 0 within
+ * n_tokens.  seq_lens is read, not written: the caller advances it.
+ */
+int fasa_paged_append(const void* k_new, const void* v_new, int32_t n_tokens, const int32_t* cu_new,
+                      const int32_t* pos, const int32_t* page_table, const int32_t* seq_lens,
+                      void* k_pages, void* v_pages, float* weight, int32_t* token_pos,
+                      const fasa_paged_dims_t* dims, fasa_stream_t stream);
+
+/*
+ * Attention of one new token per sequence over its cached tokens: for every
+ * query head, out = softmax(R(pos) q K^T / sqrt(d)) V over the slots
+ * 0 .. seq_lens[b]-1 (the new token's own row among them once it was
+ * appended).  A sequence with no cached token gives zeros.  With weight (not
+ * NULL), every cached token's softmax weights are added to it:
+ *   weight[b,h,t] += sum_{hq in group(h)} softmax_t(hq).
+ * The cache's length is split over the SMs, whatever the lengths are, and the
+ * parts are joined in a fixed order: equal calls give equal bits.
+ * workspace: at least fasa_paged_workspace_size bytes of device memory, its
+ * contents not kept and not read; calls that may overlap need one each.
+ */
+int fasa_paged_workspace_size(const fasa_paged_dims_t* dims, int32_t with_weight, size_t* bytes);
+int fasa_paged_attention(const void* q, const int32_t* pos, const void* k_pages, const void* v_pages,
+                         const int32_t* page_table, const int32_t* seq_lens, float* out, float* weight,
+                         void* workspace, size_t workspace_bytes, const fasa_paged_dims_t* dims,
+                         fasa_stream_t stream);
+
+/*
+ * Cuts every (sequence, KV head) down to `keep` tokens.  Where seq_lens[b] >
+ * keep, these stay: first the tokens held, token_pos < sinks or token_pos >
+ * pos[b] - recent (pos[b]: the position of the newest token), then those of
+ * the largest weight; equal ones (held ones among themselves, too) the lower
+ * slot first; -0 equals +0 and a NaN comes behind every number.  The kept
+ * tokens at slots >= keep, in slot order, move to the slots below `keep` that
+ * are not kept, in slot order: K and V rows, weight and token_pos.  The order
+ * of the slots does not matter to the attention (keys carry their rotation),
+ * and a cache one token over its bound moves one row.
+ * new_lens[b] = min(seq_lens[b], keep).
+ * weight_out, token_pos_out: the same buffers as weight and token_pos (then only
+ * the moved tokens' entries are written), or others of that shape, apart from
+ * them: slots 0 .. new_lens[b]-1 are written there and the inputs are left as
+ * they were.  Slots at or behind new_lens[b] keep their contents everywhere.
+ * new_lens must not be seq_lens.  1 <= keep, 0 <= sinks, 0 <= recent,
+ * sinks + recent <= keep.  Table entries from ceil(new_len / page_size)
+ * on are free for other use afterwards.
+ * workspace: at least fasa_paged_evict_workspace_size bytes, as above.
+ */
+int fasa_paged_evict_workspace_size(const fasa_paged_dims_t* dims, int32_t keep, size_t* bytes);
+int fasa_paged_evict(const float* weight, const int32_t* token_pos, const int32_t* pos,
+                     const int32_t* page_table, const int32_t* seq_lens, int32_t keep, int32_t sinks,
+                     int32_t recent, void* k_pages, void* v_pages, float* weight_out,
+                     int32_t* token_pos_out, int32_t* new_lens, void* workspace, size_t workspace_bytes,
+                     const fasa_paged_dims_t* dims, fasa_stream_t stream);
+
+/*
  * Synchronises `stream`, stores the device status word of the current device
  * in *status (FASA_DEV_* bits, 0 = clean) and clears it.  There is one word
  * per device, shared by every call on every stream of that device: a bit may

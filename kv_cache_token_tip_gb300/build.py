@@ -24,9 +24,10 @@ LIBSYNTH = os.path.join(ROOT, "workload", "libfasa_synth.so")
 
 FASA_SOURCES = [os.path.join(PKG, "csrc", f) for f in
                 ("fasa_api.cu", "fasa_cluster_bf16.cu", "fasa_cluster_f32.cu", "fasa_step_bf16.cu", "fasa_noalloc.cu",
-                 "fasa_ca.cu")]
+                 "fasa_ca.cu", "fasa_paged.cu", "fasa_paged_attend.cu", "fasa_paged_cache.cu")]
 FASA_DEPS = [os.path.join(PKG, "csrc", f) for f in
-             ("fasa_cluster.cuh", "fasa_step.cuh", "fasa_ptx.cuh", "fasa_internal.h")] + [
+             ("fasa_cluster.cuh", "fasa_step.cuh", "fasa_ptx.cuh", "fasa_internal.h",
+              "fasa_paged.h", "fasa_paged_index.h")] + [
     os.path.join(ROOT, "include", "fasa.h")]
 SYNTH_SOURCES = [os.path.join(ROOT, "workload", "csrc", "synth_gen.cu")]
 

@@ -14,6 +14,7 @@
 #include "../../include/fasa.h"
 #include "fasa_cluster.cuh"
 #include "fasa_internal.h"
+#include "fasa_paged.h"
 
 using namespace fasa;
 
@@ -89,6 +90,45 @@ int device_info(DevInfo* out) {
   *out = it->second;
   return FASA_OK;
 }
+
+}  // namespace
+
+namespace fasa {
+
+// theta_i / (2 pi) as 64-bit fixed-point turns, theta_i = B^(-2i/d)
+// (cached for the last base and head dim).
+void rope_turns_table(double rope_theta, int head_dim, unsigned long long (&turns)[64]) {
+  static std::mutex mu;
+  static double c_theta = -1.0;
+  static int c_dim = -1;
+  static unsigned long long c_turns[64];
+  std::lock_guard<std::mutex> lk(mu);
+  if (c_theta != rope_theta || c_dim != head_dim) {
+    const long double two64_over_2pi = 18446744073709551616.0L / (2.0L * 3.14159265358979323846264338327950288L);
+    for (int i = 0; i < head_dim / 2 && i < 64; ++i) {
+      const double th = pow(rope_theta, -2.0 * i / head_dim);
+      c_turns[i] = (unsigned long long)((long double)th * two64_over_2pi);
+    }
+    c_theta = rope_theta;
+    c_dim = head_dim;
+  }
+  memcpy(turns, c_turns, sizeof(c_turns));
+}
+
+int device_facts(int* sms, int** status) {
+  DevInfo di;
+  const int st = device_info(&di);
+  if (st) return st;
+  *sms = di.sms;
+  *status = di.status;
+  return FASA_OK;
+}
+
+int report_cuda(cudaError_t e) { return cuda_fail(e); }
+
+}  // namespace fasa
+
+namespace {
 
 // How many clusters of C CTAs with `smem` bytes each can be resident at once
 // (0: the cluster cannot be launched).  Cached per configuration.
@@ -228,25 +268,7 @@ int plan_smem(Params& p, const fasa_dims_t* d, int C, int flags, bool allow_ws, 
   return FASA_ERR_UNSUPPORTED;
 }
 
-// theta_i / (2 pi) as 64-bit fixed-point turns, theta_i = B^(-2i/d)
-// (cached for the last base and head dim).
-void fill_rope_turns(Params& p, const fasa_dims_t* d) {
-  static std::mutex mu;
-  static double c_theta = -1.0;
-  static int c_dim = -1;
-  static unsigned long long c_turns[64];
-  std::lock_guard<std::mutex> lk(mu);
-  if (c_theta != d->rope_theta || c_dim != d->head_dim) {
-    const long double two64_over_2pi = 18446744073709551616.0L / (2.0L * 3.14159265358979323846264338327950288L);
-    for (int i = 0; i < d->head_dim / 2 && i < 64; ++i) {
-      const double th = pow(d->rope_theta, -2.0 * i / d->head_dim);
-      c_turns[i] = (unsigned long long)((long double)th * two64_over_2pi);
-    }
-    c_theta = d->rope_theta;
-    c_dim = d->head_dim;
-  }
-  memcpy(p.rope_turns, c_turns, sizeof(c_turns));
-}
+void fill_rope_turns(Params& p, const fasa_dims_t* d) { rope_turns_table(d->rope_theta, d->head_dim, p.rope_turns); }
 
 void fill_common(Params& p, const fasa_dims_t* d, int32_t budget, int* status) {
   memset(&p, 0, sizeof(p));

@@ -1,0 +1,79 @@
+// Internal definitions of the paged cache: launch parameters, workspace
+// layouts and launchers (fasa_paged.cu checks arguments and calls them).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fasa_paged_index.h"
+
+namespace fasa {
+
+// From fasa_api.cu: theta_i / (2 pi) as 64-bit fixed-point turns; the current
+// device's SM count and status word (a FASA_* code); keeps a CUDA error for
+// fasa_last_cuda_error and returns FASA_ERR_CUDA.
+void rope_turns_table(double rope_theta, int head_dim, unsigned long long (&turns)[64]);
+int device_facts(int* sms, int** status);
+int report_cuda(cudaError_t e);
+
+struct PagedCommon {
+  int B, Hq, Hkv, G, log2_page, n_pages, max_pages, T_cap;
+  const int* page_table;
+  const int* seq_lens;
+  const int* pos;
+  int* status;
+};
+
+struct PagedAppendParams : PagedCommon {
+  unsigned long long rope_turns[64];
+  const void* k_new;
+  const void* v_new;
+  int n_tokens;
+  const int* cu_new;  // null: token b belongs to sequence b
+  void* k_pages;
+  void* v_pages;
+  float* weight;   // null: not kept
+  int* token_pos;  // null: not kept
+};
+
+// Attention workspace: the parts' records (two per part: a unit that began in
+// an earlier part, a unit that goes on in a later one), what each part leaves
+// to join, and with weights the units' log-sums and every token's logits.
+struct PagedAttendParams : PagedCommon {
+  unsigned long long rope_turns[64];
+  const void* q;
+  const void* k_pages;
+  const void* v_pages;
+  float* out;
+  float* weight;  // null: no weights kept
+  float scale;    // log2(e) / sqrt(d): logits are kept in powers of two
+  float* records; // [parts][2][G * (d + 2)]: o [G][d], then m [G], l [G]
+  int2* joins;    // [parts]: (unit that begins here and goes on, its last part), or (-1, 0)
+  float* lse;     // [units][G] of the units one part holds whole
+  float* logits;  // [units][G][T_cap]
+  int grid;       // most parts of this launch
+};
+
+struct PagedEvictParams : PagedCommon {
+  const float* weight;
+  const int* token_pos;
+  void* k_pages;
+  void* v_pages;
+  float* weight_out;
+  int* token_pos_out;
+  int* new_lens;
+  int keep, sinks, recent;
+  int2* moves;     // [units][move_cap]: (to, from)
+  int move_cap;
+  int row_bytes;   // of a K or V row
+};
+
+FASA_HD int paged_record_floats(int G, int D) { return G * (D + 2); }
+size_t paged_attend_workspace(int units, int G, int D, int T_cap, bool weights);
+void paged_attend_layout(PagedAttendParams& p, int units, int D, void* ws);
+
+cudaError_t launch_paged_append(const PagedAppendParams& p, int head_dim, bool bf16, cudaStream_t s);
+cudaError_t launch_paged_attend(const PagedAttendParams& p, int head_dim, bool bf16, int sms, cudaStream_t s);
+cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t s);
+
+}  // namespace fasa

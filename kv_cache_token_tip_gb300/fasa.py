@@ -23,6 +23,8 @@ EXPORTS = [
     "fasa_decode_step_append", "fasa_fc_agreement_workspace_size", "fasa_fc_agreement",
     "fasa_select_dominant_fcs", "fasa_compound_agreement", "fasa_test_fault_injection", "fasa_step_kernel",
     "fasa_build_knondom", "fasa_decode_step_split", "fasa_decode_step_append_split",
+    "fasa_paged_append", "fasa_paged_attention", "fasa_paged_evict", "fasa_paged_workspace_size",
+    "fasa_paged_evict_workspace_size",
 ]
 
 
@@ -51,6 +53,15 @@ def dims_for(cfg, cluster_ctas: int = 0, **override) -> FasaDims:
     d.update(override)
     return FasaDims(d["batch"], d["n_q_heads"], d["n_kv_heads"], d["head_dim"], d["t_max"],
                     d["n_tip"], d["dtype"], cluster_ctas, float(d["rope_theta"]))
+
+
+class FasaPagedDims(ctypes.Structure):
+    """Shapes of a paged cache and of the queries that read it (include/fasa.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("n_q_heads", ctypes.c_int32), ("n_kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32), ("rope_theta", ctypes.c_double),
+    ]
 
 
 _lib = None
@@ -102,6 +113,15 @@ def lib():
             "fasa_select_dominant_fcs": ([vp, i32, vp, dp, vp], ctypes.c_int),
             "fasa_test_fault_injection": ([ctypes.c_uint64, i32, i32], ctypes.c_int),
         }
+        pp = ctypes.POINTER(FasaPagedDims)
+        sig.update({
+            "fasa_paged_append": ([vp, vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, pp, vp], ctypes.c_int),
+            "fasa_paged_workspace_size": ([pp, i32, ctypes.POINTER(sz)], ctypes.c_int),
+            "fasa_paged_attention": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, pp, vp], ctypes.c_int),
+            "fasa_paged_evict_workspace_size": ([pp, i32, ctypes.POINTER(sz)], ctypes.c_int),
+            "fasa_paged_evict": ([vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, pp, vp],
+                                 ctypes.c_int),
+        })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
             fn.argtypes = args
@@ -363,6 +383,114 @@ def fasa_decode_step_noalloc(q, pos, k_cache, v_cache, k_dom, dom_fc, seq_lens, 
         _ptr(seq_lens, _i32(), "seq_lens"), int(budget), _ptr(out, _f32(), "out"),
         _ptr(idx_out, _i32(), "idx_out"), _ptr(count_out, _i32(), "count_out"),
         ctypes.byref(dims), _stream(stream)))
+
+
+# ---------------------------------------------------------------- paged cache
+def _paged_ptrs(dims, tensors):
+    """Device pointers of a paged call's tensors, each given as (name, tensor
+    or None, element type: "s" storage, "i" int32, "f" fp32, None any; number
+    of elements, None any).  All lie on the current device."""
+    import torch
+    types = {"s": torch.float32 if dims.dtype == FASA_F32 else torch.bfloat16, "i": torch.int32,
+             "f": torch.float32}
+    here = torch.cuda.current_device()
+    ptrs = []
+    for name, x, kind, count in tensors:
+        if x is None:
+            ptrs.append(None)
+            continue
+        if not x.is_cuda or x.get_device() != here:
+            raise ValueError(f"{name} must be a tensor on the current CUDA device")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if kind is not None and x.dtype is not types[kind]:
+            raise ValueError(f"{name} has dtype {x.dtype}, expected {types[kind]}")
+        if count is not None and x.numel() != count:
+            raise ValueError(f"{name} has {x.numel()} elements, expected {count}")
+        ptrs.append(x.data_ptr())
+    return ptrs
+
+
+def fasa_paged_append(k_new, v_new, pos, k_pages, v_pages, page_table, seq_lens, cu_new=None, weight=None,
+                      token_pos=None, dims: FasaPagedDims = None, stream=None):
+    """Writes new tokens behind each sequence's cached ones: k_new (pre-RoPE)
+    and v_new [n_tokens, Hkv, d], those of sequence b at cu_new[b] ..
+    cu_new[b+1], or one per sequence without cu_new; the first of b gets the
+    position pos[b].  seq_lens is not advanced."""
+    B, row = dims.batch, dims.n_kv_heads * dims.head_dim
+    pool, slots = dims.n_pages * dims.page_size * row, B * dims.n_kv_heads * dims.max_pages * dims.page_size
+    n_tokens = k_new.numel() // row
+    p = _paged_ptrs(dims, (
+        ("k_new", k_new, "s", n_tokens * row), ("v_new", v_new, "s", n_tokens * row), ("cu_new", cu_new, "i", B + 1),
+        ("pos", pos, "i", B), ("page_table", page_table, "i", B * dims.max_pages), ("seq_lens", seq_lens, "i", B),
+        ("k_pages", k_pages, "s", pool), ("v_pages", v_pages, "s", pool), ("weight", weight, "f", slots),
+        ("token_pos", token_pos, "i", slots)))
+    _check("fasa_paged_append", lib().fasa_paged_append(
+        p[0], p[1], n_tokens, p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], ctypes.byref(dims), _stream(stream)))
+
+
+def fasa_paged_workspace_size(dims: FasaPagedDims, weights: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check("fasa_paged_workspace_size",
+           lib().fasa_paged_workspace_size(ctypes.byref(dims), int(bool(weights)), ctypes.byref(out)))
+    return out.value
+
+
+def fasa_paged_attention(q, pos, k_pages, v_pages, page_table, seq_lens, out, weight=None, workspace=None,
+                         dims: FasaPagedDims = None, stream=None):
+    """Attention of one new token per sequence over its cached tokens; with
+    weight, each cached token's softmax weights are added to it.  Without a
+    workspace one is allocated here."""
+    B = dims.batch
+    pool = dims.n_pages * dims.n_kv_heads * dims.page_size * dims.head_dim
+    if workspace is None:
+        import torch
+        workspace = torch.empty(fasa_paged_workspace_size(dims, weight is not None), dtype=torch.uint8,
+                                device=out.device)
+    p = _paged_ptrs(dims, (
+        ("q", q, "s", B * dims.n_q_heads * dims.head_dim), ("pos", pos, "i", B), ("k_pages", k_pages, "s", pool),
+        ("v_pages", v_pages, "s", pool), ("page_table", page_table, "i", B * dims.max_pages),
+        ("seq_lens", seq_lens, "i", B), ("out", out, "f", B * dims.n_q_heads * dims.head_dim),
+        ("weight", weight, "f", B * dims.n_kv_heads * dims.max_pages * dims.page_size),
+        ("workspace", workspace, None, None)))
+    _check("fasa_paged_attention", lib().fasa_paged_attention(
+        p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], workspace.numel() * workspace.element_size(),
+        ctypes.byref(dims), _stream(stream)))
+
+
+def fasa_paged_evict_workspace_size(dims: FasaPagedDims, keep: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("fasa_paged_evict_workspace_size",
+           lib().fasa_paged_evict_workspace_size(ctypes.byref(dims), int(keep), ctypes.byref(out)))
+    return out.value
+
+
+def fasa_paged_evict(weight, token_pos, pos, k_pages, v_pages, page_table, seq_lens, keep: int, new_lens,
+                     sinks: int = 0, recent: int = 0, weight_out=None, token_pos_out=None, workspace=None,
+                     dims: FasaPagedDims = None, stream=None):
+    """Cuts every (sequence, KV head) down to the `keep` heaviest tokens (the
+    first `sinks` positions and the last `recent` up to pos always stay); the
+    kept ones behind slot `keep` move into the slots the others leave.
+    new_lens [B] <- min(seq_lens, keep).  The statistics change in place, or
+    go to weight_out and token_pos_out.  Without a workspace one is allocated
+    here."""
+    B = dims.batch
+    pool = dims.n_pages * dims.n_kv_heads * dims.page_size * dims.head_dim
+    slots = B * dims.n_kv_heads * dims.max_pages * dims.page_size
+    weight_out = weight if weight_out is None else weight_out
+    token_pos_out = token_pos if token_pos_out is None else token_pos_out
+    if workspace is None:
+        import torch
+        workspace = torch.empty(fasa_paged_evict_workspace_size(dims, keep), dtype=torch.uint8, device=weight.device)
+    p = _paged_ptrs(dims, (
+        ("weight", weight, "f", slots), ("token_pos", token_pos, "i", slots), ("pos", pos, "i", B),
+        ("page_table", page_table, "i", B * dims.max_pages), ("seq_lens", seq_lens, "i", B),
+        ("k_pages", k_pages, "s", pool), ("v_pages", v_pages, "s", pool), ("weight_out", weight_out, "f", slots),
+        ("token_pos_out", token_pos_out, "i", slots), ("new_lens", new_lens, "i", B),
+        ("workspace", workspace, None, None)))
+    _check("fasa_paged_evict", lib().fasa_paged_evict(
+        p[0], p[1], p[2], p[3], p[4], int(keep), int(sinks), int(recent), p[5], p[6], p[7], p[8], p[9], p[10],
+        workspace.numel() * workspace.element_size(), ctypes.byref(dims), _stream(stream)))
 
 
 def fasa_device_status(stream=None) -> int:

@@ -1,0 +1,571 @@
+"""The paged cache on a GPU: append, attention with accumulated weights and
+eviction against the fp64 oracle on the same stored values.
+
+Tolerances (u = 2^-24, the half step of fp32; derived, not fitted):
+  * a rotated element: 2e-6 of its pair's norm (the angle in turns rounds to
+    2^-25 of a half turn, cos and sin to 2 ulp, two products and a sum), plus
+    half a step of the stored type;
+  * a logit z (natural units): the query's 2e-6 and an fp32 sum of d products,
+    |dz| <= eps_z * A with A = sum |q||k| / sqrt(d), eps_z = 2e-6 + (d + 8) u,
+    plus 4 u |z|, |z| <= A, of the scaling to powers of two;
+  * a softmax weight p: relative 2 max |dz| (the weight and the sum it is divided
+    by), 2^-16 of the two-term split of P, 16 u of exp2 and the divisions, and
+    (T + 64) u for a sum of T terms in any order;
+  * out: that relative error times sum p |V|, plus an fp32 sum's (T + 64) u of it;
+  * a weight: that relative error of what it receives, plus u of its new value
+    for each of the G + 1 sums.
+Eviction moves and compares stored values: exact.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import paged_oracle as PO
+from tests.gpu_util import ensure_built
+from tests.parity import host_f64
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+EPS = {"f32": 2.0 ** -24, "bf16": 2.0 ** -8}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(cuda_ok):
+    ensure_built()
+
+
+class Cache:
+    """A paged cache on the GPU with what its calls need, seeded."""
+
+    def __init__(self, dtype, B, Hkv, G, d, page, lens, max_pages=None, theta=5e5, seed=0, sigma=1.0, spare=3):
+        import torch
+        from kv_cache_token_tip_gb300 import FASA_BF16, FASA_F32, FasaPagedDims
+        g = torch.Generator(device="cuda")
+        g.manual_seed(seed)
+        self.dtype, self.B, self.Hkv, self.G, self.d, self.page, self.theta = dtype, B, Hkv, G, d, page, theta
+        dt = torch.float32 if dtype == "f32" else torch.bfloat16
+        max_pages = max_pages or max(1, -(-max(max(lens), 1) // page))
+        self.cap = max_pages * page
+        n_pages = B * max_pages + spare
+
+        def normal(*s):
+            return torch.randn(s, generator=g, device="cuda")
+
+        self.table = torch.randperm(n_pages, generator=g, device="cuda")[:B * max_pages].to(torch.int32).view(
+            B, max_pages).contiguous()
+        self.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.kp, self.vp = normal(n_pages, Hkv, page, d).to(dt), normal(n_pages, Hkv, page, d).to(dt)
+        self.q = (sigma * normal(B, Hkv * G, d)).to(dt)
+        self.pos = torch.tensor([n + 3 for n in lens], dtype=torch.int32, device="cuda")
+        self.weight = torch.exp(normal(B, Hkv, self.cap))
+        self.token_pos = torch.arange(self.cap, dtype=torch.int32, device="cuda").expand(B, Hkv, self.cap).contiguous()
+        self.out = torch.full((B, Hkv * G, d), float("nan"), device="cuda")
+        self.dims = FasaPagedDims(B, Hkv * G, Hkv, d, page, n_pages, max_pages,
+                                  FASA_F32 if dtype == "f32" else FASA_BF16, theta)
+        self.gen = g
+
+    def host(self, x):
+        return host_f64(x, self.dtype)
+
+    def attend(self, weight=True, **kw):
+        from kv_cache_token_tip_gb300 import fasa_paged_attention
+        fasa_paged_attention(self.q, self.pos, self.kp, self.vp, self.table, self.lens, self.out,
+                             weight=self.weight if weight else None, dims=self.dims, **kw)
+        return self.out
+
+
+def status():
+    from kv_cache_token_tip_gb300 import fasa_device_status
+    return fasa_device_status()
+
+
+def check_attention(c, before, out, after, lens=None, table=None):
+    """out and the statistics after a call against the oracle; before, after:
+    the weights (numpy), or None."""
+    lens = c.lens.cpu().numpy() if lens is None else lens
+    table = c.table.cpu().numpy() if table is None else table
+    ref, got, A, pv = PO.paged_attention(c.host(c.q), c.pos.cpu().numpy(), c.host(c.kp), c.host(c.vp), table, lens,
+                                         c.theta)
+    out = out.cpu().numpy().astype(np.float64)
+    assert np.all(np.isfinite(out))
+    T = np.array([min(max(int(n), 0), c.cap) for n in lens], dtype=np.float64)
+    eps_z = 2e-6 + (c.d + 8) * U + 4 * U
+    rel = 2 * eps_z * A.max(-1) + 2.0 ** -16 + (16 + T[:, None] + 64) * U   # [B, Hq]
+    bound = (rel + (T[:, None] + 64) * U)[..., None] * pv
+    err = np.abs(out - ref)
+    assert np.all(err <= bound + 1e-30), f"out: {np.max(err / (bound + 1e-30)):.3g}x the bound"
+    assert np.all(out[T == 0] == 0)
+    if before is not None:
+        want = before + got
+        relw = rel.reshape(c.B, c.Hkv, c.G).max(-1)[..., None]
+        bound = relw * got + (c.G + 1) * U * np.abs(want)
+        err = np.abs(after - want)
+        assert np.all(err <= bound), f"weight: {np.nanmax(err / np.maximum(bound, 1e-30)):.3g}x the bound"
+        untouched = got == 0
+        assert np.array_equal(after[untouched], before[untouched])
+
+
+SHAPES = [
+    # dtype, B, Hkv, G, d, page, lengths
+    ("bf16", 1, 1, 1, 64, 16, [1]),
+    ("f32", 1, 1, 1, 64, 16, [1]),
+    ("bf16", 1, 2, 2, 128, 16, [15]),
+    ("bf16", 2, 1, 8, 128, 32, [16, 17]),
+    ("f32", 2, 2, 8, 128, 16, [33, 0]),
+    ("bf16", 4, 2, 7, 128, 64, [0, 1, 130, 127]),
+    ("f32", 3, 2, 3, 64, 256, [255, 257, 700]),
+    ("bf16", 3, 4, 5, 64, 128, [513, 2, 128]),
+    ("bf16", 1, 8, 4, 128, 64, [3001]),
+    ("f32", 1, 4, 4, 128, 64, [1999]),
+    ("bf16", 9, 2, 4, 64, 16, [0, 0, 5, 200, 0, 31, 32, 1000, 0]),
+    ("bf16", 40, 4, 2, 128, 16, [(i * 37) % 300 for i in range(40)]),
+    ("f32", 33, 8, 1, 64, 32, [(i * 53) % 200 for i in range(33)]),
+]
+
+
+@pytest.mark.parametrize("weights", [False, True], ids=["plain", "weights"])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"{s[0]}-B{s[1]}h{s[2]}g{s[3]}d{s[4]}p{s[5]}n{max(s[6])}")
+def test_attention(shape, weights):
+    c = Cache(*shape, sigma=1.5, seed=len(shape[6]) + shape[4])
+    before = c.weight.cpu().numpy().astype(np.float64) if weights else None
+    out = c.attend(weights)
+    assert status() == 0
+    check_attention(c, before, out, c.weight.cpu().numpy().astype(np.float64) if weights else None)
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 63, 64, 65, 127, 128, 129, 255, 256, 257, 1100])
+@pytest.mark.parametrize("dtype,page,d", [("bf16", 16, 128), ("f32", 64, 64), ("bf16", 256, 64), ("f32", 32, 128)])
+def test_attention_lengths(n, dtype, page, d):
+    c = Cache(dtype, 2, 2, 3, d, page, [n, max(n - 1, 0)], seed=n, sigma=2.0)
+    before = c.weight.cpu().numpy().astype(np.float64)
+    out = c.attend()
+    assert status() == 0
+    check_attention(c, before, out, c.weight.cpu().numpy().astype(np.float64))
+
+
+def test_attention_long_and_short_together():
+    """One long sequence among short and empty ones: units cut over many parts
+    beside parts that hold many units."""
+    for dtype in ("bf16", "f32"):
+        c = Cache(dtype, 6, 2, 4, 128, 32, [3, 20011, 0, 64, 1, 500], seed=5, sigma=2.0)
+        before = c.weight.cpu().numpy().astype(np.float64)
+        out = c.attend()
+        assert status() == 0
+        check_attention(c, before, out, c.weight.cpu().numpy().astype(np.float64))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_rows_behind_the_end_may_hold_anything(dtype):
+    import torch
+    c = Cache(dtype, 3, 2, 4, 128, 64, [70, 1, 0], seed=6)
+    for x, bad in ((c.kp, float("nan")), (c.vp, float("inf"))):
+        keep = torch.zeros(x.shape[0], 64, dtype=torch.bool, device="cuda")
+        for b, n in enumerate([70, 1, 0]):
+            for t in range(n):
+                keep[c.table[b, t // 64].item(), t % 64] = True
+        x.masked_fill_(~keep[:, None, :, None], bad)
+        x[~keep[:, None, :, None].expand_as(x)] = float("nan") if x is c.vp else bad
+    before = c.weight.cpu().numpy().astype(np.float64)
+    out = c.attend()
+    assert status() == 0
+    kp, vp = c.kp, c.vp
+    c.kp, c.vp = torch.nan_to_num(kp, 0.0), torch.nan_to_num(vp, 0.0)
+    check_attention(c, before, out, c.weight.cpu().numpy().astype(np.float64))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_attention_bad_pages_and_lengths(dtype):
+    """Entries of the page table outside the pool hold nothing; lengths are clamped."""
+    c = Cache(dtype, 4, 2, 3, 64, 16, [100, 48, 40, 33], max_pages=7, seed=7)
+    c.table[0, 2], c.table[0, 6], c.table[1, :] = -1, c.dims.n_pages, 2 ** 31 - 1
+    c.lens[2], c.lens[3] = -5, 10 ** 6
+    before = c.weight.cpu().numpy().astype(np.float64)
+    out = c.attend()
+    assert status() == 1 and status() == 0
+    assert np.all(out[1].cpu().numpy() == 0)   # a sequence whose every page is bad
+    check_attention(c, before, out, c.weight.cpu().numpy().astype(np.float64))
+
+
+def test_attention_sharp_and_flat_softmax():
+    import torch
+    for sigma in (0.0, 30.0):
+        c = Cache("bf16", 1, 2, 4, 128, 16, [777], sigma=sigma, seed=8)
+        before = c.weight.cpu().numpy().astype(np.float64)
+        out = c.attend()
+        check_attention(c, before, out, c.weight.cpu().numpy().astype(np.float64))
+    # one token far above all others takes everything: out is its value
+    c = Cache("bf16", 1, 1, 2, 128, 16, [300], seed=9)
+    c.pos.zero_()
+    c.kp.zero_()
+    c.kp[c.table[0, 200 // 16], 0, 200 % 16] = c.q[0, 0]
+    c.q[0, 1] = c.q[0, 0]
+    c.kp *= 100
+    out = c.attend(False)
+    v = c.vp[c.table[0, 200 // 16], 0, 200 % 16].float()
+    assert torch.equal(out[0, 0], v) and torch.equal(out[0, 1], v)
+
+
+def test_attention_shared_pages_and_far_positions():
+    """Two sequences read the same pages; a position near 2^31 turns exactly."""
+    import torch
+    c = Cache("bf16", 2, 2, 2, 128, 16, [40, 35], max_pages=4, seed=10)
+    c.table[1] = c.table[0]
+    c.pos = torch.tensor([2 ** 31 - 1, 1], dtype=torch.int32, device="cuda")
+    before = c.weight.cpu().numpy().astype(np.float64)
+    out = c.attend()
+    check_attention(c, before, out, c.weight.cpu().numpy().astype(np.float64))
+
+
+def test_attention_equal_calls_give_equal_bits_and_streams():
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_attention, fasa_paged_workspace_size
+    c = Cache("bf16", 5, 4, 4, 128, 32, [5000, 1, 0, 333, 4097], seed=11, sigma=2.0)
+    w0 = c.weight.clone()
+    out = c.attend().clone()
+    w1 = c.weight.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    # garbage in the workspace, another stream, two calls at once with a workspace each
+    runs = []
+    for s in (torch.cuda.current_stream(), side):
+        ws = torch.full((fasa_paged_workspace_size(c.dims, True),), 0xFF, dtype=torch.uint8, device="cuda")
+        w, o = w0.clone(), torch.empty_like(out)
+        runs.append((s, ws, w, o))
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, ws, w, o in runs:
+            w.copy_(w0) if s is not side else None
+            with torch.cuda.stream(s):
+                if s is side:
+                    w.copy_(w0)
+                fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, c.lens, o, weight=w, workspace=ws, dims=c.dims)
+    torch.cuda.synchronize()
+    for _, _, w, o in runs:
+        assert torch.equal(o, out) and torch.equal(w, w1)
+
+
+def test_attention_in_graphs_that_share_a_workspace():
+    """Two captured graphs over one workspace, replayed in turn with new lengths and queries."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_attention, fasa_paged_workspace_size
+    a = Cache("bf16", 2, 2, 4, 128, 16, [900, 37], max_pages=60, seed=12)
+    b = Cache("bf16", 3, 2, 4, 128, 32, [5, 64, 2000], max_pages=64, seed=13)
+    ws = torch.empty(max(fasa_paged_workspace_size(x.dims, True) for x in (a, b)), dtype=torch.uint8, device="cuda")
+    graphs = []
+    for c in (a, b):
+        c.attend(workspace=ws)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, c.lens, c.out, weight=c.weight, workspace=ws,
+                                 dims=c.dims)
+        graphs.append(g)
+    for step in range(3):
+        before = [c.weight.cpu().numpy().astype(np.float64) for c in (a, b)]
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for c, w in zip((a, b), before):
+            check_attention(c, w, c.out, c.weight.cpu().numpy().astype(np.float64))
+        a.lens[0], b.lens[1] = 100 * (step + 1), 0
+        a.q.copy_(torch.randn(a.q.shape, generator=a.gen, device="cuda"))
+    assert status() == 0
+
+
+# ---------------------------------------------------------------------- append
+def _append_ref(c, k_new, v_new, cu, kp, vp, w, tp):
+    PO.paged_append(c.host(k_new), c.host(v_new), cu, c.pos.cpu().numpy(), c.table.cpu().numpy(),
+                    c.lens.cpu().numpy(), kp, vp, w, tp, c.theta)
+
+
+def _check_append(c, k_new, v_new, cu, got, ref, k_before):
+    kp, vp, w, tp = got
+    rk, rv, rw, rt = ref
+    # the rows written are those of the oracle, the others keep their bits
+    written = np.any(rk != k_before, axis=-1) | np.any(rv != c.v_before, axis=-1)
+    gk = c.host(kp)
+    assert np.array_equal(gk[~written], k_before[~written])
+    norm = np.sqrt(rk[..., 0::2] ** 2 + rk[..., 1::2] ** 2).repeat(2, -1)
+    bound = 2e-6 * norm + EPS[c.dtype] * (np.abs(rk) + 2e-6 * norm)
+    err = np.abs(gk - rk)[written]
+    assert np.all(err <= bound[written] + 1e-38), f"{np.max(err / (bound[written] + 1e-38)):.3g}x the bound"
+    assert np.array_equal(c.host(vp), rv)
+    if w is not None:
+        assert np.array_equal(w.cpu().numpy().astype(np.float64), rw)
+    if tp is not None:
+        assert np.array_equal(tp.cpu().numpy(), rt)
+    return int(written.sum())
+
+
+def _run_append(c, news, stats=True, cu=None, pad=0):
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_append
+    n = sum(news) + pad
+    dt = c.kp.dtype
+    k_new = torch.randn((n, c.Hkv, c.d), generator=c.gen, device="cuda").to(dt)
+    v_new = torch.randn((n, c.Hkv, c.d), generator=c.gen, device="cuda").to(dt)
+    cu_host = [sum(news[:i]) for i in range(len(news) + 1)]
+    cu_dev = None if cu is None else torch.tensor(cu_host, dtype=torch.int32, device="cuda")
+    ref = [c.host(c.kp).copy(), c.host(c.vp).copy(), c.weight.cpu().numpy().astype(np.float64),
+           c.token_pos.cpu().numpy().copy()]
+    k_before, c.v_before = ref[0].copy(), ref[1].copy()
+    if not stats:
+        ref[2:] = [None, None]
+    _append_ref(c, k_new, v_new, cu_host, *ref)
+    fasa_paged_append(k_new, v_new, c.pos, c.kp, c.vp, c.table, c.lens, cu_new=cu_dev,
+                      weight=c.weight if stats else None, token_pos=c.token_pos if stats else None, dims=c.dims)
+    return _check_append(c, k_new, v_new, cu_host, (c.kp, c.vp, c.weight if stats else None,
+                                                    c.token_pos if stats else None), ref, k_before)
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,d,page,lens,news", [
+    ("bf16", 1, 1, 64, 16, [0], [1]), ("bf16", 3, 8, 128, 16, [15, 16, 40], [1, 1, 1]),
+    ("f32", 2, 3, 64, 32, [31, 0], [1, 70]), ("bf16", 4, 2, 128, 64, [1, 64, 0, 7], [0, 130, 1, 33]),
+    ("f32", 3, 5, 128, 128, [3, 500, 127], [257, 1, 2]), ("bf16", 7, 7, 64, 256, [i * 9 for i in range(7)], [5] * 7),
+    ("bf16", 2, 8, 128, 16, [100, 3], [600, 1500])])
+def test_append(dtype, B, Hkv, d, page, lens, news):
+    cap = max(n + m for n, m in zip(lens, news))
+    c = Cache(dtype, B, Hkv, 1, d, page, lens, max_pages=-(-cap // page) + 1, seed=20, theta=1e4)
+    assert _run_append(c, news, cu=True) == sum(news) * Hkv
+    if all(m == 1 for m in news):
+        assert _run_append(c, news) == B * Hkv
+        assert _run_append(c, news, stats=False) == B * Hkv
+    assert status() == 0
+
+
+def test_append_padding_is_left_out():
+    c = Cache("bf16", 2, 2, 1, 128, 16, [3, 20], max_pages=3, seed=21)
+    assert _run_append(c, [2, 5], cu=True, pad=9) == 14 and status() == 0
+
+
+def test_append_bad_slots_pages_and_tables():
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_append
+    c = Cache("f32", 4, 2, 1, 64, 16, [30, 2, 5, 5], max_pages=2, seed=22)
+    c.table[1, 0] = -1
+    c.table[2, 0] = c.dims.n_pages
+    c.lens[3] = -2
+    # sequence 0 runs out of slots after two tokens, the others have no page or length
+    assert _run_append(c, [4, 1, 1, 1], cu=True) == 4
+    assert status() == 1
+    k = torch.randn((4, 2, 64), device="cuda")
+    before = c.kp.clone()
+    for cu in ([1, 2, 3, 4, 4], [0, 5, 3, 2, 4], [0, 0, 0, 0, 9]):
+        c.lens.fill_(0)
+        c.lens[1:3] = -1
+        cu_new = torch.tensor(cu, dtype=torch.int32, device="cuda")
+        fasa_paged_append(k, k, c.pos, c.kp, c.vp, c.table, c.lens, cu_new=cu_new, dims=c.dims)
+        assert status() == 1
+    assert c.kp.shape == before.shape
+
+
+# ---------------------------------------------------------------------- evict
+def _run_evict(c, keep, sinks=0, recent=0, apart=False):
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_evict
+    kp, vp = c.host(c.kp).copy(), c.host(c.vp).copy()
+    w, tp = c.weight.cpu().numpy().copy(), c.token_pos.cpu().numpy().copy()
+    wo = torch.full_like(c.weight, -7.0) if apart else c.weight
+    to = torch.full_like(c.token_pos, -7) if apart else c.token_pos
+    rwo, rto = (wo.cpu().numpy().copy(), to.cpu().numpy().copy()) if apart else (w, tp)
+    new = torch.full((c.B,), -1, dtype=torch.int32, device="cuda")
+    w0, tp0 = c.weight.clone(), c.token_pos.clone()
+    ref_new = PO.paged_evict(w, tp, c.pos.cpu().numpy(), c.table.cpu().numpy(), c.lens.cpu().numpy(), keep, sinks,
+                             recent, kp, vp, rwo, rto)
+    fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, c.lens, keep, new, sinks=sinks,
+                     recent=recent, weight_out=wo if apart else None, token_pos_out=to if apart else None,
+                     dims=c.dims)
+    assert np.array_equal(new.cpu().numpy(), ref_new)
+    assert np.array_equal(to.cpu().numpy(), rto)
+    assert np.array_equal(wo.cpu().numpy(), rwo, equal_nan=True)
+    assert np.array_equal(c.host(c.kp), kp) and np.array_equal(c.host(c.vp), vp)
+    if apart:
+        assert torch.equal(c.token_pos, tp0) and torch.equal(torch.nan_to_num(c.weight), torch.nan_to_num(w0))
+    return new
+
+
+EVICTS = [
+    # dtype, B, Hkv, d, page, lengths, keep, sinks, recent
+    ("bf16", 1, 1, 64, 16, [2], 1, 0, 0), ("f32", 1, 1, 64, 16, [1], 1, 0, 1),
+    ("bf16", 3, 2, 128, 16, [0, 33, 32], 32, 4, 8), ("f32", 2, 3, 128, 32, [100, 99], 98, 0, 0),
+    ("bf16", 2, 8, 128, 64, [1000, 513], 512, 4, 100), ("bf16", 1, 2, 64, 256, [3000], 7, 2, 5),
+    ("f32", 5, 2, 64, 16, [17, 40, 16, 300, 0], 16, 16, 0), ("bf16", 1, 1, 128, 128, [5000], 4999, 0, 0),
+    ("bf16", 2, 4, 128, 16, [9000, 8200], 1025, 0, 1025), ("bf16", 1, 2, 128, 64, [20000], 4096, 4, 256),
+]
+
+
+@pytest.mark.parametrize("apart", [False, True], ids=["in_place", "apart"])
+@pytest.mark.parametrize("case", EVICTS, ids=lambda c: f"{c[0]}-B{c[1]}h{c[2]}d{c[3]}p{c[4]}n{max(c[5])}k{c[6]}")
+def test_evict(case, apart):
+    dtype, B, Hkv, d, page, lens, keep, sinks, recent = case
+    c = Cache(dtype, B, Hkv, 1, d, page, lens, seed=30 + keep)
+    c.pos = (c.lens - 1).clamp_min(0)
+    new = _run_evict(c, keep, sinks, recent, apart)
+    assert status() == 0
+    if not apart:   # again: nothing is over the bound
+        c.lens = new
+        _run_evict(c, keep, sinks, recent)
+
+
+@pytest.mark.parametrize("kind", ["equal", "few", "zeros", "nan", "extreme", "rising", "falling", "near"])
+@pytest.mark.parametrize("n,keep", [(40, 13), (3000, 1234), (20001, 20000), (20001, 3)])
+def test_evict_hard_weights(kind, n, keep):
+    """Ties, signed zeros, NaN and infinities, sorted weights, weights one step apart."""
+    import torch
+    c = Cache("bf16", 1, 2, 1, 64, 16, [n], seed=n + keep)
+    shape, cap = c.weight.shape, c.cap
+    t = torch.arange(cap, device="cuda").expand(shape)
+    if kind == "equal":
+        c.weight.fill_(2.5)
+    elif kind == "few":
+        c.weight.copy_(torch.randint(0, 3, shape, generator=c.gen, device="cuda"))
+    elif kind == "zeros":
+        c.weight.copy_(torch.where(torch.rand(shape, generator=c.gen, device="cuda") < 0.5, 0.0, -0.0))
+    elif kind == "nan":
+        c.weight.masked_fill_(torch.rand(shape, generator=c.gen, device="cuda") < 0.7, float("nan"))
+        c.weight[:, :, ::3] *= -1
+    elif kind == "extreme":
+        vals = torch.tensor([float("inf"), -float("inf"), 3.4e38, -3.4e38, 1e-45, -1e-45, 0.0, 1.0], device="cuda")
+        c.weight.copy_(vals[torch.randint(0, 8, shape, generator=c.gen, device="cuda")])
+    elif kind == "rising":
+        c.weight.copy_(t.float())
+    elif kind == "falling":
+        c.weight.copy_(-t.float())
+    else:
+        c.weight.copy_((torch.randint(0, 4 * n, shape, generator=c.gen, device="cuda") + 0x3F800000).to(
+            torch.int32).view(torch.float32))
+    c.pos = c.lens - 1
+    for sinks, recent in ((0, 0), (1, 2)):
+        if sinks + recent <= keep:
+            _run_evict(c, keep, sinks, recent, apart=True)
+    assert status() == 0
+
+
+def test_evict_shuffled_positions_and_held_overflow():
+    """Positions in any order, and more held tokens than `keep` (the lower slots stay)."""
+    import torch
+    c = Cache("f32", 2, 2, 1, 64, 16, [700, 650], seed=40)
+    perm = torch.stack([torch.randperm(c.cap, generator=c.gen, device="cuda") for _ in range(4)])
+    c.token_pos.copy_(perm.view(2, 2, -1))
+    c.pos = torch.tensor([690, 640], dtype=torch.int32, device="cuda")
+    _run_evict(c, 100, 10, 50, apart=True)
+    c.token_pos.fill_(3)
+    _run_evict(c, 100, 10, 50, apart=True)   # every token is a sink
+    c.token_pos.fill_(-2 ** 31)
+    c.pos.fill_(-2 ** 31)
+    _run_evict(c, 64, 0, 64)
+    assert status() == 0
+
+
+def test_evict_bad_pages_and_lengths():
+    c = Cache("bf16", 3, 2, 1, 64, 16, [100, 80, 60], max_pages=7, seed=41)
+    c.table[0, 0], c.table[0, 5], c.table[1, 3] = -1, 10 ** 6, c.dims.n_pages
+    c.lens[2] = 10 ** 6
+    c.pos = c.lens.clamp(max=112) - 1
+    _run_evict(c, 40, 2, 8)
+    assert status() == 1 and status() == 0
+
+
+# ------------------------------------------------------------------- together
+@pytest.mark.parametrize("dtype,d,page,G", [("bf16", 128, 16, 4), ("f32", 64, 32, 2)])
+def test_decode_loop_of_a_bounded_cache(dtype, d, page, G):
+    """A prompt, cut after it was read, then steps of append, attention with
+    weights and eviction, every call against the oracle on the library's own
+    state before it."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_append, fasa_paged_evict
+    B, Hkv, keep = 3, 2, 64
+    c = Cache(dtype, B, Hkv, G, d, page, [0, 0, 0], max_pages=-(-200 // page), seed=50, sigma=2.0)
+    c.lens.zero_()
+    c.pos.zero_()
+    news = [150, 64, 3]
+    assert _run_append(c, news, cu=True) == sum(news) * Hkv
+    c.lens += torch.tensor(news, dtype=torch.int32, device="cuda")
+    c.pos = c.lens - 1
+    before = c.weight.cpu().numpy().astype(np.float64)
+    check_attention(c, before, c.attend(), c.weight.cpu().numpy().astype(np.float64))
+    c.lens = _run_evict(c, keep, 2, 10)
+    for step in range(12):
+        c.pos = c.pos + 1
+        _run_append(c, [1] * B)
+        c.lens = c.lens + 1
+        before = c.weight.cpu().numpy().astype(np.float64)
+        c.q = torch.randn(c.q.shape, generator=c.gen, device="cuda").to(c.q.dtype)
+        check_attention(c, before, c.attend(), c.weight.cpu().numpy().astype(np.float64))
+        c.lens = _run_evict(c, keep, 2, 10)
+    assert c.lens.tolist() == [64, 64, 15] and status() == 0
+    newest = c.token_pos[:2, :, :64].amax(-1).cpu().tolist()
+    assert newest == [[161, 161], [75, 75]]
+
+
+def test_decode_steps_in_one_graph():
+    """append, attention and eviction captured together and replayed give the
+    bits of the same calls made one by one."""
+    import torch
+    from kv_cache_token_tip_gb300 import (fasa_paged_append, fasa_paged_attention, fasa_paged_evict,
+                                          fasa_paged_evict_workspace_size, fasa_paged_workspace_size)
+    keep, runs = 100, []
+    for _ in range(2):
+        c = Cache("bf16", 2, 2, 4, 128, 16, [100, 100], max_pages=7, seed=60)
+        c.k_new, c.v_new = c.kp[0, :, :2].transpose(0, 1).contiguous(), c.vp[1, :, :2].transpose(0, 1).contiguous()
+        c.ws = torch.empty(fasa_paged_workspace_size(c.dims, True), dtype=torch.uint8, device="cuda")
+        c.ws2 = torch.empty(fasa_paged_evict_workspace_size(c.dims, keep), dtype=torch.uint8, device="cuda")
+        c.after, c.new = c.lens + 1, torch.zeros(2, dtype=torch.int32, device="cuda")
+        runs.append(c)
+
+    def step(c):
+        c.pos.add_(1)
+        fasa_paged_append(c.k_new, c.v_new, c.pos, c.kp, c.vp, c.table, c.lens, weight=c.weight,
+                          token_pos=c.token_pos, dims=c.dims)
+        fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, c.after, c.out, weight=c.weight, workspace=c.ws,
+                             dims=c.dims)
+        fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, c.after, keep, c.new, sinks=2, recent=9,
+                         workspace=c.ws2, dims=c.dims)
+
+    a, b = runs
+    step(a)
+    step(b)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(b)
+    for _ in range(5):
+        step(a)
+        g.replay()
+    torch.cuda.synchronize()
+    for x in ("kp", "vp", "weight", "token_pos", "out", "new"):
+        assert torch.equal(getattr(a, x), getattr(b, x)), x
+    assert status() == 0
+
+
+def test_binding_refuses_what_does_not_fit():
+    import torch
+    from kv_cache_token_tip_gb300 import FasaError, fasa_paged_append, fasa_paged_attention, fasa_paged_evict
+    c = Cache("bf16", 2, 2, 2, 64, 16, [20, 30], seed=70)
+    a = dict(dims=c.dims)
+
+    def attend(**kw):
+        t = dict(q=c.q, pos=c.pos, kp=c.kp, vp=c.vp, table=c.table, lens=c.lens, out=c.out, weight=c.weight)
+        t.update(kw)
+        fasa_paged_attention(t["q"], t["pos"], t["kp"], t["vp"], t["table"], t["lens"], t["out"],
+                             weight=t["weight"], dims=t.get("dims", c.dims), workspace=t.get("ws"))
+
+    for bad in (dict(q=c.q.float()), dict(q=c.q.cpu()), dict(pos=c.pos.long()), dict(kp=c.kp[:-1]),
+                dict(vp=c.vp.transpose(1, 2)), dict(table=c.table[:, :-1]), dict(lens=c.lens[:1]),
+                dict(out=c.out.bfloat16()), dict(weight=c.weight[:, :1]), dict(out=c.out[:1])):
+        with pytest.raises(ValueError):
+            attend(**bad)
+    with pytest.raises(FasaError):
+        attend(ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    new = torch.zeros(2, dtype=torch.int32, device="cuda")
+    for keep, kw in ((0, {}), (8, dict(recent=9)), (8, dict(sinks=-1)), (8, dict(weight_out=torch.zeros_like(c.weight)))):
+        with pytest.raises(FasaError):
+            fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, c.lens, keep, new, dims=c.dims, **kw)
+    with pytest.raises(FasaError):
+        fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, c.lens, 8, c.lens, dims=c.dims)
+    k = torch.zeros((3, 2, 64), dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(FasaError):   # three rows for two sequences, and no table of rows
+        fasa_paged_append(k, k, c.pos, c.kp, c.vp, c.table, c.lens, **a)
+    with pytest.raises(ValueError):
+        fasa_paged_append(k, k[:2], c.pos, c.kp, c.vp, c.table, c.lens, cu_new=new[:1], **a)
+    assert status() == 0

@@ -1,0 +1,246 @@
+"""The paged cache without a GPU: argument checks of the entry points, the
+index arithmetic of the kernels compiled as plain C++, and pins of the oracle."""
+
+import ctypes
+import os
+import subprocess
+
+import numpy as np
+import pytest
+
+from oracle import paged_oracle as PO
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+P = 0x10000  # never dereferenced: validation fails first
+
+
+@pytest.fixture(scope="module")
+def L():
+    from kv_cache_token_tip_gb300 import build, lib
+    build.build()
+    return lib()
+
+
+def _dims(**kw):
+    from kv_cache_token_tip_gb300 import FasaPagedDims
+    d = dict(batch=2, n_q_heads=32, n_kv_heads=8, head_dim=128, page_size=16, n_pages=64, max_pages=32, dtype=1,
+             rope_theta=5e5)
+    d.update(kw)
+    return FasaPagedDims(*[d[k] for k, _ in FasaPagedDims._fields_])
+
+
+def _append(L, d, n=2, cu=None, k=P, v=P, pos=P, table=P, lens=P, kp=P, vp=P, w=P, tp=P):
+    return L.fasa_paged_append(k, v, n, cu, pos, table, lens, kp, vp, w, tp, d and ctypes.byref(d), None)
+
+
+def _attend(L, d, q=P, pos=P, kp=P, vp=P, table=P, lens=P, out=P, w=None, ws=P, n=1 << 40):
+    return L.fasa_paged_attention(q, pos, kp, vp, table, lens, out, w, ws, n, d and ctypes.byref(d), None)
+
+
+def _evict(L, d, w=P, tp=P, pos=P, table=P, lens=P, keep=100, sinks=4, recent=16, kp=P, vp=P, wo=P, tpo=P,
+           new=2 * P, ws=P, n=1 << 40):
+    return L.fasa_paged_evict(w, tp, pos, table, lens, keep, sinks, recent, kp, vp, wo, tpo, new, ws, n,
+                              d and ctypes.byref(d), None)
+
+
+BAD_DIMS = [
+    (dict(batch=0), 1), (dict(n_kv_heads=0), 1), (dict(n_q_heads=30), 1), (dict(head_dim=7), 1),
+    (dict(page_size=0), 1), (dict(n_pages=0), 1), (dict(max_pages=0), 1), (dict(rope_theta=0.0), 1),
+    (dict(rope_theta=float("nan")), 1), (dict(dtype=7), 2), (dict(head_dim=96), 2),
+    (dict(n_q_heads=72, n_kv_heads=8), 2), (dict(page_size=8), 2), (dict(page_size=48), 2),
+    (dict(page_size=512), 2), (dict(batch=4097), 2), (dict(batch=4096, n_kv_heads=16, n_q_heads=16), 2),
+    (dict(max_pages=32769), 2), (dict(n_pages=1 << 24), 2),
+]
+
+
+@pytest.mark.parametrize("kw,code", BAD_DIMS)
+def test_bad_dims_rejected(L, kw, code):
+    d = _dims(**kw)
+    n = ctypes.c_size_t(7)
+    assert _append(L, d) == code and _attend(L, d) == code and _evict(L, d) == code
+    assert L.fasa_paged_workspace_size(ctypes.byref(d), 1, ctypes.byref(n)) == code and n.value == 0
+    assert L.fasa_paged_evict_workspace_size(ctypes.byref(d), 8, ctypes.byref(n)) == code and n.value == 0
+
+
+def test_arguments_rejected_before_launch(L):
+    d = _dims()
+    assert _append(L, None) == 1 and _attend(L, None) == 1 and _evict(L, None) == 1
+    for name in ("k", "v", "pos", "table", "lens", "kp", "vp"):
+        assert _append(L, d, **{name: None}) == 1
+    for name in ("k", "v", "kp", "vp", "w", "tp"):
+        assert _append(L, d, **{name: P + 8}) == 1
+    assert _append(L, d, n=3) == 1 and _append(L, d, n=-1, cu=P) == 1   # one per sequence, or a table of rows
+    assert _append(L, d, n=0, cu=P) == 0   # nothing to write, nothing launched
+    for name in ("q", "pos", "kp", "vp", "table", "lens", "out"):
+        assert _attend(L, d, **{name: None}) == 1
+    for name in ("q", "kp", "vp", "out", "w"):
+        assert _attend(L, d, **{name: P + 4}) == 1
+    for name in ("w", "tp", "pos", "table", "lens", "kp", "vp", "wo", "tpo", "new"):
+        assert _evict(L, d, **{name: None}) == 1
+    for name in ("w", "tp", "kp", "vp", "wo", "tpo"):
+        assert _evict(L, d, **{name: P + 4}) == 1
+    assert _evict(L, d, keep=0) == 1 and _evict(L, d, sinks=-1) == 1 and _evict(L, d, recent=-1) == 1
+    assert _evict(L, d, keep=19) == 1    # sinks + recent > keep
+    assert _evict(L, d, sinks=2 ** 31 - 1, recent=2 ** 31 - 1) == 1
+    assert _evict(L, d, new=P) == 1      # new_lens is seq_lens
+    stat = 2 * 8 * 512 * 4
+    A, B, C, D = (P + i * stat for i in range(4))
+    assert _evict(L, d, w=A, tp=B, wo=A, tpo=C) == 1           # one in place, the other not
+    assert _evict(L, d, w=A, tp=B, wo=A + 16, tpo=D) == 1      # overlapping
+    assert _evict(L, d, w=A, tp=B, wo=B, tpo=A) == 1
+    assert _evict(L, d, w=A, tp=B, wo=C, tpo=C) == 1
+    assert _evict(L, d, w=A, tp=B, wo=A, tpo=B, ws=None) == 3 and _evict(L, d, w=A, tp=B, wo=C, tpo=D, n=0) == 3
+    assert _evict(L, d, w=A, tp=B, wo=C, tpo=D, ws=P + 8) == 3
+
+
+def test_workspace_sizes(L):
+    d, n = _dims(), ctypes.c_size_t(0)
+    size = L.fasa_paged_workspace_size
+    assert size(ctypes.byref(d), 0, None) == 1
+    assert size(ctypes.byref(d), 0, ctypes.byref(n)) == 0
+    plain = n.value
+    assert plain > 0 and _attend(L, d, n=plain - 1) == 3 and _attend(L, d, ws=None) == 3
+    assert _attend(L, d, ws=P + 8) == 3
+    assert size(ctypes.byref(d), 1, ctypes.byref(n)) == 0
+    # with weights: every query head's logit of every slot
+    assert n.value >= plain + 2 * 32 * 512 * 4 and _attend(L, d, w=P, n=n.value - 1) == 3
+    ev = L.fasa_paged_evict_workspace_size
+    assert ev(ctypes.byref(d), 0, ctypes.byref(n)) == 1 and ev(ctypes.byref(d), 8, None) == 1
+    assert ev(ctypes.byref(d), 100, ctypes.byref(n)) == 0 and n.value >= 2 * 8 * 100 * 8
+    assert ev(ctypes.byref(d), 500, ctypes.byref(n)) == 0 and n.value >= 2 * 8 * 12 * 8
+    assert ev(ctypes.byref(d), 512, ctypes.byref(n)) == 0 and n.value == 0   # nothing can be over the bound
+
+
+INDEX_PROGRAM = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "fasa_paged_index.h"
+using namespace fasa;
+#define CHECK(x) do { if (!(x)) { printf("line %d: %s\n", __LINE__, #x); return 1; } } while (0)
+int main() {
+  // the parts cover the line once, in order, and part_of is their inverse
+  const int grids[] = {1, 3, 152, 304, PAGED_MAX_PARTS};
+  for (int grid : grids)
+    for (int total = 1; total < 6000; total = total * 5 / 4 + 1) {
+      const int parts = paged_parts(total, grid);
+      CHECK(parts >= 1 && parts <= grid && parts <= total);
+      CHECK(paged_part_begin(total, parts, 0) == 0 && paged_part_begin(total, parts, parts) == total);
+      for (int c = 0; c < parts; ++c) {
+        const int a = paged_part_begin(total, parts, c), b = paged_part_begin(total, parts, c + 1);
+        CHECK(a < b);
+        for (int x = a; x < b; ++x) CHECK(paged_part_of(total, parts, x) == c);
+      }
+    }
+  // the longest line: 65535 units of PAGED_MAX_SLOTS slots
+  const int total = 65535 * (PAGED_MAX_SLOTS / PAGED_GROUP), parts = paged_parts(total, PAGED_MAX_PARTS);
+  CHECK(total > 0 && parts == PAGED_MAX_PARTS && paged_part_begin(total, parts, parts) == total);
+  for (int c = 0; c < parts; ++c) {
+    const int a = paged_part_begin(total, parts, c), b = paged_part_begin(total, parts, c + 1);
+    CHECK(a < b && paged_part_of(total, parts, a) == c && paged_part_of(total, parts, b - 1) == c);
+  }
+  CHECK(paged_groups(0) == 0 && paged_groups(1) == 1 && paged_groups(16) == 1 && paged_groups(17) == 2);
+  CHECK(paged_parts(0, 152) == 1);
+  // rows: inside the pool for every page in it, -1 for every other entry
+  for (int lp = 4; lp <= 8; ++lp)
+    for (int page = -2; page < 9; ++page)
+      for (int h = 0; h < 3; ++h)
+        for (int slot = 0; slot < 1024; ++slot) {
+          const long long r = paged_row(page, 7, 3, h, lp, slot);
+          if (page < 0 || page >= 7) CHECK(r == -1);
+          else CHECK(r == ((long long)page * 3 + h) * (1 << lp) + slot % (1 << lp) && r < (7ll * 3 << lp));
+        }
+  CHECK(paged_row((1 << 30), 1 << 20, 8, 0, 8, 0) == -1);
+  CHECK(paged_row((1 << 20) - 1, 1 << 20, 7, 6, 8, 255) == (7ll << 28) - 1);
+  puts("ok");
+  return 0;
+}
+"""
+
+
+def test_index_arithmetic(tmp_path):
+    src = tmp_path / "index.cpp"
+    src.write_text(INDEX_PROGRAM)
+    exe = str(tmp_path / "index")
+    inc = os.path.join(ROOT, "kv_cache_token_tip_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", inc, str(src), "-o", exe],
+                   check=True, capture_output=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+# ------------------------------------------------------------------ oracle pins
+def _pool(rng, B, Hkv, d, page, max_pages):
+    n_pages = B * max_pages + 2
+    table = rng.permutation(n_pages)[:B * max_pages].reshape(B, max_pages).astype(np.int32)
+    return rng.standard_normal((n_pages, Hkv, page, d)), rng.standard_normal((n_pages, Hkv, page, d)), table
+
+
+def test_oracle_attention_is_softmax_attention():
+    import torch
+    rng = np.random.default_rng(1)
+    B, Hkv, G, d, page = 3, 2, 3, 64, 16
+    kp, vp, table = _pool(rng, B, Hkv, d, page, 4)
+    lens = [64, 17, 0]
+    q, pos = rng.standard_normal((B, Hkv * G, d)), np.array([70, 5, 9])
+    out, got, _, _ = PO.paged_attention(q, pos, kp, vp, table, lens, 1e4)
+    for b, n in enumerate(lens):
+        if n == 0:
+            assert np.all(out[b] == 0) and np.all(got[b] == 0)
+            continue
+        z = (q[b].reshape(-1, d // 2, 2) @ [1, 1j]) * np.exp(1j * pos[b] * np.exp(-np.arange(0, d, 2) / d * np.log(1e4)))
+        qr = np.stack([z.real, z.imag], -1).reshape(Hkv * G, d)
+        K = kp[table[b]].transpose(1, 0, 2, 3).reshape(Hkv, -1, d)[:, :n]
+        V = vp[table[b]].transpose(1, 0, 2, 3).reshape(Hkv, -1, d)[:, :n]
+        t = [torch.from_numpy(np.ascontiguousarray(x)) for x in (qr[:, None], K.repeat(G, 0), V.repeat(G, 0))]
+        ref = torch.nn.functional.scaled_dot_product_attention(*t)[:, 0].numpy()
+        assert np.allclose(out[b], ref, rtol=1e-12, atol=1e-12)
+        assert np.allclose(got[b].sum(-1), G, rtol=1e-12) and np.all(got[b, :, n:] == 0)
+
+
+def test_oracle_append_then_attention_equals_a_cache_that_holds_the_token():
+    rng = np.random.default_rng(2)
+    kp, vp, table = _pool(rng, 2, 2, 64, 16, 3)
+    lens, pos = np.array([16, 30]), np.array([16, 99])
+    k_new, v_new = rng.standard_normal((3, 2, 64)), rng.standard_normal((3, 2, 64))
+    w, tp = np.ones((2, 2, 48)), np.full((2, 2, 48), -1)
+    PO.paged_append(k_new, v_new, [0, 2, 3], pos, table, lens, kp, vp, w, tp, 1e4)
+    assert np.array_equal(vp[table[0, 1], :, 0], v_new[0]) and np.array_equal(vp[table[0, 1], :, 1], v_new[1])
+    assert np.array_equal(vp[table[1, 1], :, 14], v_new[2])
+    # a rotated key meets a query at its own position as if neither were rotated
+    q = rng.standard_normal((2, 64))
+    assert np.allclose((PO.rotate(q, 17, 1e4) * kp[table[0, 1], :, 1]).sum(-1), (q * k_new[1]).sum(-1))
+    assert list(tp[0, 0, 15:19]) == [-1, 16, 17, -1] and list(w[1, 1, 29:32]) == [1, 0, 1] and tp[1, 0, 30] == 99
+
+
+def test_oracle_eviction_by_hand_and_by_brute_force():
+    import itertools
+    stay = PO.evict_choice(np.array([5.0, 1, 4, 4, 0, 9]), np.arange(6), 5, 4, 1, 1)
+    assert list(stay) == [0, 2, 5, 3] or list(stay) == [0, 2, 3, 5]
+    # ties keep the lower slot, held tokens come before any weight, NaN last
+    assert list(PO.evict_choice(np.array([1.0, 1, 1, 1]), np.arange(4), 3, 2, 0, 0)) == [0, 1]
+    assert list(PO.evict_choice(np.array([0.0, np.inf, 2, 3]), np.array([9, 0, 2, 5]), 9, 2, 0, 1)) == [0, 1]
+    assert list(PO.evict_choice(np.array([np.nan, -np.inf, 2]), np.arange(3), 2, 2, 0, 0)) == [1, 2]
+    assert list(PO.evict_choice(np.array([-0.0, 0.0, -1]), np.arange(3), 2, 1, 0, 0)) == [0]
+    rng = np.random.default_rng(3)
+    for _ in range(20):
+        w = rng.integers(0, 6, 8).astype(float)
+        k = int(rng.integers(1, 8))
+        best = max(itertools.combinations(range(8), k), key=lambda s: (sum(w[list(s)]), [-i for i in s]))
+        assert list(PO.evict_choice(w, np.zeros(8, dtype=int) + 3, 7, k, 0, 0)) == list(best)
+
+
+def test_oracle_eviction_keeps_every_kept_row_once():
+    rng = np.random.default_rng(4)
+    kp, vp, table = _pool(rng, 2, 2, 64, 16, 4)
+    w, tp = rng.random((2, 2, 64)), np.tile(np.arange(64), (2, 2, 1))
+    k0, w0 = kp.copy(), w.copy()
+    lens = [64, 20]
+    new = PO.paged_evict(w, tp, [63, 19], table, lens, 24, 2, 5, kp, vp, w, tp)
+    assert list(new) == [24, 20]
+    for h in range(2):
+        assert len(set(tp[0, h, :24])) == 24 and set(tp[0, h, :24]) >= {0, 1, 59, 60, 61, 62, 63}
+        for t in range(24):
+            m = tp[0, h, t]
+            assert w[0, h, t] == w0[0, h, m]
+            assert np.array_equal(kp[table[0, t // 16], h, t % 16], k0[table[0, m // 16], h, m % 16])
+        assert np.array_equal(w[1, h], w0[1, h])
