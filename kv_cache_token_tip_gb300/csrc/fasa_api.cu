@@ -126,6 +126,8 @@ int device_facts(int* sms, int** status) {
 
 int report_cuda(cudaError_t e) { return cuda_fail(e); }
 
+unsigned long long wait_limit_ns() { return g_wait_ns; }
+
 }  // namespace fasa
 
 namespace {

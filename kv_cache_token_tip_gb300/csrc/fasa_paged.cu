@@ -151,6 +151,7 @@ int fasa_paged_attention(const void* q, const int32_t* pos, const void* k_pages,
   p.v_pages = v_pages;
   p.out = out;
   p.weight = weight;
+  p.wait_ns = wait_limit_ns();
   p.scale = (float)(1.4426950408889634 / sqrt((double)dims->head_dim));
   paged_attend_layout(p, dims->batch * dims->n_kv_heads, dims->head_dim, workspace);
   const cudaError_t e =

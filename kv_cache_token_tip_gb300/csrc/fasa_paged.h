@@ -15,6 +15,7 @@ namespace fasa {
 void rope_turns_table(double rope_theta, int head_dim, unsigned long long (&turns)[64]);
 int device_facts(int* sms, int** status);
 int report_cuda(cudaError_t e);
+unsigned long long wait_limit_ns();  // bound of every device wait
 
 struct PagedCommon {
   int B, Hq, Hkv, G, log2_page, n_pages, max_pages, T_cap;
@@ -52,6 +53,7 @@ struct PagedAttendParams : PagedCommon {
   float* lse;     // [units][G] of the units one part holds whole
   float* logits;  // [units][G][T_cap]
   int grid;       // most parts of this launch
+  unsigned long long wait_ns;  // bound of every device wait
 };
 
 struct PagedEvictParams : PagedCommon {
