@@ -67,7 +67,7 @@ bool apart(const void* a, const void* b, size_t bytes) {
 namespace fasa {
 
 size_t paged_attend_workspace(int units, int G, int D, int T_cap, bool weights) {
-  size_t n = up((size_t)PAGED_MAX_PARTS * 2 * paged_record_floats(G, D) * 4) + up((size_t)PAGED_MAX_PARTS * 8);
+  size_t n = up((size_t)PAGED_MAX_PARTS * 2 * paged_record_floats(G, D) * 4);
   if (weights) n += up((size_t)units * G * 4) + up((size_t)units * G * T_cap * 4);
   return n;
 }
@@ -76,8 +76,6 @@ void paged_attend_layout(PagedAttendParams& p, int units, int D, void* ws) {
   char* w = static_cast<char*>(ws);
   p.records = reinterpret_cast<float*>(w);
   w += up((size_t)PAGED_MAX_PARTS * 2 * paged_record_floats(p.G, D) * 4);
-  p.joins = reinterpret_cast<int2*>(w);
-  w += up((size_t)PAGED_MAX_PARTS * 8);
   p.lse = reinterpret_cast<float*>(w);
   w += up((size_t)units * p.G * 4);
   p.logits = reinterpret_cast<float*>(w);

@@ -38,8 +38,8 @@ struct PagedAppendParams : PagedCommon {
 };
 
 // Attention workspace: the parts' records (two per part: a unit that began in
-// an earlier part, a unit that goes on in a later one), what each part leaves
-// to join, and with weights the units' log-sums and every token's logits.
+// an earlier part, a unit that goes on in a later one), and with weights the
+// units' log-sums and every token's logits.
 struct PagedAttendParams : PagedCommon {
   unsigned long long rope_turns[64];
   const void* q;
@@ -49,7 +49,6 @@ struct PagedAttendParams : PagedCommon {
   float* weight;  // null: no weights kept
   float scale;    // log2(e) / sqrt(d): logits are kept in powers of two
   float* records; // [parts][2][G * (d + 2)]: o [G][d], then m [G], l [G]
-  int2* joins;    // [parts]: (unit that begins here and goes on, its last part), or (-1, 0)
   float* lse;     // [units][G] of the units one part holds whole
   float* logits;  // [units][G][T_cap]
   int grid;       // most parts of this launch
@@ -70,7 +69,8 @@ struct PagedEvictParams : PagedCommon {
   int row_bytes;   // of a K or V row
 };
 
-FASA_HD int paged_record_floats(int G, int D) { return G * (D + 2); }
+// (whole 16-byte words, so that the next record begins on a boundary)
+FASA_HD int paged_record_floats(int G, int D) { return (G * (D + 2) + 3) / 4 * 4; }
 size_t paged_attend_workspace(int units, int G, int D, int T_cap, bool weights);
 void paged_attend_layout(PagedAttendParams& p, int units, int D, void* ws);
 

@@ -9,11 +9,16 @@
 // l 2^(m - M) + l' 2^(m' - M), and o alike.
 //
 // attend: each CTA takes one part of the line of all token groups
-// (fasa_paged_index.h), unit by unit; its warps take groups in turn, each with
-// a running (m, l, o) of its own, joined at the unit's end in the CTA.  A unit
-// the CTA holds whole is finished there; otherwise its record goes to the
-// workspace.  join: the records of a unit that was cut, in part order; and
-// with weights, a second pass over the logits the first one left.
+// (fasa_paged_index.h), unit by unit; its warps take groups of 16 tokens in
+// turn, each with a running (m, l, o) of its own, joined at the unit's end in
+// the CTA.  A unit the CTA holds whole is finished there; otherwise its record
+// goes to the workspace.  join: the records of a unit that was cut, in part
+// order; and with weights, a second pass over the logits the first one left.
+//
+// The bytes of K and V bound it, so a warp's groups come through a ring of its
+// own in shared memory that TMA fills (one copy of 16 rows for K, one for V, in
+// the 128-byte swizzle: no bank conflicts), page by page wherever the pages
+// lie, and no warp waits for another before a unit's end.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -28,26 +33,47 @@
 namespace fasa {
 namespace {
 
-constexpr int AT_NT = 256;
-constexpr int AT_NW = AT_NT / 32;
+constexpr int AT_NW = 4;  // warps of a CTA
+constexpr int AT_NT = AT_NW * 32;
+constexpr int JN_NT = 128;
 
-__device__ __forceinline__ int clamped_len(const PagedCommon& p, int b) {
-  return min(max(p.seq_lens[b], 0), p.T_cap);
-}
+// The sequences' groups as prefix sums, in shared memory: word b holds the
+// groups before sequence b (28 bits: at most 4096 * 32768) and by how many
+// tokens b's last group is short (4 bits); word B all groups.
+struct Line {
+  const unsigned* w;
+  int B, Hkv;
+  __device__ int before(int b) const { return (int)(w[b] & 0x0fffffffu); }
+  __device__ int groups(int b) const { return before(b + 1) - before(b); }
+  __device__ int tokens(int b) const { return groups(b) * PAGED_GROUP - (int)(w[b] >> 28); }
+  __device__ int total() const { return before(B) * Hkv; }
+  // The sequence whose units hold position x of the line.
+  __device__ int sequence_of(int x) const {
+    int lo = 0, hi = B;  // Hkv * before(lo) <= x < Hkv * before(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(mid) * Hkv <= x) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+};
 
-// pre[b] = groups of the sequences before b, b = 0 .. B.  Every thread calls
-// it; ends with a barrier.
+// Every thread of the block calls it; ends with a barrier.  scan: NT / 32 words.
 template <int NT>
-__device__ void group_prefix(const PagedCommon& p, int* pre, int* scan, bool report) {
+__device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     const int b = b0 + tid;
     int n = 0;
+    unsigned shy = 0u;
     if (b < p.B) {
       const int len = p.seq_lens[b];
       if (report && (len < 0 || len > p.T_cap)) atomicOr(p.status, 1);
-      n = paged_groups(min(max(len, 0), p.T_cap));
+      const int use = min(max(len, 0), p.T_cap);
+      n = paged_groups(use);
+      shy = (unsigned)(n * PAGED_GROUP - use);
     }
     int incl = n;
 #pragma unroll
@@ -57,215 +83,365 @@ __device__ void group_prefix(const PagedCommon& p, int* pre, int* scan, bool rep
     }
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
-    int before = base, tot = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-      before += w < warp ? scan[w] : 0;
-      tot += scan[w];
+    int before = base;
+#pragma unroll
+    for (int v = 0; v < NT / 32; ++v) {
+      const int s = scan[v];
+      before += v < warp ? s : 0;
+      base += s;
     }
-    if (b < p.B) pre[b + 1] = before + incl;
-    base += tot;
+    if (b < p.B) w[b] = (unsigned)(before + incl - n) | (shy << 28);
+    if (b == p.B - 1) w[p.B] = (unsigned)(before + incl);
     __syncthreads();
   }
-  if (tid == 0) pre[0] = 0;
-  __syncthreads();
-}
-
-// The sequence whose units hold position x of the line.
-__device__ __forceinline__ int sequence_of(const int* pre, int B, int Hkv, int x) {
-  int lo = 0, hi = B;  // Hkv * pre[lo] <= x < Hkv * pre[hi]
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (pre[mid] * Hkv <= x) lo = mid;
-    else hi = mid;
-  }
-  return lo;
 }
 
 // Walks the units that [x, end) of the line touches.
 struct Segments {
-  const int* pre;
-  int Hkv, end;
-  int x, b, h;           // where the next segment begins
+  Line line;
+  int end;
+  int x, b, h;  // where the next segment begins
   int unit_begin, unit_end;
-  __device__ void start(const int* pre_, int B, int Hkv_, int x_, int end_) {
-    pre = pre_;
-    Hkv = Hkv_;
+  __device__ void start(const Line& l, int x_, int end_) {
+    line = l;
     x = x_;
     end = end_;
-    b = x < end ? sequence_of(pre, B, Hkv, x) : 0;
-    const int n = pre[b + 1] - pre[b];
-    h = n ? (x - pre[b] * Hkv) / n : 0;
+    b = h = 0;
+    if (x < end) {
+      b = line.sequence_of(x);
+      h = (x - line.before(b) * line.Hkv) / line.groups(b);
+    }
   }
   // The segment at x: its unit (b, h) and where the unit lies; false at the end.
   __device__ bool at() {
     if (x >= end) return false;
-    while (pre[b + 1] == pre[b]) ++b;
-    const int n = pre[b + 1] - pre[b];
-    unit_begin = pre[b] * Hkv + h * n;
+    while (line.groups(b) == 0) ++b;
+    const int n = line.groups(b);
+    unit_begin = line.before(b) * line.Hkv + h * n;
     unit_end = unit_begin + n;
     return true;
   }
+  __device__ int unit() const { return b * line.Hkv + h; }
   __device__ int seg_end() const { return min(unit_end, end); }
   __device__ void next() {
     x = seg_end();
-    if (x == unit_end && ++h == Hkv) {
+    if (x == unit_end && ++h == line.Hkv) {
       h = 0;
       ++b;
     }
   }
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(AT_NT) paged_attend_kernel(const __grid_constant__ PagedAttendParams p) {
-  constexpr int E = D / 32;
-  extern __shared__ __align__(16) float sm[];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int G = p.G;
-  float* qs = sm;                      // [G][D]
-  float* mrg = qs + G_MAX * D;         // [AT_NW][G][D]
-  float* mml = mrg + AT_NW * G_MAX * D;  // [AT_NW][G][2]
-  int* scan = reinterpret_cast<int*>(mml + AT_NW * G_MAX * 2);
-  int* pre = scan + 32;
-  group_prefix<AT_NT>(p, pre, scan, blockIdx.x == 0);
-  const int total = pre[p.B] * p.Hkv;
-  const int parts = paged_parts(total, p.grid);
-  const int c = blockIdx.x;
-  // sequences without a token: zeros
-  for (int b = c; b < p.B; b += p.grid)
-    if (pre[b] == pre[b + 1])
-      for (int i = tid; i < p.Hq * D; i += AT_NT) p.out[(size_t)b * p.Hq * D + i] = 0.f;
-  if (tid == 0) p.joins[c] = make_int2(-1, 0);
-  if (c >= parts) return;
-  const int r0 = paged_part_begin(total, parts, c), r1 = paged_part_begin(total, parts, c + 1);
-  Segments sg;
-  sg.start(pre, p.B, p.Hkv, r0, r1);
-  while (sg.at()) {
-    const int b = sg.b, h = sg.h, unit = b * p.Hkv + h;
-    const int len = clamped_len(p, b);
-    __syncthreads();
-    for (int i = tid; i < G * (D / 2); i += AT_NT) {
-      const int g = i / (D / 2), f = i - g * (D / 2);
-      const T* q = static_cast<const T*>(p.q) + ((size_t)b * p.Hq + h * G + g) * D + 2 * f;
-      const float2 cs = rope_cos_sin(p.rope_turns[f], p.pos[b]);
-      const float x0 = to_f32<T>(q[0]), x1 = to_f32<T>(q[1]);
-      qs[g * D + 2 * f] = (x0 * cs.x - x1 * cs.y) * p.scale;
-      qs[g * D + 2 * f + 1] = (x0 * cs.y + x1 * cs.x) * p.scale;
+// ------------------------------------------------- bf16: tensor cores
+// z^T: rows of A the heads, B the tokens.  The rotated and scaled query is
+// three bf16 terms (24 bits: the logits are as exact as fp32's), the first two
+// as rows 0-7 and 8-15 of one operand, the third as another.  o^T = V^T P^T:
+// the z fragment is the P fragment of the same lane, in two bf16 terms (16 bits
+// of a weight that is summed with others), V read transposed.  Lane (g, t) =
+// (lane / 4, lane % 4) holds head g's m and its share of l, and of o the heads
+// 2t, 2t + 1 at the dims 16 i + g, 16 i + g + 8.
+template <int D>
+struct MathBf16 {
+  using T = __nv_bfloat16;
+  static constexpr int CTAS = 2;  // per SM: one streams while the other joins a unit's parts
+  static constexpr int MT = D / 16;
+  static constexpr int OREGS = 4 * MT;
+  static constexpr int QREGS = 2 * MT;   // words of a lane's share of the next unit's raw query
+  static constexpr int QUERY = 0, SCRATCH = 0;  // shared memory of the CTA, of a warp
+  static constexpr CUtensorMapDataType TYPE = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  uint32_t qa[MT][4], ql[MT][2];
+  float m, l, o[MT][4];
+
+  // This lane's words of the query rows q [G][D].
+  static __device__ void fetch_q(const void* q, int G, uint32_t (&raw)[QREGS]) {
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
+    const uint32_t* w = static_cast<const uint32_t*>(q) + (size_t)min(g, G - 1) * (D / 2) + t;
+#pragma unroll
+    for (int i = 0; i < QREGS; ++i) raw[i] = g < G ? __ldg(w + 4 * i) : 0u;  // pairs t + 4 i
+  }
+  __device__ void begin(const uint32_t (&raw)[QREGS], const float2* cs, int G, float2*) {
+    const int t = threadIdx.x & 3;
+#pragma unroll
+    for (int i = 0; i < QREGS; ++i) {
+      const float2 a = cs[t + 4 * i];
+      const float x0 = bf16_lo(raw[i]), x1 = bf16_hi(raw[i]);
+      const float y0 = x0 * a.x - x1 * a.y, y1 = x0 * a.y + x1 * a.x;
+      const uint32_t hi = pack_bf16(y0, y1);
+      qa[i >> 1][2 * (i & 1)] = hi;
+      split_bf16(y0 - bf16_lo(hi), y1 - bf16_hi(hi), qa[i >> 1][2 * (i & 1) + 1], ql[i >> 1][i & 1]);
+    }
+    m = -INFINITY;
+    l = 0.f;
+#pragma unroll
+    for (int i = 0; i < OREGS; ++i) o[i >> 2][i & 3] = 0.f;
+  }
+  __device__ void scale_o(float a) {
+    const int t = threadIdx.x & 3;
+    const float a0 = __shfl_sync(0xffffffffu, a, 8 * t), a1 = __shfl_sync(0xffffffffu, a, 8 * t + 4);
+#pragma unroll
+    for (int i = 0; i < OREGS; ++i) o[i >> 2][i & 3] *= (i & 1) ? a1 : a0;
+  }
+  // One group: K at kb, V at vb, its first n tokens count; logits [G][stride] at the group, or null.
+  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, const float2*,
+                       float*) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    // ldmatrix: this lane's row of the group and 16-byte chunk of a 16-column slab
+    const int lrow = (lane & 7) + ((lane >> 4) << 3), lch = (lane >> 3) & 1;
+    auto chunk_at = [&](int slab) {
+      const int ch = 2 * slab + lch;
+      return (ch >> 3) * (PAGED_GROUP * 128) + lrow * 128 + (((ch & 7) ^ (lrow & 7)) << 4);
+    };
+    float za[2][4] = {}, zb[2][4] = {};
+#pragma unroll
+    for (int s = 0; s < MT; ++s) {
+      uint32_t b0, b1, b2, b3;
+      ldsm_x4(kb + chunk_at(s), b0, b1, b2, b3);
+      mma_bf16_16816(za[0], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b0, b1);
+      mma_bf16_16816(za[1], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b2, b3);
+      mma_bf16_16816(zb[0], ql[s][0], 0u, ql[s][1], 0u, b0, b1);
+      mma_bf16_16816(zb[1], ql[s][0], 0u, ql[s][1], 0u, b2, b3);
+    }
+    float z[4];  // head g, tokens 2t, 2t + 1, 2t + 8, 2t + 9
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      z[i] = (zb[i >> 1][i & 1] + za[i >> 1][2 + (i & 1)]) + za[i >> 1][i & 1];
+      if (2 * t + (i & 1) + 8 * (i >> 1) >= n) z[i] = -INFINITY;
+    }
+    if (logits && g < G) {
+      float* at = logits + (size_t)g * stride + 2 * t;
+      *reinterpret_cast<float2*>(at) = make_float2(z[0], z[1]);
+      *reinterpret_cast<float2*>(at + 8) = make_float2(z[2], z[3]);
+    }
+    float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+    if (__any_sync(0xffffffffu, mx > m)) {
+      const float mn = fmaxf(m, mx);
+      const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
+      m = mn;
+      l *= a;
+      scale_o(a);
+    }
+    const float ms = m == -INFINITY ? 0.f : m;
+    float w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      w[i] = exp2f(z[i] - ms);
+      l += w[i];
+    }
+    uint32_t h0, h1, l0, l1;
+    split_bf16(w[0], w[1], h0, l0);
+    split_bf16(w[2], w[3], h1, l1);
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+      uint32_t a0, a1, a2, a3;
+      ldsm_x4_t(vb + chunk_at(i), a0, a1, a2, a3);
+      mma_bf16_16816(o[i], a0, a1, a2, a3, h0, h1);
+      mma_bf16_16816(o[i], a0, a1, a2, a3, l0, l1);
+    }
+  }
+  __device__ void finish() {
+    l += __shfl_xor_sync(0xffffffffu, l, 1);
+    l += __shfl_xor_sync(0xffffffffu, l, 2);
+  }
+  // The record of a warp: OREGS x 32 floats lane by lane, and (m, l) of 8 heads.
+  __device__ void put(float* rec, float2* ml) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < OREGS; ++i) rec[i * 32 + lane] = o[i >> 2][i & 3];
+    if ((lane & 3) == 0) ml[lane >> 2] = make_float2(m, l);
+  }
+  __device__ void add(const float* rec, const float2* ml) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+    const float2 other = ml[lane >> 2];
+    const float M = fmaxf(m, other.x), Ms = M == -INFINITY ? 0.f : M;
+    const float a = exp2f(m - Ms), e = exp2f(other.x - Ms);
+    m = M;
+    l = l * a + other.y * e;
+    scale_o(a);
+    const float e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+#pragma unroll
+    for (int i = 0; i < OREGS; ++i) o[i >> 2][i & 3] += rec[i * 32 + lane] * ((i & 1) ? e1 : e0);
+  }
+  // Head and dim of float i of a record.
+  static __device__ void place(int i, int& head, int& dim) {
+    const int lane = i & 31, e = (i >> 5) & 3;
+    head = (lane & 3) * 2 + (e & 1);
+    dim = (i >> 7) * 16 + (lane >> 2) + (e >> 1) * 8;
+  }
+};
+
+// ------------------------------------------------- fp32: CUDA cores
+// Lane (token, half) = (lane % 16, lane / 16) takes half of the dims of its
+// token's logits, K four dims at a time from its row and the query's from an
+// address all tokens share; for o a lane holds D / 32 dims of every head and
+// reads the weights of a token as a broadcast.  GP: heads in registers, 4 or 8.
+template <int D, int GP>
+struct MathF32 {
+  using T = float;
+  static constexpr int CTAS = 1;
+  static constexpr int E = D / 32;
+  static constexpr int OREGS = GP * E;
+  static constexpr int QREGS = 2;
+  static constexpr int QUERY = GP * D * 4, SCRATCH = PAGED_GROUP * GP * 4;  // the query; a group's weights
+  static constexpr CUtensorMapDataType TYPE = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
+  float m[GP], l[GP], o[GP][E];
+
+  // (the raw query is read when a unit begins: the address is what is fetched ahead)
+  static __device__ void fetch_q(const void* q, int, uint32_t (&raw)[QREGS]) {
+    raw[0] = (uint32_t)reinterpret_cast<uintptr_t>(q);
+    raw[1] = (uint32_t)(reinterpret_cast<uintptr_t>(q) >> 32);
+  }
+  __device__ void begin(const uint32_t (&raw)[QREGS], const float2* cs, int G, float2* query) {
+    const float2* q = reinterpret_cast<const float2*>((uintptr_t)raw[0] | ((uintptr_t)raw[1] << 32));
+    for (int i = threadIdx.x; i < GP * (D / 2); i += AT_NT) {
+      const float2 x = i < G * (D / 2) ? __ldg(q + i) : make_float2(0.f, 0.f), a = cs[i % (D / 2)];
+      query[i] = make_float2(x.x * a.x - x.y * a.y, x.x * a.y + x.y * a.x);
     }
     __syncthreads();
-    float m[G_MAX], l[G_MAX], o[G_MAX][E];
 #pragma unroll
-    for (int g = 0; g < G_MAX; ++g) {
+    for (int g = 0; g < GP; ++g) {
       m[g] = -INFINITY;
       l[g] = 0.f;
 #pragma unroll
       for (int e = 0; e < E; ++e) o[g][e] = 0.f;
     }
-    for (int x = sg.x + warp; x < sg.seg_end(); x += AT_NW) {
-      const int t0 = (x - sg.unit_begin) * PAGED_GROUP, n = min(PAGED_GROUP, len - t0);
-      const int page = p.page_table[(size_t)b * p.max_pages + (t0 >> p.log2_page)];
-      const long long row = paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, t0);
-      if (row < 0 && lane == 0) atomicOr(p.status, 1);
-      for (int i = 0; i < n; ++i) {
-        float k[E], v[E];
+  }
+  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, const float2* query,
+                       float* ps) {
+    const int lane = threadIdx.x & 31, tok = lane & 15, half = lane >> 4;
+    const float4* qs = reinterpret_cast<const float4*>(query) + half * (D / 8);
+    float z[GP];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) z[g] = 0.f;
+#pragma unroll 4
+    for (int c = 0; c < D / 8; ++c) {
+      const int ch = half * (D / 8) + c;
+      float4 k;
+      asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                   : "=f"(k.x), "=f"(k.y), "=f"(k.z), "=f"(k.w)
+                   : "r"(kb + (ch >> 3) * (PAGED_GROUP * 128) + tok * 128 + (((ch & 7) ^ (tok & 7)) << 4))
+                   : "memory");
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float4 q = qs[g * (D / 4) + c];
+        z[g] = fmaf(k.x, q.x, fmaf(k.y, q.y, fmaf(k.z, q.z, fmaf(k.w, q.w, z[g]))));
+      }
+    }
+    bool up = false;
+    float mx[GP];
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      z[g] += __shfl_xor_sync(0xffffffffu, z[g], 16);
+      if (tok >= n) z[g] = -INFINITY;
+      if (logits && g < G && half == 0) logits[(size_t)g * stride + tok] = z[g];
+      mx[g] = z[g];
+#pragma unroll
+      for (int s = 1; s < 16; s <<= 1) mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], s));
+      up = up || mx[g] > m[g];
+    }
+    if (up) {  // the same for the whole warp
+#pragma unroll
+      for (int g = 0; g < GP; ++g) {
+        const float mn = fmaxf(m[g], mx[g]);
+        const float a = mn == -INFINITY ? 1.f : exp2f(m[g] - mn);
+        m[g] = mn;
+        l[g] *= a;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[g][e] *= a;
+      }
+    }
+    __syncwarp();  // the last group's weights are read
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      const float w = exp2f(z[g] - (m[g] == -INFINITY ? 0.f : m[g]));
+      if (half == 0) {
+        l[g] += w;
+        ps[tok * GP + g] = w;
+      }
+    }
+    __syncwarp();
+#pragma unroll 4
+    for (int i = 0; i < PAGED_GROUP; ++i) {
+      float v[E];
+      const int ch = lane * E / 4;
+      const uint32_t at = vb + (ch >> 3) * (PAGED_GROUP * 128) + i * 128 + (((ch & 7) ^ (i & 7)) << 4);
+      if constexpr (E == 4)
+        asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];"
+                     : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3])
+                     : "r"(at)
+                     : "memory");
+      else
+        asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[0]), "=f"(v[1]) : "r"(at + 8 * (lane & 1)) : "memory");
+#pragma unroll
+      for (int g4 = 0; g4 < GP; g4 += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(ps + i * GP + g4);
 #pragma unroll
         for (int e = 0; e < E; ++e) {
-          k[e] = row < 0 ? 0.f : to_f32<T>(static_cast<const T*>(p.k_pages)[(size_t)(row + i) * D + lane * E + e]);
-          v[e] = row < 0 ? 0.f : to_f32<T>(static_cast<const T*>(p.v_pages)[(size_t)(row + i) * D + lane * E + e]);
-        }
-#pragma unroll
-        for (int g = 0; g < G_MAX; ++g) {
-          if (g >= G) break;
-          float z = 0.f;
-#pragma unroll
-          for (int e = 0; e < E; ++e) z += qs[g * D + lane * E + e] * k[e];
-#pragma unroll
-          for (int s = 16; s; s >>= 1) z += __shfl_xor_sync(0xffffffffu, z, s);
-          if (row < 0) z = -INFINITY;
-          if (p.weight && lane == 0) p.logits[((size_t)unit * G + g) * p.T_cap + t0 + i] = z;
-          const float mn = fmaxf(m[g], z);
-          const float ms = mn == -INFINITY ? 0.f : mn;
-          const float a = exp2f(m[g] - ms), w = exp2f(z - ms);
-          m[g] = mn;
-          l[g] = l[g] * a + w;
-#pragma unroll
-          for (int e = 0; e < E; ++e) o[g][e] = o[g][e] * a + w * v[e];
+          o[g4][e] = fmaf(w.x, v[e], o[g4][e]);
+          o[g4 + 1][e] = fmaf(w.y, v[e], o[g4 + 1][e]);
+          o[g4 + 2][e] = fmaf(w.z, v[e], o[g4 + 2][e]);
+          o[g4 + 3][e] = fmaf(w.w, v[e], o[g4 + 3][e]);
         }
       }
     }
-    // the warps' parts, in warp order
-#pragma unroll
-    for (int g = 0; g < G_MAX; ++g) {
-      if (g >= G) break;
-#pragma unroll
-      for (int e = 0; e < E; ++e) mrg[(warp * G + g) * D + lane * E + e] = o[g][e];
-      if (lane == 0) {
-        mml[(warp * G + g) * 2] = m[g];
-        mml[(warp * G + g) * 2 + 1] = l[g];
-      }
-    }
-    __syncthreads();
-    const bool whole = sg.x == sg.unit_begin && sg.unit_end <= r1;
-    float* rec = p.records + (size_t)(2 * c + (sg.unit_begin < r0 ? 0 : 1)) * paged_record_floats(G, D);
-    for (int i = tid; i < G * D; i += AT_NT) {
-      const int g = i / D;
-      float M = -INFINITY;
-      for (int w = 0; w < AT_NW; ++w) M = fmaxf(M, mml[(w * G + g) * 2]);
-      const float Ms = M == -INFINITY ? 0.f : M;
-      float L = 0.f, O = 0.f;
-      for (int w = 0; w < AT_NW; ++w) {
-        const float a = exp2f(mml[(w * G + g) * 2] - Ms);
-        L += mml[(w * G + g) * 2 + 1] * a;
-        O += mrg[w * G * D + i] * a;
-      }
-      if (whole) {
-        p.out[((size_t)b * p.Hq + h * G) * D + i] = L > 0.f ? O / L : 0.f;
-        if (p.weight && i == g * D) p.lse[(size_t)unit * G + g] = L > 0.f ? M + log2f(L) : INFINITY;
-      } else {
-        rec[i] = O;
-        if (i == g * D) {
-          rec[G * D + g] = M;
-          rec[G * D + G + g] = L;
-        }
-      }
-    }
-    if (tid == 0 && sg.unit_begin >= r0 && sg.unit_end > r1)
-      p.joins[c] = make_int2(unit, paged_part_of(total, parts, sg.unit_end - 1));
-    __syncthreads();
-    sg.next();
   }
-}
+  __device__ void finish() {
+#pragma unroll
+    for (int g = 0; g < GP; ++g)
+#pragma unroll
+      for (int s = 1; s < 32; s <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], s);
+  }
+  __device__ void put(float* rec, float2* ml) const {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) rec[(g * E + e) * 32 + lane] = o[g][e];
+      if (lane == g) ml[g] = make_float2(m[g], l[g]);
+    }
+  }
+  __device__ void add(const float* rec, const float2* ml) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int g = 0; g < GP; ++g) {
+      const float2 other = ml[g];
+      const float M = fmaxf(m[g], other.x), Ms = M == -INFINITY ? 0.f : M;
+      const float a = exp2f(m[g] - Ms), b = exp2f(other.x - Ms);
+      m[g] = M;
+      l[g] = l[g] * a + other.y * b;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[g][e] = o[g][e] * a + rec[(g * E + e) * 32 + lane] * b;
+    }
+  }
+  static __device__ void place(int i, int& head, int& dim) {
+    const int r = i >> 5;
+    head = r / E;
+    dim = (i & 31) * E + r % E;
+  }
+};
 
-// ------------------------------------------------------ bf16: tensor cores
-// A warp takes a group of 16 tokens at a time, through a ring of its own in
-// shared memory that TMA fills (one copy of 16 rows for K, one for V, in the
-// 128-byte swizzle, so that ldmatrix reads without bank conflicts), and no
-// warp waits for another before a unit's end.
-//   z^T: rows of A the heads, B the tokens.  The rotated and scaled query is
-//   three bf16 terms (24 bits: the logits are as exact as fp32's), the first
-//   two as rows 0-7 and 8-15 of one operand, the third as another.
-//   o^T = V^T P^T: the z fragment is the P fragment of the same lane, in two
-//   bf16 terms (16 bits of a weight that is summed with others), V read
-//   transposed.
-constexpr int TC_NW = 8;
-constexpr int TC_NT = TC_NW * 32;
-
-template <int D>
-struct Tc {
-  static constexpr int HALF = PAGED_GROUP * 128;        // bytes of 64 columns of a group
-  static constexpr int ROWS = (D / 64) * HALF;          // K or V of a group
+// ------------------------------------------------------------- attend
+// Shared memory from a 1024-byte boundary: the warps' rings; two records and
+// their (m, l); cos and sin of the sequence's position; and what follows.
+template <int D, class M>
+struct Plan {
+  static constexpr int SLABS = D * (int)sizeof(typename M::T) / 128;  // 128-byte columns of a row
+  static constexpr int ROWS = SLABS * PAGED_GROUP * 128;              // K or V of a group
   static constexpr int STAGE = 2 * ROWS;
-  static constexpr int STAGES = 196608 / (TC_NW * STAGE);
-  static constexpr int MT = D / 16;
-  static constexpr int OREGS = 4 * MT;
-  // shared memory, from a 1024-byte boundary
-  static constexpr int OFF_MRG = TC_NW * STAGES * STAGE;             // [4][OREGS][32] floats
-  static constexpr int OFF_ML = OFF_MRG + 4 * OREGS * 32 * 4;        // [4][8] (m, l)
-  static constexpr int OFF_CS = OFF_ML + 4 * 8 * 8;                  // [D/2] (cos, sin)
+  static constexpr int STAGES = 196608 / M::CTAS / (AT_NW * STAGE);
+  static constexpr int OFF_REC = AT_NW * STAGES * STAGE;
+  static constexpr int OFF_ML = OFF_REC + 2 * M::OREGS * 32 * 4;
+  static constexpr int OFF_CS = OFF_ML + 2 * 8 * 8;
   static constexpr int OFF_TURNS = OFF_CS + D / 2 * 8;
-  static constexpr int OFF_BAR = OFF_TURNS + D / 2 * 8;
-  static constexpr int OFF_HELD = OFF_BAR + TC_NW * STAGES * 8;      // whether a stage's page is in the pool
-  static constexpr int OFF_SCAN = OFF_HELD + TC_NW * STAGES * 4;
-  static constexpr int OFF_PRE = OFF_SCAN + 32 * 4;
+  static constexpr int OFF_QUERY = OFF_TURNS + D / 2 * 8;
+  static constexpr int OFF_SCRATCH = OFF_QUERY + M::QUERY;
+  static constexpr int OFF_BAR = OFF_SCRATCH + AT_NW * M::SCRATCH;
+  static constexpr int OFF_HELD = OFF_BAR + AT_NW * STAGES * 8;  // whether a stage's page is in the pool
+  static constexpr int OFF_SCAN = OFF_HELD + AT_NW * STAGES * 4;
+  static constexpr int OFF_LINE = OFF_SCAN + AT_NW * 4;
+  static constexpr int bytes(int B) { return 1024 + OFF_LINE + (B + 1) * 4; }
+  static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits one CTA");
 };
 
 __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
@@ -276,54 +452,57 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
       : "memory");
 }
 
-template <int D>
-__global__ void __launch_bounds__(TC_NT, 1)
-    paged_attend_bf16_kernel(const __grid_constant__ PagedAttendParams p, const __grid_constant__ CUtensorMap kmap,
-                             const __grid_constant__ CUtensorMap vmap) {
-  using C = Tc<D>;
-  constexpr int S = C::STAGES, MT = C::MT;
+template <int D, class M>
+__global__ void __launch_bounds__(AT_NT, M::CTAS)
+    paged_attend_kernel(const __grid_constant__ PagedAttendParams p, const __grid_constant__ CUtensorMap kmap,
+                        const __grid_constant__ CUtensorMap vmap) {
+  using P = Plan<D, M>;
+  constexpr int S = P::STAGES;
   extern __shared__ __align__(16) char raw[];
   char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int g = lane >> 2, t = lane & 3;
   const int G = p.G;
-  float* mrg = reinterpret_cast<float*>(sm + C::OFF_MRG);
-  float2* ml = reinterpret_cast<float2*>(sm + C::OFF_ML);
-  float2* cs = reinterpret_cast<float2*>(sm + C::OFF_CS);
-  unsigned long long* turns = reinterpret_cast<unsigned long long*>(sm + C::OFF_TURNS);
-  int* held = reinterpret_cast<int*>(sm + C::OFF_HELD) + warp * S;
-  int* scan = reinterpret_cast<int*>(sm + C::OFF_SCAN);
-  int* pre = reinterpret_cast<int*>(sm + C::OFF_PRE);
-  const uint32_t ring = smem_u32(sm) + warp * S * C::STAGE;
-  const uint32_t bars = smem_u32(sm + C::OFF_BAR) + warp * S * 8;
+  float* recs = reinterpret_cast<float*>(sm + P::OFF_REC);
+  float2* ml = reinterpret_cast<float2*>(sm + P::OFF_ML);
+  float2* cs = reinterpret_cast<float2*>(sm + P::OFF_CS);
+  unsigned long long* turns = reinterpret_cast<unsigned long long*>(sm + P::OFF_TURNS);
+  float2* query = reinterpret_cast<float2*>(sm + P::OFF_QUERY);
+  float* scratch = reinterpret_cast<float*>(sm + P::OFF_SCRATCH + warp * M::SCRATCH);
+  int* held = reinterpret_cast<int*>(sm + P::OFF_HELD) + warp * S;
+  unsigned* words = reinterpret_cast<unsigned*>(sm + P::OFF_LINE);
+  const uint32_t ring = smem_u32(sm) + warp * S * P::STAGE;
+  const uint32_t bars = smem_u32(sm + P::OFF_BAR) + warp * S * 8;
+  // the join's blocks may take their places: they wait for this grid's end
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(bars + 8 * i, 1);
     fence_mbar_init();
   }
   // (lanes reading different parameter words take turns: a few lanes of each warp)
-  if (lane < D / 2 / TC_NW) turns[warp * (D / 2 / TC_NW) + lane] = p.rope_turns[warp * (D / 2 / TC_NW) + lane];
-  group_prefix<TC_NT>(p, pre, scan, blockIdx.x == 0);
-  const int total = pre[p.B] * p.Hkv;
+  constexpr int TW = D / 2 / AT_NW;
+  if (lane < TW) turns[warp * TW + lane] = p.rope_turns[warp * TW + lane];
+  make_line<AT_NT>(p, words, reinterpret_cast<int*>(sm + P::OFF_SCAN), blockIdx.x == 0);
+  const Line line{words, p.B, p.Hkv};
+  const int total = line.total();
   const int parts = paged_parts(total, p.grid);
   const int c = blockIdx.x;
   for (int b = c; b < p.B; b += p.grid)  // sequences without a token: zeros
-    if (pre[b] == pre[b + 1])
-      for (int i = tid; i < p.Hq * D; i += TC_NT) p.out[(size_t)b * p.Hq * D + i] = 0.f;
-  if (tid == 0) p.joins[c] = make_int2(-1, 0);
+    if (line.groups(b) == 0)
+      for (int i = tid; i < p.Hq * D; i += AT_NT) p.out[(size_t)b * p.Hq * D + i] = 0.f;
   if (c >= parts) return;
   const int r0 = paged_part_begin(total, parts, c), r1 = paged_part_begin(total, parts, c + 1);
 
-  // This warp's groups: x = r0 + warp + k * TC_NW, k < mine.  Lane i holds the
+  // This warp's groups: x = r0 + warp + k * AT_NW, k < mine.  Lane i holds the
   // pool row of group (batch of 32) + i.
-  const int mine = max(0, (r1 - r0 - warp + TC_NW - 1) / TC_NW);
-  int rows = -1, issued = 0;
+  const int mine = max(0, (r1 - r0 - warp + AT_NW - 1) / AT_NW);
+  int rows = -1, issued = 0, landed = 0;
   bool dead = false;  // a wait ran out: nothing more is copied or waited for
   auto look_up = [&](int k) {
-    const int x = r0 + warp + (k + lane) * TC_NW;
+    const int x = r0 + warp + (k + lane) * AT_NW;
     rows = -1;
     if (k + lane < mine) {
-      const int b = sequence_of(pre, p.B, p.Hkv, x);
-      const int n = pre[b + 1] - pre[b], rem = x - pre[b] * p.Hkv;
+      const int b = line.sequence_of(x);
+      const int n = line.groups(b), rem = x - line.before(b) * p.Hkv;
       const int h = rem / n, slot = (rem - h * n) * PAGED_GROUP;
       const int page = __ldg(p.page_table + (size_t)b * p.max_pages + (slot >> p.log2_page));
       rows = (int)paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, slot);
@@ -337,11 +516,11 @@ __global__ void __launch_bounds__(TC_NT, 1)
     const int st = issued % S;
     if (lane == 0) {
       held[st] = row >= 0;
-      const uint32_t bar = bars + 8 * st, dst = ring + st * C::STAGE;
+      const uint32_t bar = bars + 8 * st, dst = ring + st * P::STAGE;
       if (row >= 0) {
-        mbar_arrive_expect_tx(bar, C::STAGE);
+        mbar_arrive_expect_tx(bar, P::STAGE);
         tma_rows(dst, &kmap, row, bar);
-        tma_rows(dst + C::ROWS, &vmap, row, bar);
+        tma_rows(dst + P::ROWS, &vmap, row, bar);
       } else {
         mbar_arrive(bar);
       }
@@ -350,267 +529,253 @@ __global__ void __launch_bounds__(TC_NT, 1)
   };
   for (int i = 0; i < S; ++i) issue();
 
-  // ldmatrix: lane's row of the group and 16-byte chunk of a 16-column slab
-  const int lrow = (lane & 7) + ((lane >> 4) << 3), lch = (lane >> 3) & 1;
-  auto chunk_at = [&](int slab) {  // byte offset in K or V of a group
-    const int ch = 2 * slab + lch;
-    return (ch >> 3) * C::HALF + lrow * 128 + (((ch & 7) ^ (lrow & 7)) << 4);
+  auto query_of = [&](const Segments& s) {
+    return static_cast<const void*>(static_cast<const typename M::T*>(p.q) + ((size_t)s.b * p.Hq + s.h * G) * D);
   };
-
+  auto turn = [&](int i, int n, int pos) {  // cos and sin of a position, by n threads
+    for (int f = i; f < D / 2; f += n) {
+      const float2 a = rope_cos_sin(turns[f], pos);
+      cs[f] = make_float2(a.x * p.scale, a.y * p.scale);
+    }
+  };
   Segments sg;
-  sg.start(pre, p.B, p.Hkv, r0, r1);
-  int k = 0, cur_b = -1;
-  while (sg.at()) {
-    const int b = sg.b, h = sg.h, unit = b * p.Hkv + h;
-    const int len = clamped_len(p, b);
-    if (b != cur_b) {
-      for (int f = tid; f < D / 2; f += TC_NT) {
-        const float2 a = rope_cos_sin(turns[f], p.pos[b]);
-        cs[f] = make_float2(a.x * p.scale, a.y * p.scale);
-      }
-      cur_b = b;
-      __syncthreads();
+  sg.start(line, r0, r1);
+  sg.at();
+  uint32_t q_raw[M::QREGS];
+  M::fetch_q(query_of(sg), G, q_raw);
+  turn(tid, AT_NT, p.pos[sg.b]);
+  __syncthreads();
+  int k = 0;
+  while (true) {
+    const int b = sg.b, unit = sg.unit(), len = line.tokens(b);
+    M mt;
+    mt.begin(q_raw, cs, G, query);
+    // the next unit's query and position are under way meanwhile
+    Segments nx = sg;
+    nx.next();
+    const bool more = nx.at();
+    int next_pos = 0;
+    if (more) {
+      M::fetch_q(query_of(nx), G, q_raw);
+      next_pos = __ldg(p.pos + nx.b);
     }
-    // the query fragments: three terms of q of head g, zeros behind the last head
-    uint32_t qa[MT][4], ql[MT][2];
-    {
-      const uint32_t* q = static_cast<const uint32_t*>(p.q) + ((size_t)b * p.Hq + h * G + min(g, G - 1)) * (D / 2);
-#pragma unroll
-      for (int s = 0; s < MT; ++s)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const int f = 8 * s + t + 4 * e;
-          const uint32_t w = g < G ? __ldg(q + f) : 0u;
-          const float2 a = cs[f];
-          const float x0 = bf16_lo(w), x1 = bf16_hi(w);
-          const float y0 = x0 * a.x - x1 * a.y, y1 = x0 * a.y + x1 * a.x;
-          const uint32_t hi = pack_bf16(y0, y1);
-          const float u0 = y0 - bf16_lo(hi), u1 = y1 - bf16_hi(hi);
-          split_bf16(u0, u1, qa[s][2 * e + 1], ql[s][e]);
-          qa[s][2 * e] = hi;
-        }
-    }
-    float m = -INFINITY, l = 0.f, o[MT][4];
-#pragma unroll
-    for (int i = 0; i < MT; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-    float* logits = p.weight ? p.logits + ((size_t)unit * G + g) * p.T_cap + 2 * t : nullptr;
-
-    for (; k < mine && r0 + warp + k * TC_NW < sg.seg_end(); ++k) {
-      const int t0 = (r0 + warp + k * TC_NW - sg.unit_begin) * PAGED_GROUP;
+    float* logits = p.weight ? p.logits + (size_t)unit * G * p.T_cap : nullptr;
+    for (; k < mine && r0 + warp + k * AT_NW < sg.seg_end(); ++k) {
+      const int t0 = (r0 + warp + k * AT_NW - sg.unit_begin) * PAGED_GROUP;
       const int st = k % S;
-      const uint32_t kb = ring + st * C::STAGE, vb = kb + C::ROWS;
+      const uint32_t kb = ring + st * P::STAGE, vb = kb + P::ROWS;
       if (!dead && !mbar_wait_bounded(bars + 8 * st, (k / S) & 1, p.wait_ns)) {
         if (lane == 0) atomicOr(p.status, 2);
         dead = true;
       }
       dead = __any_sync(0xffffffffu, dead);
+      if (!dead) landed = k + 1;
       __syncwarp();
       const int n = held[st] && !dead ? min(PAGED_GROUP, len - t0) : 0;
-      if (n < PAGED_GROUP) {  // what lies behind the end counts for nothing, NaN neither
-        for (int i = lane; i < (PAGED_GROUP - n) * (D / 8); i += 32) {
-          const int r = n + i / (D / 8), ch = i % (D / 8);
-          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (ch >> 3) * C::HALF + r * 128 + ((ch & 7) << 4)),
+      if (n < PAGED_GROUP) {  // V rows behind the end count for nothing, NaN neither
+        for (int i = lane; i < (PAGED_GROUP - n) * P::SLABS * 8; i += 32) {
+          const int r = n + i / (P::SLABS * 8), ch = i % (P::SLABS * 8);
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (ch >> 3) * (PAGED_GROUP * 128) + r * 128 +
+                                                                        ((ch & 7) << 4)),
                        "r"(0)
                        : "memory");
         }
         fence_proxy_async();
         __syncwarp();
       }
-      float za[2][4] = {}, zb[2][4] = {};
-#pragma unroll
-      for (int s = 0; s < MT; ++s) {
-        uint32_t b0, b1, b2, b3;
-        ldsm_x4(kb + chunk_at(s), b0, b1, b2, b3);
-        mma_bf16_16816(za[0], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b0, b1);
-        mma_bf16_16816(za[1], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b2, b3);
-        mma_bf16_16816(zb[0], ql[s][0], 0u, ql[s][1], 0u, b0, b1);
-        mma_bf16_16816(zb[1], ql[s][0], 0u, ql[s][1], 0u, b2, b3);
-      }
-      float z[4];  // head g, tokens 2t, 2t + 1, 2t + 8, 2t + 9
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        z[i] = (zb[i >> 1][i & 1] + za[i >> 1][2 + (i & 1)]) + za[i >> 1][i & 1];
-        if (2 * t + (i & 1) + 8 * (i >> 1) >= n) z[i] = -INFINITY;
-      }
-      if (logits && g < G) {
-        *reinterpret_cast<float2*>(logits + t0) = make_float2(z[0], z[1]);
-        *reinterpret_cast<float2*>(logits + t0 + 8) = make_float2(z[2], z[3]);
-      }
-      float mx = fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-      if (__any_sync(0xffffffffu, mx > m)) {
-        const float mn = fmaxf(m, mx);
-        const float a = mn == -INFINITY ? 1.f : exp2f(m - mn);
-        m = mn;
-        l *= a;
-        const float a0 = __shfl_sync(0xffffffffu, a, 8 * t), a1 = __shfl_sync(0xffffffffu, a, 8 * t + 4);
-#pragma unroll
-        for (int i = 0; i < MT; ++i) {
-          o[i][0] *= a0;
-          o[i][1] *= a1;
-          o[i][2] *= a0;
-          o[i][3] *= a1;
-        }
-      }
-      const float ms = m == -INFINITY ? 0.f : m;
-      float w[4];
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        w[i] = exp2f(z[i] - ms);
-        l += w[i];
-      }
-      uint32_t h0, h1, l0, l1;
-      split_bf16(w[0], w[1], h0, l0);
-      split_bf16(w[2], w[3], h1, l1);
-#pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        uint32_t a0, a1, a2, a3;
-        ldsm_x4_t(vb + chunk_at(i), a0, a1, a2, a3);
-        mma_bf16_16816(o[i], a0, a1, a2, a3, h0, h1);
-        mma_bf16_16816(o[i], a0, a1, a2, a3, l0, l1);
-      }
+      mt.step(kb, vb, n, logits ? logits + t0 : nullptr, p.T_cap, G, query, scratch);
       __syncwarp();
       issue();
     }
-
-    // the eight warps' parts: 4-7 into 0-3 lane by lane, then four records
-    l += __shfl_xor_sync(0xffffffffu, l, 1);
-    l += __shfl_xor_sync(0xffffffffu, l, 2);
-    float* dump = mrg + (warp & 3) * C::OREGS * 32 + lane;
-    auto put = [&]() {
-#pragma unroll
-      for (int i = 0; i < C::OREGS; ++i) dump[i * 32] = o[i >> 2][i & 3];
-      if (t == 0) ml[(warp & 3) * 8 + g] = make_float2(m, l);
-    };
-    if (warp >= 4) put();
+    // the warps' parts, in a fixed order: 2 and 3 into 0 and 1, then both
+    mt.finish();
+    if (warp >= 2) mt.put(recs + (warp - 2) * M::OREGS * 32, ml + (warp - 2) * 8);
     __syncthreads();
-    if (warp < 4) {
-      const float2 other = ml[warp * 8 + g];
-      const float M = fmaxf(m, other.x), Ms = M == -INFINITY ? 0.f : M;
-      const float a = exp2f(m - Ms), e = exp2f(other.x - Ms);
-      m = M;
-      l = l * a + other.y * e;
-      const float a0 = __shfl_sync(0xffffffffu, a, 8 * t), a1 = __shfl_sync(0xffffffffu, a, 8 * t + 4);
-      const float e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
-#pragma unroll
-      for (int i = 0; i < C::OREGS; ++i)
-        o[i >> 2][i & 3] = o[i >> 2][i & 3] * ((i & 1) ? a1 : a0) + dump[i * 32] * ((i & 1) ? e1 : e0);
+    if (warp < 2) {
+      mt.add(recs + warp * M::OREGS * 32, ml + warp * 8);
       __syncwarp();
-      put();
+      mt.put(recs + warp * M::OREGS * 32, ml + warp * 8);
+    } else if (more && nx.b != b) {
+      turn(tid - 64, 64, next_pos);
     }
     __syncthreads();
     const bool whole = sg.x == sg.unit_begin && sg.unit_end <= r1;
     float* rec = p.records + (size_t)(2 * c + (sg.unit_begin < r0 ? 0 : 1)) * paged_record_floats(G, D);
-    for (int i = tid; i < C::OREGS * 32; i += TC_NT) {
-      const int ln = i & 31, e = (i >> 5) & 3;
-      const int hd = (ln & 3) * 2 + (e & 1), dim = (i >> 7) * 16 + (ln >> 2) + (e >> 1) * 8;
+    for (int i = tid; i < M::OREGS * 32; i += AT_NT) {
+      int hd, dim;
+      M::place(i, hd, dim);
       if (hd >= G) continue;
-      float2 r[4];
-      float M = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        r[w] = ml[w * 8 + hd];
-        M = fmaxf(M, r[w].x);
-      }
-      const float Ms = M == -INFINITY ? 0.f : M;
-      float L = 0.f, O = 0.f;
-#pragma unroll
-      for (int w = 0; w < 4; ++w) {
-        const float a = exp2f(r[w].x - Ms);
-        L += r[w].y * a;
-        O += mrg[w * C::OREGS * 32 + i] * a;
-      }
+      const float2 e0 = ml[hd], e1 = ml[8 + hd];
+      const float X = fmaxf(e0.x, e1.x), Xs = X == -INFINITY ? 0.f : X;
+      const float a0 = exp2f(e0.x - Xs), a1 = exp2f(e1.x - Xs);
+      const float L = e0.y * a0 + e1.y * a1, O = recs[i] * a0 + recs[M::OREGS * 32 + i] * a1;
       if (whole) {
-        p.out[((size_t)b * p.Hq + h * G + hd) * D + dim] = L > 0.f ? O / L : 0.f;
-        if (p.weight && dim == 0) p.lse[(size_t)unit * G + hd] = L > 0.f ? M + log2f(L) : INFINITY;
+        p.out[((size_t)unit * G + hd) * D + dim] = L > 0.f ? O / L : 0.f;
+        if (p.weight && dim == 0) p.lse[(size_t)unit * G + hd] = L > 0.f ? X + log2f(L) : INFINITY;
       } else {
         rec[hd * D + dim] = O;
         if (dim == 0) {
-          rec[G * D + hd] = M;
+          rec[G * D + hd] = X;
           rec[G * D + G + hd] = L;
         }
       }
     }
-    if (tid == 0 && sg.unit_begin >= r0 && sg.unit_end > r1)
-      p.joins[c] = make_int2(unit, paged_part_of(total, parts, sg.unit_end - 1));
+    if (!more) break;
     __syncthreads();
-    sg.next();
+    sg = nx;
   }
   // after a wait that ran out: no copy may land in memory of a block that is gone
-  if (dead)
-    for (; k < issued; ++k)
-      if (!mbar_wait_bounded(bars + 8 * (k % S), (k / S) & 1, p.wait_ns) && lane == 0) atomicOr(p.status, 4);
+  for (; landed < issued; ++landed)
+    if (!mbar_wait_bounded(bars + 8 * (landed % S), (landed / S) & 1, p.wait_ns) && lane == 0) atomicOr(p.status, 4);
 }
 
-// log2 of a cut unit's softmax denominator, from its parts' records: thread g.
-__device__ float joined_lse(const PagedAttendParams& p, int D, int g, int c0, int c1) {
-  const int R = paged_record_floats(p.G, D);
-  float M = -INFINITY, L = 0.f;
-  for (int c = c0; c <= c1; ++c) M = fmaxf(M, p.records[(size_t)(2 * c + (c == c0)) * R + p.G * D + g]);
-  const float Ms = M == -INFINITY ? 0.f : M;
-  for (int c = c0; c <= c1; ++c) {
-    const float* r = p.records + (size_t)(2 * c + (c == c0)) * R + p.G * D;
-    L += r[p.G + g] * exp2f(r[g] - Ms);
+// --------------------------------------------------------------- join
+// The scratch of one unit's parts: up to `grid` x G of (m, l).
+struct JoinShared {
+  float* m;    // [parts][G]; joined: each part's factor 2^(m - M) / L
+  float* l;    // [parts][G]
+  float* lse;  // [G]
+};
+
+// (m, l) of the parts c0 .. c1 of a unit: lse, and the parts' factors.
+__device__ void join_parts(const PagedAttendParams& p, int D, int c0, int c1, const JoinShared& js) {
+  const int G = p.G, n = (c1 - c0 + 1) * G, R = paged_record_floats(G, D);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += JN_NT) {
+    const int k = i / G, g = i - k * G;
+    const float* r = p.records + (size_t)(2 * (c0 + k) + (k == 0)) * R + G * D + g;
+    js.m[i] = __ldcg(r);
+    js.l[i] = __ldcg(r + G);
   }
-  return L > 0.f ? M + log2f(L) : INFINITY;
+  __syncthreads();
+  for (int g = warp; g < G; g += JN_NT / 32) {
+    float M = -INFINITY, L = 0.f;
+    for (int i = lane * G + g; i < n; i += 32 * G) M = fmaxf(M, js.m[i]);
+#pragma unroll
+    for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
+    const float Ms = M == -INFINITY ? 0.f : M;
+    for (int i = lane * G + g; i < n; i += 32 * G) L += js.l[i] * exp2f(js.m[i] - Ms);
+#pragma unroll
+    for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
+    const float inv = L > 0.f ? 1.f / L : 0.f;
+    for (int i = lane * G + g; i < n; i += 32 * G) js.m[i] = exp2f(js.m[i] - Ms) * inv;
+    if (lane == 0) js.lse[g] = L > 0.f ? M + log2f(L) : INFINITY;
+  }
+  __syncthreads();
 }
 
-// Block c: the unit that begins in part c and goes on; with weights then its
-// share of the line's tokens.
+// Block (c, y): 128 floats of the output of the unit that is cut between the
+// parts c and c + 1 and begins in c; with weights then its share of the line's
+// tokens.
 template <int D>
-__global__ void __launch_bounds__(AT_NT) paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
-  extern __shared__ __align__(16) float sm[];
+__global__ void __launch_bounds__(JN_NT) paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
+  extern __shared__ __align__(16) float shared[];
+  __shared__ float4 sums[JN_NT];
+  __shared__ int scan[JN_NT / 32];
   const int tid = threadIdx.x, c = blockIdx.x, G = p.G;
-  const int2 jn = c < p.grid ? p.joins[c] : make_int2(-1, 0);
-  if (jn.x >= 0) {
-    const int R = paged_record_floats(G, D);
-    for (int i = tid; i < G * D; i += AT_NT) {
+  JoinShared js;
+  js.m = shared;
+  js.l = js.m + p.grid * G;
+  js.lse = js.l + p.grid * G;
+  unsigned* words = reinterpret_cast<unsigned*>(js.lse + G_MAX);
+  make_line<JN_NT>(p, words, scan, false);
+  const Line line{words, p.B, p.Hkv};
+  const int total = line.total();
+  const int parts = paged_parts(total, p.grid);
+  Segments sg;
+  bool cut = false;
+  if (c + 1 < parts && total > 0) {
+    const int edge = paged_part_begin(total, parts, c + 1);
+    sg.start(line, edge - 1, edge);
+    sg.at();
+    cut = sg.unit_end > edge && paged_part_of(total, parts, sg.unit_begin) == c;
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (cut) {
+    const int c1 = paged_part_of(total, parts, sg.unit_end - 1), R = paged_record_floats(G, D);
+    join_parts(p, D, c, c1, js);
+    // lane: 4 floats; warp: every fourth part
+    const int i = blockIdx.y * 128 + 4 * (tid & 31);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i < G * D) {
       const int g = i / D;
-      float M = -INFINITY, L = 0.f, O = 0.f;
-      for (int k = c; k <= jn.y; ++k) M = fmaxf(M, p.records[(size_t)(2 * k + (k == c)) * R + G * D + g]);
-      const float Ms = M == -INFINITY ? 0.f : M;
-      for (int k = c; k <= jn.y; ++k) {
-        const float* r = p.records + (size_t)(2 * k + (k == c)) * R;
-        const float a = exp2f(r[G * D + g] - Ms);
-        L += r[G * D + G + g] * a;
-        O += r[i] * a;
+#pragma unroll 4
+      for (int k = tid >> 5; k <= c1 - c; k += JN_NT / 32) {
+        const float4 o =
+            __ldcg(reinterpret_cast<const float4*>(p.records + (size_t)(2 * (c + k) + (k == 0)) * R + i));
+        const float f = js.m[k * G + g];
+        a.x += o.x * f;
+        a.y += o.y * f;
+        a.z += o.z * f;
+        a.w += o.w * f;
       }
-      const int b = jn.x / p.Hkv, h = jn.x - b * p.Hkv;
-      p.out[((size_t)b * p.Hq + h * G) * D + i] = L > 0.f ? O / L : 0.f;
+    }
+    sums[tid] = a;
+    __syncthreads();
+    if (tid < 32 && i < G * D) {
+#pragma unroll
+      for (int w = 1; w < JN_NT / 32; ++w) {
+        const float4 b = sums[w * 32 + tid];
+        a.x += b.x;
+        a.y += b.y;
+        a.z += b.z;
+        a.w += b.w;
+      }
+      *reinterpret_cast<float4*>(p.out + (size_t)sg.unit() * G * D + i) = a;
     }
   }
-  if (!p.weight) return;
-  float* lse = sm;
-  int* scan = reinterpret_cast<int*>(sm + G_MAX);
-  int* pre = scan + 32;
-  group_prefix<AT_NT>(p, pre, scan, false);
-  const int total = pre[p.B] * p.Hkv;
-  const int parts = paged_parts(total, p.grid);
-  const int blocks = min((int)gridDim.x, max(total, 1));
-  if (c >= blocks || total == 0) return;
-  Segments sg;
-  sg.start(pre, p.B, p.Hkv, paged_part_begin(total, blocks, c), paged_part_begin(total, blocks, c + 1));
-  while (sg.at()) {
-    const int unit = sg.b * p.Hkv + sg.h, len = clamped_len(p, sg.b);
+  if (!p.weight || total == 0) return;
+  const int blocks = min((int)(gridDim.x * gridDim.y), total), id = blockIdx.y * gridDim.x + c;
+  if (id >= blocks) return;
+  sg.start(line, paged_part_begin(total, blocks, id), paged_part_begin(total, blocks, id + 1));
+  for (; sg.at(); sg.next()) {
+    const int unit = sg.unit();
     const int c0 = paged_part_of(total, parts, sg.unit_begin), c1 = paged_part_of(total, parts, sg.unit_end - 1);
-    __syncthreads();
-    if (tid < G) lse[tid] = c0 == c1 ? p.lse[(size_t)unit * G + tid] : joined_lse(p, D, tid, c0, c1);
-    __syncthreads();
-    const int t1 = min(len, (sg.seg_end() - sg.unit_begin) * PAGED_GROUP);
-    for (int t = (sg.x - sg.unit_begin) * PAGED_GROUP + tid; t < t1; t += AT_NT) {
-      float w = 0.f;
-      for (int g = 0; g < G; ++g) w += exp2f(p.logits[((size_t)unit * G + g) * p.T_cap + t] - lse[g]);
-      p.weight[(size_t)unit * p.T_cap + t] += w;
+    if (c0 == c1) {
+      __syncthreads();
+      if (tid < G) js.lse[tid] = __ldcg(p.lse + (size_t)unit * G + tid);
+      __syncthreads();
+    } else {
+      join_parts(p, D, c0, c1, js);
     }
-    sg.next();
+    // four tokens a thread: a group's slots, and so its logits and weights, are
+    // all there (those behind the end are -inf and get nothing)
+    const int t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP;
+    const float* z = p.logits + (size_t)unit * G * p.T_cap;
+    for (int t = (sg.x - sg.unit_begin) * PAGED_GROUP + 4 * tid; t < t1; t += 4 * JN_NT) {
+      float4* at = reinterpret_cast<float4*>(p.weight + (size_t)unit * p.T_cap + t);
+      float4 zg[G_MAX];
+#pragma unroll
+      for (int g = 0; g < G_MAX; ++g)
+        if (g < G) zg[g] = __ldcg(reinterpret_cast<const float4*>(z + (size_t)g * p.T_cap + t));
+      const float4 old = *at;
+      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int g = 0; g < G_MAX; ++g)
+        if (g < G) {
+          const float e = js.lse[g];
+          w.x += exp2f(zg[g].x - e);
+          w.y += exp2f(zg[g].y - e);
+          w.z += exp2f(zg[g].z - e);
+          w.w += exp2f(zg[g].w - e);
+        }
+      const int live = line.tokens(sg.b) - t;  // slots behind the end keep what they hold
+      if (live >= 4) {
+        *at = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+      } else {
+        float* f = reinterpret_cast<float*>(at);
+        if (live > 0) f[0] = old.x + w.x;
+        if (live > 1) f[1] = old.y + w.y;
+        if (live > 2) f[2] = old.z + w.z;
+      }
+    }
   }
 }
 
-// A pool of pages as rows of 64-column halves: a copy takes a group's 16 rows.
-cudaError_t pool_map(CUtensorMap* map, const void* pool, long long rows, int D) {
+// -------------------------------------------------------------- launch
+// A pool of pages as rows of 128-byte slabs: a copy takes a group's 16 rows.
+cudaError_t pool_map(CUtensorMap* map, const void* pool, long long rows, int D, int es, CUtensorMapDataType type) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                               const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                               CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
@@ -628,53 +793,53 @@ cudaError_t pool_map(CUtensorMap* map, const void* pool, long long rows, int D) 
       encode = reinterpret_cast<Encode>(f);
     }
   }
-  const cuuint64_t dims[3] = {64, (cuuint64_t)rows, (cuuint64_t)(D / 64)};
-  const cuuint64_t strides[2] = {(cuuint64_t)D * 2, 128};
-  const cuuint32_t box[3] = {64, PAGED_GROUP, (cuuint32_t)(D / 64)}, one[3] = {1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(pool), dims, strides, box, one,
+  const int cols = 128 / es;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)(D / cols)};
+  const cuuint64_t strides[2] = {(cuuint64_t)D * es, 128};
+  const cuuint32_t box[3] = {(cuuint32_t)cols, PAGED_GROUP, (cuuint32_t)(D / cols)}, one[3] = {1, 1, 1};
+  const CUresult r = encode(map, type, 3, const_cast<void*>(pool), dims, strides, box, one,
                             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-template <int D>
-cudaError_t join(const PagedAttendParams& p, cudaStream_t s) {
-  paged_join_kernel<D><<<p.weight ? 4 * p.grid : p.grid, AT_NT, G_MAX * 4 + 32 * 4 + (p.B + 1) * 4, s>>>(p);
-  return cudaGetLastError();
-}
-
-template <int D>
-cudaError_t launch_f32(const PagedAttendParams& p, cudaStream_t s) {
-  const int smem = (G_MAX * D + AT_NW * G_MAX * (D + 2)) * 4 + 32 * 4 + (p.B + 1) * 4;
-  cudaError_t e = cudaFuncSetAttribute(paged_attend_kernel<float, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  if (e != cudaSuccess) return e;
-  paged_attend_kernel<float, D><<<p.grid, AT_NT, smem, s>>>(p);
-  e = cudaGetLastError();
-  return e == cudaSuccess ? join<D>(p, s) : e;
-}
-
-template <int D>
-cudaError_t launch_bf16(const PagedAttendParams& p, cudaStream_t s) {
+template <int D, class M>
+cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   CUtensorMap km, vm;
   const long long rows = ((long long)p.n_pages * p.Hkv) << p.log2_page;
-  cudaError_t e = pool_map(&km, p.k_pages, rows, D);
-  if (e == cudaSuccess) e = pool_map(&vm, p.v_pages, rows, D);
+  cudaError_t e = pool_map(&km, p.k_pages, rows, D, sizeof(typename M::T), M::TYPE);
+  if (e == cudaSuccess) e = pool_map(&vm, p.v_pages, rows, D, sizeof(typename M::T), M::TYPE);
   if (e != cudaSuccess) return e;
-  const int smem = 1024 + Tc<D>::OFF_PRE + (p.B + 1) * 4;
-  e = cudaFuncSetAttribute(paged_attend_bf16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  const int smem = Plan<D, M>::bytes(p.B);
+  // as many parts as CTAs are resident at once: M::CTAS to an SM while the
+  // lengths of the batch leave them the room (228 KB, 1 KB of it the system's)
+  const int ctas = M::CTAS * (smem + 1024) <= 233472 ? M::CTAS : 1;
+  p.grid = min(ctas * sms, PAGED_MAX_PARTS);
+  e = cudaFuncSetAttribute(paged_attend_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  paged_attend_bf16_kernel<D><<<p.grid, TC_NT, smem, s>>>(p, km, vm);
+  paged_attend_kernel<D, M><<<p.grid, AT_NT, smem, s>>>(p, km, vm);
   e = cudaGetLastError();
-  return e == cudaSuccess ? join<D>(p, s) : e;
+  if (e != cudaSuccess) return e;
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(p.grid, (p.G * D + 127) / 128);
+  cfg.blockDim = dim3(JN_NT);
+  cfg.dynamicSmemBytes = (2 * p.grid * p.G + G_MAX + p.B + 1) * 4;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, static_cast<const PagedAttendParams&>(p));
 }
 
 }  // namespace
 
 cudaError_t launch_paged_attend(const PagedAttendParams& p0, int head_dim, bool bf16, int sms, cudaStream_t s) {
   PagedAttendParams p = p0;
-  p.grid = min(sms, PAGED_MAX_PARTS);
-  if (bf16) return head_dim == 128 ? launch_bf16<128>(p, s) : launch_bf16<64>(p, s);
-  return head_dim == 128 ? launch_f32<128>(p, s) : launch_f32<64>(p, s);
+  if (bf16) return head_dim == 128 ? launch<128, MathBf16<128>>(p, sms, s) : launch<64, MathBf16<64>>(p, sms, s);
+  if (p.G <= 4) return head_dim == 128 ? launch<128, MathF32<128, 4>>(p, sms, s) : launch<64, MathF32<64, 4>>(p, sms, s);
+  return head_dim == 128 ? launch<128, MathF32<128, 8>>(p, sms, s) : launch<64, MathF32<64, 8>>(p, sms, s);
 }
 
 }  // namespace fasa
