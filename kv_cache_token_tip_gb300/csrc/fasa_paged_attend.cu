@@ -35,46 +35,23 @@ namespace {
 
 constexpr int AT_NW = 4;  // warps of a CTA
 constexpr int AT_NT = AT_NW * 32;
-constexpr int JN_NT = 128;
+constexpr int JN_NT = 256;
 
-// The sequences' groups as prefix sums, in shared memory: word b holds the
-// groups before sequence b (28 bits: at most 4096 * 32768) and by how many
-// tokens b's last group is short (4 bits); word B all groups.
-struct Line {
-  const unsigned* w;
-  int B, Hkv;
-  __device__ int before(int b) const { return (int)(w[b] & 0x0fffffffu); }
-  __device__ int groups(int b) const { return before(b + 1) - before(b); }
-  __device__ int tokens(int b) const { return groups(b) * PAGED_GROUP - (int)(w[b] >> 28); }
-  __device__ int total() const { return before(B) * Hkv; }
-  // The sequence whose units hold position x of the line.
-  __device__ int sequence_of(int x) const {
-    int lo = 0, hi = B;  // Hkv * before(lo) <= x < Hkv * before(hi)
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before(mid) * Hkv <= x) lo = mid;
-      else hi = mid;
-    }
-    return lo;
-  }
-};
-
-// Every thread of the block calls it; ends with a barrier.  scan: NT / 32 words.
+// The line's words, in shared memory.  Every thread of the block calls it; ends
+// with a barrier.  scan: NT / 32 words.
 template <int NT>
 __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int base = 0;
   for (int b0 = 0; b0 < p.B; b0 += NT) {
     const int b = b0 + tid;
-    int n = 0;
-    unsigned shy = 0u;
+    int len = 0;
     if (b < p.B) {
-      const int len = p.seq_lens[b];
+      len = p.seq_lens[b];
       if (report && (len < 0 || len > p.T_cap)) atomicOr(p.status, 1);
-      const int use = min(max(len, 0), p.T_cap);
-      n = paged_groups(use);
-      shy = (unsigned)(n * PAGED_GROUP - use);
+      len = min(max(len, 0), p.T_cap);
     }
+    const int n = paged_groups(len);
     int incl = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -90,47 +67,11 @@ __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool rep
       before += v < warp ? s : 0;
       base += s;
     }
-    if (b < p.B) w[b] = (unsigned)(before + incl - n) | (shy << 28);
-    if (b == p.B - 1) w[p.B] = (unsigned)(before + incl);
+    if (b < p.B) w[b] = paged_word(before + incl - n, len);
+    if (b == p.B - 1) w[p.B] = paged_word(before + incl, 0);
     __syncthreads();
   }
 }
-
-// Walks the units that [x, end) of the line touches.
-struct Segments {
-  Line line;
-  int end;
-  int x, b, h;  // where the next segment begins
-  int unit_begin, unit_end;
-  __device__ void start(const Line& l, int x_, int end_) {
-    line = l;
-    x = x_;
-    end = end_;
-    b = h = 0;
-    if (x < end) {
-      b = line.sequence_of(x);
-      h = (x - line.before(b) * line.Hkv) / line.groups(b);
-    }
-  }
-  // The segment at x: its unit (b, h) and where the unit lies; false at the end.
-  __device__ bool at() {
-    if (x >= end) return false;
-    while (line.groups(b) == 0) ++b;
-    const int n = line.groups(b);
-    unit_begin = line.before(b) * line.Hkv + h * n;
-    unit_end = unit_begin + n;
-    return true;
-  }
-  __device__ int unit() const { return b * line.Hkv + h; }
-  __device__ int seg_end() const { return min(unit_end, end); }
-  __device__ void next() {
-    x = seg_end();
-    if (x == unit_end && ++h == line.Hkv) {
-      h = 0;
-      ++b;
-    }
-  }
-};
 
 // ------------------------------------------------- bf16: tensor cores
 // z^T: rows of A the heads, B the tokens.  The rotated and scaled query is
@@ -482,15 +423,15 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   constexpr int TW = D / 2 / AT_NW;
   if (lane < TW) turns[warp * TW + lane] = p.rope_turns[warp * TW + lane];
   make_line<AT_NT>(p, words, reinterpret_cast<int*>(sm + P::OFF_SCAN), blockIdx.x == 0);
-  const Line line{words, p.B, p.Hkv};
-  const int total = line.total();
-  const int parts = paged_parts(total, p.grid);
+  const PagedLine line{words, p.B, p.Hkv};
+  const int parts = line.parts(p.grid);
   const int c = blockIdx.x;
   for (int b = c; b < p.B; b += p.grid)  // sequences without a token: zeros
     if (line.groups(b) == 0)
       for (int i = tid; i < p.Hq * D; i += AT_NT) p.out[(size_t)b * p.Hq * D + i] = 0.f;
   if (c >= parts) return;
-  const int r0 = paged_part_begin(total, parts, c), r1 = paged_part_begin(total, parts, c + 1);
+  const int r0 = line.part_begin(parts, c), r1 = line.part_begin(parts, c + 1);
+  if (r0 == r1) return;
 
   // This warp's groups: x = r0 + warp + k * AT_NW, k < mine.  Lane i holds the
   // pool row of group (batch of 32) + i.
@@ -529,7 +470,7 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   };
   for (int i = 0; i < S; ++i) issue();
 
-  auto query_of = [&](const Segments& s) {
+  auto query_of = [&](const PagedSegments& s) {
     return static_cast<const void*>(static_cast<const typename M::T*>(p.q) + ((size_t)s.b * p.Hq + s.h * G) * D);
   };
   auto turn = [&](int i, int n, int pos) {  // cos and sin of a position, by n threads
@@ -538,7 +479,7 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
       cs[f] = make_float2(a.x * p.scale, a.y * p.scale);
     }
   };
-  Segments sg;
+  PagedSegments sg;
   sg.start(line, r0, r1);
   sg.at();
   uint32_t q_raw[M::QREGS];
@@ -551,7 +492,7 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
     M mt;
     mt.begin(q_raw, cs, G, query);
     // the next unit's query and position are under way meanwhile
-    Segments nx = sg;
+    PagedSegments nx = sg;
     nx.next();
     const bool more = nx.at();
     int next_pos = 0;
@@ -630,115 +571,119 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
 }
 
 // --------------------------------------------------------------- join
-// The scratch of one unit's parts: up to `grid` x G of (m, l).
-struct JoinShared {
-  float* m;    // [parts][G]; joined: each part's factor 2^(m - M) / L
-  float* l;    // [parts][G]
-  float* lse;  // [G]
-};
+__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
-// (m, l) of the parts c0 .. c1 of a unit: lse, and the parts' factors.
-__device__ void join_parts(const PagedAttendParams& p, int D, int c0, int c1, const JoinShared& js) {
-  const int G = p.G, n = (c1 - c0 + 1) * G, R = paged_record_floats(G, D);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  __syncthreads();
-  for (int i = threadIdx.x; i < n; i += JN_NT) {
-    const int k = i / G, g = i - k * G;
-    const float* r = p.records + (size_t)(2 * (c0 + k) + (k == 0)) * R + G * D + g;
-    js.m[i] = __ldcg(r);
-    js.l[i] = __ldcg(r + G);
-  }
-  __syncthreads();
-  for (int g = warp; g < G; g += JN_NT / 32) {
-    float M = -INFINITY, L = 0.f;
-    for (int i = lane * G + g; i < n; i += 32 * G) M = fmaxf(M, js.m[i]);
-#pragma unroll
-    for (int s = 16; s; s >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, s));
-    const float Ms = M == -INFINITY ? 0.f : M;
-    for (int i = lane * G + g; i < n; i += 32 * G) L += js.l[i] * exp2f(js.m[i] - Ms);
-#pragma unroll
-    for (int s = 16; s; s >>= 1) L += __shfl_xor_sync(0xffffffffu, L, s);
-    const float inv = L > 0.f ? 1.f / L : 0.f;
-    for (int i = lane * G + g; i < n; i += 32 * G) js.m[i] = exp2f(js.m[i] - Ms) * inv;
-    if (lane == 0) js.lse[g] = L > 0.f ? M + log2f(L) : INFINITY;
-  }
-  __syncthreads();
-}
-
-// Block (c, y): 128 floats of the output of the unit that is cut between the
-// parts c and c + 1 and begins in c; with weights then its share of the line's
-// tokens.
+// Block (c, y): 128 floats of the output of the unit that begins in part c and
+// goes on in the next; with weights, block (c, 0) then adds its share of the
+// line's tokens.
 template <int D>
 __global__ void __launch_bounds__(JN_NT) paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
-  extern __shared__ __align__(16) float shared[];
-  __shared__ float4 sums[JN_NT];
-  __shared__ int scan[JN_NT / 32];
-  const int tid = threadIdx.x, c = blockIdx.x, G = p.G;
-  JoinShared js;
-  js.m = shared;
-  js.l = js.m + p.grid * G;
-  js.lse = js.l + p.grid * G;
-  unsigned* words = reinterpret_cast<unsigned*>(js.lse + G_MAX);
+  constexpr int NW = JN_NT / 32;
+  extern __shared__ unsigned words[];
+  __shared__ float4 so[NW][32];
+  __shared__ float2 sml[NW][32];
+  __shared__ float lse[G_MAX];
+  __shared__ int scan[NW];
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x, G = p.G;
+  const int R = paged_record_floats(G, D);
   make_line<JN_NT>(p, words, scan, false);
-  const Line line{words, p.B, p.Hkv};
-  const int total = line.total();
-  const int parts = paged_parts(total, p.grid);
-  Segments sg;
+  const PagedLine line{words, p.B, p.Hkv};
+  const int parts = line.parts(p.grid), total = line.total();
+  PagedSegments sg;
   bool cut = false;
-  if (c + 1 < parts && total > 0) {
-    const int edge = paged_part_begin(total, parts, c + 1);
-    sg.start(line, edge - 1, edge);
-    sg.at();
-    cut = sg.unit_end > edge && paged_part_of(total, parts, sg.unit_begin) == c;
+  if (c + 1 < parts) {
+    const int edge = line.part_begin(parts, c + 1);
+    if (edge > 0 && edge < total) {
+      sg.start(line, edge - 1, edge);
+      sg.at();
+      cut = sg.unit_end > edge && sg.first_part(parts) == c;
+    }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
   if (cut) {
-    const int c1 = paged_part_of(total, parts, sg.unit_end - 1), R = paged_record_floats(G, D);
-    join_parts(p, D, c, c1, js);
-    // lane: 4 floats; warp: every fourth part
-    const int i = blockIdx.y * 128 + 4 * (tid & 31);
+    // a warp takes every NW-th part, a lane four floats of it, then the warps'
+    // sums meet, in order
+    const int n = sg.last_part(parts) - c + 1;
+    const int i = min(blockIdx.y * 128 + 4 * lane, G * D - 4), g = i / D;
+    const float* first = p.records + (size_t)(2 * c + 1) * R;
+    const float* rest = p.records + (size_t)(2 * c) * R;
+    float M = -INFINITY, L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (i < G * D) {
-      const int g = i / D;
-#pragma unroll 4
-      for (int k = tid >> 5; k <= c1 - c; k += JN_NT / 32) {
-        const float4 o =
-            __ldcg(reinterpret_cast<const float4*>(p.records + (size_t)(2 * (c + k) + (k == 0)) * R + i));
-        const float f = js.m[k * G + g];
-        a.x += o.x * f;
-        a.y += o.y * f;
-        a.z += o.z * f;
-        a.w += o.w * f;
+    constexpr int U = 5;
+    for (int k0 = warp; k0 < n; k0 += U * NW) {
+      float4 o[U];
+      float m[U], l[U];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int k = k0 + u * NW;
+        const float* r = k == 0 ? first : rest + (size_t)(2 * k) * R;
+        o[u] = k < n ? __ldcg(reinterpret_cast<const float4*>(r + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        m[u] = k < n ? __ldcg(r + G * D + g) : -INFINITY;
+        l[u] = k < n ? __ldcg(r + G * D + G + g) : 0.f;
+      }
+      float X = M;
+#pragma unroll
+      for (int u = 0; u < U; ++u) X = fmaxf(X, m[u]);
+      const float Xs = finite_or_0(X), f = exp2f(M - Xs);
+      M = X;
+      L *= f;
+      a = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const float e = exp2f(m[u] - Xs);
+        L += l[u] * e;
+        a = make_float4(a.x + o[u].x * e, a.y + o[u].y * e, a.z + o[u].z * e, a.w + o[u].w * e);
       }
     }
-    sums[tid] = a;
+    so[warp][lane] = a;
+    sml[warp][lane] = make_float2(M, L);
     __syncthreads();
-    if (tid < 32 && i < G * D) {
+    if (warp == 0 && blockIdx.y * 128 + 4 * lane < G * D) {
+      float X = -INFINITY;
 #pragma unroll
-      for (int w = 1; w < JN_NT / 32; ++w) {
-        const float4 b = sums[w * 32 + tid];
-        a.x += b.x;
-        a.y += b.y;
-        a.z += b.z;
-        a.w += b.w;
+      for (int w = 0; w < NW; ++w) X = fmaxf(X, sml[w][lane].x);
+      const float Xs = finite_or_0(X);
+      L = 0.f;
+      a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < NW; ++w) {
+        const float e = exp2f(sml[w][lane].x - Xs);
+        const float4 o = so[w][lane];
+        L += sml[w][lane].y * e;
+        a = make_float4(a.x + o.x * e, a.y + o.y * e, a.z + o.z * e, a.w + o.w * e);
       }
-      *reinterpret_cast<float4*>(p.out + (size_t)sg.unit() * G * D + i) = a;
+      const float inv = L > 0.f ? 1.f / L : 0.f;
+      *reinterpret_cast<float4*>(p.out + (size_t)sg.unit() * G * D + i) =
+          make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     }
   }
-  if (!p.weight || total == 0) return;
-  const int blocks = min((int)(gridDim.x * gridDim.y), total), id = blockIdx.y * gridDim.x + c;
-  if (id >= blocks) return;
-  sg.start(line, paged_part_begin(total, blocks, id), paged_part_begin(total, blocks, id + 1));
+  if (!p.weight || blockIdx.y > 0 || c >= parts) return;
+  // the part's own tokens
+  sg.start(line, line.part_begin(parts, c), line.part_begin(parts, c + 1));
   for (; sg.at(); sg.next()) {
-    const int unit = sg.unit();
-    const int c0 = paged_part_of(total, parts, sg.unit_begin), c1 = paged_part_of(total, parts, sg.unit_end - 1);
-    if (c0 == c1) {
-      __syncthreads();
-      if (tid < G) js.lse[tid] = __ldcg(p.lse + (size_t)unit * G + tid);
-      __syncthreads();
-    } else {
-      join_parts(p, D, c0, c1, js);
+    const int unit = sg.unit(), c0 = sg.first_part(parts), n = sg.last_part(parts) - c0 + 1;
+    __syncthreads();
+    if (n == 1) {
+      if (tid < G) lse[tid] = __ldcg(p.lse + (size_t)unit * G + tid);
+    } else if (warp < G) {  // warp g: the parts' (m, l) of head g
+      static_assert(NW >= G_MAX, "a warp for each head");
+      float M = -INFINITY, L = 0.f;
+      for (int k = lane; k < n; k += 32) {
+        const float* r = p.records + (size_t)(2 * (c0 + k) + (k == 0)) * R + G * D + warp;
+        const float m = __ldcg(r), l = __ldcg(r + G), X = fmaxf(M, m), Xs = finite_or_0(X);
+        L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
+        M = X;
+      }
+#pragma unroll
+      for (int s = 16; s; s >>= 1) {
+        const float m = __shfl_xor_sync(0xffffffffu, M, s), l = __shfl_xor_sync(0xffffffffu, L, s);
+        const float X = fmaxf(M, m), Xs = finite_or_0(X);
+        L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
+        M = X;
+      }
+      if (lane == 0) lse[warp] = L > 0.f ? M + log2f(L) : INFINITY;
     }
+    __syncthreads();
     // four tokens a thread: a group's slots, and so its logits and weights, are
     // all there (those behind the end are -inf and get nothing)
     const int t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP;
@@ -754,7 +699,7 @@ __global__ void __launch_bounds__(JN_NT) paged_join_kernel(const __grid_constant
 #pragma unroll
       for (int g = 0; g < G_MAX; ++g)
         if (g < G) {
-          const float e = js.lse[g];
+          const float e = lse[g];
           w.x += exp2f(zg[g].x - e);
           w.y += exp2f(zg[g].y - e);
           w.z += exp2f(zg[g].z - e);
@@ -826,7 +771,7 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.grid, (p.G * D + 127) / 128);
   cfg.blockDim = dim3(JN_NT);
-  cfg.dynamicSmemBytes = (2 * p.grid * p.G + G_MAX + p.B + 1) * 4;
+  cfg.dynamicSmemBytes = (p.B + 1) * 4;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;

@@ -5,9 +5,10 @@
 // Tokens are handled in groups of PAGED_GROUP slots; a page holds whole groups,
 // so a group's rows of one KV head are contiguous.  A unit is a (sequence, KV
 // head); unit (b, h) has ceil(len_b / PAGED_GROUP) groups.  All groups, units in
-// order, form one line 0 .. total-1, cut into `parts` ranges of nearly equal
-// length: part c takes [part_begin(c), part_begin(c + 1)).  Ragged lengths then
-// cost no balance, and a unit is joined from the parts it touches.
+// order, form one line 0 .. total-1, cut into parts, one to a CTA; a unit is
+// joined from the parts it touches.  The cuts are even in cost: a unit costs
+// its groups and PAGED_UNIT_COST more (its query, its join), so that a part of
+// many short units takes no longer than one of a long one.
 #pragma once
 
 #include <stdint.h>
@@ -21,23 +22,13 @@
 namespace fasa {
 
 constexpr int PAGED_GROUP = 16;         // tokens per group
-constexpr int PAGED_PART_GROUPS = 8;    // a part has at least this many groups (while there are as many)
+constexpr int PAGED_UNIT_COST = 6;      // what a unit costs beside its groups, in groups
+constexpr int PAGED_PART_COST = 12;     // a part costs at least this much (while there is as much)
 constexpr int PAGED_MAX_PARTS = 320;    // parts the workspace has room for
 constexpr int PAGED_MAX_BATCH = 4096;   // the lengths' prefix sums sit in shared memory
 constexpr int PAGED_MAX_SLOTS = 524288; // T_cap: the line's positions fit 31 bits
 
 FASA_HD int paged_groups(int len) { return (len + PAGED_GROUP - 1) / PAGED_GROUP; }
-
-// Parts the line is cut into, at most `grid`.
-FASA_HD int paged_parts(int total, int grid) {
-  const int most = (total + PAGED_PART_GROUPS - 1) / PAGED_PART_GROUPS;
-  return most < 1 ? 1 : (most < grid ? most : grid);
-}
-FASA_HD int paged_part_begin(int total, int parts, int c) { return (int)((long long)total * c / parts); }
-// The part that holds position x (0 <= x < total).
-FASA_HD int paged_part_of(int total, int parts, int x) {
-  return (int)((((long long)x + 1) * parts - 1) / total);
-}
 
 // Row (of d elements) of `slot`'s token of KV head h in a pool of pages
 // [n_pages, Hkv, page_size, d], the page being page_table's entry; -1 for an
@@ -46,5 +37,99 @@ FASA_HD long long paged_row(int page, int n_pages, int Hkv, int h, int log2_page
   if (page < 0 || page >= n_pages) return -1;
   return (((long long)page * Hkv + h) << log2_page) + (slot & ((1 << log2_page) - 1));
 }
+
+// Word b of the line: the groups of one head of the sequences before b (28
+// bits: at most 4096 * 32768) and by how many tokens b's last group is short (4
+// bits); word B: all sequences' groups.
+FASA_HD unsigned paged_word(int before, int len) {
+  return (unsigned)before | (unsigned)(paged_groups(len) * PAGED_GROUP - len) << 28;
+}
+
+struct PagedLine {
+  const unsigned* w;
+  int B, Hkv;
+
+  FASA_HD int before(int b) const { return (int)(w[b] & 0x0fffffffu); }
+  FASA_HD int groups(int b) const { return before(b + 1) - before(b); }
+  FASA_HD int tokens(int b) const { return groups(b) * PAGED_GROUP - (int)(w[b] >> 28); }
+  FASA_HD int total() const { return before(B) * Hkv; }
+  // The sequence whose units hold position x of the line (0 <= x < total).
+  FASA_HD int sequence_of(int x) const {
+    int lo = 0, hi = B;  // Hkv * before(lo) <= x < Hkv * before(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before(mid) * Hkv <= x) lo = mid;
+      else hi = mid;
+    }
+    return lo;
+  }
+
+  FASA_HD long long cost_before(int b) const { return (long long)Hkv * (before(b) + (long long)PAGED_UNIT_COST * b); }
+  FASA_HD long long cost() const { return cost_before(B); }
+  // Parts of the line, at most `grid`.
+  FASA_HD int parts(int grid) const {
+    const long long most = (cost() + PAGED_PART_COST - 1) / PAGED_PART_COST;
+    return most < grid ? (int)most : grid;
+  }
+  // Where part c of n begins on the line (0 <= c <= n; a part may be empty): the
+  // first group that costs no less than c n-ths.
+  FASA_HD int part_begin(int n, int c) const {
+    const long long y = cost() * c / n;
+    if (y >= cost()) return total();
+    int lo = 0, hi = B;  // cost_before(lo) <= y < cost_before(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (cost_before(mid) <= y) lo = mid;
+      else hi = mid;
+    }
+    const int g = groups(lo), rem = (int)(y - cost_before(lo));
+    const int h = rem / (g + PAGED_UNIT_COST), off = rem - h * (g + PAGED_UNIT_COST);
+    return before(lo) * Hkv + h * g + (off > PAGED_UNIT_COST ? off - PAGED_UNIT_COST : 0);
+  }
+  // The part of n that holds group g of unit (b, h).
+  FASA_HD int part_of(int n, int b, int h, int g) const {
+    const long long y = cost_before(b) + (long long)h * (groups(b) + PAGED_UNIT_COST) + PAGED_UNIT_COST + g;
+    return (int)(((y + 1) * n - 1) / cost());
+  }
+};
+
+// Walks the units that [x, end) of the line touches.
+struct PagedSegments {
+  PagedLine line;
+  int end;
+  int x, b, h;  // where the next segment begins
+  int unit_begin, unit_end;
+
+  FASA_HD void start(const PagedLine& l, int x_, int end_) {
+    line = l;
+    x = x_;
+    end = end_;
+    b = h = 0;
+    if (x < end) {
+      b = line.sequence_of(x);
+      h = (x - line.before(b) * line.Hkv) / line.groups(b);
+    }
+  }
+  // The segment at x: its unit (b, h) and where the unit lies; false at the end.
+  FASA_HD bool at() {
+    if (x >= end) return false;
+    while (line.groups(b) == 0) ++b;
+    const int n = line.groups(b);
+    unit_begin = line.before(b) * line.Hkv + h * n;
+    unit_end = unit_begin + n;
+    return true;
+  }
+  FASA_HD int unit() const { return b * line.Hkv + h; }
+  FASA_HD int seg_end() const { return unit_end < end ? unit_end : end; }
+  FASA_HD int first_part(int n) const { return line.part_of(n, b, h, 0); }
+  FASA_HD int last_part(int n) const { return line.part_of(n, b, h, unit_end - unit_begin - 1); }
+  FASA_HD void next() {
+    x = seg_end();
+    if (x == unit_end && ++h == line.Hkv) {
+      h = 0;
+      ++b;
+    }
+  }
+};
 
 }  // namespace fasa

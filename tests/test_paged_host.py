@@ -114,32 +114,96 @@ def test_workspace_sizes(L):
 INDEX_PROGRAM = r"""
 #include <cstdio>
 #include <cstdlib>
+#include <vector>
 #include "fasa_paged_index.h"
 using namespace fasa;
 #define CHECK(x) do { if (!(x)) { printf("line %d: %s\n", __LINE__, #x); return 1; } } while (0)
+
+static std::vector<unsigned> words(const std::vector<int>& lens) {
+  std::vector<unsigned> w;
+  int before = 0;
+  for (int n : lens) {
+    w.push_back(paged_word(before, n));
+    before += paged_groups(n);
+  }
+  w.push_back(paged_word(before, 0));
+  return w;
+}
+
+// The parts cover the line once, in order; part_of is their inverse; the walk
+// meets every unit's groups once, and the records of a cut unit are those of
+// its first to its last part, none of them empty.
+static int check(const std::vector<int>& lens, int Hkv, int grid) {
+  const std::vector<unsigned> w = words(lens);
+  const int B = (int)lens.size();
+  const PagedLine line{w.data(), B, Hkv};
+  int groups = 0;
+  for (int b = 0; b < B; ++b) {
+    CHECK(line.tokens(b) == lens[b] && line.groups(b) == paged_groups(lens[b]));
+    groups += paged_groups(lens[b]);
+  }
+  CHECK(line.total() == groups * Hkv);
+  const int n = line.parts(grid);
+  CHECK(n >= 1 && n <= grid);
+  CHECK(line.part_begin(n, 0) == 0 && line.part_begin(n, n) == line.total());
+  std::vector<int> seen(B * Hkv, 0), last(B * Hkv, -1);
+  long long most = 0;
+  for (int c = 0; c < n; ++c) {
+    const int r0 = line.part_begin(n, c), r1 = line.part_begin(n, c + 1);
+    CHECK(r0 <= r1);
+    PagedSegments s;
+    s.start(line, r0, r1);
+    long long cost = 0;
+    for (; s.at(); s.next()) {
+      CHECK(s.b < B && s.h < Hkv && s.x >= s.unit_begin && s.x < s.seg_end());
+      CHECK(s.unit_end - s.unit_begin == line.groups(s.b));
+      const int u = s.unit();
+      CHECK(s.x - s.unit_begin == seen[u]);
+      for (int x = s.x; x < s.seg_end(); ++x) CHECK(line.part_of(n, s.b, s.h, x - s.unit_begin) == c);
+      if (seen[u]) CHECK(last[u] == c - 1);
+      else CHECK(s.first_part(n) == c);
+      seen[u] += s.seg_end() - s.x;
+      last[u] = c;
+      if (seen[u] == line.groups(s.b)) CHECK(s.last_part(n) == c);
+      else CHECK(s.last_part(n) > c);
+      cost += s.seg_end() - s.x + (s.x == s.unit_begin ? PAGED_UNIT_COST : 0);
+    }
+    most = cost > most ? cost : most;
+  }
+  for (int u = 0; u < B * Hkv; ++u) CHECK(seen[u] == line.groups(u / Hkv));
+  CHECK(most <= line.cost() / n + 1 + PAGED_UNIT_COST);   // even in cost
+  return 0;
+}
+
 int main() {
-  // the parts cover the line once, in order, and part_of is their inverse
   const int grids[] = {1, 3, 152, 304, PAGED_MAX_PARTS};
+  srand(7);
   for (int grid : grids)
-    for (int total = 1; total < 6000; total = total * 5 / 4 + 1) {
-      const int parts = paged_parts(total, grid);
-      CHECK(parts >= 1 && parts <= grid && parts <= total);
-      CHECK(paged_part_begin(total, parts, 0) == 0 && paged_part_begin(total, parts, parts) == total);
-      for (int c = 0; c < parts; ++c) {
-        const int a = paged_part_begin(total, parts, c), b = paged_part_begin(total, parts, c + 1);
-        CHECK(a < b);
-        for (int x = a; x < b; ++x) CHECK(paged_part_of(total, parts, x) == c);
+    for (int Hkv : {1, 2, 7, 8}) {
+      for (int len = 1; len < 40000; len = len * 7 / 4 + 1)
+        if (check({len}, Hkv, grid) || check({0, len, 0, 0, 1, len / 3}, Hkv, grid)) return 1;
+      if (check({0}, Hkv, grid) || check({0, 0, 0}, Hkv, grid)) return 1;
+      for (int i = 0; i < 30; ++i) {
+        std::vector<int> lens(1 + rand() % 300);
+        for (int& n : lens) n = rand() % 4 ? rand() % (1 + rand() % 900) : 0;
+        if (check(lens, Hkv, grid)) return 1;
       }
     }
-  // the longest line: 65535 units of PAGED_MAX_SLOTS slots
-  const int total = 65535 * (PAGED_MAX_SLOTS / PAGED_GROUP), parts = paged_parts(total, PAGED_MAX_PARTS);
-  CHECK(total > 0 && parts == PAGED_MAX_PARTS && paged_part_begin(total, parts, parts) == total);
-  for (int c = 0; c < parts; ++c) {
-    const int a = paged_part_begin(total, parts, c), b = paged_part_begin(total, parts, c + 1);
-    CHECK(a < b && paged_part_of(total, parts, a) == c && paged_part_of(total, parts, b - 1) == c);
+  // the longest lines: 65535 units of PAGED_MAX_SLOTS slots; the largest batch
+  for (int B : {1, 4095}) {
+    const int Hkv = 65535 / B, g = PAGED_MAX_SLOTS / PAGED_GROUP;
+    const std::vector<unsigned> w = words(std::vector<int>(B, PAGED_MAX_SLOTS - 1));
+    const PagedLine line{w.data(), B, Hkv};
+    CHECK(line.total() == B * Hkv * g && line.total() > 0 && line.tokens(B - 1) == PAGED_MAX_SLOTS - 1);
+    const int n = line.parts(PAGED_MAX_PARTS);
+    CHECK(n == PAGED_MAX_PARTS && line.part_begin(n, n) == line.total());
+    for (int c = 0; c < n; ++c) {
+      PagedSegments s;
+      s.start(line, line.part_begin(n, c), line.part_begin(n, c + 1));
+      CHECK(s.at() && line.part_of(n, s.b, s.h, s.x - s.unit_begin) == c);
+    }
   }
   CHECK(paged_groups(0) == 0 && paged_groups(1) == 1 && paged_groups(16) == 1 && paged_groups(17) == 2);
-  CHECK(paged_parts(0, 152) == 1);
   // rows: inside the pool for every page in it, -1 for every other entry
   for (int lp = 4; lp <= 8; ++lp)
     for (int page = -2; page < 9; ++page)
@@ -162,7 +226,7 @@ def test_index_arithmetic(tmp_path):
     src.write_text(INDEX_PROGRAM)
     exe = str(tmp_path / "index")
     inc = os.path.join(ROOT, "kv_cache_token_tip_gb300", "csrc")
-    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", inc, str(src), "-o", exe],
+    subprocess.run(["g++", "-std=c++17", "-O2", "-fsanitize=undefined", "-fno-sanitize-recover=all", "-I", inc, str(src), "-o", exe],
                    check=True, capture_output=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
