@@ -396,7 +396,7 @@ int fasa_decode_step_noalloc(const void* q, const int32_t* pos,
  *    workspace 16 bytes.
  *  - Supported: dtype FASA_F32 or FASA_BF16, head_dim 64 or 128, 1 <= G <= 8,
  *    page_size 16, 32, 64, 128 or 256, batch <= 4096, batch * Hkv <= 65535,
- *    T_cap <= 524288, n_pages * Hkv * page_size < 2^31.
+ *    T_cap <= 262144, n_pages * Hkv * page_size < 2^31.
  */
 typedef struct fasa_paged_dims {
   int32_t batch;       /* B                                            */

@@ -35,7 +35,6 @@ namespace {
 
 constexpr int AT_NW = 4;  // warps of a CTA
 constexpr int AT_NT = AT_NW * 32;
-constexpr int JN_NT = 256;
 
 // The line's words, in shared memory.  Every thread of the block calls it; ends
 // with a barrier.  scan: NT / 32 words.
@@ -87,25 +86,20 @@ struct MathBf16 {
   static constexpr int CTAS = 2;  // per SM: one streams while the other joins a unit's parts
   static constexpr int MT = D / 16;
   static constexpr int OREGS = 4 * MT;
-  static constexpr int QREGS = 2 * MT;   // words of a lane's share of the next unit's raw query
-  static constexpr int QUERY = 0, SCRATCH = 0;  // shared memory of the CTA, of a warp
+  static constexpr int SCRATCH = 0;  // shared memory of a warp
   static constexpr CUtensorMapDataType TYPE = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   uint32_t qa[MT][4], ql[MT][2];
   float m, l, o[MT][4];
 
-  // This lane's words of the query rows q [G][D].
-  static __device__ void fetch_q(const void* q, int G, uint32_t (&raw)[QREGS]) {
+  // query: the unit's raw rows [G][D], behind a barrier.
+  __device__ void begin(const void* query, const float2* cs, int G) {
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-    const uint32_t* w = static_cast<const uint32_t*>(q) + (size_t)min(g, G - 1) * (D / 2) + t;
+    const uint32_t* raw = static_cast<const uint32_t*>(query) + min(g, G - 1) * (D / 2);
 #pragma unroll
-    for (int i = 0; i < QREGS; ++i) raw[i] = g < G ? __ldg(w + 4 * i) : 0u;  // pairs t + 4 i
-  }
-  __device__ void begin(const uint32_t (&raw)[QREGS], const float2* cs, int G, float2*) {
-    const int t = threadIdx.x & 3;
-#pragma unroll
-    for (int i = 0; i < QREGS; ++i) {
+    for (int i = 0; i < 2 * MT; ++i) {  // the pairs t + 4 i of head g
       const float2 a = cs[t + 4 * i];
-      const float x0 = bf16_lo(raw[i]), x1 = bf16_hi(raw[i]);
+      const uint32_t w = g < G ? raw[t + 4 * i] : 0u;
+      const float x0 = bf16_lo(w), x1 = bf16_hi(w);
       const float y0 = x0 * a.x - x1 * a.y, y1 = x0 * a.y + x1 * a.x;
       const uint32_t hi = pack_bf16(y0, y1);
       qa[i >> 1][2 * (i & 1)] = hi;
@@ -123,7 +117,7 @@ struct MathBf16 {
     for (int i = 0; i < OREGS; ++i) o[i >> 2][i & 3] *= (i & 1) ? a1 : a0;
   }
   // One group: K at kb, V at vb, its first n tokens count; logits [G][stride] at the group, or null.
-  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, const float2*,
+  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, const void*,
                        float*) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // ldmatrix: this lane's row of the group and 16-byte chunk of a 16-column slab
@@ -223,21 +217,16 @@ struct MathF32 {
   static constexpr int CTAS = 1;
   static constexpr int E = D / 32;
   static constexpr int OREGS = GP * E;
-  static constexpr int QREGS = 2;
-  static constexpr int QUERY = GP * D * 4, SCRATCH = PAGED_GROUP * GP * 4;  // the query; a group's weights
+  static constexpr int SCRATCH = PAGED_GROUP * GP * 4;  // a group's weights
   static constexpr CUtensorMapDataType TYPE = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   float m[GP], l[GP], o[GP][E];
 
-  // (the raw query is read when a unit begins: the address is what is fetched ahead)
-  static __device__ void fetch_q(const void* q, int, uint32_t (&raw)[QREGS]) {
-    raw[0] = (uint32_t)reinterpret_cast<uintptr_t>(q);
-    raw[1] = (uint32_t)(reinterpret_cast<uintptr_t>(q) >> 32);
-  }
-  __device__ void begin(const uint32_t (&raw)[QREGS], const float2* cs, int G, float2* query) {
-    const float2* q = reinterpret_cast<const float2*>((uintptr_t)raw[0] | ((uintptr_t)raw[1] << 32));
+  // The raw rows are turned where they lie (the registers' heads behind the last: zeros).
+  __device__ void begin(void* query, const float2* cs, int G) {
+    float2* q = static_cast<float2*>(query);
     for (int i = threadIdx.x; i < GP * (D / 2); i += AT_NT) {
-      const float2 x = i < G * (D / 2) ? __ldg(q + i) : make_float2(0.f, 0.f), a = cs[i % (D / 2)];
-      query[i] = make_float2(x.x * a.x - x.y * a.y, x.x * a.y + x.y * a.x);
+      const float2 x = i < G * (D / 2) ? q[i] : make_float2(0.f, 0.f), a = cs[i % (D / 2)];
+      q[i] = make_float2(x.x * a.x - x.y * a.y, x.x * a.y + x.y * a.x);
     }
     __syncthreads();
 #pragma unroll
@@ -248,10 +237,10 @@ struct MathF32 {
       for (int e = 0; e < E; ++e) o[g][e] = 0.f;
     }
   }
-  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, const float2* query,
+  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, const void* query,
                        float* ps) {
     const int lane = threadIdx.x & 31, tok = lane & 15, half = lane >> 4;
-    const float4* qs = reinterpret_cast<const float4*>(query) + half * (D / 8);
+    const float4* qs = static_cast<const float4*>(query) + half * (D / 8);
     float z[GP];
 #pragma unroll
     for (int g = 0; g < GP; ++g) z[g] = 0.f;
@@ -376,7 +365,7 @@ struct Plan {
   static constexpr int OFF_CS = OFF_ML + 2 * 8 * 8;
   static constexpr int OFF_TURNS = OFF_CS + D / 2 * 8;
   static constexpr int OFF_QUERY = OFF_TURNS + D / 2 * 8;
-  static constexpr int OFF_SCRATCH = OFF_QUERY + M::QUERY;
+  static constexpr int OFF_SCRATCH = OFF_QUERY + G_MAX * D * (int)sizeof(typename M::T);
   static constexpr int OFF_BAR = OFF_SCRATCH + AT_NW * M::SCRATCH;
   static constexpr int OFF_HELD = OFF_BAR + AT_NW * STAGES * 8;  // whether a stage's page is in the pool
   static constexpr int OFF_SCAN = OFF_HELD + AT_NW * STAGES * 4;
@@ -407,7 +396,7 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   float2* ml = reinterpret_cast<float2*>(sm + P::OFF_ML);
   float2* cs = reinterpret_cast<float2*>(sm + P::OFF_CS);
   unsigned long long* turns = reinterpret_cast<unsigned long long*>(sm + P::OFF_TURNS);
-  float2* query = reinterpret_cast<float2*>(sm + P::OFF_QUERY);
+  char* query = sm + P::OFF_QUERY;
   float* scratch = reinterpret_cast<float*>(sm + P::OFF_SCRATCH + warp * M::SCRATCH);
   int* held = reinterpret_cast<int*>(sm + P::OFF_HELD) + warp * S;
   unsigned* words = reinterpret_cast<unsigned*>(sm + P::OFF_LINE);
@@ -470,11 +459,15 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   };
   for (int i = 0; i < S; ++i) issue();
 
-  auto query_of = [&](const PagedSegments& s) {
-    return static_cast<const void*>(static_cast<const typename M::T*>(p.q) + ((size_t)s.b * p.Hq + s.h * G) * D);
+  // what a unit begins with, by n of the threads: its raw query rows, and cos and
+  // sin of its sequence's position
+  auto fetch = [&](int i0, int n, int unit) {
+    const char* q = static_cast<const char*>(p.q) + (size_t)unit * G * D * sizeof(typename M::T);
+    for (int i = i0; i < G * D * (int)sizeof(typename M::T) / 16; i += n) cp_async16(smem_u32(query) + 16 * i, q + 16 * i);
+    cp_async_commit();
   };
-  auto turn = [&](int i, int n, int pos) {  // cos and sin of a position, by n threads
-    for (int f = i; f < D / 2; f += n) {
+  auto turn = [&](int i0, int n, int pos) {
+    for (int f = i0; f < D / 2; f += n) {
       const float2 a = rope_cos_sin(turns[f], pos);
       cs[f] = make_float2(a.x * p.scale, a.y * p.scale);
     }
@@ -482,24 +475,19 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   PagedSegments sg;
   sg.start(line, r0, r1);
   sg.at();
-  uint32_t q_raw[M::QREGS];
-  M::fetch_q(query_of(sg), G, q_raw);
+  fetch(tid, AT_NT, sg.unit());
   turn(tid, AT_NT, p.pos[sg.b]);
+  cp_async_wait<0>();
   __syncthreads();
   int k = 0;
   while (true) {
     const int b = sg.b, unit = sg.unit(), len = line.tokens(b);
     M mt;
-    mt.begin(q_raw, cs, G, query);
-    // the next unit's query and position are under way meanwhile
+    mt.begin(query, cs, G);
     PagedSegments nx = sg;
     nx.next();
     const bool more = nx.at();
-    int next_pos = 0;
-    if (more) {
-      M::fetch_q(query_of(nx), G, q_raw);
-      next_pos = __ldg(p.pos + nx.b);
-    }
+    const int next_pos = more ? __ldg(p.pos + nx.b) : 0;
     float* logits = p.weight ? p.logits + (size_t)unit * G * p.T_cap : nullptr;
     for (; k < mine && r0 + warp + k * AT_NW < sg.seg_end(); ++k) {
       const int t0 = (r0 + warp + k * AT_NW - sg.unit_begin) * PAGED_GROUP;
@@ -528,7 +516,8 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
       __syncwarp();
       issue();
     }
-    // the warps' parts, in a fixed order: 2 and 3 into 0 and 1, then both
+    // the warps' parts, in a fixed order: 2 and 3 into 0 and 1, then both; 2 and 3
+    // see to the next unit meanwhile
     mt.finish();
     if (warp >= 2) mt.put(recs + (warp - 2) * M::OREGS * 32, ml + (warp - 2) * 8);
     __syncthreads();
@@ -536,8 +525,10 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
       mt.add(recs + warp * M::OREGS * 32, ml + warp * 8);
       __syncwarp();
       mt.put(recs + warp * M::OREGS * 32, ml + warp * 8);
-    } else if (more && nx.b != b) {
-      turn(tid - 64, 64, next_pos);
+    } else if (more) {
+      fetch(tid - 64, 64, nx.unit());
+      if (nx.b != b) turn(tid - 64, 64, next_pos);
+      cp_async_wait<0>();
     }
     __syncthreads();
     const bool whole = sg.x == sg.unit_begin && sg.unit_end <= r1;
@@ -573,12 +564,14 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
 // --------------------------------------------------------------- join
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
-// Block (c, y): 128 floats of the output of the unit that begins in part c and
-// goes on in the next; with weights, block (c, 0) then adds its share of the
-// line's tokens.
-template <int D>
-__global__ void __launch_bounds__(JN_NT) paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
-  constexpr int NW = JN_NT / 32;
+// Tasks: 128 floats of the output of a unit that was cut, block by block; a
+// task goes by its unit, or, where there are more units than parts, by the part
+// it begins in.  With weights, block c then adds what part c's tokens get.
+// WEIGHTS: without, a block is small enough to wait beside the first kernel's.
+template <int D, bool WEIGHTS>
+__global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
+    paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
+  constexpr int NT = WEIGHTS ? 256 : 128, NW = NT / 32;
   extern __shared__ unsigned words[];
   __shared__ float4 so[NW][32];
   __shared__ float2 sml[NW][32];
@@ -586,27 +579,48 @@ __global__ void __launch_bounds__(JN_NT) paged_join_kernel(const __grid_constant
   __shared__ int scan[NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x, G = p.G;
   const int R = paged_record_floats(G, D);
-  make_line<JN_NT>(p, words, scan, false);
+  make_line<NT>(p, words, scan, false);
   const PagedLine line{words, p.B, p.Hkv};
   const int parts = line.parts(p.grid), total = line.total();
+  const int units = p.B * p.Hkv, slices = (G * D + 127) / 128;
+  const bool by_unit = units <= parts;
+  const int tasks = (by_unit ? units : parts - 1) * slices;
+  // The unit of a task and its parts; false when it was not cut, or does not begin there.
   PagedSegments sg;
-  bool cut = false;
-  if (c + 1 < parts) {
-    const int edge = line.part_begin(parts, c + 1);
-    if (edge > 0 && edge < total) {
+  int c0 = 0, c1 = 0;
+  auto task_at = [&](int task) {
+    const int at = task / slices;
+    if (by_unit) {
+      const int b = at / p.Hkv, h = at - b * p.Hkv, n = line.groups(b);
+      if (n == 0) return false;
+      sg.start(line, 0, 0);
+      sg.b = b;
+      sg.h = h;
+      sg.end = total;
+      sg.x = line.before(b) * p.Hkv + h * n;
+      sg.at();
+    } else {
+      const int edge = line.part_begin(parts, at + 1);
+      if (edge <= 0 || edge >= total) return false;
       sg.start(line, edge - 1, edge);
       sg.at();
-      cut = sg.unit_end > edge && sg.first_part(parts) == c;
+      if (sg.unit_end <= edge) return false;
     }
-  }
+    c0 = sg.first_part(parts);
+    c1 = sg.last_part(parts);
+    return by_unit ? c0 < c1 : c0 == at;
+  };
+  int task = c;
+  bool cut = task < tasks && task_at(task);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  if (cut) {
+  for (; task < tasks; task += gridDim.x, cut = task < tasks && task_at(task)) {
+    if (!cut) continue;
     // a warp takes every NW-th part, a lane four floats of it, then the warps'
     // sums meet, in order
-    const int n = sg.last_part(parts) - c + 1;
-    const int i = min(blockIdx.y * 128 + 4 * lane, G * D - 4), g = i / D;
-    const float* first = p.records + (size_t)(2 * c + 1) * R;
-    const float* rest = p.records + (size_t)(2 * c) * R;
+    const int n = c1 - c0 + 1;
+    const int i0 = (task % slices) * 128 + 4 * lane, i = min(i0, G * D - 4), g = i / D;
+    const float* first = p.records + (size_t)(2 * c0 + 1) * R;
+    const float* rest = p.records + (size_t)(2 * c0) * R;
     float M = -INFINITY, L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 5;
@@ -635,10 +649,11 @@ __global__ void __launch_bounds__(JN_NT) paged_join_kernel(const __grid_constant
         a = make_float4(a.x + o[u].x * e, a.y + o[u].y * e, a.z + o[u].z * e, a.w + o[u].w * e);
       }
     }
+    __syncthreads();  // the last task's sums are read
     so[warp][lane] = a;
     sml[warp][lane] = make_float2(M, L);
     __syncthreads();
-    if (warp == 0 && blockIdx.y * 128 + 4 * lane < G * D) {
+    if (warp == 0 && i0 < G * D) {
       float X = -INFINITY;
 #pragma unroll
       for (int w = 0; w < NW; ++w) X = fmaxf(X, sml[w][lane].x);
@@ -657,16 +672,18 @@ __global__ void __launch_bounds__(JN_NT) paged_join_kernel(const __grid_constant
           make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     }
   }
-  if (!p.weight || blockIdx.y > 0 || c >= parts) return;
+  if constexpr (!WEIGHTS) return;
+  if (c >= parts) return;
   // the part's own tokens
   sg.start(line, line.part_begin(parts, c), line.part_begin(parts, c + 1));
   for (; sg.at(); sg.next()) {
-    const int unit = sg.unit(), c0 = sg.first_part(parts), n = sg.last_part(parts) - c0 + 1;
+    const int unit = sg.unit(), n = sg.last_part(parts) - sg.first_part(parts) + 1;
+    c0 = sg.first_part(parts);
     __syncthreads();
     if (n == 1) {
       if (tid < G) lse[tid] = __ldcg(p.lse + (size_t)unit * G + tid);
     } else if (warp < G) {  // warp g: the parts' (m, l) of head g
-      static_assert(NW >= G_MAX, "a warp for each head");
+      static_assert(!WEIGHTS || NW >= G_MAX, "a warp for each head");
       float M = -INFINITY, L = 0.f;
       for (int k = lane; k < n; k += 32) {
         const float* r = p.records + (size_t)(2 * (c0 + k) + (k == 0)) * R + G * D + warp;
@@ -688,7 +705,7 @@ __global__ void __launch_bounds__(JN_NT) paged_join_kernel(const __grid_constant
     // all there (those behind the end are -inf and get nothing)
     const int t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP;
     const float* z = p.logits + (size_t)unit * G * p.T_cap;
-    for (int t = (sg.x - sg.unit_begin) * PAGED_GROUP + 4 * tid; t < t1; t += 4 * JN_NT) {
+    for (int t = (sg.x - sg.unit_begin) * PAGED_GROUP + 4 * tid; t < t1; t += 4 * NT) {
       float4* at = reinterpret_cast<float4*>(p.weight + (size_t)unit * p.T_cap + t);
       float4 zg[G_MAX];
 #pragma unroll
@@ -769,13 +786,15 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.grid, (p.G * D + 127) / 128);
-  cfg.blockDim = dim3(JN_NT);
+  cfg.gridDim = dim3(p.weight ? p.grid : min(p.grid, sms));
+  cfg.blockDim = dim3(p.weight ? 256 : 128);
   cfg.dynamicSmemBytes = (p.B + 1) * 4;
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_join_kernel<D>, static_cast<const PagedAttendParams&>(p));
+  const PagedAttendParams& cp = p;
+  return p.weight ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, true>, cp)
+                  : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, false>, cp);
 }
 
 }  // namespace

@@ -26,7 +26,7 @@ constexpr int PAGED_UNIT_COST = 6;      // what a unit costs beside its groups, 
 constexpr int PAGED_PART_COST = 12;     // a part costs at least this much (while there is as much)
 constexpr int PAGED_MAX_PARTS = 320;    // parts the workspace has room for
 constexpr int PAGED_MAX_BATCH = 4096;   // the lengths' prefix sums sit in shared memory
-constexpr int PAGED_MAX_SLOTS = 524288; // T_cap: the line's positions fit 31 bits
+constexpr int PAGED_MAX_SLOTS = 262144; // T_cap: the line's positions and costs fit 31 bits
 
 FASA_HD int paged_groups(int len) { return (len + PAGED_GROUP - 1) / PAGED_GROUP; }
 
@@ -39,7 +39,7 @@ FASA_HD long long paged_row(int page, int n_pages, int Hkv, int h, int log2_page
 }
 
 // Word b of the line: the groups of one head of the sequences before b (28
-// bits: at most 4096 * 32768) and by how many tokens b's last group is short (4
+// bits: at most 4096 * 16384) and by how many tokens b's last group is short (4
 // bits); word B: all sequences' groups.
 FASA_HD unsigned paged_word(int before, int len) {
   return (unsigned)before | (unsigned)(paged_groups(len) * PAGED_GROUP - len) << 28;
@@ -64,32 +64,42 @@ struct PagedLine {
     return lo;
   }
 
-  FASA_HD long long cost_before(int b) const { return (long long)Hkv * (before(b) + (long long)PAGED_UNIT_COST * b); }
-  FASA_HD long long cost() const { return cost_before(B); }
+  // (32-bit arithmetic and no wide divisions: every CTA does this before its first copy)
+  FASA_HD int cost_before(int b) const { return Hkv * (before(b) + PAGED_UNIT_COST * b); }
+  FASA_HD int cost() const { return cost_before(B); }
   // Parts of the line, at most `grid`.
   FASA_HD int parts(int grid) const {
-    const long long most = (cost() + PAGED_PART_COST - 1) / PAGED_PART_COST;
-    return most < grid ? (int)most : grid;
+    const int most = (cost() + PAGED_PART_COST - 1) / PAGED_PART_COST;
+    return most < grid ? most : grid;
+  }
+  // Where part c of n begins, in cost: floor(cost() * c / n).
+  FASA_HD int cost_begin(int n, int c) const {
+    const int q = cost() / n, r = cost() - q * n;
+    return q * c + r * c / n;
   }
   // Where part c of n begins on the line (0 <= c <= n; a part may be empty): the
-  // first group that costs no less than c n-ths.
+  // first group that lies at that cost or behind it.
   FASA_HD int part_begin(int n, int c) const {
-    const long long y = cost() * c / n;
-    if (y >= cost()) return total();
+    const int y = cost_begin(n, c);
+    if (c >= n) return total();
     int lo = 0, hi = B;  // cost_before(lo) <= y < cost_before(hi)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (cost_before(mid) <= y) lo = mid;
       else hi = mid;
     }
-    const int g = groups(lo), rem = (int)(y - cost_before(lo));
+    const int g = groups(lo), rem = y - cost_before(lo);
     const int h = rem / (g + PAGED_UNIT_COST), off = rem - h * (g + PAGED_UNIT_COST);
     return before(lo) * Hkv + h * g + (off > PAGED_UNIT_COST ? off - PAGED_UNIT_COST : 0);
   }
   // The part of n that holds group g of unit (b, h).
   FASA_HD int part_of(int n, int b, int h, int g) const {
-    const long long y = cost_before(b) + (long long)h * (groups(b) + PAGED_UNIT_COST) + PAGED_UNIT_COST + g;
-    return (int)(((y + 1) * n - 1) / cost());
+    const int y = cost_before(b) + h * (groups(b) + PAGED_UNIT_COST) + PAGED_UNIT_COST + g;
+    int c = (int)((float)y * ((float)n / (float)cost()));  // at most one off
+    c = c < 0 ? 0 : (c >= n ? n - 1 : c);
+    while (cost_begin(n, c) > y) --c;
+    while (c + 1 < n && cost_begin(n, c + 1) <= y) ++c;
+    return c;
   }
 };
 

@@ -49,7 +49,7 @@ BAD_DIMS = [
     (dict(rope_theta=float("nan")), 1), (dict(dtype=7), 2), (dict(head_dim=96), 2),
     (dict(n_q_heads=72, n_kv_heads=8), 2), (dict(page_size=8), 2), (dict(page_size=48), 2),
     (dict(page_size=512), 2), (dict(batch=4097), 2), (dict(batch=4096, n_kv_heads=16, n_q_heads=16), 2),
-    (dict(max_pages=32769), 2), (dict(n_pages=1 << 24), 2),
+    (dict(max_pages=16385), 2), (dict(n_pages=1 << 24), 2),
 ]
 
 
