@@ -395,7 +395,7 @@ int fasa_decode_step_noalloc(const void* q, const int32_t* pos,
  *  - Alignment: k_pages, v_pages, k_new, v_new, q, out, weight, token_pos and
  *    workspace 16 bytes.
  *  - Supported: dtype FASA_F32 or FASA_BF16, head_dim 64 or 128, 1 <= G <= 8,
- *    page_size 16, 32, 64, 128 or 256, batch <= 4096, batch * Hkv <= 65535,
+ *    page_size 16, 32, 64, 128 or 256, batch <= 2048, batch * Hkv <= 65535,
  *    T_cap <= 262144, n_pages * Hkv * page_size < 2^31.
  */
 typedef struct fasa_paged_dims {

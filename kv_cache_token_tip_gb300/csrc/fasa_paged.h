@@ -51,7 +51,7 @@ struct PagedAttendParams : PagedCommon {
   float* records; // [parts][2][G * (d + 2)]: o [G][d], then m [G], l [G]
   float* lse;     // [units][G] of the units one part holds whole
   float* logits;  // [units][G][T_cap]
-  int grid;       // most parts of this launch
+  int parts;      // most parts of this launch
   unsigned long long wait_ns;  // bound of every device wait
 };
 

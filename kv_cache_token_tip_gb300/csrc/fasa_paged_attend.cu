@@ -8,17 +8,17 @@
 // Two parts (m, l, o), (m', l', o') of a unit join as M = max(m, m'),
 // l 2^(m - M) + l' 2^(m' - M), and o alike.
 //
-// attend: each CTA takes one part of the line of all token groups
-// (fasa_paged_index.h), unit by unit; its warps take groups of 16 tokens in
-// turn, each with a running (m, l, o) of its own, joined at the unit's end in
-// the CTA.  A unit the CTA holds whole is finished there; otherwise its record
-// goes to the workspace.  join: the records of a unit that was cut, in part
-// order; and with weights, a second pass over the logits the first one left.
+// attend: each warp takes one part of the line of all token groups
+// (fasa_paged_index.h), unit by unit, group by group, with a running (m, l, o).
+// A unit it holds whole is finished there; otherwise its record goes to the
+// workspace.  join: the records of a unit that was cut, in a fixed order; and
+// with weights, a second pass over the logits the first one left.
 //
 // The bytes of K and V bound it, so a warp's groups come through a ring of its
 // own in shared memory that TMA fills (one copy of 16 rows for K, one for V, in
 // the 128-byte swizzle: no bank conflicts), page by page wherever the pages
-// lie, and no warp waits for another before a unit's end.
+// lie, and no warp waits for another: what a unit costs beside its bytes is
+// hidden by the other seven warps of the SM.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -83,16 +83,16 @@ __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool rep
 template <int D>
 struct MathBf16 {
   using T = __nv_bfloat16;
-  static constexpr int CTAS = 2;  // per SM: one streams while the other joins a unit's parts
+  static constexpr int CTAS = 2;  // per SM
+  static constexpr int RAW = G_MAX * D * 2;  // the next unit's raw query, fetched while this one is read
   static constexpr int MT = D / 16;
-  static constexpr int OREGS = 4 * MT;
   static constexpr int SCRATCH = 0;  // shared memory of a warp
   static constexpr CUtensorMapDataType TYPE = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   uint32_t qa[MT][4], ql[MT][2];
   float m, l, o[MT][4];
 
-  // query: the unit's raw rows [G][D], behind a barrier.
-  __device__ void begin(const void* query, const float2* cs, int G) {
+  // query: the unit's raw rows [G][D].
+  __device__ void begin(const void* query, const float2* cs, int G, float*) {
     const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
     const uint32_t* raw = static_cast<const uint32_t*>(query) + min(g, G - 1) * (D / 2);
 #pragma unroll
@@ -108,17 +108,16 @@ struct MathBf16 {
     m = -INFINITY;
     l = 0.f;
 #pragma unroll
-    for (int i = 0; i < OREGS; ++i) o[i >> 2][i & 3] = 0.f;
+    for (int i = 0; i < 4 * MT; ++i) o[i >> 2][i & 3] = 0.f;
   }
   __device__ void scale_o(float a) {
     const int t = threadIdx.x & 3;
     const float a0 = __shfl_sync(0xffffffffu, a, 8 * t), a1 = __shfl_sync(0xffffffffu, a, 8 * t + 4);
 #pragma unroll
-    for (int i = 0; i < OREGS; ++i) o[i >> 2][i & 3] *= (i & 1) ? a1 : a0;
+    for (int i = 0; i < 4 * MT; ++i) o[i >> 2][i & 3] *= (i & 1) ? a1 : a0;
   }
   // One group: K at kb, V at vb, its first n tokens count; logits [G][stride] at the group, or null.
-  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, const void*,
-                       float*) {
+  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, float*) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // ldmatrix: this lane's row of the group and 16-byte chunk of a 16-column slab
     const int lrow = (lane & 7) + ((lane >> 4) << 3), lch = (lane >> 3) & 1;
@@ -175,34 +174,26 @@ struct MathBf16 {
       mma_bf16_16816(o[i], a0, a1, a2, a3, l0, l1);
     }
   }
+  // l of a head in all its lanes.
   __device__ void finish() {
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
   }
-  // The record of a warp: OREGS x 32 floats lane by lane, and (m, l) of 8 heads.
-  __device__ void put(float* rec, float2* ml) const {
+  // (m, l) of head g to ml(g, m, l), by one lane; o times inv (by head) to to[head][dim].
+  template <class F>
+  __device__ void stats(int G, F&& ml) const {
     const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int i = 0; i < OREGS; ++i) rec[i * 32 + lane] = o[i >> 2][i & 3];
-    if ((lane & 3) == 0) ml[lane >> 2] = make_float2(m, l);
+    if ((lane & 3) == 0 && (lane >> 2) < G) ml(lane >> 2, m, l);
   }
-  __device__ void add(const float* rec, const float2* ml) {
-    const int lane = threadIdx.x & 31, t = lane & 3;
-    const float2 other = ml[lane >> 2];
-    const float M = fmaxf(m, other.x), Ms = M == -INFINITY ? 0.f : M;
-    const float a = exp2f(m - Ms), e = exp2f(other.x - Ms);
-    m = M;
-    l = l * a + other.y * e;
-    scale_o(a);
-    const float e0 = __shfl_sync(0xffffffffu, e, 8 * t), e1 = __shfl_sync(0xffffffffu, e, 8 * t + 4);
+  __device__ void write(float* to, int G, bool divide) const {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const float inv = !divide ? 1.f : l > 0.f ? 1.f / l : 0.f;
+    const float i0 = __shfl_sync(0xffffffffu, inv, 8 * t), i1 = __shfl_sync(0xffffffffu, inv, 8 * t + 4);
 #pragma unroll
-    for (int i = 0; i < OREGS; ++i) o[i >> 2][i & 3] += rec[i * 32 + lane] * ((i & 1) ? e1 : e0);
-  }
-  // Head and dim of float i of a record.
-  static __device__ void place(int i, int& head, int& dim) {
-    const int lane = i & 31, e = (i >> 5) & 3;
-    head = (lane & 3) * 2 + (e & 1);
-    dim = (i >> 7) * 16 + (lane >> 2) + (e >> 1) * 8;
+    for (int i = 0; i < 4 * MT; ++i) {
+      const int head = 2 * t + (i & 1);
+      if (head < G) to[head * D + (i >> 2) * 16 + g + ((i >> 1) & 1) * 8] = o[i >> 2][i & 3] * ((i & 1) ? i1 : i0);
+    }
   }
 };
 
@@ -215,20 +206,21 @@ template <int D, int GP>
 struct MathF32 {
   using T = float;
   static constexpr int CTAS = 1;
+  static constexpr int RAW = 0;  // (no room to fetch ahead: the raw query goes where the turned one stays)
   static constexpr int E = D / 32;
-  static constexpr int OREGS = GP * E;
-  static constexpr int SCRATCH = PAGED_GROUP * GP * 4;  // a group's weights
+  static constexpr int SCRATCH = (GP * D + PAGED_GROUP * GP) * 4;  // the query, a group's weights
   static constexpr CUtensorMapDataType TYPE = CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   float m[GP], l[GP], o[GP][E];
 
-  // The raw rows are turned where they lie (the registers' heads behind the last: zeros).
-  __device__ void begin(void* query, const float2* cs, int G) {
-    float2* q = static_cast<float2*>(query);
-    for (int i = threadIdx.x; i < GP * (D / 2); i += AT_NT) {
-      const float2 x = i < G * (D / 2) ? q[i] : make_float2(0.f, 0.f), a = cs[i % (D / 2)];
-      q[i] = make_float2(x.x * a.x - x.y * a.y, x.x * a.y + x.y * a.x);
+  // The raw rows [G][D] are turned where they lie; zeros behind the last head.
+  __device__ void begin(const void*, const float2* cs, int G, float* scratch) {
+    float2* qs = reinterpret_cast<float2*>(scratch);
+#pragma unroll 4
+    for (int i = threadIdx.x & 31; i < GP * (D / 2); i += 32) {
+      const float2 x = i < G * (D / 2) ? qs[i] : make_float2(0.f, 0.f), a = cs[i % (D / 2)];
+      qs[i] = make_float2(x.x * a.x - x.y * a.y, x.x * a.y + x.y * a.x);
     }
-    __syncthreads();
+    __syncwarp();
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
       m[g] = -INFINITY;
@@ -237,10 +229,10 @@ struct MathF32 {
       for (int e = 0; e < E; ++e) o[g][e] = 0.f;
     }
   }
-  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, const void* query,
-                       float* ps) {
+  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, float* scratch) {
     const int lane = threadIdx.x & 31, tok = lane & 15, half = lane >> 4;
-    const float4* qs = static_cast<const float4*>(query) + half * (D / 8);
+    const float4* qs = reinterpret_cast<const float4*>(scratch) + half * (D / 8);
+    float* ps = scratch + GP * D;
     float z[GP];
 #pragma unroll
     for (int g = 0; g < GP; ++g) z[g] = 0.f;
@@ -322,50 +314,38 @@ struct MathF32 {
 #pragma unroll
       for (int s = 1; s < 32; s <<= 1) l[g] += __shfl_xor_sync(0xffffffffu, l[g], s);
   }
-  __device__ void put(float* rec, float2* ml) const {
+  template <class F>
+  __device__ void stats(int G, F&& ml) const {
+#pragma unroll
+    for (int g = 0; g < GP; ++g)
+      if ((threadIdx.x & 31) == g && g < G) ml(g, m[g], l[g]);
+  }
+  __device__ void write(float* to, int G, bool divide) const {
     const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int g = 0; g < GP; ++g) {
+      const float inv = !divide ? 1.f : l[g] > 0.f ? 1.f / l[g] : 0.f;
+      if (g < G) {
 #pragma unroll
-      for (int e = 0; e < E; ++e) rec[(g * E + e) * 32 + lane] = o[g][e];
-      if (lane == g) ml[g] = make_float2(m[g], l[g]);
+        for (int e = 0; e < E; ++e) to[g * D + lane * E + e] = o[g][e] * inv;
+      }
     }
-  }
-  __device__ void add(const float* rec, const float2* ml) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int g = 0; g < GP; ++g) {
-      const float2 other = ml[g];
-      const float M = fmaxf(m[g], other.x), Ms = M == -INFINITY ? 0.f : M;
-      const float a = exp2f(m[g] - Ms), b = exp2f(other.x - Ms);
-      m[g] = M;
-      l[g] = l[g] * a + other.y * b;
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[g][e] = o[g][e] * a + rec[(g * E + e) * 32 + lane] * b;
-    }
-  }
-  static __device__ void place(int i, int& head, int& dim) {
-    const int r = i >> 5;
-    head = r / E;
-    dim = (i & 31) * E + r % E;
   }
 };
 
 // ------------------------------------------------------------- attend
-// Shared memory from a 1024-byte boundary: the warps' rings; two records and
-// their (m, l); cos and sin of the sequence's position; and what follows.
+// Shared memory from a 1024-byte boundary; what a warp has, and the line.
 template <int D, class M>
 struct Plan {
-  static constexpr int SLABS = D * (int)sizeof(typename M::T) / 128;  // 128-byte columns of a row
-  static constexpr int ROWS = SLABS * PAGED_GROUP * 128;              // K or V of a group
+  static constexpr int ES = sizeof(typename M::T);
+  static constexpr int SLABS = D * ES / 128;              // 128-byte columns of a row
+  static constexpr int ROWS = SLABS * PAGED_GROUP * 128;  // K or V of a group
   static constexpr int STAGE = 2 * ROWS;
   static constexpr int STAGES = 196608 / M::CTAS / (AT_NW * STAGE);
-  static constexpr int OFF_REC = AT_NW * STAGES * STAGE;
-  static constexpr int OFF_ML = OFF_REC + 2 * M::OREGS * 32 * 4;
-  static constexpr int OFF_CS = OFF_ML + 2 * 8 * 8;
-  static constexpr int OFF_TURNS = OFF_CS + D / 2 * 8;
-  static constexpr int OFF_QUERY = OFF_TURNS + D / 2 * 8;
-  static constexpr int OFF_SCRATCH = OFF_QUERY + G_MAX * D * (int)sizeof(typename M::T);
+  static constexpr int OFF_RAW = AT_NW * STAGES * STAGE;
+  static constexpr int OFF_CS = OFF_RAW + AT_NW * M::RAW;
+  static constexpr int OFF_TURNS = OFF_CS + AT_NW * D / 2 * 8;
+  static constexpr int OFF_SCRATCH = OFF_TURNS + D / 2 * 8;
   static constexpr int OFF_BAR = OFF_SCRATCH + AT_NW * M::SCRATCH;
   static constexpr int OFF_HELD = OFF_BAR + AT_NW * STAGES * 8;  // whether a stage's page is in the pool
   static constexpr int OFF_SCAN = OFF_HELD + AT_NW * STAGES * 4;
@@ -392,12 +372,10 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int G = p.G;
-  float* recs = reinterpret_cast<float*>(sm + P::OFF_REC);
-  float2* ml = reinterpret_cast<float2*>(sm + P::OFF_ML);
-  float2* cs = reinterpret_cast<float2*>(sm + P::OFF_CS);
+  float2* cs = reinterpret_cast<float2*>(sm + P::OFF_CS) + warp * (D / 2);
   unsigned long long* turns = reinterpret_cast<unsigned long long*>(sm + P::OFF_TURNS);
-  char* query = sm + P::OFF_QUERY;
   float* scratch = reinterpret_cast<float*>(sm + P::OFF_SCRATCH + warp * M::SCRATCH);
+  char* query = M::RAW ? sm + P::OFF_RAW + warp * M::RAW : reinterpret_cast<char*>(scratch);
   int* held = reinterpret_cast<int*>(sm + P::OFF_HELD) + warp * S;
   unsigned* words = reinterpret_cast<unsigned*>(sm + P::OFF_LINE);
   const uint32_t ring = smem_u32(sm) + warp * S * P::STAGE;
@@ -413,24 +391,23 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   if (lane < TW) turns[warp * TW + lane] = p.rope_turns[warp * TW + lane];
   make_line<AT_NT>(p, words, reinterpret_cast<int*>(sm + P::OFF_SCAN), blockIdx.x == 0);
   const PagedLine line{words, p.B, p.Hkv};
-  const int parts = line.parts(p.grid);
-  const int c = blockIdx.x;
-  for (int b = c; b < p.B; b += p.grid)  // sequences without a token: zeros
+  for (int b = blockIdx.x; b < p.B; b += gridDim.x)  // sequences without a token: zeros
     if (line.groups(b) == 0)
       for (int i = tid; i < p.Hq * D; i += AT_NT) p.out[(size_t)b * p.Hq * D + i] = 0.f;
+  // few parts lie on as many SMs
+  const int parts = line.parts(p.parts), c = warp * gridDim.x + blockIdx.x;
   if (c >= parts) return;
   const int r0 = line.part_begin(parts, c), r1 = line.part_begin(parts, c + 1);
   if (r0 == r1) return;
 
-  // This warp's groups: x = r0 + warp + k * AT_NW, k < mine.  Lane i holds the
-  // pool row of group (batch of 32) + i.
-  const int mine = max(0, (r1 - r0 - warp + AT_NW - 1) / AT_NW);
+  // Lane i holds the pool row of group (batch of 32) + i of this part.
+  const int mine = r1 - r0;
   int rows = -1, issued = 0, landed = 0;
   bool dead = false;  // a wait ran out: nothing more is copied or waited for
   auto look_up = [&](int k) {
-    const int x = r0 + warp + (k + lane) * AT_NW;
+    const int x = r0 + k + lane;
     rows = -1;
-    if (k + lane < mine) {
+    if (x < r1) {
       const int b = line.sequence_of(x);
       const int n = line.groups(b), rem = x - line.before(b) * p.Hkv;
       const int h = rem / n, slot = (rem - h * n) * PAGED_GROUP;
@@ -459,38 +436,41 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   };
   for (int i = 0; i < S; ++i) issue();
 
-  // what a unit begins with, by n of the threads: its raw query rows, and cos and
-  // sin of its sequence's position
-  auto fetch = [&](int i0, int n, int unit) {
-    const char* q = static_cast<const char*>(p.q) + (size_t)unit * G * D * sizeof(typename M::T);
-    for (int i = i0; i < G * D * (int)sizeof(typename M::T) / 16; i += n) cp_async16(smem_u32(query) + 16 * i, q + 16 * i);
+  auto fetch = [&](int unit) {  // a unit's raw query rows
+    const char* q = static_cast<const char*>(p.q) + (size_t)unit * G * D * P::ES;
+    for (int i = lane; i < G * D * P::ES / 16; i += 32) cp_async16(smem_u32(query) + 16 * i, q + 16 * i);
     cp_async_commit();
-  };
-  auto turn = [&](int i0, int n, int pos) {
-    for (int f = i0; f < D / 2; f += n) {
-      const float2 a = rope_cos_sin(turns[f], pos);
-      cs[f] = make_float2(a.x * p.scale, a.y * p.scale);
-    }
   };
   PagedSegments sg;
   sg.start(line, r0, r1);
   sg.at();
-  fetch(tid, AT_NT, sg.unit());
-  turn(tid, AT_NT, p.pos[sg.b]);
-  cp_async_wait<0>();
-  __syncthreads();
-  int k = 0;
-  while (true) {
-    const int b = sg.b, unit = sg.unit(), len = line.tokens(b);
+  if (M::RAW) fetch(sg.unit());
+  int k = 0, turned = -1, pos = __ldg(p.pos + sg.b);
+  for (bool more = true; more;) {
+    const int unit = sg.unit(), len = line.tokens(sg.b);
+    if (!M::RAW) fetch(unit);
+    if (sg.b != turned) {
+      turned = sg.b;
+      for (int f = lane; f < D / 2; f += 32) {
+        const float2 a = rope_cos_sin(turns[f], pos);
+        cs[f] = make_float2(a.x * p.scale, a.y * p.scale);
+      }
+    }
+    cp_async_wait<0>();
+    __syncwarp();
     M mt;
-    mt.begin(query, cs, G);
-    PagedSegments nx = sg;
-    nx.next();
-    const bool more = nx.at();
-    const int next_pos = more ? __ldg(p.pos + nx.b) : 0;
+    mt.begin(query, cs, G, scratch);
+    __syncwarp();
+    const int first = sg.x, begin = sg.unit_begin, end = sg.unit_end, last = sg.seg_end();
+    sg.next();
+    more = sg.at();
+    if (more) {
+      if (M::RAW) fetch(sg.unit());
+      pos = __ldg(p.pos + sg.b);
+    }
     float* logits = p.weight ? p.logits + (size_t)unit * G * p.T_cap : nullptr;
-    for (; k < mine && r0 + warp + k * AT_NW < sg.seg_end(); ++k) {
-      const int t0 = (r0 + warp + k * AT_NW - sg.unit_begin) * PAGED_GROUP;
+    for (; r0 + k < last; ++k) {
+      const int t0 = (r0 + k - begin) * PAGED_GROUP;
       const int st = k % S;
       const uint32_t kb = ring + st * P::STAGE, vb = kb + P::ROWS;
       if (!dead && !mbar_wait_bounded(bars + 8 * st, (k / S) & 1, p.wait_ns)) {
@@ -512,49 +492,23 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
         fence_proxy_async();
         __syncwarp();
       }
-      mt.step(kb, vb, n, logits ? logits + t0 : nullptr, p.T_cap, G, query, scratch);
+      mt.step(kb, vb, n, logits ? logits + t0 : nullptr, p.T_cap, G, scratch);
       __syncwarp();
       issue();
     }
-    // the warps' parts, in a fixed order: 2 and 3 into 0 and 1, then both; 2 and 3
-    // see to the next unit meanwhile
     mt.finish();
-    if (warp >= 2) mt.put(recs + (warp - 2) * M::OREGS * 32, ml + (warp - 2) * 8);
-    __syncthreads();
-    if (warp < 2) {
-      mt.add(recs + warp * M::OREGS * 32, ml + warp * 8);
-      __syncwarp();
-      mt.put(recs + warp * M::OREGS * 32, ml + warp * 8);
-    } else if (more) {
-      fetch(tid - 64, 64, nx.unit());
-      if (nx.b != b) turn(tid - 64, 64, next_pos);
-      cp_async_wait<0>();
+    if (first == begin && last == end) {
+      mt.write(p.out + (size_t)unit * G * D, G, true);
+      if (p.weight)
+        mt.stats(G, [&](int g, float m, float l) { p.lse[(size_t)unit * G + g] = l > 0.f ? m + log2f(l) : INFINITY; });
+    } else {
+      float* rec = p.records + (size_t)(2 * c + (begin < r0 ? 0 : 1)) * paged_record_floats(G, D);
+      mt.write(rec, G, false);
+      mt.stats(G, [&](int g, float m, float l) {
+        rec[G * D + g] = m;
+        rec[G * D + G + g] = l;
+      });
     }
-    __syncthreads();
-    const bool whole = sg.x == sg.unit_begin && sg.unit_end <= r1;
-    float* rec = p.records + (size_t)(2 * c + (sg.unit_begin < r0 ? 0 : 1)) * paged_record_floats(G, D);
-    for (int i = tid; i < M::OREGS * 32; i += AT_NT) {
-      int hd, dim;
-      M::place(i, hd, dim);
-      if (hd >= G) continue;
-      const float2 e0 = ml[hd], e1 = ml[8 + hd];
-      const float X = fmaxf(e0.x, e1.x), Xs = X == -INFINITY ? 0.f : X;
-      const float a0 = exp2f(e0.x - Xs), a1 = exp2f(e1.x - Xs);
-      const float L = e0.y * a0 + e1.y * a1, O = recs[i] * a0 + recs[M::OREGS * 32 + i] * a1;
-      if (whole) {
-        p.out[((size_t)unit * G + hd) * D + dim] = L > 0.f ? O / L : 0.f;
-        if (p.weight && dim == 0) p.lse[(size_t)unit * G + hd] = L > 0.f ? X + log2f(L) : INFINITY;
-      } else {
-        rec[hd * D + dim] = O;
-        if (dim == 0) {
-          rec[G * D + hd] = X;
-          rec[G * D + G + hd] = L;
-        }
-      }
-    }
-    if (!more) break;
-    __syncthreads();
-    sg = nx;
   }
   // after a wait that ran out: no copy may land in memory of a block that is gone
   for (; landed < issued; ++landed)
@@ -564,27 +518,31 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
 // --------------------------------------------------------------- join
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
-// Tasks: 128 floats of the output of a unit that was cut, block by block; a
-// task goes by its unit, or, where there are more units than parts, by the part
-// it begins in.  With weights, block c then adds what part c's tokens get.
+// Tasks: a slice of the output of a unit that was cut, block by block; a task
+// goes by its unit, or, where there are more units than parts, by the part the
+// unit begins in.  A slice is 128 floats, a record's to a warp; 32, four
+// records' to a warp, where units are few and so cut into many parts.  With
+// weights, each block then adds what its share of the line's tokens gets.
 // WEIGHTS: without, a block is small enough to wait beside the first kernel's.
 template <int D, bool WEIGHTS>
 __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
     paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
   constexpr int NT = WEIGHTS ? 256 : 128, NW = NT / 32;
   extern __shared__ unsigned words[];
-  __shared__ float4 so[NW][32];
-  __shared__ float2 sml[NW][32];
+  __shared__ float4 so[NT];
+  __shared__ float2 sml[NT];
   __shared__ float lse[G_MAX];
   __shared__ int scan[NW];
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, c = blockIdx.x, G = p.G;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
   const int R = paged_record_floats(G, D);
   make_line<NT>(p, words, scan, false);
   const PagedLine line{words, p.B, p.Hkv};
-  const int parts = line.parts(p.grid), total = line.total();
-  const int units = p.B * p.Hkv, slices = (G * D + 127) / 128;
+  const int parts = line.parts(p.parts), total = line.total();
+  const int units = p.B * p.Hkv;
   const bool by_unit = units <= parts;
-  const int tasks = (by_unit ? units : parts - 1) * slices;
+  const bool fine = by_unit && (long long)units * G * (D / 32) <= gridDim.x;
+  const int lanes = fine ? 8 : 32, width = 4 * lanes, slices = (G * D + width - 1) / width;
+  const int tasks = (by_unit ? units : max(parts - 1, 0)) * slices;
   // The unit of a task and its parts; false when it was not cut, or does not begin there.
   PagedSegments sg;
   int c0 = 0, c1 = 0;
@@ -593,10 +551,10 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
     if (by_unit) {
       const int b = at / p.Hkv, h = at - b * p.Hkv, n = line.groups(b);
       if (n == 0) return false;
-      sg.start(line, 0, 0);
+      sg.line = line;
+      sg.end = total;
       sg.b = b;
       sg.h = h;
-      sg.end = total;
       sg.x = line.before(b) * p.Hkv + h * n;
       sg.at();
     } else {
@@ -610,26 +568,26 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
     c1 = sg.last_part(parts);
     return by_unit ? c0 < c1 : c0 == at;
   };
-  int task = c;
-  bool cut = task < tasks && task_at(task);
+  int task = blockIdx.x;
+  bool cut_here = task < tasks && task_at(task);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (; task < tasks; task += gridDim.x, cut = task < tasks && task_at(task)) {
-    if (!cut) continue;
-    // a warp takes every NW-th part, a lane four floats of it, then the warps'
-    // sums meet, in order
-    const int n = c1 - c0 + 1;
-    const int i0 = (task % slices) * 128 + 4 * lane, i = min(i0, G * D - 4), g = i / D;
+  for (; task < tasks; task += gridDim.x, cut_here = task < tasks && task_at(task)) {
+    if (!cut_here) continue;
+    // rows of `lanes` lanes take every rows-th part, a lane four floats of it,
+    // then the rows' sums meet, in order
+    const int n = c1 - c0 + 1, nrows = NT / lanes, row = tid / lanes, at = tid - row * lanes;
+    const int i0 = (task % slices) * width + 4 * at, i = min(i0, G * D - 4), g = i / D;
     const float* first = p.records + (size_t)(2 * c0 + 1) * R;
     const float* rest = p.records + (size_t)(2 * c0) * R;
     float M = -INFINITY, L = 0.f;
     float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
     constexpr int U = 5;
-    for (int k0 = warp; k0 < n; k0 += U * NW) {
+    for (int k0 = row; k0 < n; k0 += U * nrows) {
       float4 o[U];
       float m[U], l[U];
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const int k = k0 + u * NW;
+        const int k = k0 + u * nrows;
         const float* r = k == 0 ? first : rest + (size_t)(2 * k) * R;
         o[u] = k < n ? __ldcg(reinterpret_cast<const float4*>(r + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
         m[u] = k < n ? __ldcg(r + G * D + g) : -INFINITY;
@@ -650,21 +608,21 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
       }
     }
     __syncthreads();  // the last task's sums are read
-    so[warp][lane] = a;
-    sml[warp][lane] = make_float2(M, L);
+    so[tid] = a;
+    sml[tid] = make_float2(M, L);
     __syncthreads();
-    if (warp == 0 && i0 < G * D) {
+    if (row == 0 && i0 < G * D) {
       float X = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < NW; ++w) X = fmaxf(X, sml[w][lane].x);
+      for (int w = 0; w < nrows; ++w) X = fmaxf(X, sml[w * lanes + at].x);
       const float Xs = finite_or_0(X);
       L = 0.f;
       a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < NW; ++w) {
-        const float e = exp2f(sml[w][lane].x - Xs);
-        const float4 o = so[w][lane];
-        L += sml[w][lane].y * e;
+#pragma unroll 4
+      for (int w = 0; w < nrows; ++w) {
+        const float2 s = sml[w * lanes + at];
+        const float e = exp2f(s.x - Xs);
+        const float4 o = so[w * lanes + at];
+        L += s.y * e;
         a = make_float4(a.x + o.x * e, a.y + o.y * e, a.z + o.z * e, a.w + o.w * e);
       }
       const float inv = L > 0.f ? 1.f / L : 0.f;
@@ -673,20 +631,19 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
     }
   }
   if constexpr (!WEIGHTS) return;
-  if (c >= parts) return;
-  // the part's own tokens
-  sg.start(line, line.part_begin(parts, c), line.part_begin(parts, c + 1));
+  sg.start(line, cut(total, gridDim.x, blockIdx.x), cut(total, gridDim.x, blockIdx.x + 1));
   for (; sg.at(); sg.next()) {
-    const int unit = sg.unit(), n = sg.last_part(parts) - sg.first_part(parts) + 1;
+    const int unit = sg.unit();
     c0 = sg.first_part(parts);
+    c1 = sg.last_part(parts);
     __syncthreads();
-    if (n == 1) {
+    if (c0 == c1) {
       if (tid < G) lse[tid] = __ldcg(p.lse + (size_t)unit * G + tid);
     } else if (warp < G) {  // warp g: the parts' (m, l) of head g
       static_assert(!WEIGHTS || NW >= G_MAX, "a warp for each head");
       float M = -INFINITY, L = 0.f;
-      for (int k = lane; k < n; k += 32) {
-        const float* r = p.records + (size_t)(2 * (c0 + k) + (k == 0)) * R + G * D + warp;
+      for (int k = c0 + lane; k <= c1; k += 32) {
+        const float* r = p.records + (size_t)(2 * k + (k == c0)) * R + G * D + warp;
         const float m = __ldcg(r), l = __ldcg(r + G), X = fmaxf(M, m), Xs = finite_or_0(X);
         L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
         M = X;
@@ -703,7 +660,7 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
     __syncthreads();
     // four tokens a thread: a group's slots, and so its logits and weights, are
     // all there (those behind the end are -inf and get nothing)
-    const int t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP;
+    const int t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP, tokens = line.tokens(sg.b);
     const float* z = p.logits + (size_t)unit * G * p.T_cap;
     for (int t = (sg.x - sg.unit_begin) * PAGED_GROUP + 4 * tid; t < t1; t += 4 * NT) {
       float4* at = reinterpret_cast<float4*>(p.weight + (size_t)unit * p.T_cap + t);
@@ -722,7 +679,7 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
           w.z += exp2f(zg[g].z - e);
           w.w += exp2f(zg[g].w - e);
         }
-      const int live = line.tokens(sg.b) - t;  // slots behind the end keep what they hold
+      const int live = tokens - t;  // slots behind the end keep what they hold
       if (live >= 4) {
         *at = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
       } else {
@@ -773,20 +730,21 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   if (e == cudaSuccess) e = pool_map(&vm, p.v_pages, rows, D, sizeof(typename M::T), M::TYPE);
   if (e != cudaSuccess) return e;
   const int smem = Plan<D, M>::bytes(p.B);
-  // as many parts as CTAs are resident at once: M::CTAS to an SM while the
-  // lengths of the batch leave them the room (228 KB, 1 KB of it the system's)
+  // as many parts as warps are resident at once: M::CTAS CTAs to an SM while the
+  // lengths of the batch leave them the room (228 KB, 1 KB of it each CTA's system's)
   const int ctas = M::CTAS * (smem + 1024) <= 233472 ? M::CTAS : 1;
-  p.grid = min(ctas * sms, PAGED_MAX_PARTS);
+  const int grid = min(ctas * sms, PAGED_MAX_PARTS / AT_NW);
+  p.parts = grid * AT_NW;
   e = cudaFuncSetAttribute(paged_attend_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  paged_attend_kernel<D, M><<<p.grid, AT_NT, smem, s>>>(p, km, vm);
+  paged_attend_kernel<D, M><<<grid, AT_NT, smem, s>>>(p, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.weight ? p.grid : min(p.grid, sms));
+  cfg.gridDim = dim3(p.weight ? 2 * sms : sms);
   cfg.blockDim = dim3(p.weight ? 256 : 128);
   cfg.dynamicSmemBytes = (p.B + 1) * 4;
   cfg.stream = s;

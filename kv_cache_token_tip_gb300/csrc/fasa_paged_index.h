@@ -5,10 +5,10 @@
 // Tokens are handled in groups of PAGED_GROUP slots; a page holds whole groups,
 // so a group's rows of one KV head are contiguous.  A unit is a (sequence, KV
 // head); unit (b, h) has ceil(len_b / PAGED_GROUP) groups.  All groups, units in
-// order, form one line 0 .. total-1, cut into parts, one to a CTA; a unit is
+// order, form one line 0 .. total-1, cut into parts, one to a warp; a unit is
 // joined from the parts it touches.  The cuts are even in cost: a unit costs
-// its groups and PAGED_UNIT_COST more (its query, its join), so that a part of
-// many short units takes no longer than one of a long one.
+// its groups and PAGED_UNIT_COST more (its query, its output), so that a part
+// of many short units takes no longer than one of a long one.
 #pragma once
 
 #include <stdint.h>
@@ -22,13 +22,19 @@
 namespace fasa {
 
 constexpr int PAGED_GROUP = 16;         // tokens per group
-constexpr int PAGED_UNIT_COST = 6;      // what a unit costs beside its groups, in groups
-constexpr int PAGED_PART_COST = 12;     // a part costs at least this much (while there is as much)
-constexpr int PAGED_MAX_PARTS = 320;    // parts the workspace has room for
-constexpr int PAGED_MAX_BATCH = 4096;   // the lengths' prefix sums sit in shared memory
+constexpr int PAGED_UNIT_COST = 1;      // what a unit costs beside its groups, in groups
+constexpr int PAGED_PART_COST = 4;     // a part costs at least this much (while there is as much)
+constexpr int PAGED_MAX_PARTS = 1280;   // parts the workspace has room for
+constexpr int PAGED_MAX_BATCH = 2048;   // the lengths' prefix sums sit in shared memory
 constexpr int PAGED_MAX_SLOTS = 262144; // T_cap: the line's positions and costs fit 31 bits
 
 FASA_HD int paged_groups(int len) { return (len + PAGED_GROUP - 1) / PAGED_GROUP; }
+
+// floor(total * c / n), 0 <= c <= n <= 4096.
+FASA_HD int cut(int total, int n, int c) {
+  const int q = total / n, r = total - q * n;
+  return q * c + r * c / n;
+}
 
 // Row (of d elements) of `slot`'s token of KV head h in a pool of pages
 // [n_pages, Hkv, page_size, d], the page being page_table's entry; -1 for an
@@ -39,7 +45,7 @@ FASA_HD long long paged_row(int page, int n_pages, int Hkv, int h, int log2_page
 }
 
 // Word b of the line: the groups of one head of the sequences before b (28
-// bits: at most 4096 * 16384) and by how many tokens b's last group is short (4
+// bits: at most 2048 * 16384) and by how many tokens b's last group is short (4
 // bits); word B: all sequences' groups.
 FASA_HD unsigned paged_word(int before, int len) {
   return (unsigned)before | (unsigned)(paged_groups(len) * PAGED_GROUP - len) << 28;
@@ -72,11 +78,8 @@ struct PagedLine {
     const int most = (cost() + PAGED_PART_COST - 1) / PAGED_PART_COST;
     return most < grid ? most : grid;
   }
-  // Where part c of n begins, in cost: floor(cost() * c / n).
-  FASA_HD int cost_begin(int n, int c) const {
-    const int q = cost() / n, r = cost() - q * n;
-    return q * c + r * c / n;
-  }
+  // Where part c of n begins, in cost.
+  FASA_HD int cost_begin(int n, int c) const { return cut(cost(), n, c); }
   // Where part c of n begins on the line (0 <= c <= n; a part may be empty): the
   // first group that lies at that cost or behind it.
   FASA_HD int part_begin(int n, int c) const {

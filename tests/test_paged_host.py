@@ -48,7 +48,7 @@ BAD_DIMS = [
     (dict(page_size=0), 1), (dict(n_pages=0), 1), (dict(max_pages=0), 1), (dict(rope_theta=0.0), 1),
     (dict(rope_theta=float("nan")), 1), (dict(dtype=7), 2), (dict(head_dim=96), 2),
     (dict(n_q_heads=72, n_kv_heads=8), 2), (dict(page_size=8), 2), (dict(page_size=48), 2),
-    (dict(page_size=512), 2), (dict(batch=4097), 2), (dict(batch=4096, n_kv_heads=16, n_q_heads=16), 2),
+    (dict(page_size=512), 2), (dict(batch=2049), 2), (dict(batch=2048, n_kv_heads=32, n_q_heads=32), 2),
     (dict(max_pages=16385), 2), (dict(n_pages=1 << 24), 2),
 ]
 
@@ -176,7 +176,7 @@ static int check(const std::vector<int>& lens, int Hkv, int grid) {
 }
 
 int main() {
-  const int grids[] = {1, 3, 152, 304, PAGED_MAX_PARTS};
+  const int grids[] = {1, 3, 152, 608, PAGED_MAX_PARTS};
   srand(7);
   for (int grid : grids)
     for (int Hkv : {1, 2, 7, 8}) {
@@ -190,7 +190,7 @@ int main() {
       }
     }
   // the longest lines: 65535 units of PAGED_MAX_SLOTS slots; the largest batch
-  for (int B : {1, 4095}) {
+  for (int B : {1, PAGED_MAX_BATCH}) {
     const int Hkv = 65535 / B, g = PAGED_MAX_SLOTS / PAGED_GROUP;
     const std::vector<unsigned> w = words(std::vector<int>(B, PAGED_MAX_SLOTS - 1));
     const PagedLine line{w.data(), B, Hkv};
