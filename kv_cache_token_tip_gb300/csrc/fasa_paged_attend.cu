@@ -354,11 +354,12 @@ struct Plan {
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits one CTA");
 };
 
-__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar) {
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int row, uint32_t bar,
+                                         unsigned long long policy) {
   asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          dst),
-      "l"(map), "r"(0), "r"(row), "r"(0), "r"(bar)
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, %3, "
+      "%4}], [%5], %6;" ::"r"(dst),
+      "l"(map), "r"(0), "r"(row), "r"(0), "r"(bar), "l"(policy)
       : "memory");
 }
 
@@ -397,9 +398,15 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
   // few parts lie on as many SMs
   const int parts = line.parts(p.parts), c = warp * gridDim.x + blockIdx.x;
   if (c >= parts) return;
-  const int r0 = line.part_begin(parts, c), r1 = line.part_begin(parts, c + 1);
+  const int edge = line.part_begin(parts, c + (lane & 1));  // both at once
+  const int r0 = __shfl_sync(0xffffffffu, edge, 0), r1 = __shfl_sync(0xffffffffu, edge, 1);
   if (r0 == r1) return;
 
+  // K and V are read once: with weights they make way in L2 for the logits, which
+  // the join reads again
+  unsigned long long policy;
+  if (p.weight) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
   // Lane i holds the pool row of group (batch of 32) + i of this part.
   const int mine = r1 - r0;
   int rows = -1, issued = 0, landed = 0;
@@ -426,8 +433,8 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
       const uint32_t bar = bars + 8 * st, dst = ring + st * P::STAGE;
       if (row >= 0) {
         mbar_arrive_expect_tx(bar, P::STAGE);
-        tma_rows(dst, &kmap, row, bar);
-        tma_rows(dst + P::ROWS, &vmap, row, bar);
+        tma_rows(dst, &kmap, row, bar, policy);
+        tma_rows(dst + P::ROWS, &vmap, row, bar, policy);
       } else {
         mbar_arrive(bar);
       }
@@ -518,14 +525,35 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
 // --------------------------------------------------------------- join
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
-// Tasks: a slice of the output of a unit that was cut, block by block; a task
-// goes by its unit, or, where there are more units than parts, by the part the
-// unit begins in.  A slice is 128 floats, a record's to a warp; 32, four
-// records' to a warp, where units are few and so cut into many parts.  With
-// weights, each block then adds what its share of the line's tokens gets.
+// log2 of head g's softmax denominator over the parts c0 .. c1 of a unit; a whole warp.
+__device__ float joined_lse(const PagedAttendParams& p, int R, int GD, int g, int c0, int c1) {
+  float M = -INFINITY, L = 0.f;
+  for (int k = c0 + (threadIdx.x & 31); k <= c1; k += 32) {
+    const float* r = p.records + (size_t)(2 * k + (k == c0)) * R + GD + g;
+    const float m = __ldcg(r), l = __ldcg(r + p.G), X = fmaxf(M, m), Xs = finite_or_0(X);
+    L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
+    M = X;
+  }
+#pragma unroll
+  for (int s = 16; s; s >>= 1) {
+    const float m = __shfl_xor_sync(0xffffffffu, M, s), l = __shfl_xor_sync(0xffffffffu, L, s);
+    const float X = fmaxf(M, m), Xs = finite_or_0(X);
+    L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
+    M = X;
+  }
+  return L > 0.f ? M + log2f(L) : INFINITY;
+}
+
+// Tasks: a slice of the output of a unit that was cut; a task goes by its unit,
+// or, where there are more units than parts, by the part the unit begins in.
+// Rows of lanes take the unit's records in turn, a lane four floats of each,
+// then the rows' sums meet in order.  Where tasks are many a warp takes one (128
+// floats, its own row); where they are few, and so a unit's parts many, a block
+// does, with its warps as rows, or four rows of 8 lanes to a warp (32 floats).
+// With weights, each block then adds what its share of the line's tokens gets.
 // WEIGHTS: without, a block is small enough to wait beside the first kernel's.
 template <int D, bool WEIGHTS>
-__global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
+__global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 4 : 8)
     paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
   constexpr int NT = WEIGHTS ? 256 : 128, NW = NT / 32;
   extern __shared__ unsigned words[];
@@ -538,18 +566,20 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
   make_line<NT>(p, words, scan, false);
   const PagedLine line{words, p.B, p.Hkv};
   const int parts = line.parts(p.parts), total = line.total();
-  const int units = p.B * p.Hkv;
+  const int units = p.B * p.Hkv, blocks = gridDim.x;
   const bool by_unit = units <= parts;
-  const bool fine = by_unit && (long long)units * G * (D / 32) <= gridDim.x;
+  const int most = (by_unit ? units : max(parts - 1, 0)) * ((G * D + 127) / 128);
+  const bool team = most < 2 * blocks, fine = team && by_unit && units * (G * D / 32) <= blocks;
   const int lanes = fine ? 8 : 32, width = 4 * lanes, slices = (G * D + width - 1) / width;
   const int tasks = (by_unit ? units : max(parts - 1, 0)) * slices;
+  const int nrows = team ? NT / lanes : 1, row = team ? tid / lanes : 0, at = tid & (lanes - 1);
   // The unit of a task and its parts; false when it was not cut, or does not begin there.
   PagedSegments sg;
   int c0 = 0, c1 = 0;
   auto task_at = [&](int task) {
-    const int at = task / slices;
+    const int of = task / slices;
     if (by_unit) {
-      const int b = at / p.Hkv, h = at - b * p.Hkv, n = line.groups(b);
+      const int b = of / p.Hkv, h = of - b * p.Hkv, n = line.groups(b);
       if (n == 0) return false;
       sg.line = line;
       sg.end = total;
@@ -558,7 +588,7 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
       sg.x = line.before(b) * p.Hkv + h * n;
       sg.at();
     } else {
-      const int edge = line.part_begin(parts, at + 1);
+      const int edge = line.part_begin(parts, of + 1);
       if (edge <= 0 || edge >= total) return false;
       sg.start(line, edge - 1, edge);
       sg.at();
@@ -566,16 +596,15 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
     }
     c0 = sg.first_part(parts);
     c1 = sg.last_part(parts);
-    return by_unit ? c0 < c1 : c0 == at;
+    return by_unit ? c0 < c1 : c0 == of;
   };
-  int task = blockIdx.x;
+  const int step = team ? blocks : blocks * NW;
+  int task = team ? blockIdx.x : warp * blocks + blockIdx.x;
   bool cut_here = task < tasks && task_at(task);
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  for (; task < tasks; task += gridDim.x, cut_here = task < tasks && task_at(task)) {
+  for (; task < tasks; task += step, cut_here = task < tasks && task_at(task)) {
     if (!cut_here) continue;
-    // rows of `lanes` lanes take every rows-th part, a lane four floats of it,
-    // then the rows' sums meet, in order
-    const int n = c1 - c0 + 1, nrows = NT / lanes, row = tid / lanes, at = tid - row * lanes;
+    const int n = c1 - c0 + 1;
     const int i0 = (task % slices) * width + 4 * at, i = min(i0, G * D - 4), g = i / D;
     const float* first = p.records + (size_t)(2 * c0 + 1) * R;
     const float* rest = p.records + (size_t)(2 * c0) * R;
@@ -607,68 +636,62 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
         a = make_float4(a.x + o[u].x * e, a.y + o[u].y * e, a.z + o[u].z * e, a.w + o[u].w * e);
       }
     }
-    __syncthreads();  // the last task's sums are read
-    so[tid] = a;
-    sml[tid] = make_float2(M, L);
-    __syncthreads();
-    if (row == 0 && i0 < G * D) {
-      float X = -INFINITY;
-      for (int w = 0; w < nrows; ++w) X = fmaxf(X, sml[w * lanes + at].x);
-      const float Xs = finite_or_0(X);
-      L = 0.f;
-      a = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (team) {
+      __syncthreads();  // the last task's sums are read
+      so[tid] = a;
+      sml[tid] = make_float2(M, L);
+      __syncthreads();
+      if (row == 0) {
+        float X = -INFINITY;
+        for (int w = 0; w < nrows; ++w) X = fmaxf(X, sml[w * lanes + at].x);
+        const float Xs = finite_or_0(X);
+        L = 0.f;
+        a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-      for (int w = 0; w < nrows; ++w) {
-        const float2 s = sml[w * lanes + at];
-        const float e = exp2f(s.x - Xs);
-        const float4 o = so[w * lanes + at];
-        L += s.y * e;
-        a = make_float4(a.x + o.x * e, a.y + o.y * e, a.z + o.z * e, a.w + o.w * e);
+        for (int w = 0; w < nrows; ++w) {
+          const float2 s = sml[w * lanes + at];
+          const float e = exp2f(s.x - Xs);
+          const float4 o = so[w * lanes + at];
+          L += s.y * e;
+          a = make_float4(a.x + o.x * e, a.y + o.y * e, a.z + o.z * e, a.w + o.w * e);
+        }
       }
+    }
+    if (row == 0 && i0 < G * D) {
       const float inv = L > 0.f ? 1.f / L : 0.f;
       *reinterpret_cast<float4*>(p.out + (size_t)sg.unit() * G * D + i) =
           make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     }
   }
   if constexpr (!WEIGHTS) return;
-  sg.start(line, cut(total, gridDim.x, blockIdx.x), cut(total, gridDim.x, blockIdx.x + 1));
+  static_assert(!WEIGHTS || NW >= G_MAX, "a warp for each head");
+  sg.start(line, cut(total, blocks, blockIdx.x), cut(total, blocks, blockIdx.x + 1));
   for (; sg.at(); sg.next()) {
     const int unit = sg.unit();
     c0 = sg.first_part(parts);
     c1 = sg.last_part(parts);
-    __syncthreads();
-    if (c0 == c1) {
-      if (tid < G) lse[tid] = __ldcg(p.lse + (size_t)unit * G + tid);
-    } else if (warp < G) {  // warp g: the parts' (m, l) of head g
-      static_assert(!WEIGHTS || NW >= G_MAX, "a warp for each head");
-      float M = -INFINITY, L = 0.f;
-      for (int k = c0 + lane; k <= c1; k += 32) {
-        const float* r = p.records + (size_t)(2 * k + (k == c0)) * R + G * D + warp;
-        const float m = __ldcg(r), l = __ldcg(r + G), X = fmaxf(M, m), Xs = finite_or_0(X);
-        L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
-        M = X;
-      }
-#pragma unroll
-      for (int s = 16; s; s >>= 1) {
-        const float m = __shfl_xor_sync(0xffffffffu, M, s), l = __shfl_xor_sync(0xffffffffu, L, s);
-        const float X = fmaxf(M, m), Xs = finite_or_0(X);
-        L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
-        M = X;
-      }
-      if (lane == 0) lse[warp] = L > 0.f ? M + log2f(L) : INFINITY;
-    }
-    __syncthreads();
     // four tokens a thread: a group's slots, and so its logits and weights, are
-    // all there (those behind the end are -inf and get nothing)
+    // all there (those behind the end are -inf and get nothing); the first are
+    // under way while the parts' sums are joined
     const int t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP, tokens = line.tokens(sg.b);
     const float* z = p.logits + (size_t)unit * G * p.T_cap;
-    for (int t = (sg.x - sg.unit_begin) * PAGED_GROUP + 4 * tid; t < t1; t += 4 * NT) {
-      float4* at = reinterpret_cast<float4*>(p.weight + (size_t)unit * p.T_cap + t);
-      float4 zg[G_MAX];
+    float* weight = p.weight + (size_t)unit * p.T_cap;
+    float4 zg[G_MAX], old;
+    auto load = [&](int t) {
 #pragma unroll
       for (int g = 0; g < G_MAX; ++g)
         if (g < G) zg[g] = __ldcg(reinterpret_cast<const float4*>(z + (size_t)g * p.T_cap + t));
-      const float4 old = *at;
+      old = *reinterpret_cast<const float4*>(weight + t);
+    };
+    int t = (sg.x - sg.unit_begin) * PAGED_GROUP + 4 * tid;
+    if (t < t1) load(t);
+    __syncthreads();  // the last unit's sums are read
+    if (warp < G) {
+      const float e = c0 == c1 ? __ldcg(p.lse + (size_t)unit * G + warp) : joined_lse(p, R, G * D, warp, c0, c1);
+      if (lane == 0) lse[warp] = e;
+    }
+    __syncthreads();
+    while (t < t1) {
       float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int g = 0; g < G_MAX; ++g)
@@ -681,13 +704,14 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 3 : 8)
         }
       const int live = tokens - t;  // slots behind the end keep what they hold
       if (live >= 4) {
-        *at = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+        *reinterpret_cast<float4*>(weight + t) = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
       } else {
-        float* f = reinterpret_cast<float*>(at);
-        if (live > 0) f[0] = old.x + w.x;
-        if (live > 1) f[1] = old.y + w.y;
-        if (live > 2) f[2] = old.z + w.z;
+        if (live > 0) weight[t] = old.x + w.x;
+        if (live > 1) weight[t + 1] = old.y + w.y;
+        if (live > 2) weight[t + 2] = old.z + w.z;
       }
+      t += 4 * NT;
+      if (t < t1) load(t);
     }
   }
 }
@@ -744,7 +768,7 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.weight ? 2 * sms : sms);
+  cfg.gridDim = dim3(p.weight ? 4 * sms : sms);
   cfg.blockDim = dim3(p.weight ? 256 : 128);
   cfg.dynamicSmemBytes = (p.B + 1) * 4;
   cfg.stream = s;
