@@ -33,8 +33,7 @@
 namespace fasa {
 namespace {
 
-constexpr int AT_NW = 4;  // warps of a CTA
-constexpr int AT_NT = AT_NW * 32;
+constexpr int JN_NT = 256;  // threads of a join block
 
 // The line's words, in shared memory.  Every thread of the block calls it; ends
 // with a barrier.  scan: NT / 32 words.
@@ -84,6 +83,11 @@ template <int D>
 struct MathBf16 {
   using T = __nv_bfloat16;
   static constexpr int CTAS = 2;  // per SM
+  // Warps of a CTA.  Two with six stages each read 128 dims at 99% of the copy
+  // rate (352.8 us for 2.38 GB) and leave half the records to join that four with
+  // three do (359.9 us); a group of 64 dims is half the bytes for the same
+  // latency and wants the four (64 short sequences: 20.0 us against 25.5).
+  static constexpr int WARPS = D == 128 ? 2 : 4;
   static constexpr int RAW = G_MAX * D * 2;  // the next unit's raw query, fetched while this one is read
   static constexpr int MT = D / 16;
   static constexpr int SCRATCH = 0;  // shared memory of a warp
@@ -206,6 +210,7 @@ template <int D, int GP>
 struct MathF32 {
   using T = float;
   static constexpr int CTAS = 1;
+  static constexpr int WARPS = 4;
   static constexpr int RAW = 0;  // (no room to fetch ahead: the raw query goes where the turned one stays)
   static constexpr int E = D / 32;
   static constexpr int SCRATCH = (GP * D + PAGED_GROUP * GP) * 4;  // the query, a group's weights
@@ -341,15 +346,15 @@ struct Plan {
   static constexpr int SLABS = D * ES / 128;              // 128-byte columns of a row
   static constexpr int ROWS = SLABS * PAGED_GROUP * 128;  // K or V of a group
   static constexpr int STAGE = 2 * ROWS;
-  static constexpr int STAGES = 196608 / M::CTAS / (AT_NW * STAGE);
-  static constexpr int OFF_RAW = AT_NW * STAGES * STAGE;
-  static constexpr int OFF_CS = OFF_RAW + AT_NW * M::RAW;
-  static constexpr int OFF_TURNS = OFF_CS + AT_NW * D / 2 * 8;
+  static constexpr int STAGES = 196608 / M::CTAS / (M::WARPS * STAGE);
+  static constexpr int OFF_RAW = M::WARPS * STAGES * STAGE;
+  static constexpr int OFF_CS = OFF_RAW + M::WARPS * M::RAW;
+  static constexpr int OFF_TURNS = OFF_CS + M::WARPS * D / 2 * 8;
   static constexpr int OFF_SCRATCH = OFF_TURNS + D / 2 * 8;
-  static constexpr int OFF_BAR = OFF_SCRATCH + AT_NW * M::SCRATCH;
-  static constexpr int OFF_HELD = OFF_BAR + AT_NW * STAGES * 8;  // whether a stage's page is in the pool
-  static constexpr int OFF_SCAN = OFF_HELD + AT_NW * STAGES * 4;
-  static constexpr int OFF_LINE = OFF_SCAN + AT_NW * 4;
+  static constexpr int OFF_BAR = OFF_SCRATCH + M::WARPS * M::SCRATCH;
+  static constexpr int OFF_HELD = OFF_BAR + M::WARPS * STAGES * 8;  // whether a stage's page is in the pool
+  static constexpr int OFF_SCAN = OFF_HELD + M::WARPS * STAGES * 4;
+  static constexpr int OFF_LINE = OFF_SCAN + M::WARPS * 4;
   static constexpr int bytes(int B) { return 1024 + OFF_LINE + (B + 1) * 4; }
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits one CTA");
 };
@@ -364,7 +369,7 @@ __device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, i
 }
 
 template <int D, class M>
-__global__ void __launch_bounds__(AT_NT, M::CTAS)
+__global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
     paged_attend_kernel(const __grid_constant__ PagedAttendParams p, const __grid_constant__ CUtensorMap kmap,
                         const __grid_constant__ CUtensorMap vmap) {
   using P = Plan<D, M>;
@@ -388,13 +393,13 @@ __global__ void __launch_bounds__(AT_NT, M::CTAS)
     fence_mbar_init();
   }
   // (lanes reading different parameter words take turns: a few lanes of each warp)
-  constexpr int TW = D / 2 / AT_NW;
+  constexpr int TW = D / 2 / M::WARPS;
   if (lane < TW) turns[warp * TW + lane] = p.rope_turns[warp * TW + lane];
-  make_line<AT_NT>(p, words, reinterpret_cast<int*>(sm + P::OFF_SCAN), blockIdx.x == 0);
+  make_line<32 * M::WARPS>(p, words, reinterpret_cast<int*>(sm + P::OFF_SCAN), blockIdx.x == 0);
   const PagedLine line{words, p.B, p.Hkv};
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)  // sequences without a token: zeros
     if (line.groups(b) == 0)
-      for (int i = tid; i < p.Hq * D; i += AT_NT) p.out[(size_t)b * p.Hq * D + i] = 0.f;
+      for (int i = tid; i < p.Hq * D; i += 32 * M::WARPS) p.out[(size_t)b * p.Hq * D + i] = 0.f;
   // few parts lie on as many SMs
   const int parts = line.parts(p.parts), c = warp * gridDim.x + blockIdx.x;
   if (c >= parts) return;
@@ -551,11 +556,11 @@ __device__ float joined_lse(const PagedAttendParams& p, int R, int GD, int g, in
 // floats, its own row); where they are few, and so a unit's parts many, a block
 // does, with its warps as rows, or four rows of 8 lanes to a warp (32 floats).
 // With weights, each block then adds what its share of the line's tokens gets.
-// WEIGHTS: without, a block is small enough to wait beside the first kernel's.
+// A block is small enough to wait for the first kernel beside its CTAs.
 template <int D, bool WEIGHTS>
-__global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 4 : 8)
+__global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
     paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
-  constexpr int NT = WEIGHTS ? 256 : 128, NW = NT / 32;
+  constexpr int NT = JN_NT, NW = NT / 32;
   extern __shared__ unsigned words[];
   __shared__ float4 so[NT];
   __shared__ float2 sml[NT];
@@ -637,21 +642,34 @@ __global__ void __launch_bounds__(WEIGHTS ? 256 : 128, WEIGHTS ? 4 : 8)
       }
     }
     if (team) {
+      for (int s = lanes; s < 32; s <<= 1) {  // the rows of a warp
+        const float m = __shfl_xor_sync(0xffffffffu, M, s), X = fmaxf(M, m), Xs = finite_or_0(X);
+        const float e = exp2f(M - Xs);
+        M = X;
+        L *= e;
+        a = make_float4(a.x * e, a.y * e, a.z * e, a.w * e);
+        L += __shfl_xor_sync(0xffffffffu, L, s);
+        a.x += __shfl_xor_sync(0xffffffffu, a.x, s);
+        a.y += __shfl_xor_sync(0xffffffffu, a.y, s);
+        a.z += __shfl_xor_sync(0xffffffffu, a.z, s);
+        a.w += __shfl_xor_sync(0xffffffffu, a.w, s);
+      }
       __syncthreads();  // the last task's sums are read
       so[tid] = a;
       sml[tid] = make_float2(M, L);
       __syncthreads();
       if (row == 0) {
         float X = -INFINITY;
-        for (int w = 0; w < nrows; ++w) X = fmaxf(X, sml[w * lanes + at].x);
+#pragma unroll
+        for (int w = 0; w < NW; ++w) X = fmaxf(X, sml[w * 32 + lane].x);
         const float Xs = finite_or_0(X);
         L = 0.f;
         a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-        for (int w = 0; w < nrows; ++w) {
-          const float2 s = sml[w * lanes + at];
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+          const float2 s = sml[w * 32 + lane];
           const float e = exp2f(s.x - Xs);
-          const float4 o = so[w * lanes + at];
+          const float4 o = so[w * 32 + lane];
           L += s.y * e;
           a = make_float4(a.x + o.x * e, a.y + o.y * e, a.z + o.z * e, a.w + o.w * e);
         }
@@ -757,11 +775,11 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   // as many parts as warps are resident at once: M::CTAS CTAs to an SM while the
   // lengths of the batch leave them the room (228 KB, 1 KB of it each CTA's system's)
   const int ctas = M::CTAS * (smem + 1024) <= 233472 ? M::CTAS : 1;
-  const int grid = min(ctas * sms, PAGED_MAX_PARTS / AT_NW);
-  p.parts = grid * AT_NW;
+  const int grid = min(ctas * sms, PAGED_MAX_PARTS / M::WARPS);
+  p.parts = grid * M::WARPS;
   e = cudaFuncSetAttribute(paged_attend_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   if (e != cudaSuccess) return e;
-  paged_attend_kernel<D, M><<<grid, AT_NT, smem, s>>>(p, km, vm);
+  paged_attend_kernel<D, M><<<grid, 32 * M::WARPS, smem, s>>>(p, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   cudaLaunchAttribute attr;
@@ -769,7 +787,7 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   attr.val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.weight ? 4 * sms : sms);
-  cfg.blockDim = dim3(p.weight ? 256 : 128);
+  cfg.blockDim = dim3(JN_NT);
   cfg.dynamicSmemBytes = (p.B + 1) * 4;
   cfg.stream = s;
   cfg.attrs = &attr;
