@@ -50,7 +50,7 @@ struct PagedAttendParams : PagedCommon {
   float scale;    // log2(e) / sqrt(d): logits are kept in powers of two
   float* records; // [parts][2][G * (d + 2)]: o [G][d], then m [G], l [G]
   float* lse;     // [units][G] of the units one part holds whole
-  float* logits;  // [units][G][T_cap]
+  float* logits;  // [units][T_cap / 16][G][16]
   int parts;      // most parts of this launch
   unsigned long long wait_ns;  // bound of every device wait
 };

@@ -23,6 +23,7 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
 #include <mutex>
 
 #include "fasa_cluster.cuh"
@@ -120,8 +121,8 @@ struct MathBf16 {
 #pragma unroll
     for (int i = 0; i < 4 * MT; ++i) o[i >> 2][i & 3] *= (i & 1) ? a1 : a0;
   }
-  // One group: K at kb, V at vb, its first n tokens count; logits [G][stride] at the group, or null.
-  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, float*) {
+  // One group: K at kb, V at vb, its first n tokens count; the group's logits [G][16], or null.
+  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int G, float*) {
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     // ldmatrix: this lane's row of the group and 16-byte chunk of a 16-column slab
     const int lrow = (lane & 7) + ((lane >> 4) << 3), lch = (lane >> 3) & 1;
@@ -146,7 +147,7 @@ struct MathBf16 {
       if (2 * t + (i & 1) + 8 * (i >> 1) >= n) z[i] = -INFINITY;
     }
     if (logits && g < G) {
-      float* at = logits + (size_t)g * stride + 2 * t;
+      float* at = logits + g * PAGED_GROUP + 2 * t;
       *reinterpret_cast<float2*>(at) = make_float2(z[0], z[1]);
       *reinterpret_cast<float2*>(at + 8) = make_float2(z[2], z[3]);
     }
@@ -234,7 +235,7 @@ struct MathF32 {
       for (int e = 0; e < E; ++e) o[g][e] = 0.f;
     }
   }
-  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int stride, int G, float* scratch) {
+  __device__ void step(uint32_t kb, uint32_t vb, int n, float* logits, int G, float* scratch) {
     const int lane = threadIdx.x & 31, tok = lane & 15, half = lane >> 4;
     const float4* qs = reinterpret_cast<const float4*>(scratch) + half * (D / 8);
     float* ps = scratch + GP * D;
@@ -261,7 +262,7 @@ struct MathF32 {
     for (int g = 0; g < GP; ++g) {
       z[g] += __shfl_xor_sync(0xffffffffu, z[g], 16);
       if (tok >= n) z[g] = -INFINITY;
-      if (logits && g < G && half == 0) logits[(size_t)g * stride + tok] = z[g];
+      if (logits && g < G && half == 0) logits[g * PAGED_GROUP + tok] = z[g];
       mx[g] = z[g];
 #pragma unroll
       for (int s = 1; s < 16; s <<= 1) mx[g] = fmaxf(mx[g], __shfl_xor_sync(0xffffffffu, mx[g], s));
@@ -407,11 +408,15 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
   const int r0 = __shfl_sync(0xffffffffu, edge, 0), r1 = __shfl_sync(0xffffffffu, edge, 1);
   if (r0 == r1) return;
 
-  // K and V are read once: with weights they make way in L2 for the logits, which
-  // the join reads again
+  // K and V are read once: they make way in L2 for what the join reads again (32K
+  // tokens 28.4 us without, 26.5 with; one token of eight 4K caches 56.0 and 49.2);
+  // a stream of many times L2 with no logits runs 2% faster as it comes (2.38 GB:
+  // 356.5 us against 364.2)
   unsigned long long policy;
-  if (p.weight) asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
-  else asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
+  if (p.weight || (long long)line.total() * P::STAGE < (512ll << 20))
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
+  else
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
   // Lane i holds the pool row of group (batch of 32) + i of this part.
   const int mine = r1 - r0;
   int rows = -1, issued = 0, landed = 0;
@@ -504,7 +509,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
         fence_proxy_async();
         __syncwarp();
       }
-      mt.step(kb, vb, n, logits ? logits + t0 : nullptr, p.T_cap, G, scratch);
+      mt.step(kb, vb, n, logits ? logits + (size_t)t0 * G : nullptr, G, scratch);
       __syncwarp();
       issue();
     }
@@ -698,7 +703,10 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
     auto load = [&](int t) {
 #pragma unroll
       for (int g = 0; g < G_MAX; ++g)
-        if (g < G) zg[g] = __ldcg(reinterpret_cast<const float4*>(z + (size_t)g * p.T_cap + t));
+        if (g < G) {
+          const float* zt = z + (size_t)(t & -PAGED_GROUP) * G + g * PAGED_GROUP + (t & (PAGED_GROUP - 1));
+          zg[g] = __ldcg(reinterpret_cast<const float4*>(zt));
+        }
       old = *reinterpret_cast<const float4*>(weight + t);
     };
     int t = (sg.x - sg.unit_begin) * PAGED_GROUP + 4 * tid;
@@ -764,6 +772,21 @@ cudaError_t pool_map(CUtensorMap* map, const void* pool, long long rows, int D, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// The kernel's shared memory, for the largest batch, once a device.
+template <int D, class M>
+cudaError_t allow_shared() {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(paged_attend_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           Plan<D, M>::bytes(PAGED_MAX_BATCH));
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+  return e;
+}
+
 template <int D, class M>
 cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   CUtensorMap km, vm;
@@ -777,7 +800,7 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   const int ctas = M::CTAS * (smem + 1024) <= 233472 ? M::CTAS : 1;
   const int grid = min(ctas * sms, PAGED_MAX_PARTS / M::WARPS);
   p.parts = grid * M::WARPS;
-  e = cudaFuncSetAttribute(paged_attend_kernel<D, M>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  e = allow_shared<D, M>();
   if (e != cudaSuccess) return e;
   paged_attend_kernel<D, M><<<grid, 32 * M::WARPS, smem, s>>>(p, km, vm);
   e = cudaGetLastError();
@@ -802,8 +825,8 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
 cudaError_t launch_paged_attend(const PagedAttendParams& p0, int head_dim, bool bf16, int sms, cudaStream_t s) {
   PagedAttendParams p = p0;
   if (bf16) return head_dim == 128 ? launch<128, MathBf16<128>>(p, sms, s) : launch<64, MathBf16<64>>(p, sms, s);
-  if (p.G <= 4) return head_dim == 128 ? launch<128, MathF32<128, 4>>(p, sms, s) : launch<64, MathF32<64, 4>>(p, sms, s);
-  return head_dim == 128 ? launch<128, MathF32<128, 8>>(p, sms, s) : launch<64, MathF32<64, 8>>(p, sms, s);
+  if (head_dim == 128) return p.G <= 4 ? launch<128, MathF32<128, 4>>(p, sms, s) : launch<128, MathF32<128, 8>>(p, sms, s);
+  return p.G <= 4 ? launch<64, MathF32<64, 4>>(p, sms, s) : launch<64, MathF32<64, 8>>(p, sms, s);
 }
 
 }  // namespace fasa

@@ -386,29 +386,61 @@ def fasa_decode_step_noalloc(q, pos, k_cache, v_cache, k_dom, dom_fc, seq_lens, 
 
 
 # ---------------------------------------------------------------- paged cache
-def _paged_ptrs(dims, tensors):
-    """Device pointers of a paged call's tensors, each given as (name, tensor
-    or None, element type: "s" storage, "i" int32, "f" fp32, None any; number
-    of elements, None any).  All lie on the current device."""
-    import torch
-    types = {"s": torch.float32 if dims.dtype == FASA_F32 else torch.bfloat16, "i": torch.int32,
-             "f": torch.float32}
-    here = torch.cuda.current_device()
-    ptrs = []
-    for name, x, kind, count in tensors:
-        if x is None:
-            ptrs.append(None)
-            continue
-        if not x.is_cuda or x.get_device() != here:
-            raise ValueError(f"{name} must be a tensor on the current CUDA device")
-        if not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if kind is not None and x.dtype is not types[kind]:
-            raise ValueError(f"{name} has dtype {x.dtype}, expected {types[kind]}")
-        if count is not None and x.numel() != count:
-            raise ValueError(f"{name} has {x.numel()} elements, expected {count}")
-        ptrs.append(x.data_ptr())
-    return ptrs
+# (a small call's time is the host's: each tensor is checked in one expression,
+# and what torch gives for every call is looked up once)
+_torch = None
+
+
+def _here() -> int:
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
+    return _torch.cuda.current_device()
+
+
+def _refuse(x, here, dtype, count, name):
+    if not isinstance(x, _torch.Tensor):
+        raise ValueError(f"{name} must be a tensor")
+    if not x.is_cuda or x.get_device() != here:
+        raise ValueError(f"{name} must be a tensor on the current CUDA device")
+    if x.dtype is not dtype:
+        raise ValueError(f"{name} has dtype {x.dtype}, expected {dtype}")
+    if x.numel() != count:
+        raise ValueError(f"{name} has {x.numel()} elements, expected {count}")
+    raise ValueError(f"{name} must be contiguous")
+
+
+def _at(x, here, dtype, count, name):
+    """Device address of a contiguous tensor of `count` elements on device `here`."""
+    try:
+        if x.dtype is dtype and x.numel() == count and x.get_device() == here and x.is_contiguous():
+            return x.data_ptr()
+    except AttributeError:
+        pass
+    _refuse(x, here, dtype, count, name)
+
+
+def _room(x, here):
+    """Address and bytes of a workspace."""
+    if x.get_device() != here or not x.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
+    return x.data_ptr(), x.numel() * x.element_size()
+
+
+def _on(stream, here):
+    if stream is None:
+        return _torch._C._cuda_getCurrentRawStream(here)
+    return _stream(stream)
+
+
+def _paged_sizes(dims):
+    """Current device, storage dtype, elements of a pool, of the statistics, of the page table."""
+    here = _here()
+    B, H = dims.batch, dims.n_kv_heads
+    slots = dims.max_pages * dims.page_size
+    return (here, _torch.float32 if dims.dtype == FASA_F32 else _torch.bfloat16,
+            dims.n_pages * H * dims.page_size * dims.head_dim, B * H * slots, B * dims.max_pages)
 
 
 def fasa_paged_append(k_new, v_new, pos, k_pages, v_pages, page_table, seq_lens, cu_new=None, weight=None,
@@ -417,16 +449,19 @@ def fasa_paged_append(k_new, v_new, pos, k_pages, v_pages, page_table, seq_lens,
     and v_new [n_tokens, Hkv, d], those of sequence b at cu_new[b] ..
     cu_new[b+1], or one per sequence without cu_new; the first of b gets the
     position pos[b].  seq_lens is not advanced."""
-    B, row = dims.batch, dims.n_kv_heads * dims.head_dim
-    pool, slots = dims.n_pages * dims.page_size * row, B * dims.n_kv_heads * dims.max_pages * dims.page_size
+    here, store, pool, slots, entries = _paged_sizes(dims)
+    i32, f32, B = _torch.int32, _torch.float32, dims.batch
+    row = dims.n_kv_heads * dims.head_dim
     n_tokens = k_new.numel() // row
-    p = _paged_ptrs(dims, (
-        ("k_new", k_new, "s", n_tokens * row), ("v_new", v_new, "s", n_tokens * row), ("cu_new", cu_new, "i", B + 1),
-        ("pos", pos, "i", B), ("page_table", page_table, "i", B * dims.max_pages), ("seq_lens", seq_lens, "i", B),
-        ("k_pages", k_pages, "s", pool), ("v_pages", v_pages, "s", pool), ("weight", weight, "f", slots),
-        ("token_pos", token_pos, "i", slots)))
-    _check("fasa_paged_append", lib().fasa_paged_append(
-        p[0], p[1], n_tokens, p[2], p[3], p[4], p[5], p[6], p[7], p[8], p[9], ctypes.byref(dims), _stream(stream)))
+    st = lib().fasa_paged_append(
+        _at(k_new, here, store, n_tokens * row, "k_new"), _at(v_new, here, store, n_tokens * row, "v_new"), n_tokens,
+        None if cu_new is None else _at(cu_new, here, i32, B + 1, "cu_new"), _at(pos, here, i32, B, "pos"),
+        _at(page_table, here, i32, entries, "page_table"), _at(seq_lens, here, i32, B, "seq_lens"),
+        _at(k_pages, here, store, pool, "k_pages"), _at(v_pages, here, store, pool, "v_pages"),
+        None if weight is None else _at(weight, here, f32, slots, "weight"),
+        None if token_pos is None else _at(token_pos, here, i32, slots, "token_pos"), ctypes.byref(dims),
+        _on(stream, here))
+    _check("fasa_paged_append", st)
 
 
 def fasa_paged_workspace_size(dims: FasaPagedDims, weights: bool = False) -> int:
@@ -441,21 +476,20 @@ def fasa_paged_attention(q, pos, k_pages, v_pages, page_table, seq_lens, out, we
     """Attention of one new token per sequence over its cached tokens; with
     weight, each cached token's softmax weights are added to it.  Without a
     workspace one is allocated here."""
-    B = dims.batch
-    pool = dims.n_pages * dims.n_kv_heads * dims.page_size * dims.head_dim
+    here, store, pool, slots, entries = _paged_sizes(dims)
+    i32, f32, B = _torch.int32, _torch.float32, dims.batch
+    heads = B * dims.n_q_heads * dims.head_dim
     if workspace is None:
-        import torch
-        workspace = torch.empty(fasa_paged_workspace_size(dims, weight is not None), dtype=torch.uint8,
-                                device=out.device)
-    p = _paged_ptrs(dims, (
-        ("q", q, "s", B * dims.n_q_heads * dims.head_dim), ("pos", pos, "i", B), ("k_pages", k_pages, "s", pool),
-        ("v_pages", v_pages, "s", pool), ("page_table", page_table, "i", B * dims.max_pages),
-        ("seq_lens", seq_lens, "i", B), ("out", out, "f", B * dims.n_q_heads * dims.head_dim),
-        ("weight", weight, "f", B * dims.n_kv_heads * dims.max_pages * dims.page_size),
-        ("workspace", workspace, None, None)))
-    _check("fasa_paged_attention", lib().fasa_paged_attention(
-        p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7], p[8], workspace.numel() * workspace.element_size(),
-        ctypes.byref(dims), _stream(stream)))
+        workspace = _torch.empty(fasa_paged_workspace_size(dims, weight is not None), dtype=_torch.uint8,
+                                 device=out.device)
+    ws, ws_bytes = _room(workspace, here)
+    st = lib().fasa_paged_attention(
+        _at(q, here, store, heads, "q"), _at(pos, here, i32, B, "pos"), _at(k_pages, here, store, pool, "k_pages"),
+        _at(v_pages, here, store, pool, "v_pages"), _at(page_table, here, i32, entries, "page_table"),
+        _at(seq_lens, here, i32, B, "seq_lens"), _at(out, here, f32, heads, "out"),
+        None if weight is None else _at(weight, here, f32, slots, "weight"), ws, ws_bytes, ctypes.byref(dims),
+        _on(stream, here))
+    _check("fasa_paged_attention", st)
 
 
 def fasa_paged_evict_workspace_size(dims: FasaPagedDims, keep: int) -> int:
@@ -474,23 +508,21 @@ def fasa_paged_evict(weight, token_pos, pos, k_pages, v_pages, page_table, seq_l
     new_lens [B] <- min(seq_lens, keep).  The statistics change in place, or
     go to weight_out and token_pos_out.  Without a workspace one is allocated
     here."""
-    B = dims.batch
-    pool = dims.n_pages * dims.n_kv_heads * dims.page_size * dims.head_dim
-    slots = B * dims.n_kv_heads * dims.max_pages * dims.page_size
-    weight_out = weight if weight_out is None else weight_out
-    token_pos_out = token_pos if token_pos_out is None else token_pos_out
+    here, store, pool, slots, entries = _paged_sizes(dims)
+    i32, f32, B = _torch.int32, _torch.float32, dims.batch
     if workspace is None:
-        import torch
-        workspace = torch.empty(fasa_paged_evict_workspace_size(dims, keep), dtype=torch.uint8, device=weight.device)
-    p = _paged_ptrs(dims, (
-        ("weight", weight, "f", slots), ("token_pos", token_pos, "i", slots), ("pos", pos, "i", B),
-        ("page_table", page_table, "i", B * dims.max_pages), ("seq_lens", seq_lens, "i", B),
-        ("k_pages", k_pages, "s", pool), ("v_pages", v_pages, "s", pool), ("weight_out", weight_out, "f", slots),
-        ("token_pos_out", token_pos_out, "i", slots), ("new_lens", new_lens, "i", B),
-        ("workspace", workspace, None, None)))
-    _check("fasa_paged_evict", lib().fasa_paged_evict(
-        p[0], p[1], p[2], p[3], p[4], int(keep), int(sinks), int(recent), p[5], p[6], p[7], p[8], p[9], p[10],
-        workspace.numel() * workspace.element_size(), ctypes.byref(dims), _stream(stream)))
+        workspace = _torch.empty(fasa_paged_evict_workspace_size(dims, keep), dtype=_torch.uint8,
+                                 device=weight.device)
+    ws, ws_bytes = _room(workspace, here)
+    w, t = _at(weight, here, f32, slots, "weight"), _at(token_pos, here, i32, slots, "token_pos")
+    st = lib().fasa_paged_evict(
+        w, t, _at(pos, here, i32, B, "pos"), _at(page_table, here, i32, entries, "page_table"),
+        _at(seq_lens, here, i32, B, "seq_lens"), int(keep), int(sinks), int(recent),
+        _at(k_pages, here, store, pool, "k_pages"), _at(v_pages, here, store, pool, "v_pages"),
+        w if weight_out is None else _at(weight_out, here, f32, slots, "weight_out"),
+        t if token_pos_out is None else _at(token_pos_out, here, i32, slots, "token_pos_out"),
+        _at(new_lens, here, i32, B, "new_lens"), ws, ws_bytes, ctypes.byref(dims), _on(stream, here))
+    _check("fasa_paged_evict", st)
 
 
 def fasa_device_status(stream=None) -> int:
