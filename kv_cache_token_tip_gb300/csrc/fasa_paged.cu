@@ -208,7 +208,7 @@ int fasa_paged_evict(const float* weight, const int32_t* token_pos, const int32_
   p.moves = static_cast<int2*>(workspace);
   p.move_cap = most_moves(dims, keep);
   p.row_bytes = dims->head_dim * (dims->dtype == FASA_F32 ? 4 : 2);
-  const cudaError_t e = launch_paged_evict(p, reinterpret_cast<cudaStream_t>(stream));
+  const cudaError_t e = launch_paged_evict(p, sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FASA_OK : report_cuda(e);
 }
 

@@ -76,6 +76,6 @@ void paged_attend_layout(PagedAttendParams& p, int units, int D, void* ws);
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, int head_dim, bool bf16, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedAttendParams& p, int head_dim, bool bf16, int sms, cudaStream_t s);
-cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t s);
+cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t s);
 
 }  // namespace fasa

@@ -3,6 +3,8 @@
 #include <cuda_bf16.h>
 #include <stdint.h>
 
+#include <atomic>
+
 #include "fasa_cluster.cuh"
 #include "fasa_internal.h"
 #include "fasa_paged.h"
@@ -84,14 +86,39 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
 }
 
 // -------------------------------------------------------------------- evict
-constexpr int EV_NT = 1024;
+// One cluster per (sequence, KV head), each CTA a contiguous share of its slots
+// with their keys in shared memory.
+//   1. Keys: held tokens above every weight, NaN below every number, else the
+//      weight's order-preserving bits; the cluster's least and largest key and
+//      its count of held tokens.
+//   2. The keep-th largest key: a histogram of 2048 bins over the range of the
+//      keys, summed over the cluster slice by slice, gives the bin it falls in.
+//      A bin that is kept whole ends it; a bin of few keys is sent to every CTA
+//      and ranked there by (key, slot); else the bin becomes the range.  A single
+//      key held by many slots (ties) goes by slot order.
+//   3. Holes and movers, counted over the cluster, listed in slot order, and the
+//      i-th mover's row copied to the i-th hole by whichever threads come next.
+// Bound by the latency of these steps (cluster barriers, dependent loads), and
+// by the rows' copies where a long prompt is cut.
+constexpr int EV_NT = 512;
 constexpr int EV_NW = EV_NT / 32;
 constexpr int EV_BINS = 2048;
+constexpr int EV_CAND = 512;         // keys of a bin that are ranked one by one
+constexpr int EV_MAX_SHARE = 16384;  // slots of a CTA: 64 KB of keys
+constexpr int EV_SHORT_SHARE = 2048;
+constexpr int EV_C_MAX = 16;
 
-struct EvictScratch {
+struct EvictShared {
+  int hist[EV_BINS];
+  int slice[EV_BINS];        // this CTA's slice of the cluster's histogram
+  unsigned long long cand[EV_CAND];  // key, then ~slot: a larger entry comes first
+  int4 facts[EV_C_MAX];      // every CTA's least and largest key and held tokens
+  int slice_sum[EV_C_MAX];
+  int tie_sum[EV_C_MAX];
+  int2 sums[EV_C_MAX];       // every CTA's holes and movers
   int scan[EV_NW];
-  unsigned mn, mx;
-  int bin, above, cnt;
+  int4 red[EV_NW];
+  int bin, above, cnt, n_cand;
 };
 
 // What the selection orders by: held tokens above every weight, NaN below.
@@ -101,7 +128,7 @@ __device__ __forceinline__ unsigned evict_key(float w, int tp, int sinks, long l
 }
 
 // Exclusive prefix sum over the block (thread order) and the total.
-__device__ int block_scan(int x, EvictScratch* sc, int& total) {
+__device__ int block_scan(int x, int* scan, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = x;
 #pragma unroll
@@ -109,158 +136,283 @@ __device__ int block_scan(int x, EvictScratch* sc, int& total) {
     const int y = __shfl_up_sync(0xffffffffu, incl, o);
     if (lane >= o) incl += y;
   }
-  if (lane == 31) sc->scan[warp] = incl;
+  if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  if (warp == 0) {
-    int v = sc->scan[lane];
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, v, o);
-      if (lane >= o) v += y;
-    }
-    sc->scan[lane] = v;
-  }
+  const int v = lane < EV_NW ? scan[lane] : 0;
+  const int below = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
+  total = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
-  total = sc->scan[EV_NW - 1];
-  const int before = warp ? sc->scan[warp - 1] : 0;
-  __syncthreads();
-  return before + incl - x;
+  return below + incl - x;
 }
 
-// One block per (sequence, KV head).
 __global__ void __launch_bounds__(EV_NT) paged_evict_kernel(const __grid_constant__ PagedEvictParams p) {
-  __shared__ EvictScratch sc;
-  __shared__ int hist[EV_BINS];
+  extern __shared__ __align__(16) unsigned keys[];
+  __shared__ EvictShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int u = blockIdx.x, b = u / p.Hkv, h = u - b * p.Hkv;
+  const int C = (int)cluster_size(), rank = (int)cluster_rank();
+  const int u = blockIdx.x / C, b = u / p.Hkv, h = u - b * p.Hkv;
+  auto csync = [&]() {
+    if (C > 1) cluster_sync();
+    else __syncthreads();
+  };
   int len = p.seq_lens[b];
   if (len < 0 || len > p.T_cap) {
     if (tid == 0) atomicOr(p.status, 1);
     len = min(max(len, 0), p.T_cap);
   }
   const int keep = p.keep, left = min(len, keep);
-  if (h == 0 && tid == 0) p.new_lens[b] = left;
+  if (h == 0 && rank == 0 && tid == 0) p.new_lens[b] = left;
   const size_t base = (size_t)u * p.T_cap;
   const float* w = p.weight + base;
   const int* tp = p.token_pos + base;
   float* wo = p.weight_out + base;
   int* to = p.token_pos_out + base;
-  if (wo != w)  // into other buffers: the holes among these are written over below
-    for (int t = tid; t < left; t += EV_NT) {
-      wo[t] = w[t];
-      to[t] = tp[t];
-    }
-  if (len <= keep) return;
+  const bool apart = wo != w;
+  if (len <= keep && !apart) return;
+  if (C > 1 && len > keep) cluster_arrive_relaxed();  // (the cluster's CTAs have started before one writes to another)
+  // this CTA's slots: [first, first + n), whole groups of four but the last
+  const int share = ((len + C - 1) / C + 3) & ~3;
+  const int first = min(len, rank * share), n = min(len - first, share);
+  // 1. keys (T_cap is whole groups: a vector may pass len, its extra keys are unused)
   const long long after = (long long)p.pos[b] - p.recent;
-  auto key_at = [&](int t) { return evict_key(w[t], tp[t], p.sinks, after); };
-  // 1. the range of the keys
-  if (tid == 0) {
-    sc.mn = 0xffffffffu;
-    sc.mx = 0u;
-  }
-  __syncthreads();
   unsigned mn = 0xffffffffu, mx = 0u;
-  for (int t = tid; t < len; t += EV_NT) {
-    const unsigned k = key_at(t);
-    mn = min(mn, k);
-    mx = max(mx, k);
+  int held = 0;
+  for (int i = 4 * tid; i < n; i += 4 * EV_NT) {
+    const int t = first + i;
+    const float4 wv = *reinterpret_cast<const float4*>(w + t);
+    const int4 tv = *reinterpret_cast<const int4*>(tp + t);
+    if (apart) {  // into other buffers: the holes among these are written over below
+      if (t + 4 <= left) {
+        *reinterpret_cast<float4*>(wo + t) = wv;
+        *reinterpret_cast<int4*>(to + t) = tv;
+      } else {
+        const float we[4] = {wv.x, wv.y, wv.z, wv.w};
+        const int te[4] = {tv.x, tv.y, tv.z, tv.w};
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (t + e < left) {
+            wo[t + e] = we[e];
+            to[t + e] = te[e];
+          }
+      }
+    }
+    const unsigned k[4] = {evict_key(wv.x, tv.x, p.sinks, after), evict_key(wv.y, tv.y, p.sinks, after),
+                           evict_key(wv.z, tv.z, p.sinks, after), evict_key(wv.w, tv.w, p.sinks, after)};
+    *reinterpret_cast<uint4*>(keys + i) = make_uint4(k[0], k[1], k[2], k[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (i + e < n) {
+        if (k[e] == 0xffffffffu) {
+          ++held;
+        } else {
+          mn = min(mn, k[e]);
+          mx = max(mx, k[e]);
+        }
+      }
   }
+  if (len <= keep) return;
   mn = __reduce_min_sync(0xffffffffu, mn);
   mx = __reduce_max_sync(0xffffffffu, mx);
-  if (lane == 0) {
-    atomicMin(&sc.mn, mn);
-    atomicMax(&sc.mx, mx);
-  }
+  held = __reduce_add_sync(0xffffffffu, held);
+  if (lane == 0) sh.red[warp] = make_int4((int)mn, (int)mx, held, 0);
   __syncthreads();
-  // 2. the bin of the keep-th largest key, narrowed until it is kept whole or
-  // is a single key
-  unsigned lo = sc.mn, hi = sc.mx, tie_key = 0u;
-  unsigned long long from = 0ull;  // keys from here on are kept
-  int kr = keep, need = 0;         // and the first `need` slots of tie_key
-  while (true) {
+  if (C > 1) cluster_wait();
+  if (warp == 0) {  // to every CTA
+    const int4 r = lane < EV_NW ? sh.red[lane] : make_int4(-1, 0, 0, 0);
+    mn = __reduce_min_sync(0xffffffffu, (unsigned)r.x);
+    mx = __reduce_max_sync(0xffffffffu, (unsigned)r.y);
+    held = __reduce_add_sync(0xffffffffu, r.z);
+    if (lane < C) dsmem_st_v4u32(dsmem_map(smem_u32(&sh.facts[rank]), lane), make_uint4(mn, mx, (unsigned)held, 0u));
+  }
+  csync();
+  unsigned lo = 0xffffffffu, hi = 0u;
+  held = 0;
+  for (int r = 0; r < C; ++r) {
+    lo = min(lo, (unsigned)sh.facts[r].x);
+    hi = max(hi, (unsigned)sh.facts[r].y);
+    held += sh.facts[r].z;
+  }
+  // 2. kept: keys from `floor` on, and of tie_key the first `need` slots
+  unsigned long long floor = 1ull << 32;
+  unsigned tie_key = 0xffffffffu;
+  int need = 0, kr = keep - held;
+  if (kr < 0) {
+    need = keep;  // more held tokens than room
+  } else if (kr == 0) {
+    floor = 0xffffffffull;
+  }
+  const int SL = EV_BINS / C;
+  while (kr > 0) {
     const int shift = max(0, 32 - __clz(hi - lo) - 11);
-    for (int i = tid; i < EV_BINS; i += EV_NT) hist[i] = 0;
+    for (int i = tid; i < EV_BINS; i += EV_NT) sh.hist[i] = 0;
+    if (tid == 0) sh.n_cand = 0;
     __syncthreads();
-    for (int t = tid; t < len; t += EV_NT) {
-      const unsigned k = key_at(t);
-      if (k >= lo && k <= hi) atomicAdd(&hist[(k - lo) >> shift], 1);
+    for (int i = tid; i < n; i += EV_NT) {
+      const unsigned k = keys[i];
+      if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
+    }
+    csync();
+    // this CTA's slice of the bins, over the cluster
+    int sum = 0;
+    for (int i = tid; i < SL; i += EV_NT) {
+      int v = 0;
+      if (C == 1) {
+        v = sh.hist[i];
+      } else {
+        const uint32_t at = smem_u32(&sh.hist[rank * SL + i]);
+#pragma unroll 4
+        for (int r = 0; r < C; ++r) v += (int)dsmem_ld_u32(dsmem_map(at, r));
+      }
+      sh.slice[i] = v;
+      sum += v;
+    }
+    int total;
+    block_scan(sum, sh.scan, total);
+    if (tid < C) dsmem_st_u32(dsmem_map(smem_u32(&sh.slice_sum[rank]), tid), (uint32_t)total);
+    csync();
+    // the slice, then the bin of it, that holds the kr-th key from the top
+    int above = 0, owner = C - 1;
+    while (owner > 0 && above + sh.slice_sum[owner] < kr) above += sh.slice_sum[owner--];
+    const int per = max(1, SL / EV_NT);
+    int c[EV_BINS / EV_NT], mine = 0;
+#pragma unroll
+    for (int j = 0; j < EV_BINS / EV_NT; ++j) {
+      const int at = SL - 1 - (tid * per + j);
+      c[j] = j < per && at >= 0 ? (int)dsmem_ld_u32(dsmem_map(smem_u32(&sh.slice[max(at, 0)]), owner)) : 0;
+      mine += c[j];
+    }
+    above += block_scan(mine, sh.scan, total);
+#pragma unroll
+    for (int j = 0; j < EV_BINS / EV_NT; ++j) {
+      if (above < kr && kr <= above + c[j]) {
+        sh.bin = owner * SL + SL - 1 - (tid * per + j);
+        sh.above = above;
+        sh.cnt = c[j];
+      }
+      above += c[j];
     }
     __syncthreads();
-    // thread j: bins 2047 - 2j and the one below
-    const int hb = EV_BINS - 1 - 2 * tid;
-    const int c0 = hist[hb], c1 = hist[hb - 1];
-    int tot;
-    const int above = block_scan(c0 + c1, &sc, tot);
-    if (above < kr && kr <= above + c0 + c1) {
-      const bool first = kr <= above + c0;
-      sc.bin = first ? hb : hb - 1;
-      sc.above = first ? above : above + c0;
-      sc.cnt = first ? c0 : c1;
-    }
-    __syncthreads();
-    const int d = sc.bin, cnt = sc.cnt;
-    kr -= sc.above;
-    __syncthreads();
-    const unsigned b0 = lo + ((unsigned)d << shift);
-    if (cnt == kr) {
-      from = b0;
+    const int bin = sh.bin, cnt = sh.cnt;
+    kr -= sh.above;
+    const unsigned b0 = lo + ((unsigned)bin << shift);
+    const unsigned b1 = b0 + min(hi - b0, (1u << shift) - 1u);  // its last key
+    if (cnt == kr) {  // kept whole
+      floor = b0;
       break;
     }
-    if (shift == 0) {
+    if (cnt <= EV_CAND) {
+      // every CTA gets all keys of the bin, CTA after CTA, and marks its own as
+      // kept (largest key) or not (least)
+      int before = 0;
+      for (int r = 0; r < rank; ++r) before += (int)dsmem_ld_u32(dsmem_map(smem_u32(&sh.hist[bin]), r));
+      for (int i = tid; i < n; i += EV_NT) {
+        const unsigned k = keys[i];
+        if (k >= b0 && k <= b1) {
+          const int at = before + atomicAdd(&sh.n_cand, 1);
+          for (int r = 0; r < C; ++r)
+            dsmem_st_v2u32(dsmem_map(smem_u32(&sh.cand[at]), r), ~(unsigned)(first + i), k);
+        }
+      }
+      csync();
+      for (int i = tid; i < cnt; i += EV_NT) {
+        const unsigned long long e = sh.cand[i];
+        const int slot = (int)~(unsigned)e;
+        if (slot < first || slot >= first + n) continue;
+        int above_me = 0;
+#pragma unroll 8
+        for (int q = 0; q < cnt; ++q) above_me += sh.cand[q] > e;
+        keys[slot - first] = above_me < kr ? 0xffffffffu : 0u;
+      }
+      floor = max(b0, 1u);
+      break;
+    }
+    if (shift == 0) {  // one key in many slots
       tie_key = b0;
-      from = (unsigned long long)b0 + 1ull;
+      floor = (unsigned long long)b0 + 1ull;
       need = kr;
       break;
     }
-    hi = b0 + min(hi - b0, (1u << shift) - 1u);  // (b0 + the bin's width may pass 2^32)
     lo = b0;
-  }
-  // 3. holes and movers in slot order
-  int2* moves = p.moves + (size_t)u * p.move_cap;
-  int ties = 0, holes = 0, movers = 0;
-  for (int t0 = 0; t0 < len; t0 += EV_NT) {
-    const int t = t0 + tid;
-    const unsigned k = t < len ? key_at(t) : 0u;
-    bool kept = t < len && (unsigned long long)k >= from;
-    if (need) {
-      const bool tie = t < len && k == tie_key;
-      int tot;
-      const int r = ties + block_scan(tie, &sc, tot);
-      if (tie && r < need) kept = true;
-      ties += tot;
-    }
-    const bool hole = t < keep && !kept, mover = kept && t >= keep;
-    int tot;
-    const int r = block_scan((int)hole | ((int)mover << 16), &sc, tot);
-    if (hole) moves[holes + (r & 0xffff)].x = t;
-    if (mover) moves[movers + (r >> 16)].y = t;
-    holes += tot & 0xffff;
-    movers += tot >> 16;
+    hi = b1;
   }
   __syncthreads();
-  // 4. the moves, one warp each
-  const int n16 = p.row_bytes / 16;
-  for (int i = warp; i < holes; i += EV_NW) {
-    const int2 mv = moves[i];
-    const int* table = p.page_table + (size_t)b * p.max_pages;
-    const long long rd = paged_row(table[mv.x >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mv.x);
-    const long long rs = paged_row(table[mv.y >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mv.y);
-    if (lane == 0) {
-      wo[mv.x] = w[mv.y];
-      to[mv.x] = tp[mv.y];
+  // 3. holes and movers: a thread has a run of slots
+  const int run = ((n + EV_NT - 1) / EV_NT + 3) & ~3;
+  const int i0 = min(n, tid * run), i1 = min(n, i0 + run);
+  int ties = 0, total;
+  if (need) {
+    for (int i = i0; i < i1; ++i) ties += keys[i] == tie_key;
+    const int mine = ties;
+    ties = block_scan(mine, sh.scan, total);
+    if (tid < C) dsmem_st_u32(dsmem_map(smem_u32(&sh.tie_sum[rank]), tid), (uint32_t)total);
+    csync();
+    for (int r = 0; r < rank; ++r) ties += sh.tie_sum[r];
+  }
+  auto walk = [&](auto&& visit) {
+    int tie = ties;
+    for (int i = i0; i < i1; ++i) {
+      const unsigned k = keys[i];
+      bool kept = (unsigned long long)k >= floor;
+      if (need && k == tie_key) kept = kept || tie++ < need;
+      const int t = first + i;
+      visit(t, t < keep && !kept, t >= keep && kept);
     }
-    if (rd < 0 || rs < 0) {
-      if (lane == 0) atomicOr(p.status, 1);
-      continue;
+  };
+  int holes = 0, movers = 0;
+  walk([&](int, bool hole, bool mover) {
+    holes += hole;
+    movers += mover;
+  });
+  // (both counts of a CTA are below 2^15)
+  const int packed = block_scan(holes | movers << 16, sh.scan, total);
+  if (tid < C)
+    dsmem_st_v2u32(dsmem_map(smem_u32(&sh.sums[rank]), tid), (uint32_t)(total & 0xffff), (uint32_t)(total >> 16));
+  csync();
+  int hole_at = packed & 0xffff, mover_at = packed >> 16, moves_n = 0;
+  for (int r = 0; r < C; ++r) {
+    if (r < rank) {
+      hole_at += sh.sums[r].x;
+      mover_at += sh.sums[r].y;
     }
-    uint4* kd = reinterpret_cast<uint4*>(static_cast<char*>(p.k_pages) + rd * p.row_bytes);
-    const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const char*>(p.k_pages) + rs * p.row_bytes);
-    uint4* vd = reinterpret_cast<uint4*>(static_cast<char*>(p.v_pages) + rd * p.row_bytes);
-    const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const char*>(p.v_pages) + rs * p.row_bytes);
-    for (int c = lane; c < 2 * n16; c += 32) {
-      if (c < n16) kd[c] = ks[c];
-      else vd[c - n16] = vs[c - n16];
+    moves_n += sh.sums[r].x;
+  }
+  int2* moves = p.moves + (size_t)u * p.move_cap;
+  if (holes + movers)
+    walk([&](int t, bool hole, bool mover) {
+      if (hole) moves[hole_at++].x = t;
+      if (mover) moves[mover_at++].y = t;
+    });
+  csync();  // (and no CTA reads another's shared memory behind it)
+  // 4. the copies: 16 bytes a thread, four at a time
+  const int log2_n16 = 31 - __clz(p.row_bytes / 16), log2_move = log2_n16 + 1;
+  const int* table = p.page_table + (size_t)b * p.max_pages;
+  const long long items = (long long)moves_n << log2_move, stride = (long long)C * EV_NT;
+  for (long long q0 = (long long)rank * EV_NT + tid; q0 < items; q0 += 4 * stride) {
+    uint4 v[4];
+    char* to_row[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const long long q = q0 + j * stride;
+      to_row[j] = nullptr;
+      if (q >= items) continue;
+      const int2 mv = __ldcg(moves + (q >> log2_move));
+      const int part = (int)(q & ((1 << log2_move) - 1));
+      const long long rd = paged_row(table[mv.x >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mv.x);
+      const long long rs = paged_row(table[mv.y >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mv.y);
+      if (part == 0) {
+        wo[mv.x] = w[mv.y];
+        to[mv.x] = tp[mv.y];
+        if (rd < 0 || rs < 0) atomicOr(p.status, 1);
+      }
+      if (rd < 0 || rs < 0) continue;
+      char* pool = static_cast<char*>((part >> log2_n16) ? p.v_pages : p.k_pages);
+      const int byte = (part & ((1 << log2_n16) - 1)) * 16;
+      v[j] = __ldcg(reinterpret_cast<const uint4*>(pool + rs * p.row_bytes + byte));
+      to_row[j] = pool + rd * p.row_bytes + byte;
     }
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (to_row[j]) *reinterpret_cast<uint4*>(to_row[j]) = v[j];
   }
 }
 
@@ -280,9 +432,39 @@ cudaError_t launch_paged_append(const PagedAppendParams& p, int head_dim, bool b
   return cudaGetLastError();
 }
 
-cudaError_t launch_paged_evict(const PagedEvictParams& p, cudaStream_t s) {
-  paged_evict_kernel<<<p.B * p.Hkv, EV_NT, 0, s>>>(p);
-  return cudaGetLastError();
+cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t s) {
+  const int units = p.B * p.Hkv;
+  // CTAs to a unit: a share must fit, and while the units alone leave SMs idle a
+  // share of 2048 slots is as short as its steps' latency is worth
+  int C = 1;
+  while (C < EV_C_MAX &&
+         (p.T_cap > C * EV_MAX_SHARE || (p.T_cap > C * EV_SHORT_SHARE && units * C < sms)))
+    C *= 2;
+  const int smem = min(((p.T_cap + C - 1) / C + 3) & ~3, EV_MAX_SHARE) * 4;
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_MAX_SHARE * 4);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  cudaLaunchAttribute attr;
+  attr.id = cudaLaunchAttributeClusterDimension;
+  attr.val.clusterDim.x = (unsigned)C;
+  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * C));
+  cfg.blockDim = dim3(EV_NT);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = s;
+  cfg.attrs = &attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, paged_evict_kernel, p);
 }
 
 }  // namespace fasa
