@@ -163,7 +163,7 @@ int fasa_paged_evict_workspace_size(const fasa_paged_dims_t* dims, int32_t keep,
   const int st = check_paged_dims(dims);
   if (st) return st;
   if (keep < 1) return FASA_ERR_INVALID_ARG;
-  *bytes = up((size_t)dims->batch * dims->n_kv_heads * most_moves(dims, keep) * sizeof(int2));
+  *bytes = up((size_t)dims->batch * dims->n_kv_heads * most_moves(dims, keep) * 2 * sizeof(int2));
   return FASA_OK;
 }
 

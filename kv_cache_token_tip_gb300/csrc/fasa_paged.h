@@ -64,7 +64,7 @@ struct PagedEvictParams : PagedCommon {
   int* token_pos_out;
   int* new_lens;
   int keep, sinks, recent;
-  int2* moves;     // [units][move_cap]: (to, from)
+  int2* moves;     // [units][2][move_cap]: rows, then slots, that tokens move to and come from
   int move_cap;
   int row_bytes;   // of a K or V row
 };

@@ -111,6 +111,7 @@ constexpr int EV_C_MAX = 16;
 struct EvictShared {
   int hist[EV_BINS];
   int slice[EV_BINS];        // this CTA's slice of the cluster's histogram
+  int partial[EV_BINS / 2];  // its sums over some of the CTAs
   unsigned long long cand[EV_CAND];  // key, then ~slot: a larger entry comes first
   int4 facts[EV_C_MAX];      // every CTA's least and largest key and held tokens
   int slice_sum[EV_C_MAX];
@@ -145,7 +146,7 @@ __device__ int block_scan(int x, int* scan, int& total) {
   return below + incl - x;
 }
 
-__global__ void __launch_bounds__(EV_NT) paged_evict_kernel(const __grid_constant__ PagedEvictParams p) {
+__global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_constant__ PagedEvictParams p) {
   extern __shared__ __align__(16) unsigned keys[];
   __shared__ EvictShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -252,19 +253,27 @@ __global__ void __launch_bounds__(EV_NT) paged_evict_kernel(const __grid_constan
       if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
     }
     csync();
-    // this CTA's slice of the bins, over the cluster
+    // this CTA's slice of the bins, over the cluster: a thread takes a bin of some
+    // of the CTAs
     int sum = 0;
-    for (int i = tid; i < SL; i += EV_NT) {
-      int v = 0;
-      if (C == 1) {
-        v = sh.hist[i];
-      } else {
+    if (C == 1) {
+      for (int i = tid; i < SL; i += EV_NT) sum += sh.slice[i] = sh.hist[i];
+    } else {
+      const int np = max(1, EV_NT / SL), part = tid / SL;  // (SL 1024: two bins a thread)
+      for (int i = tid - part * SL; i < SL; i += EV_NT) {
         const uint32_t at = smem_u32(&sh.hist[rank * SL + i]);
+        int v = 0;
 #pragma unroll 4
-        for (int r = 0; r < C; ++r) v += (int)dsmem_ld_u32(dsmem_map(at, r));
+        for (int r = part; r < C; r += np) v += (int)dsmem_ld_u32(dsmem_map(at, r));
+        sh.partial[part * SL + i] = v;
       }
-      sh.slice[i] = v;
-      sum += v;
+      __syncthreads();
+      for (int i = tid; i < SL; i += EV_NT) {
+        int v = 0;
+        for (int q = 0; q < np; ++q) v += sh.partial[q * SL + i];
+        sh.slice[i] = v;
+        sum += v;
+      }
     }
     int total;
     block_scan(sum, sh.scan, total);
@@ -303,8 +312,8 @@ __global__ void __launch_bounds__(EV_NT) paged_evict_kernel(const __grid_constan
     if (cnt <= EV_CAND) {
       // every CTA gets all keys of the bin, CTA after CTA, and marks its own as
       // kept (largest key) or not (least)
-      int before = 0;
-      for (int r = 0; r < rank; ++r) before += (int)dsmem_ld_u32(dsmem_map(smem_u32(&sh.hist[bin]), r));
+      const int before = (int)__reduce_add_sync(
+          0xffffffffu, lane < rank ? dsmem_ld_u32(dsmem_map(smem_u32(&sh.hist[bin]), lane)) : 0u);
       for (int i = tid; i < n; i += EV_NT) {
         const unsigned k = keys[i];
         if (k >= b0 && k <= b1) {
@@ -376,43 +385,47 @@ __global__ void __launch_bounds__(EV_NT) paged_evict_kernel(const __grid_constan
     }
     moves_n += sh.sums[r].x;
   }
-  int2* moves = p.moves + (size_t)u * p.move_cap;
-  if (holes + movers)
+  // a move: the hole's and the mover's row, and their slots
+  int2* rows = p.moves + (size_t)u * 2 * p.move_cap;
+  int2* slots = rows + p.move_cap;
+  if (holes + movers) {
+    const int* table = p.page_table + (size_t)b * p.max_pages;
     walk([&](int t, bool hole, bool mover) {
-      if (hole) moves[hole_at++].x = t;
-      if (mover) moves[mover_at++].y = t;
+      if (!hole && !mover) return;
+      const int row = (int)paged_row(table[t >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, t);
+      if (row < 0) atomicOr(p.status, 1);
+      const int at = hole ? hole_at++ : mover_at++;
+      (hole ? rows[at].x : rows[at].y) = row;
+      (hole ? slots[at].x : slots[at].y) = t;
     });
+  }
   csync();  // (and no CTA reads another's shared memory behind it)
-  // 4. the copies: 16 bytes a thread, four at a time
+  // 4. the copies: 16 bytes a thread, several of them on the way
+  constexpr int U = 6;
   const int log2_n16 = 31 - __clz(p.row_bytes / 16), log2_move = log2_n16 + 1;
-  const int* table = p.page_table + (size_t)b * p.max_pages;
-  const long long items = (long long)moves_n << log2_move, stride = (long long)C * EV_NT;
-  for (long long q0 = (long long)rank * EV_NT + tid; q0 < items; q0 += 4 * stride) {
-    uint4 v[4];
-    char* to_row[4];
+  const int items = moves_n << log2_move, stride = C * EV_NT;  // (at most 2^17 moves of 2^6 items)
+  const int part = tid & ((1 << log2_move) - 1);               // the same for all of a thread's items
+  char* pool = static_cast<char*>((part >> log2_n16) ? p.v_pages : p.k_pages) + (part & ((1 << log2_n16) - 1)) * 16;
+  for (int q0 = rank * EV_NT + tid; q0 < items; q0 += U * stride) {
+    int2 mv[U];
+    uint4 v[U];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const long long q = q0 + j * stride;
-      to_row[j] = nullptr;
-      if (q >= items) continue;
-      const int2 mv = __ldcg(moves + (q >> log2_move));
-      const int part = (int)(q & ((1 << log2_move) - 1));
-      const long long rd = paged_row(table[mv.x >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mv.x);
-      const long long rs = paged_row(table[mv.y >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mv.y);
-      if (part == 0) {
-        wo[mv.x] = w[mv.y];
-        to[mv.x] = tp[mv.y];
-        if (rd < 0 || rs < 0) atomicOr(p.status, 1);
-      }
-      if (rd < 0 || rs < 0) continue;
-      char* pool = static_cast<char*>((part >> log2_n16) ? p.v_pages : p.k_pages);
-      const int byte = (part & ((1 << log2_n16) - 1)) * 16;
-      v[j] = __ldcg(reinterpret_cast<const uint4*>(pool + rs * p.row_bytes + byte));
-      to_row[j] = pool + rd * p.row_bytes + byte;
+    for (int j = 0; j < U; ++j) {
+      const int q = q0 + j * stride;
+      mv[j] = q < items ? __ldcg(rows + (q >> log2_move)) : make_int2(-1, -1);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-      if (to_row[j]) *reinterpret_cast<uint4*>(to_row[j]) = v[j];
+    for (int j = 0; j < U; ++j)
+      if (mv[j].x >= 0 && mv[j].y >= 0)
+        v[j] = __ldcg(reinterpret_cast<const uint4*>(pool + (long long)mv[j].y * p.row_bytes));
+#pragma unroll
+    for (int j = 0; j < U; ++j)
+      if (mv[j].x >= 0 && mv[j].y >= 0) *reinterpret_cast<uint4*>(pool + (long long)mv[j].x * p.row_bytes) = v[j];
+  }
+  for (int i = rank * EV_NT + tid; i < moves_n; i += stride) {
+    const int2 mv = __ldcg(slots + i);
+    wo[mv.x] = w[mv.y];
+    to[mv.x] = tp[mv.y];
   }
 }
 

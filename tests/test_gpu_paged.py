@@ -391,6 +391,9 @@ EVICTS = [
     ("bf16", 2, 8, 128, 64, [1000, 513], 512, 4, 100), ("bf16", 1, 2, 64, 256, [3000], 7, 2, 5),
     ("f32", 5, 2, 64, 16, [17, 40, 16, 300, 0], 16, 16, 0), ("bf16", 1, 1, 128, 128, [5000], 4999, 0, 0),
     ("bf16", 2, 4, 128, 16, [9000, 8200], 1025, 0, 1025), ("bf16", 1, 2, 128, 64, [20000], 4096, 4, 256),
+    # clusters of 1 with long shares, of 2, and of 16 with a share near the most
+    ("bf16", 40, 4, 64, 64, [5000 - 61 * (i % 9) for i in range(40)], 4700, 4, 32),
+    ("f32", 30, 4, 64, 16, [2500 + i for i in range(30)], 2510, 1, 0), ("bf16", 1, 1, 64, 256, [230001], 1200, 3, 99),
 ]
 
 

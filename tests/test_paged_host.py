@@ -106,8 +106,8 @@ def test_workspace_sizes(L):
     assert n.value >= plain + 2 * 32 * 512 * 4 and _attend(L, d, w=P, n=n.value - 1) == 3
     ev = L.fasa_paged_evict_workspace_size
     assert ev(ctypes.byref(d), 0, ctypes.byref(n)) == 1 and ev(ctypes.byref(d), 8, None) == 1
-    assert ev(ctypes.byref(d), 100, ctypes.byref(n)) == 0 and n.value >= 2 * 8 * 100 * 8
-    assert ev(ctypes.byref(d), 500, ctypes.byref(n)) == 0 and n.value >= 2 * 8 * 12 * 8
+    assert ev(ctypes.byref(d), 100, ctypes.byref(n)) == 0 and n.value >= 2 * 8 * 100 * 16
+    assert ev(ctypes.byref(d), 500, ctypes.byref(n)) == 0 and n.value >= 2 * 8 * 12 * 16
     assert ev(ctypes.byref(d), 512, ctypes.byref(n)) == 0 and n.value == 0   # nothing can be over the bound
 
 
