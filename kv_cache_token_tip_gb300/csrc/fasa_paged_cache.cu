@@ -348,6 +348,12 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   // 3. holes and movers: a thread has a run of slots
   const int run = ((n + EV_NT - 1) / EV_NT + 3) & ~3;
   const int i0 = min(n, tid * run), i1 = min(n, i0 + run);
+  const int* table = p.page_table + (size_t)b * p.max_pages;
+  int page_at = -1, page = -1;  // the table's entry at page_at, for the run's first slot ahead
+  if (i0 < i1) {
+    page_at = (first + i0) >> p.log2_page;
+    page = __ldg(table + page_at);
+  }
   int ties = 0, total;
   if (need) {
     for (int i = i0; i < i1; ++i) ties += keys[i] == tie_key;
@@ -389,10 +395,13 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   int2* rows = p.moves + (size_t)u * 2 * p.move_cap;
   int2* slots = rows + p.move_cap;
   if (holes + movers) {
-    const int* table = p.page_table + (size_t)b * p.max_pages;
     walk([&](int t, bool hole, bool mover) {
       if (!hole && !mover) return;
-      const int row = (int)paged_row(table[t >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, t);
+      if (t >> p.log2_page != page_at) {
+        page_at = t >> p.log2_page;
+        page = __ldg(table + page_at);
+      }
+      const int row = (int)paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, t);
       if (row < 0) atomicOr(p.status, 1);
       const int at = hole ? hole_at++ : mover_at++;
       (hole ? rows[at].x : rows[at].y) = row;
