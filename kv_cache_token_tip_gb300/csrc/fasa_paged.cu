@@ -113,7 +113,7 @@ int fasa_paged_append(const void* k_new, const void* v_new, int32_t n_tokens, co
   p.weight = weight;
   p.token_pos = token_pos;
   const cudaError_t e =
-      launch_paged_append(p, dims->head_dim, dims->dtype == FASA_BF16, reinterpret_cast<cudaStream_t>(stream));
+      launch_paged_append(p, dims->head_dim, dims->dtype == FASA_BF16, sms, reinterpret_cast<cudaStream_t>(stream));
   return e == cudaSuccess ? FASA_OK : report_cuda(e);
 }
 

@@ -74,7 +74,7 @@ FASA_HD int paged_record_floats(int G, int D) { return (G * (D + 2) + 3) / 4 * 4
 size_t paged_attend_workspace(int units, int G, int D, int T_cap, bool weights);
 void paged_attend_layout(PagedAttendParams& p, int units, int D, void* ws);
 
-cudaError_t launch_paged_append(const PagedAppendParams& p, int head_dim, bool bf16, cudaStream_t s);
+cudaError_t launch_paged_append(const PagedAppendParams& p, int head_dim, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_paged_attend(const PagedAttendParams& p, int head_dim, bool bf16, int sms, cudaStream_t s);
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t s);
 

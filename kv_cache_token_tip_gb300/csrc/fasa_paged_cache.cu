@@ -14,74 +14,125 @@ namespace fasa {
 namespace {
 
 // ------------------------------------------------------------------- append
+// A warp takes a token and some of its heads' rows, 16 bytes of a row to a lane,
+// so that a lane turns the same pairs of every head: their cosines and sines are
+// computed once.  The rows are on their way meanwhile.  Bound by the bytes for a
+// prompt, by the chain of loads (table, length, page, row) for a token a sequence.
 constexpr int AP_NT = 128;
+constexpr int AP_U = 4;              // rows of K and of V a lane has on the way
+constexpr int AP_MANY = 2048;        // from this many tokens a warp takes all heads of one
 
 // Sequence of new token x, and which of its tokens it is; false for padding
-// and for a table that does not ascend (reported).
+// and for a table that does not ascend (reported).  A whole warp.
 __device__ __forceinline__ bool token_of(const PagedAppendParams& p, int x, int& b, int& j) {
   if (!p.cu_new) {
     b = x;
     j = 0;
     return true;
   }
+  const int lane = threadIdx.x & 31;
   if (x >= __ldg(p.cu_new + p.B)) return false;  // padding
-  int lo = 0, hi = p.B;  // cu_new[lo] <= x < cu_new[hi]
+  int lo = 0, hi = p.B;  // cu_new[lo] <= x < cu_new[hi]: 32 places at a time
   while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (__ldg(p.cu_new + mid) <= x) lo = mid;
-    else hi = mid;
+    const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
+    lo += __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(p.cu_new + min(at, p.B)) <= x)) * step;
+    hi = min(hi, lo + step);
   }
   const int first = __ldg(p.cu_new + lo), next = __ldg(p.cu_new + lo + 1);
   b = lo;
   j = x - first;
   if (first < 0 || first > x || next <= x || next > p.n_tokens) {
-    atomicOr(p.status, 1);
+    if (lane == 0) atomicOr(p.status, 1);
     return false;
   }
   return true;
 }
 
-// One warp per (token, KV head): the key's pairs turned by the token's
-// position, the value copied.  Elements of a lane: D / 32, whole pairs.
-template <typename T, int D>
-__global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_constant__ PagedAppendParams p) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  const long long w = ((long long)blockIdx.x * AP_NT + threadIdx.x) >> 5;
-  const int x = (int)(w / p.Hkv), h = (int)(w - (long long)x * p.Hkv);
-  if (x >= p.n_tokens) return;
-  int b, j;
-  if (!token_of(p, x, b, j)) return;
-  const int len = p.seq_lens[b];
-  const long long slot = (long long)len + j;
-  if (len < 0 || slot >= p.T_cap) {
-    if (lane == 0) atomicOr(p.status, 1);
-    return;
-  }
-  const int page = p.page_table[(size_t)b * p.max_pages + (slot >> p.log2_page)];
-  const long long row = paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, (int)slot);
-  if (row < 0) {
-    if (lane == 0) atomicOr(p.status, 1);
-    return;
-  }
-  const int m = p.pos[b] + j;
-  const T* kn = static_cast<const T*>(p.k_new) + ((size_t)x * p.Hkv + h) * D + lane * E;
-  const T* vn = static_cast<const T*>(p.v_new) + ((size_t)x * p.Hkv + h) * D + lane * E;
-  T* kd = static_cast<T*>(p.k_pages) + (size_t)row * D + lane * E;
-  T* vd = static_cast<T*>(p.v_pages) + (size_t)row * D + lane * E;
+// Four or two pairs of a row, turned.
+template <typename T, int NP>
+__device__ __forceinline__ uint4 turn_row(const uint4& w, const float2 (&cs)[NP]) {
+  const uint32_t in[4] = {w.x, w.y, w.z, w.w};
+  uint32_t out[4];
 #pragma unroll
-  for (int e = 0; e < E; e += 2) {
-    const float2 c = rope_cos_sin(p.rope_turns[(lane * E + e) / 2], m);
-    const float x0 = to_f32<T>(kn[e]), x1 = to_f32<T>(kn[e + 1]);
-    kd[e] = from_f32<T>(x0 * c.x - x1 * c.y);
-    kd[e + 1] = from_f32<T>(x0 * c.y + x1 * c.x);
-    vd[e] = vn[e];
-    vd[e + 1] = vn[e + 1];
+  for (int i = 0; i < NP; ++i) {
+    float x0, x1;
+    if constexpr (sizeof(T) == 2) {
+      x0 = bf16_lo(in[i]);
+      x1 = bf16_hi(in[i]);
+    } else {
+      x0 = __uint_as_float(in[2 * i]);
+      x1 = __uint_as_float(in[2 * i + 1]);
+    }
+    const float y0 = x0 * cs[i].x - x1 * cs[i].y, y1 = x0 * cs[i].y + x1 * cs[i].x;
+    if constexpr (sizeof(T) == 2) {
+      out[i] = pack_bf16(y0, y1);
+    } else {
+      out[2 * i] = __float_as_uint(y0);
+      out[2 * i + 1] = __float_as_uint(y1);
+    }
   }
-  if (lane == 0) {
-    const size_t at = ((size_t)b * p.Hkv + h) * p.T_cap + slot;
-    if (p.weight) p.weight[at] = 0.f;
-    if (p.token_pos) p.token_pos[at] = m;
+  return make_uint4(out[0], out[1], out[2], out[3]);
+}
+
+// heads: of a warp, whole steps of the rows its lanes cover.
+template <typename T, int D>
+__global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_constant__ PagedAppendParams p, int heads) {
+  constexpr int LPR = D * (int)sizeof(T) / 16, RPW = 32 / LPR;  // lanes of a row, rows of a warp
+  constexpr int EPL = 16 / (int)sizeof(T), NP = EPL / 2;        // elements and pairs of a lane
+  __shared__ unsigned long long turns[D / 2];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  // (lanes reading different parameter words take turns: some lanes of each warp)
+  constexpr int TW = D / 2 / (AP_NT / 32);
+  if (lane < TW) turns[warp * TW + lane] = p.rope_turns[warp * TW + lane];
+  __syncthreads();
+  const int chunks = (p.Hkv + heads - 1) / heads, at = lane % LPR, sub = lane / LPR;
+  const long long items = (long long)p.n_tokens * chunks, warps = (long long)gridDim.x * (AP_NT / 32);
+  for (long long w = (long long)blockIdx.x * (AP_NT / 32) + warp; w < items; w += warps) {
+    const int x = (int)(w / chunks), h0 = (int)(w - (long long)x * chunks) * heads, h1 = min(p.Hkv, h0 + heads);
+    int b, j;
+    if (!token_of(p, x, b, j)) continue;
+    const int len = __ldg(p.seq_lens + b), m = __ldg(p.pos + b) + j;
+    const long long slot = (long long)len + j;
+    if (len < 0 || slot >= p.T_cap) {
+      if (lane == 0) atomicOr(p.status, 1);
+      continue;
+    }
+    const int page = __ldg(p.page_table + (size_t)b * p.max_pages + (slot >> p.log2_page));
+    if (page < 0 || page >= p.n_pages) {
+      if (lane == 0) atomicOr(p.status, 1);
+      continue;
+    }
+    float2 cs[NP];
+    for (int hb = h0; hb < h1; hb += RPW * AP_U) {
+      uint4 k[AP_U], v[AP_U];
+#pragma unroll
+      for (int i = 0; i < AP_U; ++i) {
+        const int h = hb + i * RPW + sub;
+        const size_t from = ((size_t)x * p.Hkv + h) * D + at * EPL;
+        if (h < h1) {
+          k[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_new) + from));
+          v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v_new) + from));
+        }
+      }
+      if (hb == h0) {
+#pragma unroll
+        for (int i = 0; i < NP; ++i) cs[i] = rope_cos_sin(turns[at * NP + i], m);
+      }
+#pragma unroll
+      for (int i = 0; i < AP_U; ++i) {
+        const int h = hb + i * RPW + sub;
+        if (h < h1) {
+          const size_t to = (size_t)paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, (int)slot) * D + at * EPL;
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.k_pages) + to) = turn_row<T, NP>(k[i], cs);
+          *reinterpret_cast<uint4*>(static_cast<T*>(p.v_pages) + to) = v[i];
+          if (at == 0) {
+            const size_t stat = ((size_t)b * p.Hkv + h) * p.T_cap + slot;
+            if (p.weight) p.weight[stat] = 0.f;
+            if (p.token_pos) p.token_pos[stat] = m;
+          }
+        }
+      }
+    }
   }
 }
 
@@ -440,18 +491,25 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
 
 }  // namespace
 
-cudaError_t launch_paged_append(const PagedAppendParams& p, int head_dim, bool bf16, cudaStream_t s) {
-  const long long warps = (long long)p.n_tokens * p.Hkv;
-  const unsigned blocks = (unsigned)((warps * 32 + AP_NT - 1) / AP_NT);
-  using B16 = __nv_bfloat16;
-  if (bf16) {
-    if (head_dim == 128) paged_append_kernel<B16, 128><<<blocks, AP_NT, 0, s>>>(p);
-    else paged_append_kernel<B16, 64><<<blocks, AP_NT, 0, s>>>(p);
-  } else {
-    if (head_dim == 128) paged_append_kernel<float, 128><<<blocks, AP_NT, 0, s>>>(p);
-    else paged_append_kernel<float, 64><<<blocks, AP_NT, 0, s>>>(p);
-  }
+namespace {
+
+template <typename T, int D>
+cudaError_t launch_append(const PagedAppendParams& p, int sms, cudaStream_t s) {
+  // few tokens: as many warps as rows allow; many: a token's cosines once
+  constexpr int RPW = 32 / (D * (int)sizeof(T) / 16);
+  const int heads = p.n_tokens < AP_MANY ? RPW : (p.Hkv + RPW - 1) / RPW * RPW;
+  const long long items = (long long)p.n_tokens * ((p.Hkv + heads - 1) / heads);
+  const long long blocks = (items + AP_NT / 32 - 1) / (AP_NT / 32);
+  paged_append_kernel<T, D><<<(unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms), AP_NT, 0, s>>>(p, heads);
   return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_paged_append(const PagedAppendParams& p, int head_dim, bool bf16, int sms, cudaStream_t s) {
+  using B16 = __nv_bfloat16;
+  if (bf16) return head_dim == 128 ? launch_append<B16, 128>(p, sms, s) : launch_append<B16, 64>(p, sms, s);
+  return head_dim == 128 ? launch_append<float, 128>(p, sms, s) : launch_append<float, 64>(p, sms, s);
 }
 
 cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t s) {
