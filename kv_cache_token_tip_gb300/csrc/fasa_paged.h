@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <utility>
+
 #include "fasa_paged_index.h"
 
 namespace fasa {
@@ -71,6 +73,35 @@ struct PagedEvictParams : PagedCommon {
 
 // (whole 16-byte words, so that the next record begins on a boundary)
 FASA_HD int paged_record_floats(int G, int D) { return (G * (D + 2) + 3) / 4 * 4; }
+// A kernel of the paged cache begins under the tail of the kernel before it in its
+// stream (paged_behind: the launch), waits for all that came before its first
+// access to memory (paged_wait: every thread of every block) and lets the next
+// kernel begin as early (paged_go).  A kernel may read ahead of its wait only what
+// is older than the kernel before it: so where that one goes on before it waits,
+// nothing.  The launch of one such kernel behind another then costs little.
+template <class... P, class... A>
+cudaError_t paged_behind(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
+                         cudaStream_t s, A&&... args) {
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = cluster;
+  attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(block);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, std::forward<A>(args)...);
+}
+#ifdef __CUDACC__
+__device__ __forceinline__ void paged_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void paged_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+#endif
+
 size_t paged_attend_workspace(int units, int G, int D, int T_cap, bool weights);
 void paged_attend_layout(PagedAttendParams& p, int units, int D, void* ws);
 

@@ -387,8 +387,6 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
   unsigned* words = reinterpret_cast<unsigned*>(sm + P::OFF_LINE);
   const uint32_t ring = smem_u32(sm) + warp * S * P::STAGE;
   const uint32_t bars = smem_u32(sm + P::OFF_BAR) + warp * S * 8;
-  // the join's blocks may take their places: they wait for this grid's end
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (lane == 0) {
     for (int i = 0; i < S; ++i) mbar_init(bars + 8 * i, 1);
     fence_mbar_init();
@@ -396,6 +394,8 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
   // (lanes reading different parameter words take turns: a few lanes of each warp)
   constexpr int TW = D / 2 / M::WARPS;
   if (lane < TW) turns[warp * TW + lane] = p.rope_turns[warp * TW + lane];
+  paged_wait();
+  paged_go();  // the join's blocks take their places beside this kernel's, and read the lengths
   make_line<32 * M::WARPS>(p, words, reinterpret_cast<int*>(sm + P::OFF_SCAN), blockIdx.x == 0);
   const PagedLine line{words, p.B, p.Hkv};
   for (int b = blockIdx.x; b < p.B; b += gridDim.x)  // sequences without a token: zeros
@@ -573,6 +573,7 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
   __shared__ int scan[NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
   const int R = paged_record_floats(G, D);
+  // (the lengths are older than the first kernel, which waited before it let this one begin)
   make_line<NT>(p, words, scan, false);
   const PagedLine line{words, p.B, p.Hkv};
   const int parts = line.parts(p.parts), total = line.total();
@@ -611,7 +612,8 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
   const int step = team ? blocks : blocks * NW;
   int task = team ? blockIdx.x : warp * blocks + blockIdx.x;
   bool cut_here = task < tasks && task_at(task);
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  paged_go();
+  paged_wait();
   for (; task < tasks; task += step, cut_here = task < tasks && task_at(task)) {
     if (!cut_here) continue;
     const int n = c1 - c0 + 1;
@@ -802,22 +804,11 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   p.parts = grid * M::WARPS;
   e = allow_shared<D, M>();
   if (e != cudaSuccess) return e;
-  paged_attend_kernel<D, M><<<grid, 32 * M::WARPS, smem, s>>>(p, km, vm);
-  e = cudaGetLastError();
+  e = paged_behind(paged_attend_kernel<D, M>, grid, 32 * M::WARPS, smem, 0, s, p, km, vm);
   if (e != cudaSuccess) return e;
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr.val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(p.weight ? 4 * sms : sms);
-  cfg.blockDim = dim3(JN_NT);
-  cfg.dynamicSmemBytes = (p.B + 1) * 4;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  const PagedAttendParams& cp = p;
-  return p.weight ? cudaLaunchKernelEx(&cfg, paged_join_kernel<D, true>, cp)
-                  : cudaLaunchKernelEx(&cfg, paged_join_kernel<D, false>, cp);
+  const size_t line = (p.B + 1) * 4;
+  return p.weight ? paged_behind(paged_join_kernel<D, true>, 4 * sms, JN_NT, line, 0, s, p)
+                  : paged_behind(paged_join_kernel<D, false>, sms, JN_NT, line, 0, s, p);
 }
 
 }  // namespace

@@ -85,6 +85,8 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
   constexpr int TW = D / 2 / (AP_NT / 32);
   if (lane < TW) turns[warp * TW + lane] = p.rope_turns[warp * TW + lane];
   __syncthreads();
+  paged_go();
+  paged_wait();
   const int chunks = (p.Hkv + heads - 1) / heads, at = lane % LPR, sub = lane / LPR;
   const long long items = (long long)p.n_tokens * chunks, warps = (long long)gridDim.x * (AP_NT / 32);
   for (long long w = (long long)blockIdx.x * (AP_NT / 32) + warp; w < items; w += warps) {
@@ -207,6 +209,8 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
     if (C > 1) cluster_sync();
     else __syncthreads();
   };
+  paged_go();
+  paged_wait();
   int len = p.seq_lens[b];
   if (len < 0 || len > p.T_cap) {
     if (tid == 0) atomicOr(p.status, 1);
@@ -500,8 +504,8 @@ cudaError_t launch_append(const PagedAppendParams& p, int sms, cudaStream_t s) {
   const int heads = p.n_tokens < AP_MANY ? RPW : (p.Hkv + RPW - 1) / RPW * RPW;
   const long long items = (long long)p.n_tokens * ((p.Hkv + heads - 1) / heads);
   const long long blocks = (items + AP_NT / 32 - 1) / (AP_NT / 32);
-  paged_append_kernel<T, D><<<(unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms), AP_NT, 0, s>>>(p, heads);
-  return cudaGetLastError();
+  return paged_behind(paged_append_kernel<T, D>, (unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms), AP_NT, 0, 0, s,
+                      p, heads);
 }
 
 }  // namespace
@@ -533,18 +537,7 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t 
     if (e != cudaSuccess) return e;
     done.fetch_or(bit, std::memory_order_release);
   }
-  cudaLaunchAttribute attr;
-  attr.id = cudaLaunchAttributeClusterDimension;
-  attr.val.clusterDim.x = (unsigned)C;
-  attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * C));
-  cfg.blockDim = dim3(EV_NT);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = s;
-  cfg.attrs = &attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, paged_evict_kernel, p);
+  return paged_behind(paged_evict_kernel, (unsigned)(units * C), EV_NT, (size_t)smem, (unsigned)C, s, p);
 }
 
 }  // namespace fasa

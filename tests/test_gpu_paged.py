@@ -501,6 +501,46 @@ def test_decode_loop_of_a_bounded_cache(dtype, d, page, G):
     assert newest == [[161, 161], [75, 75]]
 
 
+def test_each_call_sees_what_the_one_before_it_wrote():
+    """Calls one behind the other in a stream, each reading what the last one
+    writes: lengths from the eviction, rows from the append, weights from the
+    attention; nothing in between that waits."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_append, fasa_paged_attention, fasa_paged_evict
+    keep = 200
+    c = Cache("bf16", 6, 4, 4, 128, 16, [3000, 201, 10, 0, 900, 200], max_pages=200, seed=61, sigma=2.0)
+    c.pos = (c.lens - 1).clamp_min(0)
+    first = [x.clone() for x in (c.kp, c.vp, c.weight, c.token_pos)]
+    new, q0 = torch.zeros_like(c.lens), c.q.clone()
+    k_new, v_new = c.kp[:6, :, 3].contiguous(), c.vp[:6, :, 5].contiguous()
+    out = [torch.empty_like(c.out) for _ in range(3)]
+
+    def calls(wait):
+        fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, c.lens, out[0], weight=c.weight, dims=c.dims)
+        wait()
+        fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, c.lens, keep, new, 2, 16, dims=c.dims)
+        wait()
+        fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, new, out[1], weight=c.weight, dims=c.dims)
+        wait()
+        fasa_paged_append(k_new, v_new, c.pos, c.kp, c.vp, c.table, new, weight=c.weight, token_pos=c.token_pos,
+                          dims=c.dims)
+        wait()
+        fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, new, out[2], dims=c.dims)
+        wait()
+        return [x.clone() for x in (c.kp, c.vp, c.weight, c.token_pos, new, *out)]
+
+    ref = calls(torch.cuda.synchronize)
+    assert new.tolist() == [200, 200, 10, 0, 200, 200]
+    for _ in range(20):
+        for x, y in zip((c.kp, c.vp, c.weight, c.token_pos), first):
+            x.copy_(y)
+        new.fill_(77)
+        torch.cuda.synchronize()
+        for x, y in zip(calls(lambda: None), ref):
+            assert torch.equal(x, y)
+    assert torch.equal(c.q, q0) and status() == 0
+
+
 def test_decode_steps_in_one_graph():
     """append, attention and eviction captured together and replayed give the
     bits of the same calls made one by one."""
