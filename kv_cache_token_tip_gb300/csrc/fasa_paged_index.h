@@ -23,7 +23,7 @@ namespace fasa {
 
 constexpr int PAGED_GROUP = 16;         // tokens per group
 constexpr int PAGED_UNIT_COST = 1;      // what a unit costs beside its groups, in groups
-constexpr int PAGED_PART_COST = 4;     // a part costs at least this much (while there is as much)
+constexpr int PAGED_PART_COST = 1;     // a part costs at least this much (while there is as much)
 constexpr int PAGED_MAX_PARTS = 1280;   // parts the workspace has room for
 constexpr int PAGED_MAX_BATCH = 2048;   // the lengths' prefix sums sit in shared memory
 constexpr int PAGED_MAX_SLOTS = 262144; // T_cap: the line's positions and costs fit 31 bits
