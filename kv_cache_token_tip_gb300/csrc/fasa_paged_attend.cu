@@ -72,6 +72,12 @@ __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool rep
   }
 }
 
+// x0, x1 as bf16 pairs hi + mid + lo: 24 bits and more of each.
+__device__ __forceinline__ void split3_bf16(float x0, float x1, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+  hi = pack_bf16(x0, x1);
+  split_bf16(x0 - bf16_lo(hi), x1 - bf16_hi(hi), mid, lo);
+}
+
 // The logits of a group, where there are weights to add to: to[head][16], kept in
 // L2 by `policy` until the join has read them.
 struct Logits {
@@ -90,8 +96,9 @@ struct Logits {
 // z^T: rows of A the heads, B the tokens.  The rotated and scaled query is
 // three bf16 terms (24 bits: the logits are as exact as fp32's), the first two
 // as rows 0-7 and 8-15 of one operand, the third as another.  o^T = V^T P^T:
-// the z fragment is the P fragment of the same lane, in two bf16 terms (16 bits
-// of a weight that is summed with others), V read transposed.  Lane (g, t) =
+// the z fragment is the P fragment of the same lane, in three bf16 terms too (two,
+// 16 bits, left an error of 1e-6 where few tokens carry the sum), V read
+// transposed.  The tensor cores have the time: K and V's bytes take longer.  Lane (g, t) =
 // (lane / 4, lane % 4) holds head g's m and its share of l, and of o the heads
 // 2t, 2t + 1 at the dims 16 i + g, 16 i + g + 8.
 template <int D>
@@ -120,9 +127,7 @@ struct MathBf16 {
       const uint32_t w = g < G ? raw[t + 4 * i] : 0u;
       const float x0 = bf16_lo(w), x1 = bf16_hi(w);
       const float y0 = x0 * a.x - x1 * a.y, y1 = x0 * a.y + x1 * a.x;
-      const uint32_t hi = pack_bf16(y0, y1);
-      qa[i >> 1][2 * (i & 1)] = hi;
-      split_bf16(y0 - bf16_lo(hi), y1 - bf16_hi(hi), qa[i >> 1][2 * (i & 1) + 1], ql[i >> 1][i & 1]);
+      split3_bf16(y0, y1, qa[i >> 1][2 * (i & 1)], qa[i >> 1][2 * (i & 1) + 1], ql[i >> 1][i & 1]);
     }
     m = -INFINITY;
     l = 0.f;
@@ -144,20 +149,23 @@ struct MathBf16 {
       const int ch = 2 * slab + lch;
       return (ch >> 3) * (PAGED_GROUP * 128) + lrow * 128 + (((ch & 7) ^ (lrow & 7)) << 4);
     };
-    float za[2][4] = {}, zb[2][4] = {};
+    // (sums of their own for the even slabs, the odd ones and the third term: shorter
+    // chains, and less of the accumulator's rounding towards zero)
+    float za[2][2][4] = {}, zb[2][4] = {};
 #pragma unroll
     for (int s = 0; s < MT; ++s) {
       uint32_t b0, b1, b2, b3;
       ldsm_x4(kb + chunk_at(s), b0, b1, b2, b3);
-      mma_bf16_16816(za[0], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b0, b1);
-      mma_bf16_16816(za[1], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b2, b3);
+      mma_bf16_16816(za[s & 1][0], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b0, b1);
+      mma_bf16_16816(za[s & 1][1], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b2, b3);
       mma_bf16_16816(zb[0], ql[s][0], 0u, ql[s][1], 0u, b0, b1);
       mma_bf16_16816(zb[1], ql[s][0], 0u, ql[s][1], 0u, b2, b3);
     }
     float z[4];  // head g, tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      z[i] = (zb[i >> 1][i & 1] + za[i >> 1][2 + (i & 1)]) + za[i >> 1][i & 1];
+      const int nt = i >> 1, e = i & 1;
+      z[i] = (zb[nt][e] + (za[0][nt][2 + e] + za[1][nt][2 + e])) + (za[0][nt][e] + za[1][nt][e]);
       if (2 * t + (i & 1) + 8 * (i >> 1) >= n) z[i] = -INFINITY;
     }
     if (logits.to && g < G) {
@@ -181,9 +189,9 @@ struct MathBf16 {
       w[i] = exp2f(z[i] - ms);
       l += w[i];
     }
-    uint32_t h0, h1, l0, l1;
-    split_bf16(w[0], w[1], h0, l0);
-    split_bf16(w[2], w[3], h1, l1);
+    uint32_t h0, h1, m0, m1, l0, l1;
+    split3_bf16(w[0], w[1], h0, m0, l0);
+    split3_bf16(w[2], w[3], h1, m1, l1);
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       uint32_t a0, a1, a2, a3;
@@ -192,6 +200,7 @@ struct MathBf16 {
       // over the thousands of groups of a long part would add up)
       float acc[4] = {};
       mma_bf16_16816(acc, a0, a1, a2, a3, l0, l1);
+      mma_bf16_16816(acc, a0, a1, a2, a3, m0, m1);
       mma_bf16_16816(acc, a0, a1, a2, a3, h0, h1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] += acc[e];
