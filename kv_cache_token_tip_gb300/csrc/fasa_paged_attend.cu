@@ -94,14 +94,16 @@ struct Logits {
 
 // ------------------------------------------------- bf16: tensor cores
 // z^T: rows of A the heads, B the tokens.  The rotated and scaled query is
-// three bf16 terms (24 bits: the logits are as exact as fp32's), the first two
-// as rows 0-7 and 8-15 of one operand, the third as another.  o^T = V^T P^T:
+// three bf16 terms (24 bits: the logits are as exact as fp32's).  o^T = V^T P^T:
 // the z fragment is the P fragment of the same lane, in three bf16 terms too (two,
 // 16 bits, left an error of 1e-6 where few tokens carry the sum), V read
-// transposed.  The tensor cores have the time: K and V's bytes take longer.  Lane (g, t) =
-// (lane / 4, lane % 4) holds head g's m and its share of l, and of o the heads
-// 2t, 2t + 1 at the dims 16 i + g, 16 i + g + 8.
-template <int D>
+// transposed.  Lane (g, t) = (lane / 4, lane % 4) holds the m of row g's head and
+// its share of l, and of o the heads of the columns 2t, 2t + 1 at the dims 16 i + g,
+// 16 i + g + 8.
+// PACK, for at most four heads: the rows 0-3, 4-7, 8-11 of one operand are a head's
+// terms, and of P's columns 0-3 the first terms, 4-7 the second: 32 instructions a
+// group instead of 56, which a part's last group waits for.
+template <int D, bool PACK>
 struct MathBf16 {
   using T = __nv_bfloat16;
   static constexpr int CTAS = 2;  // per SM
@@ -114,20 +116,29 @@ struct MathBf16 {
   static constexpr int MT = D / 16;
   static constexpr int SCRATCH = 0;  // shared memory of a warp
   static constexpr CUtensorMapDataType TYPE = CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-  uint32_t qa[MT][4], ql[MT][2];
+  uint32_t qa[MT][4], ql[PACK ? 1 : MT][2];
   float m, l, o[MT][4];
 
   // query: the unit's raw rows [G][D].
   __device__ void begin(const void* query, const float2* cs, int G, float*) {
-    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3;
-    const uint32_t* raw = static_cast<const uint32_t*>(query) + min(g, G - 1) * (D / 2);
+    const int g = (threadIdx.x & 31) >> 2, t = threadIdx.x & 3, head = PACK ? g & 3 : g;
+    const uint32_t* raw = static_cast<const uint32_t*>(query) + min(head, G - 1) * (D / 2);
 #pragma unroll
-    for (int i = 0; i < 2 * MT; ++i) {  // the pairs t + 4 i of head g
+    for (int i = 0; i < 2 * MT; ++i) {  // the pairs t + 4 i of the head
       const float2 a = cs[t + 4 * i];
-      const uint32_t w = g < G ? raw[t + 4 * i] : 0u;
+      const uint32_t w = head < G ? raw[t + 4 * i] : 0u;
       const float x0 = bf16_lo(w), x1 = bf16_hi(w);
       const float y0 = x0 * a.x - x1 * a.y, y1 = x0 * a.y + x1 * a.x;
-      split3_bf16(y0, y1, qa[i >> 1][2 * (i & 1)], qa[i >> 1][2 * (i & 1) + 1], ql[i >> 1][i & 1]);
+      uint32_t hi, mid, lo;
+      split3_bf16(y0, y1, hi, mid, lo);
+      if constexpr (PACK) {
+        qa[i >> 1][2 * (i & 1)] = g < 4 ? hi : mid;
+        qa[i >> 1][2 * (i & 1) + 1] = g < 4 ? lo : 0u;
+      } else {
+        qa[i >> 1][2 * (i & 1)] = hi;
+        qa[i >> 1][2 * (i & 1) + 1] = mid;
+        ql[i >> 1][i & 1] = lo;
+      }
     }
     m = -INFINITY;
     l = 0.f;
@@ -151,21 +162,29 @@ struct MathBf16 {
     };
     // (sums of their own for the even slabs, the odd ones and the third term: shorter
     // chains, and less of the accumulator's rounding towards zero)
-    float za[2][2][4] = {}, zb[2][4] = {};
+    float za[2][2][4] = {}, zb[PACK ? 1 : 2][4] = {};
 #pragma unroll
     for (int s = 0; s < MT; ++s) {
       uint32_t b0, b1, b2, b3;
       ldsm_x4(kb + chunk_at(s), b0, b1, b2, b3);
       mma_bf16_16816(za[s & 1][0], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b0, b1);
       mma_bf16_16816(za[s & 1][1], qa[s][0], qa[s][1], qa[s][2], qa[s][3], b2, b3);
-      mma_bf16_16816(zb[0], ql[s][0], 0u, ql[s][1], 0u, b0, b1);
-      mma_bf16_16816(zb[1], ql[s][0], 0u, ql[s][1], 0u, b2, b3);
+      if constexpr (!PACK) {
+        mma_bf16_16816(zb[0], ql[s][0], 0u, ql[s][1], 0u, b0, b1);
+        mma_bf16_16816(zb[1], ql[s][0], 0u, ql[s][1], 0u, b2, b3);
+      }
     }
-    float z[4];  // head g, tokens 2t, 2t + 1, 2t + 8, 2t + 9
+    float z[4];  // the head's, tokens 2t, 2t + 1, 2t + 8, 2t + 9
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int nt = i >> 1, e = i & 1;
-      z[i] = (zb[nt][e] + (za[0][nt][2 + e] + za[1][nt][2 + e])) + (za[0][nt][e] + za[1][nt][e]);
+      const float low = za[0][nt][2 + e] + za[1][nt][2 + e], high = za[0][nt][e] + za[1][nt][e];
+      if constexpr (PACK) {
+        z[i] = low + high;
+        z[i] += __shfl_xor_sync(0xffffffffu, z[i], 16);
+      } else {
+        z[i] = (zb[nt][e] + low) + high;
+      }
       if (2 * t + (i & 1) + 8 * (i >> 1) >= n) z[i] = -INFINITY;
     }
     if (logits.to && g < G) {
@@ -192,6 +211,12 @@ struct MathBf16 {
     uint32_t h0, h1, m0, m1, l0, l1;
     split3_bf16(w[0], w[1], h0, m0, l0);
     split3_bf16(w[2], w[3], h1, m1, l1);
+    if constexpr (PACK) {  // column g: the first term, or head g - 4's second
+      h0 = g < 4 ? h0 : m0;
+      h1 = g < 4 ? h1 : m1;
+      l0 = g < 4 ? l0 : 0u;
+      l1 = g < 4 ? l1 : 0u;
+    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       uint32_t a0, a1, a2, a3;
@@ -200,16 +225,20 @@ struct MathBf16 {
       // over the thousands of groups of a long part would add up)
       float acc[4] = {};
       mma_bf16_16816(acc, a0, a1, a2, a3, l0, l1);
-      mma_bf16_16816(acc, a0, a1, a2, a3, m0, m1);
+      if constexpr (!PACK) mma_bf16_16816(acc, a0, a1, a2, a3, m0, m1);
       mma_bf16_16816(acc, a0, a1, a2, a3, h0, h1);
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[i][e] += acc[e];
     }
   }
-  // l of a head in all its lanes.
+  // l of a head in all its lanes, o whole.
   __device__ void finish() {
     l += __shfl_xor_sync(0xffffffffu, l, 1);
     l += __shfl_xor_sync(0xffffffffu, l, 2);
+    if constexpr (PACK) {
+#pragma unroll
+      for (int i = 0; i < 4 * MT; ++i) o[i >> 2][i & 3] += __shfl_xor_sync(0xffffffffu, o[i >> 2][i & 3], 2);
+    }
   }
   // (m, l) of head g to ml(g, m, l), by one lane; o times inv (by head) to to[head][dim].
   template <class F>
@@ -861,7 +890,9 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
 
 cudaError_t launch_paged_attend(const PagedAttendParams& p0, int head_dim, bool bf16, int sms, cudaStream_t s) {
   PagedAttendParams p = p0;
-  if (bf16) return head_dim == 128 ? launch<128, MathBf16<128>>(p, sms, s) : launch<64, MathBf16<64>>(p, sms, s);
+  if (bf16 && head_dim == 128)
+    return p.G <= 4 ? launch<128, MathBf16<128, true>>(p, sms, s) : launch<128, MathBf16<128, false>>(p, sms, s);
+  if (bf16) return p.G <= 4 ? launch<64, MathBf16<64, true>>(p, sms, s) : launch<64, MathBf16<64, false>>(p, sms, s);
   if (head_dim == 128) return p.G <= 4 ? launch<128, MathF32<128, 4>>(p, sms, s) : launch<128, MathF32<128, 8>>(p, sms, s);
   return p.G <= 4 ? launch<64, MathF32<64, 4>>(p, sms, s) : launch<64, MathF32<64, 8>>(p, sms, s);
 }
