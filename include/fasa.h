@@ -462,7 +462,7 @@ int fasa_paged_attention(const void* q, const int32_t* pos, const void* k_pages,
  * the moved tokens' entries are written), or others of that shape, apart from
  * them: slots 0 .. new_lens[b]-1 are written there and the inputs are left as
  * they were.  Slots at or behind new_lens[b] keep their contents everywhere.
- * new_lens must not be seq_lens.  1 <= keep, 0 <= sinks, 0 <= recent,
+ * new_lens must lie apart from seq_lens.  1 <= keep, 0 <= sinks, 0 <= recent,
  * sinks + recent <= keep.  Table entries from ceil(new_len / page_size)
  * on are free for other use afterwards.
  * workspace: at least fasa_paged_evict_workspace_size bytes, as above.
@@ -489,7 +489,8 @@ int fasa_device_status(fasa_stream_t stream, int32_t* status);
  * calls launched after it in this process, the bound of every device wait
  * (wait_limit_ns > 0; the default is 1 s) and:
  *  - drop_tip_tile >= 0: the fused step's TIP stage of that tile index arms
- *    its barrier but never issues the copy, so the waits on it run out;
+ *    its barrier but never issues the copy, so the waits on it run out
+ *    (and fasa_paged_attention leaves its first part's copy of that index so);
  *  - drop_fac_refill >= 0: in the single-exchange kernel's FAC after the
  *    selection, the warp that refills attending warp 0's slots withholds
  *    its completion arrivals for that refill (0 = the first), so warp 0's

@@ -128,6 +128,8 @@ int report_cuda(cudaError_t e) { return cuda_fail(e); }
 
 unsigned long long wait_limit_ns() { return g_wait_ns; }
 
+int dropped_copy() { return g_drop_tip_tile; }
+
 }  // namespace fasa
 
 namespace {

@@ -150,6 +150,7 @@ int fasa_paged_attention(const void* q, const int32_t* pos, const void* k_pages,
   p.out = out;
   p.weight = weight;
   p.wait_ns = wait_limit_ns();
+  p.drop_group = dropped_copy();
   p.scale = (float)(1.4426950408889634 / sqrt((double)dims->head_dim));
   paged_attend_layout(p, dims->batch * dims->n_kv_heads, dims->head_dim, workspace);
   const cudaError_t e =
@@ -177,7 +178,8 @@ int fasa_paged_evict(const float* weight, const int32_t* token_pos, const int32_
   if (!weight || !token_pos || !pos || !page_table || !seq_lens || !k_pages || !v_pages || !weight_out ||
       !token_pos_out || !new_lens)
     return FASA_ERR_INVALID_ARG;
-  if (sinks < 0 || recent < 0 || (long long)sinks + recent > keep || new_lens == seq_lens) return FASA_ERR_INVALID_ARG;
+  if (sinks < 0 || recent < 0 || (long long)sinks + recent > keep) return FASA_ERR_INVALID_ARG;
+  if (!apart(new_lens, seq_lens, (size_t)dims->batch * 4)) return FASA_ERR_INVALID_ARG;
   if (!aligned(weight, 16) || !aligned(token_pos, 16) || !aligned(weight_out, 16) || !aligned(token_pos_out, 16) ||
       !aligned(k_pages, 16) || !aligned(v_pages, 16))
     return FASA_ERR_INVALID_ARG;

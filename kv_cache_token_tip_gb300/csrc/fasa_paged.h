@@ -18,6 +18,7 @@ void rope_turns_table(double rope_theta, int head_dim, unsigned long long (&turn
 int device_facts(int* sms, int** status);
 int report_cuda(cudaError_t e);
 unsigned long long wait_limit_ns();  // bound of every device wait
+int dropped_copy();                  // test hook: the copy that is left unissued (-1: none)
 
 struct PagedCommon {
   int B, Hq, Hkv, G, log2_page, n_pages, max_pages, T_cap;
@@ -55,6 +56,7 @@ struct PagedAttendParams : PagedCommon {
   float* logits;  // [units][T_cap / 16][G][16]
   int parts;      // most parts of this launch
   unsigned long long wait_ns;  // bound of every device wait
+  int drop_group;              // test hook: this group of part 0 is never copied (-1: none)
 };
 
 struct PagedEvictParams : PagedCommon {
@@ -100,6 +102,33 @@ cudaError_t paged_behind(void (*kernel)(P...), unsigned grid, unsigned block, si
 #ifdef __CUDACC__
 __device__ __forceinline__ void paged_go() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void paged_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+// Loads past L1 that stay behind a wait or a barrier (the __ldg and __ldcg functions
+// may be taken for loads of what never changes, and moved ahead of it).
+__device__ __forceinline__ int ld_cg(const int* p) {
+  int v;
+  asm volatile("ld.global.cg.s32 %0, [%1];" : "=r"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float ld_cg(const float* p) {
+  float v;
+  asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ int2 ld_cg(const int2* p) {
+  int2 v;
+  asm volatile("ld.global.cg.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ float4 ld_cg(const float4* p) {
+  float4 v;
+  asm volatile("ld.global.cg.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "l"(p));
+  return v;
+}
+__device__ __forceinline__ uint4 ld_cg(const uint4* p) {
+  uint4 v;
+  asm volatile("ld.global.cg.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
+  return v;
+}
 #endif
 
 size_t paged_attend_workspace(int units, int G, int D, int T_cap, bool weights);

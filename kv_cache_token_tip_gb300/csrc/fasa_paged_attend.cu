@@ -46,7 +46,7 @@ __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool rep
     const int b = b0 + tid;
     int len = 0;
     if (b < p.B) {
-      len = p.seq_lens[b];
+      len = ld_cg(p.seq_lens + b);
       if (report && (len < 0 || len > p.T_cap)) atomicOr(p.status, 1);
       len = min(max(len, 0), p.T_cap);
     }
@@ -451,6 +451,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
   constexpr int TW = D / 2 / M::WARPS;
   if (lane < TW) turns[warp * TW + lane] = p.rope_turns[warp * TW + lane];
   paged_wait();
+  fence_proxy_async_global();  // (a kernel before this one may have stored the rows that TMA reads)
   paged_go();  // the join's blocks take their places beside this kernel's, and read the lengths
   make_line<32 * M::WARPS>(p, words, reinterpret_cast<int*>(sm + P::OFF_SCAN), blockIdx.x == 0);
   const PagedLine line{words, p.B, p.Hkv};
@@ -493,7 +494,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
       const int b = line.sequence_of(x);
       const int n = line.groups(b), rem = x - line.before(b) * p.Hkv;
       const int h = rem / n, slot = (rem - h * n) * PAGED_GROUP;
-      const int page = __ldg(p.page_table + (size_t)b * p.max_pages + (slot >> p.log2_page));
+      const int page = ld_cg(p.page_table + (size_t)b * p.max_pages + (slot >> p.log2_page));
       rows = (int)paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, slot);
       if (rows < 0) atomicOr(p.status, 1);
     }
@@ -508,8 +509,10 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
       const uint32_t bar = bars + 8 * st, dst = ring + st * P::STAGE;
       if (row >= 0) {
         mbar_arrive_expect_tx(bar, P::STAGE);
-        tma_rows(dst, &kmap, row, bar, policy);
-        tma_rows(dst + P::ROWS, &vmap, row, bar, policy);
+        if (issued != p.drop_group || c != 0) {  // (test hook: copies that never come)
+          tma_rows(dst, &kmap, row, bar, policy);
+          tma_rows(dst + P::ROWS, &vmap, row, bar, policy);
+        }
       } else {
         mbar_arrive(bar);
       }
@@ -527,7 +530,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
   sg.start(line, r0, r1);
   sg.at();
   if (M::RAW) fetch(sg.unit());
-  int k = 0, turned = -1, pos = __ldg(p.pos + sg.b);
+  int k = 0, turned = -1, pos = ld_cg(p.pos + sg.b);
   for (bool more = true; more;) {
     const int unit = sg.unit(), len = line.tokens(sg.b);
     if (!M::RAW) fetch(unit);
@@ -548,7 +551,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
     more = sg.at();
     if (more) {
       if (M::RAW) fetch(sg.unit());
-      pos = __ldg(p.pos + sg.b);
+      pos = ld_cg(p.pos + sg.b);
     }
     logits.to = p.weight ? p.logits + ((size_t)unit * p.T_cap + (size_t)(r0 + k - begin) * PAGED_GROUP) * G : nullptr;
     for (; r0 + k < last; ++k) {
@@ -595,7 +598,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
   }
   // after a wait that ran out: no copy may land in memory of a block that is gone
   for (; landed < issued; ++landed)
-    if (!mbar_wait_bounded(bars + 8 * (landed % S), (landed / S) & 1, p.wait_ns) && lane == 0) atomicOr(p.status, 4);
+    if (!mbar_wait_bounded(bars + 8 * (landed % S), (landed / S) & 1, 8 * p.wait_ns) && lane == 0) atomicOr(p.status, 4);
 }
 
 // --------------------------------------------------------------- join
@@ -606,7 +609,7 @@ __device__ float joined_lse(const PagedAttendParams& p, int R, int GD, int g, in
   float M = -INFINITY, L = 0.f;
   for (int k = c0 + (threadIdx.x & 31); k <= c1; k += 32) {
     const float* r = p.records + (size_t)(2 * k + (k == c0)) * R + GD + g;
-    const float m = __ldcg(r), l = __ldcg(r + p.G), X = fmaxf(M, m), Xs = finite_or_0(X);
+    const float m = ld_cg(r), l = ld_cg(r + p.G), X = fmaxf(M, m), Xs = finite_or_0(X);
     L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
     M = X;
   }
@@ -696,9 +699,9 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
       for (int u = 0; u < U; ++u) {
         const int k = k0 + u * nrows;
         const float* r = k == 0 ? first : rest + (size_t)(2 * k) * R;
-        o[u] = k < n ? __ldcg(reinterpret_cast<const float4*>(r + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
-        m[u] = k < n ? __ldcg(r + G * D + g) : -INFINITY;
-        l[u] = k < n ? __ldcg(r + G * D + G + g) : 0.f;
+        o[u] = k < n ? ld_cg(reinterpret_cast<const float4*>(r + i)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        m[u] = k < n ? ld_cg(r + G * D + g) : -INFINITY;
+        l[u] = k < n ? ld_cg(r + G * D + G + g) : 0.f;
       }
       float X = M;
 #pragma unroll
@@ -776,7 +779,7 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
       for (int g = 0; g < G_MAX; ++g)
         if (g < G) {
           const float* zt = z + (size_t)(t & -PAGED_GROUP) * G + g * PAGED_GROUP + (t & (PAGED_GROUP - 1));
-          zg[g] = __ldcg(reinterpret_cast<const float4*>(zt));
+          zg[g] = ld_cg(reinterpret_cast<const float4*>(zt));
         }
       old = *reinterpret_cast<const float4*>(weight + t);
     };
@@ -784,7 +787,7 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
     if (t < t1) load(t);
     __syncthreads();  // the last unit's sums are read
     if (warp < G) {
-      const float e = c0 == c1 ? __ldcg(p.lse + (size_t)unit * G + warp) : joined_lse(p, R, G * D, warp, c0, c1);
+      const float e = c0 == c1 ? ld_cg(p.lse + (size_t)unit * G + warp) : joined_lse(p, R, G * D, warp, c0, c1);
       if (lane == 0) lse[warp] = e;
     }
     __syncthreads();

@@ -31,14 +31,14 @@ __device__ __forceinline__ bool token_of(const PagedAppendParams& p, int x, int&
     return true;
   }
   const int lane = threadIdx.x & 31;
-  if (x >= __ldg(p.cu_new + p.B)) return false;  // padding
+  if (x >= ld_cg(p.cu_new + p.B)) return false;  // padding
   int lo = 0, hi = p.B;  // cu_new[lo] <= x < cu_new[hi]: 32 places at a time
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    lo += __popc(__ballot_sync(0xffffffffu, at < hi && __ldg(p.cu_new + min(at, p.B)) <= x)) * step;
+    lo += __popc(__ballot_sync(0xffffffffu, at < hi && ld_cg(p.cu_new + min(at, p.B)) <= x)) * step;
     hi = min(hi, lo + step);
   }
-  const int first = __ldg(p.cu_new + lo), next = __ldg(p.cu_new + lo + 1);
+  const int first = ld_cg(p.cu_new + lo), next = ld_cg(p.cu_new + lo + 1);
   b = lo;
   j = x - first;
   if (first < 0 || first > x || next <= x || next > p.n_tokens) {
@@ -93,13 +93,13 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
     const int x = (int)(w / chunks), h0 = (int)(w - (long long)x * chunks) * heads, h1 = min(p.Hkv, h0 + heads);
     int b, j;
     if (!token_of(p, x, b, j)) continue;
-    const int len = __ldg(p.seq_lens + b), m = __ldg(p.pos + b) + j;
+    const int len = ld_cg(p.seq_lens + b), m = ld_cg(p.pos + b) + j;
     const long long slot = (long long)len + j;
     if (len < 0 || slot >= p.T_cap) {
       if (lane == 0) atomicOr(p.status, 1);
       continue;
     }
-    const int page = __ldg(p.page_table + (size_t)b * p.max_pages + (slot >> p.log2_page));
+    const int page = ld_cg(p.page_table + (size_t)b * p.max_pages + (slot >> p.log2_page));
     if (page < 0 || page >= p.n_pages) {
       if (lane == 0) atomicOr(p.status, 1);
       continue;
@@ -112,8 +112,8 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
         const int h = hb + i * RPW + sub;
         const size_t from = ((size_t)x * p.Hkv + h) * D + at * EPL;
         if (h < h1) {
-          k[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_new) + from));
-          v[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const T*>(p.v_new) + from));
+          k[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.k_new) + from);
+          v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v_new) + from);
         }
       }
       if (hb == h0) {
@@ -407,7 +407,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   int page_at = -1, page = -1;  // the table's entry at page_at, for the run's first slot ahead
   if (i0 < i1) {
     page_at = (first + i0) >> p.log2_page;
-    page = __ldg(table + page_at);
+    page = ld_cg(table + page_at);
   }
   int ties = 0, total;
   if (need) {
@@ -454,7 +454,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       if (!hole && !mover) return;
       if (t >> p.log2_page != page_at) {
         page_at = t >> p.log2_page;
-        page = __ldg(table + page_at);
+        page = ld_cg(table + page_at);
       }
       const int row = (int)paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, t);
       if (row < 0) atomicOr(p.status, 1);
@@ -476,18 +476,18 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
 #pragma unroll
     for (int j = 0; j < U; ++j) {
       const int q = q0 + j * stride;
-      mv[j] = q < items ? __ldcg(rows + (q >> log2_move)) : make_int2(-1, -1);
+      mv[j] = q < items ? ld_cg(rows + (q >> log2_move)) : make_int2(-1, -1);
     }
 #pragma unroll
     for (int j = 0; j < U; ++j)
       if (mv[j].x >= 0 && mv[j].y >= 0)
-        v[j] = __ldcg(reinterpret_cast<const uint4*>(pool + (long long)mv[j].y * p.row_bytes));
+        v[j] = ld_cg(reinterpret_cast<const uint4*>(pool + (long long)mv[j].y * p.row_bytes));
 #pragma unroll
     for (int j = 0; j < U; ++j)
       if (mv[j].x >= 0 && mv[j].y >= 0) *reinterpret_cast<uint4*>(pool + (long long)mv[j].x * p.row_bytes) = v[j];
   }
   for (int i = rank * EV_NT + tid; i < moves_n; i += stride) {
-    const int2 mv = __ldcg(slots + i);
+    const int2 mv = ld_cg(slots + i);
     wo[mv.x] = w[mv.y];
     to[mv.x] = tp[mv.y];
   }

@@ -272,6 +272,27 @@ def test_attention_in_graphs_that_share_a_workspace():
     assert status() == 0
 
 
+def test_attention_bounded_waits():
+    """A copy that is never issued: its wait runs out within the bound, the call says
+    so and drains what it has under way, and the next call gives the bits of the
+    first.  (The wait is on a barrier in shared memory that no copy targets.)"""
+    import torch
+    from kv_cache_token_tip_gb300 import FASA_DEV_TIMEOUT, FASA_DEV_UNDRAINED, fasa_test_fault_injection
+    for dtype in ("bf16", "f32"):
+        c = Cache(dtype, 2, 4, 4, 128, 32, [9000, 5000], seed=14)
+        ref = c.attend(False).clone()
+        assert status() == 0
+        try:
+            fasa_test_fault_injection(wait_limit_ns=2_000_000)
+            assert torch.equal(c.attend(False), ref) and status() == 0   # a short bound alone changes nothing
+            fasa_test_fault_injection(wait_limit_ns=2_000_000, drop_tip_tile=1)
+            c.attend(False)
+            assert status() == FASA_DEV_TIMEOUT | FASA_DEV_UNDRAINED
+        finally:
+            fasa_test_fault_injection()
+        assert torch.equal(c.attend(False), ref) and status() == 0
+
+
 # ---------------------------------------------------------------------- append
 def _append_ref(c, k_new, v_new, cu, kp, vp, w, tp):
     PO.paged_append(c.host(k_new), c.host(v_new), cu, c.pos.cpu().numpy(), c.table.cpu().numpy(),

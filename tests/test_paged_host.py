@@ -82,7 +82,7 @@ def test_arguments_rejected_before_launch(L):
     assert _evict(L, d, keep=0) == 1 and _evict(L, d, sinks=-1) == 1 and _evict(L, d, recent=-1) == 1
     assert _evict(L, d, keep=19) == 1    # sinks + recent > keep
     assert _evict(L, d, sinks=2 ** 31 - 1, recent=2 ** 31 - 1) == 1
-    assert _evict(L, d, new=P) == 1      # new_lens is seq_lens
+    assert _evict(L, d, new=P) == 1 and _evict(L, d, new=P + 4) == 1      # new_lens is seq_lens, or overlaps it
     stat = 2 * 8 * 512 * 4
     A, B, C, D = (P + i * stat for i in range(4))
     assert _evict(L, d, w=A, tp=B, wo=A, tpo=C) == 1           # one in place, the other not
