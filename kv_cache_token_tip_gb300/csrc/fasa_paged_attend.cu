@@ -46,7 +46,7 @@ __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool rep
     const int b = b0 + tid;
     int len = 0;
     if (b < p.B) {
-      len = ld_cg(p.seq_lens + b);
+      len = p.seq_lens[b];
       if (report && (len < 0 || len > p.T_cap)) atomicOr(p.status, 1);
       len = min(max(len, 0), p.T_cap);
     }
@@ -494,7 +494,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
       const int b = line.sequence_of(x);
       const int n = line.groups(b), rem = x - line.before(b) * p.Hkv;
       const int h = rem / n, slot = (rem - h * n) * PAGED_GROUP;
-      const int page = ld_cg(p.page_table + (size_t)b * p.max_pages + (slot >> p.log2_page));
+      const int page = p.page_table[(size_t)b * p.max_pages + (slot >> p.log2_page)];
       rows = (int)paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, slot);
       if (rows < 0) atomicOr(p.status, 1);
     }
@@ -530,7 +530,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
   sg.start(line, r0, r1);
   sg.at();
   if (M::RAW) fetch(sg.unit());
-  int k = 0, turned = -1, pos = ld_cg(p.pos + sg.b);
+  int k = 0, turned = -1, pos = p.pos[sg.b];
   for (bool more = true; more;) {
     const int unit = sg.unit(), len = line.tokens(sg.b);
     if (!M::RAW) fetch(unit);
@@ -551,7 +551,7 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
     more = sg.at();
     if (more) {
       if (M::RAW) fetch(sg.unit());
-      pos = ld_cg(p.pos + sg.b);
+      pos = p.pos[sg.b];
     }
     logits.to = p.weight ? p.logits + ((size_t)unit * p.T_cap + (size_t)(r0 + k - begin) * PAGED_GROUP) * G : nullptr;
     for (; r0 + k < last; ++k) {

@@ -15,30 +15,30 @@ namespace {
 
 // ------------------------------------------------------------------- append
 // A warp takes a token and some of its heads' rows, 16 bytes of a row to a lane,
-// so that a lane turns the same pairs of every head: their cosines and sines are
-// computed once.  The rows are on their way meanwhile.  Bound by the bytes for a
+// so that a lane turns the same pairs of every head: the warp computes a token's
+// cosines and sines once.  The rows are on their way meanwhile.  Bound by the bytes for a
 // prompt, by the chain of loads (table, length, page, row) for a token a sequence.
 constexpr int AP_NT = 128;
-constexpr int AP_U = 4;              // rows of K and of V a lane has on the way
+constexpr int AP_U = 2;              // rows of K and of V a lane has on the way
 constexpr int AP_MANY = 2048;        // from this many tokens a warp takes all heads of one
 
-// Sequence of new token x, and which of its tokens it is; false for padding
-// and for a table that does not ascend (reported).  A whole warp.
-__device__ __forceinline__ bool token_of(const PagedAppendParams& p, int x, int& b, int& j) {
+// Sequence of new token x, and which of its tokens it is; false for padding (used:
+// cu_new[B]) and for a table that does not ascend (reported).  A whole warp.
+__device__ __forceinline__ bool token_of(const PagedAppendParams& p, int x, int used, int& b, int& j) {
   if (!p.cu_new) {
     b = x;
     j = 0;
     return true;
   }
   const int lane = threadIdx.x & 31;
-  if (x >= ld_cg(p.cu_new + p.B)) return false;  // padding
+  if (x >= used) return false;  // padding
   int lo = 0, hi = p.B;  // cu_new[lo] <= x < cu_new[hi]: 32 places at a time
   while (hi - lo > 1) {
     const int step = (hi - lo + 31) / 32, at = lo + (lane + 1) * step;
-    lo += __popc(__ballot_sync(0xffffffffu, at < hi && ld_cg(p.cu_new + min(at, p.B)) <= x)) * step;
+    lo += __popc(__ballot_sync(0xffffffffu, at < hi && p.cu_new[min(at, p.B)] <= x)) * step;
     hi = min(hi, lo + step);
   }
-  const int first = ld_cg(p.cu_new + lo), next = ld_cg(p.cu_new + lo + 1);
+  const int first = p.cu_new[lo], next = p.cu_new[lo + 1];
   b = lo;
   j = x - first;
   if (first < 0 || first > x || next <= x || next > p.n_tokens) {
@@ -80,6 +80,7 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
   constexpr int LPR = D * (int)sizeof(T) / 16, RPW = 32 / LPR;  // lanes of a row, rows of a warp
   constexpr int EPL = 16 / (int)sizeof(T), NP = EPL / 2;        // elements and pairs of a lane
   __shared__ unsigned long long turns[D / 2];
+  __shared__ __align__(16) float2 angles[AP_NT / 32][D / 2];  // cos and sin of a warp's token
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   // (lanes reading different parameter words take turns: some lanes of each warp)
   constexpr int TW = D / 2 / (AP_NT / 32);
@@ -89,24 +90,12 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
   paged_wait();
   const int chunks = (p.Hkv + heads - 1) / heads, at = lane % LPR, sub = lane / LPR;
   const long long items = (long long)p.n_tokens * chunks, warps = (long long)gridDim.x * (AP_NT / 32);
+  const int used = p.cu_new ? p.cu_new[p.B] : p.n_tokens;
   for (long long w = (long long)blockIdx.x * (AP_NT / 32) + warp; w < items; w += warps) {
     const int x = (int)(w / chunks), h0 = (int)(w - (long long)x * chunks) * heads, h1 = min(p.Hkv, h0 + heads);
-    int b, j;
-    if (!token_of(p, x, b, j)) continue;
-    const int len = ld_cg(p.seq_lens + b), m = ld_cg(p.pos + b) + j;
-    const long long slot = (long long)len + j;
-    if (len < 0 || slot >= p.T_cap) {
-      if (lane == 0) atomicOr(p.status, 1);
-      continue;
-    }
-    const int page = ld_cg(p.page_table + (size_t)b * p.max_pages + (slot >> p.log2_page));
-    if (page < 0 || page >= p.n_pages) {
-      if (lane == 0) atomicOr(p.status, 1);
-      continue;
-    }
-    float2 cs[NP];
-    for (int hb = h0; hb < h1; hb += RPW * AP_U) {
-      uint4 k[AP_U], v[AP_U];
+    // the rows first: they need only x, the rest is a chain of loads
+    uint4 k[AP_U], v[AP_U];
+    auto load = [&](int hb) {
 #pragma unroll
       for (int i = 0; i < AP_U; ++i) {
         const int h = hb + i * RPW + sub;
@@ -116,10 +105,30 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
           v[i] = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.v_new) + from);
         }
       }
-      if (hb == h0) {
+    };
+    load(h0);
+    int b, j;
+    if (!token_of(p, x, used, b, j)) continue;
+    const int len = p.seq_lens[b], m = p.pos[b] + j;
+    const long long slot = (long long)len + j;
+    if (len < 0 || slot >= p.T_cap) {
+      if (lane == 0) atomicOr(p.status, 1);
+      continue;
+    }
+    const int page = p.page_table[(size_t)b * p.max_pages + (slot >> p.log2_page)];
+    if (page < 0 || page >= p.n_pages) {
+      if (lane == 0) atomicOr(p.status, 1);
+      continue;
+    }
+    __syncwarp();  // (the last token's are read)
+#pragma unroll 1
+    for (int f = lane; f < D / 2; f += 32) angles[warp][f] = rope_cos_sin(turns[f], m);
+    __syncwarp();
+    float2 cs[NP];
 #pragma unroll
-        for (int i = 0; i < NP; ++i) cs[i] = rope_cos_sin(turns[at * NP + i], m);
-      }
+    for (int i = 0; i < NP; ++i) cs[i] = angles[warp][at * NP + i];
+    for (int hb = h0; hb < h1; hb += RPW * AP_U) {
+      if (hb > h0) load(hb);
 #pragma unroll
       for (int i = 0; i < AP_U; ++i) {
         const int h = hb + i * RPW + sub;
@@ -407,7 +416,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   int page_at = -1, page = -1;  // the table's entry at page_at, for the run's first slot ahead
   if (i0 < i1) {
     page_at = (first + i0) >> p.log2_page;
-    page = ld_cg(table + page_at);
+    page = table[page_at];
   }
   int ties = 0, total;
   if (need) {
@@ -454,7 +463,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       if (!hole && !mover) return;
       if (t >> p.log2_page != page_at) {
         page_at = t >> p.log2_page;
-        page = ld_cg(table + page_at);
+        page = table[page_at];
       }
       const int row = (int)paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, t);
       if (row < 0) atomicOr(p.status, 1);

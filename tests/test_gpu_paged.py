@@ -562,6 +562,37 @@ def test_each_call_sees_what_the_one_before_it_wrote():
     assert torch.equal(c.q, q0) and status() == 0
 
 
+def test_lengths_written_and_read_in_turn():
+    """Two length buffers that evictions with ever smaller bounds write in turn, each
+    read by the attention and the eviction right behind: no call may see what a
+    buffer held two evictions ago."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_attention, fasa_paged_evict
+    keeps = [900, 700, 512, 333, 200, 100, 31, 5]
+
+    def run(wait):
+        c = Cache("bf16", 5, 4, 4, 64, 16, [1000, 950, 400, 30, 0], seed=62, sigma=2.0)
+        c.pos = (c.lens - 1).clamp_min(0)
+        bufs, lens, outs = [torch.zeros_like(c.lens) for _ in range(2)], c.lens, []
+        torch.cuda.synchronize()
+        for i, keep in enumerate(keeps):
+            out = torch.empty_like(c.out)
+            fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, lens, keep, bufs[i % 2], dims=c.dims)
+            wait()
+            lens = bufs[i % 2]
+            fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, lens, out, weight=c.weight, dims=c.dims)
+            wait()
+            outs.append(out)
+        torch.cuda.synchronize()
+        return outs + [c.weight, c.token_pos, c.kp, c.vp, *bufs]
+
+    ref = run(torch.cuda.synchronize)
+    for _ in range(5):
+        for x, y in zip(run(lambda: None), ref):
+            assert torch.equal(x, y)
+    assert status() == 0
+
+
 def test_decode_steps_in_one_graph():
     """append, attention and eviction captured together and replayed give the
     bits of the same calls made one by one."""
