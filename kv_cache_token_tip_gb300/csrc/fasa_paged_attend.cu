@@ -604,17 +604,21 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
 // --------------------------------------------------------------- join
 __device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
 
-// log2 of head g's softmax denominator over the parts c0 .. c1 of a unit; a whole warp.
-__device__ float joined_lse(const PagedAttendParams& p, int R, int GD, int g, int c0, int c1) {
+// log2 of the softmax denominators over the parts c0 .. c1 of a unit, a whole warp:
+// head lane % 8's, four lanes to a head.
+__device__ float joined_lse(const PagedAttendParams& p, int R, int GD, int c0, int c1) {
+  static_assert(G_MAX == 8, "the lanes of a head");
+  const int lane = threadIdx.x & 31, g = min(lane & 7, p.G - 1);
   float M = -INFINITY, L = 0.f;
-  for (int k = c0 + (threadIdx.x & 31); k <= c1; k += 32) {
+#pragma unroll 4
+  for (int k = c0 + (lane >> 3); k <= c1; k += 4) {
     const float* r = p.records + (size_t)(2 * k + (k == c0)) * R + GD + g;
     const float m = ld_cg(r), l = ld_cg(r + p.G), X = fmaxf(M, m), Xs = finite_or_0(X);
     L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
     M = X;
   }
 #pragma unroll
-  for (int s = 16; s; s >>= 1) {
+  for (int s = 16; s >= 8; s >>= 1) {
     const float m = __shfl_xor_sync(0xffffffffu, M, s), l = __shfl_xor_sync(0xffffffffu, L, s);
     const float X = fmaxf(M, m), Xs = finite_or_0(X);
     L = L * exp2f(M - Xs) + l * exp2f(m - Xs);
@@ -629,16 +633,17 @@ __device__ float joined_lse(const PagedAttendParams& p, int R, int GD, int g, in
 // then the rows' sums meet in order.  Where tasks are many a warp takes one (128
 // floats, its own row); where they are few, and so a unit's parts many, a block
 // does, with its warps as rows, or four rows of 8 lanes to a warp (32 floats).
-// With weights, each block then adds what its share of the line's tokens gets.
+// With weights, each warp then adds what its share of the line's tokens gets, by
+// itself: blocks' barriers there cost 2 us of the 9 a step of eight 4K caches had.
 // A block is small enough to wait for the first kernel beside its CTAs.
 template <int D, bool WEIGHTS>
-__global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
+__global__ void __launch_bounds__(JN_NT, WEIGHTS ? 2 : 3)
     paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
   constexpr int NT = JN_NT, NW = NT / 32;
   extern __shared__ unsigned words[];
   __shared__ float4 so[NT];
   __shared__ float2 sml[NT];
-  __shared__ float lse[G_MAX];
+  __shared__ float lse[NW][G_MAX];
   __shared__ int scan[NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
   const int R = paged_record_floats(G, D);
@@ -758,66 +763,60 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 4 : 3)
     }
   }
   if constexpr (!WEIGHTS) return;
-  static_assert(!WEIGHTS || NW >= G_MAX, "a warp for each head");
-  // (the few blocks with a task leave the tokens to the others)
-  const int busy = team && 8 * tasks <= blocks ? tasks : 0, mine = (int)blockIdx.x - busy;
-  if (mine < 0) return;
-  sg.start(line, cut(total, blocks - busy, mine), cut(total, blocks - busy, mine + 1));
+  const int warps = blocks * NW, w = blockIdx.x * NW + warp;
+  sg.start(line, cut(total, warps, w), cut(total, warps, w + 1));
   for (; sg.at(); sg.next()) {
     const int unit = sg.unit();
     c0 = sg.first_part(parts);
     c1 = sg.last_part(parts);
-    // four tokens a thread: a group's slots, and so its logits and weights, are
-    // all there (those behind the end are -inf and get nothing); the first are
-    // under way while the parts' sums are joined
-    const int t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP, tokens = line.tokens(sg.b);
+    // four tokens a lane: a group's slots, and so its logits and weights, are all
+    // there (those behind the end are -inf and get nothing); the first are under way
+    // while the parts' sums are joined
+    const int t0 = (sg.x - sg.unit_begin) * PAGED_GROUP, t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP;
+    const int tokens = line.tokens(sg.b);
     const float* z = p.logits + (size_t)unit * G * p.T_cap;
     float* weight = p.weight + (size_t)unit * p.T_cap;
     float4 zg[G_MAX], old;
     auto load = [&](int t) {
+      const float* zt = z + (size_t)(t & -PAGED_GROUP) * G + (t & (PAGED_GROUP - 1));
 #pragma unroll
       for (int g = 0; g < G_MAX; ++g)
-        if (g < G) {
-          const float* zt = z + (size_t)(t & -PAGED_GROUP) * G + g * PAGED_GROUP + (t & (PAGED_GROUP - 1));
-          zg[g] = ld_cg(reinterpret_cast<const float4*>(zt));
-        }
+        if (g < G) zg[g] = ld_cg(reinterpret_cast<const float4*>(zt + g * PAGED_GROUP));
       old = *reinterpret_cast<const float4*>(weight + t);
     };
-    int t = (sg.x - sg.unit_begin) * PAGED_GROUP + 4 * tid;
+    int t = t0 + 4 * lane;
     if (t < t1) load(t);
-    __syncthreads();  // the last unit's sums are read
-    if (warp < G) {
-      const float e = c0 == c1 ? ld_cg(p.lse + (size_t)unit * G + warp) : joined_lse(p, R, G * D, warp, c0, c1);
-      if (lane == 0) lse[warp] = e;
-    }
-    __syncthreads();
+    const float mine = c0 == c1 ? ld_cg(p.lse + (size_t)unit * G + min(lane, G - 1)) : joined_lse(p, R, G * D, c0, c1);
+    __syncwarp();  // (the last unit's are read)
+    if (lane < G) lse[warp][lane] = mine;
+    __syncwarp();
     while (t < t1) {
-      float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
       for (int g = 0; g < G_MAX; ++g)
         if (g < G) {
-          const float e = lse[g];
-          w.x += exp2f(zg[g].x - e);
-          w.y += exp2f(zg[g].y - e);
-          w.z += exp2f(zg[g].z - e);
-          w.w += exp2f(zg[g].w - e);
+          const float e = lse[warp][g];
+          a.x += exp2f(zg[g].x - e);
+          a.y += exp2f(zg[g].y - e);
+          a.z += exp2f(zg[g].z - e);
+          a.w += exp2f(zg[g].w - e);
         }
       const int live = tokens - t;  // slots behind the end keep what they hold
       if (live >= 4) {
-        *reinterpret_cast<float4*>(weight + t) = make_float4(old.x + w.x, old.y + w.y, old.z + w.z, old.w + w.w);
+        *reinterpret_cast<float4*>(weight + t) = make_float4(old.x + a.x, old.y + a.y, old.z + a.z, old.w + a.w);
       } else {
-        if (live > 0) weight[t] = old.x + w.x;
-        if (live > 1) weight[t + 1] = old.y + w.y;
-        if (live > 2) weight[t + 2] = old.z + w.z;
+        if (live > 0) weight[t] = old.x + a.x;
+        if (live > 1) weight[t + 1] = old.y + a.y;
+        if (live > 2) weight[t + 2] = old.z + a.z;
       }
-      t += 4 * NT;
+      t += 4 * 32;
       if (t < t1) load(t);
     }
-    __syncthreads();
-    // the whole lines of logits that only this block read
-    const uintptr_t z0 = reinterpret_cast<uintptr_t>(z + (size_t)(sg.x - sg.unit_begin) * PAGED_GROUP * G);
+    __syncwarp();
+    // the whole lines of logits that only this warp read
+    const uintptr_t z0 = reinterpret_cast<uintptr_t>(z + (size_t)t0 * G);
     const uintptr_t z1 = reinterpret_cast<uintptr_t>(z + (size_t)t1 * G) & ~(uintptr_t)127;
-    for (uintptr_t at = ((z0 + 127) & ~(uintptr_t)127) + 128 * tid; at < z1; at += 128 * NT)
+    for (uintptr_t at = ((z0 + 127) & ~(uintptr_t)127) + 128 * lane; at < z1; at += 128 * 32)
       asm volatile("discard.global.L2 [%0], 128;" ::"l"(at) : "memory");
   }
 }
@@ -885,7 +884,7 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   e = paged_behind(paged_attend_kernel<D, M>, grid, 32 * M::WARPS, smem, 0, s, p, km, vm);
   if (e != cudaSuccess) return e;
   const size_t line = (p.B + 1) * 4;
-  return p.weight ? paged_behind(paged_join_kernel<D, true>, 4 * sms, JN_NT, line, 0, s, p)
+  return p.weight ? paged_behind(paged_join_kernel<D, true>, 2 * sms, JN_NT, line, 0, s, p)
                   : paged_behind(paged_join_kernel<D, false>, sms, JN_NT, line, 0, s, p);
 }
 

@@ -30,7 +30,7 @@ constexpr int PAGED_MAX_SLOTS = 262144; // T_cap: the line's positions and costs
 
 FASA_HD int paged_groups(int len) { return (len + PAGED_GROUP - 1) / PAGED_GROUP; }
 
-// floor(total * c / n), 0 <= c <= n <= 4096.
+// floor(total * c / n), 0 <= c <= n <= 32768.
 FASA_HD int cut(int total, int n, int c) {
   const int q = total / n, r = total - q * n;
   return q * c + r * c / n;
