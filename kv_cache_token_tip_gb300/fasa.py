@@ -386,8 +386,8 @@ def fasa_decode_step_noalloc(q, pos, k_cache, v_cache, k_dom, dom_fc, seq_lens, 
 
 
 # ---------------------------------------------------------------- paged cache
-# (a small call's time is the host's: each tensor is checked in one expression,
-# and what torch gives for every call is looked up once)
+# (a small call's time is the host's: its tensors are checked in one expression
+# without a call each, and what torch gives for every call is looked up once)
 _torch = None
 
 
@@ -399,31 +399,36 @@ def _here() -> int:
     return _torch.cuda.current_device()
 
 
-def _refuse(x, here, dtype, count, name):
-    if not isinstance(x, _torch.Tensor):
-        raise ValueError(f"{name} must be a tensor")
-    if not x.is_cuda or x.get_device() != here:
-        raise ValueError(f"{name} must be a tensor on the current CUDA device")
-    if x.dtype is not dtype:
-        raise ValueError(f"{name} has dtype {x.dtype}, expected {dtype}")
-    if x.numel() != count:
-        raise ValueError(f"{name} has {x.numel()} elements, expected {count}")
-    raise ValueError(f"{name} must be contiguous")
+def _refuse(here, *tensors):
+    """Raises for the first of (name, tensor, dtype, elements) that does not fit."""
+    for name, x, dtype, count in tensors:
+        if not isinstance(x, _torch.Tensor):
+            raise ValueError(f"{name} must be a tensor")
+        if not x.is_cuda or x.get_device() != here:
+            raise ValueError(f"{name} must be a tensor on the current CUDA device")
+        if x.dtype is not dtype:
+            raise ValueError(f"{name} has dtype {x.dtype}, expected {dtype}")
+        if x.numel() != count:
+            raise ValueError(f"{name} has {x.numel()} elements, expected {count}")
+        if not x.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
 
 
-def _at(x, here, dtype, count, name):
-    """Device address of a contiguous tensor of `count` elements on device `here`."""
+def _optional(x, here, dtype, count, name):
+    """Device address of a tensor that may be None."""
+    if x is None:
+        return None
     try:
         if x.dtype is dtype and x.numel() == count and x.get_device() == here and x.is_contiguous():
             return x.data_ptr()
-    except AttributeError:
+    except AttributeError:  # not a tensor
         pass
-    _refuse(x, here, dtype, count, name)
+    _refuse(here, (name, x, dtype, count))
 
 
 def _room(x, here):
     """Address and bytes of a workspace."""
-    if x.get_device() != here or not x.is_contiguous():
+    if not isinstance(x, _torch.Tensor) or not x.is_cuda or x.get_device() != here or not x.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
     return x.data_ptr(), x.numel() * x.element_size()
 
@@ -450,18 +455,33 @@ def fasa_paged_append(k_new, v_new, pos, k_pages, v_pages, page_table, seq_lens,
     cu_new[b+1], or one per sequence without cu_new; the first of b gets the
     position pos[b].  seq_lens is not advanced."""
     here, store, pool, slots, entries = _paged_sizes(dims)
-    i32, f32, B = _torch.int32, _torch.float32, dims.batch
-    row = dims.n_kv_heads * dims.head_dim
+    i32, B, row = _torch.int32, dims.batch, dims.n_kv_heads * dims.head_dim
     n_tokens = k_new.numel() // row
+    new = n_tokens * row
+    try:
+        fits = (k_new.dtype is store and v_new.dtype is store and k_pages.dtype is store
+                and v_pages.dtype is store and pos.dtype is i32 and page_table.dtype is i32
+                and seq_lens.dtype is i32 and k_new.numel() == new and v_new.numel() == new
+                and k_pages.numel() == pool and v_pages.numel() == pool and pos.numel() == B
+                and page_table.numel() == entries and seq_lens.numel() == B and k_new.get_device() == here
+                and v_new.get_device() == here and k_pages.get_device() == here and v_pages.get_device() == here
+                and pos.get_device() == here and page_table.get_device() == here
+                and seq_lens.get_device() == here and k_new.is_contiguous() and v_new.is_contiguous()
+                and k_pages.is_contiguous() and v_pages.is_contiguous() and pos.is_contiguous()
+                and page_table.is_contiguous() and seq_lens.is_contiguous())
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
+        _refuse(here, ("k_new", k_new, store, new), ("v_new", v_new, store, new), ("k_pages", k_pages, store, pool),
+                ("v_pages", v_pages, store, pool), ("pos", pos, i32, B), ("page_table", page_table, i32, entries),
+                ("seq_lens", seq_lens, i32, B))
     st = lib().fasa_paged_append(
-        _at(k_new, here, store, n_tokens * row, "k_new"), _at(v_new, here, store, n_tokens * row, "v_new"), n_tokens,
-        None if cu_new is None else _at(cu_new, here, i32, B + 1, "cu_new"), _at(pos, here, i32, B, "pos"),
-        _at(page_table, here, i32, entries, "page_table"), _at(seq_lens, here, i32, B, "seq_lens"),
-        _at(k_pages, here, store, pool, "k_pages"), _at(v_pages, here, store, pool, "v_pages"),
-        None if weight is None else _at(weight, here, f32, slots, "weight"),
-        None if token_pos is None else _at(token_pos, here, i32, slots, "token_pos"), ctypes.byref(dims),
-        _on(stream, here))
-    _check("fasa_paged_append", st)
+        k_new.data_ptr(), v_new.data_ptr(), n_tokens, _optional(cu_new, here, i32, B + 1, "cu_new"), pos.data_ptr(),
+        page_table.data_ptr(), seq_lens.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
+        _optional(weight, here, _torch.float32, slots, "weight"), _optional(token_pos, here, i32, slots, "token_pos"),
+        ctypes.byref(dims), _on(stream, here))
+    if st:
+        _check("fasa_paged_append", st)
 
 
 def fasa_paged_workspace_size(dims: FasaPagedDims, weights: bool = False) -> int:
@@ -481,15 +501,31 @@ def fasa_paged_attention(q, pos, k_pages, v_pages, page_table, seq_lens, out, we
     heads = B * dims.n_q_heads * dims.head_dim
     if workspace is None:
         workspace = _torch.empty(fasa_paged_workspace_size(dims, weight is not None), dtype=_torch.uint8,
-                                 device=out.device)
+                                 device=f"cuda:{here}")
     ws, ws_bytes = _room(workspace, here)
+    try:
+        fits = (q.dtype is store and k_pages.dtype is store and v_pages.dtype is store and pos.dtype is i32
+                and page_table.dtype is i32 and seq_lens.dtype is i32 and out.dtype is f32
+                and q.numel() == heads and k_pages.numel() == pool and v_pages.numel() == pool
+                and pos.numel() == B and page_table.numel() == entries and seq_lens.numel() == B
+                and out.numel() == heads and q.get_device() == here and k_pages.get_device() == here
+                and v_pages.get_device() == here and pos.get_device() == here
+                and page_table.get_device() == here and seq_lens.get_device() == here
+                and out.get_device() == here and q.is_contiguous() and k_pages.is_contiguous()
+                and v_pages.is_contiguous() and pos.is_contiguous() and page_table.is_contiguous()
+                and seq_lens.is_contiguous() and out.is_contiguous())
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
+        _refuse(here, ("q", q, store, heads), ("k_pages", k_pages, store, pool), ("v_pages", v_pages, store, pool),
+                ("pos", pos, i32, B), ("page_table", page_table, i32, entries), ("seq_lens", seq_lens, i32, B),
+                ("out", out, f32, heads))
     st = lib().fasa_paged_attention(
-        _at(q, here, store, heads, "q"), _at(pos, here, i32, B, "pos"), _at(k_pages, here, store, pool, "k_pages"),
-        _at(v_pages, here, store, pool, "v_pages"), _at(page_table, here, i32, entries, "page_table"),
-        _at(seq_lens, here, i32, B, "seq_lens"), _at(out, here, f32, heads, "out"),
-        None if weight is None else _at(weight, here, f32, slots, "weight"), ws, ws_bytes, ctypes.byref(dims),
-        _on(stream, here))
-    _check("fasa_paged_attention", st)
+        q.data_ptr(), pos.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
+        seq_lens.data_ptr(), out.data_ptr(), _optional(weight, here, f32, slots, "weight"), ws, ws_bytes,
+        ctypes.byref(dims), _on(stream, here))
+    if st:
+        _check("fasa_paged_attention", st)
 
 
 def fasa_paged_evict_workspace_size(dims: FasaPagedDims, keep: int) -> int:
@@ -512,17 +548,36 @@ def fasa_paged_evict(weight, token_pos, pos, k_pages, v_pages, page_table, seq_l
     i32, f32, B = _torch.int32, _torch.float32, dims.batch
     if workspace is None:
         workspace = _torch.empty(fasa_paged_evict_workspace_size(dims, keep), dtype=_torch.uint8,
-                                 device=weight.device)
+                                 device=f"cuda:{here}")
     ws, ws_bytes = _room(workspace, here)
-    w, t = _at(weight, here, f32, slots, "weight"), _at(token_pos, here, i32, slots, "token_pos")
+    try:
+        fits = (weight.dtype is f32 and token_pos.dtype is i32 and k_pages.dtype is store
+                and v_pages.dtype is store and pos.dtype is i32 and page_table.dtype is i32
+                and seq_lens.dtype is i32 and new_lens.dtype is i32 and weight.numel() == slots
+                and token_pos.numel() == slots and k_pages.numel() == pool and v_pages.numel() == pool
+                and pos.numel() == B and page_table.numel() == entries and seq_lens.numel() == B
+                and new_lens.numel() == B and weight.get_device() == here and token_pos.get_device() == here
+                and k_pages.get_device() == here and v_pages.get_device() == here and pos.get_device() == here
+                and page_table.get_device() == here and seq_lens.get_device() == here
+                and new_lens.get_device() == here and weight.is_contiguous() and token_pos.is_contiguous()
+                and k_pages.is_contiguous() and v_pages.is_contiguous() and pos.is_contiguous()
+                and page_table.is_contiguous() and seq_lens.is_contiguous() and new_lens.is_contiguous())
+    except AttributeError:  # not a tensor
+        fits = False
+    if not fits:
+        _refuse(here, ("weight", weight, f32, slots), ("token_pos", token_pos, i32, slots),
+                ("k_pages", k_pages, store, pool), ("v_pages", v_pages, store, pool), ("pos", pos, i32, B),
+                ("page_table", page_table, i32, entries), ("seq_lens", seq_lens, i32, B),
+                ("new_lens", new_lens, i32, B))
+    w, t = weight.data_ptr(), token_pos.data_ptr()
     st = lib().fasa_paged_evict(
-        w, t, _at(pos, here, i32, B, "pos"), _at(page_table, here, i32, entries, "page_table"),
-        _at(seq_lens, here, i32, B, "seq_lens"), int(keep), int(sinks), int(recent),
-        _at(k_pages, here, store, pool, "k_pages"), _at(v_pages, here, store, pool, "v_pages"),
-        w if weight_out is None else _at(weight_out, here, f32, slots, "weight_out"),
-        t if token_pos_out is None else _at(token_pos_out, here, i32, slots, "token_pos_out"),
-        _at(new_lens, here, i32, B, "new_lens"), ws, ws_bytes, ctypes.byref(dims), _on(stream, here))
-    _check("fasa_paged_evict", st)
+        w, t, pos.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), int(keep), int(sinks), int(recent),
+        k_pages.data_ptr(), v_pages.data_ptr(),
+        w if weight_out is None else _optional(weight_out, here, f32, slots, "weight_out"),
+        t if token_pos_out is None else _optional(token_pos_out, here, i32, slots, "token_pos_out"),
+        new_lens.data_ptr(), ws, ws_bytes, ctypes.byref(dims), _on(stream, here))
+    if st:
+        _check("fasa_paged_evict", st)
 
 
 def fasa_device_status(stream=None) -> int:
