@@ -22,8 +22,11 @@
 namespace fasa {
 
 constexpr int PAGED_GROUP = 16;         // tokens per group
-constexpr int PAGED_UNIT_COST = 1;      // what a unit costs beside its groups, in groups
-constexpr int PAGED_PART_COST = 1;     // a part costs at least this much (while there is as much)
+// What a unit costs beside its groups, in groups (64 sequences of 0 to 1000 tokens:
+// 30.9 us at 0, 25.5 at 1, 25.3 at 2, 26.0 at 4), and the least that a part costs while
+// there is as much (one sequence of 1024 tokens: 12.3 us at 4, 10.7 at 2, 9.3 at 1).
+constexpr int PAGED_UNIT_COST = 1;
+constexpr int PAGED_PART_COST = 1;
 constexpr int PAGED_MAX_PARTS = 1280;   // parts the workspace has room for
 constexpr int PAGED_MAX_BATCH = 2048;   // the lengths' prefix sums sit in shared memory
 constexpr int PAGED_MAX_SLOTS = 262144; // T_cap: the line's positions and costs fit 31 bits
