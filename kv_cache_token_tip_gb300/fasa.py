@@ -439,6 +439,14 @@ def _on(stream, here):
     return _stream(stream)
 
 
+def _scratch(size, here, stream):
+    """A workspace for one call, kept until the call's stream is past it."""
+    x = _torch.empty(size, dtype=_torch.uint8, device=f"cuda:{here}")
+    if stream is not None:
+        x.record_stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+    return x
+
+
 def _paged_sizes(dims):
     """Current device, storage dtype, elements of a pool, of the statistics, of the page table."""
     here = _here()
@@ -500,8 +508,7 @@ def fasa_paged_attention(q, pos, k_pages, v_pages, page_table, seq_lens, out, we
     i32, f32, B = _torch.int32, _torch.float32, dims.batch
     heads = B * dims.n_q_heads * dims.head_dim
     if workspace is None:
-        workspace = _torch.empty(fasa_paged_workspace_size(dims, weight is not None), dtype=_torch.uint8,
-                                 device=f"cuda:{here}")
+        workspace = _scratch(fasa_paged_workspace_size(dims, weight is not None), here, stream)
     ws, ws_bytes = _room(workspace, here)
     try:
         fits = (q.dtype is store and k_pages.dtype is store and v_pages.dtype is store and pos.dtype is i32
@@ -547,8 +554,7 @@ def fasa_paged_evict(weight, token_pos, pos, k_pages, v_pages, page_table, seq_l
     here, store, pool, slots, entries = _paged_sizes(dims)
     i32, f32, B = _torch.int32, _torch.float32, dims.batch
     if workspace is None:
-        workspace = _torch.empty(fasa_paged_evict_workspace_size(dims, keep), dtype=_torch.uint8,
-                                 device=f"cuda:{here}")
+        workspace = _scratch(fasa_paged_evict_workspace_size(dims, keep), here, stream)
     ws, ws_bytes = _room(workspace, here)
     try:
         fits = (weight.dtype is f32 and token_pos.dtype is i32 and k_pages.dtype is store

@@ -121,6 +121,12 @@ SHAPES = [
     ("bf16", 9, 2, 4, 64, 16, [0, 0, 5, 200, 0, 31, 32, 1000, 0]),
     ("bf16", 40, 4, 2, 128, 16, [(i * 37) % 300 for i in range(40)]),
     ("f32", 33, 8, 1, 64, 32, [(i * 53) % 200 for i in range(33)]),
+    # more units than parts: a unit is found by the part it begins in
+    ("bf16", 300, 8, 1, 64, 16, [(i * 37) % 90 for i in range(300)]),
+    ("f32", 260, 8, 2, 64, 16, [(i * 41) % 70 for i in range(260)]),
+    ("bf16", 200, 8, 5, 128, 16, [(i * 29) % 60 for i in range(200)]),
+    # the largest batch
+    ("bf16", 2048, 1, 2, 64, 16, [(i * 31) % 40 for i in range(2048)]),
 ]
 
 
@@ -291,6 +297,125 @@ def test_attention_bounded_waits():
         finally:
             fasa_test_fault_injection()
         assert torch.equal(c.attend(False), ref) and status() == 0
+
+
+def test_attention_reads_no_entry_behind_the_end():
+    """Entries of the page table behind a sequence's last page may be anything."""
+    c = Cache("bf16", 3, 2, 2, 128, 16, [33, 16, 0], max_pages=9, seed=15)
+    for b, n in enumerate([33, 16, 0]):
+        c.table[b, -(-n // 16):] = -7
+    out = c.attend()
+    assert status() == 0
+    before = c.weight.cpu().numpy().astype(np.float64)
+    check_attention(c, before, c.attend(), c.weight.cpu().numpy().astype(np.float64))
+    assert out is c.out and status() == 0
+    new = _run_evict(c, 9, 1, 2)   # (an eviction reads none either)
+    assert new.tolist() == [9, 9, 0] and status() == 0
+
+
+def test_offsets_past_32_bits():
+    """Pools of more than 2^32 elements, used at their far end by all three calls."""
+    import torch
+    from kv_cache_token_tip_gb300 import (FasaPagedDims, fasa_paged_append, fasa_paged_attention, fasa_paged_evict)
+    small = Cache("bf16", 2, 8, 4, 128, 16, [200, 77], max_pages=14, seed=16, spare=0)
+    used, n_pages = small.kp.shape[0], 270_000
+    shape = (n_pages, 8, 16, 128)
+    assert n_pages * 8 * 16 * 128 > 2 ** 32
+    kp, vp = (torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    kp[-used:], vp[-used:] = small.kp, small.vp
+    d = small.dims
+    dims = FasaPagedDims(d.batch, d.n_q_heads, d.n_kv_heads, d.head_dim, d.page_size, n_pages, d.max_pages, d.dtype,
+                         d.rope_theta)
+    far = small.table + (n_pages - used)
+    out, w, tp = torch.empty_like(small.out), small.weight.clone(), small.token_pos.clone()
+    k_new = torch.randn((2, 8, 128), generator=small.gen, device="cuda").bfloat16()
+    new = [torch.zeros_like(small.lens) for _ in range(2)]
+    for kk, vv, table, dd, o, ww, tt, nn in ((kp, vp, far, dims, out, w, tp, new[0]),
+                                             (small.kp, small.vp, small.table, d, small.out, small.weight,
+                                              small.token_pos, new[1])):
+        fasa_paged_append(k_new, k_new, small.pos, kk, vv, table, small.lens, weight=ww, token_pos=tt, dims=dd)
+        fasa_paged_attention(small.q, small.pos, kk, vv, table, small.lens + 1, o, weight=ww, dims=dd)
+        fasa_paged_evict(ww, tt, small.pos, kk, vv, table, small.lens + 1, 60, nn, 2, 9, dims=dd)
+    assert status() == 0
+    assert torch.equal(out, small.out) and torch.equal(w, small.weight) and torch.equal(tp, small.token_pos)
+    assert torch.equal(kp[-used:], small.kp) and torch.equal(vp[-used:], small.vp) and torch.equal(*new)
+
+
+def test_calls_wait_for_copies_and_events_between_them():
+    """What comes between two of the calls in a stream, a copy or an event of
+    another stream, is waited for although the second call begins early."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_append, fasa_paged_attention
+    c = Cache("bf16", 4, 8, 4, 128, 16, [700, 600, 500, 400], max_pages=80, seed=17)
+    n = 200
+    k_new = torch.randn((4 * n, 8, 128), generator=c.gen, device="cuda").bfloat16()
+    cu = torch.arange(0, 4 * n + 1, n, dtype=torch.int32, device="cuda")
+    after = c.lens + n
+    host = after.cpu().pin_memory()
+
+    def append():
+        fasa_paged_append(k_new, k_new, c.pos, c.kp, c.vp, c.table, c.lens, cu_new=cu, dims=c.dims)
+
+    def attend(lens):
+        fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, lens, c.out, dims=c.dims)
+
+    append()
+    torch.cuda.synchronize()
+    attend(after)
+    ref = c.out.clone()
+    lens, side = torch.zeros_like(after), torch.cuda.Stream()
+    for i in range(10):
+        lens.zero_()
+        torch.cuda.synchronize()
+        append()
+        lens.copy_(host, non_blocking=True)
+        attend(lens)
+        assert torch.equal(c.out, ref)
+        lens.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(200_000 * (i % 3))
+            lens.copy_(after)
+        append()
+        torch.cuda.current_stream().wait_stream(side)
+        attend(lens)
+        assert torch.equal(c.out, ref)
+    g, lens2 = torch.cuda.CUDAGraph(), torch.zeros_like(after)
+    with torch.cuda.graph(g):   # the same in a graph, with a copy and a kernel between
+        append()
+        lens2.copy_(after)
+        attend(lens2)
+        lens2.zero_()
+    for _ in range(5):
+        c.out.zero_()
+        g.replay()
+        assert torch.equal(c.out, ref)
+    assert status() == 0
+
+
+def test_own_workspace_of_a_call_on_another_stream():
+    """Without a workspace the call's own one outlives it on the stream it runs on."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_attention, fasa_paged_evict
+    c = Cache("bf16", 2, 8, 4, 128, 32, [9000, 4000], seed=18, sigma=2.0)
+    w0 = c.weight.clone()
+    ref = c.attend().clone()
+    w1, new = c.weight.clone(), torch.zeros_like(c.lens)
+    side = torch.cuda.Stream()
+    for stream in (side, side.cuda_stream):
+        c.weight.copy_(w0)
+        c.out.zero_()
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(3_000_000)
+        fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, c.lens, c.out, weight=c.weight, dims=c.dims,
+                             stream=stream)
+        junk = [torch.full((1 << 22,), float("nan"), device="cuda") for _ in range(40)]
+        torch.cuda.synchronize()
+        assert torch.equal(c.out, ref) and torch.equal(c.weight, w1) and len(junk) == 40
+    fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, c.lens, 100, new, dims=c.dims, stream=side)
+    torch.cuda.synchronize()
+    assert new.tolist() == [100, 100] and status() == 0
 
 
 # ---------------------------------------------------------------------- append
@@ -478,6 +603,15 @@ def test_evict_shuffled_positions_and_held_overflow():
     c.token_pos.fill_(-2 ** 31)
     c.pos.fill_(-2 ** 31)
     _run_evict(c, 64, 0, 64)
+    assert status() == 0
+
+
+def test_evict_bound_of_the_whole_cache():
+    """A bound that no length can pass needs no workspace and moves nothing."""
+    c = Cache("bf16", 2, 2, 1, 64, 16, [64, 10], seed=42)
+    for keep in (64, 1000):
+        assert _run_evict(c, keep, 3, 5).tolist() == [64, 10]
+        assert _run_evict(c, keep, 3, 5, apart=True).tolist() == [64, 10]
     assert status() == 0
 
 
