@@ -1,9 +1,10 @@
 """In-tree build of the CUDA libraries with nvcc (sm_103a).
 
 ``build()`` compiles every translation unit in parallel and links
-``kv_cache_token_tip_gb300/libfasa.so`` (the FASA library) and
-``workload/libfasa_synth.so`` (the synthetic-input generator used by the tests
-and the benchmark).  Object files go to ``_build/`` at the repository root.
+``kv_cache_token_tip_gb300/libfasa.so`` (the FASA library),
+``kv_cache_token_tip_gb300/_fasa_torch.so`` (the paged cache's argument
+marshalling for torch tensors) and ``workload/libfasa_synth.so`` (the
+synthetic-input generator used by the tests and the benchmark).  Object files go to ``_build/`` at the repository root.
 A library is rebuilt only when one of its sources is newer than it.
 """
 
@@ -29,6 +30,8 @@ FASA_DEPS = [os.path.join(PKG, "csrc", f) for f in
              ("fasa_cluster.cuh", "fasa_step.cuh", "fasa_ptx.cuh", "fasa_internal.h",
               "fasa_paged.h", "fasa_paged_index.h")] + [
     os.path.join(ROOT, "include", "fasa.h")]
+LIBTORCH = os.path.join(PKG, "_fasa_torch.so")
+TORCH_SOURCES = [os.path.join(PKG, "csrc", "fasa_torch.cpp")]
 SYNTH_SOURCES = [os.path.join(ROOT, "workload", "csrc", "synth_gen.cu")]
 
 
@@ -79,11 +82,31 @@ def _build_lib(target, sources, deps, extra_flags=(), verbose=False, force=False
     return target
 
 
+def _build_torch(verbose=False, force=False):
+    """The extension module, against the torch that is installed (host code alone)."""
+    if not force and not _stale(LIBTORCH, TORCH_SOURCES + [os.path.join(ROOT, "include", "fasa.h")]):
+        return LIBTORCH
+    import importlib.util
+    import sysconfig
+    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    cuda = os.path.dirname(os.path.dirname(nvcc()))
+    tmp = LIBTORCH + ".tmp"
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + [
+        "-I" + d for d in (sysconfig.get_paths()["include"], os.path.join(torch, "include"),
+                           os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                           os.path.join(cuda, "include"))] + TORCH_SOURCES + [
+        "-o", tmp, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], verbose)
+    os.replace(tmp, LIBTORCH)
+    return LIBTORCH
+
+
 def build(verbose=False, force=False, ptxas_v=False):
-    """Compile libfasa.so and libfasa_synth.so (in parallel); return their paths."""
-    with cf.ThreadPoolExecutor(max_workers=2) as ex:
+    """Compile libfasa.so and libfasa_synth.so (in parallel, with the extension module); return their paths."""
+    with cf.ThreadPoolExecutor(max_workers=3) as ex:
+        t = ex.submit(_build_torch, verbose, force)
         a = ex.submit(_build_lib, LIBFASA, FASA_SOURCES, FASA_DEPS, (), verbose, force, ptxas_v)
         b = ex.submit(_build_lib, LIBSYNTH, SYNTH_SOURCES, [], (), verbose, force, False)
+        t.result()
         return a.result(), b.result()
 
 

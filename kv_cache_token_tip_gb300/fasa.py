@@ -1,9 +1,10 @@
-"""ctypes binding of libfasa.so.
+"""Binding of libfasa.so (ctypes; the paged cache's calls are marshalled by the
+extension module _fasa_torch).
 
 Each function has the name of its C entry point and takes torch CUDA tensors
-(or raw device addresses as ints).  It checks dtypes and contiguity, passes
-``data_ptr()`` and the current CUDA stream, and raises ``FasaError`` on a
-non-zero status.  Nothing here computes on the data.
+(or, but for the paged cache, raw device addresses as ints).  It checks dtypes
+and contiguity, passes ``data_ptr()`` and the current CUDA stream, and raises
+``FasaError`` on a non-zero status.  Nothing here computes on the data.
 """
 
 import ctypes
@@ -386,74 +387,40 @@ def fasa_decode_step_noalloc(q, pos, k_cache, v_cache, k_dom, dom_fc, seq_lens, 
 
 
 # ---------------------------------------------------------------- paged cache
-# (a small call's time is the host's: its tensors are checked in one expression
-# without a call each, and what torch gives for every call is looked up once)
-_torch = None
+# (the tensors are checked and their addresses passed in csrc/fasa_torch.cpp: a
+# small call's time is the host's)
+_native = None
 
 
-def _here() -> int:
-    global _torch
-    if _torch is None:
-        import torch
-        _torch = torch
-    return _torch.cuda.current_device()
+def _marshal():
+    """The extension module, its calls bound to libfasa.so's entry points."""
+    global _native
+    if _native is None:
+        import torch  # noqa: F401  (whose libraries it needs)
+        try:
+            from . import _fasa_torch as m
+        except ImportError as e:
+            raise RuntimeError("_fasa_torch.so is missing: build it with "
+                               "`python -m kv_cache_token_tip_gb300.build` (there is no fallback)") from e
+        m.bind(*(ctypes.cast(getattr(lib(), f"fasa_paged_{n}"), ctypes.c_void_p).value
+                 for n in ("append", "attention", "evict")))
+        _native = m
+    return _native
 
 
-def _refuse(here, *tensors):
-    """Raises for the first of (name, tensor, dtype, elements) that does not fit."""
-    for name, x, dtype, count in tensors:
-        if not isinstance(x, _torch.Tensor):
-            raise ValueError(f"{name} must be a tensor")
-        if not x.is_cuda or x.get_device() != here:
-            raise ValueError(f"{name} must be a tensor on the current CUDA device")
-        if x.dtype is not dtype:
-            raise ValueError(f"{name} has dtype {x.dtype}, expected {dtype}")
-        if x.numel() != count:
-            raise ValueError(f"{name} has {x.numel()} elements, expected {count}")
-        if not x.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
+def _where(dims):
+    if not isinstance(dims, FasaPagedDims):
+        raise TypeError("dims must be FasaPagedDims")
+    return ctypes.addressof(dims)
 
 
-def _optional(x, here, dtype, count, name):
-    """Device address of a tensor that may be None."""
-    if x is None:
-        return None
-    try:
-        if x.dtype is dtype and x.numel() == count and x.get_device() == here and x.is_contiguous():
-            return x.data_ptr()
-    except AttributeError:  # not a tensor
-        pass
-    _refuse(here, (name, x, dtype, count))
-
-
-def _room(x, here):
-    """Address and bytes of a workspace."""
-    if not isinstance(x, _torch.Tensor) or not x.is_cuda or x.get_device() != here or not x.is_contiguous():
-        raise ValueError("workspace must be a contiguous tensor on the current CUDA device")
-    return x.data_ptr(), x.numel() * x.element_size()
-
-
-def _on(stream, here):
-    if stream is None:
-        return _torch._C._cuda_getCurrentRawStream(here)
-    return _stream(stream)
-
-
-def _scratch(size, here, stream):
+def _scratch(size, stream):
     """A workspace for one call, kept until the call's stream is past it."""
-    x = _torch.empty(size, dtype=_torch.uint8, device=f"cuda:{here}")
+    import torch
+    x = torch.empty(size, dtype=torch.uint8, device="cuda")
     if stream is not None:
-        x.record_stream(_torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
+        x.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
     return x
-
-
-def _paged_sizes(dims):
-    """Current device, storage dtype, elements of a pool, of the statistics, of the page table."""
-    here = _here()
-    B, H = dims.batch, dims.n_kv_heads
-    slots = dims.max_pages * dims.page_size
-    return (here, _torch.float32 if dims.dtype == FASA_F32 else _torch.bfloat16,
-            dims.n_pages * H * dims.page_size * dims.head_dim, B * H * slots, B * dims.max_pages)
 
 
 def fasa_paged_append(k_new, v_new, pos, k_pages, v_pages, page_table, seq_lens, cu_new=None, weight=None,
@@ -462,32 +429,8 @@ def fasa_paged_append(k_new, v_new, pos, k_pages, v_pages, page_table, seq_lens,
     and v_new [n_tokens, Hkv, d], those of sequence b at cu_new[b] ..
     cu_new[b+1], or one per sequence without cu_new; the first of b gets the
     position pos[b].  seq_lens is not advanced."""
-    here, store, pool, slots, entries = _paged_sizes(dims)
-    i32, B, row = _torch.int32, dims.batch, dims.n_kv_heads * dims.head_dim
-    n_tokens = k_new.numel() // row
-    new = n_tokens * row
-    try:
-        fits = (k_new.dtype is store and v_new.dtype is store and k_pages.dtype is store
-                and v_pages.dtype is store and pos.dtype is i32 and page_table.dtype is i32
-                and seq_lens.dtype is i32 and k_new.numel() == new and v_new.numel() == new
-                and k_pages.numel() == pool and v_pages.numel() == pool and pos.numel() == B
-                and page_table.numel() == entries and seq_lens.numel() == B and k_new.get_device() == here
-                and v_new.get_device() == here and k_pages.get_device() == here and v_pages.get_device() == here
-                and pos.get_device() == here and page_table.get_device() == here
-                and seq_lens.get_device() == here and k_new.is_contiguous() and v_new.is_contiguous()
-                and k_pages.is_contiguous() and v_pages.is_contiguous() and pos.is_contiguous()
-                and page_table.is_contiguous() and seq_lens.is_contiguous())
-    except AttributeError:  # not a tensor
-        fits = False
-    if not fits:
-        _refuse(here, ("k_new", k_new, store, new), ("v_new", v_new, store, new), ("k_pages", k_pages, store, pool),
-                ("v_pages", v_pages, store, pool), ("pos", pos, i32, B), ("page_table", page_table, i32, entries),
-                ("seq_lens", seq_lens, i32, B))
-    st = lib().fasa_paged_append(
-        k_new.data_ptr(), v_new.data_ptr(), n_tokens, _optional(cu_new, here, i32, B + 1, "cu_new"), pos.data_ptr(),
-        page_table.data_ptr(), seq_lens.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(),
-        _optional(weight, here, _torch.float32, slots, "weight"), _optional(token_pos, here, i32, slots, "token_pos"),
-        ctypes.byref(dims), _on(stream, here))
+    st = (_native or _marshal()).append(k_new, v_new, pos, k_pages, v_pages, page_table, seq_lens, cu_new, weight,
+                                        token_pos, _where(dims), None if stream is None else _stream(stream))
     if st:
         _check("fasa_paged_append", st)
 
@@ -504,33 +447,10 @@ def fasa_paged_attention(q, pos, k_pages, v_pages, page_table, seq_lens, out, we
     """Attention of one new token per sequence over its cached tokens; with
     weight, each cached token's softmax weights are added to it.  Without a
     workspace one is allocated here."""
-    here, store, pool, slots, entries = _paged_sizes(dims)
-    i32, f32, B = _torch.int32, _torch.float32, dims.batch
-    heads = B * dims.n_q_heads * dims.head_dim
     if workspace is None:
-        workspace = _scratch(fasa_paged_workspace_size(dims, weight is not None), here, stream)
-    ws, ws_bytes = _room(workspace, here)
-    try:
-        fits = (q.dtype is store and k_pages.dtype is store and v_pages.dtype is store and pos.dtype is i32
-                and page_table.dtype is i32 and seq_lens.dtype is i32 and out.dtype is f32
-                and q.numel() == heads and k_pages.numel() == pool and v_pages.numel() == pool
-                and pos.numel() == B and page_table.numel() == entries and seq_lens.numel() == B
-                and out.numel() == heads and q.get_device() == here and k_pages.get_device() == here
-                and v_pages.get_device() == here and pos.get_device() == here
-                and page_table.get_device() == here and seq_lens.get_device() == here
-                and out.get_device() == here and q.is_contiguous() and k_pages.is_contiguous()
-                and v_pages.is_contiguous() and pos.is_contiguous() and page_table.is_contiguous()
-                and seq_lens.is_contiguous() and out.is_contiguous())
-    except AttributeError:  # not a tensor
-        fits = False
-    if not fits:
-        _refuse(here, ("q", q, store, heads), ("k_pages", k_pages, store, pool), ("v_pages", v_pages, store, pool),
-                ("pos", pos, i32, B), ("page_table", page_table, i32, entries), ("seq_lens", seq_lens, i32, B),
-                ("out", out, f32, heads))
-    st = lib().fasa_paged_attention(
-        q.data_ptr(), pos.data_ptr(), k_pages.data_ptr(), v_pages.data_ptr(), page_table.data_ptr(),
-        seq_lens.data_ptr(), out.data_ptr(), _optional(weight, here, f32, slots, "weight"), ws, ws_bytes,
-        ctypes.byref(dims), _on(stream, here))
+        workspace = _scratch(fasa_paged_workspace_size(dims, weight is not None), stream)
+    st = (_native or _marshal()).attention(q, pos, k_pages, v_pages, page_table, seq_lens, out, weight, workspace,
+                                           _where(dims), None if stream is None else _stream(stream))
     if st:
         _check("fasa_paged_attention", st)
 
@@ -551,37 +471,11 @@ def fasa_paged_evict(weight, token_pos, pos, k_pages, v_pages, page_table, seq_l
     new_lens [B] <- min(seq_lens, keep).  The statistics change in place, or
     go to weight_out and token_pos_out.  Without a workspace one is allocated
     here."""
-    here, store, pool, slots, entries = _paged_sizes(dims)
-    i32, f32, B = _torch.int32, _torch.float32, dims.batch
     if workspace is None:
-        workspace = _scratch(fasa_paged_evict_workspace_size(dims, keep), here, stream)
-    ws, ws_bytes = _room(workspace, here)
-    try:
-        fits = (weight.dtype is f32 and token_pos.dtype is i32 and k_pages.dtype is store
-                and v_pages.dtype is store and pos.dtype is i32 and page_table.dtype is i32
-                and seq_lens.dtype is i32 and new_lens.dtype is i32 and weight.numel() == slots
-                and token_pos.numel() == slots and k_pages.numel() == pool and v_pages.numel() == pool
-                and pos.numel() == B and page_table.numel() == entries and seq_lens.numel() == B
-                and new_lens.numel() == B and weight.get_device() == here and token_pos.get_device() == here
-                and k_pages.get_device() == here and v_pages.get_device() == here and pos.get_device() == here
-                and page_table.get_device() == here and seq_lens.get_device() == here
-                and new_lens.get_device() == here and weight.is_contiguous() and token_pos.is_contiguous()
-                and k_pages.is_contiguous() and v_pages.is_contiguous() and pos.is_contiguous()
-                and page_table.is_contiguous() and seq_lens.is_contiguous() and new_lens.is_contiguous())
-    except AttributeError:  # not a tensor
-        fits = False
-    if not fits:
-        _refuse(here, ("weight", weight, f32, slots), ("token_pos", token_pos, i32, slots),
-                ("k_pages", k_pages, store, pool), ("v_pages", v_pages, store, pool), ("pos", pos, i32, B),
-                ("page_table", page_table, i32, entries), ("seq_lens", seq_lens, i32, B),
-                ("new_lens", new_lens, i32, B))
-    w, t = weight.data_ptr(), token_pos.data_ptr()
-    st = lib().fasa_paged_evict(
-        w, t, pos.data_ptr(), page_table.data_ptr(), seq_lens.data_ptr(), int(keep), int(sinks), int(recent),
-        k_pages.data_ptr(), v_pages.data_ptr(),
-        w if weight_out is None else _optional(weight_out, here, f32, slots, "weight_out"),
-        t if token_pos_out is None else _optional(token_pos_out, here, i32, slots, "token_pos_out"),
-        new_lens.data_ptr(), ws, ws_bytes, ctypes.byref(dims), _on(stream, here))
+        workspace = _scratch(fasa_paged_evict_workspace_size(dims, keep), stream)
+    st = (_native or _marshal()).evict(weight, token_pos, pos, k_pages, v_pages, page_table, seq_lens, keep, new_lens,
+                                       sinks, recent, weight_out, token_pos_out, workspace, _where(dims),
+                                       None if stream is None else _stream(stream))
     if st:
         _check("fasa_paged_evict", st)
 

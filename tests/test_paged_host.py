@@ -308,3 +308,24 @@ def test_oracle_eviction_keeps_every_kept_row_once():
             assert w[0, h, t] == w0[0, h, m]
             assert np.array_equal(kp[table[0, t // 16], h, t % 16], k0[table[0, m // 16], h, m % 16])
         assert np.array_equal(w[1, h], w0[1, h])
+
+
+def test_binding_without_a_gpu_raises():
+    """The compiled marshalling turns every failure into an exception."""
+    import torch
+    from kv_cache_token_tip_gb300 import build, fasa_paged_append, fasa_paged_attention, fasa_paged_evict
+    build.build()
+    x = torch.zeros(8)
+    with pytest.raises(TypeError):
+        fasa_paged_append(x, x, x, x, x, x, x, dims=None)
+    with pytest.raises(TypeError):
+        fasa_paged_attention(x, x, x, x, x, x, x, workspace=x, dims=7)
+    if torch.cuda.is_available():
+        return
+    d = _dims()
+    with pytest.raises((RuntimeError, ValueError)):
+        fasa_paged_append(x, x, x, x, x, x, x, dims=d)
+    with pytest.raises((RuntimeError, ValueError)):
+        fasa_paged_attention(x, x, x, x, x, x, x, workspace=x, dims=d)
+    with pytest.raises((RuntimeError, ValueError)):
+        fasa_paged_evict(x, x, x, x, x, x, x, 4, x, workspace=x, dims=d)
