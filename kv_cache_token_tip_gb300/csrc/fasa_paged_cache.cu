@@ -154,9 +154,11 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
 // One cluster per (sequence, KV head), each CTA a contiguous share of its slots
 // with their keys in shared memory.
 //   1. Keys: held tokens above every weight, NaN below every number, else the
-//      weight's order-preserving bits; the cluster's least and largest key and
-//      its count of held tokens.
-//   2. The keep-th largest key: a histogram of 2048 bins over the range of the
+//      weight's order-preserving bits.
+//   2. Up to EV_FEW tokens too many, as in a decode loop: the last of the order is
+//      found and struck out, one after the other.
+//      More: the cluster's least and largest key and its count of held tokens, then
+//      the keep-th largest key: a histogram of 2048 bins over the range of the
 //      keys, summed over the cluster slice by slice, gives the bin it falls in.
 //      A bin that is kept whole ends it; a bin of few keys is sent to every CTA
 //      and ranked there by (key, slot); else the bin becomes the range.  A single
@@ -171,6 +173,7 @@ constexpr int EV_NT = 512;
 constexpr int EV_NW = EV_NT / 32;
 constexpr int EV_BINS = 2048;
 constexpr int EV_CAND = 512;         // keys of a bin that are ranked one by one
+constexpr int EV_FEW = 4;            // tokens that are struck out one by one (a cluster of 4: 0.9 us each)
 constexpr int EV_MAX_SHARE = 16384;  // slots of a CTA: 64 KB of keys
 constexpr int EV_SHORT_SHARE = 2048;  // (8 heads of 32K: 23.3 us, 24.1 with shares of 4096)
 constexpr int EV_C_MAX = 16;
@@ -181,6 +184,7 @@ struct EvictShared {
   int partial[EV_BINS / 2];  // its sums over some of the CTAs
   unsigned long long cand[EV_CAND];  // key, then ~slot: a larger entry comes first
   int4 facts[EV_C_MAX];      // every CTA's least and largest key and held tokens
+  uint2 last_of_warp[2][EV_NW], last[2][EV_C_MAX];  // the last in the order: key, ~slot
   int slice_sum[EV_C_MAX];
   int tie_sum[EV_C_MAX];
   int2 sums[EV_C_MAX];       // every CTA's holes and movers
@@ -189,10 +193,17 @@ struct EvictShared {
   int bin, above, cnt, n_cand;
 };
 
-// What the selection orders by: held tokens above every weight, NaN below.
+// What the selection orders by: held tokens above every weight, NaN below (and 0 is
+// for what is struck out).
 __device__ __forceinline__ unsigned evict_key(float w, int tp, int sinks, long long recent_after) {
   if (tp < sinks || (long long)tp > recent_after) return 0xffffffffu;
-  return w != w ? 0u : score_key(w);
+  return w != w ? 1u : score_key(w);
+}
+
+// The warp's least pair, by x, then y.
+__device__ __forceinline__ uint2 warp_least(uint2 v) {
+  const unsigned x = __reduce_min_sync(0xffffffffu, v.x);
+  return make_uint2(x, __reduce_min_sync(0xffffffffu, v.x == x ? v.y : 0xffffffffu));
 }
 
 // Exclusive prefix sum over the block (thread order) and the total.
@@ -223,6 +234,8 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
     if (C > 1) cluster_sync();
     else __syncthreads();
   };
+  for (int i = tid; i < EV_BINS; i += EV_NT) sh.hist[i] = 0;
+  if (tid == 0) sh.n_cand = 0;
   paged_go();
   paged_wait();
   int len = p.seq_lens[b];
@@ -281,42 +294,71 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       }
   }
   if (len <= keep) return;
-  mn = __reduce_min_sync(0xffffffffu, mn);
-  mx = __reduce_max_sync(0xffffffffu, mx);
-  held = __reduce_add_sync(0xffffffffu, held);
-  if (lane == 0) sh.red[warp] = make_int4((int)mn, (int)mx, held, 0);
-  __syncthreads();
-  if (C > 1) cluster_wait();
-  if (warp == 0) {  // to every CTA
-    const int4 r = lane < EV_NW ? sh.red[lane] : make_int4(-1, 0, 0, 0);
-    mn = __reduce_min_sync(0xffffffffu, (unsigned)r.x);
-    mx = __reduce_max_sync(0xffffffffu, (unsigned)r.y);
-    held = __reduce_add_sync(0xffffffffu, r.z);
-    if (lane < C) dsmem_st_v4u32(dsmem_map(smem_u32(&sh.facts[rank]), lane), make_uint4(mn, mx, (unsigned)held, 0u));
-  }
-  csync();
-  unsigned lo = 0xffffffffu, hi = 0u;
-  held = 0;
-  for (int r = 0; r < C; ++r) {
-    lo = min(lo, (unsigned)sh.facts[r].x);
-    hi = max(hi, (unsigned)sh.facts[r].y);
-    held += sh.facts[r].z;
-  }
   // 2. kept: keys from `floor` on, and of tie_key the first `need` slots
-  unsigned long long floor = 1ull << 32;
-  unsigned tie_key = 0xffffffffu;
-  int need = 0, kr = keep - held;
-  if (kr < 0) {
-    need = keep;  // more held tokens than room
-  } else if (kr == 0) {
-    floor = 0xffffffffull;
+  unsigned long long floor = 1ull;
+  unsigned tie_key = 0xffffffffu, lo = 0xffffffffu, hi = 0u;
+  int need = 0, kr = 0;
+  if (len - keep <= EV_FEW) {
+    if (C > 1) cluster_wait();
+    __syncthreads();  // (a thread's keys for this are not those it wrote)
+    auto last_of_mine = [&]() {
+      uint2 v = make_uint2(0xffffffffu, 0xffffffffu);
+      for (int i = tid; i < n; i += EV_NT) {
+        const unsigned k = keys[i], s = ~(unsigned)(first + i);
+        if (k != 0u && (k < v.x || (k == v.x && s < v.y))) v = make_uint2(k, s);
+      }
+      return v;
+    };
+    uint2 mine = last_of_mine();
+    for (int round = 0; round < len - keep; ++round) {
+      const int side = round & 1;
+      uint2 v = warp_least(mine);
+      if (lane == 0) sh.last_of_warp[side][warp] = v;
+      __syncthreads();
+      v = warp_least(sh.last_of_warp[side][lane & (EV_NW - 1)]);
+      if (C > 1) {
+        if (tid < C) dsmem_st_v2u32(dsmem_map(smem_u32(&sh.last[side][rank]), tid), v.x, v.y);
+        cluster_sync();
+        v = warp_least(sh.last[side][lane & (C - 1)]);
+      }
+      if (v.x == mine.x && v.y == mine.y) {
+        keys[(int)~v.y - first] = 0u;
+        mine = last_of_mine();
+      }
+    }
+  } else {
+    mn = __reduce_min_sync(0xffffffffu, mn);
+    mx = __reduce_max_sync(0xffffffffu, mx);
+    held = __reduce_add_sync(0xffffffffu, held);
+    if (lane == 0) sh.red[warp] = make_int4((int)mn, (int)mx, held, 0);
+    __syncthreads();
+    if (C > 1) cluster_wait();
+    if (warp == 0) {  // to every CTA
+      const int4 r = lane < EV_NW ? sh.red[lane] : make_int4(-1, 0, 0, 0);
+      mn = __reduce_min_sync(0xffffffffu, (unsigned)r.x);
+      mx = __reduce_max_sync(0xffffffffu, (unsigned)r.y);
+      held = __reduce_add_sync(0xffffffffu, r.z);
+      if (lane < C)
+        dsmem_st_v4u32(dsmem_map(smem_u32(&sh.facts[rank]), lane), make_uint4(mn, mx, (unsigned)held, 0u));
+    }
+    csync();
+    held = 0;
+    for (int r = 0; r < C; ++r) {
+      lo = min(lo, (unsigned)sh.facts[r].x);
+      hi = max(hi, (unsigned)sh.facts[r].y);
+      held += sh.facts[r].z;
+    }
+    kr = keep - held;
+    floor = kr == 0 ? 0xffffffffull : 1ull << 32;
+    if (kr < 0) need = keep;  // more held tokens than room
   }
   const int SL = EV_BINS / C;
-  while (kr > 0) {
+  for (bool again = false; kr > 0; again = true) {
     const int shift = max(0, 32 - __clz(hi - lo) - 11);
-    for (int i = tid; i < EV_BINS; i += EV_NT) sh.hist[i] = 0;
-    if (tid == 0) sh.n_cand = 0;
-    __syncthreads();
+    if (again) {  // (zeros before the first)
+      for (int i = tid; i < EV_BINS; i += EV_NT) sh.hist[i] = 0;
+      __syncthreads();
+    }
     for (int i = tid; i < n; i += EV_NT) {
       const unsigned k = keys[i];
       if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);

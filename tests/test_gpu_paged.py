@@ -606,6 +606,28 @@ def test_evict_shuffled_positions_and_held_overflow():
     assert status() == 0
 
 
+@pytest.mark.parametrize("over", [1, 2, 3, 4, 5])
+@pytest.mark.parametrize("n", [20, 3000, 9000, 33000])
+def test_evict_a_few(n, over):
+    """A few tokens over the bound, on one CTA and on clusters: the order's last
+    ones go, among weights, ties, NaN and held tokens."""
+    import torch
+    for kind in ("plain", "ties", "nan", "held", "struck"):
+        c = Cache("bf16", 3, 2, 1, 64, 16, [n, n - 1, max(n - over, 1)], seed=n + over)
+        c.pos = c.lens - 1
+        if kind == "ties":
+            c.weight.fill_(0.5)
+        elif kind == "nan":   # NaN goes first, the higher slots of it
+            c.weight[:, :, ::max(n // 7, 1)] = float("nan")
+        elif kind == "held":
+            c.token_pos.fill_(0)
+        elif kind == "struck":   # weights whose order ends in the last CTA's share
+            c.weight.copy_(torch.arange(c.cap, 0, -1, device="cuda").float().expand(c.weight.shape))
+        _run_evict(c, n - over, 3, 5 if kind != "held" else 0, apart=True)
+        _run_evict(c, n - over, 3, 5 if kind != "held" else 0)
+    assert status() == 0
+
+
 def test_evict_bound_of_the_whole_cache():
     """A bound that no length can pass needs no workspace and moves nothing."""
     c = Cache("bf16", 2, 2, 1, 64, 16, [64, 10], seed=42)
