@@ -156,7 +156,8 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
 //   1. Keys: held tokens above every weight, NaN below every number, else the
 //      weight's order-preserving bits.
 //   2. Up to EV_FEW tokens too many, as in a decode loop: the last of the order is
-//      found and struck out, one after the other.
+//      found and struck out, one after the other, and the few moves that this leaves
+//      are made at once.
 //      More: the cluster's least and largest key and its count of held tokens, then
 //      the keep-th largest key: a histogram of 2048 bins over the range of the
 //      keys, summed over the cluster slice by slice, gives the bin it falls in.
@@ -166,14 +167,18 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
 //   3. Holes and movers, counted over the cluster, listed in slot order, and the
 //      i-th mover's row copied to the i-th hole by whichever threads come next.
 // Bound by the latency of these steps (cluster barriers, dependent loads): of the
-// 22.8 us that 8 heads of 32K tokens cut to 4096 take, keys and range are 2.6, the
-// choice 6, the lists 3.5 and the copies of 28.7 MB there and back 4 to 9; 256 heads a
-// few tokens over 2048 take 10.1 us.
+// 22.4 us that 8 heads of 32K tokens cut to 4096 take, keys and range are 2.6, the
+// choice 6, the lists 3.5 and the copies of 28.7 MB there and back 4 to 9; 256 heads
+// of 1900 to 2080 tokens cut to 2048 take 9.8 us.
 constexpr int EV_NT = 512;
 constexpr int EV_NW = EV_NT / 32;
 constexpr int EV_BINS = 2048;
 constexpr int EV_CAND = 512;         // keys of a bin that are ranked one by one
-constexpr int EV_FEW = 4;            // tokens that are struck out one by one (a cluster of 4: 0.9 us each)
+// Tokens that are struck out one by one.  One, four, eight over the bound, 8 heads of
+// 4096: 4.1, 5.9, 8.2 us against 8.9, 9.2, 8.9 with the histogram; 64 heads of 4096: 4.5,
+// 6.7, 9.6 against 10.4, 10.8, 11.0; sixteen over: 15.5 and 17.8 against 9.7 and 11.4.
+constexpr int EV_FEW = 8;
+static_assert(EV_FEW * 64 <= EV_NT, "their rows, 512 bytes of K and of V at most, one 16-byte item a thread");
 constexpr int EV_MAX_SHARE = 16384;  // slots of a CTA: 64 KB of keys
 constexpr int EV_SHORT_SHARE = 2048;  // (8 heads of 32K: 23.3 us, 24.1 with shares of 4096)
 constexpr int EV_C_MAX = 16;
@@ -294,10 +299,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       }
   }
   if (len <= keep) return;
-  // 2. kept: keys from `floor` on, and of tie_key the first `need` slots
-  unsigned long long floor = 1ull;
-  unsigned tie_key = 0xffffffffu, lo = 0xffffffffu, hi = 0u;
-  int need = 0, kr = 0;
+  // 2.
   if (len - keep <= EV_FEW) {
     if (C > 1) cluster_wait();
     __syncthreads();  // (a thread's keys for this are not those it wrote)
@@ -310,8 +312,11 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       return v;
     };
     uint2 mine = last_of_mine();
-    for (int round = 0; round < len - keep; ++round) {
-      const int side = round & 1;
+    const int few = len - keep;
+    int gone = 0x7fffffff;  // lane i's: the slot struck out i-th
+#pragma unroll 1
+    for (int i = 0; i < few; ++i) {
+      const int side = i & 1;
       uint2 v = warp_least(mine);
       if (lane == 0) sh.last_of_warp[side][warp] = v;
       __syncthreads();
@@ -321,37 +326,70 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
         cluster_sync();
         v = warp_least(sh.last[side][lane & (C - 1)]);
       }
+      if (lane == i) gone = (int)~v.y;
       if (v.x == mine.x && v.y == mine.y) {
         keys[(int)~v.y - first] = 0u;
         mine = last_of_mine();
       }
     }
-  } else {
-    mn = __reduce_min_sync(0xffffffffu, mn);
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    held = __reduce_add_sync(0xffffffffu, held);
-    if (lane == 0) sh.red[warp] = make_int4((int)mn, (int)mx, held, 0);
-    __syncthreads();
-    if (C > 1) cluster_wait();
-    if (warp == 0) {  // to every CTA
-      const int4 r = lane < EV_NW ? sh.red[lane] : make_int4(-1, 0, 0, 0);
-      mn = __reduce_min_sync(0xffffffffu, (unsigned)r.x);
-      mx = __reduce_max_sync(0xffffffffu, (unsigned)r.y);
-      held = __reduce_add_sync(0xffffffffu, r.z);
-      if (lane < C)
-        dsmem_st_v4u32(dsmem_map(smem_u32(&sh.facts[rank]), lane), make_uint4(mn, mx, (unsigned)held, 0u));
+    // every warp knows them all: the first CTA's move the few rows, 16 bytes a thread,
+    // holes and movers in slot order
+    if (rank != 0) return;
+    const int log2_n16 = 31 - __clz(p.row_bytes / 16), log2_move = log2_n16 + 1;
+    const int move = tid >> log2_move, part = tid & ((1 << log2_move) - 1);
+    int before = 0, hole = keep;
+    for (int i = 0; i < few; ++i) before += __shfl_sync(0xffffffffu, gone, i) < gone;
+    for (int i = 0; i < few; ++i) {
+      const int at = __shfl_sync(0xffffffffu, before, i), x = __shfl_sync(0xffffffffu, gone, i);
+      hole = at == move ? x : hole;
     }
-    csync();
-    held = 0;
-    for (int r = 0; r < C; ++r) {
-      lo = min(lo, (unsigned)sh.facts[r].x);
-      hi = max(hi, (unsigned)sh.facts[r].y);
-      held += sh.facts[r].z;
+    unsigned kept = ((1u << few) - 1u) &
+                    ~__reduce_or_sync(0xffffffffu, lane < few && gone >= keep ? 1u << (gone - keep) : 0u);
+    if (hole >= keep) return;
+    for (int i = 0; i < move; ++i) kept &= kept - 1u;
+    const int mover = keep + __ffs(kept) - 1;
+    const int* table = p.page_table + (size_t)b * p.max_pages;
+    const long long dst = paged_row(table[hole >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, hole);
+    const long long src = paged_row(table[mover >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mover);
+    if (dst >= 0 && src >= 0) {
+      char* pool = static_cast<char*>((part >> log2_n16) ? p.v_pages : p.k_pages) + (part & ((1 << log2_n16) - 1)) * 16;
+      *reinterpret_cast<uint4*>(pool + dst * p.row_bytes) = *reinterpret_cast<const uint4*>(pool + src * p.row_bytes);
+    } else if (part == 0) {
+      atomicOr(p.status, 1);
     }
-    kr = keep - held;
-    floor = kr == 0 ? 0xffffffffull : 1ull << 32;
-    if (kr < 0) need = keep;  // more held tokens than room
+    if (part == 0) {
+      wo[hole] = w[mover];
+      to[hole] = tp[mover];
+    }
+    return;
   }
+  mn = __reduce_min_sync(0xffffffffu, mn);
+  mx = __reduce_max_sync(0xffffffffu, mx);
+  held = __reduce_add_sync(0xffffffffu, held);
+  if (lane == 0) sh.red[warp] = make_int4((int)mn, (int)mx, held, 0);
+  __syncthreads();
+  if (C > 1) cluster_wait();
+  if (warp == 0) {  // to every CTA
+    const int4 r = lane < EV_NW ? sh.red[lane] : make_int4(-1, 0, 0, 0);
+    mn = __reduce_min_sync(0xffffffffu, (unsigned)r.x);
+    mx = __reduce_max_sync(0xffffffffu, (unsigned)r.y);
+    held = __reduce_add_sync(0xffffffffu, r.z);
+    if (lane < C)
+      dsmem_st_v4u32(dsmem_map(smem_u32(&sh.facts[rank]), lane), make_uint4(mn, mx, (unsigned)held, 0u));
+  }
+  csync();
+  // kept: keys from `floor` on, and of tie_key the first `need` slots
+  unsigned tie_key = 0xffffffffu, lo = 0xffffffffu, hi = 0u;
+  int need = 0;
+  held = 0;
+  for (int r = 0; r < C; ++r) {
+    lo = min(lo, (unsigned)sh.facts[r].x);
+    hi = max(hi, (unsigned)sh.facts[r].y);
+    held += sh.facts[r].z;
+  }
+  int kr = keep - held;
+  unsigned long long floor = kr == 0 ? 0xffffffffull : 1ull << 32;
+  if (kr < 0) need = keep;  // more held tokens than room
   const int SL = EV_BINS / C;
   for (bool again = false; kr > 0; again = true) {
     const int shift = max(0, 32 - __clz(hi - lo) - 11);

@@ -628,6 +628,27 @@ def test_evict_a_few(n, over):
     assert status() == 0
 
 
+@pytest.mark.parametrize("dtype,d,page", [("bf16", 64, 16), ("bf16", 128, 64), ("f32", 64, 16), ("f32", 128, 32)])
+@pytest.mark.parametrize("over", [1, 3, 8, 9])
+def test_evict_a_few_rows(dtype, d, page, over):
+    """The few rows that move, of every type and size: the tokens that go lie before
+    the bound in any order, behind it, or both; then with pages that are not there."""
+    import torch
+    for kind in ("before", "descending", "behind", "both", "bad"):
+        c = Cache(dtype, 2, 3, 1, d, page, [300, 300 - over], max_pages=-(-304 // page), seed=over)
+        c.pos = c.lens - 1
+        keep = 300 - over
+        c.weight.copy_(1 + torch.rand(c.weight.shape, generator=c.gen, device="cuda"))
+        for i in range(over):
+            slot = {"before": 3 + 17 * i, "descending": 290 - over - 17 * i, "behind": 299 - i,
+                    "both": 299 - i if i % 2 else 40 + i, "bad": 20 * i}[kind]
+            c.weight[:, :, slot] = 0.1 + 0.01 * i
+        if kind == "bad":
+            c.table[0, 0], c.table[0, (300 - over) // page] = -1, c.dims.n_pages
+        _run_evict(c, keep, 0, 0)
+        assert status() == (1 if kind == "bad" else 0)
+
+
 def test_evict_bound_of_the_whole_cache():
     """A bound that no length can pass needs no workspace and moves nothing."""
     c = Cache("bf16", 2, 2, 1, 64, 16, [64, 10], seed=42)
