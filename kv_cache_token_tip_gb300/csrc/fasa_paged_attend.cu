@@ -460,9 +460,10 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
     if (line.groups(b) == 0)
       for (int i = tid; i < p.Hq * D; i += 32 * M::WARPS) p.out[(size_t)b * p.Hq * D + i] = 0.f;
   // few parts lie on as many SMs
-  const int parts = line.parts(p.parts), c = warp * gridDim.x + blockIdx.x;
-  if (c >= parts) return;
-  const int edge = line.part_begin(parts, c + (lane & 1));  // both at once
+  const PagedCuts cuts = line.cuts(p.parts);
+  const int c = warp * gridDim.x + blockIdx.x;
+  if (c >= cuts.n) return;
+  const int edge = line.part_begin(cuts, c + (lane & 1));  // both at once
   const int r0 = __shfl_sync(0xffffffffu, edge, 0), r1 = __shfl_sync(0xffffffffu, edge, 1);
   if (r0 == r1) return;
 
@@ -631,16 +632,26 @@ __device__ float joined_lse(const PagedAttendParams& p, int R, int GD, int c0, i
 // Tasks: a slice of the output of a unit that was cut; a task goes by its unit,
 // or, where there are more units than parts, by the part the unit begins in.
 // Rows of lanes take the unit's records in turn, a lane four floats of each,
-// then the rows' sums meet in order.  Where tasks are many a warp takes one (128
-// floats, its own row); where they are few, and so a unit's parts many, a block
-// does, with its warps as rows, or four rows of 8 lanes to a warp (32 floats).
-// With weights, each warp then adds what its share of the line's tokens gets, by
-// itself: blocks' barriers there cost 2 us of the 9 a step of eight 4K caches had.
+// then the rows' sums meet in order.  A warp takes a task (128 floats, its own
+// row), or where a unit's parts are many a block does, with its warps as rows, or
+// four rows of 8 lanes to a warp (32 floats).
+// With weights (GM: the heads that fit the registers, 0 without), each warp then adds
+// what its share of the line's tokens gets, by itself; where the tasks take a quarter
+// of the warps or less the others do that meanwhile (16 sequences of 500 tokens, 21%:
+// 16.7 us, 19.9 with a share for all; 64 of them, 42%: 32.0 and 26.7).  What of a warp's
+// share depends on the lengths alone is worked out before the wait (1K tokens: 9.0 us
+// against 8.2).
 // A block is small enough to wait for the first kernel beside its CTAs.
-template <int D, bool WEIGHTS>
-__global__ void __launch_bounds__(JN_NT, WEIGHTS ? 2 : 3)
+// With weights a block takes a task where a unit has more parts than this: 8 units of
+// 4K tokens, 76 parts each, 12.3 us against 15.9 by warps; 64 of 4K, 9 parts each, 29.4
+// against 28.6; 16 of 64K, 38 parts each, 93.1 against 91.0.  (Without weights, where
+// nothing else fills the warps, while there are less than two tasks to a block.)
+constexpr int JN_MANY = 40;
+template <int D, int GM>
+__global__ void __launch_bounds__(JN_NT, GM ? 2 : 3)
     paged_join_kernel(const __grid_constant__ PagedAttendParams p) {
   constexpr int NT = JN_NT, NW = NT / 32;
+  constexpr bool WEIGHTS = GM > 0;
   extern __shared__ unsigned words[];
   __shared__ float4 so[NT];
   __shared__ float2 sml[NT];
@@ -651,11 +662,13 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 2 : 3)
   // (the lengths are older than the first kernel, which waited before it let this one begin)
   make_line<NT>(p, words, scan, false);
   const PagedLine line{words, p.B, p.Hkv};
-  const int parts = line.parts(p.parts), total = line.total();
+  const PagedCuts cuts = line.cuts(p.parts);
+  const int parts = cuts.n, total = line.total();
   const int units = p.B * p.Hkv, blocks = gridDim.x;
   const bool by_unit = units <= parts;
   const int most = (by_unit ? units : max(parts - 1, 0)) * ((G * D + 127) / 128);
-  const bool team = most < 2 * blocks, fine = team && by_unit && units * (G * D / 32) <= blocks;
+  const bool team = WEIGHTS ? by_unit && parts > JN_MANY * units : most < 2 * blocks;
+  const bool fine = !WEIGHTS && team && by_unit && units * (G * D / 32) <= blocks;
   const int lanes = fine ? 8 : 32, width = 4 * lanes, slices = (G * D + width - 1) / width;
   const int tasks = (by_unit ? units : max(parts - 1, 0)) * slices;
   const int nrows = team ? NT / lanes : 1, row = team ? tid / lanes : 0, at = tid & (lanes - 1);
@@ -674,19 +687,36 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 2 : 3)
       sg.x = line.before(b) * p.Hkv + h * n;
       sg.at();
     } else {
-      const int edge = line.part_begin(parts, of + 1);
+      const int edge = line.part_begin(cuts, of + 1);
       if (edge <= 0 || edge >= total) return false;
       sg.start(line, edge - 1, edge);
       sg.at();
       if (sg.unit_end <= edge) return false;
     }
-    c0 = sg.first_part(parts);
-    c1 = sg.last_part(parts);
+    c0 = sg.first_part(cuts);
+    c1 = sg.last_part(cuts);
     return by_unit ? c0 < c1 : c0 == of;
   };
   const int step = team ? blocks : blocks * NW;
   int task = team ? blockIdx.x : warp * blocks + blockIdx.x;
   bool cut_here = task < tasks && task_at(task);
+  // the warps that add weights, and this one's share of the line
+  int warps = blocks * NW, w = blockIdx.x * NW + warp;
+  if (WEIGHTS && 4 * tasks <= (team ? blocks : warps)) {
+    w = team ? w - tasks * NW : warp * blocks + blockIdx.x - tasks;
+    warps -= team ? tasks * NW : tasks;
+  }
+  PagedSegments share;
+  int s0 = 0, s1 = 0;  // the parts of its unit
+  bool more = WEIGHTS && w >= 0;
+  if (more) {
+    share.start(line, cut(total, warps, w), cut(total, warps, w + 1));
+    more = share.at();
+    if (more) {
+      s0 = share.first_part(cuts);
+      s1 = share.last_part(cuts);
+    }
+  }
   paged_go();
   paged_wait();
   for (; task < tasks; task += step, cut_here = task < tasks && task_at(task)) {
@@ -763,38 +793,33 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 2 : 3)
           make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
     }
   }
-  if constexpr (!WEIGHTS) return;
-  const int warps = blocks * NW, w = blockIdx.x * NW + warp;
-  sg.start(line, cut(total, warps, w), cut(total, warps, w + 1));
-  for (; sg.at(); sg.next()) {
-    const int unit = sg.unit();
-    c0 = sg.first_part(parts);
-    c1 = sg.last_part(parts);
+  if constexpr (WEIGHTS) while (more) {
+    const int unit = share.unit();
     // four tokens a lane: a group's slots, and so its logits and weights, are all
     // there (those behind the end are -inf and get nothing); the first are under way
     // while the parts' sums are joined
-    const int t0 = (sg.x - sg.unit_begin) * PAGED_GROUP, t1 = (sg.seg_end() - sg.unit_begin) * PAGED_GROUP;
-    const int tokens = line.tokens(sg.b);
+    const int t0 = (share.x - share.unit_begin) * PAGED_GROUP, t1 = (share.seg_end() - share.unit_begin) * PAGED_GROUP;
+    const int tokens = line.tokens(share.b);
     const float* z = p.logits + (size_t)unit * G * p.T_cap;
     float* weight = p.weight + (size_t)unit * p.T_cap;
-    float4 zg[G_MAX], old;
+    float4 zg[GM], old;
     auto load = [&](int t) {
       const float* zt = z + (size_t)(t & -PAGED_GROUP) * G + (t & (PAGED_GROUP - 1));
 #pragma unroll
-      for (int g = 0; g < G_MAX; ++g)
+      for (int g = 0; g < GM; ++g)
         if (g < G) zg[g] = ld_cg(reinterpret_cast<const float4*>(zt + g * PAGED_GROUP));
       old = *reinterpret_cast<const float4*>(weight + t);
     };
     int t = t0 + 4 * lane;
     if (t < t1) load(t);
-    const float mine = c0 == c1 ? ld_cg(p.lse + (size_t)unit * G + min(lane, G - 1)) : joined_lse(p, R, G * D, c0, c1);
+    const float mine = s0 == s1 ? ld_cg(p.lse + (size_t)unit * G + min(lane, G - 1)) : joined_lse(p, R, G * D, s0, s1);
     __syncwarp();  // (the last unit's are read)
     if (lane < G) lse[warp][lane] = mine;
     __syncwarp();
     while (t < t1) {
       float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int g = 0; g < G_MAX; ++g)
+      for (int g = 0; g < GM; ++g)
         if (g < G) {
           const float e = lse[warp][g];
           a.x += exp2f(zg[g].x - e);
@@ -819,6 +844,12 @@ __global__ void __launch_bounds__(JN_NT, WEIGHTS ? 2 : 3)
     const uintptr_t z1 = reinterpret_cast<uintptr_t>(z + (size_t)t1 * G) & ~(uintptr_t)127;
     for (uintptr_t at = ((z0 + 127) & ~(uintptr_t)127) + 128 * lane; at < z1; at += 128 * 32)
       asm volatile("discard.global.L2 [%0], 128;" ::"l"(at) : "memory");
+    share.next();
+    more = share.at();
+    if (more) {
+      s0 = share.first_part(cuts);
+      s1 = share.last_part(cuts);
+    }
   }
 }
 
@@ -885,8 +916,8 @@ cudaError_t launch(PagedAttendParams& p, int sms, cudaStream_t s) {
   e = paged_behind(paged_attend_kernel<D, M>, grid, 32 * M::WARPS, smem, 0, s, p, km, vm);
   if (e != cudaSuccess) return e;
   const size_t line = (p.B + 1) * 4;
-  return p.weight ? paged_behind(paged_join_kernel<D, true>, 2 * sms, JN_NT, line, 0, s, p)
-                  : paged_behind(paged_join_kernel<D, false>, sms, JN_NT, line, 0, s, p);
+  if (!p.weight) return paged_behind(paged_join_kernel<D, 0>, sms, JN_NT, line, 0, s, p);
+  return paged_behind(p.G <= 4 ? paged_join_kernel<D, 4> : paged_join_kernel<D, 8>, 2 * sms, JN_NT, line, 0, s, p);
 }
 
 }  // namespace

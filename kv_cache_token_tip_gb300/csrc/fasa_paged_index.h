@@ -54,6 +54,29 @@ FASA_HD unsigned paged_word(int before, int len) {
   return (unsigned)before | (unsigned)(paged_groups(len) * PAGED_GROUP - len) << 28;
 }
 
+// The line's cuts into n <= PAGED_MAX_PARTS parts, in cost.  (What a cut needs is worked
+// out once: a unit's parts are looked up by every warp that reads or joins it.)
+struct PagedCuts {
+  int n, q, r;
+  float part, inv;  // parts per cost, 1 / n
+
+  FASA_HD PagedCuts(int cost, int parts)
+      : n(parts), q(cost / (parts > 0 ? parts : 1)), r(cost - q * parts), part(over((float)parts, (float)cost)),
+        inv(over(1.f, (float)parts)) {}
+  // (within 2^-22 of a / b is enough; b = 0 is an empty line, where nothing is looked up)
+  static FASA_HD float over(float a, float b) {
+#ifdef __CUDA_ARCH__
+    return __fdividef(a, b);
+#else
+    return b > 0.f ? a / b : 0.f;
+#endif
+  }
+  // Where part c begins, floor(cost * c / n): r c < 2^21 is exact in fp32, and the half
+  // keeps the product further from a whole number (0.5 / n = 3.9e-4 at least) than it can
+  // be off (1.5 n 2^-23 = 2.3e-4 at most).
+  FASA_HD int begin(int c) const { return q * c + (int)(((float)(r * c) + 0.5f) * inv); }
+};
+
 struct PagedLine {
   const unsigned* w;
   int B, Hkv;
@@ -76,18 +99,16 @@ struct PagedLine {
   // (32-bit arithmetic and no wide divisions: every CTA does this before its first copy)
   FASA_HD int cost_before(int b) const { return Hkv * (before(b) + PAGED_UNIT_COST * b); }
   FASA_HD int cost() const { return cost_before(B); }
-  // Parts of the line, at most `grid`.
-  FASA_HD int parts(int grid) const {
-    const int most = (cost() + PAGED_PART_COST - 1) / PAGED_PART_COST;
-    return most < grid ? most : grid;
+  // Its cuts into parts, at most `grid`.
+  FASA_HD PagedCuts cuts(int grid) const {
+    const int all = cost(), most = (all + PAGED_PART_COST - 1) / PAGED_PART_COST;
+    return PagedCuts(all, most < grid ? most : grid);
   }
-  // Where part c of n begins, in cost.
-  FASA_HD int cost_begin(int n, int c) const { return cut(cost(), n, c); }
-  // Where part c of n begins on the line (0 <= c <= n; a part may be empty): the
-  // first group that lies at that cost or behind it.
-  FASA_HD int part_begin(int n, int c) const {
-    const int y = cost_begin(n, c);
-    if (c >= n) return total();
+  // Where part c begins on the line (0 <= c <= n; a part may be empty): the first
+  // group that lies at that cost or behind it.
+  FASA_HD int part_begin(const PagedCuts& cuts, int c) const {
+    const int y = cuts.begin(c);
+    if (c >= cuts.n) return total();
     int lo = 0, hi = B;  // cost_before(lo) <= y < cost_before(hi)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -98,13 +119,13 @@ struct PagedLine {
     const int h = rem / (g + PAGED_UNIT_COST), off = rem - h * (g + PAGED_UNIT_COST);
     return before(lo) * Hkv + h * g + (off > PAGED_UNIT_COST ? off - PAGED_UNIT_COST : 0);
   }
-  // The part of n that holds group g of unit (b, h).
-  FASA_HD int part_of(int n, int b, int h, int g) const {
+  // The part that holds group g of unit (b, h).
+  FASA_HD int part_of(const PagedCuts& cuts, int b, int h, int g) const {
     const int y = cost_before(b) + h * (groups(b) + PAGED_UNIT_COST) + PAGED_UNIT_COST + g;
-    int c = (int)((float)y * ((float)n / (float)cost()));  // at most one off
-    c = c < 0 ? 0 : (c >= n ? n - 1 : c);
-    while (cost_begin(n, c) > y) --c;
-    while (c + 1 < n && cost_begin(n, c + 1) <= y) ++c;
+    int c = (int)((float)y * cuts.part);  // at most one off
+    c = c < cuts.n ? c : cuts.n - 1;
+    if (cuts.begin(c) > y) --c;
+    else if (c + 1 < cuts.n && cuts.begin(c + 1) <= y) ++c;
     return c;
   }
 };
@@ -137,8 +158,10 @@ struct PagedSegments {
   }
   FASA_HD int unit() const { return b * line.Hkv + h; }
   FASA_HD int seg_end() const { return unit_end < end ? unit_end : end; }
-  FASA_HD int first_part(int n) const { return line.part_of(n, b, h, 0); }
-  FASA_HD int last_part(int n) const { return line.part_of(n, b, h, unit_end - unit_begin - 1); }
+  FASA_HD int first_part(const PagedCuts& cuts) const { return line.part_of(cuts, b, h, 0); }
+  FASA_HD int last_part(const PagedCuts& cuts) const {
+    return line.part_of(cuts, b, h, unit_end - unit_begin - 1);
+  }
   FASA_HD void next() {
     x = seg_end();
     if (x == unit_end && ++h == line.Hkv) {

@@ -143,13 +143,14 @@ static int check(const std::vector<int>& lens, int Hkv, int grid) {
     groups += paged_groups(lens[b]);
   }
   CHECK(line.total() == groups * Hkv);
-  const int n = line.parts(grid);
+  const PagedCuts cuts = line.cuts(grid);
+  const int n = cuts.n;
   CHECK(n >= 1 && n <= grid);
-  CHECK(line.part_begin(n, 0) == 0 && line.part_begin(n, n) == line.total());
+  CHECK(line.part_begin(cuts, 0) == 0 && line.part_begin(cuts, n) == line.total());
   std::vector<int> seen(B * Hkv, 0), last(B * Hkv, -1);
   long long most = 0;
   for (int c = 0; c < n; ++c) {
-    const int r0 = line.part_begin(n, c), r1 = line.part_begin(n, c + 1);
+    const int r0 = line.part_begin(cuts, c), r1 = line.part_begin(cuts, c + 1);
     CHECK(r0 <= r1);
     PagedSegments s;
     s.start(line, r0, r1);
@@ -159,13 +160,13 @@ static int check(const std::vector<int>& lens, int Hkv, int grid) {
       CHECK(s.unit_end - s.unit_begin == line.groups(s.b));
       const int u = s.unit();
       CHECK(s.x - s.unit_begin == seen[u]);
-      for (int x = s.x; x < s.seg_end(); ++x) CHECK(line.part_of(n, s.b, s.h, x - s.unit_begin) == c);
+      for (int x = s.x; x < s.seg_end(); ++x) CHECK(line.part_of(cuts, s.b, s.h, x - s.unit_begin) == c);
       if (seen[u]) CHECK(last[u] == c - 1);
-      else CHECK(s.first_part(n) == c);
+      else CHECK(s.first_part(cuts) == c);
       seen[u] += s.seg_end() - s.x;
       last[u] = c;
-      if (seen[u] == line.groups(s.b)) CHECK(s.last_part(n) == c);
-      else CHECK(s.last_part(n) > c);
+      if (seen[u] == line.groups(s.b)) CHECK(s.last_part(cuts) == c);
+      else CHECK(s.last_part(cuts) > c);
       cost += s.seg_end() - s.x + (s.x == s.unit_begin ? PAGED_UNIT_COST : 0);
     }
     most = cost > most ? cost : most;
@@ -195,12 +196,13 @@ int main() {
     const std::vector<unsigned> w = words(std::vector<int>(B, PAGED_MAX_SLOTS - 1));
     const PagedLine line{w.data(), B, Hkv};
     CHECK(line.total() == B * Hkv * g && line.total() > 0 && line.tokens(B - 1) == PAGED_MAX_SLOTS - 1);
-    const int n = line.parts(PAGED_MAX_PARTS);
-    CHECK(n == PAGED_MAX_PARTS && line.part_begin(n, n) == line.total());
+    const PagedCuts cuts = line.cuts(PAGED_MAX_PARTS);
+    const int n = cuts.n;
+    CHECK(n == PAGED_MAX_PARTS && line.part_begin(cuts, n) == line.total());
     for (int c = 0; c < n; ++c) {
       PagedSegments s;
-      s.start(line, line.part_begin(n, c), line.part_begin(n, c + 1));
-      CHECK(s.at() && line.part_of(n, s.b, s.h, s.x - s.unit_begin) == c);
+      s.start(line, line.part_begin(cuts, c), line.part_begin(cuts, c + 1));
+      CHECK(s.at() && line.part_of(cuts, s.b, s.h, s.x - s.unit_begin) == c);
     }
   }
   CHECK(paged_groups(0) == 0 && paged_groups(1) == 1 && paged_groups(16) == 1 && paged_groups(17) == 2);
