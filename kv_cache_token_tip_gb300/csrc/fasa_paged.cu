@@ -164,7 +164,7 @@ int fasa_paged_evict_workspace_size(const fasa_paged_dims_t* dims, int32_t keep,
   const int st = check_paged_dims(dims);
   if (st) return st;
   if (keep < 1) return FASA_ERR_INVALID_ARG;
-  *bytes = up((size_t)dims->batch * dims->n_kv_heads * most_moves(dims, keep) * 2 * sizeof(int2));
+  *bytes = up((size_t)dims->batch * dims->n_kv_heads * most_moves(dims, keep) * sizeof(PagedMove));
   return FASA_OK;
 }
 
@@ -207,7 +207,7 @@ int fasa_paged_evict(const float* weight, const int32_t* token_pos, const int32_
   p.keep = keep;
   p.sinks = sinks;
   p.recent = recent;
-  p.moves = static_cast<int2*>(workspace);
+  p.moves = static_cast<PagedMove*>(workspace);
   p.move_cap = most_moves(dims, keep);
   p.row_bytes = dims->head_dim * (dims->dtype == FASA_F32 ? 4 : 2);
   const cudaError_t e = launch_paged_evict(p, sms, reinterpret_cast<cudaStream_t>(stream));

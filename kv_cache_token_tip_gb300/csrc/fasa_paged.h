@@ -59,6 +59,11 @@ struct PagedAttendParams : PagedCommon {
   int drop_group;              // test hook: this group of part 0 is never copied (-1: none)
 };
 
+// A token that an eviction moves: row in the pool and slot, the hole's and its own.
+struct alignas(16) PagedMove {
+  int2 hole, mover;
+};
+
 struct PagedEvictParams : PagedCommon {
   const float* weight;
   const int* token_pos;
@@ -68,7 +73,7 @@ struct PagedEvictParams : PagedCommon {
   int* token_pos_out;
   int* new_lens;
   int keep, sinks, recent;
-  int2* moves;     // [units][2][move_cap]: rows, then slots, that tokens move to and come from
+  PagedMove* moves;  // [units][move_cap]
   int move_cap;
   int row_bytes;   // of a K or V row
 };
@@ -114,9 +119,9 @@ __device__ __forceinline__ float ld_cg(const float* p) {
   asm volatile("ld.global.cg.f32 %0, [%1];" : "=f"(v) : "l"(p));
   return v;
 }
-__device__ __forceinline__ int2 ld_cg(const int2* p) {
-  int2 v;
-  asm volatile("ld.global.cg.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+__device__ __forceinline__ int4 ld_cg(const int4* p) {
+  int4 v;
+  asm volatile("ld.global.cg.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
 __device__ __forceinline__ float4 ld_cg(const float4* p) {

@@ -164,12 +164,13 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
 //      A bin that is kept whole ends it; a bin of few keys is sent to every CTA
 //      and ranked there by (key, slot); else the bin becomes the range.  A single
 //      key held by many slots (ties) goes by slot order.
-//   3. Holes and movers, counted over the cluster, listed in slot order, and the
-//      i-th mover's row copied to the i-th hole by whichever threads come next.
+//   3. Holes and movers, counted over the cluster and listed in slot order; the i-th
+//      mover's row goes to the i-th hole by CTA i % C, which takes its part of the
+//      list into shared memory first.
 // Bound by the latency of these steps (cluster barriers, dependent loads): of the
-// 22.4 us that 8 heads of 32K tokens cut to 4096 take, keys and range are 2.6, the
-// choice 6, the lists 3.5 and the copies of 28.7 MB there and back 4 to 9; 256 heads
-// of 1900 to 2080 tokens cut to 2048 take 9.8 us.
+// 21.4 us that 8 heads of 32K tokens cut to 4096 take, keys and range are 2.6, the
+// choice 6, the lists 3.5 and the copies of 28.7 MB there and back 4 to 8; 256 heads
+// of 1900 to 2080 tokens cut to 2048 take 10.0 us.
 constexpr int EV_NT = 512;
 constexpr int EV_NW = EV_NT / 32;
 constexpr int EV_BINS = 2048;
@@ -179,15 +180,21 @@ constexpr int EV_CAND = 512;         // keys of a bin that are ranked one by one
 // 6.7, 9.6 against 10.4, 10.8, 11.0; sixteen over: 15.5 and 17.8 against 9.7 and 11.4.
 constexpr int EV_FEW = 8;
 static_assert(EV_FEW * 64 <= EV_NT, "their rows, 512 bytes of K and of V at most, one 16-byte item a thread");
+constexpr int EV_LIST = 1536;        // moves in a CTA's shared memory, where its histogram was
 constexpr int EV_MAX_SHARE = 16384;  // slots of a CTA: 64 KB of keys
 constexpr int EV_SHORT_SHARE = 2048;  // (8 heads of 32K: 23.3 us, 24.1 with shares of 4096)
 constexpr int EV_C_MAX = 16;
 
 struct EvictShared {
-  int hist[EV_BINS];
-  int slice[EV_BINS];        // this CTA's slice of the cluster's histogram
-  int partial[EV_BINS / 2];  // its sums over some of the CTAs
-  unsigned long long cand[EV_CAND];  // key, then ~slot: a larger entry comes first
+  union {
+    struct {
+      int hist[EV_BINS];
+      int slice[EV_BINS];        // this CTA's slice of the cluster's histogram
+      int partial[EV_BINS / 2];  // its sums over some of the CTAs
+      unsigned long long cand[EV_CAND];  // key, then ~slot: a larger entry comes first
+    };
+    PagedMove moves[EV_LIST];  // once the choice is made: those that this CTA makes
+  };
   int4 facts[EV_C_MAX];      // every CTA's least and largest key and held tokens
   uint2 last_of_warp[2][EV_NW], last[2][EV_C_MAX];  // the last in the order: key, ~slot
   int slice_sum[EV_C_MAX];
@@ -540,9 +547,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
     }
     moves_n += sh.sums[r].x;
   }
-  // a move: the hole's and the mover's row, and their slots
-  int2* rows = p.moves + (size_t)u * 2 * p.move_cap;
-  int2* slots = rows + p.move_cap;
+  PagedMove* listed = p.moves + (size_t)u * p.move_cap;
   if (holes + movers) {
     walk([&](int t, bool hole, bool mover) {
       if (!hole && !mover) return;
@@ -553,37 +558,44 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       const int row = (int)paged_row(page, p.n_pages, p.Hkv, h, p.log2_page, t);
       if (row < 0) atomicOr(p.status, 1);
       const int at = hole ? hole_at++ : mover_at++;
-      (hole ? rows[at].x : rows[at].y) = row;
-      (hole ? slots[at].x : slots[at].y) = t;
+      (hole ? listed[at].hole : listed[at].mover) = make_int2(row, t);
     });
   }
   csync();  // (and no CTA reads another's shared memory behind it)
-  // 4. the copies: 16 bytes a thread, several of them on the way
-  constexpr int U = 6;
+  // 4. the copies: 16 bytes a thread, several of them on the way (32K to 4096: 22.1 us
+  // with four, 21.4 with five or seven, which are slower where few rows move)
+  constexpr int U = 5;
   const int log2_n16 = 31 - __clz(p.row_bytes / 16), log2_move = log2_n16 + 1;
-  const int items = moves_n << log2_move, stride = C * EV_NT;  // (at most 2^17 moves of 2^6 items)
-  const int part = tid & ((1 << log2_move) - 1);               // the same for all of a thread's items
+  const int part = tid & ((1 << log2_move) - 1);  // the same for all of a thread's items
   char* pool = static_cast<char*>((part >> log2_n16) ? p.v_pages : p.k_pages) + (part & ((1 << log2_n16) - 1)) * 16;
-  for (int q0 = rank * EV_NT + tid; q0 < items; q0 += U * stride) {
-    int2 mv[U];
-    uint4 v[U];
+  const int log2_C = 31 - __clz(C), own = (moves_n + C - 1 - rank) >> log2_C;  // move i is CTA i % C's
+  for (int m0 = 0; m0 < own; m0 += EV_LIST) {
+    const int n_moves = min(own - m0, EV_LIST);
+    if (m0) __syncthreads();  // the last ones are read
+    for (int i = tid; i < n_moves; i += EV_NT)
+      *reinterpret_cast<int4*>(&sh.moves[i]) =
+          ld_cg(reinterpret_cast<const int4*>(listed + ((size_t)(m0 + i) << log2_C) + rank));
+    __syncthreads();
+    const int items = n_moves << log2_move;
+    for (int q0 = tid; q0 < items; q0 += U * EV_NT) {
+      uint4 v[U];
+      int into[U];
 #pragma unroll
-    for (int j = 0; j < U; ++j) {
-      const int q = q0 + j * stride;
-      mv[j] = q < items ? ld_cg(rows + (q >> log2_move)) : make_int2(-1, -1);
+      for (int j = 0; j < U; ++j) {
+        const int q = q0 + j * EV_NT;
+        const PagedMove m = q < items ? sh.moves[q >> log2_move] : PagedMove{make_int2(-1, 0), make_int2(-1, 0)};
+        into[j] = m.mover.x >= 0 ? m.hole.x : -1;
+        if (into[j] >= 0) v[j] = ld_cg(reinterpret_cast<const uint4*>(pool + (long long)m.mover.x * p.row_bytes));
+      }
+#pragma unroll
+      for (int j = 0; j < U; ++j)
+        if (into[j] >= 0) *reinterpret_cast<uint4*>(pool + (long long)into[j] * p.row_bytes) = v[j];
     }
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (mv[j].x >= 0 && mv[j].y >= 0)
-        v[j] = ld_cg(reinterpret_cast<const uint4*>(pool + (long long)mv[j].y * p.row_bytes));
-#pragma unroll
-    for (int j = 0; j < U; ++j)
-      if (mv[j].x >= 0 && mv[j].y >= 0) *reinterpret_cast<uint4*>(pool + (long long)mv[j].x * p.row_bytes) = v[j];
-  }
-  for (int i = rank * EV_NT + tid; i < moves_n; i += stride) {
-    const int2 mv = ld_cg(slots + i);
-    wo[mv.x] = w[mv.y];
-    to[mv.x] = tp[mv.y];
+    for (int i = tid; i < n_moves; i += EV_NT) {
+      const PagedMove m = sh.moves[i];
+      wo[m.hole.y] = w[m.mover.y];
+      to[m.hole.y] = tp[m.mover.y];
+    }
   }
 }
 

@@ -540,6 +540,8 @@ EVICTS = [
     # clusters of 1 with long shares, of 2, and of 16 with a share near the most
     ("bf16", 40, 4, 64, 64, [5000 - 61 * (i % 9) for i in range(40)], 4700, 4, 32),
     ("f32", 30, 4, 64, 16, [2500 + i for i in range(30)], 2510, 1, 0), ("bf16", 1, 1, 64, 256, [230001], 1200, 3, 99),
+    # more moves than a CTA lists at once, on a cluster of 16 and on one CTA
+    ("bf16", 1, 1, 64, 256, [200003], 100001, 4, 64), ("bf16", 40, 4, 64, 64, [6850 - i for i in range(40)], 3400, 4, 32),
 ]
 
 
