@@ -18,7 +18,7 @@
 // own in shared memory that TMA fills (one copy of 16 rows for K, one for V, in
 // the 128-byte swizzle: no bank conflicts), page by page wherever the pages
 // lie, and no warp waits for another: what a unit costs beside its bytes is
-// hidden by the other seven warps of the SM.
+// hidden by the other warps of the SM.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -107,10 +107,10 @@ template <int D, bool PACK>
 struct MathBf16 {
   using T = __nv_bfloat16;
   static constexpr int CTAS = 2;  // per SM
-  // Warps of a CTA.  Two with six stages each read 128 dims at 99% of the copy
-  // rate (352.8 us for 2.38 GB) and leave half the records to join that four with
-  // three do (359.9 us); a group of 64 dims is half the bytes for the same
-  // latency and wants the four (64 short sequences: 20.0 us against 25.5).
+  // Warps of a CTA.  Two with six stages each read 128 dims at the copy
+  // rate (344.4 us for 2.38 GB) and leave half the records to join that four with
+  // three do (350.6 us); a group of 64 dims is half the bytes for the same
+  // latency and wants the four (64 short sequences: 17.7 us against 23.6).
   static constexpr int WARPS = D == 128 ? 2 : 4;
   static constexpr int RAW = G_MAX * D * 2;  // the next unit's raw query, fetched while this one is read
   static constexpr int MT = D / 16;
@@ -268,8 +268,8 @@ struct MathF32 {
   using T = float;
   static constexpr int CTAS = 1;
   // Warps of a CTA: as many as hide the arithmetic's latency, then stages.  At 268 MB:
-  // 4 heads of 64 dims 84.9 us with eight warps, 120.8 with four; 8 heads of 128 dims
-  // 108.0 and 119.2 (one stage against three); 4 heads of 128 dims 87.6 and 83.5.
+  // 4 heads of 64 dims 83.6 us with eight warps, 117.1 with four; 8 heads of 128 dims
+  // 106.2 and 116.8 (one stage against three); 4 heads of 128 dims 86.7 and 82.8.
   static constexpr int WARPS = D == 128 && GP == 4 ? 4 : 8;
   static constexpr int RAW = 0;  // (no room to fetch ahead: the raw query goes where the turned one stays)
   static constexpr int E = D / 32;
@@ -468,9 +468,9 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
   if (r0 == r1) return;
 
   // K and V are read once: they make way in L2 for what the join reads again (32K
-  // tokens 28.4 us without, 26.5 with; one token of eight 4K caches 56.0 and 49.2);
-  // a stream of many times L2 with no logits runs 2% faster as it comes (2.38 GB:
-  // 356.5 us against 364.2)
+  // tokens 27.4 us without, 26.2 with; one token of eight 4K caches 40.4 and 36.5);
+  // a stream of many times L2 with no logits runs up to 1% faster as it comes (2.38 GB:
+  // 349.4 us against 353.1)
   unsigned long long policy;
   if (p.weight || (long long)line.total() * P::STAGE < (512ll << 20))
     asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(policy));
@@ -478,13 +478,10 @@ __global__ void __launch_bounds__(32 * M::WARPS, M::CTAS)
     asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(policy));
   // The logits stay in L2 as far as they can, and the join drops them there once it
   // has read them: neither K and V push them out nor do they go to memory after use
-  // (four sequences of 128K, 67 MB of logits: 381 us without, 345.6 with); a few MB
-  // stay without being asked to, and faster (eight 4K caches: 49.8 us asked, 48.9 not)
+  // (four sequences of 128K, 67 MB of logits: 352 us, 364 stored as they come, 374
+  // without the drop; eight of 4K 28.4, 28.5, 28.1)
   Logits logits;
-  if ((long long)line.total() * PAGED_GROUP * G * 4 > (8ll << 20))
-    asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(logits.policy));
-  else
-    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(logits.policy));
+  asm volatile("createpolicy.fractional.L2::evict_last.b64 %0, 1.0;" : "=l"(logits.policy));
   // Lane i holds the pool row of group (batch of 32) + i of this part.
   const int mine = r1 - r0;
   int rows = -1, issued = 0, landed = 0;

@@ -18,11 +18,11 @@ namespace {
 // so that a lane turns the same pairs of every head: the warp computes a token's
 // cosines and sines once.  The rows are on their way meanwhile.  Bound by the bytes for a
 // prompt (16.5K tokens of 8 heads, 129 MB: 23.9 us, 80% of the copy rate), by the chain
-// of loads (table, length, page) for a token a sequence (32 sequences: 2.2 us).
+// of loads (table, length, page) for a token a sequence (32 sequences: 2.0 us).
 constexpr int AP_NT = 128;
 constexpr int AP_U = 2;              // rows of K and of V a lane has on the way
-// From this many tokens a warp takes all heads of one: 16.5K tokens 24.8 us against
-// 47.1 with two heads a warp; 32 tokens 2.97 us against 2.61.
+// From this many tokens a warp takes all heads of one: 16.5K tokens 23.8 us against
+// 34.0 with two heads a warp; 32 tokens 2.6 us against 2.0.
 constexpr int AP_MANY = 2048;
 
 // Sequence of new token x, and which of its tokens it is; false for padding (used:
@@ -182,7 +182,7 @@ constexpr int EV_FEW = 8;
 static_assert(EV_FEW * 64 <= EV_NT, "their rows, 512 bytes of K and of V at most, one 16-byte item a thread");
 constexpr int EV_LIST = 1536;        // moves in a CTA's shared memory, where its histogram was
 constexpr int EV_MAX_SHARE = 16384;  // slots of a CTA: 64 KB of keys
-constexpr int EV_SHORT_SHARE = 2048;  // (8 heads of 32K: 23.3 us, 24.1 with shares of 4096)
+constexpr int EV_SHORT_SHARE = 2048;  // (8 heads of 32K: 21.3 us, 26.9 with shares of 4096)
 constexpr int EV_C_MAX = 16;
 
 struct EvictShared {

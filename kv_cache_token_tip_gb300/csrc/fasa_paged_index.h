@@ -23,9 +23,9 @@ namespace fasa {
 
 constexpr int PAGED_GROUP = 16;         // tokens per group
 // What a unit costs beside its groups, in groups (64 sequences of 0 to 1000 tokens:
-// 30.9 us at 0, 25.5 at 1, 25.3 at 2, 26.0 at 4), and the least that a part costs while
-// there is as much (one sequence of 1024 tokens: 12.3 us at 4, 10.7 at 2, 9.3 at 1).
-constexpr int PAGED_UNIT_COST = 1;
+// 22.5 us at 0, 17.7 at 1, 17.5 at 2, 18.0 at 4), and the least that a part costs while
+// there is as much (one sequence of 1024 tokens: 8.9 us at 4, 7.7 at 2, 7.4 at 1).
+constexpr int PAGED_UNIT_COST = 2;
 constexpr int PAGED_PART_COST = 1;
 constexpr int PAGED_MAX_PARTS = 1280;   // parts the workspace has room for
 constexpr int PAGED_MAX_BATCH = 2048;   // the lengths' prefix sums sit in shared memory
