@@ -37,39 +37,52 @@ namespace {
 constexpr int JN_NT = 256;  // threads of a join block
 
 // The line's words, in shared memory.  Every thread of the block calls it; ends
-// with a barrier.  scan: NT / 32 words.
+// with a barrier.  scan: NT / 32 words.  A batch of more than NT sequences has its
+// lengths read at once and a run of them to a thread (1024 of 48 tokens: 53.9 us, 55.2
+// with NT at a time).
 template <int NT>
 __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  int base = 0;
-  for (int b0 = 0; b0 < p.B; b0 += NT) {
-    const int b = b0 + tid;
-    int len = 0;
-    if (b < p.B) {
-      len = p.seq_lens[b];
-      if (report && (len < 0 || len > p.T_cap)) atomicOr(p.status, 1);
-      len = min(max(len, 0), p.T_cap);
-    }
-    const int n = paged_groups(len);
-    int incl = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
+  auto length = [&](int b) {
+    const int len = p.seq_lens[b];
+    if (report && (len < 0 || len > p.T_cap)) atomicOr(p.status, 1);
+    return min(max(len, 0), p.T_cap);
+  };
+  const bool many = p.B > NT;
+  const int run = ((p.B + NT - 1) / NT) | 1;  // (odd: its threads' words lie in as many banks)
+  const int b0 = tid * run, b1 = min(p.B, b0 + run);
+  int len = 0, groups = 0;
+  if (!many) {
+    if (tid < p.B) len = length(tid);
+    groups = paged_groups(len);
+  } else {
+#pragma unroll 8
+    for (int b = tid; b < p.B; b += NT) w[b] = (unsigned)length(b);
     __syncthreads();
-    int before = base;
-#pragma unroll
-    for (int v = 0; v < NT / 32; ++v) {
-      const int s = scan[v];
-      before += v < warp ? s : 0;
-      base += s;
-    }
-    if (b < p.B) w[b] = paged_word(before + incl - n, len);
-    if (b == p.B - 1) w[p.B] = paged_word(before + incl, 0);
-    __syncthreads();
+    for (int b = b0; b < b1; ++b) groups += paged_groups((int)w[b]);
   }
+  int incl = groups;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int before = incl - groups;
+#pragma unroll
+  for (int v = 0; v < NT / 32; ++v) before += v < warp ? scan[v] : 0;
+  if (tid == NT - 1) w[p.B] = paged_word(before + groups, 0);
+  if (!many) {
+    if (tid < p.B) w[tid] = paged_word(before, len);
+  } else {
+    for (int b = b0; b < b1; ++b) {
+      len = (int)w[b];
+      w[b] = paged_word(before, len);
+      before += paged_groups(len);
+    }
+  }
+  __syncthreads();
 }
 
 // x0, x1 as bf16 pairs hi + mid + lo: 24 bits and more of each.
