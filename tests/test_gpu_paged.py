@@ -843,3 +843,48 @@ def test_binding_refuses_what_does_not_fit():
     with pytest.raises(ValueError):
         fasa_paged_append(k, k[:2], c.pos, c.kp, c.vp, c.table, c.lens, cu_new=new[:1], **a)
     assert status() == 0
+
+
+FIRST_CALLS = """
+import torch
+from kv_cache_token_tip_gb300 import fasa_paged_append, fasa_paged_attention, fasa_paged_evict
+from kv_cache_token_tip_gb300.fasa import FasaPagedDims
+B, H, G, d, page, n = 2, 2, 4, 128, 16, 6
+dims = FasaPagedDims(B, H * G, H, d, page, B * n, n, 1, 1e4)
+z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device="cuda")
+kp, vp = z(B * n, H, page, d, t=torch.bfloat16), z(B * n, H, page, d, t=torch.bfloat16)
+table = torch.arange(B * n, dtype=torch.int32, device="cuda").view(B, n)
+lens, pos, new = z(B, t=torch.int32), z(B, t=torch.int32), z(B, t=torch.int32)
+w, tp = z(B, H, n * page), z(B, H, n * page, t=torch.int32)
+k, v = torch.ones(B, H, d, device="cuda").bfloat16(), torch.ones(B, H, d, device="cuda").bfloat16()
+q, out = torch.ones(B, H * G, d, device="cuda").bfloat16(), z(B, H * G, d)
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    fasa_paged_append(k, v, pos, kp, vp, table, lens, weight=w, token_pos=tp, dims=dims)
+    lens.add_(1)
+    fasa_paged_attention(q, pos, kp, vp, table, lens, out, weight=w, dims=dims)
+    fasa_paged_evict(w, tp, pos, kp, vp, table, lens, 4, new, dims=dims)
+    lens.copy_(new)
+    pos.add_(1)
+for _ in range(9):
+    g.replay()
+torch.cuda.synchronize()
+assert lens.tolist() == [4, 4] and pos.tolist() == [9, 9]
+# out = o / l with o = l = the sum of at most 5 softmax weights, V being 1.  o: three products and a sum of four of
+# the tensor cores, which round towards zero (4 * 2^-23), then at most 5 parts (5 * 2^-24); l: at most 7 sums of a
+# part's lanes and 5 parts (12 * 2^-24); the division and the product 3 * 2^-24.  28 * 2^-24 in all.
+assert (out - 1).abs().max() <= 28 * 2.0 ** -24, out
+print("fine")
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    """Nothing of the library has run before: what it sets up on first use does
+    not end the capture, and the graph's steps go on from replay to replay."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr[-2000:]
