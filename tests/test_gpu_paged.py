@@ -125,6 +125,10 @@ SHAPES = [
     ("bf16", 300, 8, 1, 64, 16, [(i * 37) % 90 for i in range(300)]),
     ("f32", 260, 8, 2, 64, 16, [(i * 41) % 70 for i in range(260)]),
     ("bf16", 200, 8, 5, 128, 16, [(i * 29) % 60 for i in range(200)]),
+    # cut units joined by warps, beside those that add weights, and by blocks
+    ("bf16", 8, 8, 4, 128, 64, [700 + 31 * i for i in range(8)]), ("bf16", 16, 8, 4, 64, 32, [250 + 17 * i for i in range(16)]),
+    ("bf16", 12, 4, 7, 128, 16, [900 - 61 * i for i in range(12)]), ("f32", 4, 4, 8, 128, 64, [1500, 0, 1100, 1501]),
+    ("f32", 24, 4, 6, 64, 16, [300 + 13 * i for i in range(24)]),
     # the largest batch
     ("bf16", 2048, 1, 2, 64, 16, [(i * 31) % 40 for i in range(2048)]),
 ]
@@ -249,6 +253,50 @@ def test_attention_equal_calls_give_equal_bits_and_streams():
     torch.cuda.synchronize()
     for _, _, w, o in runs:
         assert torch.equal(o, out) and torch.equal(w, w1)
+
+
+def test_calls_of_two_threads():
+    """Caches of another type, head size and rotation base each, a stream each:
+    what the library keeps between calls is not mixed up."""
+    import threading
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_append, fasa_paged_evict
+
+    def steps(c, k, v):
+        outs = []
+        for i in range(25):
+            fasa_paged_append(k, v, c.pos, c.kp, c.vp, c.table, c.lens, weight=c.weight, token_pos=c.token_pos,
+                              dims=c.dims)
+            c.lens.add_(1)
+            outs.append(c.attend().clone())
+            fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, c.lens, 300, new := c.lens.clone(),
+                             sinks=2, recent=9, dims=c.dims)
+            c.lens.copy_(new)
+            c.pos.add_(1)
+        return torch.stack(outs)
+
+    def make(i):
+        c = Cache(*(("bf16", 3, 4, 4, 128, 16, [299, 300, 7]) if i else ("f32", 2, 2, 8, 64, 32, [298, 40])),
+                  max_pages=24 if i else 12, theta=1e4 if i else 1e6, seed=60 + i)
+        k, v = (torch.randn(c.B, c.Hkv, c.d, generator=c.gen, device="cuda").to(c.q.dtype) for _ in range(2))
+        return c, k, v
+
+    alone = [steps(*make(i)) for i in range(2)]
+    made, got = [make(i) for i in range(2)], [None, None]
+    torch.cuda.synchronize()
+
+    def run(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got[i] = steps(*made[i])
+        s.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(g, a) for g, a in zip(got, alone)) and status() == 0
 
 
 def test_attention_in_graphs_that_share_a_workspace():
