@@ -171,19 +171,22 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
 // 21.4 us that 8 heads of 32K tokens cut to 4096 take, keys and range are 2.6, the
 // choice 6, the lists 3.5 and the copies of 28.7 MB there and back 4 to 8; 256 heads
 // of 1900 to 2080 tokens cut to 2048 take 10.0 us.
-constexpr int EV_NT = 512;
-constexpr int EV_NW = EV_NT / 32;
+constexpr int EV_NW = 16;            // most warps of a CTA
 constexpr int EV_BINS = 2048;
 constexpr int EV_CAND = 512;         // keys of a bin that are ranked one by one
 // Tokens that are struck out one by one.  One, four, eight over the bound, 8 heads of
 // 4096: 4.1, 5.9, 8.2 us against 8.9, 9.2, 8.9 with the histogram; 64 heads of 4096: 4.5,
 // 6.7, 9.6 against 10.4, 10.8, 11.0; sixteen over: 15.5 and 17.8 against 9.7 and 11.4.
 constexpr int EV_FEW = 8;
-static_assert(EV_FEW * 64 <= EV_NT, "their rows, 512 bytes of K and of V at most, one 16-byte item a thread");
 constexpr int EV_LIST = 1536;        // moves in a CTA's shared memory, where its histogram was
 constexpr int EV_MAX_SHARE = 16384;  // slots of a CTA: 64 KB of keys
 constexpr int EV_SHORT_SHARE = 2048;  // (8 heads of 32K: 21.3 us, 26.9 with shares of 4096)
 constexpr int EV_C_MAX = 16;
+// More CTAs to an SM than this, and they have 256 threads, not 512, so that twice as
+// many units are under way: 384, 512, 2048 units one token over 2048: 6.0, 6.0, 25.5 us
+// against 7.8, 8.7, 35.7; 512 of 4096 halved, which is copies: 118 against 110; 256
+// units have no SM to share: 5.5 against 4.8.
+constexpr int EV_NARROW = 2;
 
 struct EvictShared {
   union {
@@ -219,6 +222,7 @@ __device__ __forceinline__ uint2 warp_least(uint2 v) {
 }
 
 // Exclusive prefix sum over the block (thread order) and the total.
+template <int NT>
 __device__ int block_scan(int x, int* scan, int& total) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int incl = x;
@@ -229,14 +233,15 @@ __device__ int block_scan(int x, int* scan, int& total) {
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  const int v = lane < EV_NW ? scan[lane] : 0;
+  const int v = lane < NT / 32 ? scan[lane] : 0;
   const int below = __reduce_add_sync(0xffffffffu, lane < warp ? v : 0);
   total = __reduce_add_sync(0xffffffffu, v);
   __syncthreads();
   return below + incl - x;
 }
 
-__global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_constant__ PagedEvictParams p) {
+template <int NT>
+__global__ void __launch_bounds__(NT, 1024 / NT) paged_evict_kernel(const __grid_constant__ PagedEvictParams p) {
   extern __shared__ __align__(16) unsigned keys[];
   __shared__ EvictShared sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -246,7 +251,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
     if (C > 1) cluster_sync();
     else __syncthreads();
   };
-  for (int i = tid; i < EV_BINS; i += EV_NT) sh.hist[i] = 0;
+  for (int i = tid; i < EV_BINS; i += NT) sh.hist[i] = 0;
   if (tid == 0) sh.n_cand = 0;
   paged_go();
   paged_wait();
@@ -272,7 +277,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   const long long after = (long long)p.pos[b] - p.recent;
   unsigned mn = 0xffffffffu, mx = 0u;
   int held = 0;
-  for (int i = 4 * tid; i < n; i += 4 * EV_NT) {
+  for (int i = 4 * tid; i < n; i += 4 * NT) {
     const int t = first + i;
     const float4 wv = *reinterpret_cast<const float4*>(w + t);
     const int4 tv = *reinterpret_cast<const int4*>(tp + t);
@@ -312,7 +317,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
     __syncthreads();  // (a thread's keys for this are not those it wrote)
     auto last_of_mine = [&]() {
       uint2 v = make_uint2(0xffffffffu, 0xffffffffu);
-      for (int i = tid; i < n; i += EV_NT) {
+      for (int i = tid; i < n; i += NT) {
         const unsigned k = keys[i], s = ~(unsigned)(first + i);
         if (k != 0u && (k < v.x || (k == v.x && s < v.y))) v = make_uint2(k, s);
       }
@@ -327,7 +332,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       uint2 v = warp_least(mine);
       if (lane == 0) sh.last_of_warp[side][warp] = v;
       __syncthreads();
-      v = warp_least(sh.last_of_warp[side][lane & (EV_NW - 1)]);
+      v = warp_least(sh.last_of_warp[side][lane & (NT / 32 - 1)]);
       if (C > 1) {
         if (tid < C) dsmem_st_v2u32(dsmem_map(smem_u32(&sh.last[side][rank]), tid), v.x, v.y);
         cluster_sync();
@@ -343,30 +348,34 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
     // holes and movers in slot order
     if (rank != 0) return;
     const int log2_n16 = 31 - __clz(p.row_bytes / 16), log2_move = log2_n16 + 1;
-    const int move = tid >> log2_move, part = tid & ((1 << log2_move) - 1);
-    int before = 0, hole = keep;
-    for (int i = 0; i < few; ++i) before += __shfl_sync(0xffffffffu, gone, i) < gone;
-    for (int i = 0; i < few; ++i) {
-      const int at = __shfl_sync(0xffffffffu, before, i), x = __shfl_sync(0xffffffffu, gone, i);
-      hole = at == move ? x : hole;
-    }
-    unsigned kept = ((1u << few) - 1u) &
-                    ~__reduce_or_sync(0xffffffffu, lane < few && gone >= keep ? 1u << (gone - keep) : 0u);
-    if (hole >= keep) return;
-    for (int i = 0; i < move; ++i) kept &= kept - 1u;
-    const int mover = keep + __ffs(kept) - 1;
+    const int part = tid & ((1 << log2_move) - 1);
+    char* pool = static_cast<char*>((part >> log2_n16) ? p.v_pages : p.k_pages) + (part & ((1 << log2_n16) - 1)) * 16;
     const int* table = p.page_table + (size_t)b * p.max_pages;
-    const long long dst = paged_row(table[hole >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, hole);
-    const long long src = paged_row(table[mover >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mover);
-    if (dst >= 0 && src >= 0) {
-      char* pool = static_cast<char*>((part >> log2_n16) ? p.v_pages : p.k_pages) + (part & ((1 << log2_n16) - 1)) * 16;
-      *reinterpret_cast<uint4*>(pool + dst * p.row_bytes) = *reinterpret_cast<const uint4*>(pool + src * p.row_bytes);
-    } else if (part == 0) {
-      atomicOr(p.status, 1);
-    }
-    if (part == 0) {
-      wo[hole] = w[mover];
-      to[hole] = tp[mover];
+    int before = 0;
+    for (int i = 0; i < few; ++i) before += __shfl_sync(0xffffffffu, gone, i) < gone;
+    const unsigned all_kept = ((1u << few) - 1u) &
+                              ~__reduce_or_sync(0xffffffffu, lane < few && gone >= keep ? 1u << (gone - keep) : 0u);
+    for (int m0 = 0; m0 < few; m0 += NT >> log2_move) {
+      const int move = m0 + (tid >> log2_move);
+      int hole = keep;
+      for (int i = 0; i < few; ++i) {
+        const int at = __shfl_sync(0xffffffffu, before, i), x = __shfl_sync(0xffffffffu, gone, i);
+        hole = at == move ? x : hole;
+      }
+      if (hole >= keep) continue;
+      unsigned kept = all_kept;
+      for (int i = 0; i < move; ++i) kept &= kept - 1u;
+      const int mover = keep + __ffs(kept) - 1;
+      const long long dst = paged_row(table[hole >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, hole);
+      const long long src = paged_row(table[mover >> p.log2_page], p.n_pages, p.Hkv, h, p.log2_page, mover);
+      if (dst >= 0 && src >= 0)
+        *reinterpret_cast<uint4*>(pool + dst * p.row_bytes) = *reinterpret_cast<const uint4*>(pool + src * p.row_bytes);
+      else if (part == 0)
+        atomicOr(p.status, 1);
+      if (part == 0) {
+        wo[hole] = w[mover];
+        to[hole] = tp[mover];
+      }
     }
     return;
   }
@@ -377,7 +386,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   __syncthreads();
   if (C > 1) cluster_wait();
   if (warp == 0) {  // to every CTA
-    const int4 r = lane < EV_NW ? sh.red[lane] : make_int4(-1, 0, 0, 0);
+    const int4 r = lane < NT / 32 ? sh.red[lane] : make_int4(-1, 0, 0, 0);
     mn = __reduce_min_sync(0xffffffffu, (unsigned)r.x);
     mx = __reduce_max_sync(0xffffffffu, (unsigned)r.y);
     held = __reduce_add_sync(0xffffffffu, r.z);
@@ -401,10 +410,10 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   for (bool again = false; kr > 0; again = true) {
     const int shift = max(0, 32 - __clz(hi - lo) - 11);
     if (again) {  // (zeros before the first)
-      for (int i = tid; i < EV_BINS; i += EV_NT) sh.hist[i] = 0;
+      for (int i = tid; i < EV_BINS; i += NT) sh.hist[i] = 0;
       __syncthreads();
     }
-    for (int i = tid; i < n; i += EV_NT) {
+    for (int i = tid; i < n; i += NT) {
       const unsigned k = keys[i];
       if (k >= lo && k <= hi) atomicAdd(&sh.hist[(k - lo) >> shift], 1);
     }
@@ -413,10 +422,10 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
     // of the CTAs
     int sum = 0;
     if (C == 1) {
-      for (int i = tid; i < SL; i += EV_NT) sum += sh.slice[i] = sh.hist[i];
+      for (int i = tid; i < SL; i += NT) sum += sh.slice[i] = sh.hist[i];
     } else {
-      const int np = max(1, EV_NT / SL), part = tid / SL;  // (SL 1024: two bins a thread)
-      for (int i = tid - part * SL; i < SL; i += EV_NT) {
+      const int np = max(1, NT / SL), part = tid / SL;  // (SL 1024: two bins a thread)
+      for (int i = tid - part * SL; i < SL; i += NT) {
         const uint32_t at = smem_u32(&sh.hist[rank * SL + i]);
         int v = 0;
 #pragma unroll 4
@@ -424,7 +433,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
         sh.partial[part * SL + i] = v;
       }
       __syncthreads();
-      for (int i = tid; i < SL; i += EV_NT) {
+      for (int i = tid; i < SL; i += NT) {
         int v = 0;
         for (int q = 0; q < np; ++q) v += sh.partial[q * SL + i];
         sh.slice[i] = v;
@@ -432,23 +441,23 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       }
     }
     int total;
-    block_scan(sum, sh.scan, total);
+    block_scan<NT>(sum, sh.scan, total);
     if (tid < C) dsmem_st_u32(dsmem_map(smem_u32(&sh.slice_sum[rank]), tid), (uint32_t)total);
     csync();
     // the slice, then the bin of it, that holds the kr-th key from the top
     int above = 0, owner = C - 1;
     while (owner > 0 && above + sh.slice_sum[owner] < kr) above += sh.slice_sum[owner--];
-    const int per = max(1, SL / EV_NT);
-    int c[EV_BINS / EV_NT], mine = 0;
+    const int per = max(1, SL / NT);
+    int c[EV_BINS / NT], mine = 0;
 #pragma unroll
-    for (int j = 0; j < EV_BINS / EV_NT; ++j) {
+    for (int j = 0; j < EV_BINS / NT; ++j) {
       const int at = SL - 1 - (tid * per + j);
       c[j] = j < per && at >= 0 ? (int)dsmem_ld_u32(dsmem_map(smem_u32(&sh.slice[max(at, 0)]), owner)) : 0;
       mine += c[j];
     }
-    above += block_scan(mine, sh.scan, total);
+    above += block_scan<NT>(mine, sh.scan, total);
 #pragma unroll
-    for (int j = 0; j < EV_BINS / EV_NT; ++j) {
+    for (int j = 0; j < EV_BINS / NT; ++j) {
       if (above < kr && kr <= above + c[j]) {
         sh.bin = owner * SL + SL - 1 - (tid * per + j);
         sh.above = above;
@@ -470,7 +479,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       // kept (largest key) or not (least)
       const int before = (int)__reduce_add_sync(
           0xffffffffu, lane < rank ? dsmem_ld_u32(dsmem_map(smem_u32(&sh.hist[bin]), lane)) : 0u);
-      for (int i = tid; i < n; i += EV_NT) {
+      for (int i = tid; i < n; i += NT) {
         const unsigned k = keys[i];
         if (k >= b0 && k <= b1) {
           const int at = before + atomicAdd(&sh.n_cand, 1);
@@ -479,7 +488,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
         }
       }
       csync();
-      for (int i = tid; i < cnt; i += EV_NT) {
+      for (int i = tid; i < cnt; i += NT) {
         const unsigned long long e = sh.cand[i];
         const int slot = (int)~(unsigned)e;
         if (slot < first || slot >= first + n) continue;
@@ -502,7 +511,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   }
   __syncthreads();
   // 3. holes and movers: a thread has a run of slots
-  const int run = ((n + EV_NT - 1) / EV_NT + 3) & ~3;
+  const int run = ((n + NT - 1) / NT + 3) & ~3;
   const int i0 = min(n, tid * run), i1 = min(n, i0 + run);
   const int* table = p.page_table + (size_t)b * p.max_pages;
   int page_at = -1, page = -1;  // the table's entry at page_at, for the run's first slot ahead
@@ -514,7 +523,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   if (need) {
     for (int i = i0; i < i1; ++i) ties += keys[i] == tie_key;
     const int mine = ties;
-    ties = block_scan(mine, sh.scan, total);
+    ties = block_scan<NT>(mine, sh.scan, total);
     if (tid < C) dsmem_st_u32(dsmem_map(smem_u32(&sh.tie_sum[rank]), tid), (uint32_t)total);
     csync();
     for (int r = 0; r < rank; ++r) ties += sh.tie_sum[r];
@@ -535,7 +544,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
     movers += mover;
   });
   // (both counts of a CTA are below 2^15)
-  const int packed = block_scan(holes | movers << 16, sh.scan, total);
+  const int packed = block_scan<NT>(holes | movers << 16, sh.scan, total);
   if (tid < C)
     dsmem_st_v2u32(dsmem_map(smem_u32(&sh.sums[rank]), tid), (uint32_t)(total & 0xffff), (uint32_t)(total >> 16));
   csync();
@@ -572,17 +581,17 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
   for (int m0 = 0; m0 < own; m0 += EV_LIST) {
     const int n_moves = min(own - m0, EV_LIST);
     if (m0) __syncthreads();  // the last ones are read
-    for (int i = tid; i < n_moves; i += EV_NT)
+    for (int i = tid; i < n_moves; i += NT)
       *reinterpret_cast<int4*>(&sh.moves[i]) =
           ld_cg(reinterpret_cast<const int4*>(listed + ((size_t)(m0 + i) << log2_C) + rank));
     __syncthreads();
     const int items = n_moves << log2_move;
-    for (int q0 = tid; q0 < items; q0 += U * EV_NT) {
+    for (int q0 = tid; q0 < items; q0 += U * NT) {
       uint4 v[U];
       int into[U];
 #pragma unroll
       for (int j = 0; j < U; ++j) {
-        const int q = q0 + j * EV_NT;
+        const int q = q0 + j * NT;
         const PagedMove m = q < items ? sh.moves[q >> log2_move] : PagedMove{make_int2(-1, 0), make_int2(-1, 0)};
         into[j] = m.mover.x >= 0 ? m.hole.x : -1;
         if (into[j] >= 0) v[j] = ld_cg(reinterpret_cast<const uint4*>(pool + (long long)m.mover.x * p.row_bytes));
@@ -591,7 +600,7 @@ __global__ void __launch_bounds__(EV_NT, 2) paged_evict_kernel(const __grid_cons
       for (int j = 0; j < U; ++j)
         if (into[j] >= 0) *reinterpret_cast<uint4*>(pool + (long long)into[j] * p.row_bytes) = v[j];
     }
-    for (int i = tid; i < n_moves; i += EV_NT) {
+    for (int i = tid; i < n_moves; i += NT) {
       const PagedMove m = sh.moves[i];
       wo[m.hole.y] = w[m.mover.y];
       to[m.hole.y] = tp[m.mover.y];
@@ -614,6 +623,23 @@ cudaError_t launch_append(const PagedAppendParams& p, int sms, cudaStream_t s) {
                       p, heads);
 }
 
+template <int NT>
+cudaError_t launch_evict(const PagedEvictParams& p, int C, int smem, cudaStream_t s) {
+  static std::atomic<unsigned long long> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(done.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(paged_evict_kernel<NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_MAX_SHARE * 4);
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(paged_evict_kernel<NT>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    done.fetch_or(bit, std::memory_order_release);
+  }
+  return paged_behind(paged_evict_kernel<NT>, (unsigned)(p.B * p.Hkv * C), NT, (size_t)smem, (unsigned)C, s, p);
+}
+
 }  // namespace
 
 cudaError_t launch_paged_append(const PagedAppendParams& p, int head_dim, bool bf16, int sms, cudaStream_t s) {
@@ -631,19 +657,8 @@ cudaError_t launch_paged_evict(const PagedEvictParams& p, int sms, cudaStream_t 
          (p.T_cap > C * EV_MAX_SHARE || (p.T_cap > C * EV_SHORT_SHARE && units * C < sms)))
     C *= 2;
   const int smem = min(((p.T_cap + C - 1) / C + 3) & ~3, EV_MAX_SHARE) * 4;
-  static std::atomic<unsigned long long> done{0};
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!(done.load(std::memory_order_acquire) & bit)) {
-    e = cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, EV_MAX_SHARE * 4);
-    if (e == cudaSuccess)
-      e = cudaFuncSetAttribute(paged_evict_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
-    if (e != cudaSuccess) return e;
-    done.fetch_or(bit, std::memory_order_release);
-  }
-  return paged_behind(paged_evict_kernel, (unsigned)(units * C), EV_NT, (size_t)smem, (unsigned)C, s, p);
+  const bool narrow = (long long)units * C > EV_NARROW * sms;
+  return narrow ? launch_evict<256>(p, C, smem, s) : launch_evict<512>(p, C, smem, s);
 }
 
 }  // namespace fasa

@@ -590,6 +590,9 @@ EVICTS = [
     ("f32", 30, 4, 64, 16, [2500 + i for i in range(30)], 2510, 1, 0), ("bf16", 1, 1, 64, 256, [230001], 1200, 3, 99),
     # more moves than a CTA lists at once, on a cluster of 16 and on one CTA
     ("bf16", 1, 1, 64, 256, [200003], 100001, 4, 64), ("bf16", 40, 4, 64, 64, [6850 - i for i in range(40)], 3400, 4, 32),
+    # more units than SMs can hold of the wide CTAs, a few and many tokens over
+    ("bf16", 85, 4, 128, 16, [300 + i % 21 for i in range(85)], 305, 4, 32),
+    ("f32", 90, 4, 128, 16, [280 - i for i in range(90)], 270, 0, 3), ("bf16", 170, 2, 64, 64, [900 - i for i in range(170)], 333, 4, 32),
 ]
 
 
