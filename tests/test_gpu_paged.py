@@ -702,6 +702,23 @@ def test_evict_a_few_rows(dtype, d, page, over):
         assert status() == (1 if kind == "bad" else 0)
 
 
+@pytest.mark.parametrize("B,cap", [(80, 16400), (20, 70016), (10, 140000)])
+def test_evict_many_clusters(B, cap):
+    """Clusters of 2, 8 and 16, more CTAs than two to an SM, of caches with room for
+    far more than they hold (table entries behind the end are not pages)."""
+    import torch
+    for over in (1, 7, 150):
+        c = Cache("bf16", B, 2, 1, 64, 16, [600 - i for i in range(B)], seed=over)
+        table = torch.full((B, cap // 16), -1, dtype=torch.int32, device="cuda")
+        table[:, :c.table.shape[1]] = c.table
+        c.table, c.dims.max_pages, c.cap = table, cap // 16, cap
+        c.weight = torch.exp(torch.randn(B, 2, cap, generator=c.gen, device="cuda"))
+        c.token_pos = torch.arange(cap, dtype=torch.int32, device="cuda").expand(B, 2, cap).contiguous()
+        c.pos = c.lens - 1
+        _run_evict(c, 600 - over, 4, 32, apart=over == 7)
+        assert status() == 0
+
+
 def test_evict_bound_of_the_whole_cache():
     """A bound that no length can pass needs no workspace and moves nothing."""
     c = Cache("bf16", 2, 2, 1, 64, 16, [64, 10], seed=42)
