@@ -159,6 +159,17 @@ def _stream(stream):
     return stream.cuda_stream
 
 
+def _scratch(size, stream, device="cuda"):
+    """A workspace for one call, allocated as memory of the call's stream: what
+    was freed on another stream may still be in use there, and what this call
+    leaves is handed out again behind it."""
+    import torch
+    if stream is None:
+        return torch.empty(size, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream):
+        return torch.empty(size, dtype=torch.uint8, device=device)
+
+
 def _store_dtypes():
     import torch
     return (torch.float32, torch.bfloat16)
@@ -343,8 +354,7 @@ def fasa_fc_agreement(q_rot, k_cache, seq_lens, topk: int, ca, dims: FasaDims, w
     """Contextual Agreement of every FC for every (batch, KV head):
     ca [B, Hkv, d/2] fp32.  Without a workspace one is allocated here."""
     if workspace is None:
-        import torch
-        workspace = torch.empty(fasa_fc_agreement_workspace_size(dims), dtype=torch.uint8, device=ca.device)
+        workspace = _scratch(fasa_fc_agreement_workspace_size(dims), stream, ca.device)
     _check("fasa_fc_agreement", lib().fasa_fc_agreement(
         _ptr(q_rot, _f32(), "q_rot"), _ptr(k_cache, _store_dtypes(), "k_cache"),
         _ptr(seq_lens, _i32(), "seq_lens"), int(topk), _ptr(ca, _f32(), "ca"),
@@ -357,8 +367,7 @@ def fasa_compound_agreement(q_rot, k_cache, dom_fc, seq_lens, topk: int, cca, di
     """Compound CA of the chosen FCs dom_fc [Hkv, n_tip] per (batch, KV head):
     cca [B, Hkv] fp32.  Without a workspace one is allocated here."""
     if workspace is None:
-        import torch
-        workspace = torch.empty(fasa_fc_agreement_workspace_size(dims), dtype=torch.uint8, device=cca.device)
+        workspace = _scratch(fasa_fc_agreement_workspace_size(dims), stream, cca.device)
     _check("fasa_compound_agreement", lib().fasa_compound_agreement(
         _ptr(q_rot, _f32(), "q_rot"), _ptr(k_cache, _store_dtypes(), "k_cache"), _ptr(dom_fc, _i32(), "dom_fc"),
         _ptr(seq_lens, _i32(), "seq_lens"), int(topk), _ptr(cca, _f32(), "cca"),
@@ -412,15 +421,6 @@ def _where(dims):
     if not isinstance(dims, FasaPagedDims):
         raise TypeError("dims must be FasaPagedDims")
     return ctypes.addressof(dims)
-
-
-def _scratch(size, stream):
-    """A workspace for one call, kept until the call's stream is past it."""
-    import torch
-    x = torch.empty(size, dtype=torch.uint8, device="cuda")
-    if stream is not None:
-        x.record_stream(torch.cuda.ExternalStream(stream) if isinstance(stream, int) else stream)
-    return x
 
 
 def fasa_paged_append(k_new, v_new, pos, k_pages, v_pages, page_table, seq_lens, cu_new=None, weight=None,

@@ -466,6 +466,43 @@ def test_own_workspace_of_a_call_on_another_stream():
     assert new.tolist() == [100, 100] and status() == 0
 
 
+def test_own_workspaces_of_calls_on_two_streams_at_once():
+    """A call without a workspace on the current stream, held up there, then one on
+    another stream, with nothing between them: neither uses what the other does."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_attention, fasa_paged_evict
+
+    def make(seed):
+        return Cache("bf16", 2, 8, 4, 128, 32, [9000 - seed, 4000 + seed], max_pages=300, seed=seed, sigma=2.0)
+
+    def run(c, new, stream):
+        fasa_paged_attention(c.q, c.pos, c.kp, c.vp, c.table, c.lens, c.out, weight=c.weight, dims=c.dims,
+                             stream=stream)
+        fasa_paged_evict(c.weight, c.token_pos, c.pos, c.kp, c.vp, c.table, c.lens, 2500, new, sinks=4, recent=100,
+                         dims=c.dims, stream=stream)
+
+    def state(c, new):
+        return [x.clone() for x in (c.out, c.weight, c.token_pos, c.kp, c.vp, new)]
+
+    alone, side = [], torch.cuda.Stream()
+    for seed in (30, 31):
+        c, new = make(seed), torch.zeros(2, dtype=torch.int32, device="cuda")
+        run(c, new, None)
+        alone.append(state(c, new))
+    torch.cuda.synchronize()
+    for first, second in ((None, side), (side.cuda_stream, None), (None, side.cuda_stream), (side, None)):
+        both = [(make(seed), torch.zeros(2, dtype=torch.int32, device="cuda")) for seed in (30, 31)]
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side if first is not None else torch.cuda.current_stream()):
+            torch.cuda._sleep(3_000_000)
+        run(*both[0], first)
+        run(*both[1], second)
+        torch.cuda.synchronize()
+        for got, want in zip(both, alone):
+            assert all(torch.equal(x, y) for x, y in zip(state(*got), want))
+    assert status() == 0
+
+
 # ---------------------------------------------------------------------- append
 def _append_ref(c, k_new, v_new, cu, kp, vp, w, tp):
     PO.paged_append(c.host(k_new), c.host(v_new), cu, c.pos.cpu().numpy(), c.table.cpu().numpy(),

@@ -331,3 +331,60 @@ def test_binding_without_a_gpu_raises():
         fasa_paged_attention(x, x, x, x, x, x, x, workspace=x, dims=d)
     with pytest.raises((RuntimeError, ValueError)):
         fasa_paged_evict(x, x, x, x, x, x, x, 4, x, workspace=x, dims=d)
+
+
+@pytest.mark.parametrize("handle", [False, True], ids=["stream", "handle"])
+@pytest.mark.parametrize("call", ["attention", "evict", "agreement", "compound"])
+def test_own_workspace_belongs_to_the_stream_of_the_call(monkeypatch, call, handle):
+    """A call's own workspace is allocated with the call's stream as the current
+    one: memory that another stream freed may still be in use there."""
+    import contextlib
+    import types
+
+    import torch
+    from kv_cache_token_tip_gb300 import FasaDims, fasa
+    now, asked = ["its own"], []
+
+    @contextlib.contextmanager
+    def stream(s):
+        now.append(s.cuda_stream if s is not None else now[-1])
+        yield
+        now.pop()
+
+    def empty(size, dtype=None, device=None):
+        asked.append((now[-1], dtype))
+        return types.SimpleNamespace(numel=lambda: size, element_size=lambda: 1, size=size)
+
+    calls = []
+
+    class Anything:
+        """The library and the compiled calls: each answers 0."""
+
+        def __getattr__(self, name):
+            return lambda *a: calls.append(name) or 0
+
+    monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "ExternalStream", lambda h, *a: types.SimpleNamespace(cuda_stream=h))
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda *a: types.SimpleNamespace(cuda_stream="its own"))
+    monkeypatch.setattr(torch, "empty", empty)
+    monkeypatch.setattr(fasa, "lib", Anything)
+    monkeypatch.setattr(fasa, "_native", Anything())
+    monkeypatch.setattr(fasa, "_ptr", lambda *a: 0)
+    x = types.SimpleNamespace(device="cuda")
+    d, dp = FasaDims(), _dims()
+
+    def run(**kw):
+        if call == "attention":
+            fasa.fasa_paged_attention(x, x, x, x, x, x, x, dims=dp, **kw)
+        elif call == "evict":
+            fasa.fasa_paged_evict(x, x, x, x, x, x, x, 4, x, dims=dp, **kw)
+        elif call == "agreement":
+            fasa.fasa_fc_agreement(x, x, x, 4, x, d, **kw)
+        else:
+            fasa.fasa_compound_agreement(x, x, x, x, 4, x, d, **kw)
+
+    run(stream=77 if handle else types.SimpleNamespace(cuda_stream=77))
+    run()
+    run(stream=0 if handle else types.SimpleNamespace(cuda_stream=0))
+    assert asked == [(77, torch.uint8), ("its own", torch.uint8), (0, torch.uint8)]
+    assert len(calls) == 6   # a size and a call, three times
