@@ -421,8 +421,12 @@ typedef struct fasa_paged_dims {
  *   weight[b,h,t] = 0, token_pos[b,h,t] = m   (each of the two may be NULL).
  * Rows at or behind cu_new[B] are padding and are left out.  A token whose
  * sequence's length is negative, whose slot is not below T_cap, or whose page is
- * out of range is left out as a whole and sets FASA_DEV_BAD_INPUT, as does a cu_new that does not ascend from 0 within
- * n_tokens.  seq_lens is read, not written: the caller advances it.
+ * out of range is left out as a whole and sets FASA_DEV_BAD_INPUT.  So does a
+ * cu_new that does not ascend from 0 within n_tokens: whatever part of it is
+ * wrong, FASA_DEV_BAD_INPUT is set, and rows that it gives to no sequence, or to
+ * one whose range is not within n_tokens, are left out (n_tokens = 0 returns at
+ * once and looks at nothing).  seq_lens is read, not written: the caller
+ * advances it.
  */
 int fasa_paged_append(const void* k_new, const void* v_new, int32_t n_tokens, const int32_t* cu_new,
                       const int32_t* pos, const int32_t* page_table, const int32_t* seq_lens,

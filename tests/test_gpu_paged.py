@@ -590,6 +590,45 @@ def test_append_bad_slots_pages_and_tables():
     assert c.kp.shape == before.shape
 
 
+@pytest.mark.parametrize("dtype,d", [("bf16", 128), ("f32", 64)])
+@pytest.mark.parametrize("cu,taken", [
+    # cu_new, and how many of its own rows each sequence gets
+    ([0, 4, 9], [4, 0]),            # the second range runs past the rows, none of which it has
+    ([0, 5, 3], [0, 0]), ([0, 2, 1], [1, 0]), ([0, 4, -1], [0, 0]),    # descends at the end
+    ([0, 0, 5], [0, 0]),            # past the rows
+    ([1, 2, 4], [1, 2]), ([-1, 2, 4], [0, 2]), ([1, 1, 1], [0, 0]),    # does not begin at 0
+    ([0, 9, 4], [0, 0]), ([0, 9, 0], [0, 0]),
+    ([0, 1, 4, 2, 4], None), ([0] * 150 + [9, 4], [0] * 151), ([0, 4] + [9] * 150, [4] + [0] * 150),
+    ([0, 4, 3] + [4] * 150, None),
+    # and tables that are right
+    ([0, 4, 4], [4, 0]), ([0, 0, 0], [0, 0]), ([0] * 300 + [3], [0] * 299 + [3])],
+    ids=lambda x: f"{x[:5]}{len(x)}".replace(" ", "") if isinstance(x, list) else None)
+def test_append_tables_of_rows(cu, taken, dtype, d):
+    """A table of rows that does not ascend from 0 within the rows is reported,
+    wherever it is wrong; rows without a sequence and all other pages keep out."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_append
+    rows, B = 4, len(cu) - 1
+    right = cu[0] == 0 and all(a <= b for a, b in zip(cu, cu[1:])) and cu[-1] <= rows
+    c = Cache(dtype, B, 2, 1, d, 16, [(3 * i) % 29 for i in range(B)], max_pages=3, seed=24)
+    k_new, v_new = (torch.randn((rows, 2, d), generator=c.gen, device="cuda").to(c.kp.dtype) for _ in range(2))
+    ref = [c.host(c.kp).copy(), c.host(c.vp).copy(), c.weight.cpu().numpy().astype(np.float64),
+           c.token_pos.cpu().numpy().copy()]
+    k_before, c.v_before = ref[0].copy(), ref[1].copy()
+    if taken is not None:
+        for b, n in enumerate(taken):   # one sequence at a time, from its first row
+            if n:
+                only = [0] * (b + 1) + [n] * (B - b)
+                at = slice(cu[b], cu[b] + n)
+                _append_ref(c, k_new[at], v_new[at], only, *ref)
+    fasa_paged_append(k_new, v_new, c.pos, c.kp, c.vp, c.table, c.lens,
+                      cu_new=torch.tensor(cu, dtype=torch.int32, device="cuda"), weight=c.weight,
+                      token_pos=c.token_pos, dims=c.dims)
+    assert status() == (0 if right else 1) and status() == 0
+    if taken is not None:
+        assert _check_append(c, k_new, v_new, cu, (c.kp, c.vp, c.weight, c.token_pos), ref, k_before) == 2 * sum(taken)
+
+
 # ---------------------------------------------------------------------- evict
 def _run_evict(c, keep, sinks=0, recent=0, apart=False):
     import torch
