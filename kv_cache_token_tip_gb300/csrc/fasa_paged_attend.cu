@@ -43,9 +43,12 @@ constexpr int JN_NT = 256;  // threads of a join block
 template <int NT>
 __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  // (past L1: the join reads them ahead of its wait, when its SM's L1 may hold what
+  // they were before the kernel in front of the attention wrote them)
+  bool bad = false;
   auto length = [&](int b) {
-    const int len = p.seq_lens[b];
-    if (report && (len < 0 || len > p.T_cap)) atomicOr(p.status, 1);
+    const int len = ld_cg(p.seq_lens + b);
+    bad = bad || len < 0 || len > p.T_cap;
     return min(max(len, 0), p.T_cap);
   };
   const bool many = p.B > NT;
@@ -61,6 +64,7 @@ __device__ void make_line(const PagedCommon& p, unsigned* w, int* scan, bool rep
     __syncthreads();
     for (int b = b0; b < b1; ++b) groups += paged_groups((int)w[b]);
   }
+  if (report && bad) atomicOr(p.status, 1);
   int incl = groups;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -669,7 +673,8 @@ __global__ void __launch_bounds__(JN_NT, GM ? 2 : 3)
   __shared__ int scan[NW];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, G = p.G;
   const int R = paged_record_floats(G, D);
-  // (the lengths are older than the first kernel, which waited before it let this one begin)
+  // (the lengths are older than the first kernel, which waited before it let this one
+  // begin: they are in L2 by then)
   make_line<NT>(p, words, scan, false);
   const PagedLine line{words, p.B, p.Hkv};
   const PagedCuts cuts = line.cuts(p.parts);
