@@ -388,3 +388,82 @@ def test_own_workspace_belongs_to_the_stream_of_the_call(monkeypatch, call, hand
     run(stream=0 if handle else types.SimpleNamespace(cuda_stream=0))
     assert asked == [(77, torch.uint8), ("its own", torch.uint8), (0, torch.uint8)]
     assert len(calls) == 6   # a size and a call, three times
+
+
+CUTS_PROGRAM = r"""
+#include <cmath>
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "fasa_paged_index.h"
+using namespace fasa;
+
+static float steps(float x, int n) {
+  for (; n > 0; --n) x = std::nextafter(x, 2e9f);
+  for (; n < 0; ++n) x = std::nextafter(x, 0.f);
+  return x;
+}
+
+// begin(c) is floor(cost * c / n) for every count of parts and part, with an inverse that
+// is `off` steps from the nearest fp32.
+static int exact(int off) {
+  for (int n = 1; n <= PAGED_MAX_PARTS; ++n) {
+    PagedCuts cuts(n, n);
+    cuts.inv = steps(cuts.inv, off);
+    for (int r = n - 1; r >= 0; r -= n < 200 ? 1 : 1 + rand() % 13)  // the largest products first
+      for (int c = 0; c <= n; ++c) {
+        cuts.r = r;
+        if (cuts.begin(c) != c + (int)((long long)r * c / n)) return printf("begin: %d parts, %d, %d\n", n, r, c), 1;
+      }
+  }
+  return 0;
+}
+
+// part_of finds every group's part with the quotients as far off.
+static int inverse(int off) {
+  for (int i = 0; i < 60; ++i) {
+    const int B = 1 + rand() % 200, Hkv = 1 + rand() % 8, long_one = rand() % B;
+    std::vector<unsigned> w;
+    int before = 0;
+    for (int b = 0; b <= B; ++b) {
+      const int len = b == B ? 0 : b == long_one ? rand() % PAGED_MAX_SLOTS : rand() % 500;
+      w.push_back(paged_word(before, len));
+      before += paged_groups(len);
+    }
+    const PagedLine line{w.data(), B, Hkv};
+    PagedCuts cuts = line.cuts(i % 2 ? PAGED_MAX_PARTS : 1 + rand() % PAGED_MAX_PARTS);
+    cuts.inv = steps(cuts.inv, off);
+    cuts.part = steps(cuts.part, i % 3 ? off : -off);
+    for (int c = 0; c < cuts.n; ++c) {
+      const int r0 = line.part_begin(cuts, c), r1 = line.part_begin(cuts, c + 1);
+      PagedSegments s;
+      s.start(line, r0, r1);
+      for (; s.at(); s.next())
+        for (int x : std::vector<int>{s.x, s.x + (s.seg_end() - s.x) / 2, s.seg_end() - 1})
+          if (line.part_of(cuts, s.b, s.h, x - s.unit_begin) != c) return printf("part of %d\n", x), 1;
+    }
+  }
+  return 0;
+}
+
+int main() {
+  srand(5);
+  for (int off = -2; off <= 2; ++off)
+    if (exact(off) || inverse(off)) return printf("%d steps off\n", off), 1;
+  puts("ok");
+  return 0;
+}
+"""
+
+
+def test_cuts_are_exact_with_the_devices_quotients(tmp_path):
+    """The device's quotients may be two steps from a / b: the cuts in fp32 are the integer
+    ones all the same, and a group's part is found."""
+    src = tmp_path / "cuts.cpp"
+    src.write_text(CUTS_PROGRAM)
+    exe = str(tmp_path / "cuts")
+    inc = os.path.join(ROOT, "kv_cache_token_tip_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-ffp-contract=off", "-I", inc, str(src), "-o", exe], check=True,
+                   capture_output=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
