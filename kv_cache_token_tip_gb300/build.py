@@ -1,17 +1,21 @@
 """In-tree build of the CUDA libraries with nvcc (sm_103a).
 
 ``build()`` compiles every translation unit in parallel and links
-``kv_cache_token_tip_gb300/libfasa.so`` (the FASA library),
-``kv_cache_token_tip_gb300/_fasa_torch.so`` (the paged cache's argument
-marshalling for torch tensors) and ``workload/libfasa_synth.so`` (the
-synthetic-input generator used by the tests and the benchmark).  Object files go to ``_build/`` at the repository root.
-A library is rebuilt only when one of its sources is newer than it.
+``kv_cache_token_tip_gb300/libfasa.so`` (the FASA library) and
+``workload/libfasa_synth.so`` (the synthetic-input generator used by the tests
+and the benchmark); where torch is installed it also builds
+``kv_cache_token_tip_gb300/_fasa_torch`` + the Python ABI's suffix (the paged
+cache's argument marshalling for torch tensors).  Object files go to
+``_build/`` at the repository root.  A library is rebuilt only when one of its
+sources is newer than it, the module also when it was built for another torch.
 """
 
 import concurrent.futures as cf
 import os
+import re
 import shutil
 import subprocess
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -30,7 +34,7 @@ FASA_DEPS = [os.path.join(PKG, "csrc", f) for f in
              ("fasa_cluster.cuh", "fasa_step.cuh", "fasa_ptx.cuh", "fasa_internal.h",
               "fasa_paged.h", "fasa_paged_index.h")] + [
     os.path.join(ROOT, "include", "fasa.h")]
-LIBTORCH = os.path.join(PKG, "_fasa_torch.so")
+LIBTORCH = os.path.join(PKG, "_fasa_torch" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 TORCH_SOURCES = [os.path.join(PKG, "csrc", "fasa_torch.cpp")]
 SYNTH_SOURCES = [os.path.join(ROOT, "workload", "csrc", "synth_gen.cu")]
 
@@ -83,25 +87,41 @@ def _build_lib(target, sources, deps, extra_flags=(), verbose=False, force=False
 
 
 def _build_torch(verbose=False, force=False):
-    """The extension module, against the torch that is installed (host code alone)."""
-    if not force and not _stale(LIBTORCH, TORCH_SOURCES + [os.path.join(ROOT, "include", "fasa.h")]):
-        return LIBTORCH
+    """The extension module, against the torch that is installed (host code
+    alone); None where there is none (the C library does not need it)."""
     import importlib.util
-    import sysconfig
-    torch = os.path.dirname(importlib.util.find_spec("torch").origin)
+    found = importlib.util.find_spec("torch")
+    if found is None or not found.origin:
+        return None
+    torch = os.path.dirname(found.origin)
+    with open(os.path.join(torch, "version.py")) as f:
+        about = f.read()
+    version = re.search(r"__version__ = ['\"](.*?)['\"]", about).group(1)
+    # the torch it was built for: its inline code and layouts are in the module, and a
+    # file of another torch may be older than the module
+    stamp, built_for = os.path.join(BUILD_DIR, "_fasa_torch.torch"), f"{torch}\n{about}"
+    if not force and not _stale(LIBTORCH, TORCH_SOURCES + [os.path.join(ROOT, "include", "fasa.h")]) and \
+            os.path.exists(stamp):
+        with open(stamp) as f:
+            if f.read() == built_for:
+                return LIBTORCH
+    os.makedirs(BUILD_DIR, exist_ok=True)
     cuda = os.path.dirname(os.path.dirname(nvcc()))
     tmp = LIBTORCH + ".tmp"
-    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared"] + [
+    _run([shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", f'-DFASA_TORCH_VERSION="{version}"'] + [
         "-I" + d for d in (sysconfig.get_paths()["include"], os.path.join(torch, "include"),
                            os.path.join(torch, "include", "torch", "csrc", "api", "include"),
                            os.path.join(cuda, "include"))] + TORCH_SOURCES + [
         "-o", tmp, "-L" + os.path.join(torch, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"], verbose)
     os.replace(tmp, LIBTORCH)
+    with open(stamp, "w") as f:
+        f.write(built_for)
     return LIBTORCH
 
 
 def build(verbose=False, force=False, ptxas_v=False):
-    """Compile libfasa.so and libfasa_synth.so (in parallel, with the extension module); return their paths."""
+    """Compile libfasa.so and libfasa_synth.so (in parallel, with the extension module where torch is
+    installed); return their paths."""
     with cf.ThreadPoolExecutor(max_workers=3) as ex:
         t = ex.submit(_build_torch, verbose, force)
         a = ex.submit(_build_lib, LIBFASA, FASA_SOURCES, FASA_DEPS, (), verbose, force, ptxas_v)

@@ -244,4 +244,12 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fasa_torch", nullptr, -1, methods
 
 }  // namespace
 
-PyMODINIT_FUNC PyInit__fasa_torch(void) { return PyModule_Create(&module); }
+// torch_version: the torch that this was compiled for, which has to be the one that runs.
+PyMODINIT_FUNC PyInit__fasa_torch(void) {
+  PyObject* m = PyModule_Create(&module);
+  if (m && PyModule_AddStringConstant(m, "torch_version", FASA_TORCH_VERSION) < 0) {
+    Py_DECREF(m);
+    return nullptr;
+  }
+  return m;
+}

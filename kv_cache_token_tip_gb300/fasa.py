@@ -405,12 +405,14 @@ def _marshal():
     """The extension module, its calls bound to libfasa.so's entry points."""
     global _native
     if _native is None:
-        import torch  # noqa: F401  (whose libraries it needs)
+        import torch  # (whose libraries it needs)
+        how = "build it with `python -m kv_cache_token_tip_gb300.build` (there is no fallback)"
         try:
             from . import _fasa_torch as m
         except ImportError as e:
-            raise RuntimeError("_fasa_torch.so is missing: build it with "
-                               "`python -m kv_cache_token_tip_gb300.build` (there is no fallback)") from e
+            raise RuntimeError(f"the module _fasa_torch is missing or does not load: {how}") from e
+        if getattr(m, "torch_version", None) != str(torch.__version__):
+            raise RuntimeError(f"the module _fasa_torch was built for another torch: {how}")
         m.bind(*(ctypes.cast(getattr(lib(), f"fasa_paged_{n}"), ctypes.c_void_p).value
                  for n in ("append", "attention", "evict")))
         _native = m

@@ -467,3 +467,67 @@ def test_cuts_are_exact_with_the_devices_quotients(tmp_path):
                    capture_output=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_c_library_builds_without_torch(monkeypatch):
+    """The C library needs nvcc alone: without torch only the binding's module is left out."""
+    import importlib.util
+    from kv_cache_token_tip_gb300 import build
+    find = importlib.util.find_spec
+    monkeypatch.setattr(importlib.util, "find_spec", lambda name, *a: None if name == "torch" else find(name, *a))
+    for force in (False, True):
+        assert build._build_torch(force=force) is None
+    assert build.build()[0] == build.LIBFASA
+
+
+def test_binding_module_is_rebuilt_for_another_torch(monkeypatch, tmp_path):
+    """Its file carries the Python ABI's tag, and it is built anew for another torch, whatever the dates."""
+    import importlib.util
+    import sysconfig
+    import types
+    from kv_cache_token_tip_gb300 import build
+    assert build.LIBTORCH.endswith("_fasa_torch" + sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(build, "BUILD_DIR", str(tmp_path / "_build"))
+    monkeypatch.setattr(build, "LIBTORCH", str(tmp_path / "module.so"))
+    torch = {"at": "a", "version": "__version__ = '1'"}
+    runs = []
+
+    def find(name, *a):
+        d = tmp_path / torch["at"]
+        d.mkdir(exist_ok=True)
+        (d / "version.py").write_text(torch["version"])
+        os.utime(d / "version.py", (1, 1))   # older than every build
+        return types.SimpleNamespace(origin=str(d / "__init__.py"))
+
+    def run(cmd, verbose):
+        runs.append(cmd)
+        with open(cmd[cmd.index("-o") + 1], "w") as f:
+            f.write("module")
+
+    monkeypatch.setattr(importlib.util, "find_spec", find)
+    monkeypatch.setattr(build, "_run", run)
+    built = []
+    for change in ({}, {}, {"version": "__version__ = '2'"}, {}, {"at": "b"}, {}):
+        torch.update(change)
+        assert build._build_torch() == build.LIBTORCH
+        built.append(len(runs))
+    assert built == [1, 1, 2, 2, 3, 3]
+
+
+def test_binding_refuses_a_module_of_another_torch(monkeypatch):
+    import sys
+    import types
+    import kv_cache_token_tip_gb300 as pkg
+    from kv_cache_token_tip_gb300 import build, fasa
+    build.build()
+    bound = []
+    for version, fits in (("0.1.2", False), (None, False)):
+        m = types.SimpleNamespace(bind=lambda *a: bound.append(a))
+        if version:
+            m.torch_version = version
+        monkeypatch.setitem(sys.modules, pkg.__name__ + "._fasa_torch", m)
+        monkeypatch.setattr(pkg, "_fasa_torch", m, raising=False)
+        monkeypatch.setattr(fasa, "_native", None)
+        with pytest.raises(RuntimeError, match="build it"):
+            fasa._marshal()
+    assert not bound
