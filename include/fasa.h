@@ -466,9 +466,9 @@ int fasa_paged_attention(const void* q, const int32_t* pos, const void* k_pages,
  * the moved tokens' entries are written), or others of that shape, apart from
  * them: slots 0 .. new_lens[b]-1 are written there and the inputs are left as
  * they were.  Slots at or behind new_lens[b] keep their contents everywhere.
- * new_lens must lie apart from seq_lens.  1 <= keep, 0 <= sinks, 0 <= recent,
- * sinks + recent <= keep.  Table entries from ceil(new_len / page_size)
- * on are free for other use afterwards.
+ * new_lens must lie apart from seq_lens, pos and page_table.  1 <= keep,
+ * 0 <= sinks, 0 <= recent, sinks + recent <= keep.  Table entries from
+ * ceil(new_len / page_size) on are free for other use afterwards.
  * workspace: at least fasa_paged_evict_workspace_size bytes, as above.
  */
 int fasa_paged_evict_workspace_size(const fasa_paged_dims_t* dims, int32_t keep, size_t* bytes);

@@ -57,10 +57,11 @@ int most_moves(const fasa_paged_dims_t* d, int keep) {
   return std::max(0, std::min(keep, d->max_pages * d->page_size - keep));
 }
 
-bool apart(const void* a, const void* b, size_t bytes) {
+bool apart(const void* a, const void* b, size_t a_bytes, size_t b_bytes) {
   const char *x = static_cast<const char*>(a), *y = static_cast<const char*>(b);
-  return x + bytes <= y || y + bytes <= x;
+  return x + a_bytes <= y || y + b_bytes <= x;
 }
+bool apart(const void* a, const void* b, size_t bytes) { return apart(a, b, bytes, bytes); }
 
 }  // namespace
 
@@ -179,7 +180,11 @@ int fasa_paged_evict(const float* weight, const int32_t* token_pos, const int32_
       !token_pos_out || !new_lens)
     return FASA_ERR_INVALID_ARG;
   if (sinks < 0 || recent < 0 || (long long)sinks + recent > keep) return FASA_ERR_INVALID_ARG;
-  if (!apart(new_lens, seq_lens, (size_t)dims->batch * 4)) return FASA_ERR_INVALID_ARG;
+  // new_lens is written while other heads' blocks still read these
+  const size_t lens = (size_t)dims->batch * 4;
+  if (!apart(new_lens, seq_lens, lens, lens) || !apart(new_lens, pos, lens, lens) ||
+      !apart(new_lens, page_table, lens, lens * dims->max_pages))
+    return FASA_ERR_INVALID_ARG;
   if (!aligned(weight, 16) || !aligned(token_pos, 16) || !aligned(weight_out, 16) || !aligned(token_pos_out, 16) ||
       !aligned(k_pages, 16) || !aligned(v_pages, 16))
     return FASA_ERR_INVALID_ARG;

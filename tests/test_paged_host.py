@@ -531,3 +531,21 @@ def test_binding_refuses_a_module_of_another_torch(monkeypatch):
         with pytest.raises(RuntimeError, match="build it"):
             fasa._marshal()
     assert not bound
+
+
+def test_new_lens_apart_from_what_other_heads_still_read(L):
+    """new_lens is written while heads of other blocks read the positions and the pages."""
+    d, far = _dims(), 16 * P
+
+    def evict(new, **kw):   # right but for new_lens, until the workspace that is missing (3)
+        t = dict(pos=far, table=far, lens=far, w=far, tp=far + 8 * P, wo=far, tpo=far + 8 * P, ws=None, new=new)
+        t.update(kw)
+        return _evict(L, d, **t)
+
+    for at in (P, P + 4, P - 4):   # pos [2]: itself, overlapping from either side
+        assert evict(at, pos=P) == 1
+    table = 2 * 32 * 4             # page_table [2, 32]
+    for at in (P, P + 64, P + table - 4, P - 4):
+        assert evict(at, table=P) == 1
+    assert evict(P + 8, pos=P) == 3 and evict(P - 8, pos=P) == 3
+    assert evict(P + table, table=P) == 3 and evict(P - 8, table=P) == 3
