@@ -284,7 +284,7 @@ template <int D, int GP>
 struct MathF32 {
   using T = float;
   static constexpr int CTAS = 1;
-  // Warps of a CTA: as many as hide the arithmetic's latency, then stages.  At 268 MB:
+  // Warps of a CTA: as many as hide the arithmetic's latency, then stages.  At 537 MB:
   // 4 heads of 64 dims 83.6 us with eight warps, 117.1 with four; 8 heads of 128 dims
   // 106.2 and 116.8 (one stage against three); 4 heads of 128 dims 86.7 and 82.8.
   static constexpr int WARPS = D == 128 && GP == 4 ? 4 : 8;

@@ -184,8 +184,9 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
 //      list into shared memory first.
 // Bound by the latency of these steps (cluster barriers, dependent loads): of the
 // 21.4 us that 8 heads of 32K tokens cut to 4096 take, keys and range are 2.6, the
-// choice 6, the lists 3.5 and the copies of 28.7 MB there and back 4 to 8; 256 heads
-// of 1900 to 2080 tokens cut to 2048 take 10.0 us.
+// choice 6.1, holes and movers counted and listed 3.9, and the copies of 28.7 MB there
+// and back 4 to 8.7 from CTA to CTA, the last of which ends it; 256 heads of 1900 to 2080
+// tokens cut to 2048 take 10.0 us.
 constexpr int EV_NW = 16;            // most warps of a CTA
 constexpr int EV_BINS = 2048;
 constexpr int EV_CAND = 512;         // keys of a bin that are ranked one by one
