@@ -84,8 +84,9 @@ FASA_HD int paged_record_floats(int G, int D) { return (G * (D + 2) + 3) / 4 * 4
 // stream (paged_behind: the launch), waits for all that came before its first
 // access to memory (paged_wait: every thread of every block) and lets the next
 // kernel begin as early (paged_go).  A kernel may read ahead of its wait only what
-// is older than the kernel before it: so where that one goes on before it waits,
-// nothing.  The launch of one such kernel behind another then costs little.
+// is older than the kernel before it, and past L1 (ld_cg): so where that one goes on
+// before it waits, nothing.  The launch of one such kernel behind another then costs
+// little.
 template <class... P, class... A>
 cudaError_t paged_behind(void (*kernel)(P...), unsigned grid, unsigned block, size_t smem, unsigned cluster,
                          cudaStream_t s, A&&... args) {

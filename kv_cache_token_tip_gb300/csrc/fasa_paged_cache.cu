@@ -18,7 +18,7 @@ namespace {
 // so that a lane turns the same pairs of every head: the warp computes a token's
 // cosines and sines once.  The rows are on their way meanwhile.  Bound by the bytes for a
 // prompt (16.5K tokens of 8 heads, 129 MB: 23.9 us, 80% of the copy rate), by the chain
-// of loads (table, length, page) for a token a sequence (32 sequences: 2.0 us).
+// of loads (table, length, page) for a token a sequence (32 sequences: 1.9 us).
 constexpr int AP_NT = 128;
 constexpr int AP_U = 2;              // rows of K and of V a lane has on the way
 // From this many tokens a warp takes all heads of one: 16.5K tokens 23.8 us against
@@ -28,11 +28,6 @@ constexpr int AP_MANY = 2048;
 // Sequence of new token x, and which of its tokens it is; false for padding (used:
 // cu_new[B]) and where the table does not ascend about x (reported).  A whole warp.
 __device__ __forceinline__ bool token_of(const PagedAppendParams& p, int x, int used, int& b, int& j) {
-  if (!p.cu_new) {
-    b = x;
-    j = 0;
-    return true;
-  }
   const int lane = threadIdx.x & 31;
   if (x >= used) return false;  // padding
   int lo = 0, hi = p.B;  // cu_new[lo] <= x < cu_new[hi]: 32 places at a time
@@ -77,8 +72,10 @@ __device__ __forceinline__ uint4 turn_row(const uint4& w, const float2 (&cs)[NP]
   return make_uint4(out[0], out[1], out[2], out[3]);
 }
 
-// heads: of a warp, whole steps of the rows its lanes cover.
-template <typename T, int D>
+// heads: of a warp, whole steps of the rows its lanes cover.  TABLE: with a table of rows,
+// or a token a sequence (which then pays nothing for the table: 32 sequences 1.9 us, 2.1
+// with one kernel for both).
+template <typename T, int D, bool TABLE>
 __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_constant__ PagedAppendParams p, int heads) {
   constexpr int LPR = D * (int)sizeof(T) / 16, RPW = 32 / LPR;  // lanes of a row, rows of a warp
   constexpr int EPL = 16 / (int)sizeof(T), NP = EPL / 2;        // elements and pairs of a lane
@@ -93,10 +90,10 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
   paged_wait();
   // A table of rows is checked whole, by a block of its own: the tokens look at their
   // own sequence's range alone, and padding at none.  (8 sequences with a token each
-  // 2.40 us, 1500 of two 3.34, 8 of 700 7.24; without the check 2.35, 3.29, 7.14; checked
+  // 2.45 us, 1500 of two 3.42, 8 of 700 7.29; without the check 2.36, 3.27, 7.11; checked
   // by the last block behind its tokens 2.55, 5.33, 7.20.)
-  const int own = p.cu_new != nullptr;
-  if (own && blockIdx.x == 0) {
+  constexpr int own = TABLE;
+  if (TABLE && blockIdx.x == 0) {
     int bad = 0;
 #pragma unroll 4
     for (int i = threadIdx.x; i <= p.B; i += AP_NT) {
@@ -108,7 +105,7 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
   }
   const int chunks = (p.Hkv + heads - 1) / heads, at = lane % LPR, sub = lane / LPR;
   const long long items = (long long)p.n_tokens * chunks, warps = (long long)(gridDim.x - own) * (AP_NT / 32);
-  const int used = p.cu_new ? p.cu_new[p.B] : p.n_tokens;
+  const int used = TABLE ? p.cu_new[p.B] : p.n_tokens;
   for (long long w = (long long)(blockIdx.x - own) * (AP_NT / 32) + warp; w < items; w += warps) {
     const int x = (int)(w / chunks), h0 = (int)(w - (long long)x * chunks) * heads, h1 = min(p.Hkv, h0 + heads);
     // the rows first: they need only x, the rest is a chain of loads
@@ -126,7 +123,12 @@ __global__ void __launch_bounds__(AP_NT) paged_append_kernel(const __grid_consta
     };
     load(h0);
     int b, j;
-    if (!token_of(p, x, used, b, j)) continue;
+    if constexpr (TABLE) {
+      if (!token_of(p, x, used, b, j)) continue;
+    } else {
+      b = x;
+      j = 0;
+    }
     const int len = p.seq_lens[b], m = p.pos[b] + j;
     const long long slot = (long long)len + j;
     if (len < 0 || slot >= p.T_cap) {
@@ -635,8 +637,8 @@ cudaError_t launch_append(const PagedAppendParams& p, int sms, cudaStream_t s) {
   const int heads = p.n_tokens < AP_MANY ? RPW : (p.Hkv + RPW - 1) / RPW * RPW;
   const long long items = (long long)p.n_tokens * ((p.Hkv + heads - 1) / heads);
   const long long blocks = (items + AP_NT / 32 - 1) / (AP_NT / 32) + (p.cu_new != nullptr);  // (one looks at the table)
-  return paged_behind(paged_append_kernel<T, D>, (unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms), AP_NT, 0, 0, s,
-                      p, heads);
+  return paged_behind(p.cu_new ? paged_append_kernel<T, D, true> : paged_append_kernel<T, D, false>,
+                      (unsigned)(blocks < 16ll * sms ? blocks : 16ll * sms), AP_NT, 0, 0, s, p, heads);
 }
 
 template <int NT>
