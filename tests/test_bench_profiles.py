@@ -57,3 +57,18 @@ def test_step_summary_states_the_byte_model(fname):
     assert int(vals["algorithmic_bytes_per_launch"]) == int(model["total"])
     assert float(vals["dram_bytes_per_launch"]) >= int(model["total"])
     assert re.fullmatch(r"[0-9a-f]{16}", vals["kernel_source_hash"])
+
+
+def test_paged_summary_names_its_sources():
+    """The paged cache's summary carries the hash of the sources it was taken on; where
+    they have moved on since, a warning says so (a comment is a change too)."""
+    import warnings
+
+    import bench
+    vals = _values(os.path.join(PROFILES, "fasa_paged.md"))
+    csrc = "kv_cache_token_tip_gb300/csrc"
+    names = vals["kernel_sources"].split("`")[0].split()
+    assert {"fasa_paged.h", "fasa_paged_index.h", "fasa_paged_attend.cu", "fasa_paged_cache.cu"} <= set(names)
+    assert re.fullmatch(r"[0-9a-f]{16}", vals["kernel_source_hash"])
+    if bench.kernel_source_hash([os.path.join(csrc, f) for f in names]) != vals["kernel_source_hash"]:
+        warnings.warn("profiles/fasa_paged.md was taken on other sources of the paged cache")
