@@ -479,6 +479,119 @@ int fasa_paged_evict(const float* weight, const int32_t* token_pos, const int32_
                      const fasa_paged_dims_t* dims, fasa_stream_t stream);
 
 /*
+ * ------------------------------------------------- a step of new tokens, paged
+ * What a server does about a paged cache with many new tokens at once: pages are
+ * taken and given back, queries and keys are turned and stored, and each new
+ * token attends over its sequence.  The conventions are those of the paged cache.
+ *
+ * fasa_paged_assign goes from the tokens that sequences have to those that they
+ * want.  With h = have_lens[b], w = want_lens[b], ps = page_size:
+ *  - w < h: the pages of the entries ceil(w / ps) .. ceil(h / ps) - 1 go to the end of
+ *    the free list, in the order of the sequences and of their entries (pages that
+ *    other sequences still read must not be given back).  The entries stay as they are.
+ *  - w > h: the sequence grows by w - h tokens, and takes a page for each of the entries
+ *    ceil(h / ps) .. ceil(w / ps) - 1, which are written.  Growing sequences are served in order
+ *    while the pages last (those given back by this call among them) and the new tokens
+ *    are no more than max_tokens; the first that does not fit, and every growing one
+ *    behind it, keeps its length and gets nothing.
+ * The free list is the first free_count[0] entries of free_pages [n_pages]; pages are
+ * taken from its end: the first page taken is the last entry, after what was given back.
+ *   lens_out [B]          w, or h of a growing sequence that was not served
+ *   free_count_out [1]    entries of the list afterwards
+ *   cu_new [B+1]          where each sequence's new tokens begin, ascending from 0
+ *   token_map [max_tokens][4]  the new tokens in order: sequence, slot, page, position;
+ *                         -1, -1, -1, -1 behind the last
+ * The position of a sequence's first new token is pos[b], or its slot where pos is NULL.
+ * lens_out may be have_lens or want_lens, free_count_out free_count; else what is written
+ * lies apart from everything.  The call reads no entry of the table that it does not name.
+ * FASA_DEV_BAD_INPUT: a length outside [0, T_cap] or a free_count outside [0, n_pages]
+ * (clamped), a page outside the pool that is given back or taken (passed on as it is: the
+ * other calls leave such pages alone), more pages than the list can hold (left out).
+ * Aligned to 16 bytes: token_map; to 4: the rest.  max_tokens <= 2^24.
+ */
+int fasa_paged_assign(const int32_t* have_lens, const int32_t* want_lens, const int32_t* pos, int32_t* page_table,
+                      int32_t* free_pages, const int32_t* free_count, int32_t* lens_out, int32_t* free_count_out,
+                      int32_t* cu_new, int32_t* token_map, int32_t max_tokens, const fasa_paged_dims_t* dims,
+                      fasa_stream_t stream);
+
+/* Rotary positions: which elements of a head make a pair, and its angle per position. */
+enum { FASA_ROPE_INTERLEAVED = 0, FASA_ROPE_HALF = 1 };
+enum { FASA_ROPE_PLAIN = 0, FASA_ROPE_LINEAR = 1, FASA_ROPE_WAVELENGTH = 2, FASA_ROPE_RAMP = 3 };
+
+/*
+ * Pair i < r / 2 of the first r = rotary_dim elements of a head: (2i, 2i+1) interleaved,
+ * (i, i + r/2) in halves; it is turned by m * f_i at position m and multiplied by
+ * `magnitude`.  The elements behind them stay as they are.  With t_i = rope_theta^(-2i/r):
+ *   PLAIN       f_i = t_i
+ *   LINEAR      f_i = t_i / factor
+ *   WAVELENGTH  f_i = t_i (s + (1 - s) / factor), s = (original t_i / (2 pi) - low) / (high - low)
+ *               clamped to [0, 1]: `low` and `high` are turns within `original` positions
+ *   RAMP        f_i = t_i (1 - s + s / factor), s = (i - i0) / max(i1 - i0, 0.001) clamped to
+ *               [0, 1], i0 = max(floor(I(high)), 0), i1 = min(ceil(I(low)), r - 1),
+ *               I(x) = r ln(original / (2 pi x)) / (2 ln rope_theta)
+ * Angles are formed exactly in 64-bit fixed-point turns, as in fasa_apply_rope_q.
+ * rotary_dim: a multiple of 16, 16 .. d.  rope_theta > 0 (RAMP: > 1), factor > 0 (but
+ * PLAIN), 0 < low < high and original > 0 (WAVELENGTH, RAMP), magnitude > 0, all finite.
+ */
+typedef struct fasa_rope {
+  int32_t layout;
+  int32_t rotary_dim;
+  int32_t scaling;
+  int32_t reserved; /* 0 */
+  double rope_theta;
+  double factor, low, high, original;
+  double magnitude;
+} fasa_rope_t;
+
+/*
+ * The new tokens of a step on their way to the cache.  For row x < n_tokens of the map of
+ * fasa_paged_assign, (b, t, page, m) = token_map[x]:
+ *   q_out[x] = R(m) q[x],  K[t] = R(m) k[x],  V[t] = v[x] (in `page`, row t % page_size),
+ *   weight[b,h,t] = 0,  token_pos[b,h,t] = m   (each of the two may be NULL).
+ * R(m) is computed in fp32 and rounded once.  q [n_tokens, Hq, d], k and v [n_tokens, Hkv,
+ * d] in the storage dtype, a token's heads contiguous and tokens q_stride, k_stride,
+ * v_stride elements apart (one projection's output holds all three); q_out [n_tokens, Hq,
+ * d] contiguous.  q and q_out may both be NULL, so may k, v, k_pages and v_pages together
+ * (then weight and token_pos, too).  q_out may be q where q is contiguous; else it lies
+ * apart from q, k and v.  rope_theta of dims is not used.
+ * Rows of the map whose sequence is negative are padding: nothing is written for them, nor
+ * for an entry outside the batch, the cache or the pool, which sets FASA_DEV_BAD_INPUT.
+ * The attention of one token (fasa_paged_attention) takes such queries with positions of 0,
+ * which turn nothing.
+ * Aligned to 16 bytes: every tensor, and the strides in bytes.  n_tokens <= 2^24.
+ */
+int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                           int64_t v_stride, const int32_t* token_map, int32_t n_tokens, void* q_out, void* k_pages,
+                           void* v_pages, float* weight, int32_t* token_pos, const fasa_rope_t* rope,
+                           const fasa_paged_dims_t* dims, fasa_stream_t stream);
+
+/*
+ * Attention of each sequence's new tokens over its cached ones, themselves among them.
+ * q [n_tokens, Hq, d] are rotated queries in the storage dtype; those of sequence b are
+ * rows cu_new[b] .. cu_new[b+1], or row b alone when cu_new is NULL (n_tokens = B then).
+ * seq_lens counts the new tokens: the j-th of the n of sequence b has slot
+ * s = seq_lens[b] - n + j, and
+ *   out[x] = softmax(q K^T / sqrt(d)) V over the slots 0 .. s   (storage dtype, rounded once);
+ * zeros where there is none (s < 0).  With weight (not NULL):
+ *   weight[b,h,t] += sum over the new tokens and the group's heads of softmax_t.
+ * bf16: the softmax weights that multiply V are rounded to bf16; their sum and what goes
+ * to `weight` are not.  Equal calls give equal bits.
+ * Rows at or behind cu_new[B] are padding: their `out` is left as it is.  A cu_new that does
+ * not ascend from 0 within n_tokens sets FASA_DEV_BAD_INPUT; a sequence whose range is
+ * not within n_tokens is left out.  rope_theta of dims is not used.
+ * workspace: at least fasa_paged_chunk_workspace_size bytes of device memory, its contents
+ * not kept and not read; calls that may overlap need one each.
+ * Aligned to 16 bytes: q, k_pages, v_pages, out, weight, workspace.  out lies apart from q.
+ * n_tokens <= 2^20.
+ */
+int fasa_paged_chunk_workspace_size(const fasa_paged_dims_t* dims, int32_t n_tokens, int32_t with_weight,
+                                    size_t* bytes);
+int fasa_paged_chunk_attention(const void* q, int32_t n_tokens, const int32_t* cu_new, const void* k_pages,
+                               const void* v_pages, const int32_t* page_table, const int32_t* seq_lens, void* out,
+                               float* weight, void* workspace, size_t workspace_bytes,
+                               const fasa_paged_dims_t* dims, fasa_stream_t stream);
+
+/*
  * Synchronises `stream`, stores the device status word of the current device
  * in *status (FASA_DEV_* bits, 0 = clean) and clears it.  There is one word
  * per device, shared by every call on every stream of that device: a bit may

@@ -18,5 +18,7 @@ from .fasa import (  # noqa: F401
     fasa_focused_attention, fasa_max_budget, fasa_tip_score, fasa_topk_select, fasa_workspace_size,
     FasaPagedDims, fasa_paged_append, fasa_paged_attention, fasa_paged_evict, fasa_paged_evict_workspace_size,
     fasa_paged_workspace_size,
+    FASA_ROPE_HALF, FASA_ROPE_INTERLEAVED, FASA_ROPE_LINEAR, FASA_ROPE_PLAIN, FASA_ROPE_RAMP, FASA_ROPE_WAVELENGTH,
+    FasaRope, fasa_paged_assign, fasa_paged_chunk_attention, fasa_paged_chunk_workspace_size, fasa_paged_rope_append,
     lib, library_path,
 )

@@ -1,0 +1,119 @@
+// Index arithmetic of the attention of chunks, for the kernels and (as plain C++)
+// for the host tests: the split of the work over the CTAs.
+//
+// Sequence b has n new tokens, the last n of its len slots, taken T at a time: tile
+// i of them holds T tokens with the G heads of a KV head as rows.  Unit (b, h, i) is
+// that tile of KV head h; it reads the slots that its last token sees, in tiles of
+// KT.  All units in order form one line, cut into parts of equal cost, one to a CTA:
+// a unit costs its first tile's start-up CHUNK_UNIT_COST and a count of slots,
+// a + (i + 1) T, a = max(len - n, 0), no less than it reads, whose sum over i is a
+// formula, so that a part finds its place without a list of units.
+#pragma once
+
+#include <stdint.h>
+
+#ifdef __CUDACC__
+#define FASA_CHUNK_HD __host__ __device__ __forceinline__
+#else
+#define FASA_CHUNK_HD inline
+#endif
+
+namespace fasa {
+
+constexpr int CHUNK_UNIT_COST = 128;  // slots
+constexpr int CHUNK_MAX_SMS = 160;    // the workspace has room for their parts
+
+// One sequence: its cost up to here (of one head), its new tokens and its slots.
+struct ChunkSeq {
+  long long before;
+  int n, len;
+};
+
+struct ChunkLine {
+  const ChunkSeq* s;  // [B + 1]; the last one's `before` is the total of one head
+  int B, Hkv, T, KT;
+
+  FASA_CHUNK_HD static int tiles_of(int n, int T) { return (n + T - 1) / T; }
+  // Cost of the first i units of a head of a sequence.
+  FASA_CHUNK_HD static long long cost_of(int n, int len, int T, int i) {
+    const long long a = len > n ? len - n : 0;
+    return (long long)i * (CHUNK_UNIT_COST + a) + (long long)T * i * (i + 1) / 2;
+  }
+  FASA_CHUNK_HD static long long cost_of(int n, int len, int T) { return cost_of(n, len, T, tiles_of(n, T)); }
+
+  FASA_CHUNK_HD long long total() const { return s[B].before * Hkv; }
+  FASA_CHUNK_HD int parts(int most) const {
+    const long long t = total(), least = CHUNK_UNIT_COST + KT, n = (t + least - 1) / least;
+    return n < most ? (int)n : most;
+  }
+  FASA_CHUNK_HD long long part_begin(int parts, int c) const {
+    const long long t = total();
+    return c >= parts ? t : t / parts * c + t % parts * c / parts;
+  }
+};
+
+// A place on the line: a unit, where it begins, and how many of its tiles lie before a
+// cut there.
+struct ChunkUnit {
+  int b, h, i;
+  long long begin, cost;
+  int tiles;  // that its last token sees
+
+  FASA_CHUNK_HD void fill(const ChunkLine& l) {
+    const ChunkSeq q = l.s[b];
+    const int T = l.T, last = (i + 1) * T < q.n ? (i + 1) * T : q.n;
+    const int see = q.len - q.n + last;  // (all of len at most)
+    tiles = see > 0 ? (see + l.KT - 1) / l.KT : 0;
+    cost = CHUNK_UNIT_COST + (q.len > q.n ? q.len - q.n : 0) + (long long)(i + 1) * T;
+  }
+  // The unit that holds position y, 0 <= y < total.
+  FASA_CHUNK_HD void find(const ChunkLine& l, long long y) {
+    int lo = 0, hi = l.B;  // Hkv before(lo) <= y < Hkv before(hi)
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (l.s[mid].before * l.Hkv <= y) lo = mid;
+      else hi = mid;
+    }
+    b = lo;
+    const ChunkSeq q = l.s[b];
+    const long long head = l.s[b + 1].before - q.before;
+    y -= q.before * l.Hkv;
+    h = (int)(y / head);
+    y -= h * head;
+    lo = 0;
+    hi = ChunkLine::tiles_of(q.n, l.T);
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (ChunkLine::cost_of(q.n, q.len, l.T, mid) <= y) lo = mid;
+      else hi = mid;
+    }
+    i = lo;
+    begin = q.before * l.Hkv + h * head + ChunkLine::cost_of(q.n, q.len, l.T, i);
+    fill(l);
+  }
+  // The unit behind this one; only where there is one.
+  FASA_CHUNK_HD void next(const ChunkLine& l) {
+    begin += cost;
+    if (++i == ChunkLine::tiles_of(l.s[b].n, l.T)) {
+      i = 0;
+      if (++h == l.Hkv) {
+        h = 0;
+        do ++b;
+        while (l.s[b + 1].before == l.s[b].before);
+      }
+    }
+    fill(l);
+  }
+  // Tiles of the unit that lie before position y: tile 0 at its begin, tile t at
+  // CHUNK_UNIT_COST + KT t behind it.
+  FASA_CHUNK_HD int before(const ChunkLine& l, long long y) const {
+    if (y <= begin) return 0;
+    if (y >= begin + cost) return tiles;
+    const long long r = y - begin - CHUNK_UNIT_COST;
+    const int t = r > 0 ? (int)((r + l.KT - 1) / l.KT) : 0;
+    const int at_least = t > 1 ? t : 1;
+    return at_least < tiles ? at_least : tiles;
+  }
+};
+
+}  // namespace fasa

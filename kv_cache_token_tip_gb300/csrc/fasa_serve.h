@@ -1,0 +1,85 @@
+// Internal definitions of a step of new tokens over the paged cache: launch
+// parameters, workspace layouts and launchers (fasa_serve.cu checks arguments and
+// calls them).
+#pragma once
+
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "fasa_chunk_index.h"
+#include "fasa_paged.h"
+
+namespace fasa {
+
+constexpr int ASSIGN_MAX_TOKENS = 1 << 24;
+constexpr int CHUNK_MAX_TOKENS = 1 << 20;
+
+struct AssignParams {
+  int B, max_pages, log2_page, n_pages, T_cap, max_tokens;
+  const int* have;
+  const int* want;
+  const int* pos;  // null: a token's slot
+  int* page_table;
+  int* free_pages;
+  const int* free_count;
+  int* lens_out;
+  int* free_count_out;
+  int* cu_new;
+  int4* token_map;
+  int* status;
+};
+
+struct RopeAppendParams {
+  unsigned long long turns[64];  // of pair i per position, 2^64 to a turn
+  float magnitude;
+  int rotary_dim, n_tokens;
+  int B, Hq, Hkv, log2_page, n_pages, T_cap;
+  const void* q;  // null: no queries
+  const void* k;  // null: no keys and values
+  const void* v;
+  long long q_stride, k_stride, v_stride;
+  const int4* token_map;
+  void* q_out;
+  void* k_pages;
+  void* v_pages;
+  float* weight;
+  int* token_pos;
+  int* status;
+};
+
+// The attention of chunks.  Workspace: the parts' records (two per part: a unit that
+// began in an earlier part, a unit that goes on in a later one), and with weights the
+// rows' log-sums.
+struct ChunkParams {
+  int B, Hq, Hkv, G, log2_page, n_pages, max_pages, T_cap, n_tokens;
+  const void* q;
+  const int* cu_new;  // null: a token a sequence
+  const void* k_pages;
+  const void* v_pages;
+  const int* page_table;
+  const int* seq_lens;
+  void* out;
+  float* weight;   // null: no weights kept
+  float scale;     // log2(e) / sqrt(d): logits are kept in powers of two
+  float* records;  // [parts][2][rows * (d + 2)]: o [rows][d], m [rows], l [rows]
+  float* lse;      // [Hkv][n_tokens * G]
+  int rows;        // of a record
+  int parts;       // most parts of this launch
+  int* status;
+  unsigned long long wait_ns;
+  int drop_tile;  // test hook: this tile of part 0 is never copied (-1: none)
+};
+
+// Rows that one unit takes at once (queries times the heads of their group), slots of a
+// tile, and parts to an SM, by kernel.
+struct ChunkShape {
+  int rows, tile, per_sm;
+};
+ChunkShape chunk_shape(int head_dim, bool bf16);
+
+cudaError_t launch_paged_assign(const AssignParams& p, int sms, cudaStream_t s);
+cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, bool bf16, bool half, int sms, cudaStream_t s);
+cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t s);
+cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t s);
+
+}  // namespace fasa

@@ -23,6 +23,9 @@ namespace {
 decltype(&fasa_paged_append) c_append = nullptr;
 decltype(&fasa_paged_attention) c_attention = nullptr;
 decltype(&fasa_paged_evict) c_evict = nullptr;
+decltype(&fasa_paged_assign) c_assign = nullptr;
+decltype(&fasa_paged_rope_append) c_rope_append = nullptr;
+decltype(&fasa_paged_chunk_attention) c_chunk = nullptr;
 
 const char* type_name(at::ScalarType t) {
   return t == at::kFloat ? "torch.float32" : t == at::kBFloat16 ? "torch.bfloat16" : t == at::kInt ? "torch.int32" : c10::toString(t);
@@ -53,6 +56,37 @@ void* address(PyObject* x, const char* name, int here, at::ScalarType type, int6
 // The same, of a tensor that may be None.
 void* optional(PyObject* x, const char* name, int here, at::ScalarType type, int64_t count, bool* ok) {
   return x == Py_None ? nullptr : address(x, name, here, type, count, ok);
+}
+
+// Address of a tensor [tokens, heads, d] whose heads are contiguous, and how far apart its
+// tokens are.  tokens < 0: as many as there are.
+void* strided(PyObject* x, const char* name, int here, at::ScalarType type, int64_t* tokens, int64_t heads, int64_t d,
+              int64_t* stride, bool* ok) {
+  if (!*ok) return nullptr;
+  *ok = false;
+  if (!THPVariable_Check(x)) {
+    PyErr_Format(PyExc_ValueError, "%s must be a tensor", name);
+    return nullptr;
+  }
+  const at::Tensor& t = THPVariable_Unpack(x);
+  const bool fits = t.dim() == 3 && t.size(1) == heads && t.size(2) == d && (*tokens < 0 || t.size(0) == *tokens);
+  if (!t.is_cuda() || t.get_device() != here)
+    PyErr_Format(PyExc_ValueError, "%s must be a tensor on the current CUDA device", name);
+  else if (t.scalar_type() != type)
+    PyErr_Format(PyExc_ValueError, "%s has dtype %s, expected %s", name, type_name(t.scalar_type()), type_name(type));
+  else if (!fits && *tokens < 0)
+    PyErr_Format(PyExc_ValueError, "%s must have the shape [tokens, %lld, %lld]", name, (long long)heads, (long long)d);
+  else if (!fits)
+    PyErr_Format(PyExc_ValueError, "%s must have the shape [%lld, %lld, %lld]", name, (long long)*tokens,
+                 (long long)heads, (long long)d);
+  else if (t.stride(2) != 1 || (heads > 1 && t.stride(1) != d))
+    PyErr_Format(PyExc_ValueError, "%s must have its heads contiguous", name);
+  else
+    *ok = true;
+  if (!*ok) return nullptr;
+  *tokens = t.size(0);
+  *stride = *tokens > 1 ? t.stride(0) : heads * d;
+  return t.data_ptr();
 }
 
 // A workspace: any contiguous tensor on the device.
@@ -126,10 +160,13 @@ PyObject* guarded(F&& f) {
 }
 
 PyObject* bind(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  if (!counted(n, 3)) return nullptr;
+  if (!counted(n, 6)) return nullptr;
   c_append = reinterpret_cast<decltype(c_append)>(PyLong_AsVoidPtr(a[0]));
   c_attention = reinterpret_cast<decltype(c_attention)>(PyLong_AsVoidPtr(a[1]));
   c_evict = reinterpret_cast<decltype(c_evict)>(PyLong_AsVoidPtr(a[2]));
+  c_assign = reinterpret_cast<decltype(c_assign)>(PyLong_AsVoidPtr(a[3]));
+  c_rope_append = reinterpret_cast<decltype(c_rope_append)>(PyLong_AsVoidPtr(a[4]));
+  c_chunk = reinterpret_cast<decltype(c_chunk)>(PyLong_AsVoidPtr(a[5]));
   if (PyErr_Occurred()) return nullptr;
   Py_RETURN_NONE;
 }
@@ -233,11 +270,127 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// assign(have_lens, want_lens, page_table, free_pages, free_count, lens_out, cu_new, token_map, pos, free_count_out,
+//        dims, stream)
+PyObject* assign(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c;
+    if (!counted(n, 12) || !c.read(a[10], a[11])) return nullptr;
+    if (!c.sizes) return PyLong_FromLong(FASA_ERR_INVALID_ARG);
+    if (!THPVariable_Check(a[7])) {
+      PyErr_SetString(PyExc_ValueError, "token_map must be a tensor");
+      return nullptr;
+    }
+    const int64_t most = THPVariable_Unpack(a[7]).numel() / 4;
+    if (most > INT_MAX) return PyLong_FromLong(FASA_ERR_UNSUPPORTED);
+    bool ok = true;
+    void* have = address(a[0], "have_lens", c.here, at::kInt, c.batch, &ok);
+    void* want = address(a[1], "want_lens", c.here, at::kInt, c.batch, &ok);
+    void* table = address(a[2], "page_table", c.here, at::kInt, c.entries, &ok);
+    void* list = address(a[3], "free_pages", c.here, at::kInt, c.d->n_pages, &ok);
+    void* count = address(a[4], "free_count", c.here, at::kInt, 1, &ok);
+    void* lens = address(a[5], "lens_out", c.here, at::kInt, c.batch, &ok);
+    void* cu_new = address(a[6], "cu_new", c.here, at::kInt, c.batch + 1, &ok);
+    void* map = address(a[7], "token_map", c.here, at::kInt, 4 * most, &ok);
+    void* pos = optional(a[8], "pos", c.here, at::kInt, c.batch, &ok);
+    void* left = optional(a[9], "free_count_out", c.here, at::kInt, 1, &ok);
+    if (!ok) return nullptr;
+    if (a[9] == Py_None) left = count;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = c_assign((const int32_t*)have, (const int32_t*)want, (const int32_t*)pos, (int32_t*)table, (int32_t*)list,
+                  (const int32_t*)count, (int32_t*)lens, (int32_t*)left, (int32_t*)cu_new, (int32_t*)map, (int32_t)most,
+                  c.d, c.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// rope_append(q, k, v, token_map, q_out, k_pages, v_pages, weight, token_pos, rope, dims, stream)
+PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c;
+    if (!counted(n, 12) || !c.read(a[10], a[11])) return nullptr;
+    const fasa_rope_t* rope = static_cast<const fasa_rope_t*>(PyLong_AsVoidPtr(a[9]));
+    if (!rope) {
+      if (!PyErr_Occurred()) PyErr_SetString(PyExc_ValueError, "rope is missing");
+      return nullptr;
+    }
+    if (!c.sizes) return PyLong_FromLong(FASA_ERR_INVALID_ARG);
+    bool ok = true;
+    int64_t tokens = -1, stride[3] = {0, 0, 0};
+    const bool none_q = a[0] == Py_None, none_k = a[1] == Py_None && a[2] == Py_None;
+    if (none_q != (a[4] == Py_None) || none_k != (a[5] == Py_None && a[6] == Py_None)) {
+      PyErr_SetString(PyExc_ValueError, "q goes with q_out, k and v with k_pages and v_pages");
+      return nullptr;
+    }
+    if (none_q && none_k) return PyLong_FromLong(FASA_OK);
+    void *q = nullptr, *q_out = nullptr, *k = nullptr, *v = nullptr, *kp = nullptr, *vp = nullptr;
+    if (!none_q) {
+      q = strided(a[0], "q", c.here, c.store, &tokens, c.d->n_q_heads, c.d->head_dim, &stride[0], &ok);
+      q_out = address(a[4], "q_out", c.here, c.store, tokens * c.d->n_q_heads * c.d->head_dim, &ok);
+    }
+    if (!none_k) {
+      k = strided(a[1], "k", c.here, c.store, &tokens, c.d->n_kv_heads, c.d->head_dim, &stride[1], &ok);
+      v = strided(a[2], "v", c.here, c.store, &tokens, c.d->n_kv_heads, c.d->head_dim, &stride[2], &ok);
+      kp = address(a[5], "k_pages", c.here, c.store, c.pool, &ok);
+      vp = address(a[6], "v_pages", c.here, c.store, c.pool, &ok);
+    }
+    if (ok && tokens > INT_MAX) return PyLong_FromLong(FASA_ERR_UNSUPPORTED);
+    void* map = address(a[3], "token_map", c.here, at::kInt, 4 * tokens, &ok);
+    void* weight = optional(a[7], "weight", c.here, at::kFloat, c.slots, &ok);
+    void* token_pos = optional(a[8], "token_pos", c.here, at::kInt, c.slots, &ok);
+    if (!ok) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = c_rope_append(q, stride[0], k, stride[1], v, stride[2], (const int32_t*)map, (int32_t)tokens, q_out, kp, vp,
+                       (float*)weight, (int32_t*)token_pos, rope, c.d, c.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
+// chunk(q, k_pages, v_pages, page_table, seq_lens, out, cu_new, weight, workspace, dims, stream)
+PyObject* chunk(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded([&]() -> PyObject* {
+    Call c;
+    if (!counted(n, 11) || !c.read(a[9], a[10])) return nullptr;
+    if (!c.sizes) return PyLong_FromLong(FASA_ERR_INVALID_ARG);
+    if (!THPVariable_Check(a[0])) {
+      PyErr_SetString(PyExc_ValueError, "q must be a tensor");
+      return nullptr;
+    }
+    const int64_t row = (int64_t)c.d->n_q_heads * c.d->head_dim, tokens = THPVariable_Unpack(a[0]).numel() / row;
+    if (tokens > INT_MAX) return PyLong_FromLong(FASA_ERR_UNSUPPORTED);
+    bool ok = true;
+    size_t bytes = 0;
+    void* q = address(a[0], "q", c.here, c.store, tokens * row, &ok);
+    void* k_pages = address(a[1], "k_pages", c.here, c.store, c.pool, &ok);
+    void* v_pages = address(a[2], "v_pages", c.here, c.store, c.pool, &ok);
+    void* table = address(a[3], "page_table", c.here, at::kInt, c.entries, &ok);
+    void* lens = address(a[4], "seq_lens", c.here, at::kInt, c.batch, &ok);
+    void* out = address(a[5], "out", c.here, c.store, tokens * row, &ok);
+    void* cu_new = optional(a[6], "cu_new", c.here, at::kInt, c.batch + 1, &ok);
+    void* weight = optional(a[7], "weight", c.here, at::kFloat, c.slots, &ok);
+    void* workspace = room(a[8], c.here, &bytes, &ok);
+    if (!ok) return nullptr;
+    int st;
+    Py_BEGIN_ALLOW_THREADS;
+    st = c_chunk(q, (int32_t)tokens, (const int32_t*)cu_new, k_pages, v_pages, (const int32_t*)table,
+                 (const int32_t*)lens, out, (float*)weight, workspace, bytes, c.d, c.stream);
+    Py_END_ALLOW_THREADS;
+    return PyLong_FromLong(st);
+  });
+}
+
 PyMethodDef methods[] = {
     {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(bind)), METH_FASTCALL, nullptr},
     {"append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(append)), METH_FASTCALL, nullptr},
     {"attention", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(attention)), METH_FASTCALL, nullptr},
     {"evict", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(evict)), METH_FASTCALL, nullptr},
+    {"assign", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(assign)), METH_FASTCALL, nullptr},
+    {"rope_append", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(rope_append)), METH_FASTCALL, nullptr},
+    {"chunk", reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(chunk)), METH_FASTCALL, nullptr},
     {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_fasa_torch", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};

@@ -25,7 +25,8 @@ EXPORTS = [
     "fasa_select_dominant_fcs", "fasa_compound_agreement", "fasa_test_fault_injection", "fasa_step_kernel",
     "fasa_build_knondom", "fasa_decode_step_split", "fasa_decode_step_append_split",
     "fasa_paged_append", "fasa_paged_attention", "fasa_paged_evict", "fasa_paged_workspace_size",
-    "fasa_paged_evict_workspace_size",
+    "fasa_paged_evict_workspace_size", "fasa_paged_assign", "fasa_paged_rope_append", "fasa_paged_chunk_attention",
+    "fasa_paged_chunk_workspace_size",
 ]
 
 
@@ -80,7 +81,7 @@ def lib():
             raise RuntimeError(f"{_LIB_PATH} is missing: build it with "
                                "`python -m kv_cache_token_tip_gb300.build` (there is no fallback)")
         L = ctypes.CDLL(_LIB_PATH)
-        vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
         dp = ctypes.POINTER(FasaDims)
         sig = {
             "fasa_version": ([], ctypes.c_int),
@@ -122,6 +123,11 @@ def lib():
             "fasa_paged_evict_workspace_size": ([pp, i32, ctypes.POINTER(sz)], ctypes.c_int),
             "fasa_paged_evict": ([vp, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, sz, pp, vp],
                                  ctypes.c_int),
+            "fasa_paged_assign": ([vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, i32, pp, vp], ctypes.c_int),
+            "fasa_paged_rope_append": ([vp, i64, vp, i64, vp, i64, vp, i32, vp, vp, vp, vp, vp,
+                                        ctypes.POINTER(FasaRope), pp, vp], ctypes.c_int),
+            "fasa_paged_chunk_workspace_size": ([pp, i32, i32, ctypes.POINTER(sz)], ctypes.c_int),
+            "fasa_paged_chunk_attention": ([vp, i32, vp, vp, vp, vp, vp, vp, vp, vp, sz, pp, vp], ctypes.c_int),
         })
         for name, (args, res) in sig.items():
             fn = getattr(L, name)
@@ -414,7 +420,7 @@ def _marshal():
         if getattr(m, "torch_version", None) != str(torch.__version__):
             raise RuntimeError(f"the module _fasa_torch was built for another torch: {how}")
         m.bind(*(ctypes.cast(getattr(lib(), f"fasa_paged_{n}"), ctypes.c_void_p).value
-                 for n in ("append", "attention", "evict")))
+                 for n in ("append", "attention", "evict", "assign", "rope_append", "chunk_attention")))
         _native = m
     return _native
 
@@ -480,6 +486,84 @@ def fasa_paged_evict(weight, token_pos, pos, k_pages, v_pages, page_table, seq_l
                                        None if stream is None else _stream(stream))
     if st:
         _check("fasa_paged_evict", st)
+
+
+# ------------------------------------------------ a step of new tokens, paged
+FASA_ROPE_INTERLEAVED, FASA_ROPE_HALF = 0, 1
+FASA_ROPE_PLAIN, FASA_ROPE_LINEAR, FASA_ROPE_WAVELENGTH, FASA_ROPE_RAMP = 0, 1, 2, 3
+
+
+class FasaRope(ctypes.Structure):
+    """Rotary positions (include/fasa.h): which elements of a head make a pair,
+    how many of them turn, and how their frequencies are scaled."""
+    _fields_ = [
+        ("layout", ctypes.c_int32), ("rotary_dim", ctypes.c_int32), ("scaling", ctypes.c_int32),
+        ("reserved", ctypes.c_int32), ("rope_theta", ctypes.c_double), ("factor", ctypes.c_double),
+        ("low", ctypes.c_double), ("high", ctypes.c_double), ("original", ctypes.c_double),
+        ("magnitude", ctypes.c_double),
+    ]
+
+    def __init__(self, layout: int = FASA_ROPE_INTERLEAVED, rotary_dim: int = 128, scaling: int = FASA_ROPE_PLAIN,
+                 rope_theta: float = 1e4, factor: float = 1.0, low: float = 1.0, high: float = 4.0,
+                 original: float = 8192.0, magnitude: float = 1.0):
+        super().__init__(layout, rotary_dim, scaling, 0, float(rope_theta), float(factor), float(low), float(high),
+                         float(original), float(magnitude))
+
+
+def fasa_paged_assign(have_lens, want_lens, page_table, free_pages, free_count, lens_out, cu_new, token_map, pos=None,
+                      free_count_out=None, dims: FasaPagedDims = None, stream=None):
+    """Pages for the sequences that grow from have_lens to want_lens, from the
+    end of the list of free ones, and back to it from those that shrink:
+    page_table, free_pages and free_count change in place (the count goes to
+    free_count_out where that is given).  lens_out [B], cu_new [B+1] and
+    token_map [max_tokens, 4] (sequence, slot, page, position of each new token,
+    -1 behind the last) are written; growing sequences are served in order while
+    the pages and the map's rows last.  The first new token of b has the position
+    pos[b], or its slot."""
+    st = (_native or _marshal()).assign(have_lens, want_lens, page_table, free_pages, free_count, lens_out, cu_new,
+                                        token_map, pos, free_count_out, _where(dims),
+                                        None if stream is None else _stream(stream))
+    if st:
+        _check("fasa_paged_assign", st)
+
+
+def fasa_paged_rope_append(q, k, v, token_map, q_out, k_pages, v_pages, weight=None, token_pos=None,
+                           rope: FasaRope = None, dims: FasaPagedDims = None, stream=None):
+    """Turns the new tokens' queries (to q_out [n_tokens, Hq, d]) and keys (to their
+    pages, with the values) by the positions of token_map, and begins their
+    statistics.  q [n_tokens, Hq, d], k and v [n_tokens, Hkv, d] may be parts of
+    wider rows.  q with q_out, or k and v with the pages, may be None."""
+    if not isinstance(rope, FasaRope):
+        raise TypeError("rope must be FasaRope")
+    st = (_native or _marshal()).rope_append(q, k, v, token_map, q_out, k_pages, v_pages, weight, token_pos,
+                                             ctypes.addressof(rope), _where(dims),
+                                             None if stream is None else _stream(stream))
+    if st:
+        _check("fasa_paged_rope_append", st)
+
+
+def fasa_paged_chunk_workspace_size(dims: FasaPagedDims, n_tokens: int, weights: bool = False) -> int:
+    out = ctypes.c_size_t(0)
+    _check("fasa_paged_chunk_workspace_size",
+           lib().fasa_paged_chunk_workspace_size(ctypes.byref(dims), int(n_tokens), int(bool(weights)),
+                                                 ctypes.byref(out)))
+    return out.value
+
+
+def fasa_paged_chunk_attention(q, k_pages, v_pages, page_table, seq_lens, out, cu_new=None, weight=None,
+                               workspace=None, dims: FasaPagedDims = None, stream=None):
+    """Attention of each sequence's new tokens, the last of its seq_lens cached ones,
+    every one over the slots up to its own.  q and out [n_tokens, Hq, d] in the
+    storage dtype, q already turned; those of sequence b are cu_new[b] ..
+    cu_new[b+1], or one per sequence without cu_new.  With weight, each slot's
+    softmax weights are added to it.  Without a workspace one is allocated here."""
+    if workspace is None:
+        per = dims.n_q_heads * dims.head_dim
+        workspace = _scratch(fasa_paged_chunk_workspace_size(dims, q.numel() // max(per, 1), weight is not None), stream)
+    st = (_native or _marshal()).chunk(q, k_pages, v_pages, page_table, seq_lens, out, cu_new, weight, workspace,
+                                       _where(dims), None if stream is None else _stream(stream))
+    if st:
+        _check("fasa_paged_chunk_attention", st)
 
 
 def fasa_device_status(stream=None) -> int:
