@@ -30,10 +30,10 @@ LIBSYNTH = os.path.join(ROOT, "workload", "libfasa_synth.so")
 FASA_SOURCES = [os.path.join(PKG, "csrc", f) for f in
                 ("fasa_api.cu", "fasa_cluster_bf16.cu", "fasa_cluster_f32.cu", "fasa_step_bf16.cu", "fasa_noalloc.cu",
                  "fasa_ca.cu", "fasa_paged.cu", "fasa_paged_attend.cu", "fasa_paged_cache.cu",
-                 "fasa_serve.cu", "fasa_serve_tokens.cu", "fasa_chunk_f32.cu")]
+                 "fasa_serve.cu", "fasa_serve_tokens.cu", "fasa_chunk_f32.cu", "fasa_chunk_bf16.cu")]
 FASA_DEPS = [os.path.join(PKG, "csrc", f) for f in
              ("fasa_cluster.cuh", "fasa_step.cuh", "fasa_ptx.cuh", "fasa_internal.h",
-              "fasa_paged.h", "fasa_paged_index.h", "fasa_serve.h", "fasa_chunk_index.h", "fasa_chunk.cuh")] + [
+              "fasa_paged.h", "fasa_paged_index.h", "fasa_serve.h", "fasa_chunk_index.h", "fasa_chunk.cuh", "fasa_tcgen05.cuh")] + [
     os.path.join(ROOT, "include", "fasa.h")]
 LIBTORCH = os.path.join(PKG, "_fasa_torch" + (sysconfig.get_config_var("EXT_SUFFIX") or ".so"))
 TORCH_SOURCES = [os.path.join(PKG, "csrc", "fasa_torch.cpp")]

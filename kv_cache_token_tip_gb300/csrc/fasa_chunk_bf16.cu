@@ -1,0 +1,462 @@
+// Attention of chunks in bf16 on the 5th-generation tensor cores.  A block takes a
+// part of the line of units (fasa_chunk_index.h): two tiles of up to 128 rows (new
+// tokens times the heads of their group), the slots 128 at a time.
+//
+// Per tile of rows and of slots: S = Q K^T (fp32, tensor memory), P = 2^(scale S - m) by
+// a warpgroup, a row to a thread, back to tensor memory in bf16 over S, O += P V.  m
+// follows the row's maximum only where it rises by more than 2^8: O is seldom scaled, and
+// out = O / sum P is the same.  Roles: two warpgroups with a tile of rows each, a warp
+// that issues the matrix instructions, one that copies.  While one warpgroup works, the
+// tensor cores work for the other.
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <stdint.h>
+
+#include <algorithm>
+#include <atomic>
+#include <mutex>
+
+#include "fasa_chunk.cuh"
+#include "fasa_tcgen05.cuh"
+
+namespace fasa {
+namespace {
+
+constexpr int CB_NT = 384;
+constexpr int CB_K = 128;            // slots of a tile
+constexpr float CB_SLACK = 8.f;      // powers of two that a row's maximum may run ahead of m
+
+template <int D>
+struct CbPlan {
+  static constexpr int HALVES = D / 64;                  // 64-column slabs of a row
+  static constexpr int SLAB = 128 * 128;                 // bytes of one
+  static constexpr int TILE = HALVES * SLAB;             // Q of 128 rows, K or V of 128 slots
+  static constexpr int STAGES = D == 128 ? 4 : 8;        // K and V in turn
+  static constexpr int OFF_RING = 2 * TILE;
+  static constexpr int OFF_BAR = OFF_RING + STAGES * TILE;
+  static constexpr int BARS = 2 * STAGES + 2 + 6 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + BARS * 8;    // tensor memory's address, dead
+  static constexpr int OFF_SCAN = OFF_MISC + 16;
+  static constexpr int OFF_SEQ = (OFF_SCAN + CB_NT / 32 * 8 + 15) / 16 * 16;
+  static constexpr int bytes(int B) { return 1024 + OFF_SEQ + (B + 1) * (int)sizeof(ChunkSeq); }
+  static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
+};
+
+// The tiles of slots [f0, f1) of a unit that tile w of its rows reads: up to e.
+__device__ __forceinline__ int row_tile_end(const ChunkParams& p, const ChunkSeq& q, const ChunkUnit& u, int w, int f0,
+                                            int f1) {
+  const int TQ = 128 / p.G, j0 = (2 * u.i + w) * TQ;
+  if (j0 >= q.n) return f0;
+  const int see = q.len - q.n + min(j0 + TQ, q.n);
+  return max(f0, min(f1, see > 0 ? (see + CB_K - 1) / CB_K : 0));
+}
+
+// Walks this part's segments; f(unit, f0, f1, whole).  The same for every role.
+template <class F>
+__device__ __forceinline__ void segments(const ChunkLine& line, long long y0, long long y1, F&& f) {
+  ChunkUnit u;
+  u.find(line, y0);
+  while (true) {
+    const int f0 = u.before(line, y0), f1 = u.before(line, y1);
+    const bool whole = f0 == 0 && f1 == u.tiles && u.begin >= y0;
+    if (f0 < f1 || whole)
+      if (!f(u, f0, f1, whole)) return;
+    if (u.begin + u.cost >= y1) return;
+    u.next(line);
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(CB_NT, 1)
+    chunk_bf16_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap qmap,
+                      const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  using P = CbPlan<D>;
+  constexpr int S = P::STAGES;
+  extern __shared__ __align__(16) char raw[];
+  char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t base = smem_u32(sm), ring = base + P::OFF_RING, bars = base + P::OFF_BAR;
+  const uint32_t full = bars, empty = bars + 8 * S, q_full = bars + 16 * S, q_empty = q_full + 8;
+  const uint32_t s_full = q_full + 16, p_full = q_full + 32, o_full = q_full + 48;  // of either tile of rows
+  const uint32_t drain = q_full + 64;
+  volatile int* misc = reinterpret_cast<volatile int*>(sm + P::OFF_MISC);
+  ChunkSeq* seqs = reinterpret_cast<ChunkSeq*>(sm + P::OFF_SEQ);
+  const int TQ = 128 / p.G, TU = 2 * TQ;
+  if (warp == 0) tm_alloc(base + P::OFF_MISC, 512);
+  if (tid == 32) {
+    misc[1] = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+    }
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    mbar_init(drain, 1);
+    for (int w = 0; w < 2; ++w) {
+      mbar_init(s_full + 8 * w, 1);
+      mbar_init(p_full + 8 * w, 4);
+      mbar_init(o_full + 8 * w, 1);
+    }
+    fence_mbar_init();
+  }
+  // rows of Q that no copy writes stay zeros
+  for (int i = tid; i < 2 * P::TILE / 16; i += CB_NT) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async();
+  tm_before_sync();
+  paged_wait();
+  paged_go();  // the join reads the lengths
+  chunk_line<CB_NT>(p, seqs, reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, blockIdx.x == 0);
+  tm_after_sync();
+  const uint32_t tm = (uint32_t)misc[0];
+  const ChunkLine line{seqs, p.B, p.Hkv, TU, CB_K};
+  const int parts = line.parts(p.parts), c = blockIdx.x;
+  const Patience patience{misc + 1, p.status, p.wait_ns};
+  if (c < parts) {
+    const long long y0 = line.part_begin(parts, c), y1 = line.part_begin(parts, c + 1);
+    // (384 threads of 168 registers: 256 of 232 and 128 of 40)
+    if (warp < 8) more_registers<232>();
+    else fewer_registers<40>();
+    if (warp < 8) {
+      // ------------------------------------------------ softmax: rows of tile w
+      const int w = warp >> 2, row = tid & 127;
+      const uint32_t here = tm + ((uint32_t)(warp & 3) << 21);  // lanes 32 (warp % 4) ..
+      const uint32_t st = here + 128 * w, ot = here + 256 + 128 * w;
+      const float scale = p.scale;
+      uint32_t s_phase = 0, o_phase = 0;
+      segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool whole) {
+        const ChunkSeq q = seqs[u.b];
+        const int e = row_tile_end(p, q, u, w, f0, f1), j0 = (2 * u.i + w) * TQ;
+        const int j = j0 + row / p.G;
+        const bool live = row < TQ * p.G && j < q.n;
+        const int see = live ? q.len - q.n + j + 1 : 0;
+        // which groups of 16 slots lie in the pool, a tile ahead
+        const int* table = p.page_table + (size_t)u.b * p.max_pages;
+        auto look_up = [&](int t) {
+          const int slot = t * CB_K + 16 * lane;
+          return lane < 8 && slot < q.len ? table[slot >> p.log2_page] : 0;
+        };
+        int page = f0 < e ? look_up(f0) : 0;
+        float m = -INFINITY;
+        uint64_t l2 = 0;  // two sums
+        for (int t = f0; t < e; ++t) {
+          const unsigned held = __ballot_sync(0xffffffffu, page >= 0 && page < p.n_pages);
+          if (t + 1 < e) page = look_up(t + 1);
+          if (!patience.wait(s_full + 8 * w, s_phase)) return false;
+          s_phase ^= 1;
+          tm_after_sync();
+          uint32_t s[128];
+          tm_ld32(st, s);
+          tm_ld32(st + 32, s + 32);
+          tm_ld32(st + 64, s + 64);
+          tm_ld32(st + 96, s + 96);
+          tm_wait_ld();
+          tm_settle(s);
+          const int lim = see - t * CB_K;  // of the tile's slots
+          if (__any_sync(0xffffffffu, lim < CB_K && live) || held != 0xffffffffu) {
+#pragma unroll
+            for (int i = 0; i < 128; ++i)
+              if (i >= lim || !(held >> (i >> 4) & 1u)) s[i] = 0xff800000u;  // -inf
+          }
+          float mx[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) mx[i] = __uint_as_float(s[i]);
+#pragma unroll
+          for (int i = 4; i < 128; i += 4)
+#pragma unroll
+            for (int k = 0; k < 4; ++k) mx[k] = fmaxf(mx[k], __uint_as_float(s[i + k]));
+          const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * scale;
+          if (__any_sync(0xffffffffu, top > m + CB_SLACK)) {
+            const float mn = top > m + CB_SLACK ? top : m;
+            const float a = mn == -INFINITY ? 1.f : ex2(m - mn);
+            m = mn;
+            const uint64_t a2 = pair_of(a, a);
+            l2 = mul2(l2, a2);
+            if (t > f0) {  // (S of this tile was issued behind the last P V: O is at rest)
+#pragma unroll
+              for (int k = 0; k < D; k += 32) {
+                uint32_t o[32];
+                tm_ld32(ot + k, o);
+                tm_wait_ld();
+                tm_settle(o);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * a);
+                tm_st32(ot + k, o);
+              }
+            }
+          }
+          const float ms = m == -INFINITY ? 0.f : -m;
+          const uint64_t scale2 = pair_of(scale, scale), ms2 = pair_of(ms, ms);
+          uint32_t out[64];
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int i = 0; i < 64; ++i) {
+            float x0, x1;
+            unpair(fma2(pair_of(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, ms2), x0, x1);
+            x0 = ex2(x0);
+            x1 = ex2(x1);
+            sum[i & 1] = add2(sum[i & 1], pair_of(x0, x1));
+            out[i] = pack_bf16(x0, x1);
+          }
+          l2 = add2(l2, add2(sum[0], sum[1]));
+          tm_st32(st, out);
+          tm_st32(st + 32, out + 32);
+          tm_wait_st();
+          tm_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(p_full + 8 * w);
+        }
+        // ------------------------------------------------ the rows' results
+        float la, lb;
+        unpair(l2, la, lb);
+        const float l = la + lb;
+        if (f0 < e) {
+          if (!patience.wait(o_full + 8 * w, o_phase)) return false;
+          o_phase ^= 1;
+          tm_after_sync();
+        }
+        const int r = w * TQ * p.G + row;  // of the unit
+        const ChunkRow at(p, u, first_row(p, u.b), TU, r);
+        const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        float* rec = chunk_record(p, D, c, f0 > 0 ? 0 : 1);
+#pragma unroll
+        for (int k = 0; k < D; k += 32) {
+          uint32_t o[32];
+          if (f0 < e) {
+            tm_ld32(ot + k, o);
+            tm_wait_ld();
+            tm_settle(o);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) o[i] = 0u;
+          }
+          if (live && whole) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at.out(p, D) + k);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t x[4];
+#pragma unroll
+              for (int h = 0; h < 4; ++h)
+                x[h] = pack_bf16(__uint_as_float(o[8 * i + 2 * h]) * inv, __uint_as_float(o[8 * i + 2 * h + 1]) * inv);
+              to[i] = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+          } else if (live) {
+            // (a row of 130 floats begins on 8 bytes; o's rows lie D apart, whole 16-byte words)
+            uint4* to = reinterpret_cast<uint4*>(rec + (size_t)r * D + k);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+          }
+        }
+        tm_before_sync();  // (the next unit's first P is behind this)
+        if (live && whole && p.weight) p.lse[at.lse(p)] = chunk_lse(m, l);
+        if (live && !whole) {
+          rec[(size_t)p.rows * D + r] = m;
+          rec[(size_t)p.rows * (D + 1) + r] = l;
+        }
+        return true;
+      });
+    } else if (warp == 8) {
+      // ------------------------------------------------ matrix instructions
+      constexpr uint32_t kind_s = mma_bf16_kind(CB_K, false), kind_o = mma_bf16_kind(D, true);
+      uint32_t q_phase = 0, p_phase[2] = {0, 0};
+      int k = 0;  // tiles of the ring so far
+      auto at = [&](int i) { return ring + (i % S) * P::TILE; };
+      auto landed = [&](int i) { return patience.wait(full + 8 * (i % S), (i / S) & 1); };
+      auto scores = [&](int w, int i) {  // S of row tile w with the K of ring tile i
+        if (lane == 0) {
+#pragma unroll
+          for (int x = 0; x < D / 16; ++x) {
+            const uint32_t off = (x >> 2) * P::SLAB + (x & 3) * 32;
+            mma_ss(tm + 128 * w, mma_operand(base + w * P::TILE + off, 0), mma_operand(at(i) + off, 0), kind_s, x > 0);
+          }
+          mma_commit(s_full + 8 * w);
+        }
+        __syncwarp();
+      };
+      auto free_tile = [&](uint32_t bar) {
+        if (lane == 0) mma_commit(bar);
+        __syncwarp();
+      };
+      segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool) {
+        const ChunkSeq q = seqs[u.b];
+        const int e0 = row_tile_end(p, q, u, 0, f0, f1), e1 = row_tile_end(p, q, u, 1, f0, f1);
+        const int e[2] = {e0, e1}, end = max(e0, e1);
+        if (f0 == end) return true;
+        if (!patience.wait(q_full, q_phase)) return false;
+        q_phase ^= 1;
+        if (!landed(k)) return false;
+#pragma unroll
+        for (int w = 0; w < 2; ++w)
+          if (f0 < e[w]) scores(w, k);
+        free_tile(empty + 8 * (k % S));
+        if (f0 + 1 == end) free_tile(q_empty);
+        for (int t = f0; t < end; ++t, k += 2) {
+          if (!landed(k + 1)) return false;
+          if ((t + 1) * CB_K > q.len) {
+            // slots behind the end hold anything: V's rows are cleared, up to the pages' end
+            // (what lies behind that was not copied and is 0)
+            const int n = q.len - t * CB_K;
+            for (int i = lane; i < (CB_K - n) * P::HALVES * 8; i += 32) {
+              const int r = n + i / (P::HALVES * 8), ch = i % (P::HALVES * 8);
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(k + 1) + (ch >> 3) * P::SLAB + r * 128 +
+                                                                            ((ch & 7) << 4)),
+                           "r"(0)
+                           : "memory");
+            }
+            fence_proxy_async();
+            __syncwarp();
+          }
+          const bool more = t + 1 < end;
+#pragma unroll
+          for (int w = 0; w < 2; ++w) {
+            if (t < e[w]) {
+              if (!patience.wait(p_full + 8 * w, p_phase[w])) return false;
+              p_phase[w] ^= 1;
+              tm_after_sync();
+              if (lane == 0) {
+#pragma unroll
+                for (int x = 0; x < CB_K / 16; ++x)
+                  mma_ts(tm + 256 + 128 * w, tm + 128 * w + 8 * x, mma_operand(at(k + 1) + 2048 * x, P::SLAB), kind_o,
+                         t > f0 || x > 0);
+                if (t + 1 == e[w]) mma_commit(o_full + 8 * w);
+              }
+              __syncwarp();
+            }
+            if (w == 1) free_tile(empty + 8 * ((k + 1) % S));
+            if (more && w == 0 && !landed(k + 2)) return false;
+            if (t + 1 < e[w]) scores(w, k + 2);
+          }
+          if (more) free_tile(empty + 8 * ((k + 2) % S));
+          if (t + 2 == end) free_tile(q_empty);
+        }
+        return true;
+      });
+    } else if (warp == 9) {
+      // ------------------------------------------------ copies
+      const int box = min(1 << p.log2_page, 128), per = 128 / box;  // rows of a copy, copies of a slab
+      const int none = (int)((long long)p.n_pages * p.Hkv << p.log2_page);  // a row behind the pool: zeros
+      const int mine = lane / P::HALVES, half = lane % P::HALVES;
+      uint32_t q_phase = 1;
+      int k = 0, n_tile = 0, n_unit = 0;
+      fence_proxy_async_global();  // (a kernel before this one may have stored what is copied)
+      segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool) {
+        const ChunkSeq q = seqs[u.b];
+        const int end = max(row_tile_end(p, q, u, 0, f0, f1), row_tile_end(p, q, u, 1, f0, f1));
+        if (f0 == end) return true;
+        const int first = first_row(p, u.b) + u.i * TU;
+        if (!patience.wait(q_empty, q_phase)) return false;
+        q_phase ^= 1;
+        ++n_unit;
+        if (lane == 0) mbar_arrive_expect_tx(q_full, 2 * P::HALVES * TQ * p.G * 128);
+        __syncwarp();
+        if (lane < 2 * P::HALVES) {
+          const int w = lane / P::HALVES;
+          tma_3d(base + w * P::TILE + half * P::SLAB, &qmap, 64 * half, u.h * p.G, first + w * TQ, q_full);
+        }
+        __syncwarp();
+        const int* table = p.page_table + (size_t)u.b * p.max_pages;
+        auto look_up = [&](int t) {
+          const int slot = t * CB_K + mine * box;
+          return mine < per && slot < q.len ? table[slot >> p.log2_page] : -1;
+        };
+        int page = look_up(f0);
+        for (int t = f0; t < end; ++t) {
+          const int slot = t * CB_K + mine * box;
+          long long row = paged_row(page, p.n_pages, p.Hkv, u.h, p.log2_page, slot);
+          if (row < 0 && mine < per && slot < q.len) atomicOr(p.status, 1);
+          if (row < 0) row = none;
+          if (t + 1 < end) page = look_up(t + 1);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv, ++k) {
+            const int st = k % S;
+            if (!patience.wait(empty + 8 * st, (k / S & 1) ^ 1)) return false;
+            if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, P::TILE);
+            __syncwarp();
+            if (mine < per && (n_tile != p.drop_tile || c != 0))  // (test hook: copies that never come)
+              tma_2d(ring + st * P::TILE + half * P::SLAB + mine * box * 128, kv ? &vmap : &kmap, 64 * half, (int)row,
+                     full + 8 * st);
+            __syncwarp();
+          }
+          ++n_tile;
+        }
+        return true;
+      });
+      // After a wait that ran out no copy may land in memory of a block that is gone.
+      if (misc[1]) {
+        bool all = n_unit == 0 || mbar_wait_bounded(q_full, (n_unit - 1) & 1, 8 * p.wait_ns);
+        for (int i = max(0, k - S); i < k; ++i)
+          all = mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, 8 * p.wait_ns) && all;
+        if (!all && lane == 0) atomicOr(p.status, 4);
+      }
+    }
+    if (warp == 8 && misc[1]) {  // nor may matrix instructions be under way when tensor memory goes back
+      if (lane == 0) mma_commit(drain);
+      if (!mbar_wait_bounded(drain, 0, 8 * p.wait_ns) && lane == 0) atomicOr(p.status, 4);
+    }
+  }
+  __syncthreads();
+  if (warp == 0) tm_free(tm, 512);
+}
+
+// A tensor of `n` dimensions (sizes and boxes from the innermost on), bf16 in the
+// 128-byte swizzle.
+cudaError_t tensor_map(CUtensorMap* map, const void* at, int n, const cuuint64_t* dims, const cuuint64_t* strides,
+                       const cuuint32_t* box) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::mutex mu;
+  static Encode encode = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!encode) {
+      void* f = nullptr;
+      cudaDriverEntryPointQueryResult found;
+      const cudaError_t e =
+          cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+      if (e != cudaSuccess) return e;
+      if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorSymbolNotFound;
+      encode = reinterpret_cast<Encode>(f);
+    }
+  }
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void*>(at), dims, strides, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
+  using P = CbPlan<D>;
+  static std::atomic<unsigned long long> allowed{0};  // devices that were told of the shared memory
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!(allowed.load(std::memory_order_acquire) & bit)) {
+    e = cudaFuncSetAttribute(chunk_bf16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::bytes(PAGED_MAX_BATCH));
+    if (e != cudaSuccess) return e;
+    allowed.fetch_or(bit, std::memory_order_release);
+  }
+  const int TQ = 128 / p.G;
+  CUtensorMap qm, km, vm;
+  const cuuint64_t qd[3] = {D, (cuuint64_t)p.Hq, (cuuint64_t)p.n_tokens}, qs[2] = {D * 2, (cuuint64_t)p.Hq * D * 2};
+  const cuuint32_t qb[3] = {64, (cuuint32_t)p.G, (cuuint32_t)TQ};
+  e = tensor_map(&qm, p.q, 3, qd, qs, qb);
+  const cuuint64_t kd[2] = {D, ((cuuint64_t)p.n_pages * p.Hkv) << p.log2_page}, ks[1] = {D * 2};
+  const cuuint32_t kb[2] = {64, (cuuint32_t)std::min(1 << p.log2_page, 128)};
+  if (e == cudaSuccess) e = tensor_map(&km, p.k_pages, 2, kd, ks, kb);
+  if (e == cudaSuccess) e = tensor_map(&vm, p.v_pages, 2, kd, ks, kb);
+  if (e == cudaSuccess) e = paged_behind(chunk_bf16_kernel<D>, p.parts, CB_NT, P::bytes(p.B), 0, s, p, qm, km, vm);
+  if (e == cudaSuccess) e = launch_chunk_join<__nv_bfloat16, D>(p, 2 * TQ, CB_K, s);
+  if (e == cudaSuccess && p.weight) e = launch_chunk_weight_bf16(p, D, s);
+  return e;
+}
+
+}  // namespace
+
+cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t s) {
+  return head_dim == 128 ? launch<128>(p, s) : launch<64>(p, s);
+}
+
+}  // namespace fasa

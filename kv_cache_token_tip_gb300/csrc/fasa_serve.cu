@@ -106,8 +106,8 @@ void turns_of(const fasa_rope_t& r, unsigned long long (&turns)[64]) {
 // Rows of a record, and the most parts that the work can come to.
 void chunk_plan(const fasa_paged_dims_t* d, int n_tokens, int sms, int* rows, int* parts) {
   const int G = d->n_q_heads / d->n_kv_heads;
-  const ChunkShape s = chunk_shape(d->head_dim, d->dtype == FASA_BF16);
-  const int T = s.rows / G;
+  const ChunkShape s = chunk_shape(d->dtype == FASA_BF16, G);
+  const int T = s.tokens;
   // (whole 16-byte words to a record)
   *rows = ((int)std::min<long long>((long long)T * G, (long long)n_tokens * G) + 3) / 4 * 4;
   // a unit's parts each hold a tile: no more parts than units of the longest cache have tiles
@@ -303,9 +303,3 @@ int fasa_paged_chunk_attention(const void* q, int32_t n_tokens, const int32_t* c
 }
 
 }  // extern "C"
-
-namespace fasa {
-
-ChunkShape chunk_shape(int, bool) { return {64, 64, 1}; }
-
-}  // namespace fasa

@@ -70,16 +70,17 @@ struct ChunkParams {
   int drop_tile;  // test hook: this tile of part 0 is never copied (-1: none)
 };
 
-// Rows that one unit takes at once (queries times the heads of their group), slots of a
-// tile, and parts to an SM, by kernel.
+// Tokens of a unit (their rows: times the heads of their group), slots of a tile, and
+// parts to an SM.
 struct ChunkShape {
-  int rows, tile, per_sm;
+  int tokens, tile, per_sm;
 };
-ChunkShape chunk_shape(int head_dim, bool bf16);
+inline ChunkShape chunk_shape(bool bf16, int G) { return bf16 ? ChunkShape{2 * (128 / G), 128, 1} : ChunkShape{64 / G, 64, 1}; }
 
 cudaError_t launch_paged_assign(const AssignParams& p, int sms, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, bool bf16, bool half, int sms, cudaStream_t s);
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t s);
+cudaError_t launch_chunk_weight_bf16(const ChunkParams& p, int head_dim, cudaStream_t s);
 cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t s);
 
 }  // namespace fasa
