@@ -397,6 +397,292 @@ __global__ void __launch_bounds__(CB_NT, 1)
   if (warp == 0) tm_free(tm, 512);
 }
 
+// ------------------------------------------------------------------ weights
+// weight_t += sum over the rows that see slot t of 2^(scale S - log-sum of the row).  A
+// unit is 256 slots of a (sequence, KV head): two tiles of K as rows of S^T = K Q^T, the
+// rows of Q 128 at a time as its columns, so that a thread adds what one slot gets, in the
+// rows' order.  Units are dealt to the blocks there and back, since their costs fall with
+// the slots (the later, the fewer rows see them).
+template <int D>
+struct CwPlan {
+  using A = CbPlan<D>;
+  static constexpr int STAGES = A::STAGES;
+  static constexpr int OFF_LSE = A::OFF_BAR;
+  static constexpr int OFF_BAR = OFF_LSE + STAGES * 128 * 4;
+  static constexpr int BARS = 4 * STAGES + 2 + 8 + 1;
+  static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
+  static constexpr int OFF_SCAN = (OFF_MISC + 8 + 15) / 16 * 16;
+  static constexpr int OFF_LINE = OFF_SCAN + CB_NT / 32 * 4;
+  static constexpr int bytes(int B) { return 1024 + OFF_LINE + (B + 1) * 4; }
+  static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
+};
+
+// New tokens of a sequence, and where they begin.
+__device__ __forceinline__ int2 chunk_rows(const ChunkParams& p, int b) {
+  if (!p.cu_new) return make_int2(b, 1);
+  const int x0 = p.cu_new[b], x1 = p.cu_new[b + 1];
+  return make_int2(x0, 0 <= x0 && x0 <= x1 && x1 <= p.n_tokens ? x1 - x0 : 0);
+}
+
+struct WeightUnit {
+  int b, h, t0, first, n, len;
+  // The first tile of rows that sees a slot of tile w, and how many tiles there are.
+  __device__ int from(int w, int TQ) const { return t0 + 128 * w < len ? max(0, t0 + 128 * w - (len - n)) / TQ : tiles(TQ); }
+  __device__ int tiles(int TQ) const { return (n + TQ - 1) / TQ; }
+};
+
+// f(unit) for each of this block's units, in order; the same for every role.
+template <class F>
+__device__ __forceinline__ void weight_units(const ChunkParams& p, const int* before, F&& f) {
+  const int total = before[p.B] * p.Hkv, P = gridDim.x, c = blockIdx.x;
+  for (int k = 0;; ++k) {
+    const long long x = (k & 1) ? (long long)(k + 1) * P - 1 - c : (long long)k * P + c;
+    if ((long long)k * P >= total) return;
+    if (x >= total) continue;
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] * p.Hkv <= x) lo = mid;
+      else hi = mid;
+    }
+    const int rem = (int)x - before[lo] * p.Hkv;
+    const int2 rows = chunk_rows(p, lo);
+    WeightUnit u{lo, rem % p.Hkv, rem / p.Hkv * 256, rows.x, rows.y, min(max(p.seq_lens[lo], 0), p.T_cap)};
+    if (!f(u)) return;
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(CB_NT, 1)
+    chunk_weight_bf16_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap qmap,
+                             const __grid_constant__ CUtensorMap kmap) {
+  using P = CwPlan<D>;
+  using A = CbPlan<D>;
+  constexpr int S = P::STAGES;
+  extern __shared__ __align__(16) char raw[];
+  char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
+  const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+  const uint32_t base = smem_u32(sm), ring = base + A::OFF_RING, bars = base + P::OFF_BAR;
+  const uint32_t full = bars, empty = bars + 8 * S, lse_full = bars + 16 * S, lse_empty = bars + 24 * S;
+  const uint32_t k_full = bars + 32 * S, k_empty = k_full + 8, t_full = k_full + 16, t_empty = k_full + 48;  // [w][2]
+  const uint32_t drain = k_full + 80;
+  volatile int* misc = reinterpret_cast<volatile int*>(sm + P::OFF_MISC);
+  float* lse = reinterpret_cast<float*>(sm + P::OFF_LSE);
+  int* scan = reinterpret_cast<int*>(sm + P::OFF_SCAN);
+  int* before = reinterpret_cast<int*>(sm + P::OFF_LINE);
+  const int TQ = 128 / p.G;
+  if (warp == 0) tm_alloc(base + P::OFF_MISC, 512);
+  if (tid == 32) {
+    misc[1] = 0;
+    for (int i = 0; i < S; ++i) {
+      mbar_init(full + 8 * i, 1);
+      mbar_init(empty + 8 * i, 1);
+      mbar_init(lse_full + 8 * i, 1);
+      mbar_init(lse_empty + 8 * i, 8);
+    }
+    mbar_init(k_full, 1);
+    mbar_init(k_empty, 1);
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(t_full + 8 * i, 1);
+      mbar_init(t_empty + 8 * i, 4);
+    }
+    mbar_init(drain, 1);
+    fence_mbar_init();
+  }
+  // rows of Q that no copy writes stay zeros
+  for (int i = tid; i < S * A::TILE / 16; i += CB_NT) reinterpret_cast<uint4*>(sm + A::OFF_RING)[i] = make_uint4(0u, 0u, 0u, 0u);
+  fence_proxy_async();
+  tm_before_sync();
+  paged_go();
+  paged_wait();
+  {  // pairs of tiles of slots, before each sequence
+    const int run = (p.B + CB_NT - 1) / CB_NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      before[b] = sum;
+      if (chunk_rows(p, b).y > 0) sum += (min(max(p.seq_lens[b], 0), p.T_cap) + 255) / 256;
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += y;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int pre = incl - sum;
+    for (int v = 0; v < CB_NT / 32; ++v) pre += v < warp ? scan[v] : 0;
+    for (int b = b0; b < b1; ++b) before[b] += pre;
+    if (tid == CB_NT - 1) before[p.B] = pre + sum;
+    __syncthreads();
+  }
+  tm_after_sync();
+  const uint32_t tm = (uint32_t)misc[0];
+  const Patience patience{misc + 1, p.status, p.wait_ns};
+  // (384 threads of 168 registers: 256 of 232 and 128 of 40)
+  if (warp < 8) more_registers<232>();
+  else fewer_registers<40>();
+  if (warp < 8) {
+    // -------------------------------------------------- a slot to a thread
+    const int w = warp >> 2, row = tid & 127;
+    const uint32_t here = tm + ((uint32_t)(warp & 3) << 21) + 256 * w;
+    const float scale = p.scale;
+    int k = 0, buf = 0;  // Q tiles, and S tiles of this warpgroup, so far
+    weight_units(p, before, [&](const WeightUnit& u) {
+      const int slot = u.t0 + 128 * w + row, from = u.from(0, TQ), mine = u.from(w, TQ), tiles = u.tiles(TQ);
+      int page = -1;
+      if (slot < u.len) page = p.page_table[(size_t)u.b * p.max_pages + (slot >> p.log2_page)];
+      float* weight = p.weight + ((size_t)u.b * p.Hkv + u.h) * p.T_cap + slot;
+      const bool live = page >= 0 && page < p.n_pages;
+      const float old = live ? *weight : 0.f;
+      float total = 0.f;
+      for (int i = from; i < tiles; ++i, ++k) {
+        const int st = k % S;
+        if (!patience.wait(lse_full + 8 * st, (k / S) & 1)) return false;
+        if (i >= mine) {
+          if (!patience.wait(t_full + 8 * (2 * w + (buf & 1)), (buf >> 1) & 1)) return false;
+          tm_after_sync();
+          uint32_t s[128];
+          const uint32_t at = here + 128 * (buf & 1);
+          tm_ld32(at, s);
+          tm_ld32(at + 32, s + 32);
+          tm_ld32(at + 64, s + 64);
+          tm_ld32(at + 96, s + 96);
+          tm_wait_ld();
+          tm_settle(s);
+          tm_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(t_empty + 8 * (2 * w + (buf & 1)));
+          ++buf;
+          // the rows of this tile that there are, and of them the first that sees the slot
+          const int rows = min(TQ, u.n - i * TQ) * p.G, lo = (slot - (u.len - u.n) - i * TQ) * p.G;
+          if (rows < TQ * p.G || __any_sync(0xffffffffu, lo > 0)) {
+#pragma unroll
+            for (int x = 0; x < 128; ++x)
+              if (x < lo || x >= rows) s[x] = 0xff800000u;  // -inf
+          }
+          const uint64_t scale2 = pair_of(scale, scale);
+          const float4* l4 = reinterpret_cast<const float4*>(lse + 128 * st);  // (negative log-sums)
+          uint64_t sum[2] = {0, 0};
+#pragma unroll
+          for (int x = 0; x < 32; ++x) {
+            const float4 l = l4[x];
+            float a0, a1, b0, b1;
+            unpair(fma2(pair_of(__uint_as_float(s[4 * x]), __uint_as_float(s[4 * x + 1])), scale2, pair_of(l.x, l.y)), a0, a1);
+            unpair(fma2(pair_of(__uint_as_float(s[4 * x + 2]), __uint_as_float(s[4 * x + 3])), scale2, pair_of(l.z, l.w)), b0, b1);
+            sum[0] = add2(sum[0], pair_of(ex2(a0), ex2(a1)));
+            sum[1] = add2(sum[1], pair_of(ex2(b0), ex2(b1)));
+          }
+          float a, b;
+          unpair(add2(sum[0], sum[1]), a, b);
+          total += a + b;
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(lse_empty + 8 * st);
+      }
+      if (live && total != 0.f) *weight = old + total;
+      return true;
+    });
+  } else if (warp == 8) {
+    // -------------------------------------------------- matrix instructions
+    constexpr uint32_t kind = mma_bf16_kind(128, false);
+    uint32_t k_phase = 0;
+    int k = 0, buf[2] = {0, 0};
+    weight_units(p, before, [&](const WeightUnit& u) {
+      const int from[2] = {u.from(0, TQ), u.from(1, TQ)}, tiles = u.tiles(TQ);
+      if (from[0] >= tiles) return true;
+      if (!patience.wait(k_full, k_phase)) return false;
+      k_phase ^= 1;
+      for (int i = from[0]; i < tiles; ++i, ++k) {
+        const int st = k % S;
+        if (!patience.wait(full + 8 * st, (k / S) & 1)) return false;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          if (i < from[w]) continue;
+          const int b = 2 * w + (buf[w] & 1);
+          if (!patience.wait(t_empty + 8 * b, ((buf[w] >> 1) & 1) ^ 1)) return false;
+          ++buf[w];
+          tm_after_sync();
+          if (lane == 0) {
+#pragma unroll
+            for (int x = 0; x < D / 16; ++x) {
+              const uint32_t off = (x >> 2) * A::SLAB + (x & 3) * 32;
+              mma_ss(tm + 128 * b, mma_operand(base + w * A::TILE + off, 0), mma_operand(ring + st * A::TILE + off, 0), kind,
+                     x > 0);
+            }
+            mma_commit(t_full + 8 * b);
+          }
+          __syncwarp();
+        }
+        if (lane == 0) mma_commit(empty + 8 * st);
+        __syncwarp();
+      }
+      if (lane == 0) mma_commit(k_empty);
+      __syncwarp();
+      return true;
+    });
+  } else if (warp == 9) {
+    // -------------------------------------------------- copies
+    const int box = min(1 << p.log2_page, 128), per = 128 / box;
+    const int none = (int)((long long)p.n_pages * p.Hkv << p.log2_page);
+    uint32_t k_phase = 1;
+    int k = 0, n_unit = 0;
+    fence_proxy_async_global();
+    weight_units(p, before, [&](const WeightUnit& u) {
+      const int from = u.from(0, TQ), tiles = u.tiles(TQ);
+      if (from >= tiles) return true;
+      // K: lane = (tile, box, half)
+      const int half = lane % A::HALVES, mine = lane / A::HALVES % per, w = lane / A::HALVES / per;
+      const int slot = u.t0 + 128 * w + mine * box;
+      long long row = -1;
+      if (w < 2 && slot < u.len)
+        row = paged_row(p.page_table[(size_t)u.b * p.max_pages + (slot >> p.log2_page)], p.n_pages, p.Hkv, u.h,
+                        p.log2_page, slot);
+      if (row < 0) row = none;
+      if (!patience.wait(k_empty, k_phase)) return false;
+      k_phase ^= 1;
+      ++n_unit;
+      if (lane == 0) mbar_arrive_expect_tx(k_full, 2 * A::TILE);
+      __syncwarp();
+      if (w < 2) tma_2d(base + w * A::TILE + half * A::SLAB + mine * box * 128, &kmap, 64 * half, (int)row, k_full);
+      __syncwarp();
+      for (int i = from; i < tiles; ++i, ++k) {
+        const int st = k % S, rows = min(TQ, u.n - i * TQ) * p.G;
+        const float* from_lse = p.lse + ((size_t)u.h * p.n_tokens + u.first + i * TQ) * p.G;
+        float l[4];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) l[x] = lane + 32 * x < rows ? -ld_cg(from_lse + lane + 32 * x) : -INFINITY;
+        if (!patience.wait(lse_empty + 8 * st, (k / S & 1) ^ 1)) return false;
+        if (!patience.wait(empty + 8 * st, (k / S & 1) ^ 1)) return false;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) lse[128 * st + lane + 32 * x] = l[x];
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(lse_full + 8 * st);
+          mbar_arrive_expect_tx(full + 8 * st, A::HALVES * TQ * p.G * 128);
+        }
+        __syncwarp();
+        if (lane < A::HALVES)
+          tma_3d(ring + st * A::TILE + lane * A::SLAB, &qmap, 64 * lane, u.h * p.G, u.first + i * TQ, full + 8 * st);
+        __syncwarp();
+      }
+      return true;
+    });
+    if (misc[1]) {  // (as above)
+      bool all = n_unit == 0 || mbar_wait_bounded(k_full, (n_unit - 1) & 1, 8 * p.wait_ns);
+      for (int i = max(0, k - S); i < k; ++i)
+        all = mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, 8 * p.wait_ns) && all;
+      if (!all && lane == 0) atomicOr(p.status, 4);
+    }
+  }
+  if (warp == 8 && misc[1]) {
+    if (lane == 0) mma_commit(drain);
+    if (!mbar_wait_bounded(drain, 0, 8 * p.wait_ns) && lane == 0) atomicOr(p.status, 4);
+  }
+  __syncthreads();
+  if (warp == 0) tm_free(tm, 512);
+}
+
 // A tensor of `n` dimensions (sizes and boxes from the innermost on), bf16 in the
 // 128-byte swizzle.
 cudaError_t tensor_map(CUtensorMap* map, const void* at, int n, const cuuint64_t* dims, const cuuint64_t* strides,
@@ -435,6 +721,9 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
   if (!(allowed.load(std::memory_order_acquire) & bit)) {
     e = cudaFuncSetAttribute(chunk_bf16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, P::bytes(PAGED_MAX_BATCH));
+    if (e == cudaSuccess)
+      e = cudaFuncSetAttribute(chunk_weight_bf16_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                               CwPlan<D>::bytes(PAGED_MAX_BATCH));
     if (e != cudaSuccess) return e;
     allowed.fetch_or(bit, std::memory_order_release);
   }
@@ -449,7 +738,8 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   if (e == cudaSuccess) e = tensor_map(&vm, p.v_pages, 2, kd, ks, kb);
   if (e == cudaSuccess) e = paged_behind(chunk_bf16_kernel<D>, p.parts, CB_NT, P::bytes(p.B), 0, s, p, qm, km, vm);
   if (e == cudaSuccess) e = launch_chunk_join<__nv_bfloat16, D>(p, 2 * TQ, CB_K, s);
-  if (e == cudaSuccess && p.weight) e = launch_chunk_weight_bf16(p, D, s);
+  if (e == cudaSuccess && p.weight)
+    e = paged_behind(chunk_weight_bf16_kernel<D>, p.sms, CB_NT, CwPlan<D>::bytes(p.B), 0, s, p, qm, km);
   return e;
 }
 

@@ -313,15 +313,5 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t s) {
   return head_dim == 128 ? launch<float, 128>(p, s) : launch<float, 64>(p, s);
 }
-template <int D>
-cudaError_t weights_bf16(const ChunkParams& p, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(chunk_simt_weight_kernel<__nv_bfloat16, D>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, CfPlan<D>::OFF_SCAN);
-  const long long units = (long long)p.B * p.Hkv * ((p.T_cap + CF_K - 1) / CF_K);
-  return e != cudaSuccess ? e : paged_behind(chunk_simt_weight_kernel<__nv_bfloat16, D>, (unsigned)(units < 4096 ? units : 4096), CF_NT, CfPlan<D>::OFF_SCAN, 0, s, p);
-}
-cudaError_t launch_chunk_weight_bf16(const ChunkParams& p, int head_dim, cudaStream_t s) {
-  return head_dim == 128 ? weights_bf16<128>(p, s) : weights_bf16<64>(p, s);
-}
 
 }  // namespace fasa

@@ -291,6 +291,7 @@ int fasa_paged_chunk_attention(const void* q, int32_t n_tokens, const int32_t* c
   p.weight = weight;
   p.scale = (float)(1.4426950408889634 / sqrt((double)dims->head_dim));
   chunk_plan(dims, n_tokens, sms, &p.rows, &p.parts);
+  p.sms = sms;
   p.records = static_cast<float*>(workspace);
   p.lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + records_bytes(p.rows, p.parts, dims->head_dim));
   p.status = status;

@@ -65,6 +65,7 @@ struct ChunkParams {
   float* lse;      // [Hkv][n_tokens * G]
   int rows;        // of a record
   int parts;       // most parts of this launch
+  int sms;
   int* status;
   unsigned long long wait_ns;
   int drop_tile;  // test hook: this tile of part 0 is never copied (-1: none)
@@ -80,7 +81,6 @@ inline ChunkShape chunk_shape(bool bf16, int G) { return bf16 ? ChunkShape{2 * (
 cudaError_t launch_paged_assign(const AssignParams& p, int sms, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, bool bf16, bool half, int sms, cudaStream_t s);
 cudaError_t launch_chunk_f32(const ChunkParams& p, int head_dim, cudaStream_t s);
-cudaError_t launch_chunk_weight_bf16(const ChunkParams& p, int head_dim, cudaStream_t s);
 cudaError_t launch_chunk_bf16(const ChunkParams& p, int head_dim, cudaStream_t s);
 
 }  // namespace fasa
