@@ -96,37 +96,53 @@ template <typename T, int D>
 __global__ void __launch_bounds__(CJ_NT) chunk_join_kernel(const __grid_constant__ ChunkParams p, int T_unit, int KT) {
   extern __shared__ __align__(16) ChunkSeq seqs[];
   __shared__ long long scan[CJ_NT / 32];
+  __shared__ int before[2 * CHUNK_MAX_SMS + 2];
   chunk_line<CJ_NT>(p, seqs, scan, T_unit, false);
   const ChunkLine line{seqs, p.B, p.Hkv, T_unit, KT};
   const int parts = line.parts(p.parts), c = blockIdx.x + 1;
   paged_go();
   paged_wait();
   if (c >= parts) return;
-  const long long y = line.part_begin(parts, c);
   ChunkUnit u;
-  u.find(line, y);
-  const int cut = u.before(line, y);
-  if (cut == 0 || cut == u.tiles || u.before(line, line.part_begin(parts, c - 1)) > 0) return;
-  int last = c;  // of the unit's parts
-  while (u.before(line, line.part_begin(parts, last + 1)) < u.tiles) ++last;
+  u.find(line, line.part_begin(parts, c));
+  // tiles of the unit that lie before the cuts c - 1, c, c + 1, ..
+  for (int k = threadIdx.x; k <= parts - c + 1; k += CJ_NT) before[k] = u.before(line, line.part_begin(parts, c - 1 + k));
+  __syncthreads();
+  if (before[0] > 0 || before[1] == 0 || before[1] == u.tiles) return;
   const int n = min(T_unit, seqs[u.b].n - u.i * T_unit) * p.G, first = first_row(p, u.b);
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  constexpr int E = D / 32;
+  constexpr int E = D / 32, U = 4;  // U: parts that a lane has on the way
   for (int r = blockIdx.y * CJ_ROWS + warp; r < min(n, (int)(blockIdx.y + 1) * CJ_ROWS); r += CJ_NT / 32) {
     float M = -INFINITY, L = 0.f, o[E] = {};
-    int done = 0;
-    for (int k = c - 1; k <= last; ++k) {
-      const int upto = k == last ? u.tiles : u.before(line, line.part_begin(parts, k + 1));
-      if (upto == done) continue;  // (a part behind the unit's last tile)
-      done = upto;
-      const float* rec = chunk_record(p, D, k, k == c - 1);
-      const float m = ld_cg(rec + (size_t)p.rows * D + r), l = ld_cg(rec + (size_t)p.rows * (D + 1) + r);
-      const float X = fmaxf(M, m), Xs = X == -INFINITY ? 0.f : X;
-      const float f = exp2f(M - Xs), g = exp2f(m - Xs);
-      M = X;
-      L = L * f + l * g;
+    for (int k0 = 0; before[k0] < u.tiles; k0 += U) {
+      float x[U][E], m[U], l[U];
 #pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = o[e] * f + ld_cg(rec + (size_t)r * D + 32 * e + lane) * g;
+      for (int i = 0; i < U; ++i) {
+        const int k = min(k0 + i, parts - c);
+        // (a part without a tile of the unit left no record)
+        const bool any = k == k0 + i && before[k] < before[k + 1];
+        const float* rec = chunk_record(p, D, c - 1 + k, k == 0);
+        m[i] = any ? ld_cg(rec + (size_t)p.rows * D + r) : -INFINITY;
+        l[i] = any ? ld_cg(rec + (size_t)p.rows * (D + 1) + r) : 0.f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) x[i][e] = any ? ld_cg(rec + (size_t)r * D + 32 * e + lane) : 0.f;
+      }
+      float X = M;
+#pragma unroll
+      for (int i = 0; i < U; ++i) X = fmaxf(X, m[i]);
+      const float Xs = X == -INFINITY ? 0.f : X, f = exp2f(M - Xs);
+      M = X;
+      L *= f;
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] *= f;
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const float g = exp2f(m[i] - Xs);
+        L += l[i] * g;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] += x[i][e] * g;
+      }
+      if (k0 + U > parts - c) break;
     }
     const ChunkRow at(p, u, first, T_unit, r);
     const float inv = L > 0.f ? 1.f / L : 0.f;

@@ -5,9 +5,9 @@
 // Per tile of rows and of slots: S = Q K^T (fp32, tensor memory), P = 2^(scale S - m) by
 // a warpgroup, a row to a thread, back to tensor memory in bf16 over S, O += P V.  m
 // follows the row's maximum only where it rises by more than 2^8: O is seldom scaled, and
-// out = O / sum P is the same.  Roles: two warpgroups with a tile of rows each, a warp
-// that issues the matrix instructions, one that copies.  While one warpgroup works, the
-// tensor cores work for the other.
+// out = O / sum P is the same.  Roles: two warpgroups for each tile of rows, half of a
+// row's columns to a thread, a warp that issues the matrix instructions, one that copies.
+// While the tensor cores work for one tile of rows, its softmax is worked out for the other.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
@@ -22,7 +22,9 @@
 namespace fasa {
 namespace {
 
-constexpr int CB_NT = 384;
+constexpr int CB_NT = 384;           // 8 warps of rows, one of instructions, one of copies, two at rest
+constexpr int CB_ROWS = 8;
+constexpr uint32_t TM = 0;           // where tensor memory begins, which a block takes whole
 constexpr int CB_K = 128;            // slots of a tile
 constexpr float CB_SLACK = 8.f;      // powers of two that a row's maximum may run ahead of m
 
@@ -34,7 +36,7 @@ struct CbPlan {
   static constexpr int STAGES = D == 128 ? 4 : 8;        // K and V in turn
   static constexpr int OFF_RING = 2 * TILE;
   static constexpr int OFF_BAR = OFF_RING + STAGES * TILE;
-  static constexpr int BARS = 2 * STAGES + 2 + 6 + 1;
+  static constexpr int BARS = 2 * STAGES + 2 + 8 + 1;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;    // tensor memory's address, dead
   static constexpr int OFF_SCAN = OFF_MISC + 16;
   static constexpr int OFF_SEQ = (OFF_SCAN + CB_NT / 32 * 8 + 15) / 16 * 16;
@@ -77,8 +79,8 @@ __global__ void __launch_bounds__(CB_NT, 1)
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
   const uint32_t base = smem_u32(sm), ring = base + P::OFF_RING, bars = base + P::OFF_BAR;
   const uint32_t full = bars, empty = bars + 8 * S, q_full = bars + 16 * S, q_empty = q_full + 8;
-  const uint32_t s_full = q_full + 16, p_full = q_full + 32, o_full = q_full + 48;  // of either tile of rows
-  const uint32_t drain = q_full + 64;
+  const uint32_t s_full = q_full + 16, o_full = q_full + 32;  // of either tile of rows
+  const uint32_t p_full = q_full + 48, drain = q_full + 80;          // of either half of its P
   volatile int* misc = reinterpret_cast<volatile int*>(sm + P::OFF_MISC);
   ChunkSeq* seqs = reinterpret_cast<ChunkSeq*>(sm + P::OFF_SEQ);
   const int TQ = 128 / p.G, TU = 2 * TQ;
@@ -94,7 +96,8 @@ __global__ void __launch_bounds__(CB_NT, 1)
     mbar_init(drain, 1);
     for (int w = 0; w < 2; ++w) {
       mbar_init(s_full + 8 * w, 1);
-      mbar_init(p_full + 8 * w, 4);
+      mbar_init(p_full + 16 * w, 4);
+      mbar_init(p_full + 16 * w + 8, 4);
       mbar_init(o_full + 8 * w, 1);
     }
     fence_mbar_init();
@@ -107,19 +110,18 @@ __global__ void __launch_bounds__(CB_NT, 1)
   paged_go();  // the join reads the lengths
   chunk_line<CB_NT>(p, seqs, reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, blockIdx.x == 0);
   tm_after_sync();
-  const uint32_t tm = (uint32_t)misc[0];
   const ChunkLine line{seqs, p.B, p.Hkv, TU, CB_K};
   const int parts = line.parts(p.parts), c = blockIdx.x;
   const Patience patience{misc + 1, p.status, p.wait_ns};
   if (c < parts) {
     const long long y0 = line.part_begin(parts, c), y1 = line.part_begin(parts, c + 1);
     // (384 threads of 168 registers: 256 of 232 and 128 of 40)
-    if (warp < 8) more_registers<232>();
+    if (warp < CB_ROWS) more_registers<232>();
     else fewer_registers<40>();
-    if (warp < 8) {
+    if (warp < CB_ROWS) {
       // ------------------------------------------------ softmax: rows of tile w
       const int w = warp >> 2, row = tid & 127;
-      const uint32_t here = tm + ((uint32_t)(warp & 3) << 21);  // lanes 32 (warp % 4) ..
+      const uint32_t here = TM + ((uint32_t)(warp & 3) << 21);  // lanes 32 (warp % 4) ..
       const uint32_t st = here + 128 * w, ot = here + 256 + 128 * w;
       const float scale = p.scale;
       uint32_t s_phase = 0, o_phase = 0;
@@ -186,24 +188,27 @@ __global__ void __launch_bounds__(CB_NT, 1)
           }
           const float ms = m == -INFINITY ? 0.f : -m;
           const uint64_t scale2 = pair_of(scale, scale), ms2 = pair_of(ms, ms);
-          uint32_t out[64];
-          uint64_t sum[2] = {0, 0};
+          // by halves: the tensor cores begin with the first
 #pragma unroll
-          for (int i = 0; i < 64; ++i) {
-            float x0, x1;
-            unpair(fma2(pair_of(__uint_as_float(s[2 * i]), __uint_as_float(s[2 * i + 1])), scale2, ms2), x0, x1);
-            x0 = ex2(x0);
-            x1 = ex2(x1);
-            sum[i & 1] = add2(sum[i & 1], pair_of(x0, x1));
-            out[i] = pack_bf16(x0, x1);
+          for (int h = 0; h < 2; ++h) {
+            uint32_t out[32];
+            uint64_t sum[2] = {0, 0};
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              float x0, x1;
+              unpair(fma2(pair_of(__uint_as_float(s[64 * h + 2 * i]), __uint_as_float(s[64 * h + 2 * i + 1])), scale2, ms2), x0, x1);
+              x0 = ex2(x0);
+              x1 = ex2(x1);
+              sum[i & 1] = add2(sum[i & 1], pair_of(x0, x1));
+              out[i] = pack_bf16(x0, x1);
+            }
+            l2 = add2(l2, add2(sum[0], sum[1]));
+            tm_st32(st + 32 * h, out);
+            tm_wait_st();
+            tm_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_full + 16 * w + 8 * h);
           }
-          l2 = add2(l2, add2(sum[0], sum[1]));
-          tm_st32(st, out);
-          tm_st32(st + 32, out + 32);
-          tm_wait_st();
-          tm_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(p_full + 8 * w);
         }
         // ------------------------------------------------ the rows' results
         float la, lb;
@@ -254,27 +259,28 @@ __global__ void __launch_bounds__(CB_NT, 1)
         }
         return true;
       });
-    } else if (warp == 8) {
+    } else if (warp == CB_ROWS) {
       // ------------------------------------------------ matrix instructions
       constexpr uint32_t kind_s = mma_bf16_kind(CB_K, false), kind_o = mma_bf16_kind(D, true);
       uint32_t q_phase = 0, p_phase[2] = {0, 0};
       int k = 0;  // tiles of the ring so far
       auto at = [&](int i) { return ring + (i % S) * P::TILE; };
       auto landed = [&](int i) { return patience.wait(full + 8 * (i % S), (i / S) & 1); };
+      // (descriptors count 16 bytes)
+      const uint64_t q_tile = mma_operand(base, 0), k_tile = mma_operand(ring, 0), v_tile = mma_operand(ring, P::SLAB);
       auto scores = [&](int w, int i) {  // S of row tile w with the K of ring tile i
-        if (lane == 0) {
+        const uint64_t a = q_tile + (w * P::TILE >> 4), b = k_tile + ((uint32_t)(i % S) * P::TILE >> 4);
+        if (elected()) {
 #pragma unroll
           for (int x = 0; x < D / 16; ++x) {
-            const uint32_t off = (x >> 2) * P::SLAB + (x & 3) * 32;
-            mma_ss(tm + 128 * w, mma_operand(base + w * P::TILE + off, 0), mma_operand(at(i) + off, 0), kind_s, x > 0);
+            const uint32_t off = ((x >> 2) * P::SLAB + (x & 3) * 32) >> 4;
+            mma_ss(TM + 128 * w, a + off, b + off, kind_s, x > 0);
           }
           mma_commit(s_full + 8 * w);
         }
-        __syncwarp();
       };
       auto free_tile = [&](uint32_t bar) {
-        if (lane == 0) mma_commit(bar);
-        __syncwarp();
+        if (elected()) mma_commit(bar);
       };
       segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool) {
         const ChunkSeq q = seqs[u.b];
@@ -309,17 +315,19 @@ __global__ void __launch_bounds__(CB_NT, 1)
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
             if (t < e[w]) {
-              if (!patience.wait(p_full + 8 * w, p_phase[w])) return false;
-              p_phase[w] ^= 1;
-              tm_after_sync();
-              if (lane == 0) {
+              const uint64_t b = v_tile + ((uint32_t)((k + 1) % S) * P::TILE >> 4);
 #pragma unroll
-                for (int x = 0; x < CB_K / 16; ++x)
-                  mma_ts(tm + 256 + 128 * w, tm + 128 * w + 8 * x, mma_operand(at(k + 1) + 2048 * x, P::SLAB), kind_o,
-                         t > f0 || x > 0);
-                if (t + 1 == e[w]) mma_commit(o_full + 8 * w);
+              for (int h = 0; h < 2; ++h) {
+                if (!patience.wait(p_full + 16 * w + 8 * h, p_phase[w])) return false;
+                tm_after_sync();
+                if (elected()) {
+#pragma unroll
+                  for (int x = 4 * h; x < 4 * h + 4; ++x)
+                    mma_ts(TM + 256 + 128 * w, TM + 128 * w + 8 * x, b + (2048 * x >> 4), kind_o, t > f0 || x > 0);
+                  if (h == 1 && t + 1 == e[w]) mma_commit(o_full + 8 * w);
+                }
               }
-              __syncwarp();
+              p_phase[w] ^= 1;
             }
             if (w == 1) free_tile(empty + 8 * ((k + 1) % S));
             if (more && w == 0 && !landed(k + 2)) return false;
@@ -330,7 +338,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
         }
         return true;
       });
-    } else if (warp == 9) {
+    } else if (warp == CB_ROWS + 1) {
       // ------------------------------------------------ copies
       const int box = min(1 << p.log2_page, 128), per = 128 / box;  // rows of a copy, copies of a slab
       const int none = (int)((long long)p.n_pages * p.Hkv << p.log2_page);  // a row behind the pool: zeros
@@ -388,13 +396,13 @@ __global__ void __launch_bounds__(CB_NT, 1)
         if (!all && lane == 0) atomicOr(p.status, 4);
       }
     }
-    if (warp == 8 && misc[1]) {  // nor may matrix instructions be under way when tensor memory goes back
-      if (lane == 0) mma_commit(drain);
+    if (warp == CB_ROWS && misc[1]) {  // nor may matrix instructions be under way when tensor memory goes back
+      if (elected()) mma_commit(drain);
       if (!mbar_wait_bounded(drain, 0, 8 * p.wait_ns) && lane == 0) atomicOr(p.status, 4);
     }
   }
   __syncthreads();
-  if (warp == 0) tm_free(tm, 512);
+  if (warp == 0) tm_free(TM, 512);
 }
 
 // ------------------------------------------------------------------ weights
@@ -403,6 +411,27 @@ __global__ void __launch_bounds__(CB_NT, 1)
 // rows of Q 128 at a time as its columns, so that a thread adds what one slot gets, in the
 // rows' order.  Units are dealt to the blocks there and back, since their costs fall with
 // the slots (the later, the fewer rows see them).
+constexpr int CW_NT = 640;           // 16 warps of slots, one of instructions, one of copies, two at rest
+constexpr int CW_ROWS = 16;
+
+// Two warps with the two halves of the same rows' columns.
+struct Pair {
+  int id, half;
+  float* at;  // shared memory, 32 floats
+  // Whether either says so.  Also a barrier.
+  __device__ bool either(bool x) const { return named_bar_or(id, 64, x); }
+  // op(x, the other's x), the same in both: in a fixed order.
+  template <class F>
+  __device__ float join(float x, F&& op) const {
+    float* mine = at + (threadIdx.x & 31);
+    if (half) *mine = x;
+    named_bar_sync(id, 64);
+    if (!half) *mine = x = op(x, *mine);
+    named_bar_sync(id, 64);
+    return half ? *mine : x;
+  }
+};
+
 template <int D>
 struct CwPlan {
   using A = CbPlan<D>;
@@ -411,8 +440,8 @@ struct CwPlan {
   static constexpr int OFF_BAR = OFF_LSE + STAGES * 128 * 4;
   static constexpr int BARS = 4 * STAGES + 2 + 8 + 1;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
-  static constexpr int OFF_SCAN = (OFF_MISC + 8 + 15) / 16 * 16;
-  static constexpr int OFF_LINE = OFF_SCAN + CB_NT / 32 * 4;
+  static constexpr int OFF_PAIR = (OFF_MISC + 8 + 15) / 16 * 16;
+  static constexpr int OFF_LINE = OFF_PAIR + CW_ROWS / 2 * 128;
   static constexpr int bytes(int B) { return 1024 + OFF_LINE + (B + 1) * 4; }
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
 };
@@ -453,7 +482,7 @@ __device__ __forceinline__ void weight_units(const ChunkParams& p, const int* be
 }
 
 template <int D>
-__global__ void __launch_bounds__(CB_NT, 1)
+__global__ void __launch_bounds__(CW_NT, 1)
     chunk_weight_bf16_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap qmap,
                              const __grid_constant__ CUtensorMap kmap) {
   using P = CwPlan<D>;
@@ -468,7 +497,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
   const uint32_t drain = k_full + 80;
   volatile int* misc = reinterpret_cast<volatile int*>(sm + P::OFF_MISC);
   float* lse = reinterpret_cast<float*>(sm + P::OFF_LSE);
-  int* scan = reinterpret_cast<int*>(sm + P::OFF_SCAN);
+  int* scan = reinterpret_cast<int*>(sm + P::OFF_PAIR);
   int* before = reinterpret_cast<int*>(sm + P::OFF_LINE);
   const int TQ = 128 / p.G;
   if (warp == 0) tm_alloc(base + P::OFF_MISC, 512);
@@ -478,25 +507,25 @@ __global__ void __launch_bounds__(CB_NT, 1)
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
       mbar_init(lse_full + 8 * i, 1);
-      mbar_init(lse_empty + 8 * i, 8);
+      mbar_init(lse_empty + 8 * i, CW_ROWS);
     }
     mbar_init(k_full, 1);
     mbar_init(k_empty, 1);
     for (int i = 0; i < 4; ++i) {
       mbar_init(t_full + 8 * i, 1);
-      mbar_init(t_empty + 8 * i, 4);
+      mbar_init(t_empty + 8 * i, 8);
     }
     mbar_init(drain, 1);
     fence_mbar_init();
   }
   // rows of Q that no copy writes stay zeros
-  for (int i = tid; i < S * A::TILE / 16; i += CB_NT) reinterpret_cast<uint4*>(sm + A::OFF_RING)[i] = make_uint4(0u, 0u, 0u, 0u);
+  for (int i = tid; i < S * A::TILE / 16; i += CW_NT) reinterpret_cast<uint4*>(sm + A::OFF_RING)[i] = make_uint4(0u, 0u, 0u, 0u);
   fence_proxy_async();
   tm_before_sync();
   paged_go();
   paged_wait();
   {  // pairs of tiles of slots, before each sequence
-    const int run = (p.B + CB_NT - 1) / CB_NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
+    const int run = (p.B + CW_NT - 1) / CW_NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
     int sum = 0;
     for (int b = b0; b < b1; ++b) {
       before[b] = sum;
@@ -511,43 +540,46 @@ __global__ void __launch_bounds__(CB_NT, 1)
     if (lane == 31) scan[warp] = incl;
     __syncthreads();
     int pre = incl - sum;
-    for (int v = 0; v < CB_NT / 32; ++v) pre += v < warp ? scan[v] : 0;
+    for (int v = 0; v < CW_NT / 32; ++v) pre += v < warp ? scan[v] : 0;
     for (int b = b0; b < b1; ++b) before[b] += pre;
-    if (tid == CB_NT - 1) before[p.B] = pre + sum;
+    if (tid == CW_NT - 1) before[p.B] = pre + sum;
     __syncthreads();
   }
   tm_after_sync();
-  const uint32_t tm = (uint32_t)misc[0];
   const Patience patience{misc + 1, p.status, p.wait_ns};
-  // (384 threads of 168 registers: 256 of 232 and 128 of 40)
-  if (warp < 8) more_registers<232>();
-  else fewer_registers<40>();
-  if (warp < 8) {
-    // -------------------------------------------------- a slot to a thread
-    const int w = warp >> 2, row = tid & 127;
-    const uint32_t here = tm + ((uint32_t)(warp & 3) << 21) + 256 * w;
+  // (640 threads of 96 registers: 512 of 104 and 128 of 64)
+  if (warp < CW_ROWS) more_registers<104>();
+  else fewer_registers<64>();
+  if (warp < CW_ROWS) {
+    // -------------------------------------------------- a slot to a thread, half of Q's rows
+    const int w = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
+    const Pair pair{1 + (warp >> 3) * 4 + (warp & 3), half,
+                    reinterpret_cast<float*>(sm + P::OFF_PAIR) + 32 * ((warp >> 3) * 4 + (warp & 3))};
+    const uint32_t here = TM + ((uint32_t)(warp & 3) << 21) + 256 * w + 64 * half;
     const float scale = p.scale;
-    int k = 0, buf = 0;  // Q tiles, and S tiles of this warpgroup, so far
+    int k = 0, buf = 0;  // Q tiles, and S tiles of these rows, so far
     weight_units(p, before, [&](const WeightUnit& u) {
       const int slot = u.t0 + 128 * w + row, from = u.from(0, TQ), mine = u.from(w, TQ), tiles = u.tiles(TQ);
+      if (from >= tiles) return true;
       int page = -1;
       if (slot < u.len) page = p.page_table[(size_t)u.b * p.max_pages + (slot >> p.log2_page)];
       float* weight = p.weight + ((size_t)u.b * p.Hkv + u.h) * p.T_cap + slot;
       const bool live = page >= 0 && page < p.n_pages;
-      const float old = live ? *weight : 0.f;
+      const float old = live && !half ? *weight : 0.f;
       float total = 0.f;
+      bool ok = true;
       for (int i = from; i < tiles; ++i, ++k) {
         const int st = k % S;
-        if (!patience.wait(lse_full + 8 * st, (k / S) & 1)) return false;
+        ok = patience.wait(lse_full + 8 * st, (k / S) & 1);
+        if (!ok) break;
         if (i >= mine) {
-          if (!patience.wait(t_full + 8 * (2 * w + (buf & 1)), (buf >> 1) & 1)) return false;
+          ok = patience.wait(t_full + 8 * (2 * w + (buf & 1)), (buf >> 1) & 1);
+          if (!ok) break;
           tm_after_sync();
-          uint32_t s[128];
+          uint32_t s[64];
           const uint32_t at = here + 128 * (buf & 1);
           tm_ld32(at, s);
           tm_ld32(at + 32, s + 32);
-          tm_ld32(at + 64, s + 64);
-          tm_ld32(at + 96, s + 96);
           tm_wait_ld();
           tm_settle(s);
           tm_before_sync();
@@ -555,17 +587,17 @@ __global__ void __launch_bounds__(CB_NT, 1)
           if (lane == 0) mbar_arrive(t_empty + 8 * (2 * w + (buf & 1)));
           ++buf;
           // the rows of this tile that there are, and of them the first that sees the slot
-          const int rows = min(TQ, u.n - i * TQ) * p.G, lo = (slot - (u.len - u.n) - i * TQ) * p.G;
+          const int rows = min(TQ, u.n - i * TQ) * p.G, lo = (slot - (u.len - u.n) - i * TQ) * p.G - 64 * half;
           if (rows < TQ * p.G || __any_sync(0xffffffffu, lo > 0)) {
 #pragma unroll
-            for (int x = 0; x < 128; ++x)
-              if (x < lo || x >= rows) s[x] = 0xff800000u;  // -inf
+            for (int x = 0; x < 64; ++x)
+              if (x < lo || x >= rows - 64 * half) s[x] = 0xff800000u;  // -inf
           }
           const uint64_t scale2 = pair_of(scale, scale);
-          const float4* l4 = reinterpret_cast<const float4*>(lse + 128 * st);  // (negative log-sums)
+          const float4* l4 = reinterpret_cast<const float4*>(lse + 128 * st + 64 * half);  // (negative log-sums)
           uint64_t sum[2] = {0, 0};
 #pragma unroll
-          for (int x = 0; x < 32; ++x) {
+          for (int x = 0; x < 16; ++x) {
             const float4 l = l4[x];
             float a0, a1, b0, b1;
             unpair(fma2(pair_of(__uint_as_float(s[4 * x]), __uint_as_float(s[4 * x + 1])), scale2, pair_of(l.x, l.y)), a0, a1);
@@ -580,12 +612,15 @@ __global__ void __launch_bounds__(CB_NT, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(lse_empty + 8 * st);
       }
-      if (live && total != 0.f) *weight = old + total;
+      if (pair.either(!ok)) return false;
+      total = pair.join(total, [](float a, float b) { return a + b; });
+      if (live && !half && total != 0.f) *weight = old + total;
       return true;
     });
-  } else if (warp == 8) {
+  } else if (warp == CW_ROWS) {
     // -------------------------------------------------- matrix instructions
     constexpr uint32_t kind = mma_bf16_kind(128, false);
+    const uint64_t k_tile = mma_operand(base, 0), q_tile = mma_operand(ring, 0);  // (descriptors count 16 bytes)
     uint32_t k_phase = 0;
     int k = 0, buf[2] = {0, 0};
     weight_units(p, before, [&](const WeightUnit& u) {
@@ -603,25 +638,22 @@ __global__ void __launch_bounds__(CB_NT, 1)
           if (!patience.wait(t_empty + 8 * b, ((buf[w] >> 1) & 1) ^ 1)) return false;
           ++buf[w];
           tm_after_sync();
-          if (lane == 0) {
+          const uint64_t rows = k_tile + (w * A::TILE >> 4), columns = q_tile + ((uint32_t)st * A::TILE >> 4);
+          if (elected()) {
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
-              const uint32_t off = (x >> 2) * A::SLAB + (x & 3) * 32;
-              mma_ss(tm + 128 * b, mma_operand(base + w * A::TILE + off, 0), mma_operand(ring + st * A::TILE + off, 0), kind,
-                     x > 0);
+              const uint32_t off = ((x >> 2) * A::SLAB + (x & 3) * 32) >> 4;
+              mma_ss(TM + 128 * b, rows + off, columns + off, kind, x > 0);
             }
             mma_commit(t_full + 8 * b);
           }
-          __syncwarp();
         }
-        if (lane == 0) mma_commit(empty + 8 * st);
-        __syncwarp();
+        if (elected()) mma_commit(empty + 8 * st);
       }
-      if (lane == 0) mma_commit(k_empty);
-      __syncwarp();
+      if (elected()) mma_commit(k_empty);
       return true;
     });
-  } else if (warp == 9) {
+  } else if (warp == CW_ROWS + 1) {
     // -------------------------------------------------- copies
     const int box = min(1 << p.log2_page, 128), per = 128 / box;
     const int none = (int)((long long)p.n_pages * p.Hkv << p.log2_page);
@@ -675,12 +707,12 @@ __global__ void __launch_bounds__(CB_NT, 1)
       if (!all && lane == 0) atomicOr(p.status, 4);
     }
   }
-  if (warp == 8 && misc[1]) {
-    if (lane == 0) mma_commit(drain);
+  if (warp == CW_ROWS && misc[1]) {
+    if (elected()) mma_commit(drain);
     if (!mbar_wait_bounded(drain, 0, 8 * p.wait_ns) && lane == 0) atomicOr(p.status, 4);
   }
   __syncthreads();
-  if (warp == 0) tm_free(tm, 512);
+  if (warp == 0) tm_free(TM, 512);
 }
 
 // A tensor of `n` dimensions (sizes and boxes from the innermost on), bf16 in the
@@ -739,7 +771,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   if (e == cudaSuccess) e = paged_behind(chunk_bf16_kernel<D>, p.parts, CB_NT, P::bytes(p.B), 0, s, p, qm, km, vm);
   if (e == cudaSuccess) e = launch_chunk_join<__nv_bfloat16, D>(p, 2 * TQ, CB_K, s);
   if (e == cudaSuccess && p.weight)
-    e = paged_behind(chunk_weight_bf16_kernel<D>, p.sms, CB_NT, CwPlan<D>::bytes(p.B), 0, s, p, qm, km);
+    e = paged_behind(chunk_weight_bf16_kernel<D>, p.sms, CW_NT, CwPlan<D>::bytes(p.B), 0, s, p, qm, km);
   return e;
 }
 

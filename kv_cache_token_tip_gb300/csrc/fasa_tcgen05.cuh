@@ -80,7 +80,13 @@ __device__ __forceinline__ uint64_t mma_operand(uint32_t at, uint32_t lead) {
 __host__ __device__ constexpr uint32_t mma_bf16_kind(int n, bool b_down) {
   return 1u << 4 | 1u << 7 | 1u << 10 | (b_down ? 1u << 16 : 0u) | (uint32_t)(n / 8) << 17 | (128u / 16) << 24;
 }
-// One thread: d (tensor memory) = a b, plus d where `add`.
+// One lane of the warp, known to be one.
+__device__ __forceinline__ bool elected() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+// One thread: d (tensor memory) = a b, plus d where `add`.  a in shared or in tensor memory.
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t kind, bool add) {
   asm volatile(
       "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
@@ -148,6 +154,18 @@ struct Patience {
     return __all_sync(0xffffffffu, ok);
   }
 };
+
+// Named barrier `id` of n threads; whether any of them said so.
+__device__ __forceinline__ bool named_bar_or(int id, int n, bool x) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %3, 0;\n\t"
+      "barrier.cta.red.or.pred.aligned q, %1, %2, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(id), "r"(n), "r"((uint32_t)x)
+      : "memory");
+  return r != 0;
+}
 
 // ---- two fp32 numbers at a time --------------------------------------------------
 __device__ __forceinline__ uint64_t pair_of(float a, float b) {
