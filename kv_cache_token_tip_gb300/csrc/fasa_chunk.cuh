@@ -16,8 +16,7 @@
 namespace fasa {
 
 // The sequences' words.  Every thread of the block calls it; ends with a barrier.
-// scan: NT / 32 words.  Lengths and rows are read past L1, since the join reads them
-// ahead of its wait.
+// scan: NT / 32 words.
 template <int NT>
 __device__ void chunk_line(const ChunkParams& p, ChunkSeq* s, long long* scan, int T, bool report) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -25,12 +24,12 @@ __device__ void chunk_line(const ChunkParams& p, ChunkSeq* s, long long* scan, i
   bool bad = false;
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
-    int len = ld_cg(p.seq_lens + b);
+    int len = p.seq_lens[b];
     bad = bad || len < 0 || len > p.T_cap;
     len = min(max(len, 0), p.T_cap);
     int n = 1;
     if (p.cu_new) {
-      const int x0 = ld_cg(p.cu_new + b), x1 = ld_cg(p.cu_new + b + 1);
+      const int x0 = p.cu_new[b], x1 = p.cu_new[b + 1];
       const bool ok = 0 <= x0 && x0 <= x1 && x1 <= p.n_tokens;
       bad = bad || !ok || (b == 0 && x0 != 0);
       n = ok ? x1 - x0 : 0;
@@ -87,45 +86,69 @@ __device__ __forceinline__ void store4(T* to, float a, float b, float c, float d
 __device__ __forceinline__ float* chunk_record(const ChunkParams& p, int D, int c, int slot) {
   return p.records + (size_t)(2 * c + slot) * ((size_t)p.rows * (D + 2));
 }
+// What the join is told of a record: the unit's first token (of the call's rows), its first
+// head and its rows, and whether there is a record (1) and it is the unit's last (2).  One
+// thread of each block, for both slots, before its first unit and as its segments end.
+__device__ __forceinline__ void note_none(const ChunkParams& p, int c) {
+  p.notes[2 * c] = p.notes[2 * c + 1] = make_int4(0, 0, 0, 0);
+}
+__device__ __forceinline__ void note_record(const ChunkParams& p, int c, const ChunkUnit& u, const ChunkSeq& q, int T,
+                                            int f0, int f1) {
+  p.notes[2 * c + (f0 == 0)] = make_int4(first_row(p, u.b) + u.i * T, u.h * p.G, min(T, q.n - u.i * T) * p.G,
+                                         f0 > 0 && f1 == u.tiles ? 3 : 1);
+}
 
-// The units that were cut: block x takes the cut before part x + 1 if it is the first of
-// its unit, its warps the rows.  The parts of a row are added in part order.
+// The units that were cut: block x takes the unit that goes on behind part x, if there is
+// one, its warps the rows.  The parts of a row are added in part order.
 constexpr int CJ_NT = 256;
-constexpr int CJ_ROWS = 32;  // rows of a block
+constexpr int CJ_ROWS = 16;  // rows of a block
 template <typename T, int D>
-__global__ void __launch_bounds__(CJ_NT) chunk_join_kernel(const __grid_constant__ ChunkParams p, int T_unit, int KT) {
-  extern __shared__ __align__(16) ChunkSeq seqs[];
-  __shared__ long long scan[CJ_NT / 32];
-  __shared__ int before[2 * CHUNK_MAX_SMS + 2];
-  chunk_line<CJ_NT>(p, seqs, scan, T_unit, false);
-  const ChunkLine line{seqs, p.B, p.Hkv, T_unit, KT};
-  const int parts = line.parts(p.parts), c = blockIdx.x + 1;
+__global__ void __launch_bounds__(CJ_NT) chunk_join_kernel(const __grid_constant__ ChunkParams p) {
+  __shared__ int parts[2 * CHUNK_MAX_SMS];  // that left a record of the unit, in order
+  __shared__ int count;
+  const int c = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   paged_go();
   paged_wait();
-  if (c >= parts) return;
-  ChunkUnit u;
-  u.find(line, line.part_begin(parts, c));
-  // tiles of the unit that lie before the cuts c - 1, c, c + 1, ..
-  for (int k = threadIdx.x; k <= parts - c + 1; k += CJ_NT) before[k] = u.before(line, line.part_begin(parts, c - 1 + k));
+  const int4 unit = ld_cg(p.notes + 2 * c + 1);
+  const int r0 = blockIdx.y * CJ_ROWS, rows = min(unit.z, r0 + CJ_ROWS);
+  if (!(unit.w & 1) || r0 >= rows) return;
+  if (warp == 0) {
+    int n = 1;
+    if (lane == 0) parts[0] = c;
+    for (int k = c + 1; k < p.parts; k += 32) {
+      const int flags = k + lane < p.parts ? ld_cg(p.notes + 2 * (k + lane)).w : 0;
+      const unsigned last = __ballot_sync(0xffffffffu, flags & 2);
+      const unsigned mine = __ballot_sync(0xffffffffu, flags & 1) & (last ? (last & -last) * 2 - 1 : 0xffffffffu);
+      if (mine >> lane & 1) parts[n + __popc(mine & ((1u << lane) - 1))] = k + lane;
+      n += __popc(mine);
+      if (last) break;
+    }
+    if (lane == 0) count = n;
+  }
   __syncthreads();
-  if (before[0] > 0 || before[1] == 0 || before[1] == u.tiles) return;
-  const int n = min(T_unit, seqs[u.b].n - u.i * T_unit) * p.G, first = first_row(p, u.b);
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int n = count;
   constexpr int E = D / 32, U = 4;  // U: parts that a lane has on the way
-  for (int r = blockIdx.y * CJ_ROWS + warp; r < min(n, (int)(blockIdx.y + 1) * CJ_ROWS); r += CJ_NT / 32) {
+  for (int r = r0 + warp; r < rows; r += CJ_NT / 32) {
     float M = -INFINITY, L = 0.f, o[E] = {};
-    for (int k0 = 0; before[k0] < u.tiles; k0 += U) {
+    for (int k0 = 0; k0 < n; k0 += U) {
       float x[U][E], m[U], l[U];
 #pragma unroll
       for (int i = 0; i < U; ++i) {
-        const int k = min(k0 + i, parts - c);
-        // (a part without a tile of the unit left no record)
-        const bool any = k == k0 + i && before[k] < before[k + 1];
-        const float* rec = chunk_record(p, D, c - 1 + k, k == 0);
+        const bool any = k0 + i < n;
+        const float* rec = chunk_record(p, D, any ? parts[k0 + i] : c, k0 + i == 0);
         m[i] = any ? ld_cg(rec + (size_t)p.rows * D + r) : -INFINITY;
         l[i] = any ? ld_cg(rec + (size_t)p.rows * (D + 1) + r) : 0.f;
+        if (any) {
+          if constexpr (E == 4) {
+            const float4 v = ld_cg(reinterpret_cast<const float4*>(rec + (size_t)r * D) + lane);
+            x[i][0] = v.x, x[i][1] = v.y, x[i][2] = v.z, x[i][3] = v.w;
+          } else {
+            x[i][0] = ld_cg(rec + (size_t)r * D + 2 * lane), x[i][1] = ld_cg(rec + (size_t)r * D + 2 * lane + 1);
+          }
+        } else {
 #pragma unroll
-        for (int e = 0; e < E; ++e) x[i][e] = any ? ld_cg(rec + (size_t)r * D + 32 * e + lane) : 0.f;
+          for (int e = 0; e < E; ++e) x[i][e] = 0.f;
+        }
       }
       float X = M;
 #pragma unroll
@@ -142,19 +165,19 @@ __global__ void __launch_bounds__(CJ_NT) chunk_join_kernel(const __grid_constant
 #pragma unroll
         for (int e = 0; e < E; ++e) o[e] += x[i][e] * g;
       }
-      if (k0 + U > parts - c) break;
     }
-    const ChunkRow at(p, u, first, T_unit, r);
+    const int token = unit.x + r / p.G, head = unit.y + r % p.G;
     const float inv = L > 0.f ? 1.f / L : 0.f;
-    T* to = static_cast<T*>(p.out) + at.out(p, D);
-#pragma unroll
-    for (int e = 0; e < E; ++e) to[32 * e + lane] = from_f32<T>(o[e] * inv);
-    if (p.weight && lane == 0) p.lse[at.lse(p)] = chunk_lse(M, L);
+    T* to = static_cast<T*>(p.out) + ((size_t)token * p.Hq + head) * D + E * lane;
+    if constexpr (E == 4) store4<T>(to, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
+    else if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(to) = pack_bf16(o[0] * inv, o[1] * inv);
+    else *reinterpret_cast<float2*>(to) = make_float2(o[0] * inv, o[1] * inv);
+    if (p.weight && lane == 0) p.lse[((size_t)(head / p.G) * p.n_tokens + token) * p.G + head % p.G] = chunk_lse(M, L);
   }
 }
 
 template <typename T, int D>
-cudaError_t launch_chunk_join(const ChunkParams& p, int T_unit, int KT, cudaStream_t s) {
+cudaError_t launch_chunk_join(const ChunkParams& p, cudaStream_t s) {
   if (p.parts < 2) return cudaSuccess;
   cudaLaunchAttribute attr;
   attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -162,11 +185,10 @@ cudaError_t launch_chunk_join(const ChunkParams& p, int T_unit, int KT, cudaStre
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(p.parts - 1, (p.rows + CJ_ROWS - 1) / CJ_ROWS);
   cfg.blockDim = dim3(CJ_NT);
-  cfg.dynamicSmemBytes = (p.B + 1) * sizeof(ChunkSeq);
   cfg.stream = s;
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T, D>, p, T_unit, KT);
+  return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T, D>, p);
 }
 
 }  // namespace fasa

@@ -107,12 +107,13 @@ __global__ void __launch_bounds__(CB_NT, 1)
   fence_proxy_async();
   tm_before_sync();
   paged_wait();
-  paged_go();  // the join reads the lengths
+  paged_go();
   chunk_line<CB_NT>(p, seqs, reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, blockIdx.x == 0);
   tm_after_sync();
   const ChunkLine line{seqs, p.B, p.Hkv, TU, CB_K};
   const int parts = line.parts(p.parts), c = blockIdx.x;
   const Patience patience{misc + 1, p.status, p.wait_ns};
+  if (tid == 0) note_none(p, c);
   if (c < parts) {
     const long long y0 = line.part_begin(parts, c), y1 = line.part_begin(parts, c + 1);
     // (384 threads of 168 registers: 256 of 232 and 128 of 40)
@@ -127,6 +128,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
       uint32_t s_phase = 0, o_phase = 0;
       segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool whole) {
         const ChunkSeq q = seqs[u.b];
+        if (tid == 0 && !whole) note_record(p, c, u, q, TU, f0, f1);
         const int e = row_tile_end(p, q, u, w, f0, f1), j0 = (2 * u.i + w) * TQ;
         const int j = j0 + row / p.G;
         const bool live = row < TQ * p.G && j < q.n;
@@ -769,7 +771,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   if (e == cudaSuccess) e = tensor_map(&km, p.k_pages, 2, kd, ks, kb);
   if (e == cudaSuccess) e = tensor_map(&vm, p.v_pages, 2, kd, ks, kb);
   if (e == cudaSuccess) e = paged_behind(chunk_bf16_kernel<D>, p.parts, CB_NT, P::bytes(p.B), 0, s, p, qm, km, vm);
-  if (e == cudaSuccess) e = launch_chunk_join<__nv_bfloat16, D>(p, 2 * TQ, CB_K, s);
+  if (e == cudaSuccess) e = launch_chunk_join<__nv_bfloat16, D>(p, s);
   if (e == cudaSuccess && p.weight)
     e = paged_behind(chunk_weight_bf16_kernel<D>, p.sms, CW_NT, CwPlan<D>::bytes(p.B), 0, s, p, qm, km);
   return e;

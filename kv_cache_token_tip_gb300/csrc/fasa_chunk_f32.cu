@@ -118,6 +118,7 @@ __global__ void __launch_bounds__(CF_NT) chunk_simt_kernel(const __grid_constant
   chunk_line<CF_NT>(p, seqs, reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, blockIdx.x == 0);
   const ChunkLine line{seqs, p.B, p.Hkv, TU, CF_K};
   const int parts = line.parts(p.parts), c = blockIdx.x;
+  if (tid == 0) note_none(p, c);
   if (c >= parts) return;
   const long long y0 = line.part_begin(parts, c), y1 = line.part_begin(parts, c + 1);
   ChunkUnit u;
@@ -125,6 +126,7 @@ __global__ void __launch_bounds__(CF_NT) chunk_simt_kernel(const __grid_constant
     const int f0 = u.before(line, y0), f1 = u.before(line, y1), n = seqs[u.b].n, len = seqs[u.b].len;
     const bool whole = f0 == 0 && f1 == u.tiles && u.begin >= y0;
     if (f0 < f1 || whole) {
+      if (tid == 0 && !whole) note_record(p, c, u, seqs[u.b], TU, f0, f1);
       const int first = first_row(p, u.b), j0 = u.i * TU, rows = min(TU, n - j0) * p.G;
       __syncthreads();
       load_queries<T, D>(p, first, j0, n, u.h, qs);
@@ -300,7 +302,7 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
     allowed.fetch_or(bit, std::memory_order_release);
   }
   e = paged_behind(chunk_simt_kernel<T, D>, p.parts, CF_NT, P::bytes(p.B), 0, s, p);
-  if (e == cudaSuccess) e = launch_chunk_join<T, D>(p, CF_M / p.G, CF_K, s);
+  if (e == cudaSuccess) e = launch_chunk_join<T, D>(p, s);
   if (e == cudaSuccess && p.weight) {
     const long long units = (long long)p.B * p.Hkv * ((p.T_cap + CF_K - 1) / CF_K);
     e = paged_behind(chunk_simt_weight_kernel<T, D>, (unsigned)(units < 4096 ? units : 4096), CF_NT, P::OFF_SCAN, 0, s, p);

@@ -116,6 +116,7 @@ void chunk_plan(const fasa_paged_dims_t* d, int n_tokens, int sms, int* rows, in
   *parts = (int)std::min<long long>(s.per_sm * std::min(sms, CHUNK_MAX_SMS), units * tiles);
 }
 
+size_t notes_bytes(int parts) { return up((size_t)parts * 2 * sizeof(int4)); }
 size_t records_bytes(int rows, int parts, int D) { return up((size_t)parts * 2 * rows * (D + 2) * 4); }
 
 }  // namespace
@@ -247,7 +248,7 @@ int fasa_paged_chunk_workspace_size(const fasa_paged_dims_t* dims, int32_t n_tok
   if (n_tokens == 0) return FASA_OK;
   int rows, parts;  // (of any device)
   chunk_plan(dims, n_tokens, CHUNK_MAX_SMS, &rows, &parts);
-  *bytes = records_bytes(rows, parts, dims->head_dim);
+  *bytes = notes_bytes(parts) + records_bytes(rows, parts, dims->head_dim);
   if (with_weight) *bytes += up((size_t)n_tokens * dims->n_q_heads * 4);
   return FASA_OK;
 }
@@ -292,8 +293,11 @@ int fasa_paged_chunk_attention(const void* q, int32_t n_tokens, const int32_t* c
   p.scale = (float)(1.4426950408889634 / sqrt((double)dims->head_dim));
   chunk_plan(dims, n_tokens, sms, &p.rows, &p.parts);
   p.sms = sms;
-  p.records = static_cast<float*>(workspace);
-  p.lse = reinterpret_cast<float*>(static_cast<char*>(workspace) + records_bytes(p.rows, p.parts, dims->head_dim));
+  char* ws = static_cast<char*>(workspace);
+  p.notes = reinterpret_cast<int4*>(ws);
+  ws += notes_bytes(p.parts);
+  p.records = reinterpret_cast<float*>(ws);
+  p.lse = reinterpret_cast<float*>(ws + records_bytes(p.rows, p.parts, dims->head_dim));
   p.status = status;
   p.wait_ns = wait_limit_ns();
   p.drop_tile = dropped_copy();

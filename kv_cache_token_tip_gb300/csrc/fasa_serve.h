@@ -48,8 +48,8 @@ struct RopeAppendParams {
 };
 
 // The attention of chunks.  Workspace: the parts' records (two per part: a unit that
-// began in an earlier part, a unit that goes on in a later one), and with weights the
-// rows' log-sums.
+// began in an earlier part, a unit that goes on in a later one) with a note to each, and
+// with weights the rows' log-sums.
 struct ChunkParams {
   int B, Hq, Hkv, G, log2_page, n_pages, max_pages, T_cap, n_tokens;
   const void* q;
@@ -62,6 +62,7 @@ struct ChunkParams {
   float* weight;   // null: no weights kept
   float scale;     // log2(e) / sqrt(d): logits are kept in powers of two
   float* records;  // [parts][2][rows * (d + 2)]: o [rows][d], m [rows], l [rows]
+  int4* notes;     // [parts][2]: whose the records are
   float* lse;      // [Hkv][n_tokens * G]
   int rows;        // of a record
   int parts;       // most parts of this launch
