@@ -15,29 +15,19 @@
 
 namespace fasa {
 
-// The sequences' words.  Every thread of the block calls it; ends with a barrier.
-// scan: NT / 32 words.
+// The line, its costs in `before` (shared memory, B + 1 words).  Every thread of the block
+// calls it; ends with a barrier.  scan: NT / 32 words.
 template <int NT>
-__device__ void chunk_line(const ChunkParams& p, ChunkSeq* s, long long* scan, int T, bool report) {
+__device__ ChunkLine chunk_line(const ChunkParams& p, long long* before, long long* scan, int T, int KT, bool report) {
+  const ChunkLine line{before, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, T, KT};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.B + NT - 1) / NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
   bool bad = false;
   long long sum = 0;
   for (int b = b0; b < b1; ++b) {
-    int len = p.seq_lens[b];
-    bad = bad || len < 0 || len > p.T_cap;
-    len = min(max(len, 0), p.T_cap);
-    int n = 1;
-    if (p.cu_new) {
-      const int x0 = p.cu_new[b], x1 = p.cu_new[b + 1];
-      const bool ok = 0 <= x0 && x0 <= x1 && x1 <= p.n_tokens;
-      bad = bad || !ok || (b == 0 && x0 != 0);
-      n = ok ? x1 - x0 : 0;
-    }
-    s[b].before = sum;
-    s[b].n = n;
-    s[b].len = len;
-    sum += ChunkLine::cost_of(n, len, T);
+    const ChunkSeq q = line.sequence(b, &bad);
+    before[b] = sum;
+    sum += ChunkLine::cost_of(q.n, q.len, T);
   }
   if (report && bad) atomicOr(p.status, 1);
   long long incl = sum;
@@ -48,24 +38,20 @@ __device__ void chunk_line(const ChunkParams& p, ChunkSeq* s, long long* scan, i
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  long long before = incl - sum;
+  long long pre = incl - sum;
 #pragma unroll
-  for (int v = 0; v < NT / 32; ++v) before += v < warp ? scan[v] : 0;
-  for (int b = b0; b < b1; ++b) s[b].before += before;
-  if (tid == NT - 1) {
-    s[p.B].before = before + sum;
-    s[p.B].n = s[p.B].len = 0;
-  }
+  for (int v = 0; v < NT / 32; ++v) pre += v < warp ? scan[v] : 0;
+  for (int b = b0; b < b1; ++b) before[b] += pre;
+  if (tid == NT - 1) before[p.B] = pre + sum;
   __syncthreads();
+  return line;
 }
-
-__device__ __forceinline__ int first_row(const ChunkParams& p, int b) { return p.cu_new ? p.cu_new[b] : b; }
 
 // Place of row r of unit u in `out` and in the log-sums: its token and head.
 struct ChunkRow {
   int token, head;  // of the call's rows; of the Hq heads
-  __device__ ChunkRow(const ChunkParams& p, const ChunkUnit& u, int first, int T, int r)
-      : token(first + u.i * T + r / p.G), head(u.h * p.G + r % p.G) {}
+  __device__ ChunkRow(const ChunkParams& p, const ChunkUnit& u, int T, int r)
+      : token(u.q.first + u.i * T + r / p.G), head(u.h * p.G + r % p.G) {}
   __device__ size_t out(const ChunkParams& p, int D) const { return ((size_t)token * p.Hq + head) * D; }
   __device__ size_t lse(const ChunkParams& p) const {
     return ((size_t)(head / p.G) * p.n_tokens + token) * p.G + head % p.G;
@@ -92,9 +78,8 @@ __device__ __forceinline__ float* chunk_record(const ChunkParams& p, int D, int 
 __device__ __forceinline__ void note_none(const ChunkParams& p, int c) {
   p.notes[2 * c] = p.notes[2 * c + 1] = make_int4(0, 0, 0, 0);
 }
-__device__ __forceinline__ void note_record(const ChunkParams& p, int c, const ChunkUnit& u, const ChunkSeq& q, int T,
-                                            int f0, int f1) {
-  p.notes[2 * c + (f0 == 0)] = make_int4(first_row(p, u.b) + u.i * T, u.h * p.G, min(T, q.n - u.i * T) * p.G,
+__device__ __forceinline__ void note_record(const ChunkParams& p, int c, const ChunkUnit& u, int T, int f0, int f1) {
+  p.notes[2 * c + (f0 == 0)] = make_int4(u.q.first + u.i * T, u.h * p.G, min(T, u.q.n - u.i * T) * p.G,
                                          f0 > 0 && f1 == u.tiles ? 3 : 1);
 }
 

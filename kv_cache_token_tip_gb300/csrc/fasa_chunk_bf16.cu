@@ -39,17 +39,17 @@ struct CbPlan {
   static constexpr int BARS = 2 * STAGES + 2 + 8 + 1;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;    // tensor memory's address, dead
   static constexpr int OFF_SCAN = OFF_MISC + 16;
-  static constexpr int OFF_SEQ = (OFF_SCAN + CB_NT / 32 * 8 + 15) / 16 * 16;
-  static constexpr int bytes(int B) { return 1024 + OFF_SEQ + (B + 1) * (int)sizeof(ChunkSeq); }
+  static constexpr int OFF_TURN = (OFF_SCAN + CB_NT / 32 * 8 + 15) / 16 * 16;  // results on their way out, 2 KB a warp
+  static constexpr int OFF_SEQ = OFF_TURN + CB_ROWS * 2048;
+  static constexpr int bytes(int B) { return 1024 + OFF_SEQ + (B + 1) * 8; }
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
 };
 
 // The tiles of slots [f0, f1) of a unit that tile w of its rows reads: up to e.
-__device__ __forceinline__ int row_tile_end(const ChunkParams& p, const ChunkSeq& q, const ChunkUnit& u, int w, int f0,
-                                            int f1) {
+__device__ __forceinline__ int row_tile_end(const ChunkParams& p, const ChunkUnit& u, int w, int f0, int f1) {
   const int TQ = 128 / p.G, j0 = (2 * u.i + w) * TQ;
-  if (j0 >= q.n) return f0;
-  const int see = q.len - q.n + min(j0 + TQ, q.n);
+  if (j0 >= u.q.n) return f0;
+  const int see = u.q.len - u.q.n + min(j0 + TQ, u.q.n);
   return max(f0, min(f1, see > 0 ? (see + CB_K - 1) / CB_K : 0));
 }
 
@@ -82,7 +82,6 @@ __global__ void __launch_bounds__(CB_NT, 1)
   const uint32_t s_full = q_full + 16, o_full = q_full + 32;  // of either tile of rows
   const uint32_t p_full = q_full + 48, drain = q_full + 80;          // of either half of its P
   volatile int* misc = reinterpret_cast<volatile int*>(sm + P::OFF_MISC);
-  ChunkSeq* seqs = reinterpret_cast<ChunkSeq*>(sm + P::OFF_SEQ);
   const int TQ = 128 / p.G, TU = 2 * TQ;
   if (warp == 0) tm_alloc(base + P::OFF_MISC, 512);
   if (tid == 32) {
@@ -108,9 +107,9 @@ __global__ void __launch_bounds__(CB_NT, 1)
   tm_before_sync();
   paged_wait();
   paged_go();
-  chunk_line<CB_NT>(p, seqs, reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, blockIdx.x == 0);
+  const ChunkLine line = chunk_line<CB_NT>(p, reinterpret_cast<long long*>(sm + P::OFF_SEQ),
+                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CB_K, blockIdx.x == 0);
   tm_after_sync();
-  const ChunkLine line{seqs, p.B, p.Hkv, TU, CB_K};
   const int parts = line.parts(p.parts), c = blockIdx.x;
   const Patience patience{misc + 1, p.status, p.wait_ns};
   if (tid == 0) note_none(p, c);
@@ -127,9 +126,9 @@ __global__ void __launch_bounds__(CB_NT, 1)
       const float scale = p.scale;
       uint32_t s_phase = 0, o_phase = 0;
       segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool whole) {
-        const ChunkSeq q = seqs[u.b];
-        if (tid == 0 && !whole) note_record(p, c, u, q, TU, f0, f1);
-        const int e = row_tile_end(p, q, u, w, f0, f1), j0 = (2 * u.i + w) * TQ;
+        const ChunkSeq& q = u.q;
+        if (tid == 0 && !whole) note_record(p, c, u, TU, f0, f1);
+        const int e = row_tile_end(p, u, w, f0, f1), j0 = (2 * u.i + w) * TQ;
         const int j = j0 + row / p.G;
         const bool live = row < TQ * p.G && j < q.n;
         const int see = live ? q.len - q.n + j + 1 : 0;
@@ -222,9 +221,38 @@ __global__ void __launch_bounds__(CB_NT, 1)
           tm_after_sync();
         }
         const int r = w * TQ * p.G + row;  // of the unit
-        const ChunkRow at(p, u, first_row(p, u.b), TU, r);
-        const float inv = whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f;
+        const ChunkRow at(p, u, TU, r);
         float* rec = chunk_record(p, D, c, f0 > 0 ? 0 : 1);
+        // Through shared memory, 64 bytes of a row at a time, so that four lanes write a row's
+        // together: a store of 32 rows takes 32 turns, of eight rows eight.
+        const unsigned alive = __ballot_sync(0xffffffffu, live);
+        const long long mine = whole ? (long long)at.out(p, D) * 2 : (long long)r * D * 4;  // this row's place, bytes
+        char* to[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          to[i] = (whole ? static_cast<char*>(p.out) : reinterpret_cast<char*>(rec)) +
+                  __shfl_sync(0xffffffffu, mine, 8 * i + (lane >> 2)) + 16 * (lane & 3);
+        const uint32_t turn = base + P::OFF_TURN + warp * 2048;
+        auto send = [&](const uint32_t (&x)[16], int byte) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(turn + lane * 64 + ((i ^ (lane >> 1 & 3)) << 4)),
+                         "r"(x[4 * i]), "r"(x[4 * i + 1]), "r"(x[4 * i + 2]), "r"(x[4 * i + 3])
+                         : "memory");
+          __syncwarp();
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int row = 8 * i + (lane >> 2);
+            uint4 v;
+            asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                         : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                         : "r"(turn + row * 64 + (((lane & 3) ^ (row >> 1 & 3)) << 4))
+                         : "memory");
+            if (alive >> row & 1u) *reinterpret_cast<uint4*>(to[i] + byte) = v;
+          }
+          __syncwarp();
+        };
+        const float inv = l > 0.f ? 1.f / l : 0.f;
 #pragma unroll
         for (int k = 0; k < D; k += 32) {
           uint32_t o[32];
@@ -236,21 +264,18 @@ __global__ void __launch_bounds__(CB_NT, 1)
 #pragma unroll
             for (int i = 0; i < 32; ++i) o[i] = 0u;
           }
-          if (live && whole) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at.out(p, D) + k);
+          uint32_t x[16];
+          if (whole) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t x[4];
+            for (int i = 0; i < 16; ++i) x[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+            send(x, 2 * k);
+          } else {
 #pragma unroll
-              for (int h = 0; h < 4; ++h)
-                x[h] = pack_bf16(__uint_as_float(o[8 * i + 2 * h]) * inv, __uint_as_float(o[8 * i + 2 * h + 1]) * inv);
-              to[i] = make_uint4(x[0], x[1], x[2], x[3]);
-            }
-          } else if (live) {
-            // (a row of 130 floats begins on 8 bytes; o's rows lie D apart, whole 16-byte words)
-            uint4* to = reinterpret_cast<uint4*>(rec + (size_t)r * D + k);
+            for (int i = 0; i < 16; ++i) x[i] = o[i];
+            send(x, 4 * k);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) to[i] = make_uint4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
+            for (int i = 0; i < 16; ++i) x[i] = o[16 + i];
+            send(x, 4 * k + 64);
           }
         }
         tm_before_sync();  // (the next unit's first P is behind this)
@@ -285,8 +310,8 @@ __global__ void __launch_bounds__(CB_NT, 1)
         if (elected()) mma_commit(bar);
       };
       segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool) {
-        const ChunkSeq q = seqs[u.b];
-        const int e0 = row_tile_end(p, q, u, 0, f0, f1), e1 = row_tile_end(p, q, u, 1, f0, f1);
+        const ChunkSeq& q = u.q;
+        const int e0 = row_tile_end(p, u, 0, f0, f1), e1 = row_tile_end(p, u, 1, f0, f1);
         const int e[2] = {e0, e1}, end = max(e0, e1);
         if (f0 == end) return true;
         if (!patience.wait(q_full, q_phase)) return false;
@@ -349,10 +374,10 @@ __global__ void __launch_bounds__(CB_NT, 1)
       int k = 0, n_tile = 0, n_unit = 0;
       fence_proxy_async_global();  // (a kernel before this one may have stored what is copied)
       segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool) {
-        const ChunkSeq q = seqs[u.b];
-        const int end = max(row_tile_end(p, q, u, 0, f0, f1), row_tile_end(p, q, u, 1, f0, f1));
+        const ChunkSeq& q = u.q;
+        const int end = max(row_tile_end(p, u, 0, f0, f1), row_tile_end(p, u, 1, f0, f1));
         if (f0 == end) return true;
-        const int first = first_row(p, u.b) + u.i * TU;
+        const int first = q.first + u.i * TU;
         if (!patience.wait(q_empty, q_phase)) return false;
         q_phase ^= 1;
         ++n_unit;
@@ -363,6 +388,12 @@ __global__ void __launch_bounds__(CB_NT, 1)
           tma_3d(base + w * P::TILE + half * P::SLAB, &qmap, 64 * half, u.h * p.G, first + w * TQ, q_full);
         }
         __syncwarp();
+        if (u.begin + u.cost < y1) {  // the next unit's Q into L2: it is waited for between the units
+          ChunkUnit v = u;
+          v.next(line);
+          const int token = v.q.first + v.i * TU + lane / P::HALVES * TQ;
+          if (lane < 2 * P::HALVES && token < p.n_tokens) tma_prefetch_3d(&qmap, 64 * half, v.h * p.G, token);
+        }
         const int* table = p.page_table + (size_t)u.b * p.max_pages;
         auto look_up = [&](int t) {
           const int slot = t * CB_K + mine * box;

@@ -22,7 +22,7 @@ struct CfPlan {
   static constexpr int OFF_OK = OFF_P + CF_M * LP * 4;
   static constexpr int OFF_SCAN = OFF_OK + CF_K * 4;
   static constexpr int OFF_SEQ = OFF_SCAN + 64;
-  static constexpr int bytes(int B) { return OFF_SEQ + (B + 1) * (int)sizeof(ChunkSeq); }
+  static constexpr int bytes(int B) { return OFF_SEQ + (B + 1) * 8; }
 };
 
 // Slots t0 .. t0 + 63 of (b, h): rows of K or V in fp32, zeros for slots that do not
@@ -111,23 +111,22 @@ __global__ void __launch_bounds__(CF_NT) chunk_simt_kernel(const __grid_constant
   float* kv = reinterpret_cast<float*>(sm + P::OFF_KV);
   float* ps = reinterpret_cast<float*>(sm + P::OFF_P);
   int* ok = reinterpret_cast<int*>(sm + P::OFF_OK);
-  ChunkSeq* seqs = reinterpret_cast<ChunkSeq*>(sm + P::OFF_SEQ);
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, TU = CF_M / p.G;
   paged_wait();
   paged_go();
-  chunk_line<CF_NT>(p, seqs, reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, blockIdx.x == 0);
-  const ChunkLine line{seqs, p.B, p.Hkv, TU, CF_K};
+  const ChunkLine line = chunk_line<CF_NT>(p, reinterpret_cast<long long*>(sm + P::OFF_SEQ),
+                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CF_K, blockIdx.x == 0);
   const int parts = line.parts(p.parts), c = blockIdx.x;
   if (tid == 0) note_none(p, c);
   if (c >= parts) return;
   const long long y0 = line.part_begin(parts, c), y1 = line.part_begin(parts, c + 1);
   ChunkUnit u;
   for (u.find(line, y0); u.begin < y1;) {
-    const int f0 = u.before(line, y0), f1 = u.before(line, y1), n = seqs[u.b].n, len = seqs[u.b].len;
+    const int f0 = u.before(line, y0), f1 = u.before(line, y1), n = u.q.n, len = u.q.len;
     const bool whole = f0 == 0 && f1 == u.tiles && u.begin >= y0;
     if (f0 < f1 || whole) {
-      if (tid == 0 && !whole) note_record(p, c, u, seqs[u.b], TU, f0, f1);
-      const int first = first_row(p, u.b), j0 = u.i * TU, rows = min(TU, n - j0) * p.G;
+      if (tid == 0 && !whole) note_record(p, c, u, TU, f0, f1);
+      const int first = u.q.first, j0 = u.i * TU, rows = min(TU, n - j0) * p.G;
       __syncthreads();
       load_queries<T, D>(p, first, j0, n, u.h, qs);
       float m[4], l[4], o[4][E];
@@ -198,7 +197,7 @@ __global__ void __launch_bounds__(CF_NT) chunk_simt_kernel(const __grid_constant
         for (int s = 1; s < 16; s <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], s);
         const int r = 4 * ty + i;
         if (r >= rows) continue;
-        const ChunkRow at(p, u, first, TU, r);
+        const ChunkRow at(p, u, TU, r);
         if (whole) {
           const float inv = l[i] > 0.f ? 1.f / l[i] : 0.f;
           T* to = static_cast<T*>(p.out) + at.out(p, D);

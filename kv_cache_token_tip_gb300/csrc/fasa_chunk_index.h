@@ -23,16 +23,34 @@ namespace fasa {
 constexpr int CHUNK_UNIT_COST = 128;  // slots
 constexpr int CHUNK_MAX_SMS = 160;    // the workspace has room for their parts
 
-// One sequence: its cost up to here (of one head), its new tokens and its slots.
+// A sequence's new tokens, where they begin among the call's rows, and its slots.
 struct ChunkSeq {
-  long long before;
-  int n, len;
+  int first, n, len;
 };
 
 struct ChunkLine {
-  const ChunkSeq* s;  // [B + 1]; the last one's `before` is the total of one head
-  int B, Hkv, T, KT;
+  const long long* before;  // [B + 1]: cost of one head of the sequences before b
+  const int* cu_new;        // null: a token a sequence
+  const int* seq_lens;
+  int n_tokens, T_cap, B, Hkv, T, KT;
 
+  // Sequence b as far as it fits: no token of a range that is not within the call's rows.
+  FASA_CHUNK_HD ChunkSeq sequence(int b, bool* bad) const {
+    ChunkSeq q;
+    const int len = seq_lens[b];
+    q.len = len < 0 ? 0 : len > T_cap ? T_cap : len;
+    *bad = *bad || q.len != len;
+    q.first = b;
+    q.n = 1;
+    if (cu_new) {
+      const int end = cu_new[b + 1];
+      q.first = cu_new[b];
+      const bool ok = 0 <= q.first && q.first <= end && end <= n_tokens;
+      q.n = ok ? end - q.first : 0;
+      *bad = *bad || !ok || (b == 0 && q.first != 0);
+    }
+    return q;
+  }
   FASA_CHUNK_HD static int tiles_of(int n, int T) { return (n + T - 1) / T; }
   // Cost of the first i units of a head of a sequence.
   FASA_CHUNK_HD static long long cost_of(int n, int len, int T, int i) {
@@ -41,7 +59,7 @@ struct ChunkLine {
   }
   FASA_CHUNK_HD static long long cost_of(int n, int len, int T) { return cost_of(n, len, T, tiles_of(n, T)); }
 
-  FASA_CHUNK_HD long long total() const { return s[B].before * Hkv; }
+  FASA_CHUNK_HD long long total() const { return before[B] * Hkv; }
   FASA_CHUNK_HD int parts(int most) const {
     const long long t = total(), least = CHUNK_UNIT_COST + KT, n = (t + least - 1) / least;
     return n < most ? (int)n : most;
@@ -56,28 +74,30 @@ struct ChunkLine {
 // cut there.
 struct ChunkUnit {
   int b, h, i;
+  ChunkSeq q;
   long long begin, cost;
   int tiles;  // that its last token sees
 
   FASA_CHUNK_HD void fill(const ChunkLine& l) {
-    const ChunkSeq q = l.s[b];
-    const int T = l.T, last = (i + 1) * T < q.n ? (i + 1) * T : q.n;
+    const int last = (i + 1) * l.T < q.n ? (i + 1) * l.T : q.n;
     const int see = q.len - q.n + last;  // (all of len at most)
     tiles = see > 0 ? (see + l.KT - 1) / l.KT : 0;
-    cost = CHUNK_UNIT_COST + (q.len > q.n ? q.len - q.n : 0) + (long long)(i + 1) * T;
+    cost = CHUNK_UNIT_COST + (q.len > q.n ? q.len - q.n : 0) + (long long)(i + 1) * l.T;
   }
   // The unit that holds position y, 0 <= y < total.
   FASA_CHUNK_HD void find(const ChunkLine& l, long long y) {
     int lo = 0, hi = l.B;  // Hkv before(lo) <= y < Hkv before(hi)
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (l.s[mid].before * l.Hkv <= y) lo = mid;
+      if (l.before[mid] * l.Hkv <= y) lo = mid;
       else hi = mid;
     }
     b = lo;
-    const ChunkSeq q = l.s[b];
-    const long long head = l.s[b + 1].before - q.before;
-    y -= q.before * l.Hkv;
+    bool bad = false;
+    q = l.sequence(b, &bad);
+    const long long head = l.before[b + 1] - l.before[b];
+    begin = l.before[b] * l.Hkv;
+    y -= begin;
     h = (int)(y / head);
     y -= h * head;
     lo = 0;
@@ -88,18 +108,20 @@ struct ChunkUnit {
       else hi = mid;
     }
     i = lo;
-    begin = q.before * l.Hkv + h * head + ChunkLine::cost_of(q.n, q.len, l.T, i);
+    begin += h * head + ChunkLine::cost_of(q.n, q.len, l.T, i);
     fill(l);
   }
   // The unit behind this one; only where there is one.
   FASA_CHUNK_HD void next(const ChunkLine& l) {
     begin += cost;
-    if (++i == ChunkLine::tiles_of(l.s[b].n, l.T)) {
+    if (++i == ChunkLine::tiles_of(q.n, l.T)) {
       i = 0;
       if (++h == l.Hkv) {
         h = 0;
         do ++b;
-        while (l.s[b + 1].before == l.s[b].before);
+        while (l.before[b + 1] == l.before[b]);
+        bool bad = false;
+        q = l.sequence(b, &bad);
       }
     }
     fill(l);

@@ -156,14 +156,16 @@ using namespace fasa;
 // part that it begins in, and the place of a cut is found again from the cut alone.
 static int check(const std::vector<int>& n, const std::vector<int>& len, int Hkv, int T, int KT, int most) {
   const int B = (int)n.size();
-  std::vector<ChunkSeq> s(B + 1);
+  std::vector<long long> costs(B + 1);
+  std::vector<int> cu(B + 1);
   long long before = 0;
   for (int b = 0; b < B; ++b) {
-    s[b] = ChunkSeq{before, n[b], len[b]};
+    costs[b] = before;
+    cu[b + 1] = cu[b] + n[b];
     before += ChunkLine::cost_of(n[b], len[b], T);
   }
-  s[B] = ChunkSeq{before, 0, 0};
-  const ChunkLine line{s.data(), B, Hkv, T, KT};
+  costs[B] = before;
+  const ChunkLine line{costs.data(), cu.data(), len.data(), cu[B], 1 << 18, B, Hkv, T, KT};
   const int parts = line.parts(most);
   if (before == 0) { CHECK(parts == 0); return 0; }
   CHECK(parts >= 1 && parts <= most && line.part_begin(parts, 0) == 0 && line.part_begin(parts, parts) == line.total());
@@ -174,7 +176,7 @@ static int check(const std::vector<int>& n, const std::vector<int>& len, int Hkv
     ChunkUnit u;
     for (u.find(line, y0);;) {
       CHECK(u.b >= 0 && u.b < B && u.h >= 0 && u.h < Hkv && u.i >= 0 && u.i < ChunkLine::tiles_of(n[u.b], T));
-      CHECK(u.begin < y1 && u.begin + u.cost > y0);
+      CHECK(u.begin < y1 && u.begin + u.cost > y0 && u.q.n == n[u.b] && u.q.len == len[u.b] && u.q.first == cu[u.b]);
       const int last = (u.i + 1) * T < n[u.b] ? (u.i + 1) * T : n[u.b], see = len[u.b] - n[u.b] + last;
       CHECK(u.tiles == (see > 0 ? (see + KT - 1) / KT : 0));
       const int f0 = u.before(line, y0), f1 = u.before(line, y1);
