@@ -441,11 +441,12 @@ __global__ void __launch_bounds__(CB_NT, 1)
 // ------------------------------------------------------------------ weights
 // weight_t += sum over the rows that see slot t of 2^(scale S - log-sum of the row).  A
 // unit is 256 slots of a (sequence, KV head): two tiles of K as rows of S^T = K Q^T, the
-// rows of Q 128 at a time as its columns, so that a thread adds what one slot gets, in the
+// rows of Q 128 at a time as its columns (K in tensor memory, Q in shared memory), so that a thread adds what one slot gets, in the
 // rows' order.  Units are dealt to the blocks there and back, since their costs fall with
 // the slots (the later, the fewer rows see them).
 constexpr int CW_NT = 640;           // 16 warps of slots, one of instructions, one of copies, two at rest
 constexpr int CW_ROWS = 16;
+constexpr int CW_S = 3;              // tiles of S in tensor memory, of 128 columns, behind the two tiles of K
 
 // Two warps with the two halves of the same rows' columns.
 struct Pair {
@@ -465,18 +466,34 @@ struct Pair {
   }
 };
 
+constexpr int CW_LSE = 4;             // tiles of Q whose rows' log-sums are there
+
 template <int D>
 struct CwPlan {
   using A = CbPlan<D>;
-  static constexpr int STAGES = A::STAGES;
-  static constexpr int OFF_LSE = A::OFF_BAR;
-  static constexpr int OFF_BAR = OFF_LSE + STAGES * 128 * 4;
-  static constexpr int BARS = 4 * STAGES + 2 + 8 + 1;
+  static constexpr int STAGES = 6 * A::STAGES / 4;  // of the ring: a unit's two tiles of K, then its tiles of Q
+  static constexpr int TILE = A::TILE;
+  static constexpr int OFF_LSE = STAGES * TILE;
+  static constexpr int OFF_BAR = OFF_LSE + CW_LSE * 128 * 4;
+  static constexpr int BARS = 2 * STAGES + 2 * CW_LSE + 2 + 8 + CW_S + 1;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
   static constexpr int OFF_PAIR = (OFF_MISC + 8 + 15) / 16 * 16;
   static constexpr int OFF_LINE = OFF_PAIR + CW_ROWS / 2 * 128;
   static constexpr int bytes(int B) { return 1024 + OFF_LINE + (B + 1) * 4; }
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
+};
+
+// A place of the ring.
+template <int S>
+struct RingAt {
+  int st = 0;
+  uint32_t phase = 0;
+  __device__ void next() {
+    if (++st == S) {
+      st = 0;
+      phase ^= 1;
+    }
+  }
 };
 
 // New tokens of a sequence, and where they begin.
@@ -524,36 +541,34 @@ __global__ void __launch_bounds__(CW_NT, 1)
   extern __shared__ __align__(16) char raw[];
   char* sm = raw + ((1024 - (smem_u32(raw) & 1023)) & 1023);
   const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
-  const uint32_t base = smem_u32(sm), ring = base + A::OFF_RING, bars = base + P::OFF_BAR;
-  const uint32_t full = bars, empty = bars + 8 * S, lse_full = bars + 16 * S, lse_empty = bars + 24 * S;
-  const uint32_t k_full = bars + 32 * S, k_empty = k_full + 8, t_full = k_full + 16, t_empty = k_full + 48;  // [w][2]
-  const uint32_t drain = k_full + 80;
+  const uint32_t ring = smem_u32(sm), full = ring + P::OFF_BAR, empty = full + 8 * S;
+  const uint32_t lse_full = empty + 8 * S, lse_empty = lse_full + 8 * CW_LSE, k_go = lse_empty + 8 * CW_LSE;
+  const uint32_t k_here = k_go + 8, t_full = k_go + 16, t_empty = t_full + 64, drain = t_empty + 8 * CW_S;
   volatile int* misc = reinterpret_cast<volatile int*>(sm + P::OFF_MISC);
   float* lse = reinterpret_cast<float*>(sm + P::OFF_LSE);
   int* scan = reinterpret_cast<int*>(sm + P::OFF_PAIR);
   int* before = reinterpret_cast<int*>(sm + P::OFF_LINE);
   const int TQ = 128 / p.G;
-  if (warp == 0) tm_alloc(base + P::OFF_MISC, 512);
+  if (warp == 0) tm_alloc(ring + P::OFF_MISC, 512);
   if (tid == 32) {
     misc[1] = 0;
     for (int i = 0; i < S; ++i) {
       mbar_init(full + 8 * i, 1);
       mbar_init(empty + 8 * i, 1);
+    }
+    for (int i = 0; i < CW_LSE; ++i) {
       mbar_init(lse_full + 8 * i, 1);
       mbar_init(lse_empty + 8 * i, CW_ROWS);
     }
-    mbar_init(k_full, 1);
-    mbar_init(k_empty, 1);
-    for (int i = 0; i < 4; ++i) {
-      mbar_init(t_full + 8 * i, 1);
-      mbar_init(t_empty + 8 * i, 8);
-    }
+    mbar_init(k_go, 1);
+    mbar_init(k_here, CW_ROWS);
+    // (a barrier that its waiters may find two phases on tells them nothing: those of full
+    // tiles of S are each row tile's own, and more than there are tiles)
+    for (int i = 0; i < 8; ++i) mbar_init(t_full + 8 * i, 1);
+    for (int i = 0; i < CW_S; ++i) mbar_init(t_empty + 8 * i, 8);
     mbar_init(drain, 1);
     fence_mbar_init();
   }
-  // rows of Q that no copy writes stay zeros
-  for (int i = tid; i < S * A::TILE / 16; i += CW_NT) reinterpret_cast<uint4*>(sm + A::OFF_RING)[i] = make_uint4(0u, 0u, 0u, 0u);
-  fence_proxy_async();
   tm_before_sync();
   paged_go();
   paged_wait();
@@ -588,9 +603,11 @@ __global__ void __launch_bounds__(CW_NT, 1)
     const int w = warp >> 3, half = (warp >> 2) & 1, row = tid & 127;
     const Pair pair{1 + (warp >> 3) * 4 + (warp & 3), half,
                     reinterpret_cast<float*>(sm + P::OFF_PAIR) + 32 * ((warp >> 3) * 4 + (warp & 3))};
-    const uint32_t here = TM + ((uint32_t)(warp & 3) << 21) + 256 * w + 64 * half;
+    const uint32_t here = TM + ((uint32_t)(warp & 3) << 21);
     const float scale = p.scale;
-    int k = 0, buf = 0;  // Q tiles, and S tiles of these rows, so far
+    int at_k = 0;  // place of the next unit's K in the ring
+    uint32_t k_phase = 0;
+    int k = 0, n_s = 0, own = 0;  // Q tiles, S tiles, and those of these rows, so far
     weight_units(p, before, [&](const WeightUnit& u) {
       const int slot = u.t0 + 128 * w + row, from = u.from(0, TQ), mine = u.from(w, TQ), tiles = u.tiles(TQ);
       if (from >= tiles) return true;
@@ -600,25 +617,51 @@ __global__ void __launch_bounds__(CW_NT, 1)
       const bool live = page >= 0 && page < p.n_pages;
       const float old = live && !half ? *weight : 0.f;
       float total = 0.f;
-      bool ok = true;
-      for (int i = from; i < tiles; ++i, ++k) {
-        const int st = k % S;
-        ok = patience.wait(lse_full + 8 * st, (k / S) & 1);
+      // K from shared to tensor memory, a row to a thread: the matrix instructions then read
+      // Q alone from shared memory, whose bandwidth would bound them
+      bool ok = patience.wait(k_go, k_phase);
+      k_phase ^= 1;
+      {
+        const uint32_t tile = ring + (uint32_t)((at_k + w) % S) * P::TILE;
+        at_k = (at_k + 2 + tiles - from) % S;  // (behind the tiles of Q)
+        constexpr int CH = D / 16;  // 16-byte chunks of half a row
+        uint32_t x[4 * CH];
+#pragma unroll
+        for (int i = 0; i < CH; ++i) {
+          const int ch = CH * half + i;
+          asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                       : "=r"(x[4 * i]), "=r"(x[4 * i + 1]), "=r"(x[4 * i + 2]), "=r"(x[4 * i + 3])
+                       : "r"(tile + (ch >> 3) * A::SLAB + row * 128 + (((ch & 7) ^ (row & 7)) << 4))
+                       : "memory");
+        }
+        if constexpr (D == 128) tm_st32(here + 64 * w + 32 * half, x);
+        else tm_st16(here + 32 * w + 16 * half, x);
+        tm_wait_st();
+        tm_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(k_here);
+      }
+      const int second = u.from(1, TQ);
+      for (int i = from; ok && i < tiles; ++i, ++k) {
+        const int st = k % CW_LSE;
+        ok = patience.wait(lse_full + 8 * st, (k / CW_LSE) & 1);
         if (!ok) break;
+        const int buf = (n_s + w) % CW_S;
+        n_s += i >= second ? 2 : 1;
         if (i >= mine) {
-          ok = patience.wait(t_full + 8 * (2 * w + (buf & 1)), (buf >> 1) & 1);
+          ok = patience.wait(t_full + 32 * w + 8 * (own & 3), own >> 2 & 1);
           if (!ok) break;
+          ++own;
           tm_after_sync();
           uint32_t s[64];
-          const uint32_t at = here + 128 * (buf & 1);
+          const uint32_t at = here + 128 * (1 + buf) + 64 * half;
           tm_ld32(at, s);
           tm_ld32(at + 32, s + 32);
           tm_wait_ld();
           tm_settle(s);
           tm_before_sync();
           __syncwarp();
-          if (lane == 0) mbar_arrive(t_empty + 8 * (2 * w + (buf & 1)));
-          ++buf;
+          if (lane == 0) mbar_arrive(t_empty + 8 * buf);
           // the rows of this tile that there are, and of them the first that sees the slot
           const int rows = min(TQ, u.n - i * TQ) * p.G, lo = (slot - (u.len - u.n) - i * TQ) * p.G - 64 * half;
           if (rows < TQ * p.G || __any_sync(0xffffffffu, lo > 0)) {
@@ -626,6 +669,10 @@ __global__ void __launch_bounds__(CW_NT, 1)
             for (int x = 0; x < 64; ++x)
               if (x < lo || x >= rows - 64 * half) s[x] = 0xff800000u;  // -inf
           }
+          // (columns behind a tile's rows hold anything; a tile has 125 rows or more)
+#pragma unroll
+          for (int x = 61; x < 64; ++x)
+            if (half && 64 + x >= TQ * p.G) s[x] = 0xff800000u;
           const uint64_t scale2 = pair_of(scale, scale);
           const float4* l4 = reinterpret_cast<const float4*>(lse + 128 * st + 64 * half);  // (negative log-sums)
           uint64_t sum[2] = {0, 0};
@@ -653,89 +700,107 @@ __global__ void __launch_bounds__(CW_NT, 1)
   } else if (warp == CW_ROWS) {
     // -------------------------------------------------- matrix instructions
     constexpr uint32_t kind = mma_bf16_kind(128, false);
-    const uint64_t k_tile = mma_operand(base, 0), q_tile = mma_operand(ring, 0);  // (descriptors count 16 bytes)
+    const uint64_t q_tile = mma_operand(ring, 0);  // (descriptors count 16 bytes)
+    RingAt<S> at;
     uint32_t k_phase = 0;
-    int k = 0, buf[2] = {0, 0};
+    int n_s = 0, own[2] = {0, 0};
     weight_units(p, before, [&](const WeightUnit& u) {
       const int from[2] = {u.from(0, TQ), u.from(1, TQ)}, tiles = u.tiles(TQ);
       if (from[0] >= tiles) return true;
-      if (!patience.wait(k_full, k_phase)) return false;
+      int k_at[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        k_at[w] = at.st;
+        if (!patience.wait(full + 8 * at.st, at.phase)) return false;
+        at.next();
+      }
+      if (lane == 0) mbar_arrive(k_go);
+      __syncwarp();
+      if (!patience.wait(k_here, k_phase)) return false;
       k_phase ^= 1;
-      for (int i = from[0]; i < tiles; ++i, ++k) {
-        const int st = k % S;
-        if (!patience.wait(full + 8 * st, (k / S) & 1)) return false;
+      if (lane < 2) mbar_arrive(empty + 8 * (lane ? k_at[1] : k_at[0]));
+      __syncwarp();
+      tm_after_sync();
+      for (int i = from[0]; i < tiles; ++i, at.next()) {
+        const int st = at.st;
+        if (!patience.wait(full + 8 * st, at.phase)) return false;
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
           if (i < from[w]) continue;
-          const int b = 2 * w + (buf[w] & 1);
-          if (!patience.wait(t_empty + 8 * b, ((buf[w] >> 1) & 1) ^ 1)) return false;
-          ++buf[w];
+          const int b = n_s % CW_S;
+          if (!patience.wait(t_empty + 8 * b, (n_s / CW_S & 1) ^ 1)) return false;
+          ++n_s;
           tm_after_sync();
-          const uint64_t rows = k_tile + (w * A::TILE >> 4), columns = q_tile + ((uint32_t)st * A::TILE >> 4);
+          const uint64_t columns = q_tile + ((uint32_t)st * P::TILE >> 4);
           if (elected()) {
 #pragma unroll
             for (int x = 0; x < D / 16; ++x) {
               const uint32_t off = ((x >> 2) * A::SLAB + (x & 3) * 32) >> 4;
-              mma_ss(TM + 128 * b, rows + off, columns + off, kind, x > 0);
+              mma_ts(TM + 128 * (1 + b), TM + D / 2 * w + 8 * x, columns + off, kind, x > 0);
             }
-            mma_commit(t_full + 8 * b);
+            mma_commit(t_full + 32 * w + 8 * (own[w] & 3));
           }
+          ++own[w];
         }
         if (elected()) mma_commit(empty + 8 * st);
       }
-      if (elected()) mma_commit(k_empty);
       return true;
     });
   } else if (warp == CW_ROWS + 1) {
     // -------------------------------------------------- copies
     const int box = min(1 << p.log2_page, 128), per = 128 / box;
     const int none = (int)((long long)p.n_pages * p.Hkv << p.log2_page);
-    uint32_t k_phase = 1;
-    int k = 0, n_unit = 0;
+    const int half = lane % A::HALVES, mine = lane / A::HALVES;
+    RingAt<S> at;
+    int k = 0, issued = 0;
     fence_proxy_async_global();
     weight_units(p, before, [&](const WeightUnit& u) {
       const int from = u.from(0, TQ), tiles = u.tiles(TQ);
       if (from >= tiles) return true;
-      // K: lane = (tile, box, half)
-      const int half = lane % A::HALVES, mine = lane / A::HALVES % per, w = lane / A::HALVES / per;
-      const int slot = u.t0 + 128 * w + mine * box;
-      long long row = -1;
-      if (w < 2 && slot < u.len)
-        row = paged_row(p.page_table[(size_t)u.b * p.max_pages + (slot >> p.log2_page)], p.n_pages, p.Hkv, u.h,
+      int row[2];
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int slot = u.t0 + 128 * w + mine * box;
+        long long x = -1;
+        if (mine < per && slot < u.len)
+          x = paged_row(p.page_table[(size_t)u.b * p.max_pages + (slot >> p.log2_page)], p.n_pages, p.Hkv, u.h,
                         p.log2_page, slot);
-      if (row < 0) row = none;
-      if (!patience.wait(k_empty, k_phase)) return false;
-      k_phase ^= 1;
-      ++n_unit;
-      if (lane == 0) mbar_arrive_expect_tx(k_full, 2 * A::TILE);
-      __syncwarp();
-      if (w < 2) tma_2d(base + w * A::TILE + half * A::SLAB + mine * box * 128, &kmap, 64 * half, (int)row, k_full);
-      __syncwarp();
-      for (int i = from; i < tiles; ++i, ++k) {
-        const int st = k % S, rows = min(TQ, u.n - i * TQ) * p.G;
+        row[w] = x < 0 ? none : (int)x;
+      }
+#pragma unroll
+      for (int w = 0; w < 2; ++w, at.next()) {
+        if (!patience.wait(empty + 8 * at.st, at.phase ^ 1)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * at.st, P::TILE);
+        __syncwarp();
+        if (mine < per)
+          tma_2d(ring + at.st * P::TILE + half * A::SLAB + mine * box * 128, &kmap, 64 * half, row[w], full + 8 * at.st);
+        __syncwarp();
+        ++issued;
+      }
+      for (int i = from; i < tiles; ++i, ++k, at.next()) {
+        const int rows = min(TQ, u.n - i * TQ) * p.G, sl = k % CW_LSE;
         const float* from_lse = p.lse + ((size_t)u.h * p.n_tokens + u.first + i * TQ) * p.G;
         float l[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) l[x] = lane + 32 * x < rows ? -ld_cg(from_lse + lane + 32 * x) : -INFINITY;
-        if (!patience.wait(lse_empty + 8 * st, (k / S & 1) ^ 1)) return false;
-        if (!patience.wait(empty + 8 * st, (k / S & 1) ^ 1)) return false;
+        if (!patience.wait(lse_empty + 8 * sl, (k / CW_LSE & 1) ^ 1)) return false;
 #pragma unroll
-        for (int x = 0; x < 4; ++x) lse[128 * st + lane + 32 * x] = l[x];
+        for (int x = 0; x < 4; ++x) lse[128 * sl + lane + 32 * x] = l[x];
         __syncwarp();
-        if (lane == 0) {
-          mbar_arrive(lse_full + 8 * st);
-          mbar_arrive_expect_tx(full + 8 * st, A::HALVES * TQ * p.G * 128);
-        }
+        if (lane == 0) mbar_arrive(lse_full + 8 * sl);
+        if (!patience.wait(empty + 8 * at.st, at.phase ^ 1)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(full + 8 * at.st, A::HALVES * TQ * p.G * 128);
         __syncwarp();
         if (lane < A::HALVES)
-          tma_3d(ring + st * A::TILE + lane * A::SLAB, &qmap, 64 * lane, u.h * p.G, u.first + i * TQ, full + 8 * st);
+          tma_3d(ring + at.st * P::TILE + lane * A::SLAB, &qmap, 64 * lane, u.h * p.G, u.first + i * TQ, full + 8 * at.st);
         __syncwarp();
+        ++issued;
       }
       return true;
     });
     if (misc[1]) {  // (as above)
-      bool all = n_unit == 0 || mbar_wait_bounded(k_full, (n_unit - 1) & 1, 8 * p.wait_ns);
-      for (int i = max(0, k - S); i < k; ++i)
+      bool all = true;
+      for (int i = max(0, issued - S); i < issued; ++i)
         all = mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, 8 * p.wait_ns) && all;
       if (!all && lane == 0) atomicOr(p.status, 4);
     }
