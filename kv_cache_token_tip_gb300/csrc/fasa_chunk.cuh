@@ -1,5 +1,5 @@
 // What the kernels of the attention of chunks share: the line of units in shared
-// memory, and the join of units that were cut.
+// memory, the join of units that were cut, and the units of the weights' pass.
 //
 // For a row (a new token and a query head) with z_t = log2(e) q . K_t / sqrt(d) over the
 // slots that the token sees: m = max z_t, l = sum 2^(z_t - m), o = sum 2^(z_t - m) V_t,
@@ -174,6 +174,71 @@ cudaError_t launch_chunk_join(const ChunkParams& p, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T, D>, p);
+}
+
+// ------------------------------------------------------------------ weights
+// A unit of the weights' pass: slots [t0, t0 + SLOTS) of KV head h of sequence b, which all
+// of its tokens that see them read.
+struct WeightUnit {
+  int b, h, t0;
+  ChunkSeq q;
+  __device__ int tiles(int TQ) const { return (q.n + TQ - 1) / TQ; }  // of TQ tokens
+  // The first of them that sees a slot of t0 + off or behind (all of them, if there is none).
+  __device__ int from(int off, int TQ) const {
+    return t0 + off < q.len ? max(0, t0 + off - (q.len - q.n)) / TQ : tiles(TQ);
+  }
+};
+
+// Units of one head before each sequence, in shared memory (B + 1 words).  Every thread of
+// the block calls it; ends with a barrier.  scan: NT / 32 words.
+template <int NT, int SLOTS>
+__device__ void weight_line(const ChunkParams& p, int* before, int* scan) {
+  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0};
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int run = (p.B + NT - 1) / NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
+  int sum = 0;
+  bool bad = false;
+  for (int b = b0; b < b1; ++b) {
+    before[b] = sum;
+    const ChunkSeq q = line.sequence(b, &bad);
+    if (q.n > 0) sum += (q.len + SLOTS - 1) / SLOTS;
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += y;
+  }
+  if (lane == 31) scan[warp] = incl;
+  __syncthreads();
+  int pre = incl - sum;
+#pragma unroll
+  for (int v = 0; v < NT / 32; ++v) pre += v < warp ? scan[v] : 0;
+  for (int b = b0; b < b1; ++b) before[b] += pre;
+  if (tid == NT - 1) before[p.B] = pre + sum;
+  __syncthreads();
+}
+
+// f(unit) for each of this block's units, in order; false ends it.  A head's units fall in
+// cost (the later the slots, the fewer tokens see them), so they are dealt there and back.
+template <int SLOTS, class F>
+__device__ __forceinline__ void weight_units(const ChunkParams& p, const int* before, F&& f) {
+  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0};
+  const int total = before[p.B] * p.Hkv, P = gridDim.x, c = blockIdx.x;
+  for (int k = 0; (long long)k * P < total; ++k) {
+    const long long x = (k & 1) ? (long long)(k + 1) * P - 1 - c : (long long)k * P + c;
+    if (x >= total) continue;
+    int lo = 0, hi = p.B;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (before[mid] * p.Hkv <= x) lo = mid;
+      else hi = mid;
+    }
+    const int rem = (int)x - before[lo] * p.Hkv;
+    bool bad = false;
+    const WeightUnit u{lo, rem % p.Hkv, rem / p.Hkv * SLOTS, line.sequence(lo, &bad)};
+    if (!f(u)) return;
+  }
 }
 
 }  // namespace fasa

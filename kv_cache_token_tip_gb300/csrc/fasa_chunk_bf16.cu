@@ -5,8 +5,8 @@
 // Per tile of rows and of slots: S = Q K^T (fp32, tensor memory), P = 2^(scale S - m) by
 // a warpgroup, a row to a thread, back to tensor memory in bf16 over S, O += P V.  m
 // follows the row's maximum only where it rises by more than 2^8: O is seldom scaled, and
-// out = O / sum P is the same.  Roles: two warpgroups for each tile of rows, half of a
-// row's columns to a thread, a warp that issues the matrix instructions, one that copies.
+// out = O / sum P is the same.  Roles: a warpgroup for each tile of rows, a warp that
+// issues the matrix instructions, one that copies.
 // While the tensor cores work for one tile of rows, its softmax is worked out for the other.
 #include <cuda.h>
 #include <cuda_bf16.h>
@@ -496,41 +496,6 @@ struct RingAt {
   }
 };
 
-// New tokens of a sequence, and where they begin.
-__device__ __forceinline__ int2 chunk_rows(const ChunkParams& p, int b) {
-  if (!p.cu_new) return make_int2(b, 1);
-  const int x0 = p.cu_new[b], x1 = p.cu_new[b + 1];
-  return make_int2(x0, 0 <= x0 && x0 <= x1 && x1 <= p.n_tokens ? x1 - x0 : 0);
-}
-
-struct WeightUnit {
-  int b, h, t0, first, n, len;
-  // The first tile of rows that sees a slot of tile w, and how many tiles there are.
-  __device__ int from(int w, int TQ) const { return t0 + 128 * w < len ? max(0, t0 + 128 * w - (len - n)) / TQ : tiles(TQ); }
-  __device__ int tiles(int TQ) const { return (n + TQ - 1) / TQ; }
-};
-
-// f(unit) for each of this block's units, in order; the same for every role.
-template <class F>
-__device__ __forceinline__ void weight_units(const ChunkParams& p, const int* before, F&& f) {
-  const int total = before[p.B] * p.Hkv, P = gridDim.x, c = blockIdx.x;
-  for (int k = 0;; ++k) {
-    const long long x = (k & 1) ? (long long)(k + 1) * P - 1 - c : (long long)k * P + c;
-    if ((long long)k * P >= total) return;
-    if (x >= total) continue;
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before[mid] * p.Hkv <= x) lo = mid;
-      else hi = mid;
-    }
-    const int rem = (int)x - before[lo] * p.Hkv;
-    const int2 rows = chunk_rows(p, lo);
-    WeightUnit u{lo, rem % p.Hkv, rem / p.Hkv * 256, rows.x, rows.y, min(max(p.seq_lens[lo], 0), p.T_cap)};
-    if (!f(u)) return;
-  }
-}
-
 template <int D>
 __global__ void __launch_bounds__(CW_NT, 1)
     chunk_weight_bf16_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap qmap,
@@ -572,27 +537,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
   tm_before_sync();
   paged_go();
   paged_wait();
-  {  // pairs of tiles of slots, before each sequence
-    const int run = (p.B + CW_NT - 1) / CW_NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      before[b] = sum;
-      if (chunk_rows(p, b).y > 0) sum += (min(max(p.seq_lens[b], 0), p.T_cap) + 255) / 256;
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, incl, o);
-      if (lane >= o) incl += y;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    int pre = incl - sum;
-    for (int v = 0; v < CW_NT / 32; ++v) pre += v < warp ? scan[v] : 0;
-    for (int b = b0; b < b1; ++b) before[b] += pre;
-    if (tid == CW_NT - 1) before[p.B] = pre + sum;
-    __syncthreads();
-  }
+  weight_line<CW_NT, 256>(p, before, scan);
   tm_after_sync();
   const Patience patience{misc + 1, p.status, p.wait_ns};
   // (640 threads of 96 registers: 512 of 104 and 128 of 64)
@@ -608,11 +553,11 @@ __global__ void __launch_bounds__(CW_NT, 1)
     int at_k = 0;  // place of the next unit's K in the ring
     uint32_t k_phase = 0;
     int k = 0, n_s = 0, own = 0;  // Q tiles, S tiles, and those of these rows, so far
-    weight_units(p, before, [&](const WeightUnit& u) {
-      const int slot = u.t0 + 128 * w + row, from = u.from(0, TQ), mine = u.from(w, TQ), tiles = u.tiles(TQ);
+    weight_units<256>(p, before, [&](const WeightUnit& u) {
+      const int slot = u.t0 + 128 * w + row, from = u.from(0, TQ), mine = u.from(128 * w, TQ), tiles = u.tiles(TQ);
       if (from >= tiles) return true;
       int page = -1;
-      if (slot < u.len) page = p.page_table[(size_t)u.b * p.max_pages + (slot >> p.log2_page)];
+      if (slot < u.q.len) page = p.page_table[(size_t)u.b * p.max_pages + (slot >> p.log2_page)];
       float* weight = p.weight + ((size_t)u.b * p.Hkv + u.h) * p.T_cap + slot;
       const bool live = page >= 0 && page < p.n_pages;
       const float old = live && !half ? *weight : 0.f;
@@ -641,7 +586,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(k_here);
       }
-      const int second = u.from(1, TQ);
+      const int second = u.from(128, TQ);
       for (int i = from; ok && i < tiles; ++i, ++k) {
         const int st = k % CW_LSE;
         ok = patience.wait(lse_full + 8 * st, (k / CW_LSE) & 1);
@@ -663,7 +608,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
           __syncwarp();
           if (lane == 0) mbar_arrive(t_empty + 8 * buf);
           // the rows of this tile that there are, and of them the first that sees the slot
-          const int rows = min(TQ, u.n - i * TQ) * p.G, lo = (slot - (u.len - u.n) - i * TQ) * p.G - 64 * half;
+          const int rows = min(TQ, u.q.n - i * TQ) * p.G, lo = (slot - (u.q.len - u.q.n) - i * TQ) * p.G - 64 * half;
           if (rows < TQ * p.G || __any_sync(0xffffffffu, lo > 0)) {
 #pragma unroll
             for (int x = 0; x < 64; ++x)
@@ -704,8 +649,8 @@ __global__ void __launch_bounds__(CW_NT, 1)
     RingAt<S> at;
     uint32_t k_phase = 0;
     int n_s = 0, own[2] = {0, 0};
-    weight_units(p, before, [&](const WeightUnit& u) {
-      const int from[2] = {u.from(0, TQ), u.from(1, TQ)}, tiles = u.tiles(TQ);
+    weight_units<256>(p, before, [&](const WeightUnit& u) {
+      const int from[2] = {u.from(0, TQ), u.from(128, TQ)}, tiles = u.tiles(TQ);
       if (from[0] >= tiles) return true;
       int k_at[2];
 #pragma unroll
@@ -754,7 +699,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
     RingAt<S> at;
     int k = 0, issued = 0;
     fence_proxy_async_global();
-    weight_units(p, before, [&](const WeightUnit& u) {
+    weight_units<256>(p, before, [&](const WeightUnit& u) {
       const int from = u.from(0, TQ), tiles = u.tiles(TQ);
       if (from >= tiles) return true;
       int row[2];
@@ -762,7 +707,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
       for (int w = 0; w < 2; ++w) {
         const int slot = u.t0 + 128 * w + mine * box;
         long long x = -1;
-        if (mine < per && slot < u.len)
+        if (mine < per && slot < u.q.len)
           x = paged_row(p.page_table[(size_t)u.b * p.max_pages + (slot >> p.log2_page)], p.n_pages, p.Hkv, u.h,
                         p.log2_page, slot);
         row[w] = x < 0 ? none : (int)x;
@@ -778,8 +723,8 @@ __global__ void __launch_bounds__(CW_NT, 1)
         ++issued;
       }
       for (int i = from; i < tiles; ++i, ++k, at.next()) {
-        const int rows = min(TQ, u.n - i * TQ) * p.G, sl = k % CW_LSE;
-        const float* from_lse = p.lse + ((size_t)u.h * p.n_tokens + u.first + i * TQ) * p.G;
+        const int rows = min(TQ, u.q.n - i * TQ) * p.G, sl = k % CW_LSE;
+        const float* from_lse = p.lse + ((size_t)u.h * p.n_tokens + u.q.first + i * TQ) * p.G;
         float l[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) l[x] = lane + 32 * x < rows ? -ld_cg(from_lse + lane + 32 * x) : -INFINITY;
@@ -792,7 +737,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
         if (lane == 0) mbar_arrive_expect_tx(full + 8 * at.st, A::HALVES * TQ * p.G * 128);
         __syncwarp();
         if (lane < A::HALVES)
-          tma_3d(ring + at.st * P::TILE + lane * A::SLAB, &qmap, 64 * lane, u.h * p.G, u.first + i * TQ, full + 8 * at.st);
+          tma_3d(ring + at.st * P::TILE + lane * A::SLAB, &qmap, 64 * lane, u.h * p.G, u.q.first + i * TQ, full + 8 * at.st);
         __syncwarp();
         ++issued;
       }

@@ -77,7 +77,7 @@ struct ChunkParams {
 struct ChunkShape {
   int tokens, tile, per_sm;
 };
-inline ChunkShape chunk_shape(bool bf16, int G) { return bf16 ? ChunkShape{2 * (128 / G), 128, 1} : ChunkShape{64 / G, 64, 1}; }
+inline ChunkShape chunk_shape(bool bf16, int G) { return bf16 ? ChunkShape{2 * (128 / G), 128, 1} : ChunkShape{128 / G, 64, 1}; }
 
 cudaError_t launch_paged_assign(const AssignParams& p, int sms, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, bool bf16, bool half, int sms, cudaStream_t s);
