@@ -18,8 +18,9 @@ namespace fasa {
 // The line, its costs in `before` (shared memory, B + 1 words).  Every thread of the block
 // calls it; ends with a barrier.  scan: NT / 32 words.
 template <int NT>
-__device__ ChunkLine chunk_line(const ChunkParams& p, long long* before, long long* scan, int T, int KT, bool report) {
-  const ChunkLine line{before, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, T, KT};
+__device__ ChunkLine chunk_line(const ChunkParams& p, long long* before, long long* scan, int T, int KT, int unit,
+                                bool report) {
+  const ChunkLine line{before, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, T, KT, unit};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.B + NT - 1) / NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
   bool bad = false;
@@ -27,7 +28,7 @@ __device__ ChunkLine chunk_line(const ChunkParams& p, long long* before, long lo
   for (int b = b0; b < b1; ++b) {
     const ChunkSeq q = line.sequence(b, &bad);
     before[b] = sum;
-    sum += ChunkLine::cost_of(q.n, q.len, T);
+    sum += line.cost_of(q.n, q.len);
   }
   if (report && bad) atomicOr(p.status, 1);
   long long incl = sum;
@@ -193,7 +194,7 @@ struct WeightUnit {
 // the block calls it; ends with a barrier.  scan: NT / 32 words.
 template <int NT, int SLOTS>
 __device__ void weight_line(const ChunkParams& p, int* before, int* scan) {
-  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0};
+  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0, 0};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.B + NT - 1) / NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
   int sum = 0;
@@ -223,7 +224,7 @@ __device__ void weight_line(const ChunkParams& p, int* before, int* scan) {
 // cost (the later the slots, the fewer tokens see them), so they are dealt there and back.
 template <int SLOTS, class F>
 __device__ __forceinline__ void weight_units(const ChunkParams& p, const int* before, F&& f) {
-  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0};
+  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0, 0};
   const int total = before[p.B] * p.Hkv, P = gridDim.x, c = blockIdx.x;
   for (int k = 0; (long long)k * P < total; ++k) {
     const long long x = (k & 1) ? (long long)(k + 1) * P - 1 - c : (long long)k * P + c;

@@ -26,6 +26,7 @@ constexpr int CB_NT = 384;           // 8 warps of rows, one of instructions, on
 constexpr int CB_ROWS = 8;
 constexpr uint32_t TM = 0;           // where tensor memory begins, which a block takes whole
 constexpr int CB_K = 128;            // slots of a tile
+constexpr int CB_UNIT = 128;         // what a unit costs beside its tiles, in slots
 constexpr float CB_SLACK = 8.f;      // powers of two that a row's maximum may run ahead of m
 
 template <int D>
@@ -108,7 +109,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
   paged_wait();
   paged_go();
   const ChunkLine line = chunk_line<CB_NT>(p, reinterpret_cast<long long*>(sm + P::OFF_SEQ),
-                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CB_K, blockIdx.x == 0);
+                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CB_K, CB_UNIT, blockIdx.x == 0);
   tm_after_sync();
   const int parts = line.parts(p.parts), c = blockIdx.x;
   const Patience patience{misc + 1, p.status, p.wait_ns};

@@ -19,6 +19,7 @@ namespace fasa {
 namespace {
 
 constexpr int CF_NT = 256, CF_M = 128, CF_K = 64;
+constexpr int CF_UNIT = 48;  // what a unit costs beside its tiles, in slots
 
 template <int D>
 struct CfPlan {
@@ -115,7 +116,7 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_f32_kernel(const __grid_consta
   paged_wait();
   paged_go();
   const ChunkLine line = chunk_line<CF_NT>(p, reinterpret_cast<long long*>(sm + P::OFF_LINE),
-                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CF_K, blockIdx.x == 0);
+                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CF_K, CF_UNIT, blockIdx.x == 0);
   const int parts = line.parts(p.parts), c = blockIdx.x;
   if (tid == 0) note_none(p, c);
   if (c >= parts) return;
@@ -137,6 +138,7 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_f32_kernel(const __grid_consta
         fetch_slots<D>(p.k_pages, rows_at + (f0 & 1) * CF_K, ks);
         fetch_slots<D>(p.v_pages, rows_at + (f0 & 1) * CF_K, vs);
       }
+      const bool busy = tid / 32 * 16 < rows;  // whether this warp has rows
       float m[8], l[8];
       uint64_t o[8][2 * E];
       int see[8];
@@ -156,58 +158,62 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_f32_kernel(const __grid_consta
         if (tid < CF_K) rows_at[(t + 1 & 1) * CF_K + tid] = next;
         __syncthreads();
         if (tid < CF_K && t + 2 < f1) next = slot_row(p, u.b, u.h, t0 + 2 * CF_K + tid, len, true);
-        float z[8][4];
-        products<D>(qs, ks, z);
-        int there = 0;  // of this thread's slots
+        if (busy) {
+          float z[8][4];
+          products<D>(qs, ks, z);
+          int there = 0;  // of this thread's slots
 #pragma unroll
-        for (int j = 0; j < 4; ++j) there |= (here[tx + 16 * j] >= 0) << j;
+          for (int j = 0; j < 4; ++j) there |= (here[tx + 16 * j] >= 0) << j;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          float mx = -INFINITY;
+          for (int i = 0; i < 8; ++i) {
+            float mx = -INFINITY;
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            z[i][j] = (there >> j & 1) && t0 + tx + 16 * j < see[i] ? z[i][j] * p.scale : -INFINITY;
-            mx = fmaxf(mx, z[i][j]);
-          }
+            for (int j = 0; j < 4; ++j) {
+              z[i][j] = (there >> j & 1) && t0 + tx + 16 * j < see[i] ? z[i][j] * p.scale : -INFINITY;
+              mx = fmaxf(mx, z[i][j]);
+            }
 #pragma unroll
-          for (int s = 1; s < 16; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
-          const float mn = fmaxf(m[i], mx), ms = mn == -INFINITY ? 0.f : mn;
-          if (mn > m[i]) {
-            const float a = exp2f(m[i] - ms);
-            const uint64_t a2 = pair_of(a, a);
-            l[i] *= a;
+            for (int s = 1; s < 16; s <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, s));
+            const float mn = fmaxf(m[i], mx), ms = mn == -INFINITY ? 0.f : mn;
+            if (mn > m[i]) {
+              const float a = exp2f(m[i] - ms);
+              const uint64_t a2 = pair_of(a, a);
+              l[i] *= a;
 #pragma unroll
-            for (int e = 0; e < 2 * E; ++e) o[i][e] = mul2(o[i][e], a2);
-            m[i] = mn;
-          }
+              for (int e = 0; e < 2 * E; ++e) o[i][e] = mul2(o[i][e], a2);
+              m[i] = mn;
+            }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const float w = exp2f(z[i][j] - ms);
-            l[i] += w;
-            ps[(8 * ty + i) * P::LP + tx + 16 * j] = w;
+            for (int j = 0; j < 4; ++j) {
+              const float w = exp2f(z[i][j] - ms);
+              l[i] += w;
+              ps[(8 * ty + i) * P::LP + tx + 16 * j] = w;
+            }
           }
         }
         cp_async_wait<0>();
         __syncthreads();  // K is read, P and V are there
         if (more) fetch_slots<D>(p.k_pages, rows_at + (t + 1 & 1) * CF_K, ks);
+        if (busy) {
 #pragma unroll 2
-        for (int s4 = 0; s4 < CF_K; s4 += 4) {
-          ulonglong2 v[4][E];
+          for (int s4 = 0; s4 < CF_K; s4 += 4) {
+            ulonglong2 v[4][E];
 #pragma unroll
-          for (int s = 0; s < 4; ++s)
+            for (int s = 0; s < 4; ++s)
 #pragma unroll
-            for (int e = 0; e < E; ++e) v[s][e] = *reinterpret_cast<const ulonglong2*>(vs + (s4 + s) * P::LD + 4 * tx + 64 * e);
+              for (int e = 0; e < E; ++e) v[s][e] = *reinterpret_cast<const ulonglong2*>(vs + (s4 + s) * P::LD + 4 * tx + 64 * e);
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float4 w = *reinterpret_cast<const float4*>(ps + (8 * ty + i) * P::LP + s4);
-            const float ws[4] = {w.x, w.y, w.z, w.w};
+            for (int i = 0; i < 8; ++i) {
+              const float4 w = *reinterpret_cast<const float4*>(ps + (8 * ty + i) * P::LP + s4);
+              const float ws[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
-            for (int s = 0; s < 4; ++s) {
-              const uint64_t w2 = pair_of(ws[s], ws[s]);
+              for (int s = 0; s < 4; ++s) {
+                const uint64_t w2 = pair_of(ws[s], ws[s]);
 #pragma unroll
-              for (int e = 0; e < E; ++e) {
-                o[i][2 * e] = fma2(w2, v[s][e].x, o[i][2 * e]);
-                o[i][2 * e + 1] = fma2(w2, v[s][e].y, o[i][2 * e + 1]);
+                for (int e = 0; e < E; ++e) {
+                  o[i][2 * e] = fma2(w2, v[s][e].x, o[i][2 * e]);
+                  o[i][2 * e + 1] = fma2(w2, v[s][e].y, o[i][2 * e + 1]);
+                }
               }
             }
           }
@@ -281,6 +287,7 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_weight_f32_kernel(const __grid
       if (i + 1 < tiles) fetch(i + 1);
       const float* lse = reinterpret_cast<const float*>(sm + P::W_LSE) + (i & 1) * CF_M;
       float z[8][4];
+      if (tid / 32 * 16 >= min(TU, u.q.n - i * TU) * p.G) continue;  // no rows of this warp
       products<D>(reinterpret_cast<const float*>(sm + P::W_Q + (i & 1) * P::Q_BYTES), ks, z);
       float part[4] = {};
 #pragma unroll

@@ -5,7 +5,7 @@
 // i of them holds T tokens with the G heads of a KV head as rows.  Unit (b, h, i) is
 // that tile of KV head h; it reads the slots that its last token sees, in tiles of
 // KT.  All units in order form one line, cut into parts of equal cost, one to a CTA:
-// a unit costs its first tile's start-up CHUNK_UNIT_COST and a count of slots,
+// a unit costs its start and its end, `unit`, and a count of slots,
 // a + (i + 1) T, a = max(len - n, 0), no less than it reads, whose sum over i is a
 // formula, so that a part finds its place without a list of units.
 #pragma once
@@ -20,7 +20,6 @@
 
 namespace fasa {
 
-constexpr int CHUNK_UNIT_COST = 128;  // slots
 constexpr int CHUNK_MAX_SMS = 160;    // the workspace has room for their parts
 
 // A sequence's new tokens, where they begin among the call's rows, and its slots.
@@ -32,7 +31,7 @@ struct ChunkLine {
   const long long* before;  // [B + 1]: cost of one head of the sequences before b
   const int* cu_new;        // null: a token a sequence
   const int* seq_lens;
-  int n_tokens, T_cap, B, Hkv, T, KT;
+  int n_tokens, T_cap, B, Hkv, T, KT, unit;
 
   // Sequence b as far as it fits: no token of a range that is not within the call's rows.
   FASA_CHUNK_HD ChunkSeq sequence(int b, bool* bad) const {
@@ -53,15 +52,15 @@ struct ChunkLine {
   }
   FASA_CHUNK_HD static int tiles_of(int n, int T) { return (n + T - 1) / T; }
   // Cost of the first i units of a head of a sequence.
-  FASA_CHUNK_HD static long long cost_of(int n, int len, int T, int i) {
+  FASA_CHUNK_HD long long cost_of(int n, int len, int i) const {
     const long long a = len > n ? len - n : 0;
-    return (long long)i * (CHUNK_UNIT_COST + a) + (long long)T * i * (i + 1) / 2;
+    return (long long)i * (unit + a) + (long long)T * i * (i + 1) / 2;
   }
-  FASA_CHUNK_HD static long long cost_of(int n, int len, int T) { return cost_of(n, len, T, tiles_of(n, T)); }
+  FASA_CHUNK_HD long long cost_of(int n, int len) const { return cost_of(n, len, tiles_of(n, T)); }
 
   FASA_CHUNK_HD long long total() const { return before[B] * Hkv; }
   FASA_CHUNK_HD int parts(int most) const {
-    const long long t = total(), least = CHUNK_UNIT_COST + KT, n = (t + least - 1) / least;
+    const long long t = total(), n = (t + KT - 1) / KT;  // (no part is shorter than a tile)
     return n < most ? (int)n : most;
   }
   FASA_CHUNK_HD long long part_begin(int parts, int c) const {
@@ -82,7 +81,7 @@ struct ChunkUnit {
     const int last = (i + 1) * l.T < q.n ? (i + 1) * l.T : q.n;
     const int see = q.len - q.n + last;  // (all of len at most)
     tiles = see > 0 ? (see + l.KT - 1) / l.KT : 0;
-    cost = CHUNK_UNIT_COST + (q.len > q.n ? q.len - q.n : 0) + (long long)(i + 1) * l.T;
+    cost = l.unit + (q.len > q.n ? q.len - q.n : 0) + (long long)(i + 1) * l.T;
   }
   // The unit that holds position y, 0 <= y < total.
   FASA_CHUNK_HD void find(const ChunkLine& l, long long y) {
@@ -104,11 +103,11 @@ struct ChunkUnit {
     hi = ChunkLine::tiles_of(q.n, l.T);
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (ChunkLine::cost_of(q.n, q.len, l.T, mid) <= y) lo = mid;
+      if (l.cost_of(q.n, q.len, mid) <= y) lo = mid;
       else hi = mid;
     }
     i = lo;
-    begin += h * head + ChunkLine::cost_of(q.n, q.len, l.T, i);
+    begin += h * head + l.cost_of(q.n, q.len, i);
     fill(l);
   }
   // The unit behind this one; only where there is one.
@@ -127,11 +126,11 @@ struct ChunkUnit {
     fill(l);
   }
   // Tiles of the unit that lie before position y: tile 0 at its begin, tile t at
-  // CHUNK_UNIT_COST + KT t behind it.
+  // unit + KT t behind it.
   FASA_CHUNK_HD int before(const ChunkLine& l, long long y) const {
     if (y <= begin) return 0;
     if (y >= begin + cost) return tiles;
-    const long long r = y - begin - CHUNK_UNIT_COST;
+    const long long r = y - begin - l.unit;
     const int t = r > 0 ? (int)((r + l.KT - 1) / l.KT) : 0;
     const int at_least = t > 1 ? t : 1;
     return at_least < tiles ? at_least : tiles;

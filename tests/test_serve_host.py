@@ -154,18 +154,18 @@ using namespace fasa;
 
 // The parts hold every tile of every unit once and in order, a unit without tiles has one
 // part that it begins in, and the place of a cut is found again from the cut alone.
-static int check(const std::vector<int>& n, const std::vector<int>& len, int Hkv, int T, int KT, int most) {
+static int check(const std::vector<int>& n, const std::vector<int>& len, int Hkv, int T, int KT, int unit, int most) {
   const int B = (int)n.size();
   std::vector<long long> costs(B + 1);
   std::vector<int> cu(B + 1);
+  for (int b = 0; b < B; ++b) cu[b + 1] = cu[b] + n[b];
+  const ChunkLine line{costs.data(), cu.data(), len.data(), cu[B], 1 << 18, B, Hkv, T, KT, unit};
   long long before = 0;
   for (int b = 0; b < B; ++b) {
     costs[b] = before;
-    cu[b + 1] = cu[b] + n[b];
-    before += ChunkLine::cost_of(n[b], len[b], T);
+    before += line.cost_of(n[b], len[b]);
   }
   costs[B] = before;
-  const ChunkLine line{costs.data(), cu.data(), len.data(), cu[B], 1 << 18, B, Hkv, T, KT};
   const int parts = line.parts(most);
   if (before == 0) { CHECK(parts == 0); return 0; }
   CHECK(parts >= 1 && parts <= most && line.part_begin(parts, 0) == 0 && line.part_begin(parts, parts) == line.total());
@@ -221,10 +221,10 @@ int main() {
       len.push_back(n[b] + rand() % (long_a + 1));
       if (rand() % 9 == 0) len[b] = rand() % (n[b] + 1);  // more new tokens than cached ones
     }
-    if (check(n, len, 1 + rand() % 8, T, KT, 1 + rand() % 320)) return printf("case %d\n", k), 1;
+    if (check(n, len, 1 + rand() % 8, T, KT, rand() % 4 * 64, 1 + rand() % 320)) return printf("case %d\n", k), 1;
   }
   // the largest: positions past 32 bits
-  if (check({1 << 20}, {262144}, 2, 32, 128, 152) || check({1 << 18, 1 << 18}, {262144, 262144}, 3, 256, 128, 152)) return 1;
+  if (check({1 << 20}, {262144}, 2, 32, 128, 128, 152) || check({1 << 18, 1 << 18}, {262144, 262144}, 3, 256, 128, 16, 152)) return 1;
   printf("ok\n");
 }
 """
