@@ -190,56 +190,76 @@ struct WeightUnit {
   }
 };
 
-// Units of one head before each sequence, in shared memory (B + 1 words).  Every thread of
-// the block calls it; ends with a barrier.  scan: NT / 32 words.
+// Units of one head before each sequence, in shared memory (2 B + 2 words): first of those
+// with more tokens than a tile of rows holds, then of the others.  Every thread of the block
+// calls it; ends with a barrier.  scan: NT / 32 pairs of words.
 template <int NT, int SLOTS>
-__device__ void weight_line(const ChunkParams& p, int* before, int* scan) {
+__device__ void weight_line(const ChunkParams& p, int* before, int2* scan, int TQ) {
   const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0, 0};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.B + NT - 1) / NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
-  int sum = 0;
+  int2 sum = make_int2(0, 0);
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
-    before[b] = sum;
+    before[b] = sum.x;
+    before[p.B + 1 + b] = sum.y;
     const ChunkSeq q = line.sequence(b, &bad);
-    if (q.n > 0) sum += (q.len + SLOTS - 1) / SLOTS;
+    const int n = (q.len + SLOTS - 1) / SLOTS;
+    if (q.n > TQ) sum.x += n;
+    else if (q.n > 0) sum.y += n;
   }
-  int incl = sum;
+  int2 incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += y;
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    if (lane >= o) {
+      incl.x += x;
+      incl.y += y;
+    }
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  int pre = incl - sum;
+  int2 pre = make_int2(incl.x - sum.x, incl.y - sum.y);
 #pragma unroll
-  for (int v = 0; v < NT / 32; ++v) pre += v < warp ? scan[v] : 0;
-  for (int b = b0; b < b1; ++b) before[b] += pre;
-  if (tid == NT - 1) before[p.B] = pre + sum;
+  for (int v = 0; v < NT / 32; ++v) {
+    pre.x += v < warp ? scan[v].x : 0;
+    pre.y += v < warp ? scan[v].y : 0;
+  }
+  for (int b = b0; b < b1; ++b) {
+    before[b] += pre.x;
+    before[p.B + 1 + b] += pre.y;
+  }
+  if (tid == NT - 1) {
+    before[p.B] = pre.x + sum.x;
+    before[2 * p.B + 1] = pre.y + sum.y;
+  }
   __syncthreads();
 }
 
-// f(unit) for each of this block's units, in order; false ends it.  A head's units fall in
-// cost (the later the slots, the fewer tokens see them), so they are dealt there and back.
-template <int SLOTS, class F>
-__device__ __forceinline__ void weight_units(const ChunkParams& p, const int* before, F&& f) {
-  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0, 0};
-  const int total = before[p.B] * p.Hkv, P = gridDim.x, c = blockIdx.x;
-  for (int k = 0; (long long)k * P < total; ++k) {
-    const long long x = (k & 1) ? (long long)(k + 1) * P - 1 - c : (long long)k * P + c;
-    if (x >= total) continue;
-    int lo = 0, hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (before[mid] * p.Hkv <= x) lo = mid;
-      else hi = mid;
-    }
-    const int rem = (int)x - before[lo] * p.Hkv;
-    bool bad = false;
-    const WeightUnit u{lo, rem % p.Hkv, rem / p.Hkv * SLOTS, line.sequence(lo, &bad)};
-    if (!f(u)) return;
+// The x-th unit; false behind the last.  A head's units fall in cost (the later the slots,
+// the fewer tokens see them) and those of few tokens come last, so that blocks that take the
+// next one when they are done end together (a step of two prompts and 30 single tokens: 161
+// us dealt there and back, 148 so).
+template <int SLOTS>
+__device__ __forceinline__ bool weight_unit(const ChunkParams& p, const int* before, int x, WeightUnit& u) {
+  const int first = before[p.B] * p.Hkv;
+  const int* w = before;
+  if (x >= first) {
+    x -= first;
+    w += p.B + 1;
+    if (x >= w[p.B] * p.Hkv) return false;
   }
+  int lo = 0, hi = p.B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (w[mid] * p.Hkv <= x) lo = mid;
+    else hi = mid;
+  }
+  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0, 0};
+  const int rem = x - w[lo] * p.Hkv;
+  bool bad = false;
+  u = WeightUnit{lo, rem % p.Hkv, rem / p.Hkv * SLOTS, line.sequence(lo, &bad)};
+  return true;
 }
 
 }  // namespace fasa

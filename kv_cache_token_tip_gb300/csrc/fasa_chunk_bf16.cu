@@ -114,6 +114,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
   const int parts = line.parts(p.parts), c = blockIdx.x;
   const Patience patience{misc + 1, p.status, p.wait_ns};
   if (tid == 0) note_none(p, c);
+  if (tid == 0 && c == 0) *p.queue = 0;
   if (c < parts) {
     const long long y0 = line.part_begin(parts, c), y1 = line.part_begin(parts, c + 1);
     // (384 threads of 168 registers: 256 of 232 and 128 of 40)
@@ -443,8 +444,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
 // weight_t += sum over the rows that see slot t of 2^(scale S - log-sum of the row).  A
 // unit is 256 slots of a (sequence, KV head): two tiles of K as rows of S^T = K Q^T, the
 // rows of Q 128 at a time as its columns (K in tensor memory, Q in shared memory), so that a thread adds what one slot gets, in the
-// rows' order.  Units are dealt to the blocks there and back, since their costs fall with
-// the slots (the later, the fewer rows see them).
+// rows' order.
 constexpr int CW_NT = 640;           // 16 warps of slots, one of instructions, one of copies, two at rest
 constexpr int CW_ROWS = 16;
 constexpr int CW_S = 3;              // tiles of S in tensor memory, of 128 columns, behind the two tiles of K
@@ -476,11 +476,11 @@ struct CwPlan {
   static constexpr int TILE = A::TILE;
   static constexpr int OFF_LSE = STAGES * TILE;
   static constexpr int OFF_BAR = OFF_LSE + CW_LSE * 128 * 4;
-  static constexpr int BARS = 2 * STAGES + 2 * CW_LSE + 2 + 8 + CW_S + 1;
+  static constexpr int BARS = 2 * STAGES + 2 * CW_LSE + 2 + 8 + CW_S + 1 + 4;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
-  static constexpr int OFF_PAIR = (OFF_MISC + 8 + 15) / 16 * 16;
+  static constexpr int OFF_PAIR = (OFF_MISC + 16 + 15) / 16 * 16;
   static constexpr int OFF_LINE = OFF_PAIR + CW_ROWS / 2 * 128;
-  static constexpr int bytes(int B) { return 1024 + OFF_LINE + (B + 1) * 4; }
+  static constexpr int bytes(int B) { return 1024 + OFF_LINE + (2 * B + 2) * 4; }
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
 };
 
@@ -510,9 +510,9 @@ __global__ void __launch_bounds__(CW_NT, 1)
   const uint32_t ring = smem_u32(sm), full = ring + P::OFF_BAR, empty = full + 8 * S;
   const uint32_t lse_full = empty + 8 * S, lse_empty = lse_full + 8 * CW_LSE, k_go = lse_empty + 8 * CW_LSE;
   const uint32_t k_here = k_go + 8, t_full = k_go + 16, t_empty = t_full + 64, drain = t_empty + 8 * CW_S;
+  const uint32_t u_full = drain + 8, u_empty = drain + 24;
   volatile int* misc = reinterpret_cast<volatile int*>(sm + P::OFF_MISC);
   float* lse = reinterpret_cast<float*>(sm + P::OFF_LSE);
-  int* scan = reinterpret_cast<int*>(sm + P::OFF_PAIR);
   int* before = reinterpret_cast<int*>(sm + P::OFF_LINE);
   const int TQ = 128 / p.G;
   if (warp == 0) tm_alloc(ring + P::OFF_MISC, 512);
@@ -533,14 +533,29 @@ __global__ void __launch_bounds__(CW_NT, 1)
     for (int i = 0; i < 8; ++i) mbar_init(t_full + 8 * i, 1);
     for (int i = 0; i < CW_S; ++i) mbar_init(t_empty + 8 * i, 8);
     mbar_init(drain, 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(u_full + 8 * i, 1);
+      mbar_init(u_empty + 8 * i, CW_ROWS + 1);
+    }
     fence_mbar_init();
   }
   tm_before_sync();
   paged_go();
   paged_wait();
-  weight_line<CW_NT, 256>(p, before, scan);
+  weight_line<CW_NT, 256>(p, before, reinterpret_cast<int2*>(sm + P::OFF_PAIR), TQ);
   tm_after_sync();
   const Patience patience{misc + 1, p.status, p.wait_ns};
+  // f(unit) for each unit of this block, in order, as the copying warp takes them
+  auto units = [&](auto&& f) {
+    for (int i = 0;; ++i) {
+      if (!patience.wait(u_full + 8 * (i & 1), i >> 1 & 1)) return;
+      const int x = misc[2 + (i & 1)];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(u_empty + 8 * (i & 1));
+      WeightUnit u;
+      if (!weight_unit<256>(p, before, x, u) || !f(u)) return;
+    }
+  };
   // (640 threads of 96 registers: 512 of 104 and 128 of 64)
   if (warp < CW_ROWS) more_registers<104>();
   else fewer_registers<64>();
@@ -554,7 +569,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
     int at_k = 0;  // place of the next unit's K in the ring
     uint32_t k_phase = 0;
     int k = 0, n_s = 0, own = 0;  // Q tiles, S tiles, and those of these rows, so far
-    weight_units<256>(p, before, [&](const WeightUnit& u) {
+    units([&](const WeightUnit& u) {
       const int slot = u.t0 + 128 * w + row, from = u.from(0, TQ), mine = u.from(128 * w, TQ), tiles = u.tiles(TQ);
       if (from >= tiles) return true;
       int page = -1;
@@ -650,7 +665,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
     RingAt<S> at;
     uint32_t k_phase = 0;
     int n_s = 0, own[2] = {0, 0};
-    weight_units<256>(p, before, [&](const WeightUnit& u) {
+    units([&](const WeightUnit& u) {
       const int from[2] = {u.from(0, TQ), u.from(128, TQ)}, tiles = u.tiles(TQ);
       if (from[0] >= tiles) return true;
       int k_at[2];
@@ -700,7 +715,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
     RingAt<S> at;
     int k = 0, issued = 0;
     fence_proxy_async_global();
-    weight_units<256>(p, before, [&](const WeightUnit& u) {
+    auto copy = [&](const WeightUnit& u) {
       const int from = u.from(0, TQ), tiles = u.tiles(TQ);
       if (from >= tiles) return true;
       int row[2];
@@ -743,7 +758,22 @@ __global__ void __launch_bounds__(CW_NT, 1)
         ++issued;
       }
       return true;
-    });
+    };
+    int x = blockIdx.x;  // (the first unit is the block's own; the queue counts those behind)
+    for (int i = 0;; ++i) {
+      if (!patience.wait(u_empty + 8 * (i & 1), (i >> 1 & 1) ^ 1)) break;
+      if (lane == 0) {
+        misc[2 + (i & 1)] = x;
+        mbar_arrive(u_full + 8 * (i & 1));
+      }
+      __syncwarp();
+      WeightUnit u;
+      if (!weight_unit<256>(p, before, x, u)) break;
+      int next = 0;  // (on its way while this one is copied)
+      if (lane == 0) next = gridDim.x + atomicAdd(p.queue, 1);
+      if (!copy(u)) break;
+      x = __shfl_sync(0xffffffffu, next, 0);
+    }
     if (misc[1]) {  // (as above)
       bool all = true;
       for (int i = max(0, issued - S); i < issued; ++i)

@@ -34,8 +34,8 @@ struct CfPlan {
   static constexpr int bytes(int B) { return OFF_LINE + (B + 1) * 8; }
   // weights: K, Q and its rows' log-sums twice, sums
   static constexpr int W_Q = K_BYTES, W_LSE = W_Q + 2 * Q_BYTES, W_SUM = W_LSE + 2 * CF_M * 4;
-  static constexpr int W_ROWS = W_SUM + 16 * LP * 4, W_SCAN = W_ROWS + CF_K * 4, W_LINE = W_SCAN + CF_NT / 32 * 4;
-  static constexpr int weight_bytes(int B) { return W_LINE + (B + 1) * 4; }
+  static constexpr int W_ROWS = W_SUM + 16 * LP * 4, W_SCAN = W_ROWS + CF_K * 4, W_LINE = W_SCAN + CF_NT / 32 * 8;
+  static constexpr int weight_bytes(int B) { return W_LINE + (2 * B + 2) * 4; }
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448 && weight_bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
 };
 
@@ -119,6 +119,7 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_f32_kernel(const __grid_consta
                                            reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CF_K, CF_UNIT, blockIdx.x == 0);
   const int parts = line.parts(p.parts), c = blockIdx.x;
   if (tid == 0) note_none(p, c);
+  if (tid == 0 && c == 0) *p.queue = 0;
   if (c >= parts) return;
   const long long y0 = line.part_begin(parts, c), y1 = line.part_begin(parts, c + 1);
   ChunkUnit u;
@@ -264,10 +265,13 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_weight_f32_kernel(const __grid
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, TU = CF_M / p.G;
   paged_go();
   paged_wait();
-  weight_line<CF_NT, CF_K>(p, before, reinterpret_cast<int*>(sm + P::W_SCAN));
-  weight_units<CF_K>(p, before, [&](const WeightUnit& u) {
+  weight_line<CF_NT, CF_K>(p, before, reinterpret_cast<int2*>(sm + P::W_SCAN), TU);
+  __shared__ int ahead;
+  for (int mine = blockIdx.x;;) {  // (the first unit is the block's own; the queue counts those behind)
+    WeightUnit u;
+    if (!weight_unit<CF_K>(p, before, mine, u)) return;
+    if (tid == 0) ahead = gridDim.x + atomicAdd(p.queue, 1);
     const int from = u.from(0, TU), tiles = u.tiles(TU), a = u.q.len - u.q.n;
-    if (from >= tiles) return true;
     auto fetch = [&](int i) {
       const int rows = min(TU, u.q.n - i * TU) * p.G;
       fetch_queries<D>(p, u.q.first + i * TU, u.h, rows, reinterpret_cast<float*>(sm + P::W_Q + (i & 1) * P::Q_BYTES));
@@ -275,11 +279,12 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_weight_f32_kernel(const __grid
         reinterpret_cast<float*>(sm + P::W_LSE)[(i & 1) * CF_M + tid] =
             tid < rows ? ld_cg(p.lse + ((size_t)u.h * p.n_tokens + u.q.first + i * TU) * p.G + tid) : INFINITY;
     };
-    __syncthreads();  // the last unit's rows and sums are read
     if (tid < CF_K) rows_at[tid] = slot_row(p, u.b, u.h, u.t0 + tid, u.q.len, false);
     __syncthreads();
-    fetch_slots<D>(p.k_pages, rows_at, ks);
-    fetch(from);
+    if (from < tiles) {
+      fetch_slots<D>(p.k_pages, rows_at, ks);
+      fetch(from);
+    }
     float sum[4] = {};
     for (int i = from; i < tiles; ++i) {
       cp_async_wait<0>();
@@ -303,14 +308,15 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_weight_f32_kernel(const __grid
 #pragma unroll
     for (int j = 0; j < 4; ++j) sums[ty * P::LP + tx + 16 * j] = sum[j];
     __syncthreads();
+    mine = ahead;
     if (tid < CF_K && rows_at[tid] >= 0) {
       float x = 0.f;
 #pragma unroll
       for (int i = 0; i < 16; ++i) x += sums[i * P::LP + tid];
       if (x != 0.f) p.weight[((size_t)u.b * p.Hkv + u.h) * p.T_cap + u.t0 + tid] += x;
     }
-    return true;
-  });
+    __syncthreads();  // (`ahead` and the sums are read)
+  }
 }
 
 template <int D>

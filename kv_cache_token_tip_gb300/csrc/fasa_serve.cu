@@ -116,7 +116,7 @@ void chunk_plan(const fasa_paged_dims_t* d, int n_tokens, int sms, int* rows, in
   *parts = (int)std::min<long long>(s.per_sm * std::min(sms, CHUNK_MAX_SMS), units * tiles);
 }
 
-size_t notes_bytes(int parts) { return up((size_t)parts * 2 * sizeof(int4)); }
+size_t notes_bytes(int parts) { return 256 + up((size_t)parts * 2 * sizeof(int4)); }  // and the queue
 size_t records_bytes(int rows, int parts, int D) { return up((size_t)parts * 2 * rows * (D + 2) * 4); }
 
 }  // namespace
@@ -294,7 +294,8 @@ int fasa_paged_chunk_attention(const void* q, int32_t n_tokens, const int32_t* c
   chunk_plan(dims, n_tokens, sms, &p.rows, &p.parts);
   p.sms = sms;
   char* ws = static_cast<char*>(workspace);
-  p.notes = reinterpret_cast<int4*>(ws);
+  p.queue = reinterpret_cast<int*>(ws);
+  p.notes = reinterpret_cast<int4*>(ws + 256);
   ws += notes_bytes(p.parts);
   p.records = reinterpret_cast<float*>(ws);
   p.lse = reinterpret_cast<float*>(ws + records_bytes(p.rows, p.parts, dims->head_dim));

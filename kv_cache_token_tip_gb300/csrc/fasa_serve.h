@@ -63,6 +63,7 @@ struct ChunkParams {
   float scale;     // log2(e) / sqrt(d): logits are kept in powers of two
   float* records;  // [parts][2][rows * (d + 2)]: o [rows][d], m [rows], l [rows]
   int4* notes;     // [parts][2]: whose the records are
+  int* queue;      // the next unit of the weights' pass (the first kernel sets it to 0)
   float* lse;      // [Hkv][n_tokens * G]
   int rows;        // of a record
   int parts;       // most parts of this launch
