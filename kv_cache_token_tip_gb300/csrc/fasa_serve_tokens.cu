@@ -171,8 +171,12 @@ __device__ void write_lens(const AssignParams& p, const AssignShared& sh, const 
 }
 
 // MAP, LENS: what this launch writes.  The lengths may be written where they were read,
-// so that they wait for every block: in a launch of their own, or where one block does
-// all.
+// so that they wait for every block: one, where a thread takes a token at most, a cluster,
+// or a launch of their own behind as many as there is work for.  64, 1024, 4096, 12.8K,
+// 25.6K, 64K and 256K tokens: 3.5, 4.0, 7.3, 12.8, 22.0, 49 and 186 us by one block, 3.9,
+// 4.3, 4.6, 5.1, 6.9, 10.7 and 28 by a cluster of eight, 5.8, 6.3, 6.5, 6.2, 6.3, 7.9 and
+// 8.7 by two launches.
+constexpr int AS_CLUSTER_TOKENS = 16384;
 template <bool MAP, bool LENS>
 __global__ void __launch_bounds__(AS_NT) paged_assign_kernel(const AssignParams p) {
   __shared__ AssignShared sh;
@@ -180,8 +184,11 @@ __global__ void __launch_bounds__(AS_NT) paged_assign_kernel(const AssignParams 
   paged_wait();
   const Assignment a = assignment(p, sh, MAP && blockIdx.x == 0);
   if (MAP) map_tokens(p, sh, a);
-  if (MAP && LENS) __syncthreads();
-  if (LENS) write_lens(p, sh, a);
+  if (MAP && LENS) {
+    if (cluster_size() > 1) cluster_sync();
+    else __syncthreads();
+  }
+  if (LENS && blockIdx.x == 0) write_lens(p, sh, a);
 }
 
 // -------------------------------------------------------------- rope_append
@@ -191,8 +198,11 @@ __global__ void __launch_bounds__(AS_NT) paged_assign_kernel(const AssignParams 
 // either layout, and the same ones in every head: their cosines are worked out once.
 constexpr int RA_NT = 128;
 constexpr int RA_U = 2;  // rows that a lane has on the way
-// From this many tokens a warp takes all rows of one.
-constexpr int RA_MANY = 4096;
+// Warps of a launch for an SM, about: a warp takes as many rows of its token as that leaves
+// it.  40 heads of 128 dims and 8 of values, 32, 512, 2048 and 4096 tokens: 4 rows to a warp
+// 2.1, 4.8, 12.6 and 25.4 us, 8 rows 2.2, 3.7, 8.8 and 17.2, 24 rows 3.7, 5.7, 6.7 and 16.2,
+// all 48 rows 5.7, 6.9, 10.3 and 15.3.
+constexpr int RA_WARPS = 27;
 
 // Element e of a chunk in fp32, and back.
 template <typename T>
@@ -323,7 +333,8 @@ template <typename T, int D>
 cudaError_t launch_rope(const RopeAppendParams& p, bool half, int sms, cudaStream_t s) {
   constexpr int RPW = 32 / (D * (int)sizeof(T) / 32);
   const int rows = (p.q ? p.Hq : 0) + (p.k ? 2 * p.Hkv : 0);
-  const int each = p.n_tokens >= RA_MANY ? rows : RPW * RA_U;
+  const long long steps = ((long long)p.n_tokens * rows / RPW + RA_WARPS * sms - 1) / (RA_WARPS * sms);
+  const int each = (int)(steps * RPW < RPW ? RPW : steps * RPW < rows ? steps * RPW : rows);
   const long long items = (long long)p.n_tokens * ((rows + each - 1) / each), blocks = (items + RA_NT / 32 - 1) / (RA_NT / 32);
   const int grid = (int)(blocks < 16ll * sms ? blocks : 16ll * sms);
   return paged_behind(half ? rope_append_kernel<T, D, true> : rope_append_kernel<T, D, false>, grid, RA_NT, 0, 0, s, p,
@@ -333,7 +344,8 @@ cudaError_t launch_rope(const RopeAppendParams& p, bool half, int sms, cudaStrea
 }  // namespace
 
 cudaError_t launch_paged_assign(const AssignParams& p, int sms, cudaStream_t s) {
-  if (p.max_tokens <= 4 * AS_NT) return paged_behind(paged_assign_kernel<true, true>, 1, AS_NT, 0, 0, s, p);
+  if (p.max_tokens <= AS_NT) return paged_behind(paged_assign_kernel<true, true>, 1, AS_NT, 0, 0, s, p);
+  if (p.max_tokens <= AS_CLUSTER_TOKENS) return paged_behind(paged_assign_kernel<true, true>, 8, AS_NT, 0, 8, s, p);
   const int blocks = (p.max_tokens + AS_NT - 1) / AS_NT;
   const cudaError_t e = paged_behind(paged_assign_kernel<true, false>, blocks < sms ? blocks : sms, AS_NT, 0, 0, s, p);
   return e != cudaSuccess ? e : paged_behind(paged_assign_kernel<false, true>, 1, AS_NT, 0, 0, s, p);
