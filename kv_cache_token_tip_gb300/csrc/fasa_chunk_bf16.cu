@@ -113,6 +113,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
   tm_after_sync();
   const int parts = line.parts(p.parts), c = blockIdx.x;
   const Patience patience{misc + 1, p.status, p.wait_ns};
+  int copies = 0, q_copies = 0;  // that the copying warp has issued
   if (tid == 0) note_none(p, c);
   if (tid == 0 && c == 0) *p.queue = 0;
   if (c < parts) {
@@ -373,7 +374,8 @@ __global__ void __launch_bounds__(CB_NT, 1)
       const int none = (int)((long long)p.n_pages * p.Hkv << p.log2_page);  // a row behind the pool: zeros
       const int mine = lane / P::HALVES, half = lane % P::HALVES;
       uint32_t q_phase = 1;
-      int k = 0, n_tile = 0, n_unit = 0;
+      int& k = copies;
+      int n_tile = 0;
       fence_proxy_async_global();  // (a kernel before this one may have stored what is copied)
       segments(line, y0, y1, [&](const ChunkUnit& u, int f0, int f1, bool) {
         const ChunkSeq& q = u.q;
@@ -382,7 +384,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
         const int first = q.first + u.i * TU;
         if (!patience.wait(q_empty, q_phase)) return false;
         q_phase ^= 1;
-        ++n_unit;
+        ++q_copies;
         if (lane == 0) mbar_arrive_expect_tx(q_full, 2 * P::HALVES * TQ * p.G * 128);
         __syncwarp();
         if (lane < 2 * P::HALVES) {
@@ -423,18 +425,19 @@ __global__ void __launch_bounds__(CB_NT, 1)
         }
         return true;
       });
-      // After a wait that ran out no copy may land in memory of a block that is gone.
-      if (misc[1]) {
-        bool all = n_unit == 0 || mbar_wait_bounded(q_full, (n_unit - 1) & 1, 8 * p.wait_ns);
-        for (int i = max(0, k - S); i < k; ++i)
-          all = mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, 8 * p.wait_ns) && all;
-        if (!all && lane == 0) atomicOr(p.status, 4);
-      }
     }
-    if (warp == CB_ROWS && misc[1]) {  // nor may matrix instructions be under way when tensor memory goes back
-      if (elected()) mma_commit(drain);
-      if (!mbar_wait_bounded(drain, 0, 8 * p.wait_ns) && lane == 0) atomicOr(p.status, 4);
-    }
+  }
+  // After a wait that ran out, no copy may land in memory of a block that is gone, nor may
+  // matrix instructions be under way when tensor memory goes back.
+  __syncthreads();
+  if (misc[1] && warp == CB_ROWS) {
+    if (elected()) mma_commit(drain);
+    if (!mbar_wait_bounded(drain, 0, 8 * p.wait_ns) && lane == 0) atomicOr(p.status, 4);
+  } else if (misc[1] && warp == CB_ROWS + 1) {
+    bool all = q_copies == 0 || mbar_wait_bounded(q_full, (q_copies - 1) & 1, 8 * p.wait_ns);
+    for (int i = max(0, copies - S); i < copies; ++i)
+      all = mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, 8 * p.wait_ns) && all;
+    if (!all && lane == 0) atomicOr(p.status, 4);
   }
   __syncthreads();
   if (warp == 0) tm_free(TM, 512);
@@ -545,6 +548,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
   weight_line<CW_NT, 256>(p, before, reinterpret_cast<int2*>(sm + P::OFF_PAIR), TQ);
   tm_after_sync();
   const Patience patience{misc + 1, p.status, p.wait_ns};
+  int issued = 0;  // copies
   // f(unit) for each unit of this block, in order, as the copying warp takes them
   auto units = [&](auto&& f) {
     for (int i = 0;; ++i) {
@@ -713,7 +717,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
     const int none = (int)((long long)p.n_pages * p.Hkv << p.log2_page);
     const int half = lane % A::HALVES, mine = lane / A::HALVES;
     RingAt<S> at;
-    int k = 0, issued = 0;
+    int k = 0;
     fence_proxy_async_global();
     auto copy = [&](const WeightUnit& u) {
       const int from = u.from(0, TQ), tiles = u.tiles(TQ);
@@ -774,16 +778,16 @@ __global__ void __launch_bounds__(CW_NT, 1)
       if (!copy(u)) break;
       x = __shfl_sync(0xffffffffu, next, 0);
     }
-    if (misc[1]) {  // (as above)
-      bool all = true;
-      for (int i = max(0, issued - S); i < issued; ++i)
-        all = mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, 8 * p.wait_ns) && all;
-      if (!all && lane == 0) atomicOr(p.status, 4);
-    }
   }
-  if (warp == CW_ROWS && misc[1]) {
+  __syncthreads();  // (and then as above)
+  if (misc[1] && warp == CW_ROWS) {
     if (elected()) mma_commit(drain);
     if (!mbar_wait_bounded(drain, 0, 8 * p.wait_ns) && lane == 0) atomicOr(p.status, 4);
+  } else if (misc[1] && warp == CW_ROWS + 1) {
+    bool all = true;
+    for (int i = max(0, issued - S); i < issued; ++i)
+      all = mbar_wait_bounded(full + 8 * (i % S), (i / S) & 1, 8 * p.wait_ns) && all;
+    if (!all && lane == 0) atomicOr(p.status, 4);
   }
   __syncthreads();
   if (warp == 0) tm_free(TM, 512);

@@ -592,3 +592,342 @@ def test_a_server_s_steps(dtype, d, page, G):
     rest = free[:count.item()].tolist()
     assert sorted(used + rest) == list(range(n_pages))  # every page is somewhere, once
     assert status() == 0
+
+
+# ------------------------------------------------------------- hard conditions
+def reference(k, sequences=None):
+    """out [n, Hq, d] of a Chunk in 64 bits by torch on the GPU (long caches), and sum p |V| beside it."""
+    import torch
+    out = torch.zeros(k.q.shape, dtype=torch.float64, device="cuda")
+    pv = torch.zeros_like(out)
+    for b in range(k.B) if sequences is None else sequences:
+        x0, x1, n = k.cu_host[b], k.cu_host[b + 1], int(k.lens[b])
+        t = torch.arange(n, device="cuda")
+        pg, at = k.table[b, t // k.page].long(), t % k.page
+        for h in range(k.Hkv):
+            K, V = k.kp[pg, h, at].double(), k.vp[pg, h, at].double()
+            q = k.q[x0:x1, h * k.G:(h + 1) * k.G].double()
+            z = torch.einsum("jgd,td->jgt", q, K) / k.d ** 0.5
+            z.masked_fill_((t.view(1, 1, -1) > (n - (x1 - x0) + torch.arange(x1 - x0, device="cuda")).view(-1, 1, 1)), -float("inf"))
+            p = torch.softmax(z, dim=-1)
+            out[x0:x1, h * k.G:(h + 1) * k.G] = torch.einsum("jgt,td->jgd", p, V)
+            pv[x0:x1, h * k.G:(h + 1) * k.G] = torch.einsum("jgt,td->jgd", p, V.abs())
+    return out, pv
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G", [1, 3, 4, 7])
+def test_chunk_queries_of_others_may_hold_anything(dtype, G):
+    """NaN and infinities in padding and in one sequence's queries stay in that sequence's rows and weights."""
+    import torch
+    k = Chunk(dtype, 3, 2, G, 128, 16, [40, 3, 100], [30, 45, 37], seed=8, pad=40)
+    start = k.weight.clone()
+    clean, first = k.run().clone(), k.weight.clone()
+    for bad in (float("nan"), float("inf")):
+        k.weight.copy_(start)
+        k.q[30:75] = bad
+        k.q[112:] = bad
+        k.run()
+        assert torch.equal(k.out[:30], clean[:30]) and torch.equal(k.out[75:112], clean[75:112])
+        assert torch.equal(k.weight[0], first[0]) and torch.equal(k.weight[2], first[2])
+    assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_chunk_no_tokens_at_all(dtype):
+    import torch
+    k = Chunk(dtype, 3, 2, 2, 64, 16, [40, 0, 20], [0, 0, 0], seed=8, pad=9)
+    w = k.weight.clone()
+    k.run()
+    assert torch.isnan(k.out).all() and torch.equal(k.weight, w)
+    k = Chunk(dtype, 3, 2, 2, 64, 16, [40, 0, 20], [0, 0, 0], seed=8)
+    k.run()   # a call without rows
+    assert status() == 0
+
+
+@pytest.mark.parametrize("dtype,B,Hkv,G,d", [("bf16", 2048, 4, 8, 64), ("f32", 2048, 2, 1, 64), ("bf16", 300, 16, 1, 128),
+                                             ("bf16", 1, 64, 1, 64)])
+def test_chunk_many_sequences_and_heads(dtype, B, Hkv, G, d):
+    import torch
+    rng = np.random.default_rng(B)
+    k = Chunk(dtype, B, Hkv, G, d, 16, [int(x) for x in rng.integers(0, 60, B)], [int(x) for x in rng.integers(0, 4, B)],
+              seed=9, pad=1)
+    w0 = k.weight.clone()
+    k.run()
+    ref, pv = reference(k)
+    live = slice(0, k.cu_host[-1])
+    err = (k.out.double() - ref).abs()[live]
+    # (the logits' rounding: 2 (2 d + 16) u A, A below 4 d^0.5 here)
+    e = E[dtype]
+    assert (err <= (2 * e + 8 * d ** 0.5 * (2 * d + 16) * U + 400 * U) * pv[live] + 1e-30).all()
+    # every row's weights sum to 1
+    for b in range(0, B, 97):
+        m = k.cu_host[b + 1] - k.cu_host[b]
+        got = (k.weight[b].double() - w0[b].double()).sum(dim=1)
+        assert ((got - m * G).abs() <= 1e-5 * (m * G + w0[b].double().sum(dim=1))).all()
+    assert status() == 0
+
+
+@pytest.mark.parametrize("dtype,d,G,page", [("bf16", 64, 4, 256), ("bf16", 128, 8, 16), ("f32", 64, 2, 128)])
+def test_chunk_long_cache(dtype, d, G, page):
+    """One sequence over the whole range of slots, and a short one beside it."""
+    k = Chunk(dtype, 2, 1, G, d, page, [262144 - 5, 7], [5, 30], seed=10, max_pages=262144 // page)
+    before = k.weight.clone()
+    k.run()
+    ref, pv = reference(k)
+    err = (k.out.double() - ref).abs()
+    # sums of 262144 terms in parts: of tiles, and over a part's 1725 tiles or fewer
+    rel = 8 * d ** 0.5 * (2 * d + 16) * U + (2 * 2 ** 12 + 400) * U + (2.0 ** -8 if dtype == "bf16" else 0)
+    assert (err <= rel * pv + E[dtype] * ref.abs() + 1e-30).all()
+    got = (k.weight.double() - before.double()).clamp(min=0)
+    assert abs(float(got[0].sum()) - 5 * G) <= 1e-3 * 5 * G + float(before[0].double().sum()) * U
+    assert status() == 0
+
+
+def test_offsets_past_32_bits():
+    """Pools of more than 2^32 elements, used at their far end by all the calls."""
+    import torch
+    from kv_cache_token_tip_gb300 import FasaRope, fasa_paged_assign, fasa_paged_chunk_attention, fasa_paged_rope_append
+    B, Hkv, G, d, page, mp, n_tok = 2, 8, 4, 128, 16, 14, 90
+    dt, rope = torch.bfloat16, FasaRope(1, 128, 1, 5e5, factor=2.0)
+    got = []
+    for n_pages in (40, 270_000):
+        g = torch.Generator(device="cuda")
+        g.manual_seed(1)
+        kp, vp = (torch.zeros((n_pages, Hkv, page, d), dtype=dt, device="cuda") for _ in range(2))
+        dims = paged_dims("bf16", B, Hkv, G, d, page, n_pages, mp)
+        free = torch.arange(n_pages, dtype=torch.int32, device="cuda")   # (the last pages are taken first)
+        count, table, lens = ints([n_pages]), ints([[-1] * mp] * B), ints([0, 0])
+        cu, m = ints([0] * 3), torch.zeros((n_tok, 4), dtype=torch.int32, device="cuda")
+        w, tp = torch.zeros((B, Hkv, mp * page), device="cuda"), torch.zeros((B, Hkv, mp * page), dtype=torch.int32, device="cuda")
+        outs = []
+        for want in ([60, 30], [61, 100], [140, 101]):
+            fasa_paged_assign(lens, ints(want), table, free, count, lens, cu, m, dims=dims)
+            qkv = torch.randn((n_tok, Hkv * (G + 2), d), generator=g, device="cuda").to(dt)
+            q, o = torch.zeros((n_tok, Hkv * G, d), dtype=dt, device="cuda"), torch.zeros((n_tok, Hkv * G, d), dtype=dt, device="cuda")
+            fasa_paged_rope_append(qkv[:, :Hkv * G], qkv[:, Hkv * G:-Hkv], qkv[:, -Hkv:], m, q, kp, vp, weight=w,
+                                   token_pos=tp, rope=rope, dims=dims)
+            fasa_paged_chunk_attention(q, kp, vp, table, lens, o, cu_new=cu, weight=w, dims=dims)
+            outs += [q, o]
+        got.append(outs + [w, tp, kp[-30:].clone(), vp[-30:].clone()])
+        del kp, vp
+    assert all(torch.equal(a, b) for a, b in zip(*got)) and got[0][1].abs().sum() > 0
+    assert status() == 0
+
+
+def test_chunk_shared_pages():
+    """Two sequences with the same prompt's pages: as with pages of their own."""
+    import torch
+    k = Chunk("bf16", 2, 2, 4, 128, 32, [256, 256], [9, 40], seed=11)
+    shared = k.table.clone()
+    shared[1, :8] = shared[0, :8]
+    own = k.table
+    k.kp[own[1, :8].long()], k.vp[own[1, :8].long()] = k.kp[own[0, :8].long()], k.vp[own[0, :8].long()]
+    w = k.weight.clone()
+    a, wa = k.run().clone(), k.weight.clone()
+    k.weight.copy_(w)
+    k.table = shared
+    assert torch.equal(k.run(), a) and torch.equal(k.weight, wa) and status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_chunk_graphs_that_share_a_workspace(dtype):
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_chunk_workspace_size
+    ks = [Chunk(dtype, 3, 2, 4, 128, 32, [700, 20, 0], [90, 30, 2], seed=12), Chunk(dtype, 1, 4, 2, 64, 16, [5], [300], seed=13)]
+    ref = []
+    for k in ks:
+        k.start = k.weight.clone()
+        ref.append((k.run().clone(), k.weight.clone()))
+    ws = torch.empty(max(fasa_paged_chunk_workspace_size(k.dims, k.n, True) for k in ks), dtype=torch.uint8, device="cuda")
+    graphs = []
+    torch.cuda.synchronize()
+    for k in ks:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            k.run(workspace=ws)
+    for _ in range(4):
+        for k in ks:
+            k.weight.copy_(k.start)
+        for g in graphs + graphs[::-1]:
+            g.replay()
+        for k, (out, w) in zip(ks, ref):
+            assert torch.equal(k.out, out)
+            assert (k.weight - k.start - 2 * (w - k.start)).abs().max() <= 1e-4 * float(k.weight.max())
+    assert status() == 0
+
+
+def test_chunks_of_two_streams_at_once():
+    """Two calls with their own workspaces, on two streams: blocks of both wait for an SM, and no result changes."""
+    import torch
+    ks = [Chunk("bf16", 4, 4, 4, 128, 16, [900, 30, 5, 0], [200, 300, 1, 77], seed=14 + i) for i in range(2)]
+    ref = []
+    for k in ks:
+        k.start = k.weight.clone()
+        ref.append((k.run().clone(), k.weight.clone()))
+    streams = [torch.cuda.Stream() for _ in ks]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k, s in zip(ks, streams):
+            with torch.cuda.stream(s):
+                k.weight.copy_(k.start)
+                k.out.fill_(float("nan"))
+                k.run()
+    torch.cuda.synchronize()
+    for k, (out, w) in zip(ks, ref):
+        assert torch.equal(k.out, out) and torch.equal(k.weight, w)
+    assert status() == 0
+
+
+def test_calls_of_two_threads():
+    """Other types, rotations and shapes in two threads: what the library keeps between calls is not mixed up."""
+    import threading
+    import torch
+    from kv_cache_token_tip_gb300 import FasaRope, fasa_paged_rope_append
+
+    def steps(i):
+        k = Chunk(*(("bf16", 2, 2, 4, 128, 16, [100, 40], [60, 7]), ("f32", 3, 1, 2, 64, 32, [10, 0, 70], [5, 50, 1]))[i], seed=20 + i)
+        m = [(b, int(k.lens[b]) - (k.cu_host[b + 1] - k.cu_host[b]) + j) for b in range(k.B) for j in range(k.cu_host[b + 1] - k.cu_host[b])]
+        m = ints([(b, t, int(k.table[b, t // k.page]), 31 * t) for b, t in m])
+        outs = []
+        for r in range(20):
+            rope = FasaRope(i, 64, r % 4, 1e4 * (1 + i), factor=2.0 + r, low=1.0, high=8.0, original=512.0)
+            q = torch.zeros_like(k.q)
+            fasa_paged_rope_append(k.q, k.q[:, :k.Hkv], k.q[:, -k.Hkv:], m, q, k.kp, k.vp, rope=rope, dims=k.dims)
+            outs += [q, k.run().clone()]
+        return torch.stack(outs), k.weight
+
+    alone = [steps(i) for i in range(2)]
+    got = [None, None]
+    torch.cuda.synchronize()
+
+    def run(i):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            got[i] = steps(i)
+        s.synchronize()
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert all(torch.equal(x, y) for g, a in zip(got, alone) for x, y in zip(g, a)) and status() == 0
+
+
+def test_chunk_bounded_waits():
+    """A copy that is never issued: the waits on it run out within the bound, the call says so, drains what it has
+    under way and gives tensor memory back, and the next call gives the bits of the first.  (The wait is on a barrier
+    in shared memory that no copy targets.)"""
+    import torch
+    from kv_cache_token_tip_gb300 import FASA_DEV_TIMEOUT, FASA_DEV_UNDRAINED, fasa_test_fault_injection
+    k = Chunk("bf16", 2, 4, 4, 128, 32, [3000, 50], [200, 10], seed=15)
+    ref = k.run(False).clone()
+    assert status() == 0
+    try:
+        fasa_test_fault_injection(wait_limit_ns=2_000_000)
+        assert torch.equal(k.run(False), ref) and status() == 0   # a short bound alone changes nothing
+        fasa_test_fault_injection(wait_limit_ns=2_000_000, drop_tip_tile=1)
+        k.run(False)
+        assert status() == FASA_DEV_TIMEOUT | FASA_DEV_UNDRAINED
+    finally:
+        fasa_test_fault_injection()
+    assert torch.equal(k.run(False), ref) and status() == 0
+
+
+def test_binding_refuses_what_does_not_fit():
+    import torch
+    from kv_cache_token_tip_gb300 import (FasaError, FasaRope, fasa_paged_assign, fasa_paged_chunk_attention,
+                                          fasa_paged_rope_append)
+    k = Chunk("bf16", 2, 2, 2, 64, 16, [20, 30], [4, 5], seed=16)
+    m, rope = torch.zeros((9, 4), dtype=torch.int32, device="cuda"), FasaRope(1, 64)
+
+    def chunk(**kw):
+        t = dict(q=k.q, kp=k.kp, vp=k.vp, table=k.table, lens=k.lens, out=k.out, cu=k.cu, weight=k.weight, ws=None)
+        t.update(kw)
+        fasa_paged_chunk_attention(t["q"], t["kp"], t["vp"], t["table"], t["lens"], t["out"], cu_new=t["cu"],
+                                   weight=t["weight"], workspace=t["ws"], dims=k.dims)
+
+    for bad in (dict(q=k.q.float()), dict(q=k.q.cpu()), dict(q=k.q[:, 1:]), dict(q=k.q.transpose(0, 1)), dict(kp=k.kp[:-1]),
+                dict(vp=k.vp.float()), dict(table=k.table[:, :-1]), dict(lens=k.lens[:1]), dict(lens=k.lens.long()),
+                dict(out=k.out.float()), dict(out=k.out[1:]), dict(cu=k.cu[1:]), dict(weight=k.weight[:1]),
+                dict(weight=k.weight.double()), dict(ws=torch.empty(9))):
+        with pytest.raises(ValueError):
+            chunk(**bad)
+    for bad in (dict(ws=torch.empty(16, dtype=torch.uint8, device="cuda")), dict(out=k.q), dict(cu=None)):
+        with pytest.raises(FasaError):
+            chunk(**bad)
+
+    def append(q=k.q, kk=k.q[:, :2], v=k.q[:, 2:], m=m, qo=k.out, kp=k.kp, vp=k.vp, rope=rope, **kw):
+        fasa_paged_rope_append(q, kk, v, m, qo, kp, vp, rope=rope, dims=k.dims, **kw)
+
+    for bad in (dict(q=k.q.float()), dict(q=k.q[:, :, ::2]), dict(q=k.q.transpose(1, 2)), dict(q=k.q[0]), dict(kk=k.q),
+                dict(kk=k.q[:8, :2]), dict(v=None), dict(m=m[1:]), dict(m=m.long()), dict(qo=k.out[1:]), dict(qo=None),
+                dict(kp=None), dict(vp=k.vp[1:]), dict(weight=k.weight[:, :1]), dict(token_pos=k.weight)):
+        with pytest.raises(ValueError):
+            append(**bad)
+    odd = torch.empty(9 * 4 * 64 + 4, dtype=torch.bfloat16, device="cuda")[4:].view(9, 4, 64)
+    for bad in (dict(q=odd), dict(qo=odd), dict(qo=k.q[:9], q=k.q, kk=k.q[:, :2]), dict(rope=FasaRope(1, 72)),
+                dict(rope=FasaRope(5, 64)), dict(kk=None, v=None, kp=None, vp=None, weight=k.weight)):
+        with pytest.raises(FasaError):
+            append(**bad)
+    n = k.kp.shape[0]
+    free, one, cu = torch.zeros(n, dtype=torch.int32, device="cuda"), ints([0]), ints([0, 0, 0])
+    lens = k.lens.clone()
+
+    def assign(have=k.lens, want=k.lens, table=k.table, free=free, count=one, out=lens, cu=cu, m=m, **kw):
+        fasa_paged_assign(have, want, table, free, count, out, cu, m, dims=k.dims, **kw)
+
+    for bad in (dict(have=k.lens[:1]), dict(want=k.lens.long()), dict(table=k.table.t()), dict(free=free[1:]),
+                dict(count=ints([0, 0])), dict(out=lens.cpu()), dict(cu=cu[1:]), dict(m=m.view(-1)[:-1]), dict(pos=one)):
+        with pytest.raises(ValueError):
+            assign(**bad)
+    for bad in (dict(pos=lens), dict(out=cu[1:]), dict(free_count_out=lens[:1])):
+        with pytest.raises(FasaError):
+            assign(**bad)
+    assert status() == 0
+
+
+FIRST_CALLS = """
+import torch
+from kv_cache_token_tip_gb300 import (FasaPagedDims, FasaRope, fasa_device_status, fasa_paged_assign,
+                                      fasa_paged_chunk_attention, fasa_paged_rope_append)
+for dtype, code, d in ((torch.bfloat16, 1, 128), (torch.float32, 0, 64)):
+    B, H, G, page, n, T = 2, 2, 4, 16, 6, 40
+    dims, rope = FasaPagedDims(B, H * G, H, d, page, B * n, n, code, 1e4), FasaRope(1, d)
+    z = lambda *s, t=torch.float32: torch.zeros(*s, dtype=t, device="cuda")
+    i = lambda *s: z(*s, t=torch.int32)
+    kp, vp, w, tp = z(B * n, H, page, d, t=dtype), z(B * n, H, page, d, t=dtype), z(B, H, n * page), i(B, H, n * page)
+    table, free, count = i(B, n), torch.arange(B * n, dtype=torch.int32, device="cuda"), i(1) + B * n
+    lens, want, cu, m = i(B), i(B), i(B + 1), i(T, 4)
+    qkv = torch.ones(T, H * (G + 2), d, device="cuda").to(dtype)
+    q, out = z(T, H * G, d, t=dtype), z(T, H * G, d, t=dtype)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        want.copy_(lens)
+        want.add_(7)
+        fasa_paged_assign(lens, want, table, free, count, lens, cu, m, dims=dims)
+        fasa_paged_rope_append(qkv[:, :H * G], qkv[:, H * G:-H], qkv[:, -H:], m, q, kp, vp, weight=w, token_pos=tp,
+                               rope=rope, dims=dims)
+        fasa_paged_chunk_attention(q, kp, vp, table, lens, out, cu_new=cu, weight=w, dims=dims)
+    for _ in range(9):
+        g.replay()
+    torch.cuda.synchronize()
+    assert lens.tolist() == [63, 63] and count.item() == B * n - 8 and cu.tolist() == [0, 7, 14]
+    # out = o / l with V being 1: at most 2^-8 of the weights' rounding to bf16, and sums of 63 terms
+    assert (out[:14].float() - 1).abs().max() <= (2.0 ** -7 if code else 200 * 2.0 ** -24), out
+    assert (w[:, :, :63].sum(-1) - 9 * 7 * G).abs().max() <= 1e-3 and fasa_device_status() == 0
+print("fine")
+"""
+
+
+def test_first_calls_of_a_process_in_a_capture():
+    """Nothing of the library has run before: what it sets up on first use does
+    not end the capture, and the graph's steps go on from replay to replay."""
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "fine", r.stderr[-2000:]
