@@ -118,9 +118,9 @@ __global__ void __launch_bounds__(CB_NT, 1)
   if (tid == 0 && c == 0) *p.queue = 0;
   if (c < parts) {
     const long long y0 = line.part_begin(parts, c), y1 = line.part_begin(parts, c + 1);
-    // (384 threads of 168 registers: 256 of 232 and 128 of 40)
-    if (warp < CB_ROWS) more_registers<232>();
-    else fewer_registers<40>();
+    // (384 threads of 168 registers: 256 of 224 and 128 of 56)
+    if (warp < CB_ROWS) more_registers<224>();
+    else fewer_registers<56>();
     if (warp < CB_ROWS) {
       // ------------------------------------------------ softmax: rows of tile w
       const int w = warp >> 2, row = tid & 127;
@@ -256,28 +256,30 @@ __global__ void __launch_bounds__(CB_NT, 1)
           __syncwarp();
         };
         const float inv = l > 0.f ? 1.f / l : 0.f;
+        uint32_t o[D];
+        if (f0 < e) {
+#pragma unroll
+          for (int k = 0; k < D; k += 32) tm_ld32(ot + k, o + k);
+          tm_wait_ld();
+          tm_settle(o);
+        } else {
+#pragma unroll
+          for (int i = 0; i < D; ++i) o[i] = 0u;
+        }
 #pragma unroll
         for (int k = 0; k < D; k += 32) {
-          uint32_t o[32];
-          if (f0 < e) {
-            tm_ld32(ot + k, o);
-            tm_wait_ld();
-            tm_settle(o);
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) o[i] = 0u;
-          }
           uint32_t x[16];
           if (whole) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = pack_bf16(__uint_as_float(o[2 * i]) * inv, __uint_as_float(o[2 * i + 1]) * inv);
+            for (int i = 0; i < 16; ++i)
+              x[i] = pack_bf16(__uint_as_float(o[k + 2 * i]) * inv, __uint_as_float(o[k + 2 * i + 1]) * inv);
             send(x, 2 * k);
           } else {
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = o[i];
+            for (int i = 0; i < 16; ++i) x[i] = o[k + i];
             send(x, 4 * k);
 #pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = o[16 + i];
+            for (int i = 0; i < 16; ++i) x[i] = o[k + 16 + i];
             send(x, 4 * k + 64);
           }
         }
