@@ -7,8 +7,11 @@
 // l 2^(m - M) + l' 2^(m' - M), and o alike.
 #pragma once
 
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
+
+#include <mutex>
 
 #include "fasa_ptx.cuh"
 #include "fasa_serve.h"
@@ -67,6 +70,22 @@ __device__ __forceinline__ void store4(T* to, float a, float b, float c, float d
     *reinterpret_cast<uint2*>(to) = make_uint2(pack_bf16(a, b), pack_bf16(c, d));
   else
     *reinterpret_cast<float4*>(to) = make_float4(a, b, c, d);
+}
+
+// Walks the segments of the part [y0, y1): f(unit, f0, f1, whole) for its tiles of slots
+// f0 .. f1 - 1, until it says false.  The same for every role.
+template <class F>
+__device__ __forceinline__ void segments(const ChunkLine& line, long long y0, long long y1, F&& f) {
+  ChunkUnit u;
+  u.find(line, y0);
+  while (true) {
+    const int f0 = u.before(line, y0), f1 = u.before(line, y1);
+    const bool whole = f0 == 0 && f1 == u.tiles && u.begin >= y0;
+    if (f0 < f1 || whole)
+      if (!f(u, f0, f1, whole)) return;
+    if (u.begin + u.cost >= y1) return;
+    u.next(line);
+  }
 }
 
 // Record of part c: slot 0 of a unit that began before it, slot 1 of one that goes on.
@@ -175,6 +194,33 @@ cudaError_t launch_chunk_join(const ChunkParams& p, cudaStream_t s) {
   cfg.attrs = &attr;
   cfg.numAttrs = 1;
   return cudaLaunchKernelEx(&cfg, chunk_join_kernel<T, D>, p);
+}
+
+// A tensor of `n` dimensions (sizes and boxes from the innermost on) in the 128-byte swizzle.
+inline cudaError_t tensor_map(CUtensorMap* map, const void* at, CUtensorMapDataType type, int n, const cuuint64_t* dims, const cuuint64_t* strides,
+                       const cuuint32_t* box) {
+  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+  static std::mutex mu;
+  static Encode encode = nullptr;
+  {
+    std::lock_guard<std::mutex> lk(mu);
+    if (!encode) {
+      void* f = nullptr;
+      cudaDriverEntryPointQueryResult found;
+      const cudaError_t e =
+          cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
+      if (e != cudaSuccess) return e;
+      if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorSymbolNotFound;
+      encode = reinterpret_cast<Encode>(f);
+    }
+  }
+  const cuuint32_t one[3] = {1, 1, 1};
+  const CUresult r = encode(map, type, n, const_cast<void*>(at), dims, strides, box, one,
+                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 // ------------------------------------------------------------------ weights

@@ -14,7 +14,6 @@
 
 #include <algorithm>
 #include <atomic>
-#include <mutex>
 
 #include "fasa_chunk.cuh"
 #include "fasa_tcgen05.cuh"
@@ -52,21 +51,6 @@ __device__ __forceinline__ int row_tile_end(const ChunkParams& p, const ChunkUni
   if (j0 >= u.q.n) return f0;
   const int see = u.q.len - u.q.n + min(j0 + TQ, u.q.n);
   return max(f0, min(f1, see > 0 ? (see + CB_K - 1) / CB_K : 0));
-}
-
-// Walks this part's segments; f(unit, f0, f1, whole).  The same for every role.
-template <class F>
-__device__ __forceinline__ void segments(const ChunkLine& line, long long y0, long long y1, F&& f) {
-  ChunkUnit u;
-  u.find(line, y0);
-  while (true) {
-    const int f0 = u.before(line, y0), f1 = u.before(line, y1);
-    const bool whole = f0 == 0 && f1 == u.tiles && u.begin >= y0;
-    if (f0 < f1 || whole)
-      if (!f(u, f0, f1, whole)) return;
-    if (u.begin + u.cost >= y1) return;
-    u.next(line);
-  }
 }
 
 template <int D>
@@ -795,34 +779,6 @@ __global__ void __launch_bounds__(CW_NT, 1)
   if (warp == 0) tm_free(TM, 512);
 }
 
-// A tensor of `n` dimensions (sizes and boxes from the innermost on), bf16 in the
-// 128-byte swizzle.
-cudaError_t tensor_map(CUtensorMap* map, const void* at, int n, const cuuint64_t* dims, const cuuint64_t* strides,
-                       const cuuint32_t* box) {
-  using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-  static std::mutex mu;
-  static Encode encode = nullptr;
-  {
-    std::lock_guard<std::mutex> lk(mu);
-    if (!encode) {
-      void* f = nullptr;
-      cudaDriverEntryPointQueryResult found;
-      const cudaError_t e =
-          cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found);
-      if (e != cudaSuccess) return e;
-      if (found != cudaDriverEntryPointSuccess || !f) return cudaErrorSymbolNotFound;
-      encode = reinterpret_cast<Encode>(f);
-    }
-  }
-  const cuuint32_t one[3] = {1, 1, 1};
-  const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, n, const_cast<void*>(at), dims, strides, box, one,
-                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int D>
 cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   using P = CbPlan<D>;
@@ -843,11 +799,11 @@ cudaError_t launch(const ChunkParams& p, cudaStream_t s) {
   CUtensorMap qm, km, vm;
   const cuuint64_t qd[3] = {D, (cuuint64_t)p.Hq, (cuuint64_t)p.n_tokens}, qs[2] = {D * 2, (cuuint64_t)p.Hq * D * 2};
   const cuuint32_t qb[3] = {64, (cuuint32_t)p.G, (cuuint32_t)TQ};
-  e = tensor_map(&qm, p.q, 3, qd, qs, qb);
+  e = tensor_map(&qm, p.q, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, qd, qs, qb);
   const cuuint64_t kd[2] = {D, ((cuuint64_t)p.n_pages * p.Hkv) << p.log2_page}, ks[1] = {D * 2};
   const cuuint32_t kb[2] = {64, (cuuint32_t)std::min(1 << p.log2_page, 128)};
-  if (e == cudaSuccess) e = tensor_map(&km, p.k_pages, 2, kd, ks, kb);
-  if (e == cudaSuccess) e = tensor_map(&vm, p.v_pages, 2, kd, ks, kb);
+  if (e == cudaSuccess) e = tensor_map(&km, p.k_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kd, ks, kb);
+  if (e == cudaSuccess) e = tensor_map(&vm, p.v_pages, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, kd, ks, kb);
   if (e == cudaSuccess) e = paged_behind(chunk_bf16_kernel<D>, p.parts, CB_NT, P::bytes(p.B), 0, s, p, qm, km, vm);
   if (e == cudaSuccess) e = launch_chunk_join<__nv_bfloat16, D>(p, s);
   if (e == cudaSuccess && p.weight)

@@ -815,13 +815,14 @@ def test_calls_of_two_threads():
     assert all(torch.equal(x, y) for g, a in zip(got, alone) for x, y in zip(g, a)) and status() == 0
 
 
-def test_chunk_bounded_waits():
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_chunk_bounded_waits(dtype):
     """A copy that is never issued: the waits on it run out within the bound, the call says so, drains what it has
     under way and gives tensor memory back, and the next call gives the bits of the first.  (The wait is on a barrier
     in shared memory that no copy targets.)"""
     import torch
     from kv_cache_token_tip_gb300 import FASA_DEV_TIMEOUT, FASA_DEV_UNDRAINED, fasa_test_fault_injection
-    k = Chunk("bf16", 2, 4, 4, 128, 32, [3000, 50], [200, 10], seed=15)
+    k = Chunk(dtype, 2, 4, 4, 128, 32, [3000, 50], [200, 10], seed=15)
     ref = k.run(False).clone()
     assert status() == 0
     try:
