@@ -62,6 +62,14 @@ struct ChunkRow {
   }
 };
 
+// Whether a sequence's logits are kept (those of its head h at chunk_logits).
+__device__ __forceinline__ bool chunk_light(const ChunkParams& p, const ChunkSeq& q) {
+  return p.logits && q.n * p.G <= CHUNK_LIGHT;
+}
+__device__ __forceinline__ float* chunk_logits(const ChunkParams& p, int b, int h) {
+  return p.logits + ((size_t)b * p.Hkv + h) * CHUNK_LIGHT * p.T_pad;
+}
+
 __device__ __forceinline__ float chunk_lse(float m, float l) { return l > 0.f ? m + log2f(l) : INFINITY; }
 
 template <typename T>
@@ -236,50 +244,71 @@ struct WeightUnit {
   }
 };
 
-// Units of one head before each sequence, in shared memory (2 B + 2 words): first of those
-// with more tokens than a tile of rows holds, then of the others.  Every thread of the block
-// calls it; ends with a barrier.  scan: NT / 32 pairs of words.
+// Units of one head before each sequence, in shared memory (3 (B + 1) words): of those with more
+// tokens than a tile of rows holds, of the others, and of the light ones, in pieces of
+// WEIGHT_PIECE slots.  Every thread of the block calls it; ends with a barrier.  scan: NT / 32
+// triples of words.
+constexpr int WEIGHT_PIECE = 128;
 template <int NT, int SLOTS>
-__device__ void weight_line(const ChunkParams& p, int* before, int2* scan, int TQ) {
+__device__ void weight_line(const ChunkParams& p, int* before, int3* scan, int TQ) {
   const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0, 0};
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int run = (p.B + NT - 1) / NT, b0 = min(p.B, tid * run), b1 = min(p.B, b0 + run);
-  int2 sum = make_int2(0, 0);
+  int* few = before + p.B + 1;
+  int* light = few + p.B + 1;
+  int3 sum = make_int3(0, 0, 0);
   bool bad = false;
   for (int b = b0; b < b1; ++b) {
     before[b] = sum.x;
-    before[p.B + 1 + b] = sum.y;
+    few[b] = sum.y;
+    light[b] = sum.z;
     const ChunkSeq q = line.sequence(b, &bad);
-    const int n = (q.len + SLOTS - 1) / SLOTS;
-    if (q.n > TQ) sum.x += n;
-    else if (q.n > 0) sum.y += n;
+    if (q.n > 0 && chunk_light(p, q)) sum.z += (q.len + WEIGHT_PIECE - 1) / WEIGHT_PIECE;
+    else if (q.n > TQ) sum.x += (q.len + SLOTS - 1) / SLOTS;
+    else if (q.n > 0) sum.y += (q.len + SLOTS - 1) / SLOTS;
   }
-  int2 incl = sum;
+  int3 incl = sum;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o);
+    const int x = __shfl_up_sync(0xffffffffu, incl.x, o), y = __shfl_up_sync(0xffffffffu, incl.y, o),
+              z = __shfl_up_sync(0xffffffffu, incl.z, o);
     if (lane >= o) {
       incl.x += x;
       incl.y += y;
+      incl.z += z;
     }
   }
   if (lane == 31) scan[warp] = incl;
   __syncthreads();
-  int2 pre = make_int2(incl.x - sum.x, incl.y - sum.y);
+  int3 pre = make_int3(incl.x - sum.x, incl.y - sum.y, incl.z - sum.z);
 #pragma unroll
   for (int v = 0; v < NT / 32; ++v) {
     pre.x += v < warp ? scan[v].x : 0;
     pre.y += v < warp ? scan[v].y : 0;
+    pre.z += v < warp ? scan[v].z : 0;
   }
   for (int b = b0; b < b1; ++b) {
     before[b] += pre.x;
-    before[p.B + 1 + b] += pre.y;
+    few[b] += pre.y;
+    light[b] += pre.z;
   }
   if (tid == NT - 1) {
     before[p.B] = pre.x + sum.x;
-    before[2 * p.B + 1] = pre.y + sum.y;
+    few[p.B] = pre.y + sum.y;
+    light[p.B] = pre.z + sum.z;
   }
   __syncthreads();
+}
+
+// The sequence that holds unit x of all heads.
+__device__ __forceinline__ int weight_sequence(const int* w, int B, int Hkv, int x) {
+  int lo = 0, hi = B;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (w[mid] * Hkv <= x) lo = mid;
+    else hi = mid;
+  }
+  return lo;
 }
 
 // The x-th unit; false behind the last.  A head's units fall in cost (the later the slots,
@@ -295,17 +324,56 @@ __device__ __forceinline__ bool weight_unit(const ChunkParams& p, const int* bef
     w += p.B + 1;
     if (x >= w[p.B] * p.Hkv) return false;
   }
-  int lo = 0, hi = p.B;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (w[mid] * p.Hkv <= x) lo = mid;
-    else hi = mid;
-  }
+  const int lo = weight_sequence(w, p.B, p.Hkv, x);
   const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0, 0};
   const int rem = x - w[lo] * p.Hkv;
   bool bad = false;
   u = WeightUnit{lo, rem % p.Hkv, rem / p.Hkv * SLOTS, line.sequence(lo, &bad)};
   return true;
+}
+
+// The light sequences, by all warps of all blocks, a piece at a time, four slots to a lane.
+template <int NT>
+__device__ void weight_light(const ChunkParams& p, const int* light) {
+  const ChunkLine line{nullptr, p.cu_new, p.seq_lens, p.n_tokens, p.T_cap, p.B, p.Hkv, 0, 0, 0};
+  const int lane = threadIdx.x & 31, warps = gridDim.x * (NT / 32), all = light[p.B] * p.Hkv;
+  for (int x = (threadIdx.x >> 5) * gridDim.x + blockIdx.x; x < all; x += warps) {
+    const int b = weight_sequence(light, p.B, p.Hkv, x), rem = x - light[b] * p.Hkv, h = rem % p.Hkv;
+    bool bad = false;
+    const ChunkSeq q = line.sequence(b, &bad);
+    const int rows = q.n * p.G, t = WEIGHT_PIECE * (rem / p.Hkv) + 4 * lane;
+    if (t < q.len) {
+      const int page = p.page_table[(size_t)b * p.max_pages + (t >> p.log2_page)];
+      if (page < 0 || page >= p.n_pages) continue;
+      const float* z = chunk_logits(p, b, h) + t;
+      const float* lse = p.lse + ((size_t)h * p.n_tokens + q.first) * p.G;
+      float4 zr[CHUNK_LIGHT];
+      float l[CHUNK_LIGHT];
+#pragma unroll
+      for (int r = 0; r < CHUNK_LIGHT; ++r) {
+        zr[r] = r < rows ? ld_cg(reinterpret_cast<const float4*>(z + (size_t)r * p.T_pad)) : make_float4(0.f, 0.f, 0.f, 0.f);
+        l[r] = r < rows ? ld_cg(lse + r) : INFINITY;
+      }
+      float* weight = p.weight + ((size_t)b * p.Hkv + h) * p.T_cap + t;
+      const float4 old = *reinterpret_cast<const float4*>(weight);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int r = 0; r < CHUNK_LIGHT; ++r) {
+        a.x += exp2f(zr[r].x - l[r]);
+        a.y += exp2f(zr[r].y - l[r]);
+        a.z += exp2f(zr[r].z - l[r]);
+        a.w += exp2f(zr[r].w - l[r]);
+      }
+      const int live = q.len - t;  // slots behind the end keep what they hold
+      if (live >= 4) {
+        *reinterpret_cast<float4*>(weight) = make_float4(old.x + a.x, old.y + a.y, old.z + a.z, old.w + a.w);
+      } else {
+        weight[0] = old.x + a.x;
+        if (live > 1) weight[1] = old.y + a.y;
+        if (live > 2) weight[2] = old.z + a.z;
+      }
+    }
+  }
 }
 
 }  // namespace fasa

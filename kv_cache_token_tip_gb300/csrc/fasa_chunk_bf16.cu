@@ -126,6 +126,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
           return lane < 8 && slot < q.len ? table[slot >> p.log2_page] : 0;
         };
         int page = f0 < e ? look_up(f0) : 0;
+        float* keep = live && chunk_light(p, q) ? chunk_logits(p, u.b, u.h) + (size_t)row * p.T_pad : nullptr;
         float m = -INFINITY;
         uint64_t l2 = 0;  // two sums
         for (int t = f0; t < e; ++t) {
@@ -146,6 +147,13 @@ __global__ void __launch_bounds__(CB_NT, 1)
 #pragma unroll
             for (int i = 0; i < 128; ++i)
               if (i >= lim || !(held >> (i >> 4) & 1u)) s[i] = 0xff800000u;  // -inf
+          }
+          if (keep) {
+            float4* to = reinterpret_cast<float4*>(keep + t * CB_K);
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+              to[i] = make_float4(__uint_as_float(s[4 * i]) * scale, __uint_as_float(s[4 * i + 1]) * scale,
+                                  __uint_as_float(s[4 * i + 2]) * scale, __uint_as_float(s[4 * i + 3]) * scale);
           }
           float mx[4];
 #pragma unroll
@@ -469,7 +477,7 @@ struct CwPlan {
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;
   static constexpr int OFF_PAIR = (OFF_MISC + 16 + 15) / 16 * 16;
   static constexpr int OFF_LINE = OFF_PAIR + CW_ROWS / 2 * 128;
-  static constexpr int bytes(int B) { return 1024 + OFF_LINE + (2 * B + 2) * 4; }
+  static constexpr int bytes(int B) { return 1024 + OFF_LINE + (3 * B + 3) * 4; }
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
 };
 
@@ -531,8 +539,9 @@ __global__ void __launch_bounds__(CW_NT, 1)
   tm_before_sync();
   paged_go();
   paged_wait();
-  weight_line<CW_NT, 256>(p, before, reinterpret_cast<int2*>(sm + P::OFF_PAIR), TQ);
+  weight_line<CW_NT, 256>(p, before, reinterpret_cast<int3*>(sm + P::OFF_PAIR), TQ);
   tm_after_sync();
+  if (p.logits) weight_light<CW_NT>(p, before + 2 * (p.B + 1));
   const Patience patience{misc + 1, p.status, p.wait_ns};
   int issued = 0;  // copies
   // f(unit) for each unit of this block, in order, as the copying warp takes them

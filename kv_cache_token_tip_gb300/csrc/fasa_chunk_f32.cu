@@ -42,8 +42,8 @@ struct CfPlan {
   static constexpr int bytes(int B) { return 1024 + OFF_LINE + (B + 1) * 8; }
   // weights: K, Q and its rows' log-sums twice, sums
   static constexpr int W_Q = K_BYTES, W_LSE = W_Q + 2 * Q_BYTES, W_SUM = W_LSE + 2 * CF_M * 4;
-  static constexpr int W_ROWS = W_SUM + 16 * LP * 4, W_SCAN = W_ROWS + CF_K * 4, W_LINE = W_SCAN + CF_NT / 32 * 8;
-  static constexpr int weight_bytes(int B) { return W_LINE + (2 * B + 2) * 4; }
+  static constexpr int W_ROWS = W_SUM + 16 * LP * 4, W_SCAN = W_ROWS + CF_K * 4, W_LINE = W_SCAN + CF_NT / 32 * 12;
+  static constexpr int weight_bytes(int B) { return W_LINE + (3 * B + 3) * 4; }
   static_assert(bytes(PAGED_MAX_BATCH) <= 232448 && weight_bytes(PAGED_MAX_BATCH) <= 232448, "the largest batch fits");
 };
 
@@ -378,7 +378,7 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_weight_f32_kernel(const __grid
   const int tid = threadIdx.x, ty = tid >> 4, tx = tid & 15, TU = CF_M / p.G;
   paged_go();
   paged_wait();
-  weight_line<CF_NT, CF_K>(p, before, reinterpret_cast<int2*>(sm + P::W_SCAN), TU);
+  weight_line<CF_NT, CF_K>(p, before, reinterpret_cast<int3*>(sm + P::W_SCAN), TU);
   __shared__ int ahead;
   for (int mine = blockIdx.x;;) {  // (the first unit is the block's own; the queue counts those behind)
     WeightUnit u;

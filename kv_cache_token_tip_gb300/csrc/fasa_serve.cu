@@ -117,6 +117,12 @@ void chunk_plan(const fasa_paged_dims_t* d, int n_tokens, int sms, int* rows, in
 }
 
 size_t notes_bytes(int parts) { return 256 + up((size_t)parts * 2 * sizeof(int4)); }  // and the queue
+int padded_slots(const fasa_paged_dims_t* d) { return (d->max_pages * d->page_size + 127) / 128 * 128; }
+// Logits of the light sequences, where there is a second pass that reads them.
+size_t logits_bytes(const fasa_paged_dims_t* d) {
+  const long long n = (long long)d->batch * d->n_kv_heads * CHUNK_LIGHT * padded_slots(d) * 4;
+  return d->dtype == FASA_BF16 && n <= CHUNK_LOGITS ? up((size_t)n) : 0;
+}
 size_t records_bytes(int rows, int parts, int D) { return up((size_t)parts * 2 * rows * (D + 2) * 4); }
 
 }  // namespace
@@ -249,7 +255,7 @@ int fasa_paged_chunk_workspace_size(const fasa_paged_dims_t* dims, int32_t n_tok
   int rows, parts;  // (of any device)
   chunk_plan(dims, n_tokens, CHUNK_MAX_SMS, &rows, &parts);
   *bytes = notes_bytes(parts) + records_bytes(rows, parts, dims->head_dim);
-  if (with_weight) *bytes += up((size_t)n_tokens * dims->n_q_heads * 4);
+  if (with_weight) *bytes += logits_bytes(dims) + up((size_t)n_tokens * dims->n_q_heads * 4);
   return FASA_OK;
 }
 
@@ -298,7 +304,10 @@ int fasa_paged_chunk_attention(const void* q, int32_t n_tokens, const int32_t* c
   p.notes = reinterpret_cast<int4*>(ws + 256);
   ws += notes_bytes(p.parts);
   p.records = reinterpret_cast<float*>(ws);
-  p.lse = reinterpret_cast<float*>(ws + records_bytes(p.rows, p.parts, dims->head_dim));
+  ws += records_bytes(p.rows, p.parts, dims->head_dim);
+  p.T_pad = padded_slots(dims);
+  p.logits = weight && logits_bytes(dims) ? reinterpret_cast<float*>(ws) : nullptr;
+  p.lse = reinterpret_cast<float*>(ws + (weight ? logits_bytes(dims) : 0));
   p.status = status;
   p.wait_ns = wait_limit_ns();
   p.drop_tile = dropped_copy();

@@ -63,6 +63,8 @@ struct ChunkParams {
   float scale;     // log2(e) / sqrt(d): logits are kept in powers of two
   float* records;  // [parts][2][rows * (d + 2)]: o [rows][d], m [rows], l [rows]
   int4* notes;     // [parts][2]: whose the records are
+  float* logits;   // [B * Hkv][CHUNK_LIGHT][T_pad] of sequences of few rows; null: not kept
+  int T_pad;       // T_cap in whole tiles of slots
   int* queue;      // the next unit of the weights' pass (the first kernel sets it to 0)
   float* lse;      // [Hkv][n_tokens * G]
   int rows;        // of a record
@@ -78,6 +80,11 @@ struct ChunkParams {
 struct ChunkShape {
   int tokens, tile, per_sm;
 };
+// A sequence is light with this many rows (new tokens times the heads of a group) or fewer: its
+// logits are kept for the weights, 16 bytes a slot for 4 rows instead of K's 256 again, where
+// those of the whole batch would take no more than CHUNK_LOGITS bytes.
+constexpr int CHUNK_LIGHT = 8;
+constexpr long long CHUNK_LOGITS = 512ll << 20;
 inline ChunkShape chunk_shape(bool bf16, int G) { return bf16 ? ChunkShape{2 * (128 / G), 128, 1} : ChunkShape{128 / G, 64, 1}; }
 
 cudaError_t launch_paged_assign(const AssignParams& p, int sms, cudaStream_t s);
