@@ -194,6 +194,18 @@ __global__ void __launch_bounds__(CA_NT, 1)
         }
         free_it(k_empty);
         if (t + 1 == f1) free_it(q_empty);
+        if (busy && chunk_light(p, u.q)) {
+          float* keep = chunk_logits(p, u.b, u.h) + t0 + tx;
+#pragma unroll 1
+          for (int i = 0; 8 * ty + i < rows && i < 8; ++i)
+            for (int j = 0; j < 4; ++j) {
+              float x = 0.f;  // z[i][j], from registers
+#pragma unroll
+              for (int k = 0; k < 32; ++k) x = k == 4 * i + j ? z[k >> 2][k & 3] : x;
+              keep[(size_t)(8 * ty + i) * p.T_pad + 16 * j] =
+                  (there >> j & 1) && t0 + tx + 16 * j < len - n + j0 + (8 * ty + i) / p.G + 1 ? x * p.scale : -INFINITY;
+            }
+        }
         if (busy) {
 #pragma unroll
           for (int i = 0; i < 8; ++i) {
@@ -379,6 +391,7 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_weight_f32_kernel(const __grid
   paged_go();
   paged_wait();
   weight_line<CF_NT, CF_K>(p, before, reinterpret_cast<int3*>(sm + P::W_SCAN), TU);
+  if (p.logits) weight_light<CF_NT>(p, before + 2 * (p.B + 1));
   __shared__ int ahead;
   for (int mine = blockIdx.x;;) {  // (the first unit is the block's own; the queue counts those behind)
     WeightUnit u;

@@ -121,7 +121,7 @@ int padded_slots(const fasa_paged_dims_t* d) { return (d->max_pages * d->page_si
 // Logits of the light sequences, where there is a second pass that reads them.
 size_t logits_bytes(const fasa_paged_dims_t* d) {
   const long long n = (long long)d->batch * d->n_kv_heads * CHUNK_LIGHT * padded_slots(d) * 4;
-  return d->dtype == FASA_BF16 && n <= CHUNK_LOGITS ? up((size_t)n) : 0;
+  return n <= CHUNK_LOGITS ? up((size_t)n) : 0;
 }
 size_t records_bytes(int rows, int parts, int D) { return up((size_t)parts * 2 * rows * (D + 2) * 4); }
 

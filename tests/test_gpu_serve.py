@@ -668,7 +668,8 @@ def test_chunk_many_sequences_and_heads(dtype, B, Hkv, G, d):
     assert status() == 0
 
 
-@pytest.mark.parametrize("dtype,d,G,page", [("bf16", 64, 4, 256), ("bf16", 128, 8, 16), ("f32", 64, 2, 128)])
+@pytest.mark.parametrize("dtype,d,G,page", [("bf16", 64, 4, 256), ("bf16", 128, 8, 16), ("f32", 64, 2, 128),
+                                            ("bf16", 128, 1, 64), ("f32", 128, 1, 16)])
 def test_chunk_long_cache(dtype, d, G, page):
     """One sequence over the whole range of slots, and a short one beside it."""
     k = Chunk(dtype, 2, 1, G, d, page, [262144 - 5, 7], [5, 30], seed=10, max_pages=262144 // page)
@@ -682,6 +683,37 @@ def test_chunk_long_cache(dtype, d, G, page):
     got = (k.weight.double() - before.double()).clamp(min=0)
     assert abs(float(got[0].sum()) - 5 * G) <= 1e-3 * 5 * G + float(before[0].double().sum()) * U
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype,G", [("bf16", 4), ("bf16", 1), ("f32", 8)])
+def test_chunk_weights_of_few_rows_either_way(dtype, G):
+    """Sequences of up to eight rows have their logits kept for the weights, where a batch's logits are not too many: a
+    table of many more entries, and the second pass works them out again."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_chunk_attention, fasa_paged_chunk_workspace_size
+    B, Hkv, d, page = 64, 8, 64, 16
+    rng = np.random.default_rng(G)
+    k = Chunk(dtype, B, Hkv, G, d, page, [int(x) for x in rng.integers(0, 400, B)], [int(x) for x in rng.integers(0, 3, B)],
+              seed=17)
+    k.table[3, 1] = -1   # (reported where that sequence has a new token, and slots there)
+    looked = int(k.cu_host[4] > k.cu_host[3] and int(k.lens[3]) > page)
+    start = k.weight.clone()
+    out = k.run().clone()
+    assert status() == looked
+    wide = 2200
+    assert B * Hkv * 8 * wide * page * 4 > 1 << 29 > B * Hkv * 8 * (k.cap + 128) * 4
+    table = torch.full((B, wide), -1, dtype=torch.int32, device="cuda")
+    table[:, :k.table.shape[1]] = k.table
+    weight = torch.zeros((B, Hkv, wide * page), device="cuda")
+    weight[:, :, :k.cap] = start
+    dims = paged_dims(dtype, B, Hkv, G, d, page, k.kp.shape[0], wide)
+    assert fasa_paged_chunk_workspace_size(dims, k.n, True) < 1 << 29
+    fasa_paged_chunk_attention(k.q, k.kp, k.vp, table, k.lens, k.out, cu_new=k.cu, weight=weight, dims=dims)
+    assert status() == looked and torch.equal(k.out, out)
+    # the same logits, summed in another order: 16 u of each exp2 and 9 sums, and u of the weight
+    got = k.weight - start
+    assert ((weight[:, :, :k.cap] - k.weight).abs() <= 64 * U * got.abs() + 8 * U * k.weight + 1e-30).all()
+    assert not weight[:, :, k.cap:].any()
 
 
 def test_offsets_past_32_bits():
