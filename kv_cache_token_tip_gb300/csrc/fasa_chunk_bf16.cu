@@ -12,7 +12,7 @@
 // Bound by the tensor cores where units are long: 2048 tokens behind 30720 take 598 us by
 // themselves, 1.78 PFLOP/s of visible pairs (tensor pipe 83% busy), and 685 to 730 one after
 // another, where the card's power bounds them.  Eight prompts of 37 to 4096 tokens 327 us
-// (68%): a unit's start and end, 5000 clocks beside 2750 a tile.  Drafted tokens of 16
+// (68%): a unit's start and end, 5400 to 5800 clocks beside 2530 a tile.  Drafted tokens of 16
 // sequences 110 us, 5.8 TB/s.  What it took: instructions issued by one elected lane from
 // descriptors worked out ahead (742 -> 684 us for the first case; 670 clocks for eight
 // instructions before, 370 since), P handed over by halves and a row to a thread (598; half a

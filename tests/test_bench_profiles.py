@@ -72,18 +72,3 @@ def test_paged_summary_names_its_sources():
     assert re.fullmatch(r"[0-9a-f]{16}", vals["kernel_source_hash"])
     if bench.kernel_source_hash([os.path.join(csrc, f) for f in names]) != vals["kernel_source_hash"]:
         warnings.warn("profiles/fasa_paged.md was taken on other sources of the paged cache")
-
-
-def test_serve_summary_names_its_sources():
-    """The same of the summary of a step of new tokens."""
-    import warnings
-
-    import bench
-    vals = _values(os.path.join(PROFILES, "fasa_serve.md"))
-    csrc = "kv_cache_token_tip_gb300/csrc"
-    names = vals["kernel_sources"].split("`")[0].split()
-    assert {"fasa_chunk.cuh", "fasa_chunk_bf16.cu", "fasa_chunk_f32.cu", "fasa_serve_tokens.cu"} <= set(names)
-    assert all(os.path.exists(os.path.join(ROOT, csrc, f)) for f in names)
-    assert re.fullmatch(r"[0-9a-f]{16}", vals["kernel_source_hash"])
-    if bench.kernel_source_hash([os.path.join(csrc, f) for f in names]) != vals["kernel_source_hash"]:
-        warnings.warn("profiles/fasa_serve.md was taken on other sources")

@@ -323,3 +323,18 @@ def test_binding_without_a_gpu_raises():
         fasa_paged_rope_append(x, x, x, x, x, x, x, rope=FasaRope(), dims=d)
     with pytest.raises((RuntimeError, ValueError)):
         fasa_paged_chunk_attention(x, x, x, x, x, x, workspace=x, dims=d)
+
+
+def test_summary_of_the_captures_names_its_sources():
+    import re
+    import warnings
+
+    import bench
+    text = open(os.path.join(ROOT, "profiles", "fasa_serve.md")).read()
+    names = re.search(r"kernel_sources: `([^`]*)`", text).group(1).split()
+    told = re.search(r"kernel_source_hash: `([0-9a-f]{16})`", text).group(1)
+    csrc = "kv_cache_token_tip_gb300/csrc"
+    assert {"fasa_chunk.cuh", "fasa_chunk_bf16.cu", "fasa_chunk_f32.cu", "fasa_serve_tokens.cu"} <= set(names)
+    assert all(os.path.exists(os.path.join(ROOT, csrc, f)) for f in names)
+    if bench.kernel_source_hash([os.path.join(csrc, f) for f in names]) != told:
+        warnings.warn("profiles/fasa_serve.md was taken on other sources")
