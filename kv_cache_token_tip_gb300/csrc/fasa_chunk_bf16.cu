@@ -449,8 +449,8 @@ __global__ void __launch_bounds__(CB_NT, 1)
 // ------------------------------------------------------------------ weights
 // weight_t += sum over the rows that see slot t of 2^(scale S - log-sum of the row).  A
 // unit is 256 slots of a (sequence, KV head): two tiles of K as rows of S^T = K Q^T, the
-// rows of Q 128 at a time as its columns (K in tensor memory, Q in shared memory), so that a thread adds what one slot gets, in the
-// rows' order.
+// rows of Q 128 at a time as its columns (K in tensor memory, Q in shared memory), so that a
+// thread adds what one slot gets, in the rows' order.
 constexpr int CW_NT = 640;           // 16 warps of slots, one of instructions, one of copies, two at rest
 constexpr int CW_ROWS = 16;
 constexpr int CW_S = 3;              // tiles of S in tensor memory, of 128 columns, behind the two tiles of K
@@ -553,10 +553,12 @@ __global__ void __launch_bounds__(CW_NT, 1)
   if (p.logits) weight_light<CW_NT>(p, before + 2 * (p.B + 1));
   const Patience patience{misc + 1, p.status, p.wait_ns};
   int issued = 0;  // copies
-  // f(unit) for each unit of this block, in order, as the copying warp takes them
-  auto units = [&](auto&& f) {
+  // f(unit) for each unit of this block, in order, as the copying warp takes them.  came(x):
+  // whether the unit came for all warps that f has wait for each other: one that gives up
+  // alone would leave the others at a barrier without a limit.
+  auto units = [&](auto&& came, auto&& f) {
     for (int i = 0;; ++i) {
-      if (!patience.wait(u_full + 8 * (i & 1), i >> 1 & 1)) return;
+      if (!came(patience.wait(u_full + 8 * (i & 1), i >> 1 & 1))) return;
       const int x = misc[2 + (i & 1)];
       __syncwarp();
       if (lane == 0) mbar_arrive(u_empty + 8 * (i & 1));
@@ -577,7 +579,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
     int at_k = 0;  // place of the next unit's K in the ring
     uint32_t k_phase = 0;
     int k = 0, n_s = 0, own = 0;  // Q tiles, S tiles, and those of these rows, so far
-    units([&](const WeightUnit& u) {
+    units([&](bool x) { return !pair.either(!x); }, [&](const WeightUnit& u) {
       const int slot = u.t0 + 128 * w + row, from = u.from(0, TQ), mine = u.from(128 * w, TQ), tiles = u.tiles(TQ);
       if (from >= tiles) return true;
       int page = -1;
@@ -673,7 +675,7 @@ __global__ void __launch_bounds__(CW_NT, 1)
     RingAt<S> at;
     uint32_t k_phase = 0;
     int n_s = 0, own[2] = {0, 0};
-    units([&](const WeightUnit& u) {
+    units([](bool x) { return x; }, [&](const WeightUnit& u) {
       const int from[2] = {u.from(0, TQ), u.from(128, TQ)}, tiles = u.tiles(TQ);
       if (from[0] >= tiles) return true;
       int k_at[2];
