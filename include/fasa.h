@@ -556,6 +556,8 @@ typedef struct fasa_rope {
  * apart from q, k and v.  rope_theta of dims is not used.
  * Rows of the map whose sequence is negative are padding: nothing is written for them, nor
  * for an entry outside the batch, the cache or the pool, which sets FASA_DEV_BAD_INPUT.
+ * Rows that name one slot of one sequence twice leave a mixture of the two there (those of
+ * fasa_paged_assign never do).
  * The attention of one token (fasa_paged_attention) takes such queries with positions of 0,
  * which turn nothing.
  * Aligned to 16 bytes: every tensor, and the strides in bytes.  n_tokens <= 2^24.
@@ -572,7 +574,8 @@ int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64
  * seq_lens counts the new tokens: the j-th of the n of sequence b has slot
  * s = seq_lens[b] - n + j, and
  *   out[x] = softmax(q K^T / sqrt(d)) V over the slots 0 .. s   (storage dtype, rounded once);
- * zeros where there is none (s < 0).  With weight (not NULL):
+ * zeros where there is none (s < 0).  What is not finite in the K or V of other slots reaches
+ * no row.  With weight (not NULL):
  *   weight[b,h,t] += sum over the new tokens and the group's heads of softmax_t.
  * bf16: the softmax weights that multiply V are rounded to bf16; their sum and what goes
  * to `weight` are not.  Equal calls give equal bits.

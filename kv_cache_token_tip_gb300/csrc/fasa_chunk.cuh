@@ -80,6 +80,34 @@ __device__ __forceinline__ void store4(T* to, float a, float b, float c, float d
     *reinterpret_cast<float4*>(to) = make_float4(a, b, c, d);
 }
 
+// V at slots that only some of a unit's tokens see: a product with a weight of 0 would bring
+// what is not finite there (bits of the exponent all set) to the rows that do not see it.  So
+// such elements are cleared before P V, and a row that sees one gets it here, once its result is
+// stored: the element itself, since a sum with infinity or NaN does not depend on its weight.
+// Slots [s0, s1) are those of the row's; to: its place, of storage type T.  Seldom called.
+__device__ __forceinline__ bool not_finite(float x) { return (__float_as_uint(x) & 0x7f800000u) == 0x7f800000u; }
+__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ float as_float(float x) { return x; }
+__device__ __forceinline__ void put(__nv_bfloat16* to, float x) { *to = __float2bfloat16(x); }
+__device__ __forceinline__ void put(float* to, float x) { *to = x; }
+template <typename T, typename O>
+__device__ __noinline__ void add_not_finite(const ChunkParams& p, int b, int h, int s0, int s1, int d0, int d1, int D, O* to) {
+  for (int s = s0; s < s1; ++s) {
+    const long long row = paged_row(p.page_table[(size_t)b * p.max_pages + (s >> p.log2_page)], p.n_pages, p.Hkv, h, p.log2_page, s);
+    if (row < 0) continue;
+    for (int d = d0; d < d1; ++d) {
+      const float v = as_float(static_cast<const T*>(p.v_pages)[(size_t)row * D + d]);
+      if (not_finite(v)) put(to + d, as_float(to[d]) + v);
+    }
+  }
+}
+// The slots from the unit's second token's on, that its first does not see, and the end of
+// those that its last one sees.
+__device__ __forceinline__ int2 partly_seen(const ChunkUnit& u, int T) {
+  const int a = u.q.len - u.q.n;
+  return make_int2(max(0, a + u.i * T + 1), max(0, a + min((u.i + 1) * T, u.q.n)));
+}
+
 // Walks the segments of the part [y0, y1): f(unit, f0, f1, whole) for its tiles of slots
 // f0 .. f1 - 1, until it says false.  The same for every role.
 template <class F>

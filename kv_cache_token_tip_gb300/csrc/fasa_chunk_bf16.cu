@@ -47,7 +47,7 @@ struct CbPlan {
   static constexpr int OFF_BAR = OFF_RING + STAGES * TILE;
   static constexpr int BARS = 2 * STAGES + 2 + 8 + 1;
   static constexpr int OFF_MISC = OFF_BAR + BARS * 8;    // tensor memory's address, dead
-  static constexpr int OFF_SCAN = OFF_MISC + 16;
+  static constexpr int OFF_SCAN = OFF_MISC + 16;          // (and whether a unit's V was not finite)
   static constexpr int OFF_TURN = (OFF_SCAN + CB_NT / 32 * 8 + 15) / 16 * 16;  // results on their way out, 2 KB a warp
   static constexpr int OFF_SEQ = OFF_TURN + CB_ROWS * 2048;
   static constexpr int bytes(int B) { return 1024 + OFF_SEQ + (B + 1) * 8; }
@@ -60,6 +60,44 @@ __device__ __forceinline__ int row_tile_end(const ChunkParams& p, const ChunkUni
   if (j0 >= u.q.n) return f0;
   const int see = u.q.len - u.q.n + min(j0 + TQ, u.q.n);
   return max(f0, min(f1, see > 0 ? (see + CB_K - 1) / CB_K : 0));
+}
+
+// Clears what a tile of V (128 rows at `tile`) brings to rows that do not see it: rows n .. 127,
+// which hold anything (up to the pages' end; what lies behind that was not copied and is 0), and
+// elements of rows r0 .. n - 1 that are not finite.  A warp; whether there were any.  A function
+// of its own (eight prompts 326 us; inlined among the matrix instructions 339, without any of
+// it 319); it has to do with the 56 registers of its warp.
+template <int D>
+__device__ __noinline__ bool clear_unseen(uint32_t tile, int r0, int n) {
+  using P = CbPlan<D>;
+  constexpr int CH = P::HALVES * 8, RS = 32 / CH;  // 16-byte chunks of a row, rows at a time
+  const int lane = threadIdx.x & 31;
+  const uint32_t place = tile + (lane % CH >> 3) * P::SLAB + lane / CH * 128 + ((lane & 7) << 4);
+#pragma unroll 8
+  for (int r = n; r < CB_K; r += RS)
+    if (r + lane / CH < CB_K)
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(place + r * 128), "r"(0) : "memory");
+  bool found = false;
+#pragma unroll 4
+  for (int r = r0; r < n; r += RS) {
+    uint32_t x[4] = {0u, 0u, 0u, 0u}, f[4];
+    if (r + lane / CH < n)
+      asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3])
+                   : "r"(place + r * 128));
+#pragma unroll
+    for (int y = 0; y < 4; ++y) f[y] = ((x[y] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;  // (no carry)
+    if (f[0] | f[1] | f[2] | f[3]) {
+      found = true;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) x[y] &= ~((f[y] >> 15) * 0xffffu);
+      asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(place + r * 128), "r"(x[0]), "r"(x[1]), "r"(x[2]),
+                   "r"(x[3])
+                   : "memory");
+    }
+  }
+  fence_proxy_async();
+  return __any_sync(0xffffffffu, found);
 }
 
 template <int D>
@@ -91,7 +129,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
       mbar_init(s_full + 8 * w, 1);
       mbar_init(p_full + 16 * w, 4);
       mbar_init(p_full + 16 * w + 8, 4);
-      mbar_init(o_full + 8 * w, 1);
+      mbar_init(o_full + 8 * w, 2);
     }
     fence_mbar_init();
   }
@@ -290,6 +328,14 @@ __global__ void __launch_bounds__(CB_NT, 1)
           rec[(size_t)p.rows * D + r] = m;
           rec[(size_t)p.rows * (D + 1) + r] = l;
         }
+        if (f0 < e && misc[2 + w]) {  // (the results are stored by other lanes of the warp)
+          __syncwarp();
+          const int s0 = max(partly_seen(u, TU).x, f0 * CB_K), s1 = min(see, f1 * CB_K);
+          if (live && whole)
+            add_not_finite<__nv_bfloat16>(p, u.b, u.h, s0, s1, 0, D, D, static_cast<__nv_bfloat16*>(p.out) + at.out(p, D));
+          else if (live)
+            add_not_finite<__nv_bfloat16>(p, u.b, u.h, s0, s1, 0, D, D, rec + (size_t)r * D);
+        }
         return true;
       });
     } else if (warp == CB_ROWS) {
@@ -320,6 +366,8 @@ __global__ void __launch_bounds__(CB_NT, 1)
         const int e0 = row_tile_end(p, u, 0, f0, f1), e1 = row_tile_end(p, u, 1, f0, f1);
         const int e[2] = {e0, e1}, end = max(e0, e1);
         if (f0 == end) return true;
+        const int2 partly = partly_seen(u, TU);
+        bool odd = false;
         if (!patience.wait(q_full, q_phase)) return false;
         q_phase ^= 1;
         if (!landed(k)) return false;
@@ -330,18 +378,8 @@ __global__ void __launch_bounds__(CB_NT, 1)
         if (f0 + 1 == end) free_tile(q_empty);
         for (int t = f0; t < end; ++t, k += 2) {
           if (!landed(k + 1)) return false;
-          if ((t + 1) * CB_K > q.len) {
-            // slots behind the end hold anything: V's rows are cleared, up to the pages' end
-            // (what lies behind that was not copied and is 0)
-            const int n = q.len - t * CB_K;
-            for (int i = lane; i < (CB_K - n) * P::HALVES * 8; i += 32) {
-              const int r = n + i / (P::HALVES * 8), ch = i % (P::HALVES * 8);
-              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(k + 1) + (ch >> 3) * P::SLAB + r * 128 +
-                                                                            ((ch & 7) << 4)),
-                           "r"(0)
-                           : "memory");
-            }
-            fence_proxy_async();
+          if ((t + 1) * CB_K > partly.x) {
+            odd = clear_unseen<D>(at(k + 1), max(0, partly.x - t * CB_K), min(CB_K, partly.y - t * CB_K)) || odd;
             __syncwarp();
           }
           const bool more = t + 1 < end;
@@ -357,7 +395,11 @@ __global__ void __launch_bounds__(CB_NT, 1)
 #pragma unroll
                   for (int x = 4 * h; x < 4 * h + 4; ++x)
                     mma_ts(TM + 256 + 128 * w, TM + 128 * w + 8 * x, b + (2048 * x >> 4), kind_o, t > f0 || x > 0);
-                  if (h == 1 && t + 1 == e[w]) mma_commit(o_full + 8 * w);
+                  if (h == 1 && t + 1 == e[w]) {
+                    misc[2 + w] = odd;  // (the rows' last P came: they have read the last unit's)
+                    mbar_arrive(o_full + 8 * w);
+                    mma_commit(o_full + 8 * w);
+                  }
                 }
               }
               p_phase[w] ^= 1;
@@ -419,7 +461,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
             if (!patience.wait(empty + 8 * st, (k / S & 1) ^ 1)) return false;
             if (lane == 0) mbar_arrive_expect_tx(full + 8 * st, P::TILE);
             __syncwarp();
-            if (mine < per && (n_tile != p.drop_tile || c != 0))  // (test hook: copies that never come)
+            if (mine < per && n_tile != p.drop_tile)  // (test hook: copies that never come)
               tma_2d(ring + st * P::TILE + half * P::SLAB + mine * box * 128, kv ? &vmap : &kmap, 64 * half, (int)row,
                      full + 8 * st);
             __syncwarp();

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
   float* ps = reinterpret_cast<float*>(sm + P::OFF_P);
   volatile unsigned* held = reinterpret_cast<unsigned*>(sm + P::OFF_HELD);  // two tiles' masks of slots that count
   volatile int* dead = reinterpret_cast<int*>(sm + P::OFF_HELD) + 4;
+  volatile int* not_all_finite = dead + 1;  // V of the tile, where not all rows see it
   const uint32_t bars = smem_u32(sm + P::OFF_BAR);
   const uint32_t q_full = bars, q_empty = bars + 8, k_full = bars + 16, k_empty = bars + 24, v_full = bars + 32,
                  v_empty = bars + 40, v_raw = bars + 48;
@@ -182,6 +183,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
         if (!patience.wait(q_full, q_phase)) return false;
         q_phase ^= 1;
       }
+      int odd = 0;
       for (int t = f0; t < f1; ++t) {
         const int t0 = t * CF_K;
         if (!patience.wait(k_full, t_phase)) return false;
@@ -237,6 +239,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
         }
         if (!patience.wait(v_full, t_phase)) return false;
         t_phase ^= 1;
+        odd |= *not_all_finite;
         if (busy) {
           const char* v0 = vs + (tx >> 3) * (CF_K * 128);
 #pragma unroll 1
@@ -292,6 +295,16 @@ __global__ void __launch_bounds__(CA_NT, 1)
           rec[(size_t)p.rows * (D + 1) + r] = l[i];
         }
       }
+      if (odd) {  // (every thread the dims that it stored)
+        const int s0 = max(partly_seen(u, TU).x, f0 * CF_K);
+        for (int r = 8 * ty; r < min(rows, 8 * ty + 8); ++r) {
+          float* to = whole ? static_cast<float*>(p.out) + ChunkRow(p, u, TU, r).out(p, D)
+                            : chunk_record(p, D, c, f0 > 0 ? 0 : 1) + (size_t)r * D;
+          for (int e = 0; e < E; ++e)
+            add_not_finite<float>(p, u.b, u.h, s0, min(len - n + j0 + r / p.G + 1, f1 * CF_K), 4 * tx + 64 * e,
+                                  4 * tx + 64 * e + 4, D, to);
+        }
+      }
       return true;
     });
   } else if (warp == CF_NT / 32) {
@@ -306,6 +319,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
       if (f0 == f1) return true;
       const int len = u.q.len;
       auto look_up = [&](int t) { return mine < per ? slot_row(p, u.b, u.h, t * CF_K + mine * box, len, true) : -1; };
+      const int2 partly = partly_seen(u, TU);
       int next = look_up(f0);
       if (!patience.wait(q_empty, q_phase)) return false;
       q_phase ^= 1;
@@ -323,7 +337,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i)
           h[i] = __ballot_sync(0xffffffffu, lane + 32 * i < behind && (boxes >> ((lane + 32 * i) / box * P::SLABS) & 1u));
-        const bool drop = n_tile == p.drop_tile && c == 0;  // (test hook: copies that never come)
+        const bool drop = n_tile == p.drop_tile;  // (test hook: copies that never come)
         const int at = row >= 0 ? row : none;
         const uint32_t to = slab * CF_K * 128 + mine * box * 128;
         if (!patience.wait(k_empty, t_phase)) return false;
@@ -338,9 +352,11 @@ __global__ void __launch_bounds__(CA_NT, 1)
         ++copies;
         if (!patience.wait(v_empty, t_phase)) return false;
         t_phase ^= 1;
-        // Rows of V behind the end have weights of 0 and may hold NaN: where there are some in a
-        // page, they are cleared before V is passed on
-        const bool tail = behind < CF_K;
+        // Rows of V behind those that the unit sees have weights of 0 and may hold NaN: where
+        // there are some in a page, they are cleared before V is passed on; elements that are not
+        // finite, of slots that some of its rows do not see, too
+        const bool tail = (t + 1) * CF_K > partly.x;
+        if (lane == 0) *not_all_finite = 0;
         if (lane == 0) mbar_arrive_expect_tx(tail ? v_raw : v_full, P::K_BYTES);
         __syncwarp();
         if (mine < per && !drop) tma_2d(smem_u32(vs) + to, &vmap, 32 * slab, at, tail ? v_raw : v_full);
@@ -351,8 +367,24 @@ __global__ void __launch_bounds__(CA_NT, 1)
           ++raw_copies;
           if (!patience.wait(v_raw, raw_phase)) return false;
           raw_phase ^= 1;
-          for (int i = lane; i < (CF_K - behind) * (D / 4); i += 32)
-            *reinterpret_cast<float4*>(vs + swizzled(CF_K, behind + i / (D / 4), i % (D / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
+          const int seen = min(CF_K, partly.y - t * CF_K), r0 = max(0, partly.x - t * CF_K);
+          for (int i = lane; i < (CF_K - seen) * (D / 4); i += 32)
+            *reinterpret_cast<float4*>(vs + swizzled(CF_K, seen + i / (D / 4), i % (D / 4))) = make_float4(0.f, 0.f, 0.f, 0.f);
+          bool found = false;
+#pragma unroll 4
+          for (int i = lane; i < (seen - r0) * (D / 4); i += 32) {
+            float4* at = reinterpret_cast<float4*>(vs + swizzled(CF_K, r0 + i / (D / 4), i % (D / 4)));
+            float4 x = *at;
+            if (not_finite(x.x) || not_finite(x.y) || not_finite(x.z) || not_finite(x.w)) {
+              found = true;
+              x.x = not_finite(x.x) ? 0.f : x.x;
+              x.y = not_finite(x.y) ? 0.f : x.y;
+              x.z = not_finite(x.z) ? 0.f : x.z;
+              x.w = not_finite(x.w) ? 0.f : x.w;
+              *at = x;
+            }
+          }
+          if (__any_sync(0xffffffffu, found) && lane == 0) *not_all_finite = 1;
           fence_proxy_async();  // (before the next copy into them)
           __syncwarp();
           if (lane == 0) mbar_arrive(v_full);

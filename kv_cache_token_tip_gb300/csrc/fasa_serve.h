@@ -48,8 +48,9 @@ struct RopeAppendParams {
 };
 
 // The attention of chunks.  Workspace: the parts' records (two per part: a unit that
-// began in an earlier part, a unit that goes on in a later one) with a note to each, and
-// with weights the rows' log-sums.
+// began in an earlier part, a unit that goes on in a later one) with a note to each and the
+// queue of the weights' pass, and with weights the light sequences' logits and the rows'
+// log-sums.
 struct ChunkParams {
   int B, Hq, Hkv, G, log2_page, n_pages, max_pages, T_cap, n_tokens;
   const void* q;
@@ -72,7 +73,7 @@ struct ChunkParams {
   int sms;
   int* status;
   unsigned long long wait_ns;
-  int drop_tile;  // test hook: this tile of part 0 is never copied (-1: none)
+  int drop_tile;  // test hook: this tile of every part is never copied (-1: none)
 };
 
 // Tokens of a unit (their rows: times the heads of their group), slots of a tile, and

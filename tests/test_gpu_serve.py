@@ -634,6 +634,54 @@ def test_chunk_queries_of_others_may_hold_anything(dtype, G):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,d,page,have,new", [
+    (4, 128, 16, 40, 200), (4, 128, 64, 3000, 300), (1, 64, 256, 3, 300), (7, 128, 32, 100, 80), (3, 64, 16, 2000, 90), (8, 128, 16, 126, 5)])
+def test_chunk_tokens_behind_a_row_may_hold_anything(dtype, G, d, page, have, new):
+    """What is not finite in a new token's values reaches the rows that see it, in its dims, and no other bit; the same
+    of keys, whose rows are NaN."""
+    import torch
+    k = Chunk(dtype, 1, 2, G, d, page, [have], [new], seed=21)
+    start = k.weight.clone()
+    clean, first = k.run().clone(), k.weight.clone()
+    pool_k, pool_v = k.kp.clone(), k.vp.clone()
+
+    def place(j):
+        return k.table[0, (have + j) // page].item(), (have + j) % page
+
+    h, dim, inf = 1, d // 2 + 5, float("inf")
+    rows = torch.arange(new, device="cuda")
+    for j in sorted({1, 2, new // 2, new - 2, new - 1}):
+        for bad in (float("nan"), inf, -inf):
+            k.vp = pool_v.clone()
+            pg, at = place(j)
+            k.vp[pg, h, at, dim] = bad
+            k.weight.copy_(start)
+            out = k.run().clone()
+            want = clean.clone()
+            want[rows >= j, h * G:(h + 1) * G, dim] = bad
+            same = (out == want) | (torch.isnan(out) & torch.isnan(want))
+            assert same.all(), (j, bad, int((~same).sum()))
+            assert torch.equal(k.weight, first)
+    a, b = 1, new - 2  # of both signs: infinite between them, NaN behind
+    k.vp = pool_v.clone()
+    for j, bad in ((a, inf), (b, -inf)):
+        pg, at = place(j)
+        k.vp[pg, h, at, dim] = bad
+    k.weight.copy_(start)
+    out = k.run().clone()
+    hit = out[:, h * G:(h + 1) * G, dim].float()
+    assert torch.equal(out[:a], clean[:a]) and (hit[a:b] == inf).all() and torch.isnan(hit[b:]).all()
+    k.vp, k.kp = pool_v, pool_k.clone()
+    pg, at = place(new // 2)
+    k.kp[pg, h, at] = float("nan")
+    k.run(False)
+    assert torch.equal(k.out[:new // 2], clean[:new // 2])
+    assert torch.isnan(k.out[new // 2:, h * G:(h + 1) * G].float()).all()
+    assert torch.equal(k.out[:, :h * G], clean[:, :h * G])
+    assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_chunk_no_tokens_at_all(dtype):
     import torch
     k = Chunk(dtype, 3, 2, 2, 64, 16, [40, 0, 20], [0, 0, 0], seed=8, pad=9)
@@ -687,7 +735,7 @@ def test_chunk_long_cache(dtype, d, G, page):
 
 @pytest.mark.parametrize("dtype,G", [("bf16", 4), ("bf16", 1), ("f32", 8)])
 def test_chunk_weights_of_few_rows_either_way(dtype, G):
-    """Sequences of up to eight rows have their logits kept for the weights, where a batch's logits are not too many: a
+    """Sequences of few rows have their logits kept for the weights, where a batch's logits are not too many: a
     table of many more entries, and the second pass works them out again."""
     import torch
     from kv_cache_token_tip_gb300 import fasa_paged_chunk_attention, fasa_paged_chunk_workspace_size
@@ -714,6 +762,18 @@ def test_chunk_weights_of_few_rows_either_way(dtype, G):
     got = k.weight - start
     assert ((weight[:, :, :k.cap] - k.weight).abs() <= 64 * U * got.abs() + 8 * U * k.weight + 1e-30).all()
     assert not weight[:, :, k.cap:].any()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,new", [(1, [15, 16, 17, 1]), (4, [3, 4, 5, 1]), (8, [1, 2, 3, 0]), (3, [5, 6, 2, 1]), (5, [3, 4, 1, 2])])
+def test_chunk_weights_around_few_rows(dtype, G, new):
+    """Weights of sequences on both sides of the number of rows up to which logits are kept, some cut into parts."""
+    for d, page, have in ((128, 16, [500, 130, 0, 64]), (64, 256, [1, 2000, 700, 255])):
+        k = Chunk(dtype, 4, 2, G, d, page, have, new, seed=31)
+        before = k.weight.cpu().numpy().astype(np.float64)
+        k.run()
+        assert status() == 0
+        k.check(before)
 
 
 def test_offsets_past_32_bits():
