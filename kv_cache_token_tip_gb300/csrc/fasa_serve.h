@@ -83,8 +83,11 @@ struct ChunkShape {
 };
 // A sequence is light with this many rows (new tokens times the heads of a group) or fewer: its
 // logits are kept for the weights, 16 bytes a slot for 4 rows instead of K's 256 again, where
-// those of the whole batch would take no more than CHUNK_LOGITS bytes.
-constexpr int CHUNK_LIGHT = 8;
+// those of the whole batch would take no more than CHUNK_LOGITS bytes.  With 4, 8 and 16 rows,
+// groups of 4 heads, bf16: 16 sequences of 8000 tokens with 1 new one 111, 113 and 115 us, with 2
+// 204, 117 and 120, with 4 207, 206 and 132; fp32, 1039, 1040 and 1044, 1524, 1278 and 1282,
+// 1527, 1525 and 1301.
+constexpr int CHUNK_LIGHT = 16;
 constexpr long long CHUNK_LOGITS = 512ll << 20;
 inline ChunkShape chunk_shape(bool bf16, int G) { return bf16 ? ChunkShape{2 * (128 / G), 128, 1} : ChunkShape{128 / G, 64, 1}; }
 
