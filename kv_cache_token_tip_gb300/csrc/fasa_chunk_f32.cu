@@ -7,9 +7,11 @@
 // operands' loads need too).  A warp of its own copies (TMA boxes of a page's rows); no warp
 // waits for another's rows, so that one's softmax is hidden by the others' products.  K of
 // the next tile is on its way while P V is worked out, V while Q K^T is.  Bound by the
-// products: two prompts of 1000 and 1500 tokens, 8 heads of 128 dims, 217 us, 39 TFLOP/s of
-// visible pairs, half of the FMA rate (with all warps in step and copying, 253 us; with
-// copies row by row, whose issue takes 3.5 us a tile, 227).
+// products: two prompts of 1000 and 1500 tokens, 8 heads of 128 dims, 232 us, 36.6 TFLOP/s of
+// visible pairs, half of the FMA rate.  O is summed a tile at a time and then over tiles: one
+// after another, 217 us, but 16384 slots are off by 2.0e-6 of the result instead of 6e-7.
+// (With such sums all warps in step and copying took 253 us, copies row by row, whose issue
+// takes 3.5 us a tile, 227.)
 #include <stdint.h>
 
 #include <algorithm>
@@ -230,10 +232,10 @@ __global__ void __launch_bounds__(CA_NT, 1)
             }
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-              const float w = exp2f(z[i][j] - ms);
-              l[i] += w;
-              ps[(8 * ty + i) * P::LP + tx + 16 * j] = w;
+              z[i][j] = exp2f(z[i][j] - ms);
+              ps[(8 * ty + i) * P::LP + tx + 16 * j] = z[i][j];
             }
+            l[i] += (z[i][0] + z[i][1]) + (z[i][2] + z[i][3]);
           }
           __syncwarp();  // (P's rows are read by the lanes that wrote them)
         }
@@ -242,6 +244,11 @@ __global__ void __launch_bounds__(CA_NT, 1)
         odd |= *not_all_finite;
         if (busy) {
           const char* v0 = vs + (tx >> 3) * (CF_K * 128);
+          uint64_t part[8][2 * E];  // of this tile
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2 * E; ++e) part[i][e] = 0;
 #pragma unroll 1
           for (int s8 = 0; s8 < CF_K; s8 += 8, v0 += 8 * 128) {
 #pragma unroll
@@ -262,13 +269,17 @@ __global__ void __launch_bounds__(CA_NT, 1)
                   const uint64_t w2 = pair_of(ws[s], ws[s]);
 #pragma unroll
                   for (int e = 0; e < E; ++e) {
-                    o[i][2 * e] = fma2(w2, v[s][e].x, o[i][2 * e]);
-                    o[i][2 * e + 1] = fma2(w2, v[s][e].y, o[i][2 * e + 1]);
+                    part[i][2 * e] = fma2(w2, v[s][e].x, part[i][2 * e]);
+                    part[i][2 * e + 1] = fma2(w2, v[s][e].y, part[i][2 * e + 1]);
                   }
                 }
               }
             }
           }
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int e = 0; e < 2 * E; ++e) o[i][e] = add2(o[i][e], part[i][e]);
         }
         free_it(v_empty);
       }

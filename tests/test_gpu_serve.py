@@ -776,6 +776,23 @@ def test_chunk_weights_around_few_rows(dtype, G, new):
         k.check(before)
 
 
+def test_chunk_long_sums_in_fp32():
+    """Sums of P V over long caches: 64 slots at a time, then those.
+
+    A sum of n random terms is off by u / sqrt(3) sqrt(n / 2) of its size: sqrt(32) of that for a tile's 64 slots and
+    sqrt(128) for the 256 tiles of a cache, 5.8e-7 with u = 2^-24; flat weights (2^x and their sum) bring 1e-7 more, the
+    rounding of the result 3e-8.  One after another, 16384 slots would be off by 3.1e-6, cut in half 2.2e-6."""
+    import torch
+    k = Chunk("f32", 20, 8, 4, 128, 256, [16376] * 20, [8] * 20, seed=41, sigma=0.05)
+    k.run(False)
+    for b in (0, 9, 19):
+        ref, _ = reference(k, [b])
+        x0, x1 = k.cu_host[b], k.cu_host[b + 1]
+        err = (k.out[x0:x1].double() - ref[x0:x1]).norm() / ref[x0:x1].norm()
+        assert err <= 1e-6, f"{err:.3g}"
+    assert status() == 0
+
+
 def test_offsets_past_32_bits():
     """Pools of more than 2^32 elements, used at their far end by all the calls."""
     import torch
