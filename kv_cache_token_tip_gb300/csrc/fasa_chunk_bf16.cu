@@ -9,14 +9,14 @@
 // issues the matrix instructions, one that copies.  While the tensor cores work for one tile
 // of rows, the softmax of the other is worked out.
 //
-// Bound by the tensor cores where units are long: 2048 tokens behind 30720 take 598 us by
-// themselves, 1.78 PFLOP/s of visible pairs (tensor pipe 83% busy), and 685 to 730 one after
-// another, where the card's power bounds them.  Eight prompts of 37 to 4096 tokens 327 us
-// (68%): a unit's start and end, 5400 to 5800 clocks beside 2530 a tile.  Drafted tokens of 16
-// sequences 110 us, 5.8 TB/s.  What it took: instructions issued by one elected lane from
-// descriptors worked out ahead (742 -> 684 us for the first case; 670 clocks for eight
-// instructions before, 370 since), P handed over by halves and a row to a thread (598; half a
-// row to each of two warps 684), results by way of shared memory (eight prompts 372 -> 327).
+// Bound by the tensor cores where units are long: 2048 tokens behind 30720 take 600 us by
+// themselves (tensor pipe 81% busy), and 690 to 740 one after another, where the card's power
+// bounds them.  Eight prompts of 37 to 4096 tokens 298 us (64%): a unit's start and end cost 5400
+// to 5800 clocks beside 2530 a tile (in a traced build).  Drafted tokens of 16 sequences 112 us,
+// 5.7 TB/s.  What it took: instructions issued by one elected lane from descriptors worked out ahead (742 -> 684 us
+// for the first case), P handed over by halves and a row to a thread (598; half a row to each of
+// two warps 684), results by way of shared memory (eight prompts 372 -> 327), what a unit costs
+// (below).
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
