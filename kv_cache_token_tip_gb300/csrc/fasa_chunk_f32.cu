@@ -461,12 +461,15 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_weight_f32_kernel(const __grid
       if (i + 1 < tiles) fetch(i + 1);
       const float* lse = reinterpret_cast<const float*>(sm + P::W_LSE) + (i & 1) * CF_M;
       float z[8][4];
-      if (tid / 32 * 16 >= min(TU, u.q.n - i * TU) * p.G) continue;  // no rows of this warp
+      const int rows = min(TU, u.q.n - i * TU) * p.G;
+      if (tid / 32 * 16 >= rows) continue;  // no rows of this warp
       products<D>(sm + P::W_Q + (i & 1) * P::Q_BYTES, ks, z);
       float part[4] = {};
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        const int see = a + i * TU + (8 * ty + r) / p.G;  // the last slot that this row sees
+        // the last slot that this row sees (none of one that there is not: its queries of 0 times an
+        // infinite key are NaN)
+        const int see = 8 * ty + r < rows ? a + i * TU + (8 * ty + r) / p.G : -1;
         const float x = lse[8 * ty + r];
 #pragma unroll
         for (int j = 0; j < 4; ++j) part[j] += u.t0 + tx + 16 * j <= see ? exp2f(z[r][j] * p.scale - x) : 0.f;

@@ -1,0 +1,81 @@
+"""The attention of chunks where keys, logits and values are not finite, against the
+fp64 oracle on the same stored values.
+
+Bounds as in test_gpu_serve.py; the logits' scale A is that of the finite elements: a
+logit of -inf or NaN is exact.
+"""
+
+import numpy as np
+import pytest
+
+from oracle import serve_oracle as SO
+from tests.gpu_util import ensure_built
+from tests.test_gpu_serve import E, U, Chunk, status
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built(cuda_ok):
+    ensure_built()
+
+
+def key(k, b, h, slot):
+    """A slot's key, to be written."""
+    return k.kp[k.table[b, slot // k.page].long(), h, slot % k.page]
+
+
+def check(k, before):
+    """out and the weights, NaN where the definition gives NaN and nowhere else."""
+    lens, table = k.lens.cpu().numpy(), k.table.cpu().numpy()
+    q, kp, vp = k.host(k.q), k.host(k.kp), k.host(k.vp)
+    with np.errstate(invalid="ignore"):
+        ref, got, _, pv = SO.chunk_attention(q, k.cu_host, kp, vp, table, lens)
+    _, _, A, _ = SO.chunk_attention(q, k.cu_host, np.where(np.isfinite(kp), kp, 0.0), vp, table, lens)
+    T = np.zeros((k.n, 1))
+    for b in range(k.B):
+        T[k.cu_host[b]:k.cu_host[b + 1]] = lens[b]
+    rel = 2 * (2 * k.d + 16) * U * A + (16 + T + 64) * U
+    bound = (rel + (2.0 ** -8 if k.dtype == "bf16" else 0.0) + 2 * (T + 64) * U)[..., None] * pv + E[k.dtype] * np.abs(ref)
+    out = k.host(k.out)
+    assert np.array_equal(np.isnan(out), np.isnan(ref))
+    fine = ~np.isnan(ref)
+    assert np.all(np.abs(out - ref)[fine] <= bound[fine] + 1e-30)
+    after, want = k.weight.cpu().numpy().astype(np.float64), before + got
+    assert np.array_equal(np.isnan(after), np.isnan(want))
+    for b in range(k.B):
+        x0, x1 = k.cu_host[b], k.cu_host[b + 1]
+        relw = (rel[x0:x1].max() if x1 > x0 else 0.0) + ((x1 - x0) * k.G + 64) * U
+        fine = ~np.isnan(want[b])
+        lim = relw * got[b][fine] + 2 * U * np.abs(want[b][fine])
+        assert np.all(np.abs(after[b] - want[b])[fine] <= lim)
+        none = got[b] == 0
+        assert np.array_equal(after[b][none], before[b][none])
+    return ref, got
+
+
+# dtype, B, Hkv, G, d, page, tokens before, new tokens: few rows (their logits are kept), rows that are no
+# multiple of a warp's, more rows than a tile's, caches that are cut into parts
+CASES = [("f32", 2, 2, 1, 64, 16, [40, 90], [17, 31]), ("f32", 1, 1, 4, 128, 32, [200], [5]), ("f32", 1, 2, 3, 64, 64, [7], [9]),
+         ("f32", 2, 1, 1, 128, 16, [64, 700], [130, 19]), ("f32", 1, 2, 4, 64, 16, [300], [3]), ("f32", 1, 1, 8, 64, 16, [3000], [20]),
+         ("bf16", 2, 2, 1, 64, 16, [40, 90], [17, 31]), ("bf16", 1, 1, 4, 128, 32, [200], [5]), ("bf16", 1, 2, 3, 64, 64, [7], [9]),
+         ("bf16", 2, 1, 1, 128, 16, [64, 700], [300, 19]), ("bf16", 1, 2, 4, 64, 16, [300], [3]), ("bf16", 1, 1, 8, 128, 16, [3000], [40])]
+NAMES = [f"{c[0]}-B{c[1]}h{c[2]}g{c[3]}d{c[4]}-{max(c[6])}+{max(c[7])}" for c in CASES]
+
+
+@pytest.mark.parametrize("c", CASES, ids=NAMES)
+@pytest.mark.parametrize("sign", [1, -1])
+def test_infinite_keys_of_no_weight(c, sign):
+    """An infinite element of a key that all rows see, their queries of the other sign there: the logit is -inf, its
+    weight 0, and everything else as if the slot were not there."""
+    k = Chunk(*c, seed=51)
+    dim, inf = k.d // 2 + 1, float("inf")
+    k.q[:, :, dim] = -sign * (k.q[:, :, dim].abs() + 0.25)
+    for b in range(k.B):
+        for h in range(k.Hkv):
+            key(k, b, h, 3 + h)[dim] = sign * inf
+    before = k.weight.cpu().numpy().astype(np.float64)
+    k.run()
+    ref, got = check(k, before)
+    assert np.all(np.isfinite(ref)) and np.all(np.isfinite(got)) and np.all(got[:, 0, 3] == 0)
+    assert status() == 0
