@@ -23,6 +23,7 @@
 
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "fasa_chunk.cuh"
 #include "fasa_tcgen05.cuh"
@@ -681,11 +682,6 @@ __global__ void __launch_bounds__(CW_NT, 1)
           if (lane == 0) mbar_arrive(t_empty + 8 * buf);
           // the rows of this tile that there are, and of them the first that sees the slot
           const int rows = min(TQ, u.q.n - i * TQ) * p.G, lo = (slot - (u.q.len - u.q.n) - i * TQ) * p.G - 64 * half;
-          if (rows < TQ * p.G || __any_sync(0xffffffffu, lo > 0)) {
-#pragma unroll
-            for (int x = 0; x < 64; ++x)
-              if (x < lo || x >= rows - 64 * half) s[x] = 0xff800000u;  // -inf
-          }
           // (columns behind a tile's rows hold anything; a tile has 125 rows or more)
 #pragma unroll
           for (int x = 61; x < 64; ++x)
@@ -693,15 +689,25 @@ __global__ void __launch_bounds__(CW_NT, 1)
           const uint64_t scale2 = pair_of(scale, scale);
           const float4* l4 = reinterpret_cast<const float4*>(lse + 128 * st + 64 * half);  // (negative log-sums)
           uint64_t sum[2] = {0, 0};
+          // edge: some rows are masked, behind the sum with their log-sum, which may be NaN
+          auto add = [&](auto edge) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            const float4 l = l4[x];
-            float a0, a1, b0, b1;
-            unpair(fma2(pair_of(__uint_as_float(s[4 * x]), __uint_as_float(s[4 * x + 1])), scale2, pair_of(l.x, l.y)), a0, a1);
-            unpair(fma2(pair_of(__uint_as_float(s[4 * x + 2]), __uint_as_float(s[4 * x + 3])), scale2, pair_of(l.z, l.w)), b0, b1);
-            sum[0] = add2(sum[0], pair_of(ex2(a0), ex2(a1)));
-            sum[1] = add2(sum[1], pair_of(ex2(b0), ex2(b1)));
-          }
+            for (int x = 0; x < 16; ++x) {
+              const float4 l = l4[x];
+              float y[4];
+              unpair(fma2(pair_of(__uint_as_float(s[4 * x]), __uint_as_float(s[4 * x + 1])), scale2, pair_of(l.x, l.y)), y[0], y[1]);
+              unpair(fma2(pair_of(__uint_as_float(s[4 * x + 2]), __uint_as_float(s[4 * x + 3])), scale2, pair_of(l.z, l.w)), y[2], y[3]);
+              if constexpr (decltype(edge)::value) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (4 * x + e < lo || 4 * x + e >= rows - 64 * half) y[e] = -INFINITY;
+              }
+              sum[0] = add2(sum[0], pair_of(ex2(y[0]), ex2(y[1])));
+              sum[1] = add2(sum[1], pair_of(ex2(y[2]), ex2(y[3])));
+            }
+          };
+          if (rows < TQ * p.G || __any_sync(0xffffffffu, lo > 0)) add(std::true_type());
+          else add(std::false_type());
           float a, b;
           unpair(add2(sum[0], sum[1]), a, b);
           total += a + b;

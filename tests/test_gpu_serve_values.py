@@ -79,3 +79,46 @@ def test_infinite_keys_of_no_weight(c, sign):
     ref, got = check(k, before)
     assert np.all(np.isfinite(ref)) and np.all(np.isfinite(got)) and np.all(got[:, 0, 3] == 0)
     assert status() == 0
+
+
+@pytest.mark.parametrize("c", CASES, ids=NAMES)
+def test_an_infinite_logit(c):
+    """One token's head has a logit of +inf (the others -inf there): its row is NaN, and so are the weights of all slots
+    that it sees, of its KV head; those behind them are not."""
+    k = Chunk(*c, seed=52)
+    dim, b, h, inf = k.d // 2 + 1, k.B - 1, k.Hkv - 1, float("inf")
+    n = k.cu_host[b + 1] - k.cu_host[b]
+    j = n // 3
+    k.q[:, :, dim] = -(k.q[:, :, dim].abs() + 0.25)
+    k.q[k.cu_host[b] + j, h * k.G + k.G // 2, dim] = 0.5
+    key(k, b, h, 2)[dim] = inf
+    before = k.weight.cpu().numpy().astype(np.float64)
+    k.run()
+    ref, got = check(k, before)
+    rows = np.isnan(ref).all(axis=2)
+    assert rows.sum() == 1 and rows[k.cu_host[b] + j, h * k.G + k.G // 2]
+    see = int(k.lens[b]) - n + j + 1
+    assert np.isnan(got[b, h, :see]).all() and not np.isnan(got[b, h, see:]).any() and np.isnan(got).sum() == see
+    assert status() == 0
+
+
+@pytest.mark.parametrize("c", CASES, ids=NAMES)
+def test_weights_of_a_key_that_is_nan(c):
+    """A new token's key is NaN in one head: the rows that see it give NaN, out and weights, in that head alone."""
+    k = Chunk(*c, seed=53)
+    b, h = k.B - 1, 0
+    n = k.cu_host[b + 1] - k.cu_host[b]
+    start = k.weight.clone()
+    k.run()
+    first = k.weight.clone()
+    k.weight.copy_(start)
+    key(k, b, h, int(k.lens[b]) - n + n // 2)[:] = float("nan")
+    before = k.weight.cpu().numpy().astype(np.float64)
+    k.run()
+    ref, got = check(k, before)
+    assert np.isnan(got[b, h, :int(k.lens[b])]).all() and np.isnan(got).sum() == int(k.lens[b])
+    for i in range(k.B):
+        for g in range(k.Hkv):
+            if (i, g) != (b, h):
+                assert bool((k.weight[i, g] == first[i, g]).all())
+    assert status() == 0
