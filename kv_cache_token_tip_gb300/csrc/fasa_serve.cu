@@ -189,9 +189,10 @@ int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64
   if (st) return st;
   if (n_tokens < 0) return FASA_ERR_INVALID_ARG;
   if (n_tokens > ASSIGN_MAX_TOKENS) return FASA_ERR_UNSUPPORTED;
+  if (n_tokens == 0) return FASA_OK;  // (tensors without rows have no addresses)
   if (!q != !q_out || !k != !v || !k != !k_pages || !k != !v_pages || (!k && (weight || token_pos)))
     return FASA_ERR_INVALID_ARG;
-  if (n_tokens == 0 || (!q && !k)) return FASA_OK;
+  if (!q && !k) return FASA_OK;
   if (!token_map) return FASA_ERR_INVALID_ARG;
   for (const void* x : {q, k, v, (const void*)token_map, (const void*)q_out, (const void*)k_pages, (const void*)v_pages,
                         (const void*)weight, (const void*)token_pos})
