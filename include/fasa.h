@@ -584,7 +584,8 @@ int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64
  * not ascend from 0 within n_tokens sets FASA_DEV_BAD_INPUT; a sequence whose range is
  * not within n_tokens is left out.  rope_theta of dims is not used.
  * workspace: at least fasa_paged_chunk_workspace_size bytes of device memory, its contents
- * not kept and not read; calls that may overlap need one each.
+ * not kept and not read; calls that may overlap need one each.  A larger batch, a wider table
+ * or more tokens never need less, so that one of the largest call serves all smaller ones.
  * Aligned to 16 bytes: q, k_pages, v_pages, out, weight, workspace.  out lies apart from q.
  * n_tokens <= 2^20.
  */

@@ -62,12 +62,15 @@ struct ChunkRow {
   }
 };
 
-// Whether a sequence's logits are kept (those of its head h at chunk_logits).
-__device__ __forceinline__ bool chunk_light(const ChunkParams& p, const ChunkSeq& q) {
-  return p.logits && q.n * p.G <= CHUNK_LIGHT;
+// Whether the logits of sequence b are kept (those of its head h at chunk_logits, row after row).
+__device__ __forceinline__ int light_row(const ChunkParams& p, int b, const ChunkSeq& q) {
+  return p.logits_by_token ? q.first * p.G : b * CHUNK_LIGHT;
 }
-__device__ __forceinline__ float* chunk_logits(const ChunkParams& p, int b, int h) {
-  return p.logits + ((size_t)b * p.Hkv + h) * CHUNK_LIGHT * p.T_pad;
+__device__ __forceinline__ bool chunk_light(const ChunkParams& p, int b, const ChunkSeq& q) {
+  return p.logits && q.n * p.G <= CHUNK_LIGHT && light_row(p, b, q) + q.n * p.G <= p.logit_rows;
+}
+__device__ __forceinline__ float* chunk_logits(const ChunkParams& p, int b, int h, const ChunkSeq& q) {
+  return p.logits + ((size_t)light_row(p, b, q) * p.Hkv + (size_t)h * q.n * p.G) * p.T_pad;
 }
 
 // log2 of a row's sum: infinity where it saw nothing (its weights are 0), NaN where one of its
@@ -293,7 +296,7 @@ __device__ void weight_line(const ChunkParams& p, int* before, int3* scan, int T
     few[b] = sum.y;
     light[b] = sum.z;
     const ChunkSeq q = line.sequence(b, &bad);
-    if (q.n > 0 && chunk_light(p, q)) sum.z += (q.len + WEIGHT_PIECE - 1) / WEIGHT_PIECE;
+    if (q.n > 0 && chunk_light(p, b, q)) sum.z += (q.len + WEIGHT_PIECE - 1) / WEIGHT_PIECE;
     else if (q.n > TQ) sum.x += (q.len + SLOTS - 1) / SLOTS;
     else if (q.n > 0) sum.y += (q.len + SLOTS - 1) / SLOTS;
   }
@@ -394,7 +397,7 @@ __device__ void weight_light(const ChunkParams& p, const int* light) {
     if (t < q.len) {
       const int page = p.page_table[(size_t)b * p.max_pages + (t >> p.log2_page)];
       if (page < 0 || page >= p.n_pages) continue;
-      const float* z = chunk_logits(p, b, h) + t;
+      const float* z = chunk_logits(p, b, h, q) + t;
       const float* lse = p.lse + ((size_t)h * p.n_tokens + q.first) * p.G;
       float4 zr[CHUNK_LIGHT];
       float l[CHUNK_LIGHT];

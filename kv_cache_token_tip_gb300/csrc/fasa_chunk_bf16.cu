@@ -178,7 +178,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
           return lane < 8 && slot < q.len ? table[slot >> p.log2_page] : 0;
         };
         int page = f0 < e ? look_up(f0) : 0;
-        float* keep = live && chunk_light(p, q) ? chunk_logits(p, u.b, u.h) + (size_t)row * p.T_pad : nullptr;
+        float* keep = live && chunk_light(p, u.b, q) ? chunk_logits(p, u.b, u.h, q) + (size_t)row * p.T_pad : nullptr;
         float m = -INFINITY;
         uint64_t l2 = 0;  // two sums
         for (int t = f0; t < e; ++t) {

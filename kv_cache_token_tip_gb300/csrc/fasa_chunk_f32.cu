@@ -198,8 +198,8 @@ __global__ void __launch_bounds__(CA_NT, 1)
         }
         free_it(k_empty);
         if (t + 1 == f1) free_it(q_empty);
-        if (busy && chunk_light(p, u.q)) {
-          float* keep = chunk_logits(p, u.b, u.h) + t0 + tx;
+        if (busy && chunk_light(p, u.b, u.q)) {
+          float* keep = chunk_logits(p, u.b, u.h, u.q) + t0 + tx;
 #pragma unroll 1
           for (int i = 0; 8 * ty + i < rows && i < 8; ++i)
             for (int j = 0; j < 4; ++j) {

@@ -118,10 +118,17 @@ void chunk_plan(const fasa_paged_dims_t* d, int n_tokens, int sms, int* rows, in
 
 size_t notes_bytes(int parts) { return 256 + up((size_t)parts * 2 * sizeof(int4)); }  // and the queue
 int padded_slots(const fasa_paged_dims_t* d) { return (d->max_pages * d->page_size + 127) / 128 * 128; }
+// Rows of the light sequences' logits, were they all kept, and whether they lie by token.
+long long light_rows(const fasa_paged_dims_t* d, int n_tokens, bool* by_token) {
+  const long long tokens = (long long)n_tokens * (d->n_q_heads / d->n_kv_heads), all = (long long)d->batch * CHUNK_LIGHT;
+  *by_token = tokens < all;
+  return std::min(tokens, all);
+}
+long long logit_row_bytes(const fasa_paged_dims_t* d) { return (long long)d->n_kv_heads * padded_slots(d) * 4; }
 // Logits of the light sequences, where there is a second pass that reads them.
-size_t logits_bytes(const fasa_paged_dims_t* d) {
-  const long long n = (long long)d->batch * d->n_kv_heads * CHUNK_LIGHT * padded_slots(d) * 4;
-  return n <= CHUNK_LOGITS ? up((size_t)n) : 0;
+size_t logits_bytes(const fasa_paged_dims_t* d, int n_tokens) {
+  bool by_token;
+  return up((size_t)std::min(light_rows(d, n_tokens, &by_token) * logit_row_bytes(d), CHUNK_LOGITS));
 }
 size_t records_bytes(int rows, int parts, int D) { return up((size_t)parts * 2 * rows * (D + 2) * 4); }
 
@@ -256,7 +263,7 @@ int fasa_paged_chunk_workspace_size(const fasa_paged_dims_t* dims, int32_t n_tok
   int rows, parts;  // (of any device)
   chunk_plan(dims, n_tokens, CHUNK_MAX_SMS, &rows, &parts);
   *bytes = notes_bytes(parts) + records_bytes(rows, parts, dims->head_dim);
-  if (with_weight) *bytes += logits_bytes(dims) + up((size_t)n_tokens * dims->n_q_heads * 4);
+  if (with_weight) *bytes += logits_bytes(dims, n_tokens) + up((size_t)n_tokens * dims->n_q_heads * 4);
   return FASA_OK;
 }
 
@@ -307,8 +314,9 @@ int fasa_paged_chunk_attention(const void* q, int32_t n_tokens, const int32_t* c
   p.records = reinterpret_cast<float*>(ws);
   ws += records_bytes(p.rows, p.parts, dims->head_dim);
   p.T_pad = padded_slots(dims);
-  p.logits = weight && logits_bytes(dims) ? reinterpret_cast<float*>(ws) : nullptr;
-  p.lse = reinterpret_cast<float*>(ws + (weight ? logits_bytes(dims) : 0));
+  p.logits = weight ? reinterpret_cast<float*>(ws) : nullptr;
+  p.logit_rows = (int)std::min(light_rows(dims, n_tokens, &p.logits_by_token), CHUNK_LOGITS / logit_row_bytes(dims));
+  p.lse = reinterpret_cast<float*>(ws + (weight ? logits_bytes(dims, n_tokens) : 0));
   p.status = status;
   p.wait_ns = wait_limit_ns();
   p.drop_tile = dropped_copy();

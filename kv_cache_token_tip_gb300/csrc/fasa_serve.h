@@ -64,7 +64,9 @@ struct ChunkParams {
   float scale;     // log2(e) / sqrt(d): logits are kept in powers of two
   float* records;  // [parts][2][rows * (d + 2)]: o [rows][d], m [rows], l [rows]
   int4* notes;     // [parts][2]: whose the records are
-  float* logits;   // [B * Hkv][CHUNK_LIGHT][T_pad] of sequences of few rows; null: not kept
+  float* logits;   // [logit_rows][Hkv] of T_pad, those of sequences of few rows; null: not kept
+  int logit_rows;  // that there is room for
+  bool logits_by_token;  // a token has the rows of its own place; else a sequence has CHUNK_LIGHT
   int T_pad;       // T_cap in whole tiles of slots
   int* queue;      // the next unit of the weights' pass (the first kernel sets it to 0)
   float* lse;      // [Hkv][n_tokens * G]
@@ -82,13 +84,15 @@ struct ChunkShape {
   int tokens, tile, per_sm;
 };
 // A sequence is light with this many rows (new tokens times the heads of a group) or fewer: its
-// logits are kept for the weights, 16 bytes a slot for 4 rows instead of K's 256 again, where
-// those of the whole batch would take no more than CHUNK_LOGITS bytes.  With 4, 8 and 16 rows,
+// logits are kept for the weights, 16 bytes a slot for 4 rows instead of K's 256 again, as far as
+// CHUNK_LOGITS bytes go: the first sequences' then, so that a larger batch or table never needs a
+// smaller workspace.  Room is for the tokens' rows, or for CHUNK_LIGHT a sequence where that is
+// less (a step with prompts).  With 4, 8 and 16 rows,
 // groups of 4 heads, bf16: 16 sequences of 8000 tokens with 1 new one 111, 113 and 115 us, with 2
 // 204, 117 and 120, with 4 207, 206 and 132; fp32, 1039, 1040 and 1044, 1524, 1278 and 1282,
 // 1527, 1525 and 1301.
 constexpr int CHUNK_LIGHT = 16;
-constexpr long long CHUNK_LOGITS = 512ll << 20;
+constexpr long long CHUNK_LOGITS = 480ll << 20;
 inline ChunkShape chunk_shape(bool bf16, int G) { return bf16 ? ChunkShape{2 * (128 / G), 128, 1} : ChunkShape{128 / G, 64, 1}; }
 
 cudaError_t launch_paged_assign(const AssignParams& p, int sms, cudaStream_t s);

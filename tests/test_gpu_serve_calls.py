@@ -35,3 +35,35 @@ def test_steps_without_new_tokens(dtype):
                                dims=k.dims)
     assert status() == 0
     assert all(torch.equal(x, y) for x, y in zip((k.kp, k.vp, k.weight, token_pos), before))
+
+
+@pytest.mark.parametrize("dtype,G,tokens", [("bf16", 4, (4,)), ("bf16", 4, (3,)), ("f32", 8, (2, 0, 1)), ("bf16", 2, (8, 1, 9, 0, 300)),
+                                            ("f32", 1, (16, 17))])
+def test_weights_where_the_logits_of_some_sequences_are_kept(dtype, G, tokens):
+    """Under a table of many entries there is room for the logits of the first sequences alone; the others' are worked
+    out again.  Sequences and slots as under a narrow table."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_chunk_attention, fasa_paged_chunk_workspace_size
+    B, Hkv, d, page, wide = 64, 8, 64, 16, 4000
+    rng = np.random.default_rng(G)
+    k = Chunk(dtype, B, Hkv, G, d, page, [int(x) for x in rng.integers(0, 400, B)], [tokens[b % len(tokens)] for b in range(B)],
+              seed=62)
+    start = k.weight.clone()
+    out = k.run().clone()
+    rows = min(k.n * G, 16 * B)
+    assert rows * Hkv * wide * page * 4 > 480 << 20 > rows * Hkv * (k.cap + 128) * 4
+    table = torch.full((B, wide), -1, dtype=torch.int32, device="cuda")
+    table[:, :k.table.shape[1]] = k.table
+    weight = torch.zeros((B, Hkv, wide * page), device="cuda")
+    weight[:, :, :k.cap] = start
+    dims = paged_dims(dtype, B, Hkv, G, d, page, k.kp.shape[0], wide)
+    size = fasa_paged_chunk_workspace_size(dims, k.n, True)
+    room = torch.full((size + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+    fasa_paged_chunk_attention(k.q, k.kp, k.vp, table, k.lens, k.out, cu_new=k.cu, weight=weight, workspace=room[:size],
+                               dims=dims)
+    assert status() == 0 and torch.equal(k.out, out)
+    assert (room[size:] == 0x5a).all()
+    # the same logits, summed in another order: 16 u of each exp2, a sum of up to 300 G terms, and u of the weight
+    u, got = 2.0 ** -24, (k.weight - start).abs()
+    assert ((weight[:, :, :k.cap] - k.weight).abs() <= (32 + max(tokens) * G) * u * got + 8 * u * k.weight + 1e-30).all()
+    assert not weight[:, :, k.cap:].any()

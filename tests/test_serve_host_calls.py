@@ -23,3 +23,36 @@ def test_calls_without_rows(L):
     # the dims and the rotation are looked at all the same
     assert _rope(L, _dims(batch=0), r, n=0) == 1 and _rope(L, d, FasaRope(rotary_dim=24), n=0) == 1
     assert _rope(L, d, r, n=5, q=None) == 1 and _rope(L, d, r, n=5, k=None, v=None) == 1
+
+
+def _size(L, d, n_tokens, weights):
+    n = ctypes.c_size_t(0)
+    assert L.fasa_paged_chunk_workspace_size(ctypes.byref(d), n_tokens, weights, ctypes.byref(n)) == 0
+    return n.value
+
+
+@pytest.mark.parametrize("weights", [0, 1])
+@pytest.mark.parametrize("kw", [dict(), dict(dtype=0, head_dim=64), dict(n_q_heads=56), dict(n_q_heads=8),
+                                dict(n_q_heads=128, n_kv_heads=64, head_dim=64)])
+def test_a_workspace_serves_every_smaller_call(L, kw, weights):
+    """The size does not fall as the batch, the table or the tokens grow."""
+    batches, tables, tokens = (1, 2, 50, 100, 200, 700, 1000), (1, 31, 100, 512, 2000, 16384), (1, 4, 50, 200, 1024, 100000)
+    size = {(b, t, n): _size(L, _dims(batch=b, max_pages=t, **kw), n, weights) for b in batches for t in tables for n in tokens}
+    for axis, values in enumerate((batches, tables, tokens)):
+        for at, s in size.items():
+            i = values.index(at[axis])
+            if i + 1 < len(values):
+                more = list(at)
+                more[axis] = values[i + 1]
+                assert s <= size[tuple(more)], (at, more)
+
+
+def test_workspace_has_room_for_the_rows_that_there_are(L):
+    """Kept logits: by the new tokens' rows where they are few (a decode step), by 16 rows a sequence where not, half a
+    GB at most."""
+    for batch, n, rows in ((32, 32, 32 * 4), (32, 64, 64 * 4), (32, 100, 400), (32, 5000, 32 * 16), (1, 1, 4)):
+        d = _dims(batch=batch, max_pages=512)  # 8192 slots
+        log_sums = -(-n * 32 * 4 // 256) * 256
+        assert _size(L, d, n, 1) - _size(L, d, n, 0) == rows * 8 * 8192 * 4 + log_sums
+    d = _dims(batch=2000, max_pages=16384)
+    assert _size(L, d, 2000, 1) - _size(L, d, 2000, 0) == (480 << 20) + 2000 * 32 * 4
