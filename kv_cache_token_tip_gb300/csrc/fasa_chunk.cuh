@@ -144,6 +144,20 @@ __device__ __forceinline__ void note_record(const ChunkParams& p, int c, const C
                                          f0 > 0 && f1 == u.tiles ? 3 : 1);
 }
 
+// What is not finite among E elements of row r from d on, added up over the n parts without their
+// factors (one that is too small for a number would make NaN of infinity), to the row's result.
+template <int D, int E, typename T>
+__device__ __noinline__ void join_not_finite(const ChunkParams& p, const int* parts, int n, int r, int d, T* to) {
+  for (int e = 0; e < E; ++e) {
+    float sum = 0.f;
+    for (int i = 0; i < n; ++i) {
+      const float x = ld_cg(chunk_record(p, D, parts[i], i == 0) + (size_t)r * D + d + e);
+      if (not_finite(x)) sum += x;
+    }
+    if (not_finite(sum)) put(to + e, sum);
+  }
+}
+
 // The units that were cut: block x takes the unit that goes on behind part x, if there is
 // one, its warps the rows.  The parts of a row are added in part order.
 constexpr int CJ_NT = 256;
@@ -218,6 +232,10 @@ __global__ void __launch_bounds__(CJ_NT) chunk_join_kernel(const __grid_constant
     if constexpr (E == 4) store4<T>(to, o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv);
     else if constexpr (sizeof(T) == 2) *reinterpret_cast<uint32_t*>(to) = pack_bf16(o[0] * inv, o[1] * inv);
     else *reinterpret_cast<float2*>(to) = make_float2(o[0] * inv, o[1] * inv);
+    float any = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) any += o[e];
+    if (not_finite(any)) join_not_finite<D, E>(p, parts, n, r, E * lane, to);
     if (p.weight && lane == 0) p.lse[((size_t)(head / p.G) * p.n_tokens + token) * p.G + head % p.G] = chunk_lse(M, L);
   }
 }

@@ -122,3 +122,32 @@ def test_weights_of_a_key_that_is_nan(c):
             if (i, g) != (b, h):
                 assert bool((k.weight[i, g] == first[i, g]).all())
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype,G,d", [("bf16", 4, 128), ("bf16", 1, 64), ("f32", 4, 64), ("f32", 2, 128)])
+def test_infinite_values_in_a_cache_that_is_cut(dtype, G, d):
+    """An early slot's logits lie hundreds of powers of two above all others', so that the weight of a new token's value,
+    in another part of the cache, is below the smallest number: an infinite or NaN value reaches the rows that see it
+    all the same, whatever lies in between, and no others."""
+    import torch
+    have, new, page, inf = 8000, 12, 32, float("inf")
+    k = Chunk(dtype, 1, 2, G, d, page, [have], [new], seed=54)
+    h, dim = 1, d // 2 + 5
+    k.q[..., 0] = 40.0
+    for slot in (10, 11):  # 40 * 100 / sqrt(d) >= 350 against a few times ten
+        key(k, 0, 0, slot)[0] = 100.0
+        key(k, 0, h, slot)[0] = 100.0
+    clean = k.run(False).clone()
+    assert torch.isfinite(clean).all()
+    pool = k.vp.clone()
+    rows = torch.arange(new, device="cuda")
+    for j in (1, new // 2, new - 1):
+        for bad in (inf, -inf, float("nan")):
+            k.vp = pool.clone()
+            k.vp[k.table[0, (have + j) // page].long(), h, (have + j) % page, dim] = bad
+            out = k.run(False).clone()
+            want = clean.clone()
+            want[rows >= j, h * G:(h + 1) * G, dim] = bad
+            same = (out == want) | (torch.isnan(out) & torch.isnan(want))
+            assert same.all(), (j, bad, int((~same).sum()))
+    assert status() == 0
