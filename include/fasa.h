@@ -575,14 +575,16 @@ int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64
  * seq_lens counts the new tokens: the j-th of the n of sequence b has slot
  * s = seq_lens[b] - n + j, and
  *   out[x] = softmax(q K^T / sqrt(d)) V over the slots 0 .. s   (storage dtype, rounded once);
- * zeros where there is none (s < 0).  What is not finite in the K or V of other slots reaches
- * no row.  With weight (not NULL):
+ * zeros where there is none (s < 0) or all logits are -inf.  What is not finite in the K or V
+ * of other slots reaches no row; a logit of +inf or NaN makes its row NaN, and the weights of
+ * the slots that it sees.  With weight (not NULL):
  *   weight[b,h,t] += sum over the new tokens and the group's heads of softmax_t.
  * bf16: the softmax weights that multiply V are rounded to bf16; their sum and what goes
  * to `weight` are not.  Equal calls give equal bits.
  * Rows at or behind cu_new[B] are padding: their `out` is left as it is.  A cu_new that does
  * not ascend from 0 within n_tokens sets FASA_DEV_BAD_INPUT; a sequence whose range is
- * not within n_tokens is left out.  rope_theta of dims is not used.
+ * not within n_tokens is left out.  Rows that two ranges hold get either's result, and the
+ * weights of such sequences are not defined.  rope_theta of dims is not used.
  * workspace: at least fasa_paged_chunk_workspace_size bytes of device memory, its contents
  * not kept and not read; calls that may overlap need one each.  A larger batch, a wider table
  * or more tokens never need less, so that one of the largest call serves all smaller ones.

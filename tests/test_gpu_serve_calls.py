@@ -67,3 +67,47 @@ def test_weights_where_the_logits_of_some_sequences_are_kept(dtype, G, tokens):
     u, got = 2.0 ** -24, (k.weight - start).abs()
     assert ((weight[:, :, :k.cap] - k.weight).abs() <= (32 + max(tokens) * G) * u * got + 8 * u * k.weight + 1e-30).all()
     assert not weight[:, :, k.cap:].any()
+
+
+BAD_ROWS = [
+    # cu_new, the ranges that it gives, and of those the sequences that share no row with another
+    ([0, 40, 45, 65, 99], {0: (0, 40), 1: (40, 45), 2: (45, 65)}, (0, 1, 2)),
+    ([5, 40, 45, 65, 68], {0: (5, 40), 1: (40, 45), 2: (45, 65), 3: (65, 68)}, (0, 1, 2, 3)),
+    ([-1, 40, 45, 65, 68], {1: (40, 45), 2: (45, 65), 3: (65, 68)}, (1, 2, 3)),
+    ([0, 40, 30, 65, 68], {0: (0, 40), 2: (30, 65), 3: (65, 68)}, (3,)),
+    ([0, 40, 45, 40, 68], {0: (0, 40), 1: (40, 45), 3: (40, 68)}, (0,)),
+    ([0, 2 ** 31 - 1, -2 ** 31, 65, 68], {3: (65, 68)}, (3,)),
+    ([69, 69, 69, 69, 69], {}, ()),
+]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("cu,ranges,alone", BAD_ROWS, ids=["past_the_end", "late", "negative", "back", "back_again", "extreme", "behind"])
+def test_rows_that_do_not_ascend(dtype, cu, ranges, alone):
+    """What is wrong with some rows is reported; ranges within the call's rows are worked on, as by themselves, the
+    others and the rows of none are left as they were.  Rows (and weights) that two ranges claim may hold either's."""
+    from oracle import serve_oracle as SO
+    from tests.test_gpu_serve import E, U
+    k = Chunk(dtype, 4, 2, 2, 64, 16, [100, 60, 30, 30], [40, 5, 20, 3], seed=63)
+    before = k.weight.cpu().numpy().astype(np.float64)
+    k.run(cu_new=ints(cu))
+    assert status() == 1
+    out, after, q, kp, vp = k.host(k.out), k.weight.cpu().numpy().astype(np.float64), k.host(k.q), k.host(k.kp), k.host(k.vp)
+    claims = np.zeros(k.n, dtype=int)
+    for x0, x1 in ranges.values():
+        claims[x0:x1] += 1
+    assert np.isnan(out[claims == 0]).all() and np.isfinite(out[claims > 0]).all()
+    for b in range(4):
+        if b not in ranges:
+            assert np.array_equal(after[b], before[b])
+            continue
+        x0, x1 = ranges[b]
+        n = int(k.lens[b])
+        ref, got, A, pv = SO.chunk_attention(q[x0:x1], [0, x1 - x0], kp, vp, k.table[b:b + 1].cpu().numpy(), [n])
+        rel = 2 * (2 * k.d + 16) * U * A + (16 + n + 64) * U
+        bound = (rel + (2.0 ** -8 if dtype == "bf16" else 0.0) + 2 * (n + 64) * U)[..., None] * pv + E[dtype] * np.abs(ref)
+        mine = claims[x0:x1] == 1
+        assert np.all(np.abs(out[x0:x1] - ref)[mine] <= bound[mine] + 1e-30), b
+        if b in alone:
+            lim = (rel.max() + ((x1 - x0) * k.G + 64) * U) * got[0] + 2 * U * (before[b] + got[0])
+            assert np.all(np.abs(after[b] - before[b] - got[0]) <= lim), b

@@ -151,3 +151,16 @@ def test_infinite_values_in_a_cache_that_is_cut(dtype, G, d):
             same = (out == want) | (torch.isnan(out) & torch.isnan(want))
             assert same.all(), (j, bad, int((~same).sum()))
     assert status() == 0
+
+
+@pytest.mark.parametrize("c", CASES, ids=NAMES)
+def test_logits_that_are_all_minus_infinity(c):
+    """Rows of which no slot counts give zeros, and nothing to the weights."""
+    k = Chunk(*c, seed=55)
+    dim = k.d // 2 + 1
+    k.q[:, :, dim] = -(k.q[:, :, dim].abs() + 0.25)
+    k.kp[..., dim] = float("inf")
+    before = k.weight.clone()
+    k.run()
+    assert not k.out.any() and bool((k.weight == before).all())
+    assert status() == 0
