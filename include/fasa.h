@@ -588,8 +588,8 @@ int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64
  * workspace: at least fasa_paged_chunk_workspace_size bytes of device memory, its contents
  * not kept and not read; calls that may overlap need one each.  A larger batch, a wider table
  * or more tokens never need less, so that one of the largest call serves all smaller ones.
- * Aligned to 16 bytes: q, k_pages, v_pages, out, weight, workspace.  out lies apart from q.
- * n_tokens <= 2^20.
+ * Aligned to 16 bytes: q, k_pages, v_pages, out, weight, workspace; to 4: the rest.  out,
+ * weight and workspace lie apart from each other and from everything.  n_tokens <= 2^20.
  */
 int fasa_paged_chunk_workspace_size(const fasa_paged_dims_t* dims, int32_t n_tokens, int32_t with_weight,
                                     size_t* bytes);

@@ -41,6 +41,13 @@ int check_dims(const fasa_paged_dims_t* d) {
   return fasa_paged_workspace_size(d, 0, &bytes);
 }
 
+size_t pool_bytes(const fasa_paged_dims_t* d) {  // of K's or V's pages
+  return (size_t)d->n_pages * d->n_kv_heads * d->page_size * d->head_dim * (d->dtype == FASA_F32 ? 4 : 2);
+}
+size_t stat_bytes(const fasa_paged_dims_t* d) {  // of the weights or the positions
+  return (size_t)d->batch * d->n_kv_heads * d->max_pages * d->page_size * 4;
+}
+
 int log2_of(int n) {
   int k = 0;
   while ((1 << k) < n) ++k;
@@ -280,9 +287,18 @@ int fasa_paged_chunk_attention(const void* q, int32_t n_tokens, const int32_t* c
   if (!aligned(q, 16) || !aligned(k_pages, 16) || !aligned(v_pages, 16) || !aligned(out, 16) || !aligned(weight, 16))
     return FASA_ERR_INVALID_ARG;
   if (n_tokens == 0) return FASA_OK;
-  const size_t io = (size_t)n_tokens * dims->n_q_heads * dims->head_dim * (dims->dtype == FASA_F32 ? 4 : 2);
-  if (!apart(Range{q, io}, Range{out, io})) return FASA_ERR_INVALID_ARG;
+  for (const void* x : {(const void*)cu_new, (const void*)page_table, (const void*)seq_lens})
+    if (!aligned(x, 4)) return FASA_ERR_INVALID_ARG;
   if (!workspace || workspace_bytes < need || !aligned(workspace, 16)) return FASA_ERR_WORKSPACE;
+  // Rows, lengths and pages are read again and again, by roles that have to agree on them, while
+  // results, weights and workspace are written
+  const size_t es = dims->dtype == FASA_F32 ? 4 : 2, io = (size_t)n_tokens * dims->n_q_heads * dims->head_dim * es;
+  const Range query{q, io}, cu{cu_new, (size_t)dims->batch * 4 + 4}, keys{k_pages, pool_bytes(dims)}, values{v_pages, pool_bytes(dims)},
+      table{page_table, (size_t)dims->batch * dims->max_pages * 4}, lens{seq_lens, (size_t)dims->batch * 4}, result{out, io},
+      given{weight, stat_bytes(dims)}, room{workspace, need};
+  if (!apart(result, {query, cu, keys, values, table, lens, given, room}) ||
+      !apart(given, {query, cu, keys, values, table, lens, room}) || !apart(room, {query, cu, keys, values, table, lens}))
+    return FASA_ERR_INVALID_ARG;
   int sms = 0, *status = nullptr;
   st = device_facts(&sms, &status);
   if (st) return st;

@@ -56,3 +56,20 @@ def test_workspace_has_room_for_the_rows_that_there_are(L):
         assert _size(L, d, n, 1) - _size(L, d, n, 0) == rows * 8 * 8192 * 4 + log_sums
     d = _dims(batch=2000, max_pages=16384)
     assert _size(L, d, 2000, 1) - _size(L, d, 2000, 0) == (480 << 20) + 2000 * 32 * 4
+
+
+def test_chunk_overlaps_rejected(L):
+    """What the call writes lies apart from what it reads and from itself: the smallest overlap, at either end."""
+    from tests.test_serve_host import P
+    d = _dims()  # of 2 sequences, 32 pages each of a pool of 100, 8 of 32 heads of 128 dims, bf16
+    io, pool, stat = 5 * 32 * 128 * 2, 100 * 8 * 16 * 128 * 2, 2 * 8 * 512 * 4
+    at = [x + (1 << 30) for x in A]
+    read = dict(q=(at[0], io), cu=(at[1], 12), kp=(at[2], pool), vp=(at[3], pool), table=(at[4], 2 * 32 * 4), lens=(at[5], 8))
+    written = dict(out=(at[6], io), w=(at[7], stat), ws=(at[8], _size(L, d, 5, 1)))
+    every = {name: x for name, (x, _) in (read | written).items()}
+    for name, (_, size) in written.items():
+        for other, (x, n) in list(read.items()) + [y for y in written.items() if y[0] != name]:
+            for to in (x, x + (n - 1) // 16 * 16, x - (size - 1) // 16 * 16):
+                assert _chunk(L, d, **{**every, name: to}) == 1, (name, other, to - x)
+    for name in ("cu", "table", "lens"):
+        assert _chunk(L, d, **{name: P + (3 << 29) + 2}) == 1
