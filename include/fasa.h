@@ -553,8 +553,8 @@ typedef struct fasa_rope {
  * v_stride elements apart (one projection's output holds all three); q_out [n_tokens, Hq,
  * d] contiguous.  q and q_out may both be NULL, so may k, v, k_pages and v_pages together
  * (then weight and token_pos, too); with n_tokens = 0 any may be, and nothing is done.
- * q_out may be q where q is contiguous; else it lies apart from q, k and v.  rope_theta of
- * dims is not used.
+ * q_out may be q where q is contiguous; else what is written (q_out, the pages, weight,
+ * token_pos) lies apart from each other and from everything.  rope_theta of dims is not used.
  * Rows of the map whose sequence is negative are padding: nothing is written for them, nor
  * for an entry outside the batch, the cache or the pool, which sets FASA_DEV_BAD_INPUT.
  * Rows that name one slot of one sequence twice leave a mixture of the two there (those of

@@ -225,7 +225,13 @@ int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64
   const int64_t row = heads[0] * dims->head_dim;
   const Range out{q_out, q ? (size_t)n_tokens * row * es : 0};
   if (q && !(q_out == q && q_stride == row) && !apart(out, in[0])) return FASA_ERR_INVALID_ARG;
-  if (q && !apart(out, {in[1], in[2], Range{token_map, (size_t)n_tokens * 16}})) return FASA_ERR_INVALID_ARG;
+  // a token's rows are read and written by its own warps, in no order among tokens
+  const Range map{token_map, (size_t)n_tokens * 16}, keys{k_pages, pool_bytes(dims)}, values{v_pages, pool_bytes(dims)},
+      given{weight, stat_bytes(dims)}, at{token_pos, stat_bytes(dims)};
+  if (!apart(out, {in[1], in[2], map, keys, values, given, at}) || !apart(keys, {in[0], in[1], in[2], map, values, given, at}) ||
+      !apart(values, {in[0], in[1], in[2], map, given, at}) || !apart(given, {in[0], in[1], in[2], map, at}) ||
+      !apart(at, {in[0], in[1], in[2], map}))
+    return FASA_ERR_INVALID_ARG;
   int sms = 0, *status = nullptr;
   st = device_facts(&sms, &status);
   if (st) return st;

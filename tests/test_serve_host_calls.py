@@ -73,3 +73,22 @@ def test_chunk_overlaps_rejected(L):
                 assert _chunk(L, d, **{**every, name: to}) == 1, (name, other, to - x)
     for name in ("cu", "table", "lens"):
         assert _chunk(L, d, **{name: P + (3 << 29) + 2}) == 1
+
+
+def test_rope_overlaps_rejected(L):
+    from kv_cache_token_tip_gb300 import FasaRope
+    d, r = _dims(), FasaRope()
+    q, kv, pool, stat = 5 * 32 * 128 * 2, 5 * 8 * 128 * 2, 100 * 8 * 16 * 128 * 2, 2 * 8 * 512 * 4
+    at = [x + (1 << 30) for x in A]
+    read = dict(q=(at[0], q), k=(at[1], kv), v=(at[2], kv), m=(at[3], 5 * 16))
+    written = dict(qo=(at[4], q), kp=(at[5], pool), vp=(at[6], pool), w=(at[7], stat), tp=(at[8], stat))
+    every = {name: x for name, (x, _) in (read | written).items()}
+    for name, (_, size) in written.items():
+        for other, (x, n) in list(read.items()) + [y for y in written.items() if y[0] != name]:
+            for to in (x, x + (n - 1) // 16 * 16, x - (size - 1) // 16 * 16):
+                if (name, other, to) != ("qo", "q", x):  # (in place)
+                    assert _rope(L, d, r, **{**every, name: to}) == 1, (name, other, to - x)
+    # rows of one projection's output: what lies between them counts as theirs
+    parts = dict(q=at[0], qs=48 * 128, k=at[0] + 32 * 256, ks=48 * 128, v=at[0] + 40 * 256, vs=48 * 128)
+    for name in ("qo", "kp", "w", "tp"):
+        assert _rope(L, d, r, **{**every, **parts, name: at[0] + 3 * 48 * 256}) == 1
