@@ -324,7 +324,7 @@ PyObject* rope_append(PyObject*, PyObject* const* a, Py_ssize_t n) {
       PyErr_SetString(PyExc_ValueError, "q goes with q_out, k and v with k_pages and v_pages");
       return nullptr;
     }
-    if (none_q && none_k) return PyLong_FromLong(FASA_OK);
+    if (none_q && none_k) return PyLong_FromLong(a[7] == Py_None && a[8] == Py_None ? FASA_OK : FASA_ERR_INVALID_ARG);
     void *q = nullptr, *q_out = nullptr, *k = nullptr, *v = nullptr, *kp = nullptr, *vp = nullptr;
     if (!none_q) {
       q = strided(a[0], "q", c.here, c.store, &tokens, c.d->n_q_heads, c.d->head_dim, &stride[0], &ok);

@@ -111,3 +111,18 @@ def test_rows_that_do_not_ascend(dtype, cu, ranges, alone):
         if b in alone:
             lim = (rel.max() + ((x1 - x0) * k.G + 64) * U) * got[0] + 2 * U * (before[b] + got[0])
             assert np.all(np.abs(after[b] - before[b] - got[0]) <= lim), b
+
+
+def test_statistics_of_no_keys_are_refused():
+    """With the queries or without: the statistics begin as keys are stored."""
+    import torch
+    from kv_cache_token_tip_gb300 import FasaError, FasaRope, fasa_paged_rope_append
+    k = Chunk("bf16", 2, 2, 2, 64, 16, [20, 30], [4, 5], seed=64)
+    m, rope = torch.full((9, 4), -1, dtype=torch.int32, device="cuda"), FasaRope(1, 64)
+    token_pos = torch.zeros(k.weight.shape, dtype=torch.int32, device="cuda")
+    for q, out in ((None, None), (k.q, torch.empty_like(k.q))):
+        for kw in (dict(weight=k.weight), dict(token_pos=token_pos), dict(weight=k.weight, token_pos=token_pos)):
+            with pytest.raises(FasaError):
+                fasa_paged_rope_append(q, None, None, m, out, None, None, rope=rope, dims=k.dims, **kw)
+        fasa_paged_rope_append(q, None, None, m, out, None, None, rope=rope, dims=k.dims)
+    assert status() == 0
