@@ -34,12 +34,7 @@ namespace {
 constexpr int CB_NT = 384;           // 8 warps of rows, one of instructions, one of copies, two at rest
 constexpr int CB_ROWS = 8;
 constexpr uint32_t TM = 0;           // where tensor memory begins, which a block takes whole
-constexpr int CB_K = 128;            // slots of a tile
-// What a unit costs beside its tiles, in slots.  With 128, 256 and 512: eight prompts of 37 to
-// 4096 tokens 381, 368 and 332 us, eight of 1000 73, 63 and 64, a server's step 299, 285 and 266;
-// drafted tokens 113, 112 and 114, 64 tokens behind 4000 26.0, 27.8 and 27.4, 8 behind 1000
-// 13.2, 13.3 and 14.3 (384 and 768 lie beside 512: eight prompts 351 and 351 where 512 took 345).
-constexpr int CB_UNIT = 512;
+constexpr int CB_K = CHUNK_TILE_BF16;
 constexpr float CB_SLACK = 8.f;      // powers of two that a row's maximum may run ahead of m
 
 template <int D>
@@ -145,7 +140,7 @@ __global__ void __launch_bounds__(CB_NT, 1)
   paged_wait();
   paged_go();
   const ChunkLine line = chunk_line<CB_NT>(p, reinterpret_cast<long long*>(sm + P::OFF_SEQ),
-                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CB_K, CB_UNIT, blockIdx.x == 0);
+                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CB_K, CHUNK_UNIT_BF16, blockIdx.x == 0);
   tm_after_sync();
   const int parts = line.parts(p.parts), c = blockIdx.x;
   const Patience patience{misc + 1, p.status, p.wait_ns};

@@ -24,10 +24,7 @@
 namespace fasa {
 namespace {
 
-constexpr int CF_NT = 256, CF_M = 128, CF_K = 64;
-// What a unit costs beside its tiles, in slots (the same prompts 274 us at 16, 256 at 48 or
-// 128 before the copying warp; 65 tokens behind 959 want parts of a tile).
-constexpr int CF_UNIT = 48;
+constexpr int CF_NT = 256, CF_M = 128, CF_K = CHUNK_TILE_F32;
 
 template <int D>
 struct CfPlan {
@@ -147,7 +144,7 @@ __global__ void __launch_bounds__(CA_NT, 1)
   paged_wait();
   paged_go();
   const ChunkLine line = chunk_line<CA_NT>(p, reinterpret_cast<long long*>(sm + P::OFF_LINE),
-                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CF_K, CF_UNIT, blockIdx.x == 0);
+                                           reinterpret_cast<long long*>(sm + P::OFF_SCAN), TU, CF_K, CHUNK_UNIT_F32, blockIdx.x == 0);
   const int parts = line.parts(p.parts), c = blockIdx.x;
   if (tid == 0) note_none(p, c);
   if (tid == 0 && c == 0) *p.queue = 0;

@@ -22,6 +22,22 @@ namespace fasa {
 
 constexpr int CHUNK_MAX_SMS = 160;    // the workspace has room for their parts
 
+// Tokens of a unit (their rows: times the heads of their group), slots of a tile, and what a
+// unit costs beside its tiles, in slots.  That is more than its start and end take, about 290
+// slots in a traced build of the bf16 kernel: it was picked by times, and few rows pay for it.
+// bf16, with 128, 256 and 512: eight prompts of 37 to 4096 tokens 381, 368 and 332 us, eight of
+// 1000 73, 63 and 64, a server's step 299, 285 and 266; drafted tokens 113, 112 and 114, 64
+// tokens behind 4000 26.0, 27.8 and 27.4, 8 behind 1000 13.2, 13.3 and 14.3 (384 and 768 lie
+// beside 512: eight prompts 351 and 351 where 512 took 345).  fp32: two prompts 274 us at 16,
+// 256 at 48 or 128 before the copying warp; 65 tokens behind 959 want parts of a tile.
+struct ChunkShape {
+  int tokens, tile, unit;
+};
+constexpr int CHUNK_TILE_BF16 = 128, CHUNK_UNIT_BF16 = 512, CHUNK_TILE_F32 = 64, CHUNK_UNIT_F32 = 48;
+inline ChunkShape chunk_shape(bool bf16, int G) {
+  return bf16 ? ChunkShape{2 * (128 / G), CHUNK_TILE_BF16, CHUNK_UNIT_BF16} : ChunkShape{128 / G, CHUNK_TILE_F32, CHUNK_UNIT_F32};
+}
+
 // A sequence's new tokens, where they begin among the call's rows, and its slots.
 struct ChunkSeq {
   int first, n, len;

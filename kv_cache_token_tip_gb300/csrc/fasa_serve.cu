@@ -117,10 +117,10 @@ void chunk_plan(const fasa_paged_dims_t* d, int n_tokens, int sms, int* rows, in
   const int T = s.tokens;
   // (whole 16-byte words to a record)
   *rows = ((int)std::min<long long>((long long)T * G, (long long)n_tokens * G) + 3) / 4 * 4;
-  // a unit's parts each hold a tile: no more parts than units of the longest cache have tiles
+  // a part without a tile has nothing to do: no more parts than units of the longest cache have tiles
   const long long units = ((long long)n_tokens / T + std::min(d->batch, n_tokens)) * d->n_kv_heads;
   const long long tiles = ((long long)d->max_pages * d->page_size + T + s.tile - 1) / s.tile + 1;
-  *parts = (int)std::min<long long>(s.per_sm * std::min(sms, CHUNK_MAX_SMS), units * tiles);
+  *parts = (int)std::min<long long>(std::min(sms, CHUNK_MAX_SMS), units * tiles);
 }
 
 size_t notes_bytes(int parts) { return 256 + up((size_t)parts * 2 * sizeof(int4)); }  // and the queue

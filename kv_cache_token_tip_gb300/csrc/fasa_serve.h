@@ -78,11 +78,6 @@ struct ChunkParams {
   int drop_tile;  // test hook: this tile of every part is never copied (-1: none)
 };
 
-// Tokens of a unit (their rows: times the heads of their group), slots of a tile, and
-// parts to an SM.
-struct ChunkShape {
-  int tokens, tile, per_sm;
-};
 // A sequence is light with this many rows (new tokens times the heads of a group) or fewer: its
 // logits are kept for the weights, 16 bytes a slot for 4 rows instead of K's 256 again, as far as
 // CHUNK_LOGITS bytes go: the first sequences' then, so that a larger batch or table never needs a
@@ -93,7 +88,6 @@ struct ChunkShape {
 // 1527, 1525 and 1301.
 constexpr int CHUNK_LIGHT = 16;
 constexpr long long CHUNK_LOGITS = 480ll << 20;
-inline ChunkShape chunk_shape(bool bf16, int G) { return bf16 ? ChunkShape{2 * (128 / G), 128, 1} : ChunkShape{128 / G, 64, 1}; }
 
 cudaError_t launch_paged_assign(const AssignParams& p, int sms, cudaStream_t s);
 cudaError_t launch_rope_append(const RopeAppendParams& p, int head_dim, bool bf16, bool half, int sms, cudaStream_t s);

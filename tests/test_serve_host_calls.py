@@ -92,3 +92,49 @@ def test_rope_overlaps_rejected(L):
     parts = dict(q=at[0], qs=48 * 128, k=at[0] + 32 * 256, ks=48 * 128, v=at[0] + 40 * 256, vs=48 * 128)
     for name in ("qo", "kp", "w", "tp"):
         assert _rope(L, d, r, **{**every, **parts, name: at[0] + 3 * 48 * 256}) == 1
+
+
+KERNELS_LINE = r"""
+// The kernels' own units, tiles and costs: those of either type, with every number of heads to a group.
+int main() {
+  srand(2);
+  for (int k = 0; k < 1600; ++k) {
+    const bool bf16 = k & 1;
+    const int G = 1 + k / 2 % 8, Hkv = 1 + rand() % 8, B = 1 + rand() % (k % 10 ? 6 : 60);
+    const ChunkShape s = chunk_shape(bf16, G);
+    CHECK(s.tokens == (bf16 ? 2 * (128 / G) : 128 / G) && s.tile == (bf16 ? 128 : 64) && s.unit == (bf16 ? 512 : 48));
+    std::vector<int> n, len;
+    const int long_n = 1 + rand() % (k % 7 ? 300 : 3000), long_a = rand() % (k % 5 ? 400 : 20000);
+    for (int b = 0; b < B; ++b) {
+      n.push_back(rand() % 4 ? rand() % (long_n + 1) : rand() % 2);
+      len.push_back(n[b] + rand() % (long_a + 1));
+      if (rand() % 9 == 0) len[b] = rand() % (n[b] + 1);
+    }
+    if (check(n, len, Hkv, s.tokens, s.tile, s.unit, k % 3 ? 152 : 1 + rand() % 160)) return printf("case %d\n", k), 1;
+  }
+  for (int G = 1; G <= 8; ++G)
+    for (int bf16 = 0; bf16 < 2; ++bf16) {
+      const ChunkShape s = chunk_shape(bf16, G);
+      const int T = s.tokens;
+      // a token a sequence; lengths about the tiles'; more new tokens than cached ones; nothing cached
+      if (check(std::vector<int>(2048, 1), std::vector<int>(2048, 1 + 77 * G), 2, T, s.tile, s.unit, 152)) return 1;
+      for (int d = -1; d <= 1; ++d)
+        if (check({T + d, 2 * T + d, 1}, {s.tile + d, 3 * s.tile + T + d, 5 * s.tile + d}, 3, T, s.tile, s.unit, 152)) return 1;
+      if (check({100, 1, 7}, {0, 0, 3}, 2, T, s.tile, s.unit, 152)) return 1;
+      // the largest: positions past 32 bits
+      if (check({1 << 20}, {262144}, 2, T, s.tile, s.unit, 152) || check({1 << 18, 1 << 18}, {262144, 262144}, 3, T, s.tile, s.unit, 152)) return 1;
+    }
+  printf("ok\n");
+}
+"""
+
+
+def test_index_arithmetic_of_the_kernels(tmp_path):
+    from tests.test_serve_host import INDEX_PROGRAM, ROOT
+    src = tmp_path / "line.cpp"
+    src.write_text(INDEX_PROGRAM[:INDEX_PROGRAM.index("int main()")] + KERNELS_LINE)
+    exe = str(tmp_path / "line")
+    inc = os.path.join(ROOT, "kv_cache_token_tip_gb300", "csrc")
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", inc, str(src), "-o", exe], check=True, capture_output=True)
+    r = subprocess.run([exe], capture_output=True, text=True)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
