@@ -557,11 +557,12 @@ def fasa_paged_chunk_attention(q, k_pages, v_pages, page_table, seq_lens, out, c
     storage dtype, q already turned; those of sequence b are cu_new[b] ..
     cu_new[b+1], or one per sequence without cu_new.  With weight, each slot's
     softmax weights are added to it.  Without a workspace one is allocated here."""
-    if workspace is None:
-        per = dims.n_q_heads * dims.head_dim
-        workspace = _scratch(fasa_paged_chunk_workspace_size(dims, q.numel() // max(per, 1), weight is not None), stream)
-    st = (_native or _marshal()).chunk(q, k_pages, v_pages, page_table, seq_lens, out, cu_new, weight, workspace,
-                                       _where(dims), None if stream is None else _stream(stream))
+    where, native = _where(dims), _native or _marshal()
+    if workspace is None:  # (of what is no tensor: none; the call says so)
+        n = q.numel() // max(dims.n_q_heads * dims.head_dim, 1) if hasattr(q, "numel") else 0
+        workspace = _scratch(fasa_paged_chunk_workspace_size(dims, n, weight is not None), stream)
+    st = native.chunk(q, k_pages, v_pages, page_table, seq_lens, out, cu_new, weight, workspace, where,
+                      None if stream is None else _stream(stream))
     if st:
         _check("fasa_paged_chunk_attention", st)
 

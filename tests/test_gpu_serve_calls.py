@@ -126,3 +126,12 @@ def test_statistics_of_no_keys_are_refused():
                 fasa_paged_rope_append(q, None, None, m, out, None, None, rope=rope, dims=k.dims, **kw)
         fasa_paged_rope_append(q, None, None, m, out, None, None, rope=rope, dims=k.dims)
     assert status() == 0
+
+
+def test_chunk_queries_that_are_no_tensor_are_refused():
+    from kv_cache_token_tip_gb300 import fasa_paged_chunk_attention
+    k = Chunk("bf16", 2, 2, 2, 64, 16, [20, 30], [4, 5], seed=65)
+    for bad in (None, 3, [1.0]):
+        with pytest.raises(ValueError):
+            fasa_paged_chunk_attention(bad, k.kp, k.vp, k.table, k.lens, k.out, cu_new=k.cu, dims=k.dims)
+    assert status() == 0

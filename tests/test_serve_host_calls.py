@@ -138,3 +138,12 @@ def test_index_arithmetic_of_the_kernels(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-O2", "-I", inc, str(src), "-o", exe], check=True, capture_output=True)
     r = subprocess.run([exe], capture_output=True, text=True)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stdout + r.stderr
+
+
+def test_chunk_binding_without_a_workspace_names_what_is_wrong(L):
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_chunk_attention
+    x = torch.zeros(8)
+    for dims in (None, 3):
+        with pytest.raises(TypeError):
+            fasa_paged_chunk_attention(x, x, x, x, x, x, dims=dims)
