@@ -71,16 +71,18 @@ __device__ __forceinline__ void fetch_slots(const void* pages, const int* rows, 
   cp_async_commit();
 }
 
-// Rows of a unit's queries: `count` of them from token `token` on, head group h; zeros behind.
+// Rows of a unit's queries: `count` of them from token `token` on, head group h; behind them the
+// last one again: zeros times an infinite key would be NaN, and add that to a slot, where a row's
+// copy, of weight 0, adds nothing unless the row itself makes the slot NaN.
 template <int D>
 __device__ __forceinline__ void fetch_queries(const ChunkParams& p, int token, int h, int count, char* to) {
   constexpr int CH = D / 4;
+  const int all = (count + 15) / 16 * 16 * CH;  // (warps without rows read nothing)
 #pragma unroll 4
-  for (int i = threadIdx.x; i < CF_M * CH; i += CF_NT) {
-    const int r = i / CH, c = i % CH, j = r / p.G;
-    const bool live = r < count;
-    const size_t from = ((size_t)(token + (live ? j : 0)) * p.Hq + h * p.G + (live ? r - j * p.G : 0)) * D + 4 * c;
-    cp_async16_zfill(smem_u32(to + swizzled(CF_M, r, c)), static_cast<const float*>(p.q) + from, live ? 16u : 0u);
+  for (int i = threadIdx.x; i < all; i += CF_NT) {
+    const int r = i / CH, c = i % CH, x = min(r, count - 1), j = x / p.G;
+    const size_t from = ((size_t)(token + j) * p.Hq + h * p.G + x - j * p.G) * D + 4 * c;
+    cp_async16(smem_u32(to + swizzled(CF_M, r, c)), static_cast<const float*>(p.q) + from);
   }
   cp_async_commit();
 }
@@ -458,15 +460,13 @@ __global__ void __launch_bounds__(CF_NT, 1) chunk_weight_f32_kernel(const __grid
       if (i + 1 < tiles) fetch(i + 1);
       const float* lse = reinterpret_cast<const float*>(sm + P::W_LSE) + (i & 1) * CF_M;
       float z[8][4];
-      const int rows = min(TU, u.q.n - i * TU) * p.G;
-      if (tid / 32 * 16 >= rows) continue;  // no rows of this warp
+      if (tid / 32 * 16 >= min(TU, u.q.n - i * TU) * p.G) continue;  // no rows of this warp
       products<D>(sm + P::W_Q + (i & 1) * P::Q_BYTES, ks, z);
       float part[4] = {};
 #pragma unroll
       for (int r = 0; r < 8; ++r) {
-        // the last slot that this row sees (none of one that there is not: its queries of 0 times an
-        // infinite key are NaN)
-        const int see = 8 * ty + r < rows ? a + i * TU + (8 * ty + r) / p.G : -1;
+        // the last slot that this row sees (or the row that it is a copy of)
+        const int see = a + i * TU + min((8 * ty + r) / p.G, TU - 1);
         const float x = lse[8 * ty + r];
 #pragma unroll
         for (int j = 0; j < 4; ++j) part[j] += u.t0 + tx + 16 * j <= see ? exp2f(z[r][j] * p.scale - x) : 0.f;

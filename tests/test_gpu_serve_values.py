@@ -164,3 +164,27 @@ def test_logits_that_are_all_minus_infinity(c):
     k.run()
     assert not k.out.any() and bool((k.weight == before).all())
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("G,d,new", [(1, 64, 300), (3, 128, 100), (4, 64, 70), (5, 64, 60), (7, 128, 41), (8, 64, 33), (3, 64, 5)])
+def test_infinite_keys_of_new_tokens(dtype, G, d, new):
+    """A new token's key is infinite in an element where the queries before it have its sign (a logit of +inf, did they
+    see it) and those from it on the other: no row and no slot gives anything but numbers."""
+    import torch
+    TU = 128 // G
+    for j in sorted({1, new // 2, new - 1} | {x for t in (TU, 2 * TU) for x in (t - 1, t, t + 1) if 0 < x < new}):
+        k = Chunk(dtype, 2, 2, G, d, 16, [50, 9], [new, 20], seed=56, pad=3)
+        dim = d // 2 + 1
+        q = k.q[:new, :, dim].abs() + 0.25
+        k.q[:new, :, dim] = torch.where(torch.arange(new, device="cuda").view(-1, 1) < j, q, -q)
+        key(k, 0, 1, 50 + j)[dim] = float("inf")
+        k.q[-3:] = float("nan")
+        before = k.weight.cpu().numpy().astype(np.float64)
+        k.run()
+        live = k.cu_host[-1]
+        k.q[live:] = 0  # (rows of no sequence: zeros in the reference, too)
+        k.out[live:] = 0
+        ref, got = check(k, before)
+        assert np.isfinite(ref).all() and np.isfinite(got).all() and np.all(got[0, 1, 50 + j] == 0)
+    assert status() == 0
