@@ -9,21 +9,24 @@
 // issues the matrix instructions, one that copies.  While the tensor cores work for one tile
 // of rows, the softmax of the other is worked out.
 //
-// Bound by the tensor cores where units are long: 2048 tokens behind 30720 take 600 us by
+// Bound by the tensor cores where units are long: 2048 tokens behind 30720 take 610 to 630 us by
 // themselves (tensor pipe 81% busy), and 690 to 740 one after another, where the card's power
-// bounds them.  Eight prompts of 37 to 4096 tokens 298 us (64%): a unit's start and end cost 5400
-// to 5800 clocks beside 2530 a tile (in a traced build).  Drafted tokens of 16 sequences 112 us,
-// 5.7 TB/s.  What it took: instructions issued by one elected lane from descriptors worked out ahead (742 -> 684 us
-// for the first case), P handed over by halves and a row to a thread (598; half a row to each of
-// two warps 684), results by way of shared memory (eight prompts 372 -> 327), what a unit costs
-// (below).
+// bounds them.  Eight prompts of 37 to 4096 tokens 295 to 305 us (64%): a unit's start and end cost
+// 5400 to 5800 clocks beside 2530 a tile (in a traced build).  Drafted tokens of 16 sequences 113
+// us, 5.7 TB/s.  What it took, one step after another: instructions issued by one elected lane from
+// descriptors worked out ahead (742 -> 684 us for the first case), P handed over by halves and a row
+// to a thread (598; half a row to each of two warps 684), results by way of shared memory (eight
+// prompts 372 -> 327), what a unit costs (fasa_chunk_index.h).
+//
+// P is rounded to bf16, an operand's type here: results are off by 2.2e-3 to 2.3e-3 of their norm
+// where weights in fp32, and one rounding of the result, give 1.6e-3 to 1.7e-3.  P in two terms
+// would bring that and take half of all products once more.
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <stdint.h>
 
 #include <algorithm>
 #include <atomic>
-#include <type_traits>
 
 #include "fasa_chunk.cuh"
 #include "fasa_tcgen05.cuh"
@@ -65,8 +68,8 @@ __device__ __forceinline__ int row_tile_end(const ChunkParams& p, const ChunkUni
 // Clears what a tile of V (128 rows at `tile`) brings to rows that do not see it: rows n .. 127,
 // which hold anything (up to the pages' end; what lies behind that was not copied and is 0), and
 // elements of rows r0 .. n - 1 that are not finite.  A warp; whether there were any.  A function
-// of its own (eight prompts 326 us; inlined among the matrix instructions 339, without any of
-// it 319); it has to do with the 56 registers of its warp.
+// of its own (eight prompts 314 us; inlined among the matrix instructions 326, without any of
+// it 310); it has to do with the 56 registers of its warp.
 template <int D>
 __device__ __noinline__ bool clear_unseen(uint32_t tile, int r0, int n) {
   using P = CbPlan<D>;
@@ -545,6 +548,47 @@ struct RingAt {
   }
 };
 
+// What a slot gets of 64 columns of S at `at`, which are then free (`done`): those that `there` says
+// are rows, and of them those that `sees` says see the slot.  l: the rows' negative log-sums, maybe
+// NaN, so that a row that does not see the slot is masked behind the sum with it.
+template <class There, class Sees>
+__device__ __forceinline__ float columns_sum(uint32_t at, uint32_t done, const float* l, float scale, There&& there, Sees&& sees) {
+  uint32_t s[64];
+  tm_ld32(at, s);
+  tm_ld32(at + 32, s + 32);
+  tm_wait_ld();
+  tm_settle(s);
+  tm_before_sync();
+  __syncwarp();
+  if ((threadIdx.x & 31) == 0) mbar_arrive(done);
+#pragma unroll
+  for (int x = 0; x < 64; ++x)
+    if (!there(x)) s[x] = 0xff800000u;  // -inf
+  const uint64_t scale2 = pair_of(scale, scale);
+  uint64_t sum[2] = {0, 0};
+#pragma unroll
+  for (int x = 0; x < 16; ++x) {
+    const float4 y = reinterpret_cast<const float4*>(l)[x];
+    float a[4];
+    unpair(fma2(pair_of(__uint_as_float(s[4 * x]), __uint_as_float(s[4 * x + 1])), scale2, pair_of(y.x, y.y)), a[0], a[1]);
+    unpair(fma2(pair_of(__uint_as_float(s[4 * x + 2]), __uint_as_float(s[4 * x + 3])), scale2, pair_of(y.z, y.w)), a[2], a[3]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (!sees(4 * x + e)) a[e] = -INFINITY;
+    sum[0] = add2(sum[0], pair_of(ex2(a[0]), ex2(a[1])));
+    sum[1] = add2(sum[1], pair_of(ex2(a[2]), ex2(a[3])));
+  }
+  float a, b;
+  unpair(add2(sum[0], sum[1]), a, b);
+  return a + b;
+}
+// A tile whose rows end, or of which some do not see all of the warp's slots: few.  A function of
+// its own: a prompt of 16K tokens with weights 2022 us, 2060 with both kinds of sums in line (2014
+// with the mask ahead of the log-sum, where NaN reaches slots that its row does not see).
+__device__ __noinline__ static float edge_sum(uint32_t at, uint32_t done, const float* l, float scale, int lo, int rows) {
+  return columns_sum(at, done, l, scale, [](int) { return true; }, [&](int x) { return x >= lo && x < rows; });
+}
+
 template <int D>
 __global__ void __launch_bounds__(CW_NT, 1)
     chunk_weight_bf16_kernel(const __grid_constant__ ChunkParams p, const __grid_constant__ CUtensorMap qmap,
@@ -662,50 +706,21 @@ __global__ void __launch_bounds__(CW_NT, 1)
         const int buf = (n_s + w) % CW_S;
         n_s += i >= second ? 2 : 1;
         if (i >= mine) {
+          // the rows of this tile that there are, and of them the first that sees the slot
+          const int rows = min(TQ, u.q.n - i * TQ) * p.G - 64 * half, lo = (slot - (u.q.len - u.q.n) - i * TQ) * p.G - 64 * half;
+          const bool edge = rows < TQ * p.G - 64 * half || __any_sync(0xffffffffu, lo > 0);
           ok = patience.wait(t_full + 32 * w + 8 * (own & 3), own >> 2 & 1);
           if (!ok) break;
           ++own;
           tm_after_sync();
-          uint32_t s[64];
-          const uint32_t at = here + 128 * (1 + buf) + 64 * half;
-          tm_ld32(at, s);
-          tm_ld32(at + 32, s + 32);
-          tm_wait_ld();
-          tm_settle(s);
-          tm_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(t_empty + 8 * buf);
-          // the rows of this tile that there are, and of them the first that sees the slot
-          const int rows = min(TQ, u.q.n - i * TQ) * p.G, lo = (slot - (u.q.len - u.q.n) - i * TQ) * p.G - 64 * half;
-          // (columns behind a tile's rows hold anything; a tile has 125 rows or more)
-#pragma unroll
-          for (int x = 61; x < 64; ++x)
-            if (half && 64 + x >= TQ * p.G) s[x] = 0xff800000u;
-          const uint64_t scale2 = pair_of(scale, scale);
-          const float4* l4 = reinterpret_cast<const float4*>(lse + 128 * st + 64 * half);  // (negative log-sums)
-          uint64_t sum[2] = {0, 0};
-          // edge: some rows are masked, behind the sum with their log-sum, which may be NaN
-          auto add = [&](auto edge) {
-#pragma unroll
-            for (int x = 0; x < 16; ++x) {
-              const float4 l = l4[x];
-              float y[4];
-              unpair(fma2(pair_of(__uint_as_float(s[4 * x]), __uint_as_float(s[4 * x + 1])), scale2, pair_of(l.x, l.y)), y[0], y[1]);
-              unpair(fma2(pair_of(__uint_as_float(s[4 * x + 2]), __uint_as_float(s[4 * x + 3])), scale2, pair_of(l.z, l.w)), y[2], y[3]);
-              if constexpr (decltype(edge)::value) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (4 * x + e < lo || 4 * x + e >= rows - 64 * half) y[e] = -INFINITY;
-              }
-              sum[0] = add2(sum[0], pair_of(ex2(y[0]), ex2(y[1])));
-              sum[1] = add2(sum[1], pair_of(ex2(y[2]), ex2(y[3])));
-            }
-          };
-          if (rows < TQ * p.G || __any_sync(0xffffffffu, lo > 0)) add(std::true_type());
-          else add(std::false_type());
-          float a, b;
-          unpair(add2(sum[0], sum[1]), a, b);
-          total += a + b;
+          const uint32_t at = here + 128 * (1 + buf) + 64 * half, done = t_empty + 8 * buf;
+          const float* l = lse + 128 * st + 64 * half;  // (negative log-sums)
+          if (edge) {
+            total += edge_sum(at, done, l, scale, lo, rows);
+          } else {
+            // (columns behind a tile's rows hold anything; a tile has 125 rows or more)
+            total += columns_sum(at, done, l, scale, [&](int x) { return x < 61 || x < rows; }, [](int) { return true; });
+          }
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(lse_empty + 8 * st);
