@@ -580,7 +580,8 @@ int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64
  * the slots that it sees.  With weight (not NULL):
  *   weight[b,h,t] += sum over the new tokens and the group's heads of softmax_t.
  * bf16: the softmax weights that multiply V are rounded to bf16; their sum and what goes
- * to `weight` are not.  Equal calls give equal bits.
+ * to `weight` are not.  Equal calls give equal bits; another batch around a sequence may cut
+ * its work elsewhere, and round its sums otherwise.
  * Rows at or behind cu_new[B] are padding: their `out` is left as it is.  A cu_new that does
  * not ascend from 0 within n_tokens sets FASA_DEV_BAD_INPUT; a sequence whose range is
  * not within n_tokens is left out.  Rows that two ranges hold get either's result, and the

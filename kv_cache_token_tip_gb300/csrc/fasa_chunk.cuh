@@ -364,8 +364,8 @@ __device__ __forceinline__ int weight_sequence(const int* w, int B, int Hkv, int
 
 // The x-th unit; false behind the last.  A head's units fall in cost (the later the slots,
 // the fewer tokens see them) and those of few tokens come last, so that blocks that take the
-// next one when they are done end together (a step of two prompts and 30 single tokens: 161
-// us dealt there and back, 148 so).
+// next one when they are done end together (a step of two prompts and 30 single tokens, before
+// light sequences kept their logits: 161 us dealt there and back, 148 so).
 template <int SLOTS>
 __device__ __forceinline__ bool weight_unit(const ChunkParams& p, const int* before, int x, WeightUnit& u) {
   const int first = before[p.B] * p.Hkv;

@@ -23,13 +23,13 @@ namespace fasa {
 constexpr int CHUNK_MAX_SMS = 160;    // the workspace has room for their parts
 
 // Tokens of a unit (their rows: times the heads of their group), slots of a tile, and what a
-// unit costs beside its tiles, in slots.  That is more than its start and end take, about 290
-// slots in a traced build of the bf16 kernel: it was picked by times, and few rows pay for it.
-// bf16, with 128, 256 and 512: eight prompts of 37 to 4096 tokens 381, 368 and 332 us, eight of
-// 1000 73, 63 and 64, a server's step 299, 285 and 266; drafted tokens 113, 112 and 114, 64
-// tokens behind 4000 26.0, 27.8 and 27.4, 8 behind 1000 13.2, 13.3 and 14.3 (384 and 768 lie
-// beside 512: eight prompts 351 and 351 where 512 took 345).  fp32: two prompts 274 us at 16,
-// 256 at 48 or 128 before the copying warp; 65 tokens behind 959 want parts of a tile.
+// unit costs beside its tiles, in slots.  bf16: a start and an end take as long as 290 slots in a
+// traced build; more than that was picked by times, and calls of few rows pay for it.  With 128,
+// 256, 384, 512 and 768: eight prompts of 37 to 4096 tokens 377, 359, 322, 311 and 323 us, eight of
+// 1000 110, 108, 109, 106 and 110, a server's step 298, 284, 273, 269 and 268; drafted tokens 111,
+// 110, 111, 113 and 114, 64 tokens behind 4000 26.5, 28.4, 28.0, 28.1 and 27.7, 8 behind 1000 13.6,
+// 13.7, 14.2, 14.7 and 14.2.  fp32, with 16, 48 and 128: two prompts 238, 230 and 236, 65 tokens
+// behind 959 34.5, 34.5 and 35.0.
 struct ChunkShape {
   int tokens, tile, unit;
 };

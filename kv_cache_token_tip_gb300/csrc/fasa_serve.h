@@ -82,10 +82,9 @@ struct ChunkParams {
 // logits are kept for the weights, 16 bytes a slot for 4 rows instead of K's 256 again, as far as
 // CHUNK_LOGITS bytes go: the first sequences' then, so that a larger batch or table never needs a
 // smaller workspace.  Room is for the tokens' rows, or for CHUNK_LIGHT a sequence where that is
-// less (a step with prompts).  With 4, 8 and 16 rows,
-// groups of 4 heads, bf16: 16 sequences of 8000 tokens with 1 new one 111, 113 and 115 us, with 2
-// 204, 117 and 120, with 4 207, 206 and 132; fp32, 1039, 1040 and 1044, 1524, 1278 and 1282,
-// 1527, 1525 and 1301.
+// less (a step with prompts).  With 4, 8 and 16 rows, groups of 4 heads, bf16: 16 sequences of 8000
+// tokens with 1 new one 111, 112 and 115 us, with 2 201, 118 and 119, with 4 205, 204 and 131; fp32,
+// 1076, 1076 and 1080, 1480, 1311 and 1313, 1483, 1483 and 1328.
 constexpr int CHUNK_LIGHT = 16;
 constexpr long long CHUNK_LOGITS = 480ll << 20;
 
