@@ -135,3 +135,37 @@ def test_chunk_queries_that_are_no_tensor_are_refused():
         with pytest.raises(ValueError):
             fasa_paged_chunk_attention(bad, k.kp, k.vp, k.table, k.lens, k.out, cu_new=k.cu, dims=k.dims)
     assert status() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_a_sequence_alone_and_in_a_batch(dtype):
+    """The batch around a sequence moves the cuts of its work: by itself it gives the same within the rounding, though
+    not the same bits, and each of the two the same bits again."""
+    import torch
+    from kv_cache_token_tip_gb300 import fasa_paged_chunk_attention
+    from tests.test_gpu_serve import E, U
+    k = Chunk(dtype, 4, 2, 4, 128, 32, [700, 20, 3000, 0], [90, 300, 40, 2], seed=66)
+    start = k.weight.clone()
+    before = start.cpu().numpy().astype(np.float64)
+    out = k.run().clone()
+    k.check(before)
+    weight = k.weight.clone()
+    k.weight.copy_(start)
+    assert torch.equal(k.run(), out) and torch.equal(k.weight, weight)
+    dims = paged_dims(dtype, 1, 2, 4, 128, 32, k.kp.shape[0], k.table.shape[1])
+    for b in range(4):
+        x0, x1, n = k.cu_host[b], k.cu_host[b + 1], int(k.lens[b])
+        alone, again, w = torch.empty_like(k.q[x0:x1]), torch.empty_like(k.q[x0:x1]), start[b:b + 1].clone()
+        for to in (alone, again):
+            w.copy_(start[b:b + 1])
+            fasa_paged_chunk_attention(k.q[x0:x1], k.kp, k.vp, k.table[b:b + 1], k.lens[b:b + 1], to,
+                                       cu_new=ints([0, x1 - x0]), weight=w, dims=dims)
+        assert torch.equal(alone, again)
+        # sums of n terms in another order (2 u a term at most), maxima that lag elsewhere (bf16: other roundings of P),
+        # and the result's rounding, of results below 8 (values and weights' sums of 1)
+        err = (alone.double() - out[x0:x1].double()).abs().max()
+        assert float(err) <= 8 * (2 * n * U + 64 * U + 2 * E[dtype] + (2.0 ** -7 if dtype == "bf16" else 0))
+        got = (weight[b] - start[b]).double()
+        lim = (2 * n + 64 + (x1 - x0) * 4) * U * got.abs() + 4 * U * weight[b].double() + 1e-30
+        assert ((w[0] - weight[b]).double().abs() <= lim).all()
+    assert status() == 0
