@@ -577,7 +577,9 @@ int fasa_paged_rope_append(const void* q, int64_t q_stride, const void* k, int64
  *   out[x] = softmax(q K^T / sqrt(d)) V over the slots 0 .. s   (storage dtype, rounded once);
  * zeros where there is none (s < 0) or all logits are -inf.  What is not finite in the K or V
  * of other slots reaches no row; a logit of +inf or NaN makes its row NaN, and the weights of
- * the slots that it sees.  With weight (not NULL):
+ * the slots that it sees; a value that is not finite makes its element of the rows that see it
+ * so (NaN for infinity, maybe, where its weight is below the smallest number).  With weight
+ * (not NULL):
  *   weight[b,h,t] += sum over the new tokens and the group's heads of softmax_t.
  * bf16: the softmax weights that multiply V are rounded to bf16; their sum and what goes
  * to `weight` are not.  Equal calls give equal bits; another batch around a sequence may cut
